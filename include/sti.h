@@ -360,6 +360,104 @@ sti_status sti_decode_fused_noalloc(const sti_decode_args *a, sti_stream stream)
 /* Synchronises `stream` and returns the STI_FLAG_* bits the last no-allocation call left. */
 sti_status sti_decode_noalloc_status(uint32_t *flags, sti_stream stream);
 
+/* ------------------------------------------------------------------ bounded 4-bit cache */
+/*
+ * Not operations of the pages: a cache of fp4 rows that is written, attended as a whole and kept
+ * within a budget of rows, for layers that attend over every row they hold instead of the Indexer's
+ * selection.  The three calls of a step share start_pos (position of the step's first token, one per
+ * sequence), seqlen (its tokens), ratio (tokens per row) and `dropped`:
+ *   G(b) = (start_pos[b] + seqlen) // ratio groups are complete after the step; the rows of group
+ *   g >= the groups complete before the step sit at row g - dropped[b], and
+ *   held(b) = G(b) - dropped[b], clamped to [0, n_rows], rows are in use.
+ * dropped: int32 [b], the rows evicted so far (zeros at first; sti_kv_evict advances it); NULL: none.
+ * start_pos >= 0, dropped >= 0.
+ *
+ * sti_kv_append_fp4: quantise the step's completed groups and write their rows.
+ *   x: bf16 [b, m, dim], m = ceil(seqlen / ratio) rows, batch b at x + b*x_bstride (elements, a
+ *      multiple of 8): row i is group start_pos[b]//ratio + i; rows of groups that the step does not
+ *      complete are ignored.
+ *   format: how a group of elements shares its scale s; an element is stored as the E2M1 code nearest
+ *      to x / s (ties to the even code, saturating at 6, no negative zero), element 2j in the low
+ *      nibble of byte j:
+ *        STI_FP4_E4M3_16: groups of 16, s = E4M3(max|x| / 6), round to nearest even, at most 448 (0: the
+ *           group is zeros) -- the compressed rows of sti_sparse_attn_sink_fp4kv, sti_decode_args
+ *           (comp_codes, comp_scales) and sti_attn_fp4kv; scales [b, n_rows, dim/16]
+ *        STI_FP4_E8M0_32: groups of 32, s = 2^X, X = floor(log2 max|x|) - 2 clamped to [-127, 127] --
+ *           the index keys of sti_idx_scores_mxfp4; scales [b, n_rows, dim/32], byte X + 127
+ *      A group holding a NaN gets the NaN scale (0x7F, 0xFF) and zero codes; infinities saturate.
+ *   codes: uint8 [b, n_rows, dim/2], batch b at + b*codes_bstride bytes; scales likewise.
+ *   row_pos: optional int32 [b, n_rows] (batch stride in elements): the row's group number;
+ *   row_weight: optional fp32 [b, n_rows]: set to 0 for the rows written.
+ *   A row outside [0, n_rows) is not written and raises STI_FLAG_INDEX_RANGE when ws is given (ws: optional,
+ *   as for sti_window_idxs).
+ * Supported: dim a multiple of 64; x and codes 16-byte aligned, codes_bstride a multiple of 16 (the scales
+ * may lie anywhere), both strides covering n_rows rows; m * dim < 2^31.
+ */
+#define STI_FP4_E4M3_16 0
+#define STI_FP4_E8M0_32 1
+sti_status sti_kv_append_fp4(const uint16_t *x, int64_t x_bstride, const int32_t *start_pos, const int32_t *dropped,
+                             int b, int seqlen, int ratio, int dim, int format, uint8_t *codes, int64_t codes_bstride,
+                             uint8_t *scales, int64_t scales_bstride, int n_rows, int32_t *row_pos,
+                             int64_t row_pos_bstride, float *row_weight, int64_t row_weight_bstride, void *ws,
+                             sti_stream stream);
+
+/*
+ * sti_attn_fp4kv: attention of every query over all the rows it sees, the row serving as key and value
+ * for all heads.  Query (b, t) sees the first vis = (start_pos[b] + t + 1) // ratio - dropped[b] rows
+ * (clamped to [0, n_rows]):
+ *   s_hj = softmax_scale * q[b,t,h,:] . row_j,   j < vis
+ *   L_h  = ln( sum_j e^{s_hj} + e^{attn_sink[h]} + e^{prev_lse[b,t,h]} )
+ *   out[b,t,h,:] = ( sum_j e^{s_hj} row_j + e^{prev_lse} prev_out[b,t,h,:] ) / e^{L_h},   lse = L_h
+ *   row_weight[b,j] += sum_{t,h} e^{s_hj - L_h}
+ * A query that sees no row: out = prev_out and lse = prev_lse, or 0 and -inf without them (the sink then
+ * plays no part, as in sti_sparse_attn_sink).  Rows past vis are never used, whatever they hold.
+ *   codes / scales: fp4 rows as STI_FP4_E4M3_16 above
+ *   attn_sink: fp32 [h] or NULL (no sink; also when prev_lse already counts it)
+ *   prev_out, prev_lse: bf16 [b, seqlen, h, d] and fp32 [b, seqlen, h], or both NULL: the same queries'
+ *      attention over other rows (a window's: out and lse of sti_sparse_attn_sink), joined here.  Where
+ *      prev_lse is -inf, prev_out is not used.
+ *   lse: fp32 [b, seqlen, h] or NULL;  row_weight: fp32 [b, n_rows] (batch stride in elements) or NULL
+ * out may be prev_out itself; otherwise the outputs must not overlap the inputs.
+ * f16 tensor-core MMAs over the exactly decoded rows with fp32 accumulation, fp32 online softmax, P rounded
+ * to f16 for the PV product, bf16 output; results do not depend on the timing of the GPU (no atomics).
+ * Two kernels, one or two more with row_weight.
+ * Supported: 1 <= h <= 64, d a multiple of 64 up to 512; q, out, prev_out, codes 16-byte aligned and
+ * codes_bstride a multiple of 16, scales 4-byte aligned and scales_bstride a multiple of 4, both strides
+ * covering n_rows rows.  ws: sti_attn_fp4kv_workspace_size() bytes.
+ */
+size_t sti_attn_fp4kv_workspace_size(int b, int seqlen, int h, int d, int n_rows);
+sti_status sti_attn_fp4kv(const uint16_t *q, const uint8_t *codes, int64_t codes_bstride, const uint8_t *scales,
+                          int64_t scales_bstride, int n_rows, const int32_t *start_pos, const int32_t *dropped,
+                          int ratio, const float *attn_sink, float softmax_scale, const uint16_t *prev_out,
+                          const float *prev_lse, int b, int seqlen, int h, int d, uint16_t *out, float *lse,
+                          float *row_weight, int64_t row_weight_bstride, void *ws, size_t ws_bytes, sti_stream stream);
+
+/*
+ * sti_kv_evict: bring every sequence that holds more than `budget` rows back to budget rows.  Of its rows
+ * stay, in this order until the budget is full: those of the first n_first groups and of the latest n_recent
+ * ones (row_pos < n_first or row_pos >= G - n_recent); then by row_weight, largest first (a NaN counts as the
+ * largest); equal ones by row, lowest first.  Freed rows below the budget are refilled by the rows that
+ * stay at or above it, in ascending order on both sides; a moved row takes its row_weight, its row_pos
+ * and its row of every array in `arrays` along (the caches that share the rows).  Then
+ * dropped[b] += held - budget; rows at and above the budget keep what they held.  Sequences within the
+ * budget are left as they are.
+ *   row_weight: fp32 [b, n_rows], row_pos: int32 [b, n_rows] (batch strides in elements)
+ *   arrays: n_arrays <= 16 arrays [b, n_rows, row_bytes], batch strides in bytes (a host array, read during
+ *      the call)
+ * Supported: budget >= n_first + n_recent; row_bytes <= 65536.
+ * ws: sti_kv_evict_workspace_size() bytes.
+ */
+typedef struct sti_row_array {
+    void *base;
+    int64_t bstride;    /* bytes */
+    int64_t row_bytes;
+} sti_row_array;
+size_t sti_kv_evict_workspace_size(int b, int n_rows, int budget);
+sti_status sti_kv_evict(float *row_weight, int64_t row_weight_bstride, int32_t *row_pos, int64_t row_pos_bstride,
+                        const int32_t *start_pos, int32_t *dropped, int b, int seqlen, int ratio, int n_rows,
+                        int budget, int n_first, int n_recent, const sti_row_array *arrays, int n_arrays, void *ws,
+                        size_t ws_bytes, sti_stream stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 /*
  * Not an operation of the paper: a check of the library's failure handling.  Every wait in the

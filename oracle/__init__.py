@@ -270,6 +270,113 @@ def sparse_attn_fp4kv(q, kv1, kv2_codes, kv2_scales, sink, idx, scale: float, th
     return sparse_attn(q, kv1, sink, idx, scale, kv2=kv2, threads=threads, rope_cs=rope_cs)
 
 
+# ------------------------------------------------------------------ bounded 4-bit cache
+#
+# The cache that sti_kv_append_fp4 / sti_attn_fp4kv / sti_kv_evict keep (include/sti.h states the rules), in
+# numpy fp64.  start_pos, dropped: [b]; groups complete after a step: (start_pos + seqlen) // ratio.
+
+
+def fp4_rows(x, fmt: str):
+    """Rows [..., dim] -> (codes, scales) in format "e4m3" (groups of 16) or "e8m0" (groups of 32); a group
+    holding a NaN gets the NaN scale byte and zero codes, infinities saturate."""
+    x = np.asarray(x, dtype=np.float64)
+    group, quantize, nan_byte = (16, kvfp4_quantize, 0x7F) if fmt == "e4m3" else (32, mxfp4_quantize, 0xFF)
+    blk = x.reshape(x.shape[:-1] + (x.shape[-1] // group, group))
+    bad = np.isnan(blk).any(axis=-1)
+    inf = np.isinf(blk).any(axis=-1) & ~bad
+    # every scale saturates below 2^130; in a saturated group only infinities and signs remain to be told
+    clean = np.where(bad[..., None], 0.0, np.clip(blk, -2.0 ** 140, 2.0 ** 140))
+    codes, scales = quantize(clean.reshape(x.shape))
+    scales = np.where(bad, nan_byte, scales).astype(np.uint8)
+    assert not (inf & (scales < (0x7E if fmt == "e4m3" else 254))).any()
+    return codes, scales
+
+
+def kv_append_fp4(x, start_pos, dropped, seqlen: int, ratio: int, fmt: str, codes, scales, row_pos=None,
+                  row_weight=None) -> bool:
+    """Write the completed groups' rows into codes / scales (and row_pos, row_weight) in place; True when
+    a row fell outside the cache."""
+    outside = False
+    for b in range(len(x)):
+        first, end = int(start_pos[b]) // ratio, (int(start_pos[b]) + seqlen) // ratio
+        for i in range(end - first):
+            row = first + i - int(dropped[b])
+            if not 0 <= row < codes.shape[1]:
+                outside = True
+                continue
+            codes[b, row], scales[b, row] = fp4_rows(x[b, i], fmt)
+            if row_pos is not None:
+                row_pos[b, row] = first + i
+            if row_weight is not None:
+                row_weight[b, row] = 0.0
+    return outside
+
+
+def attn_fp4kv(q, codes, scales, start_pos, ratio: int, scale: float, sink=None, dropped=None, prev_out=None,
+               prev_lse=None):
+    """Attention over every visible row.  q: float [b, s, h, d]; returns (out, lse, weights [b, rows],
+    mass [b, s, h, d] = the sum of the absolute values that out averages)."""
+    q = np.asarray(q, dtype=np.float64)
+    b, s, h, d = q.shape
+    rows = codes.shape[1]
+    out, mass = np.zeros((b, s, h, d)), np.zeros((b, s, h, d))
+    lse = np.full((b, s, h), -np.inf)
+    weights = np.zeros((b, rows))
+    for i in range(b):
+        kv = kvfp4_decode(codes[i], scales[i], d)
+        for t in range(s):
+            n = (int(start_pos[i]) + t + 1) // ratio - (0 if dropped is None else int(dropped[i]))
+            n = min(rows, max(0, n))
+            x = scale * (q[i, t] @ kv[:n].T)                                   # [h, n]
+            parts = [x]
+            if n and sink is not None:
+                parts.append(np.asarray(sink, dtype=np.float64)[:, None])
+            if prev_lse is not None:
+                parts.append(np.asarray(prev_lse[i, t], dtype=np.float64)[:, None])
+            z = np.concatenate(parts, axis=1)
+            if z.shape[1] == 0:
+                continue
+            top = z.max(axis=1, keepdims=True)
+            with np.errstate(invalid="ignore", divide="ignore"):
+                e = np.where(np.isneginf(top), 0.0, np.exp(z - np.where(np.isneginf(top), 0.0, top)))
+                den = e.sum(axis=1, keepdims=True)
+                p = np.where(den > 0, e / den, np.where(np.isnan(den), np.nan, 0.0))
+                lse[i, t] = (top + np.log(den))[:, 0]
+            out[i, t], mass[i, t] = p[:, :n] @ kv[:n], p[:, :n] @ np.abs(kv[:n])
+            if prev_lse is not None:
+                po = np.where(p[:, -1:] == 0, 0.0, np.asarray(prev_out[i, t], dtype=np.float64))
+                out[i, t] += p[:, -1:] * po
+                mass[i, t] += p[:, -1:] * np.abs(po)
+            weights[i, :n] += p[:, :n].sum(axis=0)
+    return out, lse, weights, mass
+
+
+def kv_evict(row_weight, row_pos, start_pos, seqlen: int, ratio: int, dropped, budget: int, n_first: int, n_recent: int,
+             arrays=()) -> None:
+    """Evict in place: the rows that stay are the protected ones, then the most attended, ties to the lower
+    row; rows that stay at or above the budget move into the freed rows below it, both in ascending order."""
+    rows = row_weight.shape[1]
+    for b in range(len(row_weight)):
+        groups = (int(start_pos[b]) + seqlen) // ratio
+        held = min(rows, max(0, groups - int(dropped[b])))
+        if held <= budget:
+            continue
+        pos, w = row_pos[b, :held].astype(np.int64), row_weight[b, :held].astype(np.float64)
+        safe = (pos < n_first) | (pos >= groups - n_recent)
+        nan = np.isnan(w)
+        order = np.lexsort((np.arange(held), -np.where(nan, 0.0, w), ~nan, ~safe))   # last key first
+        # protected rows tie with each other whatever their weight
+        order = np.concatenate([np.flatnonzero(safe), order[~safe[order]]])
+        keep = np.zeros(held, dtype=bool)
+        keep[order[:budget]] = True
+        free = np.flatnonzero(~keep[:budget])
+        move = budget + np.flatnonzero(keep[budget:])
+        for a in (row_weight, row_pos, *arrays):
+            a[b, free[:len(move)]] = a[b, move]
+        assert len(free) == len(move)
+        dropped[b] += held - budget
+
+
 def _bf16_exact(x) -> np.ndarray:
     """float64 values exactly representable in bf16 -> their bit patterns (checked)."""
     f = np.asarray(x, dtype=np.float32)

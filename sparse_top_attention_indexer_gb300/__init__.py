@@ -9,9 +9,11 @@ here, and a missing library is an error.
 
 Functions mirror the C entry points (``sti_`` prefix dropped):
   window_idxs, idx_scores, idx_topk, sparse_attn_sink, decode_fused, read_device_status
+and, for a bounded 4-bit cache, kv_append_fp4, attn_fp4kv, kv_evict.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -34,7 +36,10 @@ EXPORTS = ["sti_status_string", "sti_last_cuda_error", "sti_version", "sti_read_
            "sti_sparse_attn_sink_fp4kv",
            "sti_decode_workspace_size",
            "sti_decode_fused", "sti_decode_kernel_count", "sti_decode_fused_noalloc", "sti_decode_noalloc_status",
-           "sti_selftest_wait_timeout", "sti_window_idxs_chunked", "sti_idx_scores_mxfp4"]
+           "sti_selftest_wait_timeout", "sti_window_idxs_chunked", "sti_idx_scores_mxfp4",
+           "sti_kv_append_fp4", "sti_attn_fp4kv_workspace_size", "sti_attn_fp4kv", "sti_kv_evict_workspace_size",
+           "sti_kv_evict"]
+FP4_E4M3_16, FP4_E8M0_32 = 0, 1
 
 
 class StiError(RuntimeError):
@@ -60,6 +65,12 @@ class DecodeArgs(ctypes.Structure):
         ("comp_codes", ctypes.c_void_p), ("comp_codes_bstride", ctypes.c_int64), ("comp_scales", ctypes.c_void_p),
         ("comp_scales_bstride", ctypes.c_int64),
     ]
+
+
+class RowArray(ctypes.Structure):
+    """Mirror of sti_row_array."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("bstride", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -109,6 +120,14 @@ def lib() -> ctypes.CDLL:
         L.sti_decode_fused_noalloc.restype = I
         L.sti_decode_noalloc_status.argtypes = [P, P]
         L.sti_decode_noalloc_status.restype = I
+        L.sti_kv_append_fp4.argtypes = [P, I64, P, P, I, I, I, I, I, P, I64, P, I64, I, P, I64, P, I64, P, P]
+        L.sti_kv_append_fp4.restype = I
+        L.sti_attn_fp4kv_workspace_size.argtypes, L.sti_attn_fp4kv_workspace_size.restype = [I, I, I, I, I], SZ
+        L.sti_attn_fp4kv.argtypes = [P, P, I64, P, I64, I, P, P, I, P, F, P, P, I, I, I, I, P, P, P, I64, P, SZ, P]
+        L.sti_attn_fp4kv.restype = I
+        L.sti_kv_evict_workspace_size.argtypes, L.sti_kv_evict_workspace_size.restype = [I, I, I], SZ
+        L.sti_kv_evict.argtypes = [P, I64, P, I64, P, P, I, I, I, I, I, I, I, ctypes.POINTER(RowArray), I, P, SZ, P]
+        L.sti_kv_evict.restype = I
         _lib = L
     return _lib
 
@@ -429,6 +448,177 @@ def decode_noalloc_status(stream=None) -> int:
     flags = ctypes.c_uint32(0)
     lib().sti_decode_noalloc_status(ctypes.byref(flags), _stream(stream))
     return int(flags.value)
+
+
+# ---------------------------------------------------------------------------- bounded 4-bit cache
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The tensors' device and the call's stream (a torch stream, a raw handle, or None: the device's
+    current one) as the current ones, so that what the call allocates belongs to that stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device)
+            if s.device != torch.device(device):
+                raise ValueError(f"stream is on {s.device}, the tensors on {device}")
+            with torch.cuda.stream(s):
+                yield
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
+
+
+def _call_workspace(nbytes: int, device) -> torch.Tensor:
+    """A workspace for one call: only its status word has to start at zero."""
+    ws = torch.empty(max(256, int(nbytes)), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _rows_of(t, dtype, name, b, inner, n_rows=None):
+    """[b, rows, inner] (or [b, rows] when inner is None) with contiguous rows; returns rows."""
+    _need(t, dtype, name, contiguous=False)
+    shape = "[b, rows]" if inner is None else f"[b, rows, {inner}]"
+    if t.dim() != (2 if inner is None else 3) or t.shape[0] != b or (inner is not None and t.shape[2] != inner):
+        raise ValueError(f"{name} must be {shape}")
+    if t.numel() and (t.stride(-1) != 1 or (inner is not None and t.stride(1) != inner)):
+        raise ValueError(f"{name} must be {shape} with contiguous rows")
+    if n_rows is not None and t.shape[1] < n_rows:
+        raise ValueError(f"{name} must hold at least {n_rows} rows")
+    return t.shape[1]
+
+
+def _bstride(t) -> int:
+    """Elements between sequences; of a single sequence, whose stride may be anything, its own size."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else 0
+
+
+def _per_sequence(t, name, b):
+    if t is not None:
+        _need(t, torch.int32, name)
+        if t.numel() != b:
+            raise ValueError(f"{name} must hold one value per sequence")
+
+
+def kv_append_fp4(x: torch.Tensor, start_pos: torch.Tensor, seqlen: int, ratio: int, codes: torch.Tensor,
+                  scales: torch.Tensor, dropped: torch.Tensor | None = None, row_pos: torch.Tensor | None = None,
+                  row_weight: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise the rows that a step of seqlen tokens at start_pos completes and write them into the
+    cache (sti_kv_append_fp4).  x: bf16 [b, ceil(seqlen / ratio), dim]; codes: uint8 [b, rows, dim/2];
+    scales: uint8 [b, rows, dim/16] (E4M3 scales) or [b, rows, dim/32] (MXFP4).  row_pos int32 [b, rows]
+    and row_weight fp32 [b, rows] of the rows written become their group number and 0."""
+    _need(x, torch.bfloat16, "x", contiguous=False)
+    if x.dim() != 3 or seqlen < 1 or ratio < 1 or x.shape[1] != -(-seqlen // ratio):
+        raise ValueError("x must be [b, ceil(seqlen / ratio), dim]")
+    b, _, dim = x.shape
+    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != dim)):
+        raise ValueError("x must have contiguous rows")
+    if dim % 64:
+        raise ValueError("dim must be a multiple of 64")
+    _per_sequence(start_pos, "start_pos", b)
+    _per_sequence(dropped, "dropped", b)
+    n_rows = _rows_of(codes, torch.uint8, "codes", b, dim // 2)
+    if scales.dim() != 3 or scales.shape[2] not in (dim // 16, dim // 32):
+        raise ValueError(f"scales must be [b, rows, {dim // 16}] (E4M3) or [b, rows, {dim // 32}] (MXFP4)")
+    fmt = FP4_E4M3_16 if scales.shape[2] == dim // 16 else FP4_E8M0_32
+    _rows_of(scales, torch.uint8, "scales", b, scales.shape[2], n_rows)
+    if row_pos is not None:
+        _rows_of(row_pos, torch.int32, "row_pos", b, None, n_rows)
+    if row_weight is not None:
+        _rows_of(row_weight, torch.float32, "row_weight", b, None, n_rows)
+    _same_device(x.device, start_pos, codes, scales, dropped, row_pos, row_weight, ws)
+    with _on(x.device, stream):
+        _check(lib().sti_kv_append_fp4(
+            _ptr(x), _bstride(x), _ptr(start_pos), _ptr(dropped), b, seqlen, ratio, dim, fmt, _ptr(codes),
+            _bstride(codes), _ptr(scales), _bstride(scales), n_rows, _ptr(row_pos), _bstride(row_pos), _ptr(row_weight),
+            _bstride(row_weight), _ptr(ws), _stream(None)), "sti_kv_append_fp4")
+
+
+def attn_fp4kv_workspace_size(b: int, s: int, h: int, d: int, n_rows: int) -> int:
+    return int(lib().sti_attn_fp4kv_workspace_size(b, s, h, d, n_rows))
+
+
+def attn_fp4kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, start_pos: torch.Tensor, ratio: int,
+               softmax_scale: float, attn_sink: torch.Tensor | None = None, dropped: torch.Tensor | None = None,
+               prev_out: torch.Tensor | None = None, prev_lse: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               row_weight: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q [b, s, h, d] over every row of a 4-bit cache that each query sees
+    (sti_attn_fp4kv).  codes uint8 [b, rows, d/2], scales uint8 [b, rows, d/16]; prev_out / prev_lse: the
+    same queries' attention over other rows, joined into the result; lse (fp32 [b, s, h]) is written and
+    row_weight (fp32 [b, rows]) added to when given."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [b, s, h, d]")
+    b, s, h, d = q.shape
+    n_rows = _rows_of(codes, torch.uint8, "codes", b, d // 2)
+    _rows_of(scales, torch.uint8, "scales", b, d // 16, n_rows)
+    _per_sequence(start_pos, "start_pos", b)
+    _per_sequence(dropped, "dropped", b)
+    for name, t, dtype, shape in (("attn_sink", attn_sink, torch.float32, (h,)),
+                                  ("prev_out", prev_out, torch.bfloat16, (b, s, h, d)),
+                                  ("prev_lse", prev_lse, torch.float32, (b, s, h)),
+                                  ("out", out, torch.bfloat16, (b, s, h, d)), ("lse", lse, torch.float32, (b, s, h))):
+        if t is not None:
+            _need(t, dtype, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+    if row_weight is not None:
+        _rows_of(row_weight, torch.float32, "row_weight", b, None, n_rows)
+    _same_device(q.device, codes, scales, start_pos, attn_sink, dropped, prev_out, prev_lse, out, lse, row_weight, ws)
+    with _on(q.device, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if ws is None:
+            ws = _call_workspace(attn_fp4kv_workspace_size(b, s, h, d, n_rows), q.device)
+        _check(lib().sti_attn_fp4kv(
+            _ptr(q), _ptr(codes), _bstride(codes), _ptr(scales), _bstride(scales), n_rows, _ptr(start_pos), _ptr(dropped), ratio,
+            _ptr(attn_sink), float(softmax_scale), _ptr(prev_out), _ptr(prev_lse), b, s, h, d, _ptr(out),
+            _ptr(lse), _ptr(row_weight), _bstride(row_weight), _ptr(ws), ws.numel(), _stream(None)), "sti_attn_fp4kv")
+    return out
+
+
+def kv_evict_workspace_size(b: int, n_rows: int, budget: int) -> int:
+    return int(lib().sti_kv_evict_workspace_size(b, n_rows, budget))
+
+
+def kv_evict(row_weight: torch.Tensor, row_pos: torch.Tensor, start_pos: torch.Tensor, seqlen: int, ratio: int,
+             dropped: torch.Tensor, budget: int, n_first: int = 0, n_recent: int = 0, arrays=(),
+             ws: torch.Tensor | None = None, stream=None) -> None:
+    """Bring every sequence of a cache back to `budget` rows after a step of seqlen tokens at start_pos,
+    keeping the most attended ones (sti_kv_evict).  row_weight fp32 and row_pos int32 [b, rows]; arrays:
+    the tensors [b, rows, ...] (any type, rows contiguous) whose rows move along; dropped int32 [b] is
+    advanced."""
+    if row_weight.dim() != 2:
+        raise ValueError("row_weight must be [b, rows]")
+    b = row_weight.shape[0]
+    n_rows = _rows_of(row_weight, torch.float32, "row_weight", b, None)
+    _rows_of(row_pos, torch.int32, "row_pos", b, None, n_rows)
+    _per_sequence(start_pos, "start_pos", b)
+    _per_sequence(dropped, "dropped", b)
+    arr = (RowArray * max(1, len(arrays)))()
+    for i, t in enumerate(arrays):
+        if not t.is_cuda or t.dim() < 2 or t.shape[0] != b or t.shape[1] < n_rows:
+            raise ValueError(f"arrays[{i}] must be a CUDA tensor [b, at least {n_rows} rows, ...]")
+        row = t[0, 0].numel() if t.numel() else 1
+        if t.numel() and (t.stride(1) != row or not t[0, 0].is_contiguous()):
+            raise ValueError(f"arrays[{i}] must have contiguous rows")
+        arr[i].base, arr[i].bstride = _ptr(t), _bstride(t) * t.element_size()
+        arr[i].row_bytes = row * t.element_size()
+    _same_device(row_weight.device, row_pos, start_pos, dropped, ws, *arrays)
+    with _on(row_weight.device, stream):
+        if ws is None:
+            ws = _call_workspace(kv_evict_workspace_size(b, n_rows, budget), row_weight.device)
+        _check(lib().sti_kv_evict(
+            _ptr(row_weight), _bstride(row_weight), _ptr(row_pos), _bstride(row_pos), _ptr(start_pos), _ptr(dropped), b,
+            seqlen, ratio, n_rows, budget, n_first, n_recent, arr, len(arrays), _ptr(ws), ws.numel(), _stream(None)),
+            "sti_kv_evict")
 
 
 def selftest_wait_timeout(ws: torch.Tensor, limit_us: int = 2000, stream=None) -> None:

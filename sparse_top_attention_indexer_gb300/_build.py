@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsti.so")
 SOURCES = ["api.cu", "idx_scores.cu", "idx_topk.cu", "sparse_attn.cu", "sparse_attn_stream.cu", "sparse_attn_hs.cu",
-           "decode_attn.cu"]
+           "decode_attn.cu", "kv_append.cu", "attn_fp4.cu", "kv_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -462,7 +462,7 @@ const char* sti_status_string(sti_status s) {
 
 const char* sti_last_cuda_error(void) { return g_last_cuda_error; }
 
-int sti_version(void) { return 100; }
+int sti_version(void) { return 200; }
 
 sti_status sti_read_device_status(void* ws, uint32_t* flags, sti_stream stream) {
     if (!ws) return STI_ERR_INVALID_ARG;
@@ -850,6 +850,203 @@ sti_status sti_decode_fused_noalloc(const sti_decode_args* a, sti_stream stream)
                      a->topk_idxs, k_total, a->softmax_scale, a->b, 1, a->h, a->d, k_total, a->out, nullptr, status,
                      acc, acc_used, st, /*pdl=*/a->n_cols > 0 && !a->q_ready, /*win_ring=*/W, a->start_pos,
                      a->rope_cs, a->rope_dims);
+}
+
+// ---------------------------------------------------------------------- bounded 4-bit cache
+
+// [a, a + an) and [b, b + bn) share a byte
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + bn && y < x + an;
+}
+
+// A cache array [b, n_rows, row_bytes]: base and batch stride aligned, the stride covering n_rows rows.
+static bool rows_ok(const void* base, int64_t bstride, int n_rows, int64_t row_bytes, int align) {
+    return base && aligned(base, align) && bstride % align == 0 && bstride >= (int64_t)n_rows * row_bytes;
+}
+
+sti_status sti_kv_append_fp4(const uint16_t* x, int64_t x_bstride, const int32_t* start_pos, const int32_t* dropped,
+                             int b, int seqlen, int ratio, int dim, int format, uint8_t* codes, int64_t codes_bstride,
+                             uint8_t* scales, int64_t scales_bstride, int n_rows, int32_t* row_pos,
+                             int64_t row_pos_bstride, float* row_weight, int64_t row_weight_bstride, void* ws,
+                             sti_stream stream) {
+    if (ws && !aligned(ws, sti::kWsAlign)) return STI_ERR_INVALID_ARG;
+    if (b < 0 || seqlen < 1 || ratio < 1 || dim < 1 || n_rows < 0) return STI_ERR_INVALID_ARG;
+    if (format != STI_FP4_E4M3_16 && format != STI_FP4_E8M0_32) return STI_ERR_INVALID_ARG;
+    const int64_t m = ((int64_t)seqlen + ratio - 1) / ratio;
+    if (dim % 64 != 0 || m * dim > 0x7FFFFFFF) return STI_ERR_UNSUPPORTED;
+    if (b == 0) return STI_OK;
+    const bool mx = format == STI_FP4_E8M0_32;
+    if (!x || !start_pos || !aligned(x, 16) || x_bstride % 8 != 0 || (b > 1 && x_bstride < m * dim))
+        return STI_ERR_INVALID_ARG;
+    if (!rows_ok(codes, codes_bstride, n_rows, dim / 2, 16) ||
+        !rows_ok(scales, scales_bstride, n_rows, dim / (mx ? 32 : 16), 1))
+        return STI_ERR_INVALID_ARG;
+    if ((row_pos && row_pos_bstride < n_rows) || (row_weight && row_weight_bstride < n_rows)) return STI_ERR_INVALID_ARG;
+    sti::KvAppendParams p{};
+    p.x = x;
+    p.x_bstride = x_bstride;
+    p.start_pos = start_pos;
+    p.dropped = dropped;
+    p.codes = codes;
+    p.codes_bstride = codes_bstride;
+    p.scales = scales;
+    p.scales_bstride = scales_bstride;
+    p.row_pos = row_pos;
+    p.row_pos_bstride = row_pos_bstride;
+    p.row_weight = row_weight;
+    p.row_weight_bstride = row_weight_bstride;
+    p.status = ws ? status_word(ws) : nullptr;
+    p.B = b;
+    p.m = (int)m;
+    p.s = seqlen;
+    p.ratio = ratio;
+    p.dim = dim;
+    p.n_rows = n_rows;
+    const cudaError_t e = sti::launch_kv_append(p, mx, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_kv_append_fp4");
+}
+
+// attention workspace: [status | split records | partial (max, sum) | partial outputs | lse | partial row
+// weights].  Sized for the largest GB300 (160 SMs), whatever device is current.
+static constexpr int kAttnFp4MaxSms = 160;
+struct AttnFp4Layout {
+    size_t rec, ml, o, lse, w, end;
+    int grid, w_grid, w_split;
+};
+static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows) {
+    AttnFp4Layout l;
+    sti::attn_fp4_plan(b, seqlen, n_rows, kAttnFp4MaxSms, &l.grid, &l.w_grid, &l.w_split);
+    auto after = [](size_t at, size_t bytes) { return sti::align_up(at + bytes, sti::kWsAlign); };
+    l.rec = sti::kWsStatusBytes;
+    l.ml = after(l.rec, (size_t)l.grid * sizeof(int2));
+    l.o = after(l.ml, (size_t)2 * l.grid * 64 * sizeof(float2));
+    l.lse = after(l.o, (size_t)2 * l.grid * h * d * sizeof(float));
+    l.w = after(l.lse, (size_t)b * seqlen * h * sizeof(float));
+    l.end = after(l.w, l.w_split > 1 ? (size_t)l.w_split * b * n_rows * sizeof(float) : 0);
+    return l;
+}
+
+size_t sti_attn_fp4kv_workspace_size(int b, int seqlen, int h, int d, int n_rows) {
+    if (b <= 0 || seqlen < 1 || h < 1 || h > 64 || d < 1 || d > 512 || n_rows < 0) return sti::kWsStatusBytes;
+    return attn_fp4_layout(b, seqlen, h, d, n_rows).end;
+}
+
+sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes_bstride, const uint8_t* scales,
+                          int64_t scales_bstride, int n_rows, const int32_t* start_pos, const int32_t* dropped,
+                          int ratio, const float* attn_sink, float softmax_scale, const uint16_t* prev_out,
+                          const float* prev_lse, int b, int seqlen, int h, int d, uint16_t* out, float* lse,
+                          float* row_weight, int64_t row_weight_bstride, void* ws, size_t ws_bytes,
+                          sti_stream stream) {
+    if (b < 0 || seqlen < 1 || h < 1 || d < 1 || n_rows < 0 || ratio < 1) return STI_ERR_INVALID_ARG;
+    if (h > 64 || d % 64 != 0 || d > 512 || (int64_t)b * seqlen > 0x3FFFFFFF) return STI_ERR_UNSUPPORTED;
+    if (!prev_out != !prev_lse) return STI_ERR_INVALID_ARG;
+    if (b == 0) return STI_OK;
+    if (!ws_ok(ws, ws_bytes, sti_attn_fp4kv_workspace_size(b, seqlen, h, d, n_rows))) return STI_ERR_INVALID_ARG;
+    if (!q || !start_pos || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(prev_out, 16))
+        return STI_ERR_INVALID_ARG;
+    if (n_rows > 0 &&
+        (!rows_ok(codes, codes_bstride, n_rows, d / 2, 16) || !rows_ok(scales, scales_bstride, n_rows, d / 16, 4)))
+        return STI_ERR_INVALID_ARG;
+    if (row_weight && row_weight_bstride < n_rows) return STI_ERR_INVALID_ARG;
+    const size_t o_bytes = (size_t)b * seqlen * h * d * 2, l_bytes = (size_t)b * seqlen * h * 4;
+    if (overlap(out, o_bytes, q, o_bytes) || (out != prev_out && overlap(out, o_bytes, prev_out, o_bytes)) ||
+        overlap(lse, l_bytes, prev_lse, l_bytes))
+        return STI_ERR_INVALID_ARG;
+    const AttnFp4Layout l = attn_fp4_layout(b, seqlen, h, d, n_rows);
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    sti::AttnFp4Params p{};
+    p.q = q;
+    p.codes = codes;
+    p.codes_bstride = codes_bstride;
+    p.scales = scales;
+    p.scales_bstride = scales_bstride;
+    p.start_pos = start_pos;
+    p.dropped = dropped;
+    p.sink = attn_sink;
+    p.prev_out = prev_out;
+    p.prev_lse = prev_lse;
+    p.out = out;
+    p.lse = lse ? lse : row_weight ? reinterpret_cast<float*>(wsb + l.lse) : nullptr;
+    p.row_weight = row_weight;
+    p.row_weight_bstride = row_weight_bstride;
+    p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+    p.B = b;
+    p.s = seqlen;
+    p.h = h;
+    p.d = d;
+    p.n_rows = n_rows;
+    p.ratio = ratio;
+    p.status = status_word(ws);
+    p.rec = reinterpret_cast<int2*>(wsb + l.rec);
+    p.part_ml = reinterpret_cast<float2*>(wsb + l.ml);
+    p.part_o = reinterpret_cast<float*>(wsb + l.o);
+    p.w_part = reinterpret_cast<float*>(wsb + l.w);
+    const int sms = sti::device_num_sms();
+    sti::attn_fp4_plan(b, seqlen, n_rows, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms, &p.grid, &p.w_grid, &p.w_split);
+    const cudaError_t e = sti::launch_attn_fp4(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_attn_fp4kv");
+}
+
+// eviction workspace: [status | row lists int32 [b, 2, most]], most = the rows that can move
+static int evict_most(int n_rows, int budget) { return budget < n_rows - budget ? budget : n_rows - budget; }
+
+size_t sti_kv_evict_workspace_size(int b, int n_rows, int budget) {
+    if (b <= 0 || budget < 0 || n_rows <= budget) return sti::kWsStatusBytes;
+    return sti::align_up(sti::kWsStatusBytes + (size_t)b * 2 * evict_most(n_rows, budget) * sizeof(int32_t), sti::kWsAlign);
+}
+
+sti_status sti_kv_evict(float* row_weight, int64_t row_weight_bstride, int32_t* row_pos, int64_t row_pos_bstride,
+                        const int32_t* start_pos, int32_t* dropped, int b, int seqlen, int ratio, int n_rows,
+                        int budget, int n_first, int n_recent, const sti_row_array* arrays, int n_arrays, void* ws,
+                        size_t ws_bytes, sti_stream stream) {
+    if (b < 0 || seqlen < 1 || ratio < 1 || n_rows < 0 || budget < 0 || n_first < 0 || n_recent < 0 || n_arrays < 0)
+        return STI_ERR_INVALID_ARG;
+    if ((int64_t)n_first + n_recent > budget || n_arrays > 16 || (n_arrays > 0 && !arrays)) return STI_ERR_INVALID_ARG;
+    if (b > 0x7FFFFFFF / 8) return STI_ERR_UNSUPPORTED;
+    if (b == 0) return STI_OK;
+    for (int i = 0; i < n_arrays; ++i) {
+        const sti_row_array& a = arrays[i];
+        if (a.row_bytes < 1 || (n_rows > 0 && !a.base) || a.bstride < n_rows * a.row_bytes) return STI_ERR_INVALID_ARG;
+        if (a.row_bytes > 65536) return STI_ERR_UNSUPPORTED;
+    }
+    if (n_rows <= budget) return STI_OK;   // nothing can be over the budget
+    if (!ws_ok(ws, ws_bytes, sti_kv_evict_workspace_size(b, n_rows, budget))) return STI_ERR_INVALID_ARG;
+    if (!row_weight || !row_pos || !start_pos || !dropped || row_weight_bstride < n_rows || row_pos_bstride < n_rows)
+        return STI_ERR_INVALID_ARG;
+    sti::KvEvictParams p{};
+    p.row_weight = row_weight;
+    p.row_weight_bstride = row_weight_bstride;
+    p.row_pos = row_pos;
+    p.row_pos_bstride = row_pos_bstride;
+    p.start_pos = start_pos;
+    p.dropped = dropped;
+    p.lists = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + sti::kWsStatusBytes);
+    p.B = b;
+    p.s = seqlen;
+    p.ratio = ratio;
+    p.n_rows = n_rows;
+    p.budget = budget;
+    p.n_first = n_first;
+    p.n_recent = n_recent;
+    p.most = evict_most(n_rows, budget);
+    auto add = [&p](void* base, int64_t bstride, int64_t row_bytes) {
+        sti::MovedArray& a = p.arr[p.n_arr++];
+        a.base = base;
+        a.bstride = bstride;
+        a.row_bytes = row_bytes;
+        uint32_t piece = 16;
+        while (!aligned(base, piece) || bstride % piece != 0 || row_bytes % piece != 0) piece /= 2;
+        a.piece_bytes = piece;
+        a.pieces = (uint32_t)(row_bytes / piece);
+    };
+    for (int i = 0; i < n_arrays; ++i) add(arrays[i].base, arrays[i].bstride, arrays[i].row_bytes);
+    add(row_weight, row_weight_bstride * 4, 4);
+    add(row_pos, row_pos_bstride * 4, 4);
+    for (int i = 0; i < p.n_arr; ++i)
+        if ((uint64_t)p.most * p.arr[i].pieces > 0xFFFFFFFFu) return STI_ERR_UNSUPPORTED;
+    const cudaError_t e = sti::launch_kv_evict(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_kv_evict");
 }
 
 sti_status sti_selftest_wait_timeout(void* ws, size_t ws_bytes, uint32_t limit_us, sti_stream stream) {

@@ -149,6 +149,79 @@ cudaError_t launch_decode_topk_attn(const CUtensorMap& tm_q, const CUtensorMap& 
                                     const CUtensorMap& tm_comp_rows, const DecodeAttnParams& p, bool pdl,
                                     cudaStream_t stream);
 
+// ------------------------------------------------------------------ bounded fp4 cache: append, attend, evict
+struct KvAppendParams {
+    const uint16_t* x;          // bf16 [B, m, dim], batch stride x_bstride (elements)
+    int64_t x_bstride;
+    const int32_t* start_pos;   // [B]
+    const int32_t* dropped;     // [B] or null (none)
+    uint8_t* codes;             // [B, n_rows, dim/2], batch stride in bytes
+    int64_t codes_bstride;
+    uint8_t* scales;            // [B, n_rows, dim/16] (E4M3) or [B, n_rows, dim/32] (E8M0)
+    int64_t scales_bstride;
+    int32_t* row_pos;           // optional
+    int64_t row_pos_bstride;
+    float* row_weight;          // optional
+    int64_t row_weight_bstride;
+    uint32_t* status;           // optional
+    int B, m, s, ratio, dim, n_rows;
+};
+cudaError_t launch_kv_append(const KvAppendParams& p, bool mx, cudaStream_t stream);
+
+// One array whose rows move with the cache's: piece_bytes (16, 8, 4, 2 or 1) divides row_bytes, the base
+// and the batch stride.
+struct MovedArray {
+    void* base;
+    int64_t bstride;            // bytes
+    int64_t row_bytes;
+    uint32_t pieces;            // row_bytes / piece_bytes
+    uint32_t piece_bytes;
+};
+constexpr int kMaxMoved = 18;   // the caller's arrays (at most 16), row_weight, row_pos
+struct KvEvictParams {
+    float* row_weight;
+    int64_t row_weight_bstride;
+    int32_t* row_pos;
+    int64_t row_pos_bstride;
+    const int32_t* start_pos;
+    int32_t* dropped;
+    int32_t* lists;             // [B, 2, most]: rows moved to, rows moved from
+    int B, s, ratio, n_rows, budget, n_first, n_recent, most;
+    int n_arr;
+    MovedArray arr[kMaxMoved];
+};
+cudaError_t launch_kv_evict(const KvEvictParams& p, cudaStream_t stream);
+
+struct AttnFp4Params {
+    const uint16_t* q;          // bf16 [B, s, h, d]
+    const uint8_t* codes;       // [B, n_rows, d/2], batch stride in bytes
+    int64_t codes_bstride;
+    const uint8_t* scales;      // [B, n_rows, d/16]
+    int64_t scales_bstride;
+    const int32_t* start_pos;
+    const int32_t* dropped;     // or null
+    const float* sink;          // [h] or null
+    const uint16_t* prev_out;   // bf16 [B, s, h, d] or null
+    const float* prev_lse;      // [B, s, h] or null
+    uint16_t* out;
+    float* lse;                 // [B, s, h] or null (required by the row weights)
+    float* row_weight;          // [B, n_rows] or null
+    int64_t row_weight_bstride;
+    float scale_log2;           // softmax_scale * log2(e)
+    int B, s, h, d, n_rows, ratio;
+    uint32_t* status;
+    int grid;                   // CTAs of the attention kernel
+    int2* rec;                  // [grid]: the split query that starts in a CTA and its last CTA, or {-1, 0}
+    float* part_o;              // [2 * grid][h][d] unnormalised partial outputs
+    float2* part_ml;            // [2 * grid][64] running maximum (log2) and sum
+    int w_split;                // row weights: query splits (partial sums in w_part when > 1)
+    int w_grid;                 // row weights: CTAs, a multiple of w_split
+    float* w_part;              // [w_split][B][n_rows]
+};
+// CTAs of the attention kernel, of the row-weight kernel, and its query splits
+void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid, int* w_split);
+cudaError_t launch_attn_fp4(const AttnFp4Params& p, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device properties
 int device_num_sms();
 
