@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -142,6 +143,11 @@ def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream's handle on device `index`, without making a torch stream object."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -453,6 +459,9 @@ def decode_noalloc_status(stream=None) -> int:
 # ---------------------------------------------------------------------------- bounded 4-bit cache
 
 
+# These calls take a few microseconds on the GPU, so the checks are written to cost little on the host.
+
+
 @contextlib.contextmanager
 def _on(device, stream):
     """The tensors' device and the call's stream (a torch stream, a raw handle, or None: the device's
@@ -462,48 +471,58 @@ def _on(device, stream):
             yield
         else:
             s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device)
-            if s.device != torch.device(device):
+            if s.device != device:
                 raise ValueError(f"stream is on {s.device}, the tensors on {device}")
             with torch.cuda.stream(s):
                 yield
 
 
-def _same_device(device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"all tensors must be on {device}, got one on {t.device}")
+def _elsewhere(device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
 
 def _call_workspace(nbytes: int, device) -> torch.Tensor:
     """A workspace for one call: only its status word has to start at zero."""
-    ws = torch.empty(max(256, int(nbytes)), dtype=torch.uint8, device=device)
+    ws = torch.empty(max(256, nbytes), dtype=torch.uint8, device=device)
     ws[:256].zero_()
     return ws
 
 
-def _rows_of(t, dtype, name, b, inner, n_rows=None):
-    """[b, rows, inner] (or [b, rows] when inner is None) with contiguous rows; returns rows."""
-    _need(t, dtype, name, contiguous=False)
-    shape = "[b, rows]" if inner is None else f"[b, rows, {inner}]"
-    if t.dim() != (2 if inner is None else 3) or t.shape[0] != b or (inner is not None and t.shape[2] != inner):
-        raise ValueError(f"{name} must be {shape}")
-    if t.numel() and (t.stride(-1) != 1 or (inner is not None and t.stride(1) != inner)):
-        raise ValueError(f"{name} must be {shape} with contiguous rows")
-    if n_rows is not None and t.shape[1] < n_rows:
-        raise ValueError(f"{name} must hold at least {n_rows} rows")
-    return t.shape[1]
+def _dense(t, dtype, shape, device, name):
+    """Check a contiguous tensor of a given type, shape and device; its pointer (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
 
 
-def _bstride(t) -> int:
-    """Elements between sequences; of a single sequence, whose stride may be anything, its own size."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t[0].numel() if t.shape[0] else 0
+def _rows(t, dtype, b, n_rows, inner, device, name):
+    """Check [b, at least n_rows rows, inner] (inner 0: [b, rows]) with contiguous rows and any stride between
+    sequences; its pointer and that stride in elements (a single sequence's may be anything: its size)."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if (len(shape) != (3 if inner else 2) or shape[0] != b or shape[1] < n_rows or (inner and shape[2] != inner) or
+            (n_rows > 0 and b > 0 and (stride[-1] != 1 or (inner and shape[1] > 1 and stride[1] != inner)))):
+        raise ValueError(f"{name} must be [{b}, at least {n_rows} rows{', ' + str(inner) if inner else ''}] with "
+                         f"contiguous rows, got {list(shape)} with strides {list(stride)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr(), stride[0] if b > 1 else shape[1] * (inner or 1)
 
 
-def _per_sequence(t, name, b):
-    if t is not None:
-        _need(t, torch.int32, name)
-        if t.numel() != b:
-            raise ValueError(f"{name} must hold one value per sequence")
+def _workspace_ptr(ws, device):
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    return ws.data_ptr()
 
 
 def kv_append_fp4(x: torch.Tensor, start_pos: torch.Tensor, seqlen: int, ratio: int, codes: torch.Tensor,
@@ -512,32 +531,33 @@ def kv_append_fp4(x: torch.Tensor, start_pos: torch.Tensor, seqlen: int, ratio: 
     """Quantise the rows that a step of seqlen tokens at start_pos completes and write them into the
     cache (sti_kv_append_fp4).  x: bf16 [b, ceil(seqlen / ratio), dim]; codes: uint8 [b, rows, dim/2];
     scales: uint8 [b, rows, dim/16] (E4M3 scales) or [b, rows, dim/32] (MXFP4).  row_pos int32 [b, rows]
-    and row_weight fp32 [b, rows] of the rows written become their group number and 0."""
-    _need(x, torch.bfloat16, "x", contiguous=False)
-    if x.dim() != 3 or seqlen < 1 or ratio < 1 or x.shape[1] != -(-seqlen // ratio):
-        raise ValueError("x must be [b, ceil(seqlen / ratio), dim]")
-    b, _, dim = x.shape
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != dim)):
-        raise ValueError("x must have contiguous rows")
-    if dim % 64:
-        raise ValueError("dim must be a multiple of 64")
-    _per_sequence(start_pos, "start_pos", b)
-    _per_sequence(dropped, "dropped", b)
-    n_rows = _rows_of(codes, torch.uint8, "codes", b, dim // 2)
-    if scales.dim() != 3 or scales.shape[2] not in (dim // 16, dim // 32):
+    and row_weight fp32 [b, rows] of the rows written become their group number and 0.  ws: optional
+    workspace whose status word reports rows outside the cache."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a CUDA tensor")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_append_fp4(x, start_pos, seqlen, ratio, codes, scales, dropped, row_pos, row_weight, ws)
+    if x.dim() != 3 or seqlen < 1 or ratio < 1 or x.shape[2] % 64 or codes.dim() != 3 or scales.dim() != 3:
+        raise ValueError("x must be [b, ceil(seqlen / ratio), dim] with dim a multiple of 64, codes and scales [b, rows, *]")
+    b, m, dim = x.shape
+    if m != -(-seqlen // ratio):
+        raise ValueError(f"x must hold ceil(seqlen / ratio) = {-(-seqlen // ratio)} rows per sequence, got {m}")
+    n_rows, per = codes.shape[1], scales.shape[2]
+    if per * 16 != dim and per * 32 != dim:
         raise ValueError(f"scales must be [b, rows, {dim // 16}] (E4M3) or [b, rows, {dim // 32}] (MXFP4)")
-    fmt = FP4_E4M3_16 if scales.shape[2] == dim // 16 else FP4_E8M0_32
-    _rows_of(scales, torch.uint8, "scales", b, scales.shape[2], n_rows)
-    if row_pos is not None:
-        _rows_of(row_pos, torch.int32, "row_pos", b, None, n_rows)
-    if row_weight is not None:
-        _rows_of(row_weight, torch.float32, "row_weight", b, None, n_rows)
-    _same_device(x.device, start_pos, codes, scales, dropped, row_pos, row_weight, ws)
-    with _on(x.device, stream):
-        _check(lib().sti_kv_append_fp4(
-            _ptr(x), _bstride(x), _ptr(start_pos), _ptr(dropped), b, seqlen, ratio, dim, fmt, _ptr(codes),
-            _bstride(codes), _ptr(scales), _bstride(scales), n_rows, _ptr(row_pos), _bstride(row_pos), _ptr(row_weight),
-            _bstride(row_weight), _ptr(ws), _stream(None)), "sti_kv_append_fp4")
+    px, sx = _rows(x, torch.bfloat16, b, m, dim, dev, "x")
+    pc, sc = _rows(codes, torch.uint8, b, n_rows, dim // 2, dev, "codes")
+    ps, ss = _rows(scales, torch.uint8, b, n_rows, per, dev, "scales")
+    pp, sp = _rows(row_pos, torch.int32, b, n_rows, 0, dev, "row_pos")
+    pw, sw = _rows(row_weight, torch.float32, b, n_rows, 0, dev, "row_weight")
+    st = lib().sti_kv_append_fp4(
+        px, sx, _dense(start_pos, torch.int32, (b,), dev, "start_pos"), _dense(dropped, torch.int32, (b,), dev, "dropped"),
+        b, seqlen, ratio, dim, FP4_E4M3_16 if per * 16 == dim else FP4_E8M0_32, pc, sc, ps, ss, n_rows, pp, sp, pw, sw,
+        None if ws is None else _workspace_ptr(ws, dev), _raw_stream(dev.index))
+    if st:
+        _check(st, "sti_kv_append_fp4")
 
 
 def attn_fp4kv_workspace_size(b: int, s: int, h: int, d: int, n_rows: int) -> int:
@@ -553,34 +573,34 @@ def attn_fp4kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, start
     (sti_attn_fp4kv).  codes uint8 [b, rows, d/2], scales uint8 [b, rows, d/16]; prev_out / prev_lse: the
     same queries' attention over other rows, joined into the result; lse (fp32 [b, s, h]) is written and
     row_weight (fp32 [b, rows]) added to when given."""
-    _need(q, torch.bfloat16, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [b, s, h, d]")
-    b, s, h, d = q.shape
-    n_rows = _rows_of(codes, torch.uint8, "codes", b, d // 2)
-    _rows_of(scales, torch.uint8, "scales", b, d // 16, n_rows)
-    _per_sequence(start_pos, "start_pos", b)
-    _per_sequence(dropped, "dropped", b)
-    for name, t, dtype, shape in (("attn_sink", attn_sink, torch.float32, (h,)),
-                                  ("prev_out", prev_out, torch.bfloat16, (b, s, h, d)),
-                                  ("prev_lse", prev_lse, torch.float32, (b, s, h)),
-                                  ("out", out, torch.bfloat16, (b, s, h, d)), ("lse", lse, torch.float32, (b, s, h))):
-        if t is not None:
-            _need(t, dtype, name)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-    if row_weight is not None:
-        _rows_of(row_weight, torch.float32, "row_weight", b, None, n_rows)
-    _same_device(q.device, codes, scales, start_pos, attn_sink, dropped, prev_out, prev_lse, out, lse, row_weight, ws)
-    with _on(q.device, stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if ws is None:
-            ws = _call_workspace(attn_fp4kv_workspace_size(b, s, h, d, n_rows), q.device)
-        _check(lib().sti_attn_fp4kv(
-            _ptr(q), _ptr(codes), _bstride(codes), _ptr(scales), _bstride(scales), n_rows, _ptr(start_pos), _ptr(dropped), ratio,
-            _ptr(attn_sink), float(softmax_scale), _ptr(prev_out), _ptr(prev_lse), b, s, h, d, _ptr(out),
-            _ptr(lse), _ptr(row_weight), _bstride(row_weight), _ptr(ws), ws.numel(), _stream(None)), "sti_attn_fp4kv")
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_fp4kv(q, codes, scales, start_pos, ratio, softmax_scale, attn_sink, dropped, prev_out, prev_lse,
+                              out, lse, row_weight, ws)
+    if q.dim() != 4 or codes.dim() != 3:
+        raise ValueError("q must be [b, s, h, d], codes [b, rows, d/2]")
+    shape = q.shape
+    b, s, h, d = shape
+    n_rows = codes.shape[1]
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if ws is None:
+        ws = _call_workspace(attn_fp4kv_workspace_size(b, s, h, d, n_rows), dev)
+    pc, sc = _rows(codes, torch.uint8, b, n_rows, d // 2, dev, "codes")
+    ps, ss = _rows(scales, torch.uint8, b, n_rows, d // 16, dev, "scales")
+    pw, sw = _rows(row_weight, torch.float32, b, n_rows, 0, dev, "row_weight")
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    st = lib().sti_attn_fp4kv(
+        _dense(q, bf16, shape, dev, "q"), pc, sc, ps, ss, n_rows, _dense(start_pos, i32, (b,), dev, "start_pos"),
+        _dense(dropped, i32, (b,), dev, "dropped"), ratio, _dense(attn_sink, f32, (h,), dev, "attn_sink"), softmax_scale,
+        _dense(prev_out, bf16, shape, dev, "prev_out"), _dense(prev_lse, f32, (b, s, h), dev, "prev_lse"), b, s, h, d,
+        _dense(out, bf16, shape, dev, "out"), _dense(lse, f32, (b, s, h), dev, "lse"), pw, sw, _workspace_ptr(ws, dev),
+        ws.numel(), _raw_stream(dev.index))
+    if st:
+        _check(st, "sti_attn_fp4kv")
     return out
 
 
@@ -595,30 +615,38 @@ def kv_evict(row_weight: torch.Tensor, row_pos: torch.Tensor, start_pos: torch.T
     keeping the most attended ones (sti_kv_evict).  row_weight fp32 and row_pos int32 [b, rows]; arrays:
     the tensors [b, rows, ...] (any type, rows contiguous) whose rows move along; dropped int32 [b] is
     advanced."""
+    dev = row_weight.device
+    if dev.type != "cuda":
+        raise ValueError("row_weight must be a CUDA tensor")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_evict(row_weight, row_pos, start_pos, seqlen, ratio, dropped, budget, n_first, n_recent, arrays, ws)
     if row_weight.dim() != 2:
         raise ValueError("row_weight must be [b, rows]")
-    b = row_weight.shape[0]
-    n_rows = _rows_of(row_weight, torch.float32, "row_weight", b, None)
-    _rows_of(row_pos, torch.int32, "row_pos", b, None, n_rows)
-    _per_sequence(start_pos, "start_pos", b)
-    _per_sequence(dropped, "dropped", b)
-    arr = (RowArray * max(1, len(arrays)))()
+    b, n_rows = row_weight.shape
+    n = len(arrays)
+    arr = (RowArray * max(1, n))()
     for i, t in enumerate(arrays):
-        if not t.is_cuda or t.dim() < 2 or t.shape[0] != b or t.shape[1] < n_rows:
-            raise ValueError(f"arrays[{i}] must be a CUDA tensor [b, at least {n_rows} rows, ...]")
-        row = t[0, 0].numel() if t.numel() else 1
-        if t.numel() and (t.stride(1) != row or not t[0, 0].is_contiguous()):
-            raise ValueError(f"arrays[{i}] must have contiguous rows")
-        arr[i].base, arr[i].bstride = _ptr(t), _bstride(t) * t.element_size()
-        arr[i].row_bytes = row * t.element_size()
-    _same_device(row_weight.device, row_pos, start_pos, dropped, ws, *arrays)
-    with _on(row_weight.device, stream):
-        if ws is None:
-            ws = _call_workspace(kv_evict_workspace_size(b, n_rows, budget), row_weight.device)
-        _check(lib().sti_kv_evict(
-            _ptr(row_weight), _bstride(row_weight), _ptr(row_pos), _bstride(row_pos), _ptr(start_pos), _ptr(dropped), b,
-            seqlen, ratio, n_rows, budget, n_first, n_recent, arr, len(arrays), _ptr(ws), ws.numel(), _stream(None)),
-            "sti_kv_evict")
+        shape = t.shape
+        row = math.prod(shape[2:])
+        if len(shape) == 2:
+            p, stride = _rows(t, t.dtype, b, n_rows, 0, dev, f"arrays[{i}]")
+        else:
+            p, stride = _rows(t if len(shape) == 3 else t.flatten(2), t.dtype, b, n_rows, row, dev, f"arrays[{i}]")
+            if p != t.data_ptr():
+                raise ValueError(f"arrays[{i}] must have contiguous rows")
+        size = t.element_size()
+        arr[i] = RowArray(p, stride * size, row * size)
+    pw, sw = _rows(row_weight, torch.float32, b, n_rows, 0, dev, "row_weight")
+    pp, sp = _rows(row_pos, torch.int32, b, n_rows, 0, dev, "row_pos")
+    if ws is None:
+        ws = _call_workspace(kv_evict_workspace_size(b, n_rows, budget), dev)
+    st = lib().sti_kv_evict(
+        pw, sw, pp, sp, _dense(start_pos, torch.int32, (b,), dev, "start_pos"),
+        _dense(dropped, torch.int32, (b,), dev, "dropped"), b, seqlen, ratio, n_rows, budget, n_first, n_recent, arr, n,
+        _workspace_ptr(ws, dev), ws.numel(), _raw_stream(dev.index))
+    if st:
+        _check(st, "sti_kv_evict")
 
 
 def selftest_wait_timeout(ws: torch.Tensor, limit_us: int = 2000, stream=None) -> None:

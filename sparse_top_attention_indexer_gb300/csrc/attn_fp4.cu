@@ -10,9 +10,9 @@
 // into equal contiguous pieces, so a few long queries, many short ones and ragged batches all fill
 // the GPU.  A query whose tiles fall to several CTAs leaves one fp32 partial per CTA; merge_kernel joins
 // them.  Roles (640 threads):
-//   * warps 8..15 load the rows' codes into registers and decode them into the shared tile, one pair of
-//     column blocks (128 dims) at a time, as the previous tile's PV releases them;
-//   * warp 16 issues the MMAs:  S^T = tile . Q^T (M = 128 rows, N = heads), O^T += V^T . P^T (M = 128
+//   * warps 8..15 load the rows' codes into registers and decode them into the shared tile, each its own
+//     d-block (128 dims), as soon as the previous tile's PV releases it;
+//   * warp -4 issues the MMAs:  S^T = tile . Q^T (M = 128 rows, N = heads), O^T += V^T . P^T (M = 128
 //     dims per block, K = 128 rows; the same tile read as an MN-major operand);
 //   * warps 0..7 load Q, run the online softmax (thread = row, two groups of 32 heads; the running
 //     maxima move only when a score passes them by 2^8) and write the outputs.
@@ -41,14 +41,14 @@ namespace sti {
 namespace {
 
 constexpr int kThreads = 640;                  // warps 17..19 only complete the MMA warp's warpgroup
-// registers per thread after the roles' setmaxnreg: 256 x 128 + 256 x 80 + 128 x 48 = 59,392, within the
-// 640 x 96 = 61,440 of the launch
-constexpr int kRegsSoft = 128, kRegsDecode = 80, kRegsMma = 48;
+// registers per thread after the roles' setmaxnreg: 256 x 128 + 256 x 80 + 128 x 64 = 61,440, the
+// 640 x 96 of the launch
+constexpr int kRegsSoft = 128, kRegsDecode = 80, kRegsMma = 64;
 constexpr int kRows = 128;                     // rows per tile
 constexpr uint32_t kQBlk = 64 * 128;           // a Q column block: 64 heads x 64 dims
 constexpr uint32_t kTBlk = kRows * 128;        // a tile column block: 128 rows x 64 dims
-constexpr uint32_t kTmS0 = 0, kTmS1 = 64;      // TMEM columns of the two S^T partials
-constexpr uint32_t kTmO = 128;                 // O^T d-block m at [128 + 64 m, 192 + 64 m)
+constexpr uint32_t kTmS = 0;                   // TMEM columns of S^T
+constexpr uint32_t kTmO = 64;                  // O^T d-block m at [64 + 64 m, 128 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr int kWTiles = 16;                    // row weights: tiles per chunk (accumulators in shared memory)
 
@@ -58,6 +58,54 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_maj
            ((uint32_t)(M >> 4) << 24);
 }
 
+// umma_bf16's instruction with the descriptors as (low, high) words, so that stepping through an operand is
+// one 32-bit add: the issuing thread is alone, and every instruction between two MMAs delays the second.
+template <bool ACC>
+__device__ __forceinline__ void umma(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                     uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t lo32(uint64_t v) { return (uint32_t)v; }
+__device__ __forceinline__ uint32_t hi32(uint64_t v) { return (uint32_t)(v >> 32); }
+
+// Keep the value from being combined with constants ahead of time: the descriptors of a tile's 64 MMAs, all
+// known before the loop, would otherwise be kept (and spilled) as 64 values instead of one and an add each.
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+    asm volatile("" : "+r"(v));
+    return v;
+}
+// S^T (+)= tile . Q^T over one d-block (two column blocks).  a, b: low descriptor words of the tile and Q.
+__device__ __forceinline__ void qk_blocks(bool first, uint32_t s_tmem, uint32_t a, uint32_t b, uint32_t hi,
+                                          uint32_t idesc) {
+    a = opaque(a);
+    b = opaque(b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t ak = a + (k >> 2) * (kTBlk / 16) + 2 * (k & 3), bk = b + (k >> 2) * (kQBlk / 16) + 2 * (k & 3);
+        if (first && k == 0) umma<false>(s_tmem, ak, hi, bk, hi, idesc);
+        else umma<true>(s_tmem, ak, hi, bk, hi, idesc);
+    }
+}
+// O^T (+)= V^T . P^T: one d-block, eight K steps.
+template <bool FIRST>
+__device__ __forceinline__ void pv_block(uint32_t o_tmem, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
+                                         uint32_t idesc) {
+    a = opaque(a);
+    b = opaque(b);
+#pragma unroll
+    for (int k = 0; k < kRows / 16; ++k) {
+        if (FIRST && k == 0) umma<false>(o_tmem, a, a_hi, b, b_hi, idesc);
+        else umma<true>(o_tmem, a + 128 * k, a_hi, b + 128 * k, b_hi, idesc);
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -65,6 +113,38 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Bounded wait, as attn_wait, for waits that come several times per tile: reading the global timer takes
+// about 200 ns, so it is read only every 256th failed poll (a failed try_wait has already slept a while).
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 255u) == 0u) {
+            if (*abort) return false;
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            else if (now - t0 > STI_WAIT_TIMEOUT_NS) {
+                if (status) atomicOr(status, 2u /* STI_FLAG_TIMEOUT */);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// tile_wait for a converged warp.  The vote makes the result visibly warp-uniform; without it the compiler
+// treats what follows as divergent, and the MMAs of the issuing warp take three times as long to issue.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+    return __all_sync(kWarpFull, tile_wait(bar, parity, status, abort));
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // ------------------------------------------------------------------ the list of tiles
@@ -162,22 +242,45 @@ __device__ __forceinline__ void plan_work(int n, int part, int parts, long long*
 
 // ------------------------------------------------------------------ operands
 
-// The codes and scales of one row's column blocks fh, fh + 2, ... (row fr of a tile), as loaded.
-struct RowCodes {
-    uint4 c[4][2];
-    uint32_t s[4];
+// Decoding: the 8 decoding warps are dealt out to the NM d-blocks, so that each d-block is refilled by its
+// own warps as soon as the PV releases it (one group walking from block to block pays the latency of its
+// stores, the fence and the next wait on the way: 850 cycles per d-block).  A d-block of a tile is 256 units
+// of one row x one column block (64 dims: 32 code bytes, 4 scale bytes); a thread takes U of them.
+template <int NM>
+struct Deal {
+    static constexpr int kWarps = NM == 1 ? 8 : NM == 2 ? 4 : 2;   // per d-block (NM == 3: two warps idle)
+    static constexpr int U = 8 / kWarps;
+};
+template <int U>
+struct Codes {
+    uint4 c[U][2];
+    uint32_t s[U];
 };
 
-__device__ __forceinline__ void load_row(const AttnFp4Params& p, int b, int row, int fh, int n_cb, RowCodes& r) {
-    const uint8_t* cr = p.codes + (int64_t)b * p.codes_bstride + (int64_t)row * (p.d / 2);
-    const uint8_t* sr = p.scales + (int64_t)b * p.scales_bstride + (int64_t)row * (p.d / 16);
+// Unit u of thread `lt` of d-block m's warps.
+template <int NM>
+__device__ __forceinline__ void unit_of(int u, int lt, int m, int& row, int& cb) {
+    const int i = u * 32 * Deal<NM>::kWarps + lt;
+    row = i & 127;
+    cb = 2 * m + (i >> 7);
+}
+
+template <int NM>
+__device__ __forceinline__ void load_units(const AttnFp4Params& p, int b, int row0, int vis, int m, int lt, int n_cb,
+                                           Codes<Deal<NM>::U>& r) {
+    const uint8_t* cb0 = p.codes + (int64_t)b * p.codes_bstride;
+    const uint8_t* sb0 = p.scales + (int64_t)b * p.scales_bstride;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int j = 2 * m + fh;
-        if (j >= n_cb) break;
-        r.c[m][0] = __ldg(reinterpret_cast<const uint4*>(cr + j * 32));
-        r.c[m][1] = __ldg(reinterpret_cast<const uint4*>(cr + j * 32 + 16));
-        r.s[m] = __ldg(reinterpret_cast<const uint32_t*>(sr + j * 4));
+    for (int u = 0; u < Deal<NM>::U; ++u) {
+        int row, cb;
+        unit_of<NM>(u, lt, m, row, cb);
+        row += row0;
+        if (row < vis && cb < n_cb) {
+            const uint8_t* cr = cb0 + (int64_t)row * (p.d / 2) + cb * 32;
+            r.c[u][0] = __ldg(reinterpret_cast<const uint4*>(cr));
+            r.c[u][1] = __ldg(reinterpret_cast<const uint4*>(cr + 16));
+            r.s[u] = __ldg(reinterpret_cast<const uint32_t*>(sb0 + (int64_t)row * (p.d / 16) + cb * 4));
+        }
     }
 }
 
@@ -221,6 +324,17 @@ __device__ __forceinline__ void decode_block(uint8_t* dst, int fr, bool valid, c
     } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(dst + (c << 4)) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int NM>
+__device__ __forceinline__ void decode_units(uint8_t* t_s, int row0, int vis, int m, int lt, int n_cb,
+                                             const Codes<Deal<NM>::U>& r) {
+#pragma unroll
+    for (int u = 0; u < Deal<NM>::U; ++u) {
+        int row, cb;
+        unit_of<NM>(u, lt, m, row, cb);
+        if (cb < n_cb) decode_block(t_s + (size_t)cb * kTBlk + row * 128, row, row0 + row < vis, r.c[u][0], r.c[u][1], r.s[u]);
     }
 }
 
@@ -278,13 +392,13 @@ __device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float((ui
 // ------------------------------------------------------------------ attention
 
 struct __align__(16) Tail {
-    float mcp[2][4][32];      // each warp's copy of its head group's running maxima
+    float2 cm[2][4][32];      // each warp's copy of its head group's (softmax scale, -running maximum)
     float qc[2][64];          // [segment parity] per head: softmax scale (log2) over its f16 scaling
     float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
     float lsum[2][4][32];
     Work work;
     long long scratch[kThreads / 32];
-    uint64_t full[8];         // column block j of the tile decoded: one arrival per decoding warp of its parity
+    uint64_t full[4];         // d-block m of the tile decoded: one arrival per warp
     uint64_t pv[4];           // the tile's PV of d-block m done
     uint64_t s_full, p_full, q_full;
     uint32_t tmem_base;
@@ -296,29 +410,33 @@ size_t attn_smem(int d) {
     return 1024 + (size_t)n_cb * (kQBlk + kTBlk) + kRows * 128 + sizeof(Tail);
 }
 
+template <int NM>   // d-blocks of 128 dims
 __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;                 // column blocks of 64 dims
-    const int n_m = (n_cb + 1) / 2;            // d-blocks of 128
+    constexpr int n_m = NM;
     uint8_t* q_s = smem;                       // [2 n_m][64 heads][128 B]
     uint8_t* t_s = q_s + 2 * n_m * kQBlk;      // [2 n_m][128 rows][128 B]
     uint8_t* p_s = t_s + 2 * n_m * kTBlk;      // P^T [128 rows][64 heads] f16
     Tail* tl = reinterpret_cast<Tail*>(p_s + kRows * 128);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // warps -4 .. -1: the MMA warp's warpgroup, 0 .. 7: softmax, 8 .. 15: decode
+    const int tid = (int)threadIdx.x - 128, warp = ((int)threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
     const int nq = p.B * p.s;
     const int groups = p.h > 32 ? 2 : 1;       // groups of 32 heads
     const uint32_t n_mma = 32u * (uint32_t)groups;
     volatile int* abort = &tl->abort;
 
-    if (warp == 16) {
+    if (warp == -4) {
         tmem_alloc(&tl->tmem_base, n_m <= 2 ? 256 : 512);
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int j = 0; j < 8; ++j) mbar_init(&tl->full[j], 4);
-        for (int m = 0; m < 4; ++m) mbar_init(&tl->pv[m], 1);
+        for (int m = 0; m < 4; ++m) {
+            mbar_init(&tl->full[m], Deal<NM>::kWarps);
+            mbar_init(&tl->pv[m], 1);
+        }
         mbar_init(&tl->s_full, 1);
         mbar_init(&tl->p_full, 4 * groups);
         mbar_init(&tl->q_full, 4 * groups);
@@ -326,10 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         fence_mbar_init();
     }
     // what no thread writes later: Q rows of heads >= h, the dims past d of the last d-block
-    for (int i = tid; i < 2 * n_m * 64 * 8; i += kThreads)
-        if (((i >> 3) & 63) >= p.h) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 2 * n_m * 64 * 8; i += kThreads)
+        if (((i >> 3) & 63) >= p.h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
     if (n_cb & 1)
-        for (int i = tid; i < (int)kTBlk / 16; i += kThreads)
+        for (int i = threadIdx.x; i < (int)kTBlk / 16; i += kThreads)
             reinterpret_cast<uint4*>(t_s + (size_t)n_cb * kTBlk)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
@@ -337,82 +455,77 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tl->tmem_base;
+    const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);   // warp-uniform, as the compiler can see
     const Work wk = tl->work;
     griddep_launch_dependents();
 
-    if (warp >= 8 && warp < 16) {
+    if (warp >= 8) {
         regs_down<kRegsDecode>();
         // -------------------------------------------------------------- decode: thread = (row, column block parity)
-        const int fr = tid & 127, fh = (tid >> 7) & 1;
-        uint32_t n = 0;
-        bool dead = false;
-        Walk walk(wk);
-        Seg sg;
-        while (!dead && walk.next(p, sg)) {
-            for (int t = sg.t0; t < sg.t1 && !dead; ++t, ++n) {
-                const int row = t * kRows + fr;
-                const bool valid = row < sg.vis;
-                RowCodes r;
-                if (valid) load_row(p, sg.b, row, fh, n_cb, r);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int j = 2 * m + fh;
-                    if (2 * m >= n_cb) break;
-                    if (n > 0) {
-                        if (!dead) dead = !attn_wait(&tl->pv[m], (n - 1) & 1u, p.status, abort);
-                        dead = __any_sync(kWarpFull, dead);
-                    }
-                    if (dead || j >= n_cb) continue;
-                    decode_block(t_s + (size_t)j * kTBlk + fr * 128, fr, valid, r.c[m][0], r.c[m][1], r.s[m]);
+        const int m = (warp - 8) / Deal<NM>::kWarps, lt = (warp - 8) % Deal<NM>::kWarps * 32 + lane;
+        if (m < NM) {
+            uint32_t n = 0;
+            bool dead = false;
+            Walk walk(wk);
+            Seg sg;
+            while (!dead && walk.next(p, sg)) {
+                for (int t = sg.t0; t < sg.t1 && !dead; ++t, ++n) {
+                    Codes<Deal<NM>::U> r;
+                    load_units<NM>(p, sg.b, t * kRows, sg.vis, m, lt, n_cb, r);
+                    if (n > 0) dead = !warp_wait(&tl->pv[m], (n - 1) & 1u, p.status, abort);
+                    if (dead) break;
+                    decode_units<NM>(t_s, t * kRows, sg.vis, m, lt, n_cb, r);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&tl->full[j]);
+                    if (lane == 0) mbar_arrive(&tl->full[m]);
                 }
             }
         }
-    } else if (warp >= 16) {
+    } else if (warp < 0) {
         regs_down<kRegsMma>();
         // -------------------------------------------------------------- MMA issue
         const uint32_t idesc_qk = idesc_f16_f32(kRows, (int)n_mma, false, false);
         const uint32_t idesc_pv = idesc_f16_f32(kRows, (int)n_mma, true, true);
-        const uint32_t q0 = smem_u32(q_s), t0 = smem_u32(t_s), p0 = smem_u32(p_s);
+        // descriptors of the tile and Q (K-major), the tile (MN-major) and P^T (MN-major)
+        const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
+        const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128);
+        const uint64_t dp = sdesc(smem_u32(p_s), kRows * 128u, 1024, kLayoutSW128);
         uint32_t n = 0, qn = 0;
         Walk walk(wk);
         Seg sg;
-        bool ok = warp == 16 && lane == 0;
+        // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
+        bool ok = warp == -4;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = warp_wait(bar, parity, p.status, abort);
+            tc_fence_after();
+            return ok;
+        };
         while (ok && walk.next(p, sg)) {
-            ok = attn_wait(&tl->q_full, qn & 1u, p.status, abort);
+            if (!wait(&tl->q_full, qn & 1u)) break;
             ++qn;
             for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
-                for (int j = 0; j < n_cb && ok; ++j) {
-                    ok = attn_wait(&tl->full[j], n & 1u, p.status, abort);
-                    if (!ok) break;
-                    tc_fence_after();
 #pragma unroll
-                    for (int kq = 0; kq < 4; ++kq) {
-                        const int kk = 4 * j + kq;
-                        umma_bf16(tmem + ((kk & 1) ? kTmS1 : kTmS0),
-                                  sdesc(t0 + (uint32_t)j * kTBlk + (uint32_t)kq * 32u, 16, 1024, kLayoutSW128),
-                                  sdesc(q0 + (uint32_t)j * kQBlk + (uint32_t)kq * 32u, 16, 1024, kLayoutSW128),
-                                  idesc_qk, kk >= 2 ? 1u : 0u);
+                for (int m = 0; m < NM; ++m) {
+                    if (!wait(&tl->full[m], n & 1u)) break;
+                    if (elect_one()) {
+                        qk_blocks(m == 0, tmem + kTmS, lo32(dk) + (uint32_t)m * (2 * kTBlk / 16),
+                                  lo32(dq) + (uint32_t)m * (2 * kQBlk / 16), hi32(dk), idesc_qk);
+                        if (m == NM - 1) umma_commit(&tl->s_full);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (!wait(&tl->p_full, n & 1u)) break;
+                if (elect_one()) {
+#pragma unroll
+                    for (int m = 0; m < NM; ++m) {
+                        const uint32_t o = tmem + kTmO + 64u * (uint32_t)m, a = lo32(dv) + (uint32_t)m * (2 * kTBlk / 16);
+                        if (t == sg.t0) pv_block<true>(o, a, hi32(dv), lo32(dp), hi32(dp), idesc_pv);
+                        else pv_block<false>(o, a, hi32(dv), lo32(dp), hi32(dp), idesc_pv);
+                        umma_commit(&tl->pv[m]);
                     }
                 }
-                if (!ok) break;
-                umma_commit(&tl->s_full);
-                ok = attn_wait(&tl->p_full, n & 1u, p.status, abort);
-                if (!ok) break;
-                tc_fence_after();
-                for (int m = 0; m < n_m; ++m) {
-#pragma unroll
-                    for (int kk = 0; kk < kRows / 16; ++kk)
-                        umma_bf16(tmem + kTmO + 64u * (uint32_t)m,
-                                  sdesc(t0 + (uint32_t)(2 * m) * kTBlk + (uint32_t)kk * 2048u, kTBlk, 1024,
-                                        kLayoutSW128),
-                                  sdesc(p0 + (uint32_t)kk * 2048u, kRows * 128u, 1024, kLayoutSW128), idesc_pv,
-                                  (t > sg.t0 || kk > 0) ? 1u : 0u);
-                    umma_commit(&tl->pv[m]);
-                }
+                __syncwarp();
             }
         }
         __syncwarp();
@@ -432,70 +545,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         float l_thr[32];
 
         auto mwait = [&](uint64_t* bar, uint32_t parity) {
-            if (!dead) dead = !attn_wait(bar, parity, p.status, abort);
-            dead = __any_sync(kWarpFull, dead);
+            if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
         };
 
+        // One tile's probabilities.  cm holds (c, -m) of each head: c the softmax scale (log2) over the head's f16
+        // scaling, m its running maximum, so y = S c - m is one FMA and 2^y the probability.
         auto softmax = [&](bool valid, bool first) {
             mwait(&tl->s_full, n & 1u);
             tc_fence_after();
             valid = valid && !dead;
-            float x[32];
-            {
-                uint32_t r0[32], r1[32];
-                tmem_ld32(tmem + lane_base + kTmS0 + 32u * (uint32_t)set, r0);
-                tmem_ld32(tmem + lane_base + kTmS1 + 32u * (uint32_t)set, r1);
-                tmem_ld_wait();
+            const float2* cm = &tl->cm[set][qd][0];
+            uint32_t r[32];
+            tmem_ld32(tmem + lane_base + kTmS + 32u * (uint32_t)set, r);
+            tmem_ld_wait();
+            float y[32];
+            float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 q4 = *reinterpret_cast<const float4*>(&tl->qc[qbuf][32 * set + 4 * c]);
-                    const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[4 * c + e] = valid ? (__uint_as_float(r0[4 * c + e]) + __uint_as_float(r1[4 * c + e])) * qv[e]
-                                             : -INFINITY;
-                }
+            for (int c = 0; c < 16; ++c) {
+                const float4 v = *reinterpret_cast<const float4*>(cm + 2 * c);
+                y[2 * c] = fmaf(__uint_as_float(r[2 * c]), v.x, v.y);
+                y[2 * c + 1] = fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w);
+                top = fmaxf(top, fmaxf(y[2 * c], y[2 * c + 1]));
             }
-            const float* mc = &tl->mcp[set][qd][0];
-            bool need = first;
-            if (!first) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 m4 = *reinterpret_cast<const float4*>(mc + 4 * c);
-                    need = need || x[4 * c] > m4.x + 8.f || x[4 * c + 1] > m4.y + 8.f || x[4 * c + 2] > m4.z + 8.f ||
-                           x[4 * c + 3] > m4.w + 8.f;
-                }
-            }
-            need = !named_bar_and(bar_set, 128, !need);
+            // the maxima stay unless a visible score passes its head's by 2^8
+            const bool need = !named_bar_and(bar_set, 128, !(first || (valid && top > 8.f)));
             if (need) {
                 {
                     float v2[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v2[i] = x[i];
+                    for (int i = 0; i < 32; ++i) v2[i] = valid ? y[i] : -INFINITY;
                     warp_reduce_scatter_n<32, true>(v2);
                     tl->red[n & 1u][set][qd][lane] = v2[0];
                 }
                 named_bar_sync(bar_set, 128);
                 const float* rr = &tl->red[n & 1u][set][0][0];
-                const float mt = fmaxf(fmaxf(rr[lane], rr[32 + lane]), fmaxf(rr[64 + lane], rr[96 + lane]));
+                const float old = -cm[lane].y;    // what y is relative to
+                const float mt = fmaxf(fmaxf(rr[lane], rr[32 + lane]), fmaxf(rr[64 + lane], rr[96 + lane])) + old;
                 const float m_new = (m_run == -INFINITY || mt > m_run + 8.f) ? fmaxf(m_run, mt) : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
                 m_run = m_new;
                 // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
                 // scores show in its output
-                tl->mcp[set][qd][lane] = m_new == -INFINITY ? 0.f : m_new;
+                const float neg = m_new == -INFINITY ? 0.f : -m_new;
                 __syncwarp();
+                tl->cm[set][qd][lane].y = neg;
+                __syncwarp();
+                tmem_ld32(tmem + lane_base + kTmS + 32u * (uint32_t)set, r);   // again: y of the new maxima
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(cm + 2 * c);
+                    y[2 * c] = fmaf(__uint_as_float(r[2 * c]), v.x, v.y);
+                    y[2 * c + 1] = fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w);
+                }
                 if (!first && !dead && __any_sync(kWarpFull, alpha != 1.f)) {
 #pragma unroll 1
                     for (int m = 0; m < n_m; ++m) {
                         const uint32_t ta = tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set;
-                        uint32_t r[32];
-                        tmem_ld32(ta, r);
-                        tmem_ld_wait();
+#pragma unroll 1
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t o[16];
+                            tmem_ld16(ta + 16u * (uint32_t)hf, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(kWarpFull, alpha, i));
-                        tmem_st32(ta, r);
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kWarpFull, alpha, 16 * hf + i));
+                            tmem_st16(ta + 16u * (uint32_t)hf, o);
+                        }
                     }
                     tmem_st_wait();
 #pragma unroll
@@ -505,21 +621,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             uint8_t* prow = p_s + row * 128;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float4 ma = *reinterpret_cast<const float4*>(mc + 8 * c);
-                const float4 mb = *reinterpret_cast<const float4*>(mc + 8 * c + 4);
-                const float mm[8] = {ma.x, ma.y, ma.z, ma.w, mb.x, mb.y, mb.z, mb.w};
+                uint32_t pk[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float e = fast_exp2(x[8 * c + j] - mm[j]);   // 0 for rows that are not visible
-                    x[8 * c + j] = e;
-                    l_thr[8 * c + j] += e;
+                for (int j = 0; j < 4; ++j) {
+                    const int i = 8 * c + 2 * j;
+                    const float e0 = valid ? fast_exp2(y[i]) : 0.f, e1 = valid ? fast_exp2(y[i + 1]) : 0.f;
+                    l_thr[i] += e0;
+                    l_thr[i + 1] += e1;
+                    pk[j] = pack_f16x2(e0, e1);
                 }
-                uint4 pk;
-                pk.x = pack_f16x2(x[8 * c + 0], x[8 * c + 1]);
-                pk.y = pack_f16x2(x[8 * c + 2], x[8 * c + 3]);
-                pk.z = pack_f16x2(x[8 * c + 4], x[8 * c + 5]);
-                pk.w = pack_f16x2(x[8 * c + 6], x[8 * c + 7]);
-                *reinterpret_cast<uint4*>(prow + (((4 * set + c) ^ (row & 7)) << 4)) = pk;
+                *reinterpret_cast<uint4*>(prow + (((4 * set + c) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -650,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             if (pending) epilogue(prev);
             named_bar_sync(3, n_soft);
             m_run = -INFINITY;
+            tl->cm[set][qd][lane] = make_float2(tl->qc[qbuf][32 * set + lane], 0.f);
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 32; ++i) l_thr[i] = 0.f;
             for (int t = sg.t0; t < sg.t1; ++t, ++n) softmax(t * kRows + row < sg.vis, t == sg.t0);
@@ -675,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         while (global_timer_ns() - t0 < 50000ull) {
         }
     }
-    if (warp == 16) {
+    if (warp == -4) {
         tc_fence_after();
         tmem_dealloc(tmem, n_m <= 2 ? 256 : 512);
     }
@@ -757,13 +870,13 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnFp4Params p) {
 // ------------------------------------------------------------------ row weights
 
 struct __align__(16) WTail {
-    float qc[2][64];
-    float ls[2][64];                 // [query parity] the heads' lse in log2
+    float2 cl[2][64];                // [query parity] per head: (softmax scale over the f16 scaling, -lse in log2)
+    float qc[64];
     float acc[kWTiles][2][kRows];    // [tile of the chunk][head group][row]
     Work work;
     long long scratch[kThreads / 32];
-    uint64_t full[8];
-    uint64_t freed[4];               // the tile's QK has read column blocks 2m, 2m + 1
+    uint64_t full[4];
+    uint64_t freed[4];               // the tile's QK has read d-block m
     uint64_t s_full[2];              // [tile parity] S^T done
     uint64_t s_free[2];              // S^T read
     uint64_t q_full;
@@ -802,16 +915,17 @@ struct WWalk {
     }
 };
 
+template <int NM>
 __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Params p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;
-    const int n_m = (n_cb + 1) / 2;
+    constexpr int n_m = NM;
     uint8_t* q_s = smem;
     uint8_t* t_s = q_s + 2 * n_m * kQBlk;
     WTail* tl = reinterpret_cast<WTail*>(t_s + 2 * n_m * kTBlk);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = (int)threadIdx.x - 128, warp = ((int)threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
     const int groups = p.h > 32 ? 2 : 1;
     const uint32_t n_mma = 32u * (uint32_t)groups;
     volatile int* abort = &tl->abort;
@@ -819,13 +933,15 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
     const int split = (int)blockIdx.x % p.w_split;
     const int ta = (int)((long long)split * p.s / p.w_split), tb = (int)((long long)(split + 1) * p.s / p.w_split);
 
-    if (warp == 16) {
+    if (warp == -4) {
         tmem_alloc(&tl->tmem_base, 256);
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int j = 0; j < 8; ++j) mbar_init(&tl->full[j], 4);
-        for (int m = 0; m < 4; ++m) mbar_init(&tl->freed[m], 1);
+        for (int m = 0; m < 4; ++m) {
+            mbar_init(&tl->full[m], Deal<NM>::kWarps);
+            mbar_init(&tl->freed[m], 1);
+        }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&tl->s_full[k], 1);
             mbar_init(&tl->s_free[k], 4 * groups);
@@ -834,15 +950,18 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         tl->abort = 0;
         fence_mbar_init();
     }
-    for (int i = tid; i < 2 * n_m * 64 * 8; i += kThreads)
-        if (((i >> 3) & 63) >= p.h) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < 2 * n_m * 64 * 8; i += kThreads)
+        if (((i >> 3) & 63) >= p.h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    if (n_cb & 1)
+        for (int i = threadIdx.x; i < (int)kTBlk / 16; i += kThreads)
+            reinterpret_cast<uint4*>(t_s + (size_t)n_cb * kTBlk)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     plan_work(p.B, (int)blockIdx.x / p.w_split, (int)gridDim.x / p.w_split, tl->scratch, &tl->work,
               [&](int b) { return (visible_rows(p, b, p.s - 1) + kRows - 1) / kRows; });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tl->tmem_base;
+    const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);   // warp-uniform, as the compiler can see
     const Work wk = tl->work;
     griddep_wait();   // lse is complete from here on
 
@@ -852,45 +971,42 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         return nt < sg.t1 ? nt : sg.t1;
     };
 
-    if (warp >= 8 && warp < 16) {
+    if (warp >= 8) {
         regs_down<kRegsDecode>();
-        const int fr = tid & 127, fh = (tid >> 7) & 1;
-        uint32_t n = 0;
-        bool dead = false;
-        WWalk walk(wk);
-        Seg sg;
-        while (!dead && walk.next(p, sg)) {
-            for (int t = ta; t < tb && !dead; ++t) {
-                const int end = last_tile(sg, t);
-                for (int k = sg.t0; k < end && !dead; ++k, ++n) {
-                    const int row = k * kRows + fr;
-                    const bool valid = row < sg.vis;
-                    RowCodes r;
-                    if (valid) load_row(p, sg.b, row, fh, n_cb, r);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int j = 2 * m + fh;
-                        if (2 * m >= n_cb) break;
-                        if (n > 0) {
-                            if (!dead) dead = !attn_wait(&tl->freed[m], (n - 1) & 1u, p.status, abort);
-                            dead = __any_sync(kWarpFull, dead);
-                        }
-                        if (dead || j >= n_cb) continue;
-                        decode_block(t_s + (size_t)j * kTBlk + fr * 128, fr, valid, r.c[m][0], r.c[m][1], r.s[m]);
+        const int m = (warp - 8) / Deal<NM>::kWarps, lt = (warp - 8) % Deal<NM>::kWarps * 32 + lane;
+        if (m < NM) {
+            uint32_t n = 0;
+            bool dead = false;
+            WWalk walk(wk);
+            Seg sg;
+            while (!dead && walk.next(p, sg)) {
+                for (int t = ta; t < tb && !dead; ++t) {
+                    const int end = last_tile(sg, t);
+                    for (int k = sg.t0; k < end && !dead; ++k, ++n) {
+                        Codes<Deal<NM>::U> r;
+                        load_units<NM>(p, sg.b, k * kRows, sg.vis, m, lt, n_cb, r);
+                        if (n > 0) dead = !warp_wait(&tl->freed[m], (n - 1) & 1u, p.status, abort);
+                        if (dead) break;
+                        decode_units<NM>(t_s, k * kRows, sg.vis, m, lt, n_cb, r);
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&tl->full[j]);
+                        if (lane == 0) mbar_arrive(&tl->full[m]);
                     }
                 }
             }
         }
-    } else if (warp >= 16) {
+    } else if (warp < 0) {
         regs_down<kRegsMma>();
         const uint32_t idesc_qk = idesc_f16_f32(kRows, (int)n_mma, false, false);
-        const uint32_t q0 = smem_u32(q_s), t0 = smem_u32(t_s);
+        const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
         uint32_t n = 0, qn = 0;
         int have = -1;
-        bool ok = warp == 16 && lane == 0;
+        bool ok = warp == -4;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = warp_wait(bar, parity, p.status, abort);
+            tc_fence_after();
+            return ok;
+        };
         WWalk walk(wk);
         Seg sg;
         while (ok && walk.next(p, sg)) {
@@ -898,28 +1014,24 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                 const int end = last_tile(sg, t);
                 if (sg.t0 >= end) continue;
                 if (have != sg.b * p.s + t) {   // another query: its Q
-                    ok = attn_wait(&tl->q_full, qn & 1u, p.status, abort);
+                    if (!wait(&tl->q_full, qn & 1u)) break;
                     ++qn;
                     have = sg.b * p.s + t;
                 }
                 for (int k = sg.t0; k < end && ok; ++k, ++n) {
                     const uint32_t st = n & 1u;
-                    if (n >= 2) ok = attn_wait(&tl->s_free[st], ((n >> 1) - 1) & 1u, p.status, abort);
-                    for (int j = 0; j < n_cb && ok; ++j) {
-                        ok = attn_wait(&tl->full[j], n & 1u, p.status, abort);
-                        if (!ok) break;
-                        tc_fence_after();
+                    if (n >= 2 && !wait(&tl->s_free[st], ((n >> 1) - 1) & 1u)) break;
 #pragma unroll
-                        for (int kq = 0; kq < 4; ++kq) {
-                            const int kk = 4 * j + kq;
-                            umma_bf16(tmem + 128u * st + ((kk & 1) ? kTmS1 : kTmS0),
-                                      sdesc(t0 + (uint32_t)j * kTBlk + (uint32_t)kq * 32u, 16, 1024, kLayoutSW128),
-                                      sdesc(q0 + (uint32_t)j * kQBlk + (uint32_t)kq * 32u, 16, 1024, kLayoutSW128),
-                                      idesc_qk, kk >= 2 ? 1u : 0u);
+                    for (int m = 0; m < NM; ++m) {
+                        if (!wait(&tl->full[m], n & 1u)) break;
+                        if (elect_one()) {
+                            qk_blocks(m == 0, tmem + 64u * st, lo32(dk) + (uint32_t)m * (2 * kTBlk / 16),
+                                      lo32(dq) + (uint32_t)m * (2 * kQBlk / 16), hi32(dk), idesc_qk);
+                            umma_commit(&tl->freed[m]);
+                            if (m == NM - 1) umma_commit(&tl->s_full[st]);
                         }
-                        if ((j & 1) || j == n_cb - 1) umma_commit(&tl->freed[j >> 1]);
+                        __syncwarp();
                     }
-                    if (ok) umma_commit(&tl->s_full[st]);
                 }
             }
         }
@@ -944,10 +1056,14 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                 const int q = sg.b * p.s + t;
                 if (have != q) {   // this thread has seen the previous query's last S^T: the Q buffer is free
                     qbuf ^= 1;
-                    load_q(p, q, tid, q_s, tl->qc[qbuf]);
-                    if (tid < 64) tl->ls[qbuf][tid] = tid < p.h ? __ldcg(p.lse + (int64_t)q * p.h + tid) * kLog2e : 0.f;
+                    load_q(p, q, tid, q_s, tl->qc);
                     fence_proxy_async_smem();
                     __syncwarp();
+                    if (lane < 8) {   // the warp's own eight heads
+                        const int hd = 8 * warp + lane;
+                        tl->cl[qbuf][hd] =
+                            make_float2(tl->qc[hd], hd < p.h ? -__ldcg(p.lse + (int64_t)q * p.h + hd) * kLog2e : 0.f);
+                    }
                     if (lane == 0) mbar_arrive(&tl->q_full);
                     named_bar_sync(3, n_soft);
                     have = q;
@@ -955,12 +1071,10 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                 const int vis = visible_rows(p, sg.b, t);
                 for (int k = sg.t0; k < end; ++k, ++n) {
                     const uint32_t st = n & 1u;
-                    if (!dead) dead = !attn_wait(&tl->s_full[st], (n >> 1) & 1u, p.status, abort);
-                    dead = __any_sync(kWarpFull, dead);
+                    if (!dead) dead = !warp_wait(&tl->s_full[st], (n >> 1) & 1u, p.status, abort);
                     tc_fence_after();
-                    uint32_t r0[32], r1[32];
-                    tmem_ld32(tmem + lane_base + 128u * st + kTmS0 + 32u * (uint32_t)set, r0);
-                    tmem_ld32(tmem + lane_base + 128u * st + kTmS1 + 32u * (uint32_t)set, r1);
+                    uint32_t r[32];
+                    tmem_ld32(tmem + lane_base + 64u * st + 32u * (uint32_t)set, r);
                     tmem_ld_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -969,16 +1083,12 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                         float sum = 0.f;
                         const int hn = p.h - 32 * set < 32 ? p.h - 32 * set : 32;
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float4 q4 = *reinterpret_cast<const float4*>(&tl->qc[qbuf][32 * set + 4 * c]);
-                            const float4 l4 = *reinterpret_cast<const float4*>(&tl->ls[qbuf][32 * set + 4 * c]);
-                            const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, lv[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int i = 4 * c + e;
-                                const float x = (__uint_as_float(r0[i]) + __uint_as_float(r1[i])) * qv[e];
-                                if (i < hn) sum += fast_exp2(x - lv[e]);
-                            }
+                        for (int c = 0; c < 16; ++c) {
+                            const float4 v = *reinterpret_cast<const float4*>(&tl->cl[qbuf][32 * set + 2 * c]);
+                            const float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * c]), v.x, v.y));
+                            const float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w));
+                            if (2 * c < hn) sum += e0;
+                            if (2 * c + 1 < hn) sum += e1;
                         }
                         tl->acc[k - sg.t0][set][row] += sum;
                     }
@@ -1007,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         while (global_timer_ns() - t0 < 50000ull) {
         }
     }
-    if (warp == 16) {
+    if (warp == -4) {
         tc_fence_after();
         tmem_dealloc(tmem, 256);
     }
@@ -1056,25 +1166,37 @@ void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid
     *w_grid = (int)(split * (all < per ? (all > 0 ? all : 1) : per));
 }
 
-cudaError_t launch_attn_fp4(const AttnFp4Params& p, cudaStream_t stream) {
+namespace {
+template <int NM>
+cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
     const int nq = p.B * p.s;
-    if (nq == 0) return cudaSuccess;
     size_t smem = attn_smem(p.d);
-    cudaError_t e = cudaFuncSetAttribute(attn_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_fp4_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attn_fp4_kernel<<<p.grid, kThreads, smem, stream>>>(p);
+    attn_fp4_kernel<NM><<<p.grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_after(merge_kernel, dim3((unsigned)(nq < p.grid ? nq : p.grid), (unsigned)p.h), 128, 0, p, stream);
     if (e != cudaSuccess || !p.row_weight || p.n_rows == 0) return e;
     smem = row_weight_smem(p.d);
-    e = cudaFuncSetAttribute(row_weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(row_weight_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_after(row_weight_kernel, dim3((unsigned)p.w_grid), kThreads, smem, p, stream);
+    e = launch_after(row_weight_kernel<NM>, dim3((unsigned)p.w_grid), kThreads, smem, p, stream);
     if (e != cudaSuccess || p.w_split == 1) return e;
+    const int blocks = (p.n_rows + 255) / 256;
     return launch_after(row_weight_add_kernel,
-                        dim3((unsigned)((p.n_rows + 255) / 256 < 64 ? (p.n_rows + 255) / 256 : 64),
-                             (unsigned)(p.B < 65535 ? p.B : 65535)),
-                        256, 0, p, stream);
+                        dim3((unsigned)(blocks < 64 ? blocks : 64), (unsigned)(p.B < 65535 ? p.B : 65535)), 256, 0, p,
+                        stream);
+}
+}  // namespace
+
+cudaError_t launch_attn_fp4(const AttnFp4Params& p, cudaStream_t stream) {
+    if (p.B * p.s == 0) return cudaSuccess;
+    switch ((p.d + 127) / 128) {
+        case 1: return launch_nm<1>(p, stream);
+        case 2: return launch_nm<2>(p, stream);
+        case 3: return launch_nm<3>(p, stream);
+        default: return launch_nm<4>(p, stream);
+    }
 }
 
 }  // namespace sti
