@@ -9,14 +9,17 @@
 // attn_fp4_kernel: persistent CTAs, one per SM; the queries' 128-row tiles form one long list that is cut
 // into equal contiguous pieces, so a few long queries, many short ones and ragged batches all fill
 // the GPU.  A query whose tiles fall to several CTAs leaves one fp32 partial per CTA; merge_kernel joins
-// them.  Roles (640 threads):
-//   * warps 8..15 load the rows' codes into registers and decode them into the shared tile, each its own
-//     d-block (128 dims), as soon as the previous tile's PV releases it;
-//   * warp -4 issues the MMAs:  S^T = tile . Q^T (M = 128 rows, N = heads), O^T += V^T . P^T (M = 128
+// them.  17 working warps:
+//   * warp 16 issues the MMAs:  S^T = tile . Q^T (M = 128 rows, N = heads), O^T += V^T . P^T (M = 128
 //     dims per block, K = 128 rows; the same tile read as an MN-major operand);
-//   * warps 0..7 load Q, run the online softmax (thread = row, two groups of 32 heads; the running
-//     maxima move only when a score passes them by 2^8) and write the outputs.
-// The decode runs in its own warps so that it overlaps the MMAs and the softmax.
+//   * warps 0..15 do the rest of a tile in turn: decode its rows from codes loaded a tile ahead (one d-block
+//     of 128 dims at a time, as the previous tile's PV releases it), then its softmax (thread = row, four
+//     groups of 16 heads; the running maxima move only when a score passes them by 2^8), and per
+//     query load Q and write the output.
+// With 512 dims, Q (64 KB), one tile (128 KB) and P^T (16 KB) fill shared memory, so a tile is a chain: decode
+// what the PV has released, QK, softmax, PV.  What bounds the kernel is that chain's latency, not the 3072
+// cycles of its MMAs; hence all 16 warps on each link of it (separate decoding and softmax warps, 8 each,
+// took 6,800 cycles a tile).
 //
 // f16 operands: an E2M1 value (2 significant bits) times an E4M3 value (4) is exact in f16 (at most 6
 // significant bits, magnitudes 2^-10 .. 2688), so the tile is exact.  Q is bf16: each head's values are
@@ -40,17 +43,18 @@
 namespace sti {
 namespace {
 
-constexpr int kThreads = 640;                  // warps 17..19 only complete the MMA warp's warpgroup
-// registers per thread after the roles' setmaxnreg: 256 x 128 + 256 x 80 + 128 x 64 = 61,440, the
-// 640 x 96 of the launch
-constexpr int kRegsSoft = 128, kRegsDecode = 80, kRegsMma = 64;
+constexpr int kMath = 512;                     // decode, softmax, Q, outputs: warps 0..15
+constexpr int kThreads = kMath + 128;          // warp 16: MMA issue; 17..19 only complete its warpgroup
+// registers per thread after setmaxnreg: 512 x 104 + 128 x 64 = 61,440, the 640 x 96 of the launch
+constexpr int kRegsMath = 104, kRegsMma = 64;
 constexpr int kRows = 128;                     // rows per tile
 constexpr uint32_t kQBlk = 64 * 128;           // a Q column block: 64 heads x 64 dims
 constexpr uint32_t kTBlk = kRows * 128;        // a tile column block: 128 rows x 64 dims
 constexpr uint32_t kTmS = 0;                   // TMEM columns of S^T
 constexpr uint32_t kTmO = 64;                  // O^T d-block m at [64 + 64 m, 128 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kWTiles = 16;                    // row weights: tiles per chunk (accumulators in shared memory)
+constexpr int kWTiles = 8;                     // row weights: tiles per chunk (accumulators in shared memory)
+constexpr uint32_t kBarMath = 5;               // named barriers: 1..4 the head groups, 5 all math warps
 
 // instruction descriptor, kind::f16 with f16 A/B (format 0) and fp32 accumulator
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
@@ -242,46 +246,37 @@ __device__ __forceinline__ void plan_work(int n, int part, int parts, long long*
 
 // ------------------------------------------------------------------ operands
 
-// Decoding: the 8 decoding warps are dealt out to the NM d-blocks, so that each d-block is refilled by its
-// own warps as soon as the PV releases it (one group walking from block to block pays the latency of its
-// stores, the fence and the next wait on the way: 850 cycles per d-block).  A d-block of a tile is 256 units
-// of one row x one column block (64 dims: 32 code bytes, 4 scale bytes); a thread takes U of them.
-template <int NM>
-struct Deal {
-    static constexpr int kWarps = NM == 1 ? 8 : NM == 2 ? 4 : 2;   // per d-block (NM == 3: two warps idle)
-    static constexpr int U = 8 / kWarps;
-};
-template <int U>
+// Decoding: 8 warps take a d-block (warps 0..7 blocks 0 and 2, warps 8..15 blocks 1 and 3).  A lane takes 32
+// codes (16 bytes, 2 scales) of one row: lane = 4 (row % 8) + quarter of the d-block, so that a warp's load
+// covers 64 contiguous bytes of 8 rows (one row per lane would touch 32 cache lines per load: the loads of a
+// tile then took 3600 cycles to issue) and its stores spread over all banks.
 struct Codes {
-    uint4 c[U][2];
-    uint32_t s[U];
+    uint4 c[2][2];      // [d-block][row, row + 64]
+    uint32_t s[2];      // the two rows' scale pairs
 };
 
-// Unit u of thread `lt` of d-block m's warps.
-template <int NM>
-__device__ __forceinline__ void unit_of(int u, int lt, int m, int& row, int& cb) {
-    const int i = u * 32 * Deal<NM>::kWarps + lt;
-    row = i & 127;
-    cb = 2 * m + (i >> 7);
-}
-
-template <int NM>
-__device__ __forceinline__ void load_units(const AttnFp4Params& p, int b, int row0, int vis, int m, int lt, int n_cb,
-                                           Codes<Deal<NM>::U>& r) {
-    const uint8_t* cb0 = p.codes + (int64_t)b * p.codes_bstride;
-    const uint8_t* sb0 = p.scales + (int64_t)b * p.scales_bstride;
-#pragma unroll
-    for (int u = 0; u < Deal<NM>::U; ++u) {
-        int row, cb;
-        unit_of<NM>(u, lt, m, row, cb);
-        row += row0;
-        if (row < vis && cb < n_cb) {
-            const uint8_t* cr = cb0 + (int64_t)row * (p.d / 2) + cb * 32;
-            r.c[u][0] = __ldg(reinterpret_cast<const uint4*>(cr));
-            r.c[u][1] = __ldg(reinterpret_cast<const uint4*>(cr + 16));
-            r.s[u] = __ldg(reinterpret_cast<const uint32_t*>(sb0 + (int64_t)row * (p.d / 16) + cb * 4));
-        }
+// This thread's codes of its d-block number u of a tile.
+__device__ __forceinline__ void load_unit(const AttnFp4Params& p, int b, int row0, int vis, int n_cb, int u, Codes& r) {
+    const int lane = threadIdx.x & 31, ch = lane & 3, m = 2 * u + (threadIdx.x >> 8);
+    const int row = row0 + ((threadIdx.x >> 5) & 7) * 8 + (lane >> 2);
+    if (2 * m + (ch >> 1) >= n_cb) return;
+    const uint8_t* cr = p.codes + (int64_t)b * p.codes_bstride + (int64_t)row * (p.d / 2) + m * 64 + ch * 16;
+    const uint8_t* sr = p.scales + (int64_t)b * p.scales_bstride + (int64_t)row * (p.d / 16) + m * 8 + ch * 2;
+    uint32_t s0 = 0u, s1 = 0u;
+    if (row < vis) {
+        r.c[u][0] = __ldg(reinterpret_cast<const uint4*>(cr));
+        s0 = __ldg(reinterpret_cast<const uint16_t*>(sr));
     }
+    if (row + 64 < vis) {
+        r.c[u][1] = __ldg(reinterpret_cast<const uint4*>(cr + 32 * p.d));
+        s1 = __ldg(reinterpret_cast<const uint16_t*>(sr + 4 * p.d));
+    }
+    r.s[u] = s0 | (s1 << 16);
+}
+template <int NM>
+__device__ __forceinline__ void load_units(const AttnFp4Params& p, int b, int row0, int vis, int n_cb, Codes& r) {
+#pragma unroll
+    for (int u = 0; u < (NM + 1) / 2; ++u) load_unit(p, b, row0, vis, n_cb, u, r);
 }
 
 // Eight codes (nibble i = element i) times the scale pair s2 = (s, s), as eight f16.
@@ -303,83 +298,86 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s2) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 64 elements of row fr (one column block at dst) from their codes; zeros when the row is not visible.
-__device__ __forceinline__ void decode_block(uint8_t* dst, int fr, bool valid, const uint4& c0, const uint4& c1,
-                                             uint32_t s) {
-    if (valid) {
-        uint32_t h01, h23;   // the four scales as f16
-        asm("{\n\t.reg .b16 lo, hi;\n\t"
-            "mov.b32 {lo, hi}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-            : "=r"(h01), "=r"(h23)
-            : "r"(s));
-        const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const uint32_t sc[4] = {__byte_perm(h01, h01, 0x1010), __byte_perm(h01, h01, 0x3232),
-                                __byte_perm(h23, h23, 0x1010), __byte_perm(h23, h23, 0x3232)};
+// 32 elements of a tile row (half of one column block; `dst` the row's 128 bytes) from their codes and two
+// scales; zeros when the row is not visible.
+__device__ __forceinline__ void decode_half(uint8_t* dst, int row, int half, bool valid, const uint4& c, uint32_t s) {
+    uint32_t h = 0u;   // the scales as f16
+    if (valid)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(s));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    const uint32_t sc[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(dst + ((c ^ (fr & 7)) << 4)) =
-                decode8(w[c], *reinterpret_cast<const __half2*>(&sc[c >> 1]));
-    } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(dst + (c << 4)) = make_uint4(0, 0, 0, 0);
-    }
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(dst + (((4 * half + i) ^ (row & 7)) << 4)) =
+            valid ? decode8(w[i], *reinterpret_cast<const __half2*>(&sc[i >> 1])) : make_uint4(0, 0, 0, 0);
 }
 
-template <int NM>
-__device__ __forceinline__ void decode_units(uint8_t* t_s, int row0, int vis, int m, int lt, int n_cb,
-                                             const Codes<Deal<NM>::U>& r) {
+// Decode this thread's part of the tile; `released(m)` waits until d-block m may be overwritten (false: gave
+// up), full[m] gets one arrival per warp.
+template <int NM, class F>
+__device__ __forceinline__ void decode_units(uint8_t* t_s, int row0, int vis, int n_cb, const Codes& r, uint64_t* full,
+                                             F released) {
+    const int lane = threadIdx.x & 31, ch = lane & 3;
+    const int row = ((threadIdx.x >> 5) & 7) * 8 + (lane >> 2);
 #pragma unroll
-    for (int u = 0; u < Deal<NM>::U; ++u) {
-        int row, cb;
-        unit_of<NM>(u, lt, m, row, cb);
-        if (cb < n_cb) decode_block(t_s + (size_t)cb * kTBlk + row * 128, row, row0 + row < vis, r.c[u][0], r.c[u][1], r.s[u]);
-    }
-}
-
-// Query qi's heads as f16 into the swizzled column blocks at q_s, four threads per head, each head
-// scaled by 2^f; qc[head] = scale_log2 * 2^-f.  `t`: thread of the loading group (4 threads per head).
-__device__ __forceinline__ void load_q(const AttnFp4Params& p, int qi, int t, uint8_t* q_s, float* qc) {
-    const int head = t >> 2, part = t & 3;
-    const int n = p.d / 8;
-    const bool in = head < p.h;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qi * p.h + (in ? head : 0)) * p.d);
-    uint32_t mx = 0;
-    if (in) {
-#pragma unroll 8
-        for (int k = part; k < n; k += 4) {
-            const uint4 v = __ldg(src + k);
-            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+    for (int u = 0; u < (NM + 1) / 2; ++u) {
+        const int m = 2 * u + (threadIdx.x >> 8), cb = 2 * m + (ch >> 1);
+        if (m < NM) {
+            if (!released(m)) return;
+            if (cb < n_cb) {
+                uint8_t* dst = t_s + (size_t)cb * kTBlk + row * 128;
+                decode_half(dst, row, ch & 1, row0 + row < vis, r.c[u][0], r.s[u] & 0xFFFFu);
+                decode_half(dst + 64 * 128, row, ch & 1, row0 + row + 64 < vis, r.c[u][1], r.s[u] >> 16);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[m]);
         }
     }
+}
+
+// Query qi's heads as f16 into the swizzled column blocks at q_s, eight math threads per head, each head
+// scaled by 2^f; qc[head] = scale_log2 * 2^-f.
+template <int NM>
+__device__ __forceinline__ void load_q(const AttnFp4Params& p, int qi, uint8_t* q_s, float* qc) {
+    const int head = threadIdx.x >> 3, part = threadIdx.x & 7;
+    const int n = p.d / 8;   // 16-byte chunks of a head: part, part + 8, ... (at most eight per thread)
+    const bool in = head < p.h;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qi * p.h + (in ? head : 0)) * p.d);
+    uint4 v[2 * NM];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int k = 0; k < 2 * NM; ++k) {
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (in && part + 8 * k < n) v[k] = __ldg(src + part + 8 * k);
+    }
+#pragma unroll
+    for (int k = 0; k < 2 * NM; ++k)
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu),
+                                   __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
     mx = max(mx & 0xFFFFu, mx >> 16);
-    mx = max(mx, __shfl_xor_sync(kWarpFull, mx, 1));
-    mx = max(mx, __shfl_xor_sync(kWarpFull, mx, 2));
+#pragma unroll
+    for (int o = 1; o <= 4; o <<= 1) mx = max(mx, __shfl_xor_sync(kWarpFull, mx, o));
     int f = 139 - (int)(mx >> 7);   // largest into [2^12, 2^13); mx >> 7: its exponent field
     f = f > 127 ? 127 : f;          // (-116 .. 127)
     const float up = __uint_as_float((uint32_t)(f + 127) << 23);
     // 2^-f: subnormal at f = 127
     const float down = f == 127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(127 - f) << 23);
-    if (in) {
-        if (part == 0) qc[head] = p.scale_log2 * down;
-#pragma unroll 8
-        for (int k = part; k < n; k += 4) {
-            const uint4 v = __ldg(src + k);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[4];
+    if (part == 0) qc[head] = in ? p.scale_log2 * down : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * up,
-                                                    __uint_as_float(w[i] & 0xFFFF0000u) * up);
-                o[i] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            *reinterpret_cast<uint4*>(q_s + (k >> 3) * kQBlk + head * 128 + (((k & 7) ^ (head & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < 2 * NM; ++k) {
+        if (!in || part + 8 * k >= n) continue;
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 x = __floats2half2_rn(__uint_as_float(w[i] << 16) * up,
+                                                __uint_as_float(w[i] & 0xFFFF0000u) * up);
+            o[i] = *reinterpret_cast<const uint32_t*>(&x);
         }
-    } else if (part == 0) {
-        qc[head] = 0.f;
+        // chunk part + 8 k: column block k, chunk `part` of its row
+        *reinterpret_cast<uint4*>(q_s + k * kQBlk + head * 128 + ((part ^ (head & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -392,10 +390,10 @@ __device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float((ui
 // ------------------------------------------------------------------ attention
 
 struct __align__(16) Tail {
-    float2 cm[2][4][32];      // each warp's copy of its head group's (softmax scale, -running maximum)
-    float qc[2][64];          // [segment parity] per head: softmax scale (log2) over its f16 scaling
-    float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
-    float lsum[2][4][32];
+    float2 cm[4][4][16];      // [head group][warp of the group]: its copy of (softmax scale, -running maximum)
+    float qc[64];             // per head: softmax scale (log2) over its f16 scaling
+    float red[2][4][4][16];   // [tile parity][group][warp]: per-warp maxima
+    float lsum[4][4][16];
     Work work;
     long long scratch[kThreads / 32];
     uint64_t full[4];         // d-block m of the tile decoded: one arrival per warp
@@ -415,39 +413,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;                 // column blocks of 64 dims
-    constexpr int n_m = NM;
-    uint8_t* q_s = smem;                       // [2 n_m][64 heads][128 B]
-    uint8_t* t_s = q_s + 2 * n_m * kQBlk;      // [2 n_m][128 rows][128 B]
-    uint8_t* p_s = t_s + 2 * n_m * kTBlk;      // P^T [128 rows][64 heads] f16
+    uint8_t* q_s = smem;                       // [2 NM][64 heads][128 B]
+    uint8_t* t_s = q_s + 2 * NM * kQBlk;       // [2 NM][128 rows][128 B]
+    uint8_t* p_s = t_s + 2 * NM * kTBlk;       // P^T [128 rows][64 heads] f16
     Tail* tl = reinterpret_cast<Tail*>(p_s + kRows * 128);
 
-    // warps -4 .. -1: the MMA warp's warpgroup, 0 .. 7: softmax, 8 .. 15: decode
-    const int tid = (int)threadIdx.x - 128, warp = ((int)threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nq = p.B * p.s;
-    const int groups = p.h > 32 ? 2 : 1;       // groups of 32 heads
-    const uint32_t n_mma = 32u * (uint32_t)groups;
+    const int groups = (p.h + 15) / 16;        // groups of 16 heads
     volatile int* abort = &tl->abort;
 
-    if (warp == -4) {
-        tmem_alloc(&tl->tmem_base, n_m <= 2 ? 256 : 512);
+    if (warp == 16) {
+        tmem_alloc(&tl->tmem_base, NM <= 2 ? 256 : 512);
         tmem_relinquish();
     }
     if (tid == 0) {
         for (int m = 0; m < 4; ++m) {
-            mbar_init(&tl->full[m], Deal<NM>::kWarps);
+            mbar_init(&tl->full[m], 8);
             mbar_init(&tl->pv[m], 1);
         }
         mbar_init(&tl->s_full, 1);
         mbar_init(&tl->p_full, 4 * groups);
-        mbar_init(&tl->q_full, 4 * groups);
+        mbar_init(&tl->q_full, 16);
         tl->abort = 0;
         fence_mbar_init();
     }
     // what no thread writes later: Q rows of heads >= h, the dims past d of the last d-block
-    for (int i = threadIdx.x; i < 2 * n_m * 64 * 8; i += kThreads)
+    for (int i = tid; i < 2 * NM * 64 * 8; i += kThreads)
         if (((i >> 3) & 63) >= p.h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
     if (n_cb & 1)
-        for (int i = threadIdx.x; i < (int)kTBlk / 16; i += kThreads)
+        for (int i = tid; i < (int)kTBlk / 16; i += kThreads)
             reinterpret_cast<uint4*>(t_s + (size_t)n_cb * kTBlk)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
@@ -459,33 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
     const Work wk = tl->work;
     griddep_launch_dependents();
 
-    if (warp >= 8) {
-        regs_down<kRegsDecode>();
-        // -------------------------------------------------------------- decode: thread = (row, column block parity)
-        const int m = (warp - 8) / Deal<NM>::kWarps, lt = (warp - 8) % Deal<NM>::kWarps * 32 + lane;
-        if (m < NM) {
-            uint32_t n = 0;
-            bool dead = false;
-            Walk walk(wk);
-            Seg sg;
-            while (!dead && walk.next(p, sg)) {
-                for (int t = sg.t0; t < sg.t1 && !dead; ++t, ++n) {
-                    Codes<Deal<NM>::U> r;
-                    load_units<NM>(p, sg.b, t * kRows, sg.vis, m, lt, n_cb, r);
-                    if (n > 0) dead = !warp_wait(&tl->pv[m], (n - 1) & 1u, p.status, abort);
-                    if (dead) break;
-                    decode_units<NM>(t_s, t * kRows, sg.vis, m, lt, n_cb, r);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tl->full[m]);
-                }
-            }
-        }
-    } else if (warp < 0) {
+    if (warp >= 16) {
         regs_down<kRegsMma>();
         // -------------------------------------------------------------- MMA issue
-        const uint32_t idesc_qk = idesc_f16_f32(kRows, (int)n_mma, false, false);
-        const uint32_t idesc_pv = idesc_f16_f32(kRows, (int)n_mma, true, true);
+        const uint32_t idesc_qk = idesc_f16_f32(kRows, 16 * groups, false, false);
+        const uint32_t idesc_pv = idesc_f16_f32(kRows, 16 * groups, true, true);
         // descriptors of the tile and Q (K-major), the tile (MN-major) and P^T (MN-major)
         const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
         const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128);
@@ -494,13 +467,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         Walk walk(wk);
         Seg sg;
         // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
-        bool ok = warp == -4;
+        bool ok = warp == 16;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = warp_wait(bar, parity, p.status, abort);
             tc_fence_after();
             return ok;
         };
+        int2 rec = make_int2(-1, 0);
         while (ok && walk.next(p, sg)) {
+            if (sg.t0 == 0 && sg.t1 < sg.nt) {
+                const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
+                int c = (int)(last * wk.ctas / wk.total);
+                while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
+                while ((long long)c * wk.total / wk.ctas > last) --c;
+                rec = make_int2(sg.q, c);
+            }
             if (!wait(&tl->q_full, qn & 1u)) break;
             ++qn;
             for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
@@ -528,21 +509,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 __syncwarp();
             }
         }
+        if (warp == 16 && lane == 0) p.rec[blockIdx.x] = rec;
         __syncwarp();
     } else {
-        regs_up<kRegsSoft>();
-        if (warp < 4 * groups) {
-        // -------------------------------------------------------------- Q, softmax, outputs
+        regs_up<kRegsMath>();
+        // -------------------------------------------------------------- decode, Q, softmax, outputs
         const int set = warp >> 2, qd = warp & 3;
         const int row = 32 * qd + lane;
+        const bool active = set < groups;      // this warp's head group has heads
         const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
         const uint32_t bar_set = 1u + (uint32_t)set;
-        const uint32_t n_soft = 128u * (uint32_t)groups;
         uint32_t n = 0;
-        int qbuf = 0;
         bool dead = false;
-        float m_run = -INFINITY;   // lane l: head 32 set + l
-        float l_thr[32];
+        float m_run = -INFINITY;               // lane l: head 16 set + l / 2
+        float l_thr[16];                       // this row's running sums of the group's heads
 
         auto mwait = [&](uint64_t* bar, uint32_t parity) {
             if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
@@ -555,13 +535,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             tc_fence_after();
             valid = valid && !dead;
             const float2* cm = &tl->cm[set][qd][0];
-            uint32_t r[32];
-            tmem_ld32(tmem + lane_base + kTmS + 32u * (uint32_t)set, r);
+            uint32_t r[16];
+            tmem_ld16(tmem + lane_base + kTmS + 16u * (uint32_t)set, r);
             tmem_ld_wait();
-            float y[32];
+            float y[16];
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 const float4 v = *reinterpret_cast<const float4*>(cm + 2 * c);
                 y[2 * c] = fmaf(__uint_as_float(r[2 * c]), v.x, v.y);
                 y[2 * c + 1] = fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w);
@@ -571,56 +551,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             const bool need = !named_bar_and(bar_set, 128, !(first || (valid && top > 8.f)));
             if (need) {
                 {
-                    float v2[32];
+                    float v2[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v2[i] = valid ? y[i] : -INFINITY;
-                    warp_reduce_scatter_n<32, true>(v2);
-                    tl->red[n & 1u][set][qd][lane] = v2[0];
+                    for (int i = 0; i < 16; ++i) v2[i] = valid ? y[i] : -INFINITY;
+                    warp_reduce_scatter_n<16, true>(v2);   // lane l: head l / 2 over this warp's rows
+                    if (!(lane & 1)) tl->red[n & 1u][set][qd][lane >> 1] = v2[0];
                 }
                 named_bar_sync(bar_set, 128);
-                const float* rr = &tl->red[n & 1u][set][0][0];
-                const float old = -cm[lane].y;    // what y is relative to
-                const float mt = fmaxf(fmaxf(rr[lane], rr[32 + lane]), fmaxf(rr[64 + lane], rr[96 + lane])) + old;
+                const float* rr = &tl->red[n & 1u][set][0][lane >> 1];
+                const float old = -cm[lane >> 1].y;        // what y is relative to
+                const float mt = fmaxf(fmaxf(rr[0], rr[16]), fmaxf(rr[32], rr[48])) + old;
                 const float m_new = (m_run == -INFINITY || mt > m_run + 8.f) ? fmaxf(m_run, mt) : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
                 m_run = m_new;
+                __syncwarp();
                 // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
                 // scores show in its output
-                const float neg = m_new == -INFINITY ? 0.f : -m_new;
+                if (!(lane & 1)) tl->cm[set][qd][lane >> 1].y = m_new == -INFINITY ? 0.f : -m_new;
                 __syncwarp();
-                tl->cm[set][qd][lane].y = neg;
-                __syncwarp();
-                tmem_ld32(tmem + lane_base + kTmS + 32u * (uint32_t)set, r);   // again: y of the new maxima
-                tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     const float4 v = *reinterpret_cast<const float4*>(cm + 2 * c);
                     y[2 * c] = fmaf(__uint_as_float(r[2 * c]), v.x, v.y);
                     y[2 * c + 1] = fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w);
                 }
                 if (!first && !dead && __any_sync(kWarpFull, alpha != 1.f)) {
 #pragma unroll 1
-                    for (int m = 0; m < n_m; ++m) {
-                        const uint32_t ta = tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set;
-#pragma unroll 1
-                        for (int hf = 0; hf < 2; ++hf) {
-                            uint32_t o[16];
-                            tmem_ld16(ta + 16u * (uint32_t)hf, o);
-                            tmem_ld_wait();
+                    for (int m = 0; m < NM; ++m) {
+                        const uint32_t ta = tmem + lane_base + kTmO + 64u * (uint32_t)m + 16u * (uint32_t)set;
+                        uint32_t o[16];
+                        tmem_ld16(ta, o);
+                        tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kWarpFull, alpha, 16 * hf + i));
-                            tmem_st16(ta + 16u * (uint32_t)hf, o);
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kWarpFull, alpha, 2 * i));
+                        tmem_st16(ta, o);
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) l_thr[i] *= __shfl_sync(kWarpFull, alpha, i);
+                    for (int i = 0; i < 16; ++i) l_thr[i] *= __shfl_sync(kWarpFull, alpha, 2 * i);
                 }
             }
             uint8_t* prow = p_s + row * 128;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 uint32_t pk[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -630,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                     l_thr[i + 1] += e1;
                     pk[j] = pack_f16x2(e0, e1);
                 }
-                *reinterpret_cast<uint4*>(prow + (((4 * set + c) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                *reinterpret_cast<uint4*>(prow + (((2 * set + c) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -639,34 +613,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         };
 
         // a segment's O^T and sums: the query's output when the segment holds all its tiles, else a partial
-        auto epilogue = [&](const Seg& sg) {
-            mwait(&tl->pv[n_m - 1], (n - 1) & 1u);
+        // (slot >= 0: where)
+        auto epilogue = [&](int q, int slot) {
+            mwait(&tl->pv[NM - 1], (n - 1) & 1u);
             tc_fence_after();
             {
-                float v2[32];
+                float v2[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v2[i] = l_thr[i];
-                warp_reduce_scatter_n<32, false>(v2);
-                tl->lsum[set][qd][lane] = v2[0];
+                for (int i = 0; i < 16; ++i) v2[i] = l_thr[i];
+                warp_reduce_scatter_n<16, false>(v2);
+                if (!(lane & 1)) tl->lsum[set][qd][lane >> 1] = v2[0];
             }
             named_bar_sync(bar_set, 128);
-            const float* ls = &tl->lsum[set][0][0];
-            const float lt = (ls[lane] + ls[32 + lane]) + (ls[64 + lane] + ls[96 + lane]);
-            const int hh = 32 * set + lane;
-            if (sg.t0 > 0 || sg.t1 < sg.nt) {
-                const int slot = 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
-                if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
-                float* po = p.part_o + (int64_t)slot * p.h * p.d;
+            const float* ls = &tl->lsum[set][0][lane >> 1];
+            const float lt = (ls[0] + ls[16]) + (ls[32] + ls[48]);
+            const int hh = 16 * set + (lane >> 1);
+            if (slot >= 0) {
+                if (qd == 0 && !(lane & 1)) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
+                float* po = p.part_o + ((int64_t)slot * p.h + 16 * set) * p.d;
 #pragma unroll 1
-                for (int m = 0; m < n_m; ++m) {
+                for (int m = 0; m < NM; ++m) {
                     const int dd = 128 * m + 32 * qd + lane;
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set, r);
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 16u * (uint32_t)set, r);
                     tmem_ld_wait();
                     if (dd < p.d) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * set + i < p.h) po[(32 * set + i) * p.d + dd] = __uint_as_float(r[i]);
+                        for (int i = 0; i < 16; ++i)
+                            if (16 * set + i < p.h) po[i * p.d + dd] = __uint_as_float(r[i]);
                     }
                 }
             } else {
@@ -674,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 if (hh < p.h) {
                     // everything relative to the largest of the running maximum, the sink and prev_lse
                     const float sk = p.sink ? __ldg(p.sink + hh) * kLog2e : -INFINITY;
-                    const float pl = p.prev_lse ? __ldg(p.prev_lse + (int64_t)sg.q * p.h + hh) * kLog2e : -INFINITY;
+                    const float pl = p.prev_lse ? __ldg(p.prev_lse + (int64_t)q * p.h + hh) * kLog2e : -INFINITY;
                     float mx = fmaxf(m_run, fmaxf(sk, pl));
                     if (mx == -INFINITY) mx = 0.f;
                     const float f = m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);
@@ -682,34 +656,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                     const float den = lt * f + exp2f(sk - mx) + ep;
                     inv = f / den;
                     wp = ep / den;
-                    if (p.lse && qd == 0) p.lse[(int64_t)sg.q * p.h + hh] = (mx + log2f(den)) * kLn2;
+                    if (p.lse && qd == 0 && !(lane & 1)) p.lse[(int64_t)q * p.h + hh] = (mx + log2f(den)) * kLn2;
                 }
-                float invh[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) invh[i] = __shfl_sync(kWarpFull, inv, i);
-                uint16_t* orow = p.out + (int64_t)sg.q * p.h * p.d;
-                uint16_t* stg = reinterpret_cast<uint16_t*>(p_s) + warp * 32 * 32;   // this warp's [32 heads][32 dims]
+                uint16_t* orow = p.out + (int64_t)q * p.h * p.d;
+                uint16_t* stg = reinterpret_cast<uint16_t*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
                 const bool odd = (lane & 1) != 0;
 #pragma unroll 1
-                for (int m = 0; m < n_m; ++m) {
+                for (int m = 0; m < NM; ++m) {
                     const int dd = 128 * m + 32 * qd + lane;
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set, r);
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 16u * (uint32_t)set, r);
                     tmem_ld_wait();
-                    float vv[32];
+                    float vv[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) vv[i] = dead ? 0.f : __uint_as_float(r[i]) * invh[i];
+                    for (int i = 0; i < 16; ++i) vv[i] = dead ? 0.f : __uint_as_float(r[i]) * __shfl_sync(kWarpFull, inv, 2 * i);
                     if (p.prev_out) {
-                        const uint16_t* pr = p.prev_out + (int64_t)sg.q * p.h * p.d + dd;
+                        const uint16_t* pr = p.prev_out + ((int64_t)q * p.h + 16 * set) * p.d + dd;
+                        uint16_t pv[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float w = __shfl_sync(kWarpFull, wp, i);
-                            if (w != 0.f && 32 * set + i < p.h && dd < p.d)   // weight 0: prev_out is not used
-                                vv[i] += w * bf16_f(pr[(32 * set + i) * p.d]);
+                        for (int i = 0; i < 16; ++i) pv[i] = 16 * set + i < p.h && dd < p.d ? pr[i * p.d] : (uint16_t)0;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float w = __shfl_sync(kWarpFull, wp, 2 * i);
+                            vv[i] = w != 0.f ? vv[i] + w * bf16_f(pv[i]) : vv[i];   // weight 0: prev_out is not used
                         }
                     }
+                    // lane pairs write 4 bytes: the even lane head i, the odd lane head i + 1
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         const float send = odd ? vv[i] : vv[i + 1];
                         const float recv = __shfl_xor_sync(kWarpFull, send, 1);
                         const uint32_t pk = odd ? pack_bf16x2(recv, vv[i + 1]) : pack_bf16x2(vv[i], recv);
@@ -717,9 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         const int c = lane + 32 * k;
-                        const int hw = 32 * set + (c >> 2);
+                        const int hw = 16 * set + (c >> 2);
                         const int dw = 128 * m + 32 * qd + 8 * (c & 3);
                         if (hw < p.h && dw < p.d)
                             *reinterpret_cast<uint4*>(orow + (int64_t)hw * p.d + dw) =
@@ -728,13 +702,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                     __syncwarp();
                 }
             }
-            named_bar_sync(3, n_soft);   // the staging area is the P^T buffer of every warp
         };
+
+        Walk walk(wk);
+        Seg cur;
+        Codes codes;
+        bool more = walk.next(p, cur), first = true;
+        int t = cur.t0;
+        int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
+        if (more) load_units<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
+        while (more) {
+            if (first) {
+                // the Q buffer is free: this warp has seen the last S^T of the previous query (a warp whose
+                // head group is empty writes no Q)
+                load_q<NM>(p, cur.q, q_s, tl->qc);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tl->q_full);
+            }
+            const int row0 = t * kRows, vis = cur.vis;
+            const bool valid = row0 + row < vis, begins = first;
+            const int old_q = pend_q, old_slot = pend_slot;
+            first = ++t == cur.t1;
+            if (first) {
+                pend_q = cur.q;
+                pend_slot = cur.t0 == 0 && cur.t1 == cur.nt ? -1 : 2 * (int)blockIdx.x + (cur.t0 == 0 ? 1 : 0);
+                more = walk.next(p, cur);
+                t = cur.t0;
+            }
+            decode_units<NM>(
+                t_s, row0, vis, n_cb, codes, tl->full,
+                [&](int m) {
+                    if (n > 0) mwait(&tl->pv[m], (n - 1) & 1u);
+                    return !dead;
+                });
+            if (more) load_units<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
+            if (begins) {
+                if (old_q >= 0 && active) epilogue(old_q, old_slot);
+                named_bar_sync(kBarMath, kMath);   // the staging area is every warp's P^T buffer; qc is complete
+                m_run = -INFINITY;
+                if (lane < 16) tl->cm[set][qd][lane] = make_float2(tl->qc[16 * set + lane], 0.f);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) l_thr[i] = 0.f;
+            }
+            if (active) softmax(valid, begins);
+            ++n;
+        }
+        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot);
 
         // queries without a visible row
         for (int q = blockIdx.x; q < nq; q += gridDim.x) {
             if (visible_rows(p, q / p.s, q % p.s) > 0) continue;
-            for (int hh = warp; hh < p.h; hh += 4 * groups) {
+            for (int hh = warp; hh < p.h; hh += 16) {
                 const int64_t at = (int64_t)q * p.h + hh;
                 const float pl = p.prev_lse ? p.prev_lse[at] : -INFINITY;
                 if (p.lse && lane == 0) p.lse[at] = pl;
@@ -745,40 +765,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 }
             }
         }
-
-        Walk walk(wk);
-        Seg sg, prev;
-        bool pending = false;
-        int2 rec = make_int2(-1, 0);
-        while (walk.next(p, sg)) {
-            // the Q buffer is free: this thread has seen the last S^T of the previous query
-            // (another warp may still scale that S^T: qc has two buffers)
-            qbuf ^= 1;
-            load_q(p, sg.q, tid, q_s, tl->qc[qbuf]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tl->q_full);
-            if (pending) epilogue(prev);
-            named_bar_sync(3, n_soft);
-            m_run = -INFINITY;
-            tl->cm[set][qd][lane] = make_float2(tl->qc[qbuf][32 * set + lane], 0.f);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) l_thr[i] = 0.f;
-            for (int t = sg.t0; t < sg.t1; ++t, ++n) softmax(t * kRows + row < sg.vis, t == sg.t0);
-            prev = sg;
-            pending = true;
-            if (sg.t0 == 0 && sg.t1 < sg.nt) {
-                const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
-                int c = (int)(last * wk.ctas / wk.total);
-                while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
-                while ((long long)c * wk.total / wk.ctas > last) --c;
-                rec = make_int2(sg.q, c);
-            }
-        }
-        if (pending) epilogue(prev);
-        if (tid == 0) p.rec[blockIdx.x] = rec;
-        }
     }
 
     tc_fence_before();
@@ -788,42 +774,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         while (global_timer_ns() - t0 < 50000ull) {
         }
     }
-    if (warp == -4) {
+    if (warp == 16) {
         tc_fence_after();
-        tmem_dealloc(tmem, n_m <= 2 ? 256 : 512);
+        tmem_dealloc(tmem, NM <= 2 ? 256 : 512);
     }
 }
 
 // ------------------------------------------------------------------ joining split queries
 
 // Block (x, head): the split queries that start in CTAs x, x + gridDim.x, ... of the attention kernel.
-// Thread i takes dims 4i .. 4i + 3.
-__global__ void __launch_bounds__(128) merge_kernel(const AttnFp4Params p) {
-    __shared__ float fac[1024];
+// Thread (g, i), g < G, takes dims 4i .. 4i + 3 of every G-th part, four of them in flight; the groups' sums
+// join in shared memory in a fixed order.  G follows from the parts a query can have: one long query (152
+// parts of 2 KB per head) has too few loads in flight with G = 1 (44 us against 12), thousands of short ones
+// (two parts each) would spend their time starting wide blocks (18 us with G = 1, 190 with 8).
+template <int G>
+__global__ void __launch_bounds__(128 * G) merge_kernel(const AttnFp4Params p) {
+    __shared__ float fac[256];
     __shared__ float stat[2];
+    __shared__ float4 part[G][128];
     const int hh = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    const int g = tid >> 7, i4 = tid & 127;
+    __shared__ int2 recs[160];
     griddep_wait();
     griddep_launch_dependents();
-    for (int c = blockIdx.x; c < p.grid; c += gridDim.x) {
-        const int2 rec = p.rec[c];
+    // all of the block's records at once: one after another, a single query's 152 took 50 us
+    for (int k = tid; blockIdx.x + k * gridDim.x < p.grid; k += 128 * G) recs[k] = __ldcg(p.rec + blockIdx.x + k * gridDim.x);
+    __syncthreads();
+    for (int k0 = 0; blockIdx.x + k0 * gridDim.x < p.grid; ++k0) {
+        const int2 rec = recs[k0];
         if (rec.x < 0) continue;
+        const int c = blockIdx.x + k0 * gridDim.x;
         const int parts = rec.y - c + 1;   // slots 2c + 1, 2 (c + 1), 2 (c + 2), ...
         auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
         const int64_t at = (int64_t)rec.x * p.h + hh;
+        // the partial outputs start loading before their factors are known
+        float4 v[4];
+        const bool in = 4 * i4 < p.d;
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)hh * p.d) + (in ? i4 : 0);
+        const int64_t step = (int64_t)p.h * p.d / 4;
+        auto load = [&](int i) { return __ldcg(src + slot(i < parts ? i : parts - 1) * step); };   // always a part
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = load(g + k * G);
         const float sk = p.sink ? __ldg(p.sink + hh) * kLog2e : -INFINITY;
         const float pl = p.prev_lse ? p.prev_lse[at] * kLog2e : -INFINITY;
         if (tid < 32) {
+            float2 ml[5];   // parts <= 160
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+                ml[k] = lane + 32 * k < parts ? __ldcg(p.part_ml + slot(lane + 32 * k) * 64 + hh) : make_float2(-INFINITY, 0.f);
             float mx = fmaxf(sk, pl);
-            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_ml[slot(i) * 64 + hh].x);
+#pragma unroll
+            for (int k = 0; k < 5; ++k) mx = fmaxf(mx, ml[k].x);
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kWarpFull, mx, o));
             if (mx == -INFINITY) mx = 0.f;
             float l = 0.f;
-            for (int i = lane; i < parts; i += 32) {
-                const float2 ml = p.part_ml[slot(i) * 64 + hh];
-                const float f = exp2f((ml.x == -INFINITY ? 0.f : ml.x) - mx);
-                fac[i] = f;
-                l += ml.y * f;
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+                if (lane + 32 * k < parts) {
+                    const float f = exp2f((ml[k].x == -INFINITY ? 0.f : ml[k].x) - mx);
+                    fac[lane + 32 * k] = f;
+                    l += ml[k].y * f;
+                }
             }
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kWarpFull, l, o);
@@ -836,17 +848,34 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnFp4Params p) {
             }
         }
         __syncthreads();
-        if (4 * tid < p.d) {
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    p.part_o + ((int64_t)slot(i) * p.h + hh) * p.d + 4 * tid));
-                const float f = fac[i];
-                o.x += f * v.x;
-                o.y += f * v.y;
-                o.z += f * v.z;
-                o.w += f * v.w;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = g; i0 < parts; i0 += 4 * G) {
+            float4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = load(i0 + (4 + k) * G);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * G;
+                if (i < parts) {
+                    const float f = fac[i];
+                    o.x += f * v[k].x;
+                    o.y += f * v[k].y;
+                    o.z += f * v[k].z;
+                    o.w += f * v[k].w;
+                }
+                v[k] = w[k];
+            }
+        }
+        part[g][i4] = o;
+        __syncthreads();
+        if (g == 0 && in) {
+#pragma unroll
+            for (int k = 1; k < G; ++k) {
+                const float4 q = part[k][i4];
+                o.x += q.x;
+                o.y += q.y;
+                o.z += q.z;
+                o.w += q.w;
             }
             const float inv = stat[0], wp = stat[1];
             o.x *= inv;
@@ -854,13 +883,13 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnFp4Params p) {
             o.z *= inv;
             o.w *= inv;
             if (wp != 0.f && p.prev_out) {
-                const uint2 v = *reinterpret_cast<const uint2*>(p.prev_out + at * p.d + 4 * tid);
-                o.x += wp * __uint_as_float(v.x << 16);
-                o.y += wp * __uint_as_float(v.x & 0xFFFF0000u);
-                o.z += wp * __uint_as_float(v.y << 16);
-                o.w += wp * __uint_as_float(v.y & 0xFFFF0000u);
+                const uint2 pv = *reinterpret_cast<const uint2*>(p.prev_out + at * p.d + 4 * i4);
+                o.x += wp * __uint_as_float(pv.x << 16);
+                o.y += wp * __uint_as_float(pv.x & 0xFFFF0000u);
+                o.z += wp * __uint_as_float(pv.y << 16);
+                o.w += wp * __uint_as_float(pv.y & 0xFFFF0000u);
             }
-            *reinterpret_cast<uint2*>(p.out + at * p.d + 4 * tid) =
+            *reinterpret_cast<uint2*>(p.out + at * p.d + 4 * i4) =
                 make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
         }
         __syncthreads();
@@ -870,9 +899,9 @@ __global__ void __launch_bounds__(128) merge_kernel(const AttnFp4Params p) {
 // ------------------------------------------------------------------ row weights
 
 struct __align__(16) WTail {
-    float2 cl[2][64];                // [query parity] per head: (softmax scale over the f16 scaling, -lse in log2)
+    float2 cl[3][64];                // [query % 3] per head: (softmax scale over the f16 scaling, -lse in log2)
     float qc[64];
-    float acc[kWTiles][2][kRows];    // [tile of the chunk][head group][row]
+    float acc[kWTiles][4][kRows];    // [tile of the chunk][head group][row]
     Work work;
     long long scratch[kThreads / 32];
     uint64_t full[4];
@@ -889,27 +918,40 @@ size_t row_weight_smem(int d) {
     return 1024 + (size_t)n_cb * (kQBlk + kTBlk) + sizeof(WTail);
 }
 
-// The CTA's tiles in chunks of one sequence (at most kWTiles tiles); within a chunk, for each of the CTA's
-// queries, the chunk's tiles.  Items of the list are the sequences.
+// One CTA's work: its piece of the sequences' tiles in chunks of at most kWTiles tiles of one sequence; per
+// chunk its queries [ta, tb) of that sequence; per query the chunk's tiles that the query sees.
 struct WWalk {
     long long pos, hi;
-    int b, off;
-    __device__ __forceinline__ explicit WWalk(const Work& w) : pos(w.lo), hi(w.hi), b(w.q), off(w.off) {}
-    __device__ __forceinline__ bool next(const AttnFp4Params& p, Seg& s) {
+    int b, off, ta, tb;
+    int t0, t1, vis_all;   // the chunk: tiles [t0, t1) of sequence `seq`
+    int seq, q, end, k;    // the query, the end of its tiles, the tile
+    __device__ __forceinline__ WWalk(const Work& w, int ta_, int tb_)
+        : pos(w.lo), hi(w.hi), b(w.q), off(w.off), ta(ta_), tb(tb_), t0(0), t1(0), vis_all(0), seq(0), q(tb_), end(0), k(0) {}
+    __device__ __forceinline__ bool chunk(const AttnFp4Params& p) {
         while (pos < hi) {
-            s.b = b;
-            s.vis = visible_rows(p, b, p.s - 1);
-            s.nt = (s.vis + kRows - 1) / kRows;
-            s.t0 = off;
-            s.t1 = (long long)(s.nt - off) < hi - pos ? s.nt : off + (int)(hi - pos);
-            if (s.t1 - s.t0 > kWTiles) s.t1 = s.t0 + kWTiles;
-            pos += s.t1 - s.t0;
-            off = s.t1;
-            if (off >= s.nt) {
+            seq = b;
+            vis_all = visible_rows(p, b, p.s - 1);
+            const int nt = (vis_all + kRows - 1) / kRows;
+            t0 = off;
+            t1 = (long long)(nt - off) < hi - pos ? nt : off + (int)(hi - pos);
+            if (t1 - t0 > kWTiles) t1 = t0 + kWTiles;
+            pos += t1 - t0;
+            off = t1;
+            if (off >= nt) {
                 ++b;
                 off = 0;
             }
-            if (s.t1 > s.t0) return true;
+            if (t1 > t0) return true;
+        }
+        return false;
+    }
+    // first tile of the next query (from q on) that sees one of the chunk's; false: none is left
+    __device__ __forceinline__ bool query(const AttnFp4Params& p) {
+        for (; q < tb; ++q) {
+            const int nt = (visible_rows(p, seq, q) + kRows - 1) / kRows;
+            end = nt < t1 ? nt : t1;
+            k = t0;
+            if (k < end) return true;
         }
         return false;
     }
@@ -920,40 +962,38 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;
-    constexpr int n_m = NM;
     uint8_t* q_s = smem;
-    uint8_t* t_s = q_s + 2 * n_m * kQBlk;
-    WTail* tl = reinterpret_cast<WTail*>(t_s + 2 * n_m * kTBlk);
+    uint8_t* t_s = q_s + 2 * NM * kQBlk;
+    WTail* tl = reinterpret_cast<WTail*>(t_s + 2 * NM * kTBlk);
 
-    const int tid = (int)threadIdx.x - 128, warp = ((int)threadIdx.x >> 5) - 4, lane = threadIdx.x & 31;
-    const int groups = p.h > 32 ? 2 : 1;
-    const uint32_t n_mma = 32u * (uint32_t)groups;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int groups = (p.h + 15) / 16;
     volatile int* abort = &tl->abort;
     // this CTA's queries of every sequence, and its piece of the tiles
     const int split = (int)blockIdx.x % p.w_split;
     const int ta = (int)((long long)split * p.s / p.w_split), tb = (int)((long long)(split + 1) * p.s / p.w_split);
 
-    if (warp == -4) {
-        tmem_alloc(&tl->tmem_base, 256);
+    if (warp == 16) {
+        tmem_alloc(&tl->tmem_base, 128);
         tmem_relinquish();
     }
     if (tid == 0) {
         for (int m = 0; m < 4; ++m) {
-            mbar_init(&tl->full[m], Deal<NM>::kWarps);
+            mbar_init(&tl->full[m], 8);
             mbar_init(&tl->freed[m], 1);
         }
         for (int k = 0; k < 2; ++k) {
             mbar_init(&tl->s_full[k], 1);
             mbar_init(&tl->s_free[k], 4 * groups);
         }
-        mbar_init(&tl->q_full, 4 * groups);
+        mbar_init(&tl->q_full, 16);
         tl->abort = 0;
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < 2 * n_m * 64 * 8; i += kThreads)
+    for (int i = tid; i < 2 * NM * 64 * 8; i += kThreads)
         if (((i >> 3) & 63) >= p.h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
     if (n_cb & 1)
-        for (int i = threadIdx.x; i < (int)kTBlk / 16; i += kThreads)
+        for (int i = tid; i < (int)kTBlk / 16; i += kThreads)
             reinterpret_cast<uint4*>(t_s + (size_t)n_cb * kTBlk)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     plan_work(p.B, (int)blockIdx.x / p.w_split, (int)gridDim.x / p.w_split, tl->scratch, &tl->work,
@@ -961,64 +1001,30 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);   // warp-uniform, as the compiler can see
-    const Work wk = tl->work;
+    const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);
+    WWalk w(tl->work, ta, tb);
     griddep_wait();   // lse is complete from here on
 
-    // a query's tiles within the chunk: those with a row it sees
-    auto last_tile = [&](const Seg& sg, int t) {
-        const int nt = (visible_rows(p, sg.b, t) + kRows - 1) / kRows;
-        return nt < sg.t1 ? nt : sg.t1;
-    };
-
-    if (warp >= 8) {
-        regs_down<kRegsDecode>();
-        const int m = (warp - 8) / Deal<NM>::kWarps, lt = (warp - 8) % Deal<NM>::kWarps * 32 + lane;
-        if (m < NM) {
-            uint32_t n = 0;
-            bool dead = false;
-            WWalk walk(wk);
-            Seg sg;
-            while (!dead && walk.next(p, sg)) {
-                for (int t = ta; t < tb && !dead; ++t) {
-                    const int end = last_tile(sg, t);
-                    for (int k = sg.t0; k < end && !dead; ++k, ++n) {
-                        Codes<Deal<NM>::U> r;
-                        load_units<NM>(p, sg.b, k * kRows, sg.vis, m, lt, n_cb, r);
-                        if (n > 0) dead = !warp_wait(&tl->freed[m], (n - 1) & 1u, p.status, abort);
-                        if (dead) break;
-                        decode_units<NM>(t_s, k * kRows, sg.vis, m, lt, n_cb, r);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tl->full[m]);
-                    }
-                }
-            }
-        }
-    } else if (warp < 0) {
+    if (warp >= 16) {
         regs_down<kRegsMma>();
-        const uint32_t idesc_qk = idesc_f16_f32(kRows, (int)n_mma, false, false);
+        const uint32_t idesc_qk = idesc_f16_f32(kRows, 16 * groups, false, false);
         const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
         uint32_t n = 0, qn = 0;
         int have = -1;
-        bool ok = warp == -4;
+        bool ok = warp == 16;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = warp_wait(bar, parity, p.status, abort);
             tc_fence_after();
             return ok;
         };
-        WWalk walk(wk);
-        Seg sg;
-        while (ok && walk.next(p, sg)) {
-            for (int t = ta; t < tb && ok; ++t) {
-                const int end = last_tile(sg, t);
-                if (sg.t0 >= end) continue;
-                if (have != sg.b * p.s + t) {   // another query: its Q
+        while (ok && w.chunk(p)) {
+            for (w.q = ta; ok && w.query(p); ++w.q) {
+                if (have != w.seq * p.s + w.q) {   // another query: its Q
                     if (!wait(&tl->q_full, qn & 1u)) break;
                     ++qn;
-                    have = sg.b * p.s + t;
+                    have = w.seq * p.s + w.q;
                 }
-                for (int k = sg.t0; k < end && ok; ++k, ++n) {
+                for (int k = w.k; k < w.end && ok; ++k, ++n) {
                     const uint32_t st = n & 1u;
                     if (n >= 2 && !wait(&tl->s_free[st], ((n >> 1) - 1) & 1u)) break;
 #pragma unroll
@@ -1037,76 +1043,98 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         }
         __syncwarp();
     } else {
-        regs_up<kRegsSoft>();
-        if (warp < 4 * groups) {
+        regs_up<kRegsMath>();
         const int set = warp >> 2, qd = warp & 3;
         const int row = 32 * qd + lane;
+        const bool active = set < groups;
         const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
-        const uint32_t n_soft = 128u * (uint32_t)groups;
         uint32_t n = 0;
-        int have = -1, qbuf = 0;
+        int have = -1, qn = 0;               // qn: queries loaded
         bool dead = false;
-        WWalk walk(wk);
-        Seg sg;
-        while (walk.next(p, sg)) {
-            for (int k = 0; k < sg.t1 - sg.t0; ++k) tl->acc[k][set][row] = 0.f;
-            for (int t = ta; t < tb; ++t) {
-                const int end = last_tile(sg, t);
-                if (sg.t0 >= end) continue;
-                const int q = sg.b * p.s + t;
-                if (have != q) {   // this thread has seen the previous query's last S^T: the Q buffer is free
-                    qbuf ^= 1;
-                    load_q(p, q, tid, q_s, tl->qc);
+        auto mwait = [&](uint64_t* bar, uint32_t parity) {
+            if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
+        };
+        // a tile's scores -> this row's probabilities, summed over the group's heads into acc
+        auto weigh = [&](uint32_t nn, int q, int vis, int k, int slot) {
+            const uint32_t st = nn & 1u;
+            mwait(&tl->s_full[st], (nn >> 1) & 1u);
+            tc_fence_after();
+            uint32_t r[16];
+            tmem_ld16(tmem + lane_base + 64u * st + 16u * (uint32_t)set, r);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tl->s_free[st]);
+            if (k * kRows + row < vis && !dead) {
+                float sum = 0.f;
+                const int hn = p.h - 16 * set;   // heads of the group
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(&tl->cl[q][16 * set + 2 * c]);
+                    const float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * c]), v.x, v.y));
+                    const float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w));
+                    if (2 * c < hn) sum += e0;
+                    if (2 * c + 1 < hn) sum += e1;
+                }
+                tl->acc[slot][set][row] += sum;
+            }
+        };
+        Codes codes;
+        while (w.chunk(p)) {
+            for (int k = 0; k < w.t1 - w.t0; ++k) tl->acc[k][set][row] = 0.f;
+            // the tiles of the chunk's queries in turn; a tile is weighed after the next one has been decoded,
+            // while its QK runs
+            int l_q = -1, l_vis = 0, l_k = 0;     // the tile to be weighed (l_q < 0: none)
+            w.q = ta;
+            bool more = w.query(p);
+            if (more) load_units<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
+            while (more) {
+                const int qi = w.seq * p.s + w.q, k = w.k, vis = visible_rows(p, w.seq, w.q);
+                if (have != qi) {
+                    // the Q buffer is free once the last QK has read the last d-block
+                    if (n > 0) mwait(&tl->freed[NM - 1], (n - 1) & 1u);
+                    load_q<NM>(p, qi, q_s, tl->qc);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane < 8) {   // the warp's own eight heads
-                        const int hd = 8 * warp + lane;
-                        tl->cl[qbuf][hd] =
-                            make_float2(tl->qc[hd], hd < p.h ? -__ldcg(p.lse + (int64_t)q * p.h + hd) * kLog2e : 0.f);
-                    }
                     if (lane == 0) mbar_arrive(&tl->q_full);
-                    named_bar_sync(3, n_soft);
-                    have = q;
-                }
-                const int vis = visible_rows(p, sg.b, t);
-                for (int k = sg.t0; k < end; ++k, ++n) {
-                    const uint32_t st = n & 1u;
-                    if (!dead) dead = !warp_wait(&tl->s_full[st], (n >> 1) & 1u, p.status, abort);
-                    tc_fence_after();
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lane_base + 64u * st + 32u * (uint32_t)set, r);
-                    tmem_ld_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tl->s_free[st]);
-                    if (k * kRows + row < vis && !dead) {
-                        float sum = 0.f;
-                        const int hn = p.h - 32 * set < 32 ? p.h - 32 * set : 32;
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const float4 v = *reinterpret_cast<const float4*>(&tl->cl[qbuf][32 * set + 2 * c]);
-                            const float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * c]), v.x, v.y));
-                            const float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w));
-                            if (2 * c < hn) sum += e0;
-                            if (2 * c + 1 < hn) sum += e1;
-                        }
-                        tl->acc[k - sg.t0][set][row] += sum;
+                    qn = qn == 2 ? 0 : qn + 1;
+                    if (lane < 4) {   // the warp's own four heads
+                        const int hd = 4 * warp + lane;
+                        tl->cl[qn][hd] =
+                            make_float2(tl->qc[hd], hd < p.h ? -__ldcg(p.lse + (int64_t)qi * p.h + hd) * kLog2e : 0.f);
                     }
+                    named_bar_sync(kBarMath, kMath);
+                    have = qi;
+                }
+                if (++w.k == w.end) {
+                    ++w.q;
+                    more = w.query(p);
+                }
+                decode_units<NM>(
+                    t_s, k * kRows, w.vis_all, n_cb, codes, tl->full,
+                    [&](int m) {
+                        if (n > 0) mwait(&tl->freed[m], (n - 1) & 1u);
+                        return !dead;
+                    });
+                if (more) load_units<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
+                if (active && l_q >= 0) weigh(n - 1, l_q, l_vis, l_k, l_k - w.t0);
+                l_q = qn;
+                l_vis = vis;
+                l_k = k;
+                ++n;
+            }
+            if (active && l_q >= 0) weigh(n - 1, l_q, l_vis, l_k, l_k - w.t0);
+            named_bar_sync(kBarMath, kMath);
+            for (int i = tid; i < (w.t1 - w.t0) * kRows; i += kMath) {
+                const int j = w.t0 * kRows + i;
+                if (j < w.vis_all) {
+                    const float* a = &tl->acc[i >> 7][0][i & 127];
+                    const float v = (a[0] + a[kRows]) + (a[2 * kRows] + a[3 * kRows]);
+                    if (p.w_split > 1) p.w_part[((int64_t)split * p.B + w.seq) * p.n_rows + j] = v;
+                    else p.row_weight[(int64_t)w.seq * p.row_weight_bstride + j] += v;
                 }
             }
-            named_bar_sync(3, n_soft);
-            // the chunk's rows: thread = (row, every second tile) when there are two groups
-            for (int k = sg.t0 + set; k < sg.t1; k += groups) {
-                const int j = k * kRows + row;
-                if (j < sg.vis) {
-                    float v = tl->acc[k - sg.t0][0][row];
-                    if (groups == 2) v += tl->acc[k - sg.t0][1][row];
-                    if (p.w_split > 1) p.w_part[((int64_t)split * p.B + sg.b) * p.n_rows + j] = v;
-                    else p.row_weight[(int64_t)sg.b * p.row_weight_bstride + j] += v;
-                }
-            }
-            named_bar_sync(3, n_soft);
-        }
+            named_bar_sync(kBarMath, kMath);
         }
     }
 
@@ -1117,9 +1145,9 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         while (global_timer_ns() - t0 < 50000ull) {
         }
     }
-    if (warp == -4) {
+    if (warp == 16) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, 128);
     }
 }
 
@@ -1175,7 +1203,11 @@ cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attn_fp4_kernel<NM><<<p.grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_after(merge_kernel, dim3((unsigned)(nq < p.grid ? nq : p.grid), (unsigned)p.h), 128, 0, p, stream);
+    const int parts = p.grid / nq + 1;   // of a query, when they are alike
+    const dim3 mg((unsigned)(nq < p.grid ? nq : p.grid), (unsigned)p.h);
+    e = parts > 16  ? launch_after(merge_kernel<8>, mg, 1024, 0, p, stream)
+        : parts > 4 ? launch_after(merge_kernel<2>, mg, 256, 0, p, stream)
+                    : launch_after(merge_kernel<1>, mg, 128, 0, p, stream);
     if (e != cudaSuccess || !p.row_weight || p.n_rows == 0) return e;
     smem = row_weight_smem(p.d);
     e = cudaFuncSetAttribute(row_weight_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
