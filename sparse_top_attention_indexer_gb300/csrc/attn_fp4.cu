@@ -6,20 +6,19 @@
 //   row_weight[b, j] += sum_{t, h} e^{s_hj - L_h}
 // k_j = the row's E2M1 codes times its E4M3 scale per 16, serving as key and value for all heads.
 //
-// attn_fp4_kernel: persistent CTAs, one per SM; the queries' 128-row tiles form one long list that is cut
+// attn_fp4_kernel: persistent CTAs, one per SM; the queries' 64-row tiles form one long list that is cut
 // into equal contiguous pieces, so a few long queries, many short ones and ragged batches all fill
 // the GPU.  A query whose tiles fall to several CTAs leaves one fp32 partial per CTA; merge_kernel joins
-// them.  17 working warps:
-//   * warp 16 issues the MMAs:  S^T = tile . Q^T (M = 128 rows, N = heads), O^T += V^T . P^T (M = 128
-//     dims per block, K = 128 rows; the same tile read as an MN-major operand);
-//   * warps 0..15 do the rest of a tile in turn: decode its rows from codes loaded a tile ahead (one d-block
-//     of 128 dims at a time, as the previous tile's PV releases it), then its softmax (thread = row, four
-//     groups of 16 heads; the running maxima move only when a score passes them by 2^8), and per
-//     query load Q and write the output.
-// With 512 dims, Q (64 KB), one tile (128 KB) and P^T (16 KB) fill shared memory, so a tile is a chain: decode
-// what the PV has released, QK, softmax, PV.  What bounds the kernel is that chain's latency, not the 3072
-// cycles of its MMAs; hence all 16 warps on each link of it (separate decoding and softmax warps, 8 each,
-// took 6,800 cycles a tile).
+// them.  Two tile buffers; 17 working warps:
+//   * warps 8..15 decode the rows into the free buffer, from codes loaded a tile ahead, one half (256 dims)
+//     at a time as the PV two tiles earlier releases it;
+//   * warp 16 issues the MMAs: QK of tile i + 1, S^T = tile . Q^T (M = 64 rows, N = heads), then PV of tile i,
+//     O^T += V^T . P^T (M = 128 dims per block, K = 64 rows; the same tile read as an MN-major operand);
+//   * warps 0..7 load Q, run the online softmax (two groups of 32 heads; the running maxima move only when a
+//     score passes them by 2^8) and write the outputs.
+// With 512 dims, Q (64 KB), two tiles of 64 rows (128 KB) and two P^T (16 KB) fill shared memory.  One tile of
+// 128 rows instead would halve the QK's MMAs (one of M = 64 costs as much as one of M = 128), but leaves
+// decode, QK, softmax and PV of a tile to run one after another: 8,400 cycles per 128 rows.
 //
 // f16 operands: an E2M1 value (2 significant bits) times an E4M3 value (4) is exact in f16 (at most 6
 // significant bits, magnitudes 2^-10 .. 2688), so the tile is exact.  Q is bf16: each head's values are
@@ -43,18 +42,19 @@
 namespace sti {
 namespace {
 
-constexpr int kMath = 512;                     // decode, softmax, Q, outputs: warps 0..15
-constexpr int kThreads = kMath + 128;          // warp 16: MMA issue; 17..19 only complete its warpgroup
-// registers per thread after setmaxnreg: 512 x 104 + 128 x 64 = 61,440, the 640 x 96 of the launch
-constexpr int kRegsMath = 104, kRegsMma = 64;
-constexpr int kRows = 128;                     // rows per tile
+constexpr int kThreads = 640;                  // 8 softmax warps, 8 decoding warps, 1 MMA warp (and 3 that
+                                               // only complete its warpgroup)
+// registers per thread after setmaxnreg: 256 x 128 + 256 x 80 + 128 x 64 = 61,440, the 640 x 96 of the launch
+constexpr int kRegsSoft = 128, kRegsDecode = 80, kRegsMma = 64;
+constexpr int kRows = 64;                      // rows per tile
 constexpr uint32_t kQBlk = 64 * 128;           // a Q column block: 64 heads x 64 dims
-constexpr uint32_t kTBlk = kRows * 128;        // a tile column block: 128 rows x 64 dims
-constexpr uint32_t kTmS = 0;                   // TMEM columns of S^T
-constexpr uint32_t kTmO = 64;                  // O^T d-block m at [64 + 64 m, 128 + 64 m)
+constexpr uint32_t kTBlk = kRows * 128;        // a tile column block: 64 rows x 64 dims
+constexpr uint32_t kPBuf = kRows * 128;        // a P^T buffer: 64 rows x 64 heads
+constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at columns [64 b, 64 b + 64), O^T d-block
+                                               // m at [128 + 64 m, 192 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kWTiles = 8;                     // row weights: tiles per chunk (accumulators in shared memory)
-constexpr uint32_t kBarMath = 5;               // named barriers: 1..4 the head groups, 5 all math warps
+constexpr int kWTiles = 56;                    // row weights: tiles per chunk (accumulators in shared memory)
+constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 // instruction descriptor, kind::f16 with f16 A/B (format 0) and fp32 accumulator
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
@@ -85,19 +85,18 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
     asm volatile("" : "+r"(v));
     return v;
 }
-// S^T (+)= tile . Q^T over one d-block (two column blocks).  a, b: low descriptor words of the tile and Q.
-__device__ __forceinline__ void qk_blocks(bool first, uint32_t s_tmem, uint32_t a, uint32_t b, uint32_t hi,
-                                          uint32_t idesc) {
+// S^T (+)= tile . Q^T over d-block m (two column blocks).  a, b: low descriptor words of the tile and Q.
+__device__ __forceinline__ void qk_blocks(int m, uint32_t s_tmem, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc) {
     a = opaque(a);
     b = opaque(b);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 8 * m; k < 8 * m + 8; ++k) {
         const uint32_t ak = a + (k >> 2) * (kTBlk / 16) + 2 * (k & 3), bk = b + (k >> 2) * (kQBlk / 16) + 2 * (k & 3);
-        if (first && k == 0) umma<false>(s_tmem, ak, hi, bk, hi, idesc);
+        if (k == 0) umma<false>(s_tmem, ak, hi, bk, hi, idesc);
         else umma<true>(s_tmem, ak, hi, bk, hi, idesc);
     }
 }
-// O^T (+)= V^T . P^T: one d-block, eight K steps.
+// O^T (+)= V^T . P^T: one d-block, four K steps.
 template <bool FIRST>
 __device__ __forceinline__ void pv_block(uint32_t o_tmem, uint32_t a, uint32_t a_hi, uint32_t b, uint32_t b_hi,
                                          uint32_t idesc) {
@@ -108,6 +107,15 @@ __device__ __forceinline__ void pv_block(uint32_t o_tmem, uint32_t a, uint32_t a
         if (FIRST && k == 0) umma<false>(o_tmem, a, a_hi, b, b_hi, idesc);
         else umma<true>(o_tmem, a + 128 * k, a_hi, b + 128 * k, b_hi, idesc);
     }
+}
+// S^T of 16 rows (a warp's TMEM lanes 0..15: M = 64 accumulators lie there) x 32 heads: lane l receives, for
+// g < 4, heads 8 g + 2 (l % 4) + {0, 1} of row l / 4 in r[4 g], r[4 g + 1] and of row l / 4 + 8 in r[4 g + 2], r[4 g + 3].
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
 }
 
 template <int N>
@@ -246,37 +254,29 @@ __device__ __forceinline__ void plan_work(int n, int part, int parts, long long*
 
 // ------------------------------------------------------------------ operands
 
-// Decoding: 8 warps take a d-block (warps 0..7 blocks 0 and 2, warps 8..15 blocks 1 and 3).  A lane takes 32
-// codes (16 bytes, 2 scales) of one row: lane = 4 (row % 8) + quarter of the d-block, so that a warp's load
-// covers 64 contiguous bytes of 8 rows (one row per lane would touch 32 cache lines per load: the loads of a
-// tile then took 3600 cycles to issue) and its stores spread over all banks.
+// Decoding: a warp takes 8 rows of a tile, a lane 32 codes (16 bytes, 2 scales) of one row in every d-block:
+// lane = 4 (row % 8) + quarter of the d-block, so that a warp's load covers 64 contiguous bytes of 8 rows (one
+// row per lane would touch 32 cache lines per load) and its stores spread over all banks.
+template <int NM>
 struct Codes {
-    uint4 c[2][2];      // [d-block][row, row + 64]
-    uint32_t s[2];      // the two rows' scale pairs
+    uint4 c[NM];
+    uint16_t s[NM];
 };
 
-// This thread's codes of its d-block number u of a tile.
-__device__ __forceinline__ void load_unit(const AttnFp4Params& p, int b, int row0, int vis, int n_cb, int u, Codes& r) {
-    const int lane = threadIdx.x & 31, ch = lane & 3, m = 2 * u + (threadIdx.x >> 8);
-    const int row = row0 + ((threadIdx.x >> 5) & 7) * 8 + (lane >> 2);
-    if (2 * m + (ch >> 1) >= n_cb) return;
-    const uint8_t* cr = p.codes + (int64_t)b * p.codes_bstride + (int64_t)row * (p.d / 2) + m * 64 + ch * 16;
-    const uint8_t* sr = p.scales + (int64_t)b * p.scales_bstride + (int64_t)row * (p.d / 16) + m * 8 + ch * 2;
-    uint32_t s0 = 0u, s1 = 0u;
-    if (row < vis) {
-        r.c[u][0] = __ldg(reinterpret_cast<const uint4*>(cr));
-        s0 = __ldg(reinterpret_cast<const uint16_t*>(sr));
-    }
-    if (row + 64 < vis) {
-        r.c[u][1] = __ldg(reinterpret_cast<const uint4*>(cr + 32 * p.d));
-        s1 = __ldg(reinterpret_cast<const uint16_t*>(sr + 4 * p.d));
-    }
-    r.s[u] = s0 | (s1 << 16);
-}
 template <int NM>
-__device__ __forceinline__ void load_units(const AttnFp4Params& p, int b, int row0, int vis, int n_cb, Codes& r) {
+__device__ __forceinline__ void load_codes(const AttnFp4Params& p, int b, int row0, int vis, int n_cb, Codes<NM>& r) {
+    const int lane = threadIdx.x & 31, ch = lane & 3;
+    const int row = row0 + ((threadIdx.x >> 5) & 7) * 8 + (lane >> 2);
+    if (row >= vis) return;
+    const uint8_t* cr = p.codes + (int64_t)b * p.codes_bstride + (int64_t)row * (p.d / 2) + ch * 16;
+    const uint8_t* sr = p.scales + (int64_t)b * p.scales_bstride + (int64_t)row * (p.d / 16) + ch * 2;
 #pragma unroll
-    for (int u = 0; u < (NM + 1) / 2; ++u) load_unit(p, b, row0, vis, n_cb, u, r);
+    for (int m = 0; m < NM; ++m) {
+        if (2 * m + (ch >> 1) < n_cb) {
+            r.c[m] = __ldg(reinterpret_cast<const uint4*>(cr + 64 * m));
+            r.s[m] = __ldg(reinterpret_cast<const uint16_t*>(sr + 8 * m));
+        }
+    }
 }
 
 // Eight codes (nibble i = element i) times the scale pair s2 = (s, s), as eight f16.
@@ -312,52 +312,50 @@ __device__ __forceinline__ void decode_half(uint8_t* dst, int row, int half, boo
             valid ? decode8(w[i], *reinterpret_cast<const __half2*>(&sc[i >> 1])) : make_uint4(0, 0, 0, 0);
 }
 
-// Decode this thread's part of the tile; `released(m)` waits until d-block m may be overwritten (false: gave
-// up), full[m] gets one arrival per warp.
+// Decode this thread's part of the tile into the buffer at t_s, half by half: `released(h)` waits until half h
+// may be overwritten (false: gave up), full[h] gets one arrival per warp.
 template <int NM, class F>
-__device__ __forceinline__ void decode_units(uint8_t* t_s, int row0, int vis, int n_cb, const Codes& r, uint64_t* full,
-                                             F released) {
+__device__ __forceinline__ bool decode_tile(uint8_t* t_s, int row0, int vis, int n_cb, const Codes<NM>& r, uint64_t* full,
+                                            F released) {
     const int lane = threadIdx.x & 31, ch = lane & 3;
     const int row = ((threadIdx.x >> 5) & 7) * 8 + (lane >> 2);
 #pragma unroll
-    for (int u = 0; u < (NM + 1) / 2; ++u) {
-        const int m = 2 * u + (threadIdx.x >> 8), cb = 2 * m + (ch >> 1);
-        if (m < NM) {
-            if (!released(m)) return;
-            if (cb < n_cb) {
-                uint8_t* dst = t_s + (size_t)cb * kTBlk + row * 128;
-                decode_half(dst, row, ch & 1, row0 + row < vis, r.c[u][0], r.s[u] & 0xFFFFu);
-                decode_half(dst + 64 * 128, row, ch & 1, row0 + row + 64 < vis, r.c[u][1], r.s[u] >> 16);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[m]);
+    for (int h = 0; h < (NM + 1) / 2; ++h) {
+        if (!released(h)) return false;
+#pragma unroll
+        for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m) {
+            const int cb = 2 * m + (ch >> 1);
+            if (cb < n_cb) decode_half(t_s + (size_t)cb * kTBlk + row * 128, row, ch & 1, row0 + row < vis, r.c[m], r.s[m]);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[h]);
     }
+    return true;
 }
 
-// Query qi's heads as f16 into the swizzled column blocks at q_s, eight math threads per head, each head
+// Query qi's heads as f16 into the swizzled column blocks at q_s, four softmax threads per head, each head
 // scaled by 2^f; qc[head] = scale_log2 * 2^-f.
 template <int NM>
 __device__ __forceinline__ void load_q(const AttnFp4Params& p, int qi, uint8_t* q_s, float* qc) {
-    const int head = threadIdx.x >> 3, part = threadIdx.x & 7;
-    const int n = p.d / 8;   // 16-byte chunks of a head: part, part + 8, ... (at most eight per thread)
+    const int head = threadIdx.x >> 2, part = threadIdx.x & 3;
+    const int n = p.d / 8;   // 16-byte chunks of a head: part, part + 4, ... (at most sixteen per thread)
     const bool in = head < p.h;
     const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qi * p.h + (in ? head : 0)) * p.d);
-    uint4 v[2 * NM];
+    uint4 v[4 * NM];
     uint32_t mx = 0;
 #pragma unroll
-    for (int k = 0; k < 2 * NM; ++k) {
+    for (int k = 0; k < 4 * NM; ++k) {
         v[k] = make_uint4(0, 0, 0, 0);
-        if (in && part + 8 * k < n) v[k] = __ldg(src + part + 8 * k);
+        if (in && part + 4 * k < n) v[k] = __ldg(src + part + 4 * k);
     }
 #pragma unroll
-    for (int k = 0; k < 2 * NM; ++k)
+    for (int k = 0; k < 4 * NM; ++k)
         mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[k].x & 0x7FFF7FFFu, v[k].y & 0x7FFF7FFFu),
                                    __vmaxu2(v[k].z & 0x7FFF7FFFu, v[k].w & 0x7FFF7FFFu)));
     mx = max(mx & 0xFFFFu, mx >> 16);
 #pragma unroll
-    for (int o = 1; o <= 4; o <<= 1) mx = max(mx, __shfl_xor_sync(kWarpFull, mx, o));
+    for (int o = 1; o <= 2; o <<= 1) mx = max(mx, __shfl_xor_sync(kWarpFull, mx, o));
     int f = 139 - (int)(mx >> 7);   // largest into [2^12, 2^13); mx >> 7: its exponent field
     f = f > 127 ? 127 : f;          // (-116 .. 127)
     const float up = __uint_as_float((uint32_t)(f + 127) << 23);
@@ -365,8 +363,8 @@ __device__ __forceinline__ void load_q(const AttnFp4Params& p, int qi, uint8_t* 
     const float down = f == 127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(127 - f) << 23);
     if (part == 0) qc[head] = in ? p.scale_log2 * down : 0.f;
 #pragma unroll
-    for (int k = 0; k < 2 * NM; ++k) {
-        if (!in || part + 8 * k >= n) continue;
+    for (int k = 0; k < 4 * NM; ++k) {
+        if (!in || part + 4 * k >= n) continue;
         const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
         uint32_t o[4];
 #pragma unroll
@@ -375,8 +373,8 @@ __device__ __forceinline__ void load_q(const AttnFp4Params& p, int qi, uint8_t* 
                                                 __uint_as_float(w[i] & 0xFFFF0000u) * up);
             o[i] = *reinterpret_cast<const uint32_t*>(&x);
         }
-        // chunk part + 8 k: column block k, chunk `part` of its row
-        *reinterpret_cast<uint4*>(q_s + k * kQBlk + head * 128 + ((part ^ (head & 7)) << 4)) =
+        const int chunk = part + 4 * (k & 1);   // of column block k / 2
+        *reinterpret_cast<uint4*>(q_s + (k >> 1) * kQBlk + head * 128 + ((chunk ^ (head & 7)) << 4)) =
             make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
@@ -390,37 +388,51 @@ __device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float((ui
 // ------------------------------------------------------------------ attention
 
 struct __align__(16) Tail {
-    float2 cm[4][4][16];      // [head group][warp of the group]: its copy of (softmax scale, -running maximum)
+    float2 cm[2][4][32];      // [head group][warp of the group]: its copy of (softmax scale, -running maximum)
     float qc[64];             // per head: softmax scale (log2) over its f16 scaling
-    float red[2][4][4][16];   // [tile parity][group][warp]: per-warp maxima
-    float lsum[4][4][16];
+    float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
+    float lsum[2][4][32];
     Work work;
     long long scratch[kThreads / 32];
-    uint64_t full[4];         // d-block m of the tile decoded: one arrival per warp
-    uint64_t pv[4];           // the tile's PV of d-block m done
-    uint64_t s_full, p_full, q_full;
+    uint64_t full[2][2];      // [buffer][half of the dims] decoded: one arrival per decoding warp
+    uint64_t freed[2][2];     // the PV has read it
+    uint64_t s_full[2], p_full[2];
+    uint64_t q_full;
     uint32_t tmem_base;
     int abort;
 };
 
 size_t attn_smem(int d) {
     const int n_cb = (d + 127) / 128 * 2;
-    return 1024 + (size_t)n_cb * (kQBlk + kTBlk) + kRows * 128 + sizeof(Tail);
+    return 1024 + (size_t)n_cb * (kQBlk + 2 * kTBlk) + 2 * kPBuf + sizeof(Tail);
+}
+
+// What no thread writes later: Q rows of heads >= h, the dims past d of the last d-block.
+__device__ __forceinline__ void zero_padding(int h, int n_cb, int n_m, uint8_t* q_s, uint8_t* t_s) {
+    for (int i = threadIdx.x; i < 2 * n_m * 64 * 8; i += kThreads)
+        if (((i >> 3) & 63) >= h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
+    if (n_cb & 1)
+        for (int i = threadIdx.x; i < 2 * (int)kTBlk / 16; i += kThreads) {
+            const int buf = i / (int)(kTBlk / 16), k = i % (int)(kTBlk / 16);
+            reinterpret_cast<uint4*>(t_s + (size_t)(2 * n_m * buf + n_cb) * kTBlk)[k] = make_uint4(0, 0, 0, 0);
+        }
 }
 
 template <int NM>   // d-blocks of 128 dims
 __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Params p) {
+    constexpr int kHalves = (NM + 1) / 2;
+    constexpr uint32_t kTile = 2 * NM * kTBlk;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;                 // column blocks of 64 dims
     uint8_t* q_s = smem;                       // [2 NM][64 heads][128 B]
-    uint8_t* t_s = q_s + 2 * NM * kQBlk;       // [2 NM][128 rows][128 B]
-    uint8_t* p_s = t_s + 2 * NM * kTBlk;       // P^T [128 rows][64 heads] f16
-    Tail* tl = reinterpret_cast<Tail*>(p_s + kRows * 128);
+    uint8_t* t_s = q_s + 2 * NM * kQBlk;       // two tiles [2 NM][64 rows][128 B]
+    uint8_t* p_s = t_s + 2 * kTile;            // two P^T [64 rows][64 heads] f16
+    Tail* tl = reinterpret_cast<Tail*>(p_s + 2 * kPBuf);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nq = p.B * p.s;
-    const int groups = (p.h + 15) / 16;        // groups of 16 heads
+    const int groups = p.h > 32 ? 2 : 1;       // groups of 32 heads
     volatile int* abort = &tl->abort;
 
     if (warp == 16) {
@@ -428,22 +440,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int m = 0; m < 4; ++m) {
-            mbar_init(&tl->full[m], 8);
-            mbar_init(&tl->pv[m], 1);
+        for (int k = 0; k < 2; ++k) {
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&tl->full[k][h], 8);
+                mbar_init(&tl->freed[k][h], 1);
+            }
+            mbar_init(&tl->s_full[k], 1);
+            mbar_init(&tl->p_full[k], 4 * groups);
         }
-        mbar_init(&tl->s_full, 1);
-        mbar_init(&tl->p_full, 4 * groups);
-        mbar_init(&tl->q_full, 16);
+        mbar_init(&tl->q_full, 8);
         tl->abort = 0;
         fence_mbar_init();
     }
-    // what no thread writes later: Q rows of heads >= h, the dims past d of the last d-block
-    for (int i = tid; i < 2 * NM * 64 * 8; i += kThreads)
-        if (((i >> 3) & 63) >= p.h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
-    if (n_cb & 1)
-        for (int i = tid; i < (int)kTBlk / 16; i += kThreads)
-            reinterpret_cast<uint4*>(t_s + (size_t)n_cb * kTBlk)[i] = make_uint4(0, 0, 0, 0);
+    zero_padding(p.h, n_cb, NM, q_s, t_s);
     fence_proxy_async_smem();
     plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
               [&](int q) { return (visible_rows(p, q / p.s, q % p.s) + kRows - 1) / kRows; });
@@ -457,23 +466,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
     if (warp >= 16) {
         regs_down<kRegsMma>();
         // -------------------------------------------------------------- MMA issue
-        const uint32_t idesc_qk = idesc_f16_f32(kRows, 16 * groups, false, false);
-        const uint32_t idesc_pv = idesc_f16_f32(kRows, 16 * groups, true, true);
+        const int n_mma = (p.h + 15) / 16 * 16;
+        const uint32_t idesc_qk = idesc_f16_f32(kRows, n_mma, false, false);
+        const uint32_t idesc_pv = idesc_f16_f32(128, n_mma, true, true);
         // descriptors of the tile and Q (K-major), the tile (MN-major) and P^T (MN-major)
         const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
         const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128);
-        const uint64_t dp = sdesc(smem_u32(p_s), kRows * 128u, 1024, kLayoutSW128);
+        const uint64_t dp = sdesc(smem_u32(p_s), kPBuf, 1024, kLayoutSW128);
         uint32_t n = 0, qn = 0;
-        Walk walk(wk);
-        Seg sg;
         // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
-        bool ok = warp == 16;
+        bool ok = warp == 16, starts = false;   // starts: tile n - 1 is its segment's first
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = warp_wait(bar, parity, p.status, abort);
             tc_fence_after();
             return ok;
         };
+        auto pv = [&](uint32_t i) {
+            const uint32_t buf = i & 1u;
+            if (!wait(&tl->p_full[buf], (i >> 1) & 1u)) return;
+            if (elect_one()) {
+#pragma unroll
+                for (int m = 0; m < NM; ++m) {
+                    const uint32_t o = tmem + kTmO + 64u * (uint32_t)m;
+                    const uint32_t a = lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16);
+                    const uint32_t b = lo32(dp) + buf * (kPBuf / 16);
+                    if (starts) pv_block<true>(o, a, hi32(dv), b, hi32(dp), idesc_pv);
+                    else pv_block<false>(o, a, hi32(dv), b, hi32(dp), idesc_pv);
+                    if ((m & 1) || m == NM - 1) umma_commit(&tl->freed[buf][m >> 1]);
+                }
+            }
+            __syncwarp();
+        };
         int2 rec = make_int2(-1, 0);
+        Walk walk(wk);
+        Seg sg;
         while (ok && walk.next(p, sg)) {
             if (sg.t0 == 0 && sg.t1 < sg.nt) {
                 const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
@@ -482,47 +508,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 while ((long long)c * wk.total / wk.ctas > last) --c;
                 rec = make_int2(sg.q, c);
             }
-            if (!wait(&tl->q_full, qn & 1u)) break;
+            if (n > 0) pv(n - 1);   // the previous segment's last tile
+            if (!ok || !wait(&tl->q_full, qn & 1u)) break;
             ++qn;
             for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
+                const uint32_t buf = n & 1u;
 #pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    if (!wait(&tl->full[m], n & 1u)) break;
+                for (int h = 0; h < kHalves; ++h) {
+                    if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
                     if (elect_one()) {
-                        qk_blocks(m == 0, tmem + kTmS, lo32(dk) + (uint32_t)m * (2 * kTBlk / 16),
-                                  lo32(dq) + (uint32_t)m * (2 * kQBlk / 16), hi32(dk), idesc_qk);
-                        if (m == NM - 1) umma_commit(&tl->s_full);
+#pragma unroll
+                        for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
+                            qk_blocks(m, tmem + 64u * buf, lo32(dk) + buf * (kTile / 16), lo32(dq), hi32(dk), idesc_qk);
+                        if (h == kHalves - 1) umma_commit(&tl->s_full[buf]);
                     }
                     __syncwarp();
                 }
-                if (!ok) break;
-                if (!wait(&tl->p_full, n & 1u)) break;
-                if (elect_one()) {
-#pragma unroll
-                    for (int m = 0; m < NM; ++m) {
-                        const uint32_t o = tmem + kTmO + 64u * (uint32_t)m, a = lo32(dv) + (uint32_t)m * (2 * kTBlk / 16);
-                        if (t == sg.t0) pv_block<true>(o, a, hi32(dv), lo32(dp), hi32(dp), idesc_pv);
-                        else pv_block<false>(o, a, hi32(dv), lo32(dp), hi32(dp), idesc_pv);
-                        umma_commit(&tl->pv[m]);
-                    }
-                }
-                __syncwarp();
+                if (ok && t > sg.t0) pv(n - 1);
+                starts = t == sg.t0;
             }
         }
+        if (ok && n > 0) pv(n - 1);
         if (warp == 16 && lane == 0) p.rec[blockIdx.x] = rec;
         __syncwarp();
+    } else if (warp >= 8) {
+        regs_down<kRegsDecode>();
+        // -------------------------------------------------------------- decode
+        uint32_t n = 0;
+        bool dead = false;
+        Walk walk(wk);
+        Seg cur;
+        Codes<NM> codes;
+        bool more = walk.next(p, cur);
+        int t = cur.t0;
+        if (more) load_codes<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
+        while (more && !dead) {
+            const uint32_t buf = n & 1u;
+            dead = !decode_tile<NM>(t_s + buf * kTile, t * kRows, cur.vis, n_cb, codes, tl->full[buf], [&](int h) {
+                return n < 2 || warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort);
+            });
+            ++n;
+            if (++t == cur.t1) {
+                more = walk.next(p, cur);
+                t = cur.t0;
+            }
+            if (more) load_codes<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
+        }
     } else {
-        regs_up<kRegsMath>();
-        // -------------------------------------------------------------- decode, Q, softmax, outputs
+        regs_up<kRegsSoft>();
+        // -------------------------------------------------------------- Q, softmax, outputs
         const int set = warp >> 2, qd = warp & 3;
-        const int row = 32 * qd + lane;
-        const bool active = set < groups;      // this warp's head group has heads
+        const int row = 16 * qd + (lane >> 2);   // this thread's tile rows: row, row + 8
+        const int l4 = lane & 3;                 // its heads: 32 set + 8 g + 2 l4 + {0, 1}
+        const bool active = set < groups;        // this warp's head group has heads
         const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
         const uint32_t bar_set = 1u + (uint32_t)set;
         uint32_t n = 0;
         bool dead = false;
-        float m_run = -INFINITY;               // lane l: head 16 set + l / 2
-        float l_thr[16];                       // this row's running sums of the group's heads
+        float m_run = -INFINITY;                 // lane l: head 32 set + l
+        float l_thr[8];                          // running sums of the thread's heads over its rows
 
         auto mwait = [&](uint64_t* bar, uint32_t parity) {
             if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
@@ -530,231 +574,236 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
 
         // One tile's probabilities.  cm holds (c, -m) of each head: c the softmax scale (log2) over the head's f16
         // scaling, m its running maximum, so y = S c - m is one FMA and 2^y the probability.
-        auto softmax = [&](bool valid, bool first) {
-            mwait(&tl->s_full, n & 1u);
+        auto softmax = [&](int left, bool first) {   // left: visible rows from this thread's first one on
+            const uint32_t buf = n & 1u;
+            mwait(&tl->s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
-            valid = valid && !dead;
+            const bool v0 = left > 0 && !dead, v1 = left > 8 && !dead;
             const float2* cm = &tl->cm[set][qd][0];
+            const uint32_t ts = tmem + lane_base + 64u * buf + 32u * (uint32_t)set;
             uint32_t r[16];
-            tmem_ld16(tmem + lane_base + kTmS + 16u * (uint32_t)set, r);
+            tmem_ld_rows16(ts, r);
             tmem_ld_wait();
             float y[16];
-            float top = -INFINITY;
+            float top0 = -INFINITY, top1 = -INFINITY;
+            auto scale = [&]() {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float4 v = *reinterpret_cast<const float4*>(cm + 2 * c);
-                y[2 * c] = fmaf(__uint_as_float(r[2 * c]), v.x, v.y);
-                y[2 * c + 1] = fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w);
-                top = fmaxf(top, fmaxf(y[2 * c], y[2 * c + 1]));
+                for (int g = 0; g < 4; ++g) {
+                    const float4 v = *reinterpret_cast<const float4*>(cm + 8 * g + 2 * l4);
+                    y[4 * g] = fmaf(__uint_as_float(r[4 * g]), v.x, v.y);
+                    y[4 * g + 1] = fmaf(__uint_as_float(r[4 * g + 1]), v.z, v.w);
+                    y[4 * g + 2] = fmaf(__uint_as_float(r[4 * g + 2]), v.x, v.y);
+                    y[4 * g + 3] = fmaf(__uint_as_float(r[4 * g + 3]), v.z, v.w);
+                }
+            };
+            scale();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                top0 = fmaxf(top0, fmaxf(y[4 * g], y[4 * g + 1]));
+                top1 = fmaxf(top1, fmaxf(y[4 * g + 2], y[4 * g + 3]));
             }
             // the maxima stay unless a visible score passes its head's by 2^8
-            const bool need = !named_bar_and(bar_set, 128, !(first || (valid && top > 8.f)));
+            const bool need = !named_bar_and(bar_set, 128, !(first || (v0 && top0 > 8.f) || (v1 && top1 > 8.f)));
             if (need) {
-                {
-                    float v2[16];
+                float* red = &tl->red[buf][set][qd][0];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v2[i] = valid ? y[i] : -INFINITY;
-                    warp_reduce_scatter_n<16, true>(v2);   // lane l: head l / 2 over this warp's rows
-                    if (!(lane & 1)) tl->red[n & 1u][set][qd][lane >> 1] = v2[0];
-                }
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v = fmaxf(v0 ? y[4 * g + c] : -INFINITY, v1 ? y[4 * g + 2 + c] : -INFINITY);
+#pragma unroll
+                        for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kWarpFull, v, o));
+                        if (lane < 4) red[8 * g + 2 * lane + c] = v;
+                    }
                 named_bar_sync(bar_set, 128);
-                const float* rr = &tl->red[n & 1u][set][0][lane >> 1];
-                const float old = -cm[lane >> 1].y;        // what y is relative to
-                const float mt = fmaxf(fmaxf(rr[0], rr[16]), fmaxf(rr[32], rr[48])) + old;
+                const float* rr = &tl->red[buf][set][0][lane];
+                const float old = -cm[lane].y;             // what y is relative to
+                const float mt = fmaxf(fmaxf(rr[0], rr[32]), fmaxf(rr[64], rr[96])) + old;
                 const float m_new = (m_run == -INFINITY || mt > m_run + 8.f) ? fmaxf(m_run, mt) : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
                 m_run = m_new;
                 __syncwarp();
                 // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
                 // scores show in its output
-                if (!(lane & 1)) tl->cm[set][qd][lane >> 1].y = m_new == -INFINITY ? 0.f : -m_new;
+                tl->cm[set][qd][lane].y = m_new == -INFINITY ? 0.f : -m_new;
                 __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(cm + 2 * c);
-                    y[2 * c] = fmaf(__uint_as_float(r[2 * c]), v.x, v.y);
-                    y[2 * c + 1] = fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w);
-                }
+                scale();
                 if (!first && !dead && __any_sync(kWarpFull, alpha != 1.f)) {
+                    mwait(&tl->freed[buf ^ 1u][kHalves - 1], ((n - 1) >> 1) & 1u);   // the previous tile's PV is done
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int m = 0; m < NM; ++m) {
-                        const uint32_t ta = tmem + lane_base + kTmO + 64u * (uint32_t)m + 16u * (uint32_t)set;
+                    for (int k = 0; k < 2 * NM; ++k) {
+                        const uint32_t ta = tmem + lane_base + kTmO + 32u * (uint32_t)(2 * (k >> 1) + set) + 16u * (k & 1);
                         uint32_t o[16];
                         tmem_ld16(ta, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kWarpFull, alpha, 2 * i));
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kWarpFull, alpha, 16 * (k & 1) + i));
                         tmem_st16(ta, o);
                     }
                     tmem_st_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) l_thr[i] *= __shfl_sync(kWarpFull, alpha, 2 * i);
+                    for (int g = 0; g < 4; ++g) {
+                        l_thr[2 * g] *= __shfl_sync(kWarpFull, alpha, 8 * g + 2 * l4);
+                        l_thr[2 * g + 1] *= __shfl_sync(kWarpFull, alpha, 8 * g + 2 * l4 + 1);
+                    }
                 }
             }
-            uint8_t* prow = p_s + row * 128;
+            uint8_t* prow = p_s + buf * kPBuf + row * 128 + 4 * l4;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = 8 * c + 2 * j;
-                    const float e0 = valid ? fast_exp2(y[i]) : 0.f, e1 = valid ? fast_exp2(y[i + 1]) : 0.f;
-                    l_thr[i] += e0;
-                    l_thr[i + 1] += e1;
-                    pk[j] = pack_f16x2(e0, e1);
-                }
-                *reinterpret_cast<uint4*>(prow + (((2 * set + c) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int g = 0; g < 4; ++g) {
+                const float a0 = v0 ? fast_exp2(y[4 * g]) : 0.f, a1 = v0 ? fast_exp2(y[4 * g + 1]) : 0.f;
+                const float b0 = v1 ? fast_exp2(y[4 * g + 2]) : 0.f, b1 = v1 ? fast_exp2(y[4 * g + 3]) : 0.f;
+                l_thr[2 * g] += a0 + b0;
+                l_thr[2 * g + 1] += a1 + b1;
+                const int at = ((4 * set + g) ^ (row & 7)) << 4;
+                *reinterpret_cast<uint32_t*>(prow + at) = pack_f16x2(a0, a1);
+                *reinterpret_cast<uint32_t*>(prow + 8 * 128 + at) = pack_f16x2(b0, b1);
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tl->p_full);
+            if (lane == 0) mbar_arrive(&tl->p_full[buf]);
         };
 
         // a segment's O^T and sums: the query's output when the segment holds all its tiles, else a partial
         // (slot >= 0: where)
         auto epilogue = [&](int q, int slot) {
-            mwait(&tl->pv[NM - 1], (n - 1) & 1u);
+            mwait(&tl->freed[(n - 1) & 1u][kHalves - 1], ((n - 1) >> 1) & 1u);
             tc_fence_after();
-            {
-                float v2[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v2[i] = l_thr[i];
-                warp_reduce_scatter_n<16, false>(v2);
-                if (!(lane & 1)) tl->lsum[set][qd][lane >> 1] = v2[0];
+            for (int i = 0; i < 8; ++i) {
+                float v = l_thr[i];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(kWarpFull, v, o);
+                if (lane < 4) tl->lsum[set][qd][8 * (i >> 1) + 2 * lane + (i & 1)] = v;
             }
             named_bar_sync(bar_set, 128);
-            const float* ls = &tl->lsum[set][0][lane >> 1];
-            const float lt = (ls[0] + ls[16]) + (ls[32] + ls[48]);
-            const int hh = 16 * set + (lane >> 1);
+            const float* ls = &tl->lsum[set][0][lane];
+            const float lt = (ls[0] + ls[32]) + (ls[64] + ls[96]);
+            const int hh = 32 * set + lane;
+            float inv = 0.f, wp = 0.f;
             if (slot >= 0) {
-                if (qd == 0 && !(lane & 1)) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
-                float* po = p.part_o + ((int64_t)slot * p.h + 16 * set) * p.d;
+                if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
+            } else if (hh < p.h) {
+                // everything relative to the largest of the running maximum, the sink and prev_lse
+                const float sk = p.sink ? __ldg(p.sink + hh) * kLog2e : -INFINITY;
+                const float pl = p.prev_lse ? __ldg(p.prev_lse + (int64_t)q * p.h + hh) * kLog2e : -INFINITY;
+                float mx = fmaxf(m_run, fmaxf(sk, pl));
+                if (mx == -INFINITY) mx = 0.f;
+                const float f = m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);
+                const float ep = exp2f(pl - mx);
+                const float den = lt * f + exp2f(sk - mx) + ep;
+                inv = f / den;
+                wp = ep / den;
+                if (p.lse && qd == 0) p.lse[(int64_t)q * p.h + hh] = (mx + log2f(den)) * kLn2;
+            }
+            uint16_t* stg = reinterpret_cast<uint16_t*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
+            const bool odd = (lane & 1) != 0;
+            // 16 heads x 32 dims of this warp at a time: k / 2 the d-block, heads 32 set + 16 (k & 1) ...
+            // Pieces of 8 dims, two per lane: piece c = lane + 32 j is head c / 4, dims 8 (c % 4) ...
+            auto piece = [&](int k, int j, int64_t& at) {
+                const int c = lane + 32 * j;
+                const int hw = 32 * set + 16 * (k & 1) + (c >> 2), dw = 128 * (k >> 1) + 32 * qd + 8 * (c & 3);
+                at = ((int64_t)q * p.h + hw) * p.d + dw;
+                return k < 2 * NM && hw < p.h && dw < p.d;
+            };
+            const bool joins = p.prev_out != nullptr && slot < 0;
+            uint4 pre[2];   // prev_out of the step, loaded a step ahead
+            auto load_prev = [&](int k) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    int64_t at;
+                    pre[j] = make_uint4(0, 0, 0, 0);
+                    if (piece(k, j, at)) pre[j] = *reinterpret_cast<const uint4*>(p.prev_out + at);
+                }
+            };
+            if (joins) load_prev(0);
 #pragma unroll 1
-                for (int m = 0; m < NM; ++m) {
-                    const int dd = 128 * m + 32 * qd + lane;
-                    uint32_t r[16];
-                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 16u * (uint32_t)set, r);
-                    tmem_ld_wait();
+            for (int k = 0; k < 2 * NM; ++k) {
+                const int m = k >> 1, h0 = 16 * (k & 1);
+                const int dd = 128 * m + 32 * qd + lane;
+                uint32_t r[16];
+                tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set + (uint32_t)h0, r);
+                tmem_ld_wait();
+                if (slot >= 0) {
+                    float* po = p.part_o + ((int64_t)slot * p.h + 32 * set + h0) * p.d + dd;
                     if (dd < p.d) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (16 * set + i < p.h) po[i * p.d + dd] = __uint_as_float(r[i]);
+                            if (32 * set + h0 + i < p.h) po[i * p.d] = __uint_as_float(r[i]);
                     }
+                    continue;
                 }
-            } else {
-                float inv = 0.f, wp = 0.f;
-                if (hh < p.h) {
-                    // everything relative to the largest of the running maximum, the sink and prev_lse
-                    const float sk = p.sink ? __ldg(p.sink + hh) * kLog2e : -INFINITY;
-                    const float pl = p.prev_lse ? __ldg(p.prev_lse + (int64_t)q * p.h + hh) * kLog2e : -INFINITY;
-                    float mx = fmaxf(m_run, fmaxf(sk, pl));
-                    if (mx == -INFINITY) mx = 0.f;
-                    const float f = m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);
-                    const float ep = exp2f(pl - mx);
-                    const float den = lt * f + exp2f(sk - mx) + ep;
-                    inv = f / den;
-                    wp = ep / den;
-                    if (p.lse && qd == 0 && !(lane & 1)) p.lse[(int64_t)q * p.h + hh] = (mx + log2f(den)) * kLn2;
-                }
-                uint16_t* orow = p.out + (int64_t)q * p.h * p.d;
-                uint16_t* stg = reinterpret_cast<uint16_t*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
-                const bool odd = (lane & 1) != 0;
-#pragma unroll 1
-                for (int m = 0; m < NM; ++m) {
-                    const int dd = 128 * m + 32 * qd + lane;
-                    uint32_t r[16];
-                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 16u * (uint32_t)set, r);
-                    tmem_ld_wait();
-                    float vv[16];
+                float vv[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) vv[i] = dead ? 0.f : __uint_as_float(r[i]) * __shfl_sync(kWarpFull, inv, 2 * i);
-                    if (p.prev_out) {
-                        const uint16_t* pr = p.prev_out + ((int64_t)q * p.h + 16 * set) * p.d + dd;
-                        uint16_t pv[16];
+                for (int i = 0; i < 16; ++i) vv[i] = dead ? 0.f : __uint_as_float(r[i]) * __shfl_sync(kWarpFull, inv, h0 + i);
+                if (joins) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) pv[i] = 16 * set + i < p.h && dd < p.d ? pr[i * p.d] : (uint16_t)0;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float w = __shfl_sync(kWarpFull, wp, 2 * i);
-                            vv[i] = w != 0.f ? vv[i] + w * bf16_f(pv[i]) : vv[i];   // weight 0: prev_out is not used
-                        }
-                    }
-                    // lane pairs write 4 bytes: the even lane head i, the odd lane head i + 1
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float send = odd ? vv[i] : vv[i + 1];
-                        const float recv = __shfl_xor_sync(kWarpFull, send, 1);
-                        const uint32_t pk = odd ? pack_bf16x2(recv, vv[i + 1]) : pack_bf16x2(vv[i], recv);
-                        *reinterpret_cast<uint32_t*>(stg + (i + (odd ? 1 : 0)) * 32 + (lane & ~1)) = pk;
-                    }
+                    for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(stg + (lane + 32 * j) * 8) = pre[j];
+                    load_prev(k + 1);
                     __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int c = lane + 32 * k;
-                        const int hw = 16 * set + (c >> 2);
-                        const int dw = 128 * m + 32 * qd + 8 * (c & 3);
-                        if (hw < p.h && dw < p.d)
-                            *reinterpret_cast<uint4*>(orow + (int64_t)hw * p.d + dw) =
-                                *reinterpret_cast<const uint4*>(stg + c * 8);
+                    for (int i = 0; i < 16; ++i) {
+                        const float w = __shfl_sync(kWarpFull, wp, h0 + i);
+                        const float pv = bf16_f(stg[i * 32 + lane]);
+                        vv[i] = w != 0.f ? vv[i] + w * pv : vv[i];   // weight 0: prev_out is not used
                     }
                     __syncwarp();
                 }
+                // lane pairs write 4 bytes: the even lane head i, the odd lane head i + 1
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float send = odd ? vv[i] : vv[i + 1];
+                    const float recv = __shfl_xor_sync(kWarpFull, send, 1);
+                    const uint32_t pk = odd ? pack_bf16x2(recv, vv[i + 1]) : pack_bf16x2(vv[i], recv);
+                    *reinterpret_cast<uint32_t*>(stg + (i + (odd ? 1 : 0)) * 32 + (lane & ~1)) = pk;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    int64_t at;
+                    if (piece(k, j, at))
+                        *reinterpret_cast<uint4*>(p.out + at) = *reinterpret_cast<const uint4*>(stg + (lane + 32 * j) * 8);
+                }
+                __syncwarp();
             }
         };
 
         Walk walk(wk);
-        Seg cur;
-        Codes codes;
-        bool more = walk.next(p, cur), first = true;
-        int t = cur.t0;
+        Seg sg;
         int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
-        if (more) load_units<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
-        while (more) {
-            if (first) {
-                // the Q buffer is free: this warp has seen the last S^T of the previous query (a warp whose
-                // head group is empty writes no Q)
-                load_q<NM>(p, cur.q, q_s, tl->qc);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tl->q_full);
+        while (walk.next(p, sg)) {
+            // the Q buffer is free: this warp has seen the last S^T of the previous query (a warp whose head
+            // group is empty writes no Q)
+            load_q<NM>(p, sg.q, q_s, tl->qc);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tl->q_full);
+            if (tid == 0) {   // what the next segment and this one's end will read, into L2
+                const uint32_t bytes = (uint32_t)(p.h * p.d * 2);
+                if (sg.q + 1 < nq) prefetch_l2_bulk(p.q + (int64_t)(sg.q + 1) * p.h * p.d, bytes);
+                if (p.prev_out) prefetch_l2_bulk(p.prev_out + (int64_t)sg.q * p.h * p.d, bytes);
             }
-            const int row0 = t * kRows, vis = cur.vis;
-            const bool valid = row0 + row < vis, begins = first;
-            const int old_q = pend_q, old_slot = pend_slot;
-            first = ++t == cur.t1;
-            if (first) {
-                pend_q = cur.q;
-                pend_slot = cur.t0 == 0 && cur.t1 == cur.nt ? -1 : 2 * (int)blockIdx.x + (cur.t0 == 0 ? 1 : 0);
-                more = walk.next(p, cur);
-                t = cur.t0;
-            }
-            decode_units<NM>(
-                t_s, row0, vis, n_cb, codes, tl->full,
-                [&](int m) {
-                    if (n > 0) mwait(&tl->pv[m], (n - 1) & 1u);
-                    return !dead;
-                });
-            if (more) load_units<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
-            if (begins) {
-                if (old_q >= 0 && active) epilogue(old_q, old_slot);
-                named_bar_sync(kBarMath, kMath);   // the staging area is every warp's P^T buffer; qc is complete
-                m_run = -INFINITY;
-                if (lane < 16) tl->cm[set][qd][lane] = make_float2(tl->qc[16 * set + lane], 0.f);
-                __syncwarp();
+            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot);
+            named_bar_sync(kBarSoft, 256);     // the staging area is every warp's P^T; qc is complete
+            m_run = -INFINITY;
+            tl->cm[set][qd][lane] = make_float2(tl->qc[32 * set + lane], 0.f);
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) l_thr[i] = 0.f;
-            }
-            if (active) softmax(valid, begins);
-            ++n;
+            for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
+            for (int t = sg.t0; t < sg.t1; ++t, ++n)
+                if (active) softmax(sg.vis - t * kRows - row, t == sg.t0);
+            pend_q = sg.q;
+            pend_slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
         }
         if (pend_q >= 0 && active) epilogue(pend_q, pend_slot);
 
         // queries without a visible row
         for (int q = blockIdx.x; q < nq; q += gridDim.x) {
             if (visible_rows(p, q / p.s, q % p.s) > 0) continue;
-            for (int hh = warp; hh < p.h; hh += 16) {
+            for (int hh = warp; hh < p.h; hh += 8) {
                 const int64_t at = (int64_t)q * p.h + hh;
                 const float pl = p.prev_lse ? p.prev_lse[at] : -INFINITY;
                 if (p.lse && lane == 0) p.lse[at] = pl;
@@ -899,13 +948,13 @@ __global__ void __launch_bounds__(128 * G) merge_kernel(const AttnFp4Params p) {
 // ------------------------------------------------------------------ row weights
 
 struct __align__(16) WTail {
-    float2 cl[3][64];                // [query % 3] per head: (softmax scale over the f16 scaling, -lse in log2)
+    float2 cl[2][64];                // [query parity] per head: (softmax scale over the f16 scaling, -lse in log2)
     float qc[64];
-    float acc[kWTiles][4][kRows];    // [tile of the chunk][head group][row]
+    float acc[kWTiles][2][kRows];    // [tile of the chunk][head group][row]
     Work work;
     long long scratch[kThreads / 32];
-    uint64_t full[4];
-    uint64_t freed[4];               // the tile's QK has read d-block m
+    uint64_t full[2][2];
+    uint64_t freed[2][2];            // the QK has read it
     uint64_t s_full[2];              // [tile parity] S^T done
     uint64_t s_free[2];              // S^T read
     uint64_t q_full;
@@ -915,7 +964,7 @@ struct __align__(16) WTail {
 
 size_t row_weight_smem(int d) {
     const int n_cb = (d + 127) / 128 * 2;
-    return 1024 + (size_t)n_cb * (kQBlk + kTBlk) + sizeof(WTail);
+    return 1024 + (size_t)n_cb * (kQBlk + 2 * kTBlk) + sizeof(WTail);
 }
 
 // One CTA's work: its piece of the sequences' tiles in chunks of at most kWTiles tiles of one sequence; per
@@ -959,15 +1008,17 @@ struct WWalk {
 
 template <int NM>
 __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Params p) {
+    constexpr int kHalves = (NM + 1) / 2;
+    constexpr uint32_t kTile = 2 * NM * kTBlk;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;
     uint8_t* q_s = smem;
     uint8_t* t_s = q_s + 2 * NM * kQBlk;
-    WTail* tl = reinterpret_cast<WTail*>(t_s + 2 * NM * kTBlk);
+    WTail* tl = reinterpret_cast<WTail*>(t_s + 2 * kTile);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = (p.h + 15) / 16;
+    const int groups = p.h > 32 ? 2 : 1;
     volatile int* abort = &tl->abort;
     // this CTA's queries of every sequence, and its piece of the tiles
     const int split = (int)blockIdx.x % p.w_split;
@@ -978,23 +1029,19 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         tmem_relinquish();
     }
     if (tid == 0) {
-        for (int m = 0; m < 4; ++m) {
-            mbar_init(&tl->full[m], 8);
-            mbar_init(&tl->freed[m], 1);
-        }
         for (int k = 0; k < 2; ++k) {
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&tl->full[k][h], 8);
+                mbar_init(&tl->freed[k][h], 1);
+            }
             mbar_init(&tl->s_full[k], 1);
             mbar_init(&tl->s_free[k], 4 * groups);
         }
-        mbar_init(&tl->q_full, 16);
+        mbar_init(&tl->q_full, 8);
         tl->abort = 0;
         fence_mbar_init();
     }
-    for (int i = tid; i < 2 * NM * 64 * 8; i += kThreads)
-        if (((i >> 3) & 63) >= p.h || (i >> 9) >= n_cb) reinterpret_cast<uint4*>(q_s)[i] = make_uint4(0, 0, 0, 0);
-    if (n_cb & 1)
-        for (int i = tid; i < (int)kTBlk / 16; i += kThreads)
-            reinterpret_cast<uint4*>(t_s + (size_t)n_cb * kTBlk)[i] = make_uint4(0, 0, 0, 0);
+    zero_padding(p.h, n_cb, NM, q_s, t_s);
     fence_proxy_async_smem();
     plan_work(p.B, (int)blockIdx.x / p.w_split, (int)gridDim.x / p.w_split, tl->scratch, &tl->work,
               [&](int b) { return (visible_rows(p, b, p.s - 1) + kRows - 1) / kRows; });
@@ -1007,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
 
     if (warp >= 16) {
         regs_down<kRegsMma>();
-        const uint32_t idesc_qk = idesc_f16_f32(kRows, 16 * groups, false, false);
+        const uint32_t idesc_qk = idesc_f16_f32(kRows, (p.h + 15) / 16 * 16, false, false);
         const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
         uint32_t n = 0, qn = 0;
         int have = -1;
@@ -1025,16 +1072,17 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                     have = w.seq * p.s + w.q;
                 }
                 for (int k = w.k; k < w.end && ok; ++k, ++n) {
-                    const uint32_t st = n & 1u;
-                    if (n >= 2 && !wait(&tl->s_free[st], ((n >> 1) - 1) & 1u)) break;
+                    const uint32_t buf = n & 1u;
+                    if (n >= 2 && !wait(&tl->s_free[buf], ((n >> 1) - 1) & 1u)) break;
 #pragma unroll
-                    for (int m = 0; m < NM; ++m) {
-                        if (!wait(&tl->full[m], n & 1u)) break;
+                    for (int h = 0; h < kHalves; ++h) {
+                        if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
                         if (elect_one()) {
-                            qk_blocks(m == 0, tmem + 64u * st, lo32(dk) + (uint32_t)m * (2 * kTBlk / 16),
-                                      lo32(dq) + (uint32_t)m * (2 * kQBlk / 16), hi32(dk), idesc_qk);
-                            umma_commit(&tl->freed[m]);
-                            if (m == NM - 1) umma_commit(&tl->s_full[st]);
+#pragma unroll
+                            for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
+                                qk_blocks(m, tmem + 64u * buf, lo32(dk) + buf * (kTile / 16), lo32(dq), hi32(dk), idesc_qk);
+                            umma_commit(&tl->freed[buf][h]);
+                            if (h == kHalves - 1) umma_commit(&tl->s_full[buf]);
                         }
                         __syncwarp();
                     }
@@ -1042,99 +1090,108 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
             }
         }
         __syncwarp();
-    } else {
-        regs_up<kRegsMath>();
-        const int set = warp >> 2, qd = warp & 3;
-        const int row = 32 * qd + lane;
-        const bool active = set < groups;
-        const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
+    } else if (warp >= 8) {
+        regs_down<kRegsDecode>();
         uint32_t n = 0;
-        int have = -1, qn = 0;               // qn: queries loaded
         bool dead = false;
-        auto mwait = [&](uint64_t* bar, uint32_t parity) {
-            if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
-        };
-        // a tile's scores -> this row's probabilities, summed over the group's heads into acc
-        auto weigh = [&](uint32_t nn, int q, int vis, int k, int slot) {
-            const uint32_t st = nn & 1u;
-            mwait(&tl->s_full[st], (nn >> 1) & 1u);
-            tc_fence_after();
-            uint32_t r[16];
-            tmem_ld16(tmem + lane_base + 64u * st + 16u * (uint32_t)set, r);
-            tmem_ld_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tl->s_free[st]);
-            if (k * kRows + row < vis && !dead) {
-                float sum = 0.f;
-                const int hn = p.h - 16 * set;   // heads of the group
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float4 v = *reinterpret_cast<const float4*>(&tl->cl[q][16 * set + 2 * c]);
-                    const float e0 = fast_exp2(fmaf(__uint_as_float(r[2 * c]), v.x, v.y));
-                    const float e1 = fast_exp2(fmaf(__uint_as_float(r[2 * c + 1]), v.z, v.w));
-                    if (2 * c < hn) sum += e0;
-                    if (2 * c + 1 < hn) sum += e1;
-                }
-                tl->acc[slot][set][row] += sum;
-            }
-        };
-        Codes codes;
-        while (w.chunk(p)) {
-            for (int k = 0; k < w.t1 - w.t0; ++k) tl->acc[k][set][row] = 0.f;
-            // the tiles of the chunk's queries in turn; a tile is weighed after the next one has been decoded,
-            // while its QK runs
-            int l_q = -1, l_vis = 0, l_k = 0;     // the tile to be weighed (l_q < 0: none)
+        Codes<NM> codes;
+        while (!dead && w.chunk(p)) {
             w.q = ta;
             bool more = w.query(p);
-            if (more) load_units<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
-            while (more) {
-                const int qi = w.seq * p.s + w.q, k = w.k, vis = visible_rows(p, w.seq, w.q);
-                if (have != qi) {
-                    // the Q buffer is free once the last QK has read the last d-block
-                    if (n > 0) mwait(&tl->freed[NM - 1], (n - 1) & 1u);
-                    load_q<NM>(p, qi, q_s, tl->qc);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tl->q_full);
-                    qn = qn == 2 ? 0 : qn + 1;
-                    if (lane < 4) {   // the warp's own four heads
-                        const int hd = 4 * warp + lane;
-                        tl->cl[qn][hd] =
-                            make_float2(tl->qc[hd], hd < p.h ? -__ldcg(p.lse + (int64_t)qi * p.h + hd) * kLog2e : 0.f);
-                    }
-                    named_bar_sync(kBarMath, kMath);
-                    have = qi;
-                }
+            if (more) load_codes<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
+            while (more && !dead) {
+                const uint32_t buf = n & 1u;
+                dead = !decode_tile<NM>(t_s + buf * kTile, w.k * kRows, w.vis_all, n_cb, codes, tl->full[buf], [&](int h) {
+                    return n < 2 || warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort);
+                });
+                ++n;
                 if (++w.k == w.end) {
                     ++w.q;
                     more = w.query(p);
                 }
-                decode_units<NM>(
-                    t_s, k * kRows, w.vis_all, n_cb, codes, tl->full,
-                    [&](int m) {
-                        if (n > 0) mwait(&tl->freed[m], (n - 1) & 1u);
-                        return !dead;
-                    });
-                if (more) load_units<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
-                if (active && l_q >= 0) weigh(n - 1, l_q, l_vis, l_k, l_k - w.t0);
-                l_q = qn;
-                l_vis = vis;
-                l_k = k;
-                ++n;
+                if (more) load_codes<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
             }
-            if (active && l_q >= 0) weigh(n - 1, l_q, l_vis, l_k, l_k - w.t0);
-            named_bar_sync(kBarMath, kMath);
-            for (int i = tid; i < (w.t1 - w.t0) * kRows; i += kMath) {
+        }
+    } else {
+        regs_up<kRegsSoft>();
+        const int set = warp >> 2, qd = warp & 3;
+        const int row = 16 * qd + (lane >> 2), l4 = lane & 3;
+        const bool active = set < groups;
+        const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
+        uint32_t n = 0, qn = 0;
+        int have = -1;
+        bool dead = false;
+        while (w.chunk(p)) {
+            for (int i = tid; i < (w.t1 - w.t0) * 2 * kRows; i += 256) (&tl->acc[0][0][0])[i] = 0.f;
+            named_bar_sync(kBarSoft, 256);
+            for (w.q = ta; w.query(p); ++w.q) {
+                const int qi = w.seq * p.s + w.q, vis = visible_rows(p, w.seq, w.q);
+                if (have != qi) {
+                    // the Q buffer is free: this warp has seen the previous query's last S^T
+                    qn ^= 1u;
+                    load_q<NM>(p, qi, q_s, tl->qc);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tl->q_full);
+                    if (lane < 8) {   // the warp's own eight heads
+                        const int hd = 8 * warp + lane;
+                        tl->cl[qn][hd] =
+                            make_float2(tl->qc[hd], hd < p.h ? -__ldcg(p.lse + (int64_t)qi * p.h + hd) * kLog2e : 0.f);
+                    }
+                    named_bar_sync(kBarSoft, 256);
+                    have = qi;
+                }
+                for (int k = w.k; k < w.end; ++k, ++n) {
+                    if (!active) continue;
+                    const uint32_t buf = n & 1u;
+                    if (!dead) dead = !warp_wait(&tl->s_full[buf], (n >> 1) & 1u, p.status, abort);
+                    tc_fence_after();
+                    uint32_t r[16];
+                    tmem_ld_rows16(tmem + lane_base + 64u * buf + 32u * (uint32_t)set, r);
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tl->s_free[buf]);
+                    // probabilities of the thread's two rows, summed over its heads, then over the four lanes of a row
+                    float a = 0.f, b = 0.f;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int hd = 32 * set + 8 * g + 2 * l4;
+                        const float4 v = *reinterpret_cast<const float4*>(&tl->cl[qn][hd]);
+                        const float a0 = fast_exp2(fmaf(__uint_as_float(r[4 * g]), v.x, v.y));
+                        const float a1 = fast_exp2(fmaf(__uint_as_float(r[4 * g + 1]), v.z, v.w));
+                        const float b0 = fast_exp2(fmaf(__uint_as_float(r[4 * g + 2]), v.x, v.y));
+                        const float b1 = fast_exp2(fmaf(__uint_as_float(r[4 * g + 3]), v.z, v.w));
+                        if (hd < p.h) {
+                            a += a0;
+                            b += b0;
+                        }
+                        if (hd + 1 < p.h) {
+                            a += a1;
+                            b += b1;
+                        }
+                    }
+#pragma unroll
+                    for (int o = 1; o <= 2; o <<= 1) {
+                        a += __shfl_xor_sync(kWarpFull, a, o);
+                        b += __shfl_xor_sync(kWarpFull, b, o);
+                    }
+                    if (l4 < 2 && !dead) {   // lane 0 of the four: the first row, lane 1: the second
+                        const int rr = row + 8 * l4;
+                        if (k * kRows + rr < vis) tl->acc[k - w.t0][set][rr] += l4 ? b : a;
+                    }
+                }
+            }
+            named_bar_sync(kBarSoft, 256);
+            for (int i = tid; i < (w.t1 - w.t0) * kRows; i += 256) {
                 const int j = w.t0 * kRows + i;
                 if (j < w.vis_all) {
-                    const float* a = &tl->acc[i >> 7][0][i & 127];
-                    const float v = (a[0] + a[kRows]) + (a[2 * kRows] + a[3 * kRows]);
+                    const float v = tl->acc[i / kRows][0][i % kRows] + tl->acc[i / kRows][1][i % kRows];
                     if (p.w_split > 1) p.w_part[((int64_t)split * p.B + w.seq) * p.n_rows + j] = v;
                     else p.row_weight[(int64_t)w.seq * p.row_weight_bstride + j] += v;
                 }
             }
-            named_bar_sync(kBarMath, kMath);
+            named_bar_sync(kBarSoft, 256);
         }
     }
 
