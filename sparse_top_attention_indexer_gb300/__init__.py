@@ -479,7 +479,7 @@ def _on(device, stream):
 
 def _elsewhere(device, stream) -> bool:
     """Whether a call has to change the current device or stream first."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or device.index != torch._C._cuda_getDevice()
 
 
 def _call_workspace(nbytes: int, device) -> torch.Tensor:
@@ -493,12 +493,8 @@ def _dense(t, dtype, shape, device, name):
     """Check a contiguous tensor of a given type, shape and device; its pointer (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device.index or not t.is_contiguous():
+        raise _mismatch(t, dtype, f"contiguous with shape {list(shape)}", device, name)
     return t.data_ptr()
 
 
@@ -507,16 +503,21 @@ def _rows(t, dtype, b, n_rows, inner, device, name):
     sequences; its pointer and that stride in elements (a single sequence's may be anything: its size)."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     shape, stride = t.shape, t.stride()
-    if (len(shape) != (3 if inner else 2) or shape[0] != b or shape[1] < n_rows or (inner and shape[2] != inner) or
+    if (t.dtype is not dtype or t.get_device() != device.index or len(shape) != (3 if inner else 2) or shape[0] != b or
+            shape[1] < n_rows or (inner and shape[2] != inner) or
             (n_rows > 0 and b > 0 and (stride[-1] != 1 or (inner and shape[1] > 1 and stride[1] != inner)))):
-        raise ValueError(f"{name} must be [{b}, at least {n_rows} rows{', ' + str(inner) if inner else ''}] with "
-                         f"contiguous rows, got {list(shape)} with strides {list(stride)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+        raise _mismatch(t, dtype, f"[{b}, at least {n_rows} rows{', ' + str(inner) if inner else ''}] with contiguous rows",
+                        device, name)
     return t.data_ptr(), stride[0] if b > 1 else shape[1] * (inner or 1)
+
+
+def _mismatch(t, dtype, form, device, name):
+    if t.dtype is not dtype:
+        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        return ValueError(f"{name} must be on {device}, got {t.device}")
+    return ValueError(f"{name} must be {form}, got {list(t.shape)} with strides {list(t.stride())}")
 
 
 def _workspace_ptr(ws, device):
