@@ -162,7 +162,9 @@ __device__ __forceinline__ bool elect_one() {
 // ------------------------------------------------------------------ the list of tiles
 
 __device__ __forceinline__ int visible_rows(const AttnFp4Params& p, int b, int t) {
-    const int64_t v = ((int64_t)__ldg(p.start_pos + b) + t + 1) / p.ratio - (p.dropped ? __ldg(p.dropped + b) : 0);
+    // start_pos >= 0 and t < 2^30: the sum fits 32 unsigned bits (a 64-bit division takes some hundred cycles)
+    const uint32_t groups = ((uint32_t)__ldg(p.start_pos + b) + (uint32_t)t + 1u) / (uint32_t)p.ratio;
+    const int64_t v = (int64_t)groups - (p.dropped ? __ldg(p.dropped + b) : 0);
     return v < 0 ? 0 : v > p.n_rows ? p.n_rows : (int)v;
 }
 
@@ -298,17 +300,20 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s2) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// 32 elements of a tile row (half of one column block; `dst` the row's 128 bytes) from their codes and two
-// scales; zeros when the row is not visible.
-__device__ __forceinline__ void decode_half(uint8_t* dst, int row, int half, bool valid, const uint4& c, uint32_t s) {
+// 32 elements of a tile row from their codes and two scales; zeros when the row is not visible.  `dst`: the row's
+// 128 bytes in the column block ch / 2 of the d-block, of which they are half ch % 2.  The upper two quarters
+// store their 16-byte pieces in the order 2, 3, 0, 1: eight consecutive lanes (two rows, four quarters) then
+// write eight different positions of the swizzled rows; in the same order they would meet on four.
+__device__ __forceinline__ void decode_quarter(uint8_t* dst, int row, int ch, bool valid, const uint4& c, uint32_t s) {
     uint32_t h = 0u;   // the scales as f16
     if (valid)
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(s));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    const uint32_t sc[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
+    const bool turn = (ch & 2) != 0;
+    const uint32_t w[4] = {turn ? c.z : c.x, turn ? c.w : c.y, turn ? c.x : c.z, turn ? c.y : c.w};
+    const uint32_t sc[2] = {__byte_perm(h, h, turn ? 0x3232 : 0x1010), __byte_perm(h, h, turn ? 0x1010 : 0x3232)};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(dst + (((4 * half + i) ^ (row & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(dst + (((4 * (ch & 1) + (i ^ (ch & 2))) ^ (row & 7)) << 4)) =
             valid ? decode8(w[i], *reinterpret_cast<const __half2*>(&sc[i >> 1])) : make_uint4(0, 0, 0, 0);
 }
 
@@ -325,7 +330,7 @@ __device__ __forceinline__ bool decode_tile(uint8_t* t_s, int row0, int vis, int
 #pragma unroll
         for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m) {
             const int cb = 2 * m + (ch >> 1);
-            if (cb < n_cb) decode_half(t_s + (size_t)cb * kTBlk + row * 128, row, ch & 1, row0 + row < vis, r.c[m], r.s[m]);
+            if (cb < n_cb) decode_quarter(t_s + (size_t)cb * kTBlk + row * 128, row, ch, row0 + row < vis, r.c[m], r.s[m]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -832,28 +837,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
 // ------------------------------------------------------------------ joining split queries
 
 // Block (x, head): the split queries that start in CTAs x, x + gridDim.x, ... of the attention kernel.
-// Thread (g, i), g < G, takes dims 4i .. 4i + 3 of every G-th part, four of them in flight; the groups' sums
-// join in shared memory in a fixed order.  G follows from the parts a query can have: one long query (152
-// parts of 2 KB per head) has too few loads in flight with G = 1 (44 us against 12), thousands of short ones
-// (two parts each) would spend their time starting wide blocks (18 us with G = 1, 190 with 8).
-template <int G>
-__global__ void __launch_bounds__(128 * G) merge_kernel(const AttnFp4Params p) {
+// Block (x, head, z) takes dims 4 W z .. 4 W (z + 1) - 1; thread (g, i), g < G, dims 4 (W z + i) + {0..3} of every
+// G-th part, four parts in flight; the groups' sums join in shared memory in a fixed order.  G follows from the
+// parts a query can have: a single long query (152 parts) needs many loads in flight (20 us with G = 8, W = 128),
+// thousands of short ones (two parts each) would spend their time starting wide blocks.
+template <int G, int W>
+__global__ void __launch_bounds__(G * W) merge_kernel(const AttnFp4Params p) {
     __shared__ float fac[256];
     __shared__ float stat[2];
-    __shared__ float4 part[G][128];
+    __shared__ float4 part[G][W];
     const int hh = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    const int g = tid >> 7, i4 = tid & 127;
-    __shared__ int2 recs[160];
+    const int g = tid / W, ti = tid % W, i4 = (int)blockIdx.z * W + ti;
+    __shared__ int3 recs[160];   // (query, first CTA, last CTA) of the block's split queries
+    __shared__ int n_recs;
     griddep_wait();
     griddep_launch_dependents();
-    // all of the block's records at once: one after another, a single query's 152 took 50 us
-    for (int k = tid; blockIdx.x + k * gridDim.x < p.grid; k += 128 * G) recs[k] = __ldcg(p.rec + blockIdx.x + k * gridDim.x);
+    // one warp reads all of the block's records at once and keeps the real ones (read one after another, and
+    // looked through by every warp, a single query's 152 took 50 and 13 us)
+    if (tid < 32) {
+        int2 r[5];
+        int cnt = 0;
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            const int c = (int)blockIdx.x + (lane + 32 * k) * (int)gridDim.x;
+            r[k] = c < p.grid ? __ldcg(p.rec + c) : make_int2(-1, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 5; ++k) {
+            const uint32_t real = __ballot_sync(kWarpFull, r[k].x >= 0);
+            if (r[k].x >= 0)
+                recs[cnt + __popc(real & ((1u << lane) - 1u))] =
+                    make_int3(r[k].x, (int)blockIdx.x + (lane + 32 * k) * (int)gridDim.x, r[k].y);
+            cnt += __popc(real);
+        }
+        if (lane == 0) n_recs = cnt;
+    }
     __syncthreads();
-    for (int k0 = 0; blockIdx.x + k0 * gridDim.x < p.grid; ++k0) {
-        const int2 rec = recs[k0];
-        if (rec.x < 0) continue;
-        const int c = blockIdx.x + k0 * gridDim.x;
-        const int parts = rec.y - c + 1;   // slots 2c + 1, 2 (c + 1), 2 (c + 2), ...
+    for (int k0 = 0; k0 < n_recs; ++k0) {
+        const int3 rec = recs[k0];
+        const int c = rec.y;
+        const int parts = rec.z - c + 1;   // slots 2c + 1, 2 (c + 1), 2 (c + 2), ...
         auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
         const int64_t at = (int64_t)rec.x * p.h + hh;
         // the partial outputs start loading before their factors are known
@@ -893,7 +916,7 @@ __global__ void __launch_bounds__(128 * G) merge_kernel(const AttnFp4Params p) {
             if (lane == 0) {
                 stat[0] = 1.f / den;
                 stat[1] = ep / den;
-                if (p.lse) p.lse[at] = (mx + log2f(den)) * kLn2;
+                if (p.lse && blockIdx.z == 0) p.lse[at] = (mx + log2f(den)) * kLn2;
             }
         }
         __syncthreads();
@@ -915,12 +938,12 @@ __global__ void __launch_bounds__(128 * G) merge_kernel(const AttnFp4Params p) {
                 v[k] = w[k];
             }
         }
-        part[g][i4] = o;
+        part[g][ti] = o;
         __syncthreads();
         if (g == 0 && in) {
 #pragma unroll
             for (int k = 1; k < G; ++k) {
-                const float4 q = part[k][i4];
+                const float4 q = part[k][ti];
                 o.x += q.x;
                 o.y += q.y;
                 o.z += q.z;
@@ -1261,10 +1284,10 @@ cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
     attn_fp4_kernel<NM><<<p.grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
-    const dim3 mg((unsigned)(nq < p.grid ? nq : p.grid), (unsigned)p.h);
-    e = parts > 16  ? launch_after(merge_kernel<8>, mg, 1024, 0, p, stream)
-        : parts > 4 ? launch_after(merge_kernel<2>, mg, 256, 0, p, stream)
-                    : launch_after(merge_kernel<1>, mg, 128, 0, p, stream);
+    const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)p.h;
+    e = parts > 16  ? launch_after(merge_kernel<16, 32>, dim3(mx, mh, (unsigned)NM), 512, 0, p, stream)
+        : parts > 4 ? launch_after(merge_kernel<2, 128>, dim3(mx, mh), 256, 0, p, stream)
+                    : launch_after(merge_kernel<1, 128>, dim3(mx, mh), 128, 0, p, stream);
     if (e != cudaSuccess || !p.row_weight || p.n_rows == 0) return e;
     smem = row_weight_smem(p.d);
     e = cudaFuncSetAttribute(row_weight_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
