@@ -53,7 +53,7 @@ constexpr uint32_t kPBuf = kRows * 128;        // a P^T buffer: 64 rows x 64 hea
 constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at columns [64 b, 64 b + 64), O^T d-block
                                                // m at [128 + 64 m, 192 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kWTiles = 56;                    // row weights: tiles per chunk (accumulators in shared memory)
+constexpr int kWTiles = 32;                    // row weights: tiles per chunk (accumulators in shared memory)
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 // instruction descriptor, kind::f16 with f16 A/B (format 0) and fp32 accumulator
@@ -275,7 +275,10 @@ __device__ __forceinline__ void load_codes(const AttnFp4Params& p, int b, int ro
 #pragma unroll
     for (int m = 0; m < NM; ++m) {
         if (2 * m + (ch >> 1) < n_cb) {
-            r.c[m] = __ldg(reinterpret_cast<const uint4*>(cr + 64 * m));
+            // codes are read once: not kept in L1, whose fill the loads would wait for
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(r.c[m].x), "=r"(r.c[m].y), "=r"(r.c[m].z), "=r"(r.c[m].w)
+                         : "l"(cr + 64 * m));
             r.s[m] = __ldg(reinterpret_cast<const uint16_t*>(sr + 8 * m));
         }
     }
@@ -577,14 +580,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
         };
 
-        // One tile's probabilities.  cm holds (c, -m) of each head: c the softmax scale (log2) over the head's f16
-        // scaling, m its running maximum, so y = S c - m is one FMA and 2^y the probability.
+        // One tile's probabilities.  cm holds (c, -m) of the thread's heads: c the softmax scale (log2) over the head's
+        // f16 scaling, m its running maximum, so y = S c - m is one FMA and 2^y the probability.
+        float2 cm[8];
+        auto load_cm = [&]() {   // from the warp's copy, which has every head of the group
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4 v = *reinterpret_cast<const float4*>(&tl->cm[set][qd][8 * g + 2 * l4]);
+                cm[2 * g] = make_float2(v.x, v.y);
+                cm[2 * g + 1] = make_float2(v.z, v.w);
+            }
+        };
         auto softmax = [&](int left, bool first) {   // left: visible rows from this thread's first one on
             const uint32_t buf = n & 1u;
             mwait(&tl->s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
             const bool v0 = left > 0 && !dead, v1 = left > 8 && !dead;
-            const float2* cm = &tl->cm[set][qd][0];
             const uint32_t ts = tmem + lane_base + 64u * buf + 32u * (uint32_t)set;
             uint32_t r[16];
             tmem_ld_rows16(ts, r);
@@ -593,13 +604,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             float top0 = -INFINITY, top1 = -INFINITY;
             auto scale = [&]() {
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float4 v = *reinterpret_cast<const float4*>(cm + 8 * g + 2 * l4);
-                    y[4 * g] = fmaf(__uint_as_float(r[4 * g]), v.x, v.y);
-                    y[4 * g + 1] = fmaf(__uint_as_float(r[4 * g + 1]), v.z, v.w);
-                    y[4 * g + 2] = fmaf(__uint_as_float(r[4 * g + 2]), v.x, v.y);
-                    y[4 * g + 3] = fmaf(__uint_as_float(r[4 * g + 3]), v.z, v.w);
-                }
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        y[4 * g + c] = fmaf(__uint_as_float(r[4 * g + c]), cm[2 * g + (c & 1)].x, cm[2 * g + (c & 1)].y);
             };
             scale();
 #pragma unroll
@@ -622,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                     }
                 named_bar_sync(bar_set, 128);
                 const float* rr = &tl->red[buf][set][0][lane];
-                const float old = -cm[lane].y;             // what y is relative to
+                float2* own = &tl->cm[set][qd][0];
+                const float old = -own[lane].y;            // what y is relative to
                 const float mt = fmaxf(fmaxf(rr[0], rr[32]), fmaxf(rr[64], rr[96])) + old;
                 const float m_new = (m_run == -INFINITY || mt > m_run + 8.f) ? fmaxf(m_run, mt) : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
@@ -630,8 +639,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 __syncwarp();
                 // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
                 // scores show in its output
-                tl->cm[set][qd][lane].y = m_new == -INFINITY ? 0.f : -m_new;
+                own[lane].y = m_new == -INFINITY ? 0.f : -m_new;
                 __syncwarp();
+                load_cm();
                 scale();
                 if (!first && !dead && __any_sync(kWarpFull, alpha != 1.f)) {
                     mwait(&tl->freed[buf ^ 1u][kHalves - 1], ((n - 1) >> 1) & 1u);   // the previous tile's PV is done
@@ -796,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             m_run = -INFINITY;
             tl->cm[set][qd][lane] = make_float2(tl->qc[32 * set + lane], 0.f);
             __syncwarp();
+            load_cm();
 #pragma unroll
             for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
             for (int t = sg.t0; t < sg.t1; ++t, ++n)
@@ -1267,8 +1278,12 @@ void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid
     const int64_t all = tiles * B;                                   // row tiles at most
     const int64_t list = all * s > 0 ? all * s : 1;
     *grid = (int)(list < num_sms ? list : num_sms);
-    int64_t split = all > 0 ? num_sms / all : 1;                     // CTAs per row tile
-    split = split < 1 ? 1 : split > s ? s : split;
+    // Row weights: loading a query costs as much as two of its tiles, so a CTA takes about kWTiles tiles of each and
+    // the CTAs that this leaves over take other queries (never fewer with more SMs: the workspace counts on it).
+    int64_t split = all > 0 ? num_sms * kWTiles / all : 1;
+    const int64_t most = s < num_sms ? s : num_sms;
+    split = split > most ? most : split < 1 ? 1 : split;
+    if (s > 0) split = (s + (s + split - 1) / split - 1) / ((s + split - 1) / split);   // same share with fewer CTAs
     *w_split = (int)split;
     const int64_t per = num_sms / split;
     *w_grid = (int)(split * (all < per ? (all > 0 ? all : 1) : per));
