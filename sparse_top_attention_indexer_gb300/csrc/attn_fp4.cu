@@ -53,6 +53,7 @@ constexpr uint32_t kPBuf = kRows * 128;        // a P^T buffer: 64 rows x 64 hea
 constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at columns [64 b, 64 b + 64), O^T d-block
                                                // m at [128 + 64 m, 192 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr int kAhead = 3;                      // tiles ahead
 constexpr int kWTiles = 32;                    // row weights: tiles per chunk (accumulators in shared memory)
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
@@ -284,6 +285,16 @@ __device__ __forceinline__ void load_codes(const AttnFp4Params& p, int b, int ro
     }
 }
 
+// Bring the codes and scales of rows [row0, row1) into L2 (one thread; whole 16-byte pieces of them).
+__device__ __forceinline__ void prefetch_rows(const AttnFp4Params& p, int b, int row0, int row1) {
+    if (row0 >= row1) return;
+    const uint32_t rows = (uint32_t)(row1 - row0);
+    prefetch_l2_bulk(p.codes + (int64_t)b * p.codes_bstride + (int64_t)row0 * (p.d / 2), rows * (uint32_t)(p.d / 2));
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(p.scales + (int64_t)b * p.scales_bstride + (int64_t)row0 * (p.d / 16));
+    const uintptr_t lo = (s0 + 15) & ~(uintptr_t)15, hi = (s0 + rows * (uint32_t)(p.d / 16)) & ~(uintptr_t)15;
+    if (lo < hi) prefetch_l2_bulk(reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo));
+}
+
 // Eight codes (nibble i = element i) times the scale pair s2 = (s, s), as eight f16.
 __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s2) {
     uint32_t o[4];
@@ -408,6 +419,7 @@ struct __align__(16) Tail {
     uint64_t q_full;
     uint32_t tmem_base;
     int abort;
+    int qk_tile;              // tiles whose QK was issued, for the prefetching warp
 };
 
 size_t attn_smem(int d) {
@@ -458,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         }
         mbar_init(&tl->q_full, 8);
         tl->abort = 0;
+        tl->qk_tile = 0;
         fence_mbar_init();
     }
     zero_padding(p.h, n_cb, NM, q_s, t_s);
@@ -474,70 +487,91 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
     if (warp >= 16) {
         regs_down<kRegsMma>();
         // -------------------------------------------------------------- MMA issue
+        // Warp 16 issues the QKs and warp 17 the PVs, each as its operands come: in one warp's order a PV waits for the
+        // next tile's QK, that for its decode, and the decode for the buffer of the PV before.
         const int n_mma = (p.h + 15) / 16 * 16;
-        const uint32_t idesc_qk = idesc_f16_f32(kRows, n_mma, false, false);
-        const uint32_t idesc_pv = idesc_f16_f32(128, n_mma, true, true);
-        // descriptors of the tile and Q (K-major), the tile (MN-major) and P^T (MN-major)
-        const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
-        const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128);
-        const uint64_t dp = sdesc(smem_u32(p_s), kPBuf, 1024, kLayoutSW128);
-        uint32_t n = 0, qn = 0;
-        // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
-        bool ok = warp == 16, starts = false;   // starts: tile n - 1 is its segment's first
+        uint32_t n = 0;
+        bool ok = true;   // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = warp_wait(bar, parity, p.status, abort);
             tc_fence_after();
             return ok;
         };
-        auto pv = [&](uint32_t i) {
-            const uint32_t buf = i & 1u;
-            if (!wait(&tl->p_full[buf], (i >> 1) & 1u)) return;
-            if (elect_one()) {
-#pragma unroll
-                for (int m = 0; m < NM; ++m) {
-                    const uint32_t o = tmem + kTmO + 64u * (uint32_t)m;
-                    const uint32_t a = lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16);
-                    const uint32_t b = lo32(dp) + buf * (kPBuf / 16);
-                    if (starts) pv_block<true>(o, a, hi32(dv), b, hi32(dp), idesc_pv);
-                    else pv_block<false>(o, a, hi32(dv), b, hi32(dp), idesc_pv);
-                    if ((m & 1) || m == NM - 1) umma_commit(&tl->freed[buf][m >> 1]);
-                }
-            }
-            __syncwarp();
-        };
-        int2 rec = make_int2(-1, 0);
         Walk walk(wk);
         Seg sg;
-        while (ok && walk.next(p, sg)) {
-            if (sg.t0 == 0 && sg.t1 < sg.nt) {
-                const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
-                int c = (int)(last * wk.ctas / wk.total);
-                while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
-                while ((long long)c * wk.total / wk.ctas > last) --c;
-                rec = make_int2(sg.q, c);
-            }
-            if (n > 0) pv(n - 1);   // the previous segment's last tile
-            if (!ok || !wait(&tl->q_full, qn & 1u)) break;
-            ++qn;
-            for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
-                const uint32_t buf = n & 1u;
+        if (warp == 16) {
+            // the tile and Q, both K-major
+            const uint32_t idesc = idesc_f16_f32(kRows, n_mma, false, false);
+            const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
+            uint32_t qn = 0;
+            int2 rec = make_int2(-1, 0);
+            while (ok && walk.next(p, sg)) {
+                if (sg.t0 == 0 && sg.t1 < sg.nt) {
+                    const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
+                    int c = (int)(last * wk.ctas / wk.total);
+                    while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
+                    while ((long long)c * wk.total / wk.ctas > last) --c;
+                    rec = make_int2(sg.q, c);
+                }
+                if (!wait(&tl->q_full, qn & 1u)) break;
+                ++qn;
+                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
+                    if (lane == 0) tl->qk_tile = (int)n;
+                    const uint32_t buf = n & 1u;   // its S^T has been read: the tile was decoded after the PV of n - 2
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
+                    for (int h = 0; h < kHalves; ++h) {
+                        if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
+                                qk_blocks(m, tmem + 64u * buf, lo32(dk) + buf * (kTile / 16), lo32(dq), hi32(dk), idesc);
+                            if (h == kHalves - 1) umma_commit(&tl->s_full[buf]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (lane == 0) p.rec[blockIdx.x] = rec;
+        } else if (warp == 17) {
+            // the tile and P^T, both MN-major
+            const uint32_t idesc = idesc_f16_f32(128, n_mma, true, true);
+            const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128), dp = sdesc(smem_u32(p_s), kPBuf, 1024, kLayoutSW128);
+            while (ok && walk.next(p, sg)) {
+                for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+                    const uint32_t buf = n & 1u;
+                    if (!wait(&tl->p_full[buf], (n >> 1) & 1u)) break;
                     if (elect_one()) {
 #pragma unroll
-                        for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
-                            qk_blocks(m, tmem + 64u * buf, lo32(dk) + buf * (kTile / 16), lo32(dq), hi32(dk), idesc_qk);
-                        if (h == kHalves - 1) umma_commit(&tl->s_full[buf]);
+                        for (int m = 0; m < NM; ++m) {
+                            const uint32_t o = tmem + kTmO + 64u * (uint32_t)m;
+                            const uint32_t a = lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16);
+                            const uint32_t b = lo32(dp) + buf * (kPBuf / 16);
+                            if (t == sg.t0) pv_block<true>(o, a, hi32(dv), b, hi32(dp), idesc);
+                            else pv_block<false>(o, a, hi32(dv), b, hi32(dp), idesc);
+                            if ((m & 1) || m == NM - 1) umma_commit(&tl->freed[buf][m >> 1]);
+                        }
                     }
                     __syncwarp();
                 }
-                if (ok && t > sg.t0) pv(n - 1);
-                starts = t == sg.t0;
+            }
+        } else if (warp == 18 && lane == 0) {
+            // The rows of the next kAhead tiles are on their way to L2 when a tile is decoded (64 long rows of one query
+            // each: 112 -> 106 us), asked for by a sequence's first query only: the others find them there.
+            volatile int* now = &tl->qk_tile;
+            bool on = true;
+            while (on && walk.next(p, sg)) {
+                const bool asks = sg.q == sg.b * p.s;
+                for (int t = sg.t0; on && t < sg.t1; ++t, ++n) {
+                    if (!asks) continue;
+                    prefetch_rows(p, sg.b, t * kRows, min((t + 1) * kRows, sg.vis));
+                    // wait (a while at most) until the tile kAhead before is at hand
+                    for (int i = 0; *now + kAhead < (int)n && on; ++i) {
+                        on = i < 100000 && !*abort;
+                        __nanosleep(200);
+                    }
+                }
             }
         }
-        if (ok && n > 0) pv(n - 1);
-        if (warp == 16 && lane == 0) p.rec[blockIdx.x] = rec;
         __syncwarp();
     } else if (warp >= 8) {
         regs_down<kRegsDecode>();
