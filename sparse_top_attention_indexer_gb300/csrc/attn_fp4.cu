@@ -9,11 +9,12 @@
 // attn_fp4_kernel: persistent CTAs, one per SM; the queries' 64-row tiles form one long list that is cut
 // into equal contiguous pieces, so a few long queries, many short ones and ragged batches all fill
 // the GPU.  A query whose tiles fall to several CTAs leaves one fp32 partial per CTA; merge_kernel joins
-// them.  Two tile buffers; 17 working warps:
+// them.  Two tile buffers; 19 working warps:
 //   * warps 8..15 decode the rows into the free buffer, from codes loaded a tile ahead, one half (256 dims)
 //     at a time as the PV two tiles earlier releases it;
-//   * warp 16 issues the MMAs: QK of tile i + 1, S^T = tile . Q^T (M = 64 rows, N = heads), then PV of tile i,
-//     O^T += V^T . P^T (M = 128 dims per block, K = 64 rows; the same tile read as an MN-major operand);
+//   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128
+//     dims per block, K = 64 rows; the same tile read as an MN-major operand);
+//   * warp 18 asks for the rows of the next tiles, into L2;
 //   * warps 0..7 load Q, run the online softmax (two groups of 32 heads; the running maxima move only when a
 //     score passes them by 2^8) and write the outputs.
 // With 512 dims, Q (64 KB), two tiles of 64 rows (128 KB) and two P^T (16 KB) fill shared memory.  One tile of
@@ -42,8 +43,8 @@
 namespace sti {
 namespace {
 
-constexpr int kThreads = 640;                  // 8 softmax warps, 8 decoding warps, 1 MMA warp (and 3 that
-                                               // only complete its warpgroup)
+constexpr int kThreads = 640;                  // 8 softmax warps, 8 decoding warps, 2 MMA warps, 1 that
+                                               // prefetches (and 1 that only completes its warpgroup)
 // registers per thread after setmaxnreg: 256 x 128 + 256 x 80 + 128 x 64 = 61,440, the 640 x 96 of the launch
 constexpr int kRegsSoft = 128, kRegsDecode = 80, kRegsMma = 64;
 constexpr int kRows = 64;                      // rows per tile
@@ -53,7 +54,7 @@ constexpr uint32_t kPBuf = kRows * 128;        // a P^T buffer: 64 rows x 64 hea
 constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at columns [64 b, 64 b + 64), O^T d-block
                                                // m at [128 + 64 m, 192 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kAhead = 3;                      // tiles ahead
+constexpr int kAhead = 3;                      // tiles whose rows are asked for ahead
 constexpr int kWTiles = 32;                    // row weights: tiles per chunk (accumulators in shared memory)
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
