@@ -908,10 +908,10 @@ sti_status sti_kv_append_fp4(const uint16_t* x, int64_t x_bstride, const int32_t
 }
 
 // attention workspace: [status | split records | partial (max, sum) | partial outputs | lse | partial row
-// weights].  Sized for the largest GB300 (160 SMs), whatever device is current.
+// weights | scores].  Sized for the largest GB300 (160 SMs), whatever device is current.
 static constexpr int kAttnFp4MaxSms = 160;
 struct AttnFp4Layout {
-    size_t rec, ml, o, lse, w, end;
+    size_t rec, ml, o, lse, w, scores, end;
     int grid, w_grid, w_split;
 };
 static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows) {
@@ -923,7 +923,9 @@ static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows
     l.o = after(l.ml, (size_t)2 * l.grid * 64 * sizeof(float2));
     l.lse = after(l.o, (size_t)2 * l.grid * h * d * sizeof(float));
     l.w = after(l.lse, (size_t)b * seqlen * h * sizeof(float));
-    l.end = after(l.w, l.w_split > 1 ? (size_t)l.w_split * b * n_rows * sizeof(float) : 0);
+    const size_t scores = sti::attn_fp4_score_bytes(b, seqlen, n_rows);
+    l.scores = after(l.w, scores == 0 && l.w_split > 1 ? (size_t)l.w_split * b * n_rows * sizeof(float) : 0);
+    l.end = l.scores + scores;
     return l;
 }
 
@@ -982,6 +984,7 @@ sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes
     p.part_ml = reinterpret_cast<float2*>(wsb + l.ml);
     p.part_o = reinterpret_cast<float*>(wsb + l.o);
     p.w_part = reinterpret_cast<float*>(wsb + l.w);
+    p.scores = row_weight && l.end > l.scores ? reinterpret_cast<float*>(wsb + l.scores) : nullptr;
     const int sms = sti::device_num_sms();
     sti::attn_fp4_plan(b, seqlen, n_rows, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms, &p.grid, &p.w_grid, &p.w_split);
     const cudaError_t e = sti::launch_attn_fp4(p, static_cast<cudaStream_t>(stream));

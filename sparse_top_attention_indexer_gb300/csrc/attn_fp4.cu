@@ -28,10 +28,10 @@
 // off by less than 2^-37 of the largest.  P is rounded to f16 (2^-11) for the PV product; its sum l is
 // taken before the rounding, in fp32.
 //
-// row_weight_kernel (only when asked for): p = e^{s - L} needs the final L, so it runs after the merge and
-// recomputes S^T (the tile's codes are read again, mostly from L2: cheaper than storing 4 bytes per
-// score).  Each row tile belongs to one CTA, which adds the queries in order: no atomics.  When there are
-// fewer tiles than SMs, queries split over CTAs and a last kernel adds the parts in order.
+// Row weights (only when asked for): p = e^{s - L} needs the final L, so they come after the merge.  A few queries a
+// sequence (decoding, drafts) leave their scores in the workspace, 4 bytes each, and row_weight_scores_kernel sums
+// them; row_weight_kernel computes S^T again from the codes.  Each row tile belongs to one CTA, which adds the queries
+// in order: no atomics.  With many queries row_weight_kernel's CTAs split over them and a last kernel adds the parts.
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stddef.h>
@@ -56,6 +56,9 @@ constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr int kAhead = 3;                      // tiles whose rows are asked for ahead
 constexpr int kWTiles = 32;                    // row weights: tiles per chunk (accumulators in shared memory)
+constexpr int kScoreQueries = 8;               // row weights from kept scores: at most this many queries a sequence,
+constexpr int kScoreTiles = 16384;             // and this many tiles of scores (256 MB)
+constexpr int kManyTiles = 4096;               // row weights from scores: from here on a block takes four tiles
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 // instruction descriptor, kind::f16 with f16 A/B (format 0) and fp32 accumulator
@@ -439,7 +442,7 @@ __device__ __forceinline__ void zero_padding(int h, int n_cb, int n_m, uint8_t* 
         }
 }
 
-template <int NM>   // d-blocks of 128 dims
+template <int NM, bool kScores>   // d-blocks of 128 dims; whether the scores are kept for the row weights
 __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Params p) {
     constexpr int kHalves = (NM + 1) / 2;
     constexpr uint32_t kTile = 2 * NM * kTBlk;
@@ -626,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 cm[2 * g + 1] = make_float2(v.z, v.w);
             }
         };
-        auto softmax = [&](int left, bool first) {   // left: visible rows from this thread's first one on
+        // left: visible rows from this thread's first one on; tile: of all the queries' (kScores)
+        auto softmax = [&](int left, bool first, int64_t tile) {
             const uint32_t buf = n & 1u;
             mwait(&tl->s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
@@ -635,6 +639,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             uint32_t r[16];
             tmem_ld_rows16(ts, r);
             tmem_ld_wait();
+            if (kScores) {
+                float4* sc = reinterpret_cast<float4*>(p.scores) + (tile * 8 + warp) * 128 + lane;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    __stcs(sc + 32 * g, make_float4(__uint_as_float(r[4 * g]) * cm[2 * g].x,
+                                                    __uint_as_float(r[4 * g + 1]) * cm[2 * g + 1].x,
+                                                    __uint_as_float(r[4 * g + 2]) * cm[2 * g].x,
+                                                    __uint_as_float(r[4 * g + 3]) * cm[2 * g + 1].x));
+            }
             float y[16];
             float top0 = -INFINITY, top1 = -INFINITY;
             auto scale = [&]() {
@@ -845,7 +858,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
 #pragma unroll
             for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
             for (int t = sg.t0; t < sg.t1; ++t, ++n)
-                if (active) softmax(sg.vis - t * kRows - row, t == sg.t0);
+                if (active)
+                    softmax(sg.vis - t * kRows - row, t == sg.t0,
+                            kScores ? (int64_t)sg.q * ((p.n_rows + kRows - 1) / kRows) + t : 0);
             pend_q = sg.q;
             pend_slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
         }
@@ -1277,6 +1292,84 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
     }
 }
 
+// Row weights from the kept scores (in units of log2, as the softmax threads held them): block (x, b) takes `per` tiles
+// of sequence b and adds each one's queries in order.  Per score 4 bytes are read and one 2^x taken.
+__global__ void __launch_bounds__(256, 6) row_weight_scores_kernel(const AttnFp4Params p, int per) {
+    __shared__ float part[2][kRows];
+    __shared__ float lse[kScoreQueries][64];   // in log2; read once per block: every block of a sequence wants the same
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int set = warp >> 2, row = 16 * (warp & 3) + (lane >> 2), l4 = lane & 3;
+    const bool active = 32 * set < p.h;
+    const int tiles = (p.n_rows + kRows - 1) / kRows;
+    griddep_wait();
+    for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
+        const int vis_all = visible_rows(p, b, p.s - 1);
+        int t = blockIdx.x * per;
+        const int end = min(t + per, (vis_all + kRows - 1) / kRows);
+        if (t >= end) continue;
+        float4 v[4];
+        auto load = [&](int tt, int kk) {
+            const int64_t q = (int64_t)b * p.s + kk;
+            const float4* sc = reinterpret_cast<const float4*>(p.scores) + ((q * tiles + tt) * 8 + warp) * 128 + lane;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) v[g] = __ldcs(sc + 32 * g);
+        };
+        // the queries see ever more rows: those from the first one on that sees the tile's first row
+        auto first = [&](int tt, int kk) {
+            while (visible_rows(p, b, kk) <= tt * kRows) ++kk;
+            return kk;
+        };
+        int k0 = first(t, 0), k = k0;
+        if (active) load(t, k);
+        for (int i = tid; i < p.s * 64; i += 256) {
+            const int hd = i & 63;
+            lse[i >> 6][hd] = hd < p.h ? __ldcg(p.lse + ((int64_t)b * p.s + (i >> 6)) * p.h + hd) * kLog2e : 0.f;
+        }
+        __syncthreads();
+        while (t < end) {
+            float sum0 = 0.f, sum1 = 0.f;
+            const int k_next = t + 1 < end ? first(t + 1, k0) : 0;
+            if (active)
+                for (k = k0; k < p.s; ++k) {
+                    const int vis = visible_rows(p, b, k) - t * kRows;
+                    float a = 0.f, c = 0.f;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int hd = 32 * set + 8 * g + 2 * l4;
+                        const float2 l = *reinterpret_cast<const float2*>(&lse[k][hd]);
+                        if (hd < p.h) {
+                            a += fast_exp2(v[g].x - l.x);
+                            c += fast_exp2(v[g].z - l.x);
+                        }
+                        if (hd + 1 < p.h) {
+                            a += fast_exp2(v[g].y - l.y);
+                            c += fast_exp2(v[g].w - l.y);
+                        }
+                    }
+                    if (k + 1 < p.s) load(t, k + 1);
+                    else if (t + 1 < end) load(t + 1, k_next);
+                    if (row < vis) sum0 += a;
+                    if (row + 8 < vis) sum1 += c;
+                }
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                sum0 += __shfl_xor_sync(kWarpFull, sum0, o);
+                sum1 += __shfl_xor_sync(kWarpFull, sum1, o);
+            }
+            if (l4 == 0) {
+                part[set][row] = sum0;
+                part[set][row + 8] = sum1;
+            }
+            __syncthreads();
+            if (tid < kRows && t * kRows + tid < vis_all)
+                p.row_weight[(int64_t)b * p.row_weight_bstride + t * kRows + tid] += part[0][tid] + part[1][tid];
+            __syncthreads();
+            ++t;
+            k0 = k_next;
+        }
+    }
+}
+
 // The query splits' partial row weights, added in order.
 __global__ void __launch_bounds__(256) row_weight_add_kernel(const AttnFp4Params p) {
     const int b = blockIdx.y;
@@ -1291,8 +1384,8 @@ __global__ void __launch_bounds__(256) row_weight_add_kernel(const AttnFp4Params
     }
 }
 
-template <class K>
-cudaError_t launch_after(K* kernel, dim3 grid, int threads, size_t smem, const AttnFp4Params& p, cudaStream_t stream) {
+template <class... T>
+cudaError_t launch_after(void (*kernel)(T...), dim3 grid, int threads, size_t smem, cudaStream_t stream, T... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -1303,7 +1396,7 @@ cudaError_t launch_after(K* kernel, dim3 grid, int threads, size_t smem, const A
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
@@ -1324,30 +1417,46 @@ void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid
     *w_grid = (int)(split * (all < per ? (all > 0 ? all : 1) : per));
 }
 
+// Keeping the scores (256 bytes a row, next to the 288 of its codes) costs less than computing them again: row weights
+// of 32 x 1, 16 x 2 and 4 x 8 queries over 16384 rows 42, 42 and 38 us, computed again 92, 90 and 83; of 8 queries over
+// 1024 rows 7 and 9 us.  Many queries would ask for too large a workspace and, with few rows, for too few blocks.
+size_t attn_fp4_score_bytes(int B, int s, int n_rows) {
+    const int64_t tiles = ((int64_t)n_rows + kRows - 1) / kRows;
+    if (s > kScoreQueries || tiles * s > kScoreTiles / B) return 0;
+    return (size_t)(tiles * s * B) * kRows * 64 * sizeof(float);
+}
+
 namespace {
 template <int NM>
 cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
     const int nq = p.B * p.s;
     size_t smem = attn_smem(p.d);
-    cudaError_t e = cudaFuncSetAttribute(attn_fp4_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto* kernel = p.scores ? attn_fp4_kernel<NM, true> : attn_fp4_kernel<NM, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    attn_fp4_kernel<NM><<<p.grid, kThreads, smem, stream>>>(p);
+    kernel<<<p.grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
     const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)p.h;
-    e = parts > 16  ? launch_after(merge_kernel<16, 32>, dim3(mx, mh, (unsigned)NM), 512, 0, p, stream)
-        : parts > 4 ? launch_after(merge_kernel<2, 128>, dim3(mx, mh), 256, 0, p, stream)
-                    : launch_after(merge_kernel<1, 128>, dim3(mx, mh), 128, 0, p, stream);
+    e = parts > 16  ? launch_after(merge_kernel<16, 32>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
+        : parts > 4 ? launch_after(merge_kernel<2, 128>, dim3(mx, mh), 256, 0, stream, p)
+                    : launch_after(merge_kernel<1, 128>, dim3(mx, mh), 128, 0, stream, p);
     if (e != cudaSuccess || !p.row_weight || p.n_rows == 0) return e;
+    if (p.scores) {
+        const int tiles = (p.n_rows + kRows - 1) / kRows, per = (int64_t)tiles * p.B >= kManyTiles ? 4 : 1;
+        return launch_after(row_weight_scores_kernel,
+                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)(p.B < 65535 ? p.B : 65535)), 256, 0, stream,
+                            p, per);
+    }
     smem = row_weight_smem(p.d);
     e = cudaFuncSetAttribute(row_weight_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_after(row_weight_kernel<NM>, dim3((unsigned)p.w_grid), kThreads, smem, p, stream);
+    e = launch_after(row_weight_kernel<NM>, dim3((unsigned)p.w_grid), kThreads, smem, stream, p);
     if (e != cudaSuccess || p.w_split == 1) return e;
     const int blocks = (p.n_rows + 255) / 256;
     return launch_after(row_weight_add_kernel,
-                        dim3((unsigned)(blocks < 64 ? blocks : 64), (unsigned)(p.B < 65535 ? p.B : 65535)), 256, 0, p,
-                        stream);
+                        dim3((unsigned)(blocks < 64 ? blocks : 64), (unsigned)(p.B < 65535 ? p.B : 65535)), 256, 0,
+                        stream, p);
 }
 }  // namespace
 

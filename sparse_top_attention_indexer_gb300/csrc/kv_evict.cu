@@ -16,9 +16,12 @@
 //      and prefix sums over warps and CTAs (no atomics whose order could show);
 //   4. holes and movers get their ranks the same way and go to two lists in the workspace;
 //   5. the cluster copies mover i to hole i, in pieces of up to 16 bytes, over all arrays at once.
-// Bound by latency: the chain of cluster barriers (two per pass, four after), not by the 8 bytes per row
-// it reads.  C = 1 up to kOneCtaRows rows (a CTA covers them in a few iterations and a cluster barrier
-// costs more than it saves), else 8.
+// Bound by latency: the chain of barriers (two per pass and four after over the cluster, with C = 8), not by the 8 bytes
+// per row it reads: 32 sequences of 4097 rows losing one row each 10 us, 8 of 4096 + 2048 rows 18 us, one of 65,536
+// down to 16,384 rows 25 us.  Adding equal bins within a warp before the histogram costs more (12, 19, 28 us) than
+// the collisions of its atomics.
+// C = 1 up to kOneCtaRows rows (a CTA covers them in a few iterations and a cluster barrier costs more than it saves),
+// else 8.
 #include <math.h>
 
 #include "sti_internal.h"
@@ -35,11 +38,11 @@ constexpr int kKeyCache = 40960;   // keys a CTA holds in shared memory; rows pa
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 struct EvTail {
-    uint32_t hist[kBins];
+    uint32_t hist[2][kBins];    // [pass parity]
     uint32_t sum[kBins];        // this CTA's slice of the cluster-wide bins
     uint32_t slice_total;
     uint32_t warp_cnt[2][kEvWarps];
-    uint32_t cta_cnt[2];
+    uint32_t cta_cnt[2][2];     // [call of rank_base]
     uint32_t scratch[kEvWarps];
     uint32_t found[2];          // bin, rows above it
 };
@@ -79,8 +82,9 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* scratch, ui
     return (warp ? before : 0u) + inc - v;
 }
 
-// Counts of two kinds of rows per warp -> the counts in all earlier warps of the cluster.
-template <int C>
+// Counts of two kinds of rows per warp -> the counts in all earlier warps of the cluster.  The two calls have counts of
+// their own: nobody waits until they are read.
+template <int C, int kCall>
 __device__ __forceinline__ void rank_base(EvTail* tl, int rank, uint32_t c0, uint32_t c1, uint32_t& b0, uint32_t& b1) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) {
@@ -95,15 +99,14 @@ __device__ __forceinline__ void rank_base(EvTail* tl, int rank, uint32_t c0, uin
     b1 = __reduce_add_sync(kFull, w1);
     if (C > 1) {
         if (threadIdx.x == 0) {
-            tl->cta_cnt[0] = t0;
-            tl->cta_cnt[1] = t1;
+            tl->cta_cnt[kCall][0] = t0;
+            tl->cta_cnt[kCall][1] = t1;
         }
         ev_sync<C>();
         for (int c = 0; c < rank; ++c) {
-            b0 += peer_u32<C>(&tl->cta_cnt[0], c);
-            b1 += peer_u32<C>(&tl->cta_cnt[1], c);
+            b0 += peer_u32<C>(&tl->cta_cnt[kCall][0], c);
+            b1 += peer_u32<C>(&tl->cta_cnt[kCall][1], c);
         }
-        ev_sync<C>();   // the counts may be overwritten
     } else {
         __syncthreads();
     }
@@ -156,7 +159,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
     };
     auto key = [&](int j) -> uint32_t { return j - cta0 < kKeyCache ? keys[j - cta0] : make_key(j); };
 
-    for (int i = tid; i < kBins; i += kEvThreads) tl->hist[i] = 0u;
+    for (int i = tid; i < 2 * kBins; i += kEvThreads) tl->hist[0][i] = 0u;
     for (int j = w0 + lane; j < w1 && j - cta0 < kKeyCache; j += 32) keys[j - cta0] = make_key(j);
     __syncthreads();
 
@@ -168,17 +171,18 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
             const int bins = pass == 2 ? 1024 : 2048;
             const uint32_t above = pass == 0 ? 0u : 0xFFFFFFFFu << (pass == 1 ? 21 : 10);   // bits already fixed
+            uint32_t* hist = tl->hist[pass & 1];
             for (int j = w0 + lane; j < w1; j += 32) {
                 const uint32_t k = key(j);
-                if ((k & above) == prefix) atomicAdd(&tl->hist[(k >> shift) & (uint32_t)(bins - 1)], 1u);
+                if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & (uint32_t)(bins - 1)], 1u);
             }
-            ev_sync<C>();
+            ev_sync<C>();   // also: every CTA has read the sums of the pass before
             // this CTA's slice of the bins, summed over the cluster; totals per slice
             const int per = bins / C;
             for (int i = tid; i < per; i += kEvThreads) {
                 uint32_t v = 0u;
 #pragma unroll
-                for (int c = 0; c < C; ++c) v += peer_u32<C>(&tl->hist[rank * per + i], c);
+                for (int c = 0; c < C; ++c) v += peer_u32<C>(&hist[rank * per + i], c);
                 tl->sum[i] = v;
             }
             if (C > 1) {
@@ -189,7 +193,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
                 block_scan(t, tl->scratch, &tot);
                 if (tid == 0) tl->slice_total = tot;
             }
-            ev_sync<C>();
+            ev_sync<C>();   // also: every CTA has read this pass's histograms
             // from the top: the slice, then the bin, in which the want-th row lies
             int slice = C - 1;
             if (C > 1) {
@@ -213,8 +217,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
                 tl->found[0] = (uint32_t)(slice * per + per - 1 - (2 * tid + e));
                 tl->found[1] = before + (e ? v[0] : 0u);
             }
-            for (int i = tid; i < kBins; i += kEvThreads) tl->hist[i] = 0u;
-            ev_sync<C>();   // every CTA has read the sums
+            for (int i = tid; i < kBins; i += kEvThreads) hist[i] = 0u;   // for the pass after the next
+            __syncthreads();
             prefix |= tl->found[0] << shift;
             want -= tl->found[1];
             __syncthreads();
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
             const int j = j0 + lane;
             c += __popc(__ballot_sync(kFull, j < w1 && key(j) == T));
         }
-        rank_base<C>(tl, rank, c, 0u, eq_base, unused);
+        rank_base<C, 0>(tl, rank, c, 0u, eq_base, unused);
     }
     auto for_rows = [&](auto&& f) {
         uint32_t eq = eq_base;
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
         n_hole += __popc(holes);
         n_move += __popc(movers);
     });
-    rank_base<C>(tl, rank, n_hole, n_move, hole_base, move_base);
+    rank_base<C, 1>(tl, rank, n_hole, n_move, hole_base, move_base);
     int32_t* to = p.lists + (int64_t)b * 2 * p.most;
     int32_t* of = to + p.most;
     for_rows([&](int j, uint32_t holes, uint32_t movers) {
@@ -264,9 +268,9 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
         move_base += __popc(movers);
     });
     // the cluster's last warp ends at the number of moves
-    if (tid == kEvThreads - 1) tl->cta_cnt[0] = move_base;
+    if (tid == kEvThreads - 1) tl->cta_cnt[0][0] = move_base;
     ev_sync<C>();   // lists complete, every row's weight and position read
-    const uint32_t n = peer_u32<C>(&tl->cta_cnt[0], C - 1);
+    const uint32_t n = peer_u32<C>(&tl->cta_cnt[0][0], C - 1);
 
     // move: pieces of every array, one flat index over (array, move, piece)
     int a = 0;

@@ -217,7 +217,10 @@ struct AttnFp4Params {
     int w_split;                // row weights: query splits (partial sums in w_part when > 1)
     int w_grid;                 // row weights: CTAs, a multiple of w_split
     float* w_part;              // [w_split][B][n_rows]
+    float* scores;              // [B * s][tiles][8 warps][4][32 lanes][4]: kept for the row weights, or null
 };
+// whether a call with row weights keeps its scores, and their size
+size_t attn_fp4_score_bytes(int B, int s, int n_rows);
 // CTAs of the attention kernel, of the row-weight kernel, and its query splits
 void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid, int* w_split);
 cudaError_t launch_attn_fp4(const AttnFp4Params& p, cudaStream_t stream);
