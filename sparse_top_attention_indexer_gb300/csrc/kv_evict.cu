@@ -17,8 +17,8 @@
 //   4. holes and movers get their ranks the same way and go to two lists in the workspace;
 //   5. the cluster copies mover i to hole i, in pieces of up to 16 bytes, over all arrays at once.
 // Bound by latency: the chain of barriers (two per pass and four after over the cluster, with C = 8), not by the 8 bytes
-// per row it reads: 32 sequences of 4097 rows losing one row each 10 us, 8 of 4096 + 2048 rows 18 us, one of 65,536
-// down to 16,384 rows 25 us.  Adding equal bins within a warp before the histogram costs more (12, 19, 28 us) than
+// per row it reads: 32 sequences of 2049 rows losing one each 10 us, 8 of 8704 rows losing 512 18 us, one of 52,003
+// rows losing 2002 23 us.  Adding equal bins within a warp before the histogram costs more (12, 19, 28 us) than
 // the collisions of its atomics.
 // C = 1 up to kOneCtaRows rows (a CTA covers them in a few iterations and a cluster barrier costs more than it saves),
 // else 8.
@@ -103,14 +103,16 @@ __device__ __forceinline__ void rank_base(EvTail* tl, int rank, uint32_t c0, uin
             tl->cta_cnt[kCall][1] = t1;
         }
         ev_sync<C>();
-        for (int c = 0; c < rank; ++c) {
-            b0 += peer_u32<C>(&tl->cta_cnt[kCall][0], c);
-            b1 += peer_u32<C>(&tl->cta_cnt[kCall][1], c);
-        }
+        // one remote read per CTA and warp, all at once
+        const bool before = lane < rank;
+        b0 += __reduce_add_sync(kFull, before ? peer_u32<C>(&tl->cta_cnt[kCall][0], lane) : 0u);
+        b1 += __reduce_add_sync(kFull, before ? peer_u32<C>(&tl->cta_cnt[kCall][1], lane) : 0u);
     } else {
         __syncthreads();
     }
 }
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u; }
 
 template <int BYTES>
 struct Piece;
@@ -150,17 +152,30 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
     const int cta0 = min(held, rank * per_warp * kEvWarps);
     const int w0 = min(held, cta0 + warp * per_warp), w1 = min(held, w0 + per_warp);
 
-    auto make_key = [&](int j) -> uint32_t {
-        const int q = pos[j];
+    auto key_of = [&](int q, float w) -> uint32_t {
         if (q < p.n_first || q >= recent) return 0xFFFFFFFFu;
-        const float w = weight[j] + 0.f;   // -0 counts as 0
+        w += 0.f;                          // -0 counts as 0
         if (w != w) return 0xFFFFFFFEu;    // NaN: above every number
         return float_key(w);
     };
+    auto make_key = [&](int j) -> uint32_t { return key_of(pos[j], weight[j]); };
     auto key = [&](int j) -> uint32_t { return j - cta0 < kKeyCache ? keys[j - cta0] : make_key(j); };
 
     for (int i = tid; i < 2 * kBins; i += kEvThreads) tl->hist[0][i] = 0u;
-    for (int j = w0 + lane; j < w1 && j - cta0 < kKeyCache; j += 32) keys[j - cta0] = make_key(j);
+    const int w_cached = min(w1, cta0 + kKeyCache);
+    for (int j0 = w0 + lane; j0 < w_cached; j0 += 8 * 32) {   // eight rows' loads in flight
+        int q[8];
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = min(j0 + 32 * i, w_cached - 1);
+            q[i] = pos[j];
+            w[i] = weight[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j0 + 32 * i < w_cached) keys[j0 + 32 * i - cta0] = key_of(q[i], w[i]);
+    }
     __syncthreads();
 
     // the budget-th largest key
@@ -197,8 +212,9 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
             // from the top: the slice, then the bin, in which the want-th row lies
             int slice = C - 1;
             if (C > 1) {
+                const uint32_t mine = lane < C ? peer_u32<C>(&tl->slice_total, lane) : 0u;
                 for (; slice > 0; --slice) {
-                    const uint32_t t = peer_u32<C>(&tl->slice_total, slice);
+                    const uint32_t t = __shfl_sync(kFull, mine, slice);
                     if (t >= want) break;
                     want -= t;
                 }
@@ -232,11 +248,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
     uint32_t eq_base, unused;
     {
         uint32_t c = 0u;
-        for (int j0 = w0; j0 < w1; j0 += 32) {
-            const int j = j0 + lane;
-            c += __popc(__ballot_sync(kFull, j < w1 && key(j) == T));
-        }
-        rank_base<C, 0>(tl, rank, c, 0u, eq_base, unused);
+        for (int j = w0 + lane; j < w1; j += 32) c += key(j) == T ? 1u : 0u;
+        rank_base<C, 0>(tl, rank, __reduce_add_sync(kFull, c), 0u, eq_base, unused);
     }
     auto for_rows = [&](auto&& f) {
         uint32_t eq = eq_base;
@@ -247,9 +260,9 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(const KvEvictParam
             const uint32_t m = __ballot_sync(kFull, is_eq);
             const bool kept = j < w1 && (k > T || (is_eq && eq + __popc(m & ((1u << lane) - 1u)) < want));
             eq += __popc(m);
-            const uint32_t holes = __ballot_sync(kFull, j < w1 && !kept && j < budget);
-            const uint32_t movers = __ballot_sync(kFull, kept && j >= budget);
-            f(j, holes, movers);
+            // bits of the step's rows that exist, and of those below the budget
+            const uint32_t stay = __ballot_sync(kFull, kept), real = low_bits(w1 - j0), below = low_bits(budget - j0);
+            f(j, real & ~stay & below, stay & ~below);
         }
     };
     uint32_t n_hole = 0u, n_move = 0u, hole_base, move_base;
