@@ -912,20 +912,18 @@ sti_status sti_kv_append_fp4(const uint16_t* x, int64_t x_bstride, const int32_t
 static constexpr int kAttnFp4MaxSms = 160;
 struct AttnFp4Layout {
     size_t rec, ml, o, lse, w, scores, end;
-    int grid, w_grid, w_split;
 };
 static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows) {
     AttnFp4Layout l;
-    sti::attn_fp4_plan(b, seqlen, n_rows, kAttnFp4MaxSms, &l.grid, &l.w_grid, &l.w_split);
+    const sti::AttnFp4Plan pl = sti::attn_fp4_plan(b, seqlen, h, n_rows, kAttnFp4MaxSms);
     auto after = [](size_t at, size_t bytes) { return sti::align_up(at + bytes, sti::kWsAlign); };
     l.rec = sti::kWsStatusBytes;
-    l.ml = after(l.rec, (size_t)l.grid * sizeof(int2));
-    l.o = after(l.ml, (size_t)2 * l.grid * 64 * sizeof(float2));
-    l.lse = after(l.o, (size_t)2 * l.grid * h * d * sizeof(float));
+    l.ml = after(l.rec, (size_t)pl.grid * sizeof(int2));
+    l.o = after(l.ml, (size_t)2 * pl.grid * 64 * sizeof(float2));
+    l.lse = after(l.o, (size_t)2 * pl.grid * pl.pack * h * d * sizeof(float));
     l.w = after(l.lse, (size_t)b * seqlen * h * sizeof(float));
-    const size_t scores = sti::attn_fp4_score_bytes(b, seqlen, n_rows);
-    l.scores = after(l.w, scores == 0 && l.w_split > 1 ? (size_t)l.w_split * b * n_rows * sizeof(float) : 0);
-    l.end = l.scores + scores;
+    l.scores = after(l.w, pl.score_bytes == 0 && pl.w_split > 1 ? (size_t)pl.w_split * b * n_rows * sizeof(float) : 0);
+    l.end = l.scores + pl.score_bytes;
     return l;
 }
 
@@ -986,7 +984,12 @@ sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes
     p.w_part = reinterpret_cast<float*>(wsb + l.w);
     p.scores = row_weight && l.end > l.scores ? reinterpret_cast<float*>(wsb + l.scores) : nullptr;
     const int sms = sti::device_num_sms();
-    sti::attn_fp4_plan(b, seqlen, n_rows, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms, &p.grid, &p.w_grid, &p.w_split);
+    const sti::AttnFp4Plan pl = sti::attn_fp4_plan(b, seqlen, h, n_rows, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms);
+    p.pack = pl.pack;
+    p.groups = pl.groups;
+    p.grid = pl.grid;
+    p.w_grid = pl.w_grid;
+    p.w_split = pl.w_split;
     const cudaError_t e = sti::launch_attn_fp4(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_attn_fp4kv");
 }

@@ -15,7 +15,7 @@
 //   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128
 //     dims per block, K = 64 rows; the same tile read as an MN-major operand);
 //   * warp 18 asks for the rows of the next tiles, into L2;
-//   * warps 0..7 load Q, run the online softmax (two groups of 32 heads; the running maxima move only when a
+//   * warps 0..7 load Q, run the online softmax (two sets of 32 heads; the running maxima move only when a
 //     score passes them by 2^8) and write the outputs.
 // With 512 dims, Q (64 KB), two tiles of 64 rows (128 KB) and two P^T (16 KB) fill shared memory.  One tile of
 // 128 rows instead would halve the QK's MMAs (one of M = 64 costs as much as one of M = 128), but leaves
@@ -56,7 +56,7 @@ constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr int kAhead = 3;                      // tiles whose rows are asked for ahead
 constexpr int kWTiles = 32;                    // row weights: tiles per chunk (accumulators in shared memory)
-constexpr int kScoreQueries = 8;               // row weights from kept scores: at most this many queries a sequence,
+constexpr int kScoreQueries = 8;               // row weights from kept scores: at most this many query groups a sequence,
 constexpr int kScoreTiles = 16384;             // and this many tiles of scores (256 MB)
 constexpr int kManyTiles = 4096;               // row weights from scores: from here on a block takes four tiles
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
@@ -173,18 +173,41 @@ __device__ __forceinline__ int visible_rows(const AttnFp4Params& p, int b, int t
     return v < 0 ? 0 : v > p.n_rows ? p.n_rows : (int)v;
 }
 
+// Query groups: `pack` consecutive queries of a sequence whose heads together fill the 64 rows of Q (pack = 1: one
+// query).  In memory they are one query of pack * h heads, each head with its own number of visible rows.
+struct Group {
+    int b, t0, heads;
+    int64_t row0;       // of q, out, prev_out, lse, prev_lse: their first head
+};
+__device__ __forceinline__ Group group_of(const AttnFp4Params& p, int u) {
+    Group g;
+    g.b = u / p.groups;
+    g.t0 = (u - g.b * p.groups) * p.pack;
+    g.heads = min(p.pack, p.s - g.t0) * p.h;
+    g.row0 = ((int64_t)g.b * p.s + g.t0) * p.h;
+    return g;
+}
+// rows that the last query of group u (of sequence b) sees
+__device__ __forceinline__ int group_rows(const AttnFp4Params& p, int b, int u) {
+    return visible_rows(p, b, min((u + 1) * p.pack, p.s) - 1);
+}
+// rows that head hd of the group sees
+__device__ __forceinline__ int head_rows(const AttnFp4Params& p, const Group& g, int hd) {
+    return hd < g.heads ? visible_rows(p, g.b, g.t0 + hd / p.h) : 0;
+}
+
 struct Work {           // this CTA's piece of the list
     long long lo, hi;   // tiles [lo, hi) of the list
-    int q, off;         // the first one: tile `off` of query q
+    int q, off;         // the first one: tile `off` of query group q
     long long total;
     int ctas;           // CTAs that have tiles
 };
 
-struct Seg {            // a run of one query's tiles
+struct Seg {            // a run of one group's tiles
     int q, b, vis, nt, t0, t1;
 };
 
-// Walk the piece: query by query, those without a visible row skipped.
+// Walk the piece: group by group, those without a visible row skipped.
 struct Walk {
     long long pos, hi;
     int q, off;
@@ -192,8 +215,8 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttnFp4Params& p, Seg& s) {
         while (pos < hi) {
             s.q = q;
-            s.b = q / p.s;
-            s.vis = visible_rows(p, s.b, q - s.b * p.s);
+            s.b = q / p.groups;
+            s.vis = group_rows(p, s.b, q - s.b * p.groups);
             s.nt = (s.vis + kRows - 1) / kRows;
             s.t0 = off;
             s.t1 = (long long)(s.nt - off) < hi - pos ? s.nt : off + (int)(hi - pos);
@@ -337,9 +360,10 @@ __device__ __forceinline__ void decode_quarter(uint8_t* dst, int row, int ch, bo
 
 // Decode this thread's part of the tile into the buffer at t_s, half by half: `released(h)` waits until half h
 // may be overwritten (false: gave up), full[h] gets one arrival per warp.
-template <int NM, class F>
+// kTag: a NaN scale counts as 0, and tag[row] = serial marks its row.
+template <int NM, bool kTag, class F>
 __device__ __forceinline__ bool decode_tile(uint8_t* t_s, int row0, int vis, int n_cb, const Codes<NM>& r, uint64_t* full,
-                                            F released) {
+                                            uint32_t* tag, uint32_t serial, F released) {
     const int lane = threadIdx.x & 31, ch = lane & 3;
     const int row = ((threadIdx.x >> 5) & 7) * 8 + (lane >> 2);
 #pragma unroll
@@ -348,7 +372,14 @@ __device__ __forceinline__ bool decode_tile(uint8_t* t_s, int row0, int vis, int
 #pragma unroll
         for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m) {
             const int cb = 2 * m + (ch >> 1);
-            if (cb < n_cb) decode_quarter(t_s + (size_t)cb * kTBlk + row * 128, row, ch, row0 + row < vis, r.c[m], r.s[m]);
+            uint32_t sc = r.s[m];
+            if (kTag && cb < n_cb && row0 + row < vis) {
+                const bool n0 = (sc & 0x7Fu) == 0x7Fu, n1 = (sc & 0x7F00u) == 0x7F00u;
+                if (n0) sc &= 0xFF00u;
+                if (n1) sc &= 0x00FFu;
+                if (n0 || n1) tag[row] = serial;
+            }
+            if (cb < n_cb) decode_quarter(t_s + (size_t)cb * kTBlk + row * 128, row, ch, row0 + row < vis, r.c[m], sc);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -357,14 +388,14 @@ __device__ __forceinline__ bool decode_tile(uint8_t* t_s, int row0, int vis, int
     return true;
 }
 
-// Query qi's heads as f16 into the swizzled column blocks at q_s, four softmax threads per head, each head
+// The group's heads as f16 into the swizzled column blocks at q_s, four softmax threads per head, each head
 // scaled by 2^f; qc[head] = scale_log2 * 2^-f.
 template <int NM>
-__device__ __forceinline__ void load_q(const AttnFp4Params& p, int qi, uint8_t* q_s, float* qc) {
+__device__ __forceinline__ void load_q(const AttnFp4Params& p, const Group& grp, uint8_t* q_s, float* qc) {
     const int head = threadIdx.x >> 2, part = threadIdx.x & 3;
     const int n = p.d / 8;   // 16-byte chunks of a head: part, part + 4, ... (at most sixteen per thread)
-    const bool in = head < p.h;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)qi * p.h + (in ? head : 0)) * p.d);
+    const bool in = head < grp.heads;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (grp.row0 + (in ? head : 0)) * p.d);
     uint4 v[4 * NM];
     uint32_t mx = 0;
 #pragma unroll
@@ -415,6 +446,8 @@ struct __align__(16) Tail {
     float qc[64];             // per head: softmax scale (log2) over its f16 scaling
     float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
     float lsum[2][4][32];
+    int hvis[2][64];          // [segment parity] per head: its visible rows (kPack)
+    uint32_t nan_tag[2][kRows];   // [tile parity][row]: 1 + the last tile in which it held a NaN (kPack)
     Work work;
     long long scratch[kThreads / 32];
     uint64_t full[2][2];      // [buffer][half of the dims] decoded: one arrival per decoding warp
@@ -442,8 +475,13 @@ __device__ __forceinline__ void zero_padding(int h, int n_cb, int n_m, uint8_t* 
         }
 }
 
-template <int NM, bool kScores>   // d-blocks of 128 dims; whether the scores are kept for the row weights
+// What a kernel does besides: kPlain nothing, kKeeps keeps the scores for the row weights, kPacks takes groups of
+// several queries (and keeps the scores when there is room for them).
+enum Mode { kPlain, kKeeps, kPacks };
+
+template <int NM, Mode kMode>   // d-blocks of 128 dims
 __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Params p) {
+    constexpr bool kPack = kMode == kPacks;
     constexpr int kHalves = (NM + 1) / 2;
     constexpr uint32_t kTile = 2 * NM * kTBlk;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -455,8 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
     Tail* tl = reinterpret_cast<Tail*>(p_s + 2 * kPBuf);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nq = p.B * p.s;
-    const int groups = p.h > 32 ? 2 : 1;       // groups of 32 heads
+    const int nq = p.B * p.groups;
+    const int hp = p.pack * p.h;               // heads of a full group
+    const int sets = hp > 32 ? 2 : 1;          // sets of 32 heads
     volatile int* abort = &tl->abort;
 
     if (warp == 16) {
@@ -470,17 +509,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 mbar_init(&tl->freed[k][h], 1);
             }
             mbar_init(&tl->s_full[k], 1);
-            mbar_init(&tl->p_full[k], 4 * groups);
+            mbar_init(&tl->p_full[k], 4 * sets);
         }
         mbar_init(&tl->q_full, 8);
         tl->abort = 0;
         tl->qk_tile = 0;
         fence_mbar_init();
     }
-    zero_padding(p.h, n_cb, NM, q_s, t_s);
+    if (kPack && tid < 2 * kRows) tl->nan_tag[0][tid] = 0u;
+    zero_padding(hp, n_cb, NM, q_s, t_s);
     fence_proxy_async_smem();
     plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
-              [&](int q) { return (visible_rows(p, q / p.s, q % p.s) + kRows - 1) / kRows; });
+              [&](int q) { return (group_rows(p, q / p.groups, q % p.groups) + kRows - 1) / kRows; });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -493,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         // -------------------------------------------------------------- MMA issue
         // Warp 16 issues the QKs and warp 17 the PVs, each as its operands come: in one warp's order a PV waits for the
         // next tile's QK, that for its decode, and the decode for the buffer of the PV before.
-        const int n_mma = (p.h + 15) / 16 * 16;
+        const int n_mma = (hp + 15) / 16 * 16;
         uint32_t n = 0;
         bool ok = true;   // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -564,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             volatile int* now = &tl->qk_tile;
             bool on = true;
             while (on && walk.next(p, sg)) {
-                const bool asks = sg.q == sg.b * p.s;
+                const bool asks = sg.q == sg.b * p.groups;
                 for (int t = sg.t0; on && t < sg.t1; ++t, ++n) {
                     if (!asks) continue;
                     prefetch_rows(p, sg.b, t * kRows, min((t + 1) * kRows, sg.vis));
@@ -590,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         if (more) load_codes<NM>(p, cur.b, t * kRows, cur.vis, n_cb, codes);
         while (more && !dead) {
             const uint32_t buf = n & 1u;
-            dead = !decode_tile<NM>(t_s + buf * kTile, t * kRows, cur.vis, n_cb, codes, tl->full[buf], [&](int h) {
+            dead = !decode_tile<NM, kPack>(t_s + buf * kTile, t * kRows, cur.vis, n_cb, codes, tl->full[buf], tl->nan_tag[buf],
+                                           n + 1u, [&](int h) {
                 return n < 2 || warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort);
             });
             ++n;
@@ -606,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         const int set = warp >> 2, qd = warp & 3;
         const int row = 16 * qd + (lane >> 2);   // this thread's tile rows: row, row + 8
         const int l4 = lane & 3;                 // its heads: 32 set + 8 g + 2 l4 + {0, 1}
-        const bool active = set < groups;        // this warp's head group has heads
+        const bool active = set < sets;          // this warp's set has heads
         const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
         const uint32_t bar_set = 1u + (uint32_t)set;
         uint32_t n = 0;
@@ -629,17 +670,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 cm[2 * g + 1] = make_float2(v.z, v.w);
             }
         };
-        // left: visible rows from this thread's first one on; tile: of all the queries' (kScores)
-        auto softmax = [&](int left, bool first, int64_t tile) {
+        // vis: rows that the group's last query sees; row0: this thread's first one; tile: of all the groups' (kept scores)
+        int hv[8] = {};   // kPack: rows that each of the thread's heads sees
+        auto softmax = [&](int vis, int row0, bool first, int64_t tile) {
             const uint32_t buf = n & 1u;
             mwait(&tl->s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
-            const bool v0 = left > 0 && !dead, v1 = left > 8 && !dead;
+            const bool v0 = vis > row0 && !dead, v1 = vis > row0 + 8 && !dead;
+            auto sees = [&](int i, int second) {   // the thread's head i its first or second row
+                if (kPack) return hv[i] > row0 + 8 * second && !dead;
+                return second ? v1 : v0;
+            };
             const uint32_t ts = tmem + lane_base + 64u * buf + 32u * (uint32_t)set;
             uint32_t r[16];
             tmem_ld_rows16(ts, r);
             tmem_ld_wait();
-            if (kScores) {
+            if (kPack) {
+                // a NaN row was decoded as 0, so that P = 0 keeps it from the heads that do not see it
+                const bool n0 = tl->nan_tag[buf][row] == n + 1u, n1 = tl->nan_tag[buf][row + 8] == n + 1u;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (n0) r[4 * g] = r[4 * g + 1] = 0x7FFFFFFFu;
+                    if (n1) r[4 * g + 2] = r[4 * g + 3] = 0x7FFFFFFFu;
+                }
+            }
+            if (kMode == kKeeps || (kPack && p.scores)) {
                 float4* sc = reinterpret_cast<float4*>(p.scores) + (tile * 8 + warp) * 128 + lane;
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
@@ -660,18 +715,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             scale();
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                top0 = fmaxf(top0, fmaxf(y[4 * g], y[4 * g + 1]));
-                top1 = fmaxf(top1, fmaxf(y[4 * g + 2], y[4 * g + 3]));
+                if (kPack) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (sees(2 * g + (c & 1), c >> 1)) top0 = fmaxf(top0, y[4 * g + c]);
+                } else {
+                    top0 = fmaxf(top0, fmaxf(y[4 * g], y[4 * g + 1]));
+                    top1 = fmaxf(top1, fmaxf(y[4 * g + 2], y[4 * g + 3]));
+                }
             }
             // the maxima stay unless a visible score passes its head's by 2^8
-            const bool need = !named_bar_and(bar_set, 128, !(first || (v0 && top0 > 8.f) || (v1 && top1 > 8.f)));
+            const bool need = !named_bar_and(bar_set, 128, !(first || ((kPack || v0) && top0 > 8.f) || (v1 && top1 > 8.f)));
             if (need) {
                 float* red = &tl->red[buf][set][qd][0];
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float v = fmaxf(v0 ? y[4 * g + c] : -INFINITY, v1 ? y[4 * g + 2 + c] : -INFINITY);
+                        float v = fmaxf(sees(2 * g + c, 0) ? y[4 * g + c] : -INFINITY,
+                                        sees(2 * g + c, 1) ? y[4 * g + 2 + c] : -INFINITY);
 #pragma unroll
                         for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kWarpFull, v, o));
                         if (lane < 4) red[8 * g + 2 * lane + c] = v;
@@ -716,8 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             uint8_t* prow = p_s + buf * kPBuf + row * 128 + 4 * l4;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const float a0 = v0 ? fast_exp2(y[4 * g]) : 0.f, a1 = v0 ? fast_exp2(y[4 * g + 1]) : 0.f;
-                const float b0 = v1 ? fast_exp2(y[4 * g + 2]) : 0.f, b1 = v1 ? fast_exp2(y[4 * g + 3]) : 0.f;
+                const float a0 = sees(2 * g, 0) ? fast_exp2(y[4 * g]) : 0.f, a1 = sees(2 * g + 1, 0) ? fast_exp2(y[4 * g + 1]) : 0.f;
+                const float b0 = sees(2 * g, 1) ? fast_exp2(y[4 * g + 2]) : 0.f, b1 = sees(2 * g + 1, 1) ? fast_exp2(y[4 * g + 3]) : 0.f;
                 l_thr[2 * g] += a0 + b0;
                 l_thr[2 * g + 1] += a1 + b1;
                 const int at = ((4 * set + g) ^ (row & 7)) << 4;
@@ -730,9 +792,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             if (lane == 0) mbar_arrive(&tl->p_full[buf]);
         };
 
-        // a segment's O^T and sums: the query's output when the segment holds all its tiles, else a partial
-        // (slot >= 0: where)
-        auto epilogue = [&](int q, int slot) {
+        // a segment's O^T and sums: the group's output when the segment holds all its tiles, else a partial
+        // (slot >= 0: where); par: the segment's parity
+        auto epilogue = [&](int q, int slot, int par) {
+            const Group grp = group_of(p, q);
             mwait(&tl->freed[(n - 1) & 1u][kHalves - 1], ((n - 1) >> 1) & 1u);
             tc_fence_after();
 #pragma unroll
@@ -749,18 +812,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             float inv = 0.f, wp = 0.f;
             if (slot >= 0) {
                 if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
-            } else if (hh < p.h) {
+            } else if (kPack && hh < grp.heads && tl->hvis[par][hh] == 0) {
+                // a query that sees no row, next to one that does: what it had
+                const float pl = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) : -INFINITY;
+                wp = pl == -INFINITY ? 0.f : 1.f;
+                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = pl;
+            } else if (hh < grp.heads) {
                 // everything relative to the largest of the running maximum, the sink and prev_lse
-                const float sk = p.sink ? __ldg(p.sink + hh) * kLog2e : -INFINITY;
-                const float pl = p.prev_lse ? __ldg(p.prev_lse + (int64_t)q * p.h + hh) * kLog2e : -INFINITY;
+                const float sk = p.sink ? __ldg(p.sink + (kPack ? hh % p.h : hh)) * kLog2e : -INFINITY;
+                const float pl = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) * kLog2e : -INFINITY;
                 float mx = fmaxf(m_run, fmaxf(sk, pl));
                 if (mx == -INFINITY) mx = 0.f;
-                const float f = m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);
+                const float f = lt == 0.f ? 0.f : m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);   // (inf * 0)
                 const float ep = exp2f(pl - mx);
                 const float den = lt * f + exp2f(sk - mx) + ep;
                 inv = f / den;
                 wp = ep / den;
-                if (p.lse && qd == 0) p.lse[(int64_t)q * p.h + hh] = (mx + log2f(den)) * kLn2;
+                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = (mx + log2f(den)) * kLn2;
             }
             uint16_t* stg = reinterpret_cast<uint16_t*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
             const bool odd = (lane & 1) != 0;
@@ -769,8 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
             auto piece = [&](int k, int j, int64_t& at) {
                 const int c = lane + 32 * j;
                 const int hw = 32 * set + 16 * (k & 1) + (c >> 2), dw = 128 * (k >> 1) + 32 * qd + 8 * (c & 3);
-                at = ((int64_t)q * p.h + hw) * p.d + dw;
-                return k < 2 * NM && hw < p.h && dw < p.d;
+                at = (grp.row0 + hw) * p.d + dw;
+                return k < 2 * NM && hw < grp.heads && dw < p.d;
             };
             const bool joins = p.prev_out != nullptr && slot < 0;
             uint4 pre[2];   // prev_out of the step, loaded a step ahead
@@ -791,11 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set + (uint32_t)h0, r);
                 tmem_ld_wait();
                 if (slot >= 0) {
-                    float* po = p.part_o + ((int64_t)slot * p.h + 32 * set + h0) * p.d + dd;
+                    float* po = p.part_o + ((int64_t)slot * hp + 32 * set + h0) * p.d + dd;
                     if (dd < p.d) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (32 * set + h0 + i < p.h) po[i * p.d] = __uint_as_float(r[i]);
+                            if (32 * set + h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
                     }
                     continue;
                 }
@@ -837,47 +905,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         Walk walk(wk);
         Seg sg;
         int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
+        int par = 0;                           // segment parity
         while (walk.next(p, sg)) {
             // the Q buffer is free: this warp has seen the last S^T of the previous query (a warp whose head
             // group is empty writes no Q)
-            load_q<NM>(p, sg.q, q_s, tl->qc);
+            const Group grp = group_of(p, sg.q);
+            load_q<NM>(p, grp, q_s, tl->qc);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tl->q_full);
+            if (kPack && tid < 64) tl->hvis[par][tid] = head_rows(p, grp, tid);   // (every warp is done with par's last)
             if (tid == 0) {   // what the next segment and this one's end will read, into L2
-                const uint32_t bytes = (uint32_t)(p.h * p.d * 2);
-                if (sg.q + 1 < nq) prefetch_l2_bulk(p.q + (int64_t)(sg.q + 1) * p.h * p.d, bytes);
-                if (p.prev_out) prefetch_l2_bulk(p.prev_out + (int64_t)sg.q * p.h * p.d, bytes);
+                const uint32_t row = (uint32_t)p.d * 2;
+                if (sg.q + 1 < nq) {
+                    const Group nx = group_of(p, sg.q + 1);
+                    prefetch_l2_bulk(p.q + nx.row0 * p.d, (uint32_t)nx.heads * row);
+                }
+                if (p.prev_out) prefetch_l2_bulk(p.prev_out + grp.row0 * p.d, (uint32_t)grp.heads * row);
             }
-            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot);
+            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, par ^ 1);
             named_bar_sync(kBarSoft, 256);     // the staging area is every warp's P^T; qc is complete
             m_run = -INFINITY;
             tl->cm[set][qd][lane] = make_float2(tl->qc[32 * set + lane], 0.f);
             __syncwarp();
             load_cm();
+            if (kPack) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hv[i] = tl->hvis[par][32 * set + 8 * (i >> 1) + 2 * l4 + (i & 1)];
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
             for (int t = sg.t0; t < sg.t1; ++t, ++n)
                 if (active)
-                    softmax(sg.vis - t * kRows - row, t == sg.t0,
-                            kScores ? (int64_t)sg.q * ((p.n_rows + kRows - 1) / kRows) + t : 0);
+                    softmax(sg.vis, t * kRows + row, t == sg.t0,
+                            kMode == kPlain ? 0 : (int64_t)sg.q * ((p.n_rows + kRows - 1) / kRows) + t);
+            par ^= 1;
             pend_q = sg.q;
             pend_slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
         }
-        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot);
+        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, par ^ 1);
 
-        // queries without a visible row
+        // groups without a visible row
         for (int q = blockIdx.x; q < nq; q += gridDim.x) {
-            if (visible_rows(p, q / p.s, q % p.s) > 0) continue;
-            for (int hh = warp; hh < p.h; hh += 8) {
-                const int64_t at = (int64_t)q * p.h + hh;
-                const float pl = p.prev_lse ? p.prev_lse[at] : -INFINITY;
-                if (p.lse && lane == 0) p.lse[at] = pl;
-                for (int k = lane; k < p.d / 8; k += 32) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (pl != -INFINITY) v = reinterpret_cast<const uint4*>(p.prev_out + at * p.d)[k];
-                    reinterpret_cast<uint4*>(p.out + at * p.d)[k] = v;
+            const Group grp = group_of(p, q);
+            if (visible_rows(p, grp.b, min(grp.t0 + p.pack, p.s) - 1) > 0) continue;
+            for (int i = tid; i < grp.heads; i += 256)
+                if (p.lse) p.lse[grp.row0 + i] = p.prev_lse ? p.prev_lse[grp.row0 + i] : -INFINITY;
+            const int chunks = p.d / 8;
+#pragma unroll 4
+            for (int i = tid; i < grp.heads * chunks; i += 256) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (p.prev_out) {
+                    v = reinterpret_cast<const uint4*>(p.prev_out + grp.row0 * p.d)[i];
+                    if (p.prev_lse[grp.row0 + i / chunks] == -INFINITY) v = make_uint4(0, 0, 0, 0);
                 }
+                reinterpret_cast<uint4*>(p.out + grp.row0 * p.d)[i] = v;
             }
         }
     }
@@ -897,10 +979,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
 
 // ------------------------------------------------------------------ joining split queries
 
-// Block (x, head): the split queries that start in CTAs x, x + gridDim.x, ... of the attention kernel.
-// Block (x, head, z) takes dims 4 W z .. 4 W (z + 1) - 1; thread (g, i), g < G, dims 4 (W z + i) + {0..3} of every
-// G-th part, four parts in flight; the groups' sums join in shared memory in a fixed order.  G follows from the
-// parts a query can have: a single long query (152 parts) needs many loads in flight (20 us with G = 8, W = 128),
+// Block (x, head, z): the x-th split query group (there are at most gridDim.x), dims 4 W z .. 4 W (z + 1) - 1; thread
+// (g, i), g < G, dims 4 (W z + i) + {0..3} of every G-th part, four parts in flight; their sums join in shared memory
+// in a fixed order.  G follows from the parts a query can have: a single long query (152 parts) needs many loads in flight (20 us with G = 8, W = 128),
 // thousands of short ones (two parts each) would spend their time starting wide blocks.
 template <int G, int W>
 __global__ void __launch_bounds__(G * W) merge_kernel(const AttnFp4Params p) {
@@ -909,129 +990,130 @@ __global__ void __launch_bounds__(G * W) merge_kernel(const AttnFp4Params p) {
     __shared__ float4 part[G][W];
     const int hh = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     const int g = tid / W, ti = tid % W, i4 = (int)blockIdx.z * W + ti;
-    __shared__ int3 recs[160];   // (query, first CTA, last CTA) of the block's split queries
-    __shared__ int n_recs;
+    __shared__ int3 found;   // (query, first CTA, last CTA)
     griddep_wait();
     griddep_launch_dependents();
-    // one warp reads all of the block's records at once and keeps the real ones (read one after another, and
-    // looked through by every warp, a single query's 152 took 50 and 13 us)
+    // One warp reads all records at once and takes the blockIdx.x-th real one (read one after another, and looked
+    // through by every warp, a single query's 152 took 50 and 13 us; dealt out by the CTA they come from, equal
+    // queries' records all fall to a few blocks).
     if (tid < 32) {
         int2 r[5];
         int cnt = 0;
+        if (lane == 0) found.x = -1;
+        __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 5; ++k) {
-            const int c = (int)blockIdx.x + (lane + 32 * k) * (int)gridDim.x;
-            r[k] = c < p.grid ? __ldcg(p.rec + c) : make_int2(-1, 0);
-        }
+        for (int k = 0; k < 5; ++k) r[k] = lane + 32 * k < p.grid ? __ldcg(p.rec + lane + 32 * k) : make_int2(-1, 0);
 #pragma unroll
         for (int k = 0; k < 5; ++k) {
             const uint32_t real = __ballot_sync(kWarpFull, r[k].x >= 0);
-            if (r[k].x >= 0)
-                recs[cnt + __popc(real & ((1u << lane) - 1u))] =
-                    make_int3(r[k].x, (int)blockIdx.x + (lane + 32 * k) * (int)gridDim.x, r[k].y);
+            if (r[k].x >= 0 && cnt + __popc(real & ((1u << lane) - 1u)) == (int)blockIdx.x)
+                found = make_int3(r[k].x, lane + 32 * k, r[k].y);
             cnt += __popc(real);
         }
-        if (lane == 0) n_recs = cnt;
     }
     __syncthreads();
-    for (int k0 = 0; k0 < n_recs; ++k0) {
-        const int3 rec = recs[k0];
-        const int c = rec.y;
-        const int parts = rec.z - c + 1;   // slots 2c + 1, 2 (c + 1), 2 (c + 2), ...
-        auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
-        const int64_t at = (int64_t)rec.x * p.h + hh;
-        // the partial outputs start loading before their factors are known
-        float4 v[4];
-        const bool in = 4 * i4 < p.d;
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)hh * p.d) + (in ? i4 : 0);
-        const int64_t step = (int64_t)p.h * p.d / 4;
-        auto load = [&](int i) { return __ldcg(src + slot(i < parts ? i : parts - 1) * step); };   // always a part
+    const int3 rec = found;
+    if (rec.x < 0) return;
+    const int c = rec.y;
+    const int parts = rec.z - c + 1;   // slots 2c + 1, 2 (c + 1), 2 (c + 2), ...
+    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+    const Group grp = group_of(p, rec.x);
+    if (hh >= grp.heads) return;
+    const bool seen = p.pack == 1 || head_rows(p, grp, hh) > 0;
+    const int64_t at = grp.row0 + hh;
+    const int hp = p.pack * p.h;
+    // the partial outputs start loading before their factors are known
+    float4 v[4];
+    const bool in = 4 * i4 < p.d;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o + (int64_t)hh * p.d) + (in ? i4 : 0);
+    const int64_t step = (int64_t)hp * p.d / 4;
+    auto load = [&](int i) { return __ldcg(src + slot(i < parts ? i : parts - 1) * step); };   // always a part
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = load(g + k * G);
-        const float sk = p.sink ? __ldg(p.sink + hh) * kLog2e : -INFINITY;
-        const float pl = p.prev_lse ? p.prev_lse[at] * kLog2e : -INFINITY;
-        if (tid < 32) {
-            float2 ml[5];   // parts <= 160
+    for (int k = 0; k < 4; ++k) v[k] = load(g + k * G);
+    const float sk = p.sink && seen ? __ldg(p.sink + hh % p.h) * kLog2e : -INFINITY;
+    const float pl_in = p.prev_lse ? p.prev_lse[at] : -INFINITY, pl = pl_in * kLog2e;
+    if (tid < 32) {
+        float2 ml[5];   // parts <= 160
 #pragma unroll
-            for (int k = 0; k < 5; ++k)
-                ml[k] = lane + 32 * k < parts ? __ldcg(p.part_ml + slot(lane + 32 * k) * 64 + hh) : make_float2(-INFINITY, 0.f);
-            float mx = fmaxf(sk, pl);
+        for (int k = 0; k < 5; ++k)
+            ml[k] = lane + 32 * k < parts ? __ldcg(p.part_ml + slot(lane + 32 * k) * 64 + hh) : make_float2(-INFINITY, 0.f);
+        float mx = fmaxf(sk, pl);
 #pragma unroll
-            for (int k = 0; k < 5; ++k) mx = fmaxf(mx, ml[k].x);
+        for (int k = 0; k < 5; ++k) mx = fmaxf(mx, ml[k].x);
 #pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kWarpFull, mx, o));
-            if (mx == -INFINITY) mx = 0.f;
-            float l = 0.f;
+        for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kWarpFull, mx, o));
+        if (mx == -INFINITY) mx = 0.f;
+        float l = 0.f;
 #pragma unroll
-            for (int k = 0; k < 5; ++k) {
-                if (lane + 32 * k < parts) {
-                    const float f = exp2f((ml[k].x == -INFINITY ? 0.f : ml[k].x) - mx);
-                    fac[lane + 32 * k] = f;
-                    l += ml[k].y * f;
-                }
-            }
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kWarpFull, l, o);
-            const float ep = exp2f(pl - mx);
-            const float den = l + exp2f(sk - mx) + ep;
-            if (lane == 0) {
-                stat[0] = 1.f / den;
-                stat[1] = ep / den;
-                if (p.lse && blockIdx.z == 0) p.lse[at] = (mx + log2f(den)) * kLn2;
+        for (int k = 0; k < 5; ++k) {
+            if (lane + 32 * k < parts) {
+                // a part of which the head sees nothing: not inf * 0
+                const float f = ml[k].y == 0.f ? 0.f : exp2f((ml[k].x == -INFINITY ? 0.f : ml[k].x) - mx);
+                fac[lane + 32 * k] = f;
+                l += ml[k].y * f;
             }
         }
-        __syncthreads();
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = g; i0 < parts; i0 += 4 * G) {
-            float4 w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = load(i0 + (4 + k) * G);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = i0 + k * G;
-                if (i < parts) {
-                    const float f = fac[i];
-                    o.x += f * v[k].x;
-                    o.y += f * v[k].y;
-                    o.z += f * v[k].z;
-                    o.w += f * v[k].w;
-                }
-                v[k] = w[k];
-            }
+        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kWarpFull, l, o);
+        const float ep = exp2f(pl - mx);
+        const float den = l + exp2f(sk - mx) + ep;
+        if (lane == 0) {   // a query that sees no row, next to one that does, keeps what it had
+            stat[0] = seen ? 1.f / den : 0.f;
+            stat[1] = seen ? ep / den : pl == -INFINITY ? 0.f : 1.f;
+            if (p.lse && blockIdx.z == 0) p.lse[at] = seen ? (mx + log2f(den)) * kLn2 : pl_in;
         }
-        part[g][ti] = o;
-        __syncthreads();
-        if (g == 0 && in) {
+    }
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = g; i0 < parts; i0 += 4 * G) {
+        float4 w[4];
 #pragma unroll
-            for (int k = 1; k < G; ++k) {
-                const float4 q = part[k][ti];
-                o.x += q.x;
-                o.y += q.y;
-                o.z += q.z;
-                o.w += q.w;
+        for (int k = 0; k < 4; ++k) w[k] = load(i0 + (4 + k) * G);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = i0 + k * G;
+            if (i < parts) {
+                const float f = fac[i];
+                o.x += f * v[k].x;
+                o.y += f * v[k].y;
+                o.z += f * v[k].z;
+                o.w += f * v[k].w;
             }
-            const float inv = stat[0], wp = stat[1];
-            o.x *= inv;
-            o.y *= inv;
-            o.z *= inv;
-            o.w *= inv;
-            if (wp != 0.f && p.prev_out) {
-                const uint2 pv = *reinterpret_cast<const uint2*>(p.prev_out + at * p.d + 4 * i4);
-                o.x += wp * __uint_as_float(pv.x << 16);
-                o.y += wp * __uint_as_float(pv.x & 0xFFFF0000u);
-                o.z += wp * __uint_as_float(pv.y << 16);
-                o.w += wp * __uint_as_float(pv.y & 0xFFFF0000u);
-            }
-            *reinterpret_cast<uint2*>(p.out + at * p.d + 4 * i4) =
-                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+            v[k] = w[k];
         }
-        __syncthreads();
+    }
+    part[g][ti] = o;
+    __syncthreads();
+    if (g == 0 && in) {
+#pragma unroll
+        for (int k = 1; k < G; ++k) {
+            const float4 q = part[k][ti];
+            o.x += q.x;
+            o.y += q.y;
+            o.z += q.z;
+            o.w += q.w;
+        }
+        const float inv = stat[0], wp = stat[1];
+        o.x *= inv;
+        o.y *= inv;
+        o.z *= inv;
+        o.w *= inv;
+        if (wp != 0.f && p.prev_out) {
+            const uint2 pv = *reinterpret_cast<const uint2*>(p.prev_out + at * p.d + 4 * i4);
+            o.x += wp * __uint_as_float(pv.x << 16);
+            o.y += wp * __uint_as_float(pv.x & 0xFFFF0000u);
+            o.z += wp * __uint_as_float(pv.y << 16);
+            o.w += wp * __uint_as_float(pv.y & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint2*>(p.out + at * p.d + 4 * i4) =
+            make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
     }
 }
 
 // ------------------------------------------------------------------ row weights
 
 struct __align__(16) WTail {
+    int hvis[2][64];                 // [query parity] per head: its visible rows
     float2 cl[2][64];                // [query parity] per head: (softmax scale over the f16 scaling, -lse in log2)
     float qc[64];
     float acc[kWTiles][2][kRows];    // [tile of the chunk][head group][row]
@@ -1081,7 +1163,7 @@ struct WWalk {
     // first tile of the next query (from q on) that sees one of the chunk's; false: none is left
     __device__ __forceinline__ bool query(const AttnFp4Params& p) {
         for (; q < tb; ++q) {
-            const int nt = (visible_rows(p, seq, q) + kRows - 1) / kRows;
+            const int nt = (group_rows(p, seq, q) + kRows - 1) / kRows;
             end = nt < t1 ? nt : t1;
             k = t0;
             if (k < end) return true;
@@ -1102,11 +1184,12 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
     WTail* tl = reinterpret_cast<WTail*>(t_s + 2 * kTile);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int groups = p.h > 32 ? 2 : 1;
+    const int hp = p.pack * p.h, sets = hp > 32 ? 2 : 1;
     volatile int* abort = &tl->abort;
     // this CTA's queries of every sequence, and its piece of the tiles
     const int split = (int)blockIdx.x % p.w_split;
-    const int ta = (int)((long long)split * p.s / p.w_split), tb = (int)((long long)(split + 1) * p.s / p.w_split);
+    const int ta = (int)((long long)split * p.groups / p.w_split);
+    const int tb = (int)((long long)(split + 1) * p.groups / p.w_split);
 
     if (warp == 16) {
         tmem_alloc(&tl->tmem_base, 128);
@@ -1119,13 +1202,13 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                 mbar_init(&tl->freed[k][h], 1);
             }
             mbar_init(&tl->s_full[k], 1);
-            mbar_init(&tl->s_free[k], 4 * groups);
+            mbar_init(&tl->s_free[k], 4 * sets);
         }
         mbar_init(&tl->q_full, 8);
         tl->abort = 0;
         fence_mbar_init();
     }
-    zero_padding(p.h, n_cb, NM, q_s, t_s);
+    zero_padding(hp, n_cb, NM, q_s, t_s);
     fence_proxy_async_smem();
     plan_work(p.B, (int)blockIdx.x / p.w_split, (int)gridDim.x / p.w_split, tl->scratch, &tl->work,
               [&](int b) { return (visible_rows(p, b, p.s - 1) + kRows - 1) / kRows; });
@@ -1138,7 +1221,7 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
 
     if (warp >= 16) {
         regs_down<kRegsMma>();
-        const uint32_t idesc_qk = idesc_f16_f32(kRows, (p.h + 15) / 16 * 16, false, false);
+        const uint32_t idesc_qk = idesc_f16_f32(kRows, (hp + 15) / 16 * 16, false, false);
         const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
         uint32_t n = 0, qn = 0;
         int have = -1;
@@ -1150,10 +1233,10 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         };
         while (ok && w.chunk(p)) {
             for (w.q = ta; ok && w.query(p); ++w.q) {
-                if (have != w.seq * p.s + w.q) {   // another query: its Q
+                if (have != w.seq * p.groups + w.q) {   // another query: its Q
                     if (!wait(&tl->q_full, qn & 1u)) break;
                     ++qn;
-                    have = w.seq * p.s + w.q;
+                    have = w.seq * p.groups + w.q;
                 }
                 for (int k = w.k; k < w.end && ok; ++k, ++n) {
                     const uint32_t buf = n & 1u;
@@ -1185,7 +1268,8 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
             if (more) load_codes<NM>(p, w.seq, w.k * kRows, w.vis_all, n_cb, codes);
             while (more && !dead) {
                 const uint32_t buf = n & 1u;
-                dead = !decode_tile<NM>(t_s + buf * kTile, w.k * kRows, w.vis_all, n_cb, codes, tl->full[buf], [&](int h) {
+                dead = !decode_tile<NM, false>(t_s + buf * kTile, w.k * kRows, w.vis_all, n_cb, codes, tl->full[buf], nullptr, 0u,
+                                               [&](int h) {
                     return n < 2 || warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort);
                 });
                 ++n;
@@ -1200,7 +1284,7 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
         regs_up<kRegsSoft>();
         const int set = warp >> 2, qd = warp & 3;
         const int row = 16 * qd + (lane >> 2), l4 = lane & 3;
-        const bool active = set < groups;
+        const bool active = set < sets;
         const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
         uint32_t n = 0, qn = 0;
         int have = -1;
@@ -1209,18 +1293,20 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
             for (int i = tid; i < (w.t1 - w.t0) * 2 * kRows; i += 256) (&tl->acc[0][0][0])[i] = 0.f;
             named_bar_sync(kBarSoft, 256);
             for (w.q = ta; w.query(p); ++w.q) {
-                const int qi = w.seq * p.s + w.q, vis = visible_rows(p, w.seq, w.q);
+                const int qi = w.seq * p.groups + w.q;
                 if (have != qi) {
                     // the Q buffer is free: this warp has seen the previous query's last S^T
                     qn ^= 1u;
-                    load_q<NM>(p, qi, q_s, tl->qc);
+                    const Group grp = group_of(p, qi);
+                    load_q<NM>(p, grp, q_s, tl->qc);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tl->q_full);
                     if (lane < 8) {   // the warp's own eight heads
                         const int hd = 8 * warp + lane;
                         tl->cl[qn][hd] =
-                            make_float2(tl->qc[hd], hd < p.h ? -__ldcg(p.lse + (int64_t)qi * p.h + hd) * kLog2e : 0.f);
+                            make_float2(tl->qc[hd], hd < grp.heads ? -__ldcg(p.lse + grp.row0 + hd) * kLog2e : 0.f);
+                        tl->hvis[qn][hd] = head_rows(p, grp, hd);
                     }
                     named_bar_sync(kBarSoft, 256);
                     have = qi;
@@ -1246,14 +1332,10 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                         const float a1 = fast_exp2(fmaf(__uint_as_float(r[4 * g + 1]), v.z, v.w));
                         const float b0 = fast_exp2(fmaf(__uint_as_float(r[4 * g + 2]), v.x, v.y));
                         const float b1 = fast_exp2(fmaf(__uint_as_float(r[4 * g + 3]), v.z, v.w));
-                        if (hd < p.h) {
-                            a += a0;
-                            b += b0;
-                        }
-                        if (hd + 1 < p.h) {
-                            a += a1;
-                            b += b1;
-                        }
+                        const int2 hv = *reinterpret_cast<const int2*>(&tl->hvis[qn][hd]);
+                        const int j = k * kRows + row;
+                        a += (hv.x > j ? a0 : 0.f) + (hv.y > j ? a1 : 0.f);
+                        b += (hv.x > j + 8 ? b0 : 0.f) + (hv.y > j + 8 ? b1 : 0.f);
                     }
 #pragma unroll
                     for (int o = 1; o <= 2; o <<= 1) {
@@ -1261,8 +1343,7 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
                         b += __shfl_xor_sync(kWarpFull, b, o);
                     }
                     if (l4 < 2 && !dead) {   // lane 0 of the four: the first row, lane 1: the second
-                        const int rr = row + 8 * l4;
-                        if (k * kRows + rr < vis) tl->acc[k - w.t0][set][rr] += l4 ? b : a;
+                        tl->acc[k - w.t0][set][row + 8 * l4] += l4 ? b : a;
                     }
                 }
             }
@@ -1293,13 +1374,14 @@ __global__ void __launch_bounds__(kThreads, 1) row_weight_kernel(const AttnFp4Pa
 }
 
 // Row weights from the kept scores (in units of log2, as the softmax threads held them): block (x, b) takes `per` tiles
-// of sequence b and adds each one's queries in order.  Per score 4 bytes are read and one 2^x taken.
+// of sequence b and adds each one's query groups in order.  Per score 4 bytes are read and one 2^x taken.
 __global__ void __launch_bounds__(256, 6) row_weight_scores_kernel(const AttnFp4Params p, int per) {
     __shared__ float part[2][kRows];
+    __shared__ int hvis[kScoreQueries][64];    // [group] per head: its visible rows
     __shared__ float lse[kScoreQueries][64];   // in log2; read once per block: every block of a sequence wants the same
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int set = warp >> 2, row = 16 * (warp & 3) + (lane >> 2), l4 = lane & 3;
-    const bool active = 32 * set < p.h;
+    const bool active = 32 * set < p.pack * p.h;
     const int tiles = (p.n_rows + kRows - 1) / kRows;
     griddep_wait();
     for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
@@ -1309,47 +1391,40 @@ __global__ void __launch_bounds__(256, 6) row_weight_scores_kernel(const AttnFp4
         if (t >= end) continue;
         float4 v[4];
         auto load = [&](int tt, int kk) {
-            const int64_t q = (int64_t)b * p.s + kk;
+            const int64_t q = (int64_t)b * p.groups + kk;
             const float4* sc = reinterpret_cast<const float4*>(p.scores) + ((q * tiles + tt) * 8 + warp) * 128 + lane;
 #pragma unroll
             for (int g = 0; g < 4; ++g) v[g] = __ldcs(sc + 32 * g);
         };
-        // the queries see ever more rows: those from the first one on that sees the tile's first row
+        // the groups see ever more rows: those from the first one on that sees the tile's first row
         auto first = [&](int tt, int kk) {
-            while (visible_rows(p, b, kk) <= tt * kRows) ++kk;
+            while (group_rows(p, b, kk) <= tt * kRows) ++kk;
             return kk;
         };
         int k0 = first(t, 0), k = k0;
         if (active) load(t, k);
-        for (int i = tid; i < p.s * 64; i += 256) {
+        for (int i = tid; i < p.groups * 64; i += 256) {
             const int hd = i & 63;
-            lse[i >> 6][hd] = hd < p.h ? __ldcg(p.lse + ((int64_t)b * p.s + (i >> 6)) * p.h + hd) * kLog2e : 0.f;
+            const Group grp = group_of(p, b * p.groups + (i >> 6));
+            lse[i >> 6][hd] = hd < grp.heads ? __ldcg(p.lse + grp.row0 + hd) * kLog2e : 0.f;
+            hvis[i >> 6][hd] = head_rows(p, grp, hd);
         }
         __syncthreads();
         while (t < end) {
             float sum0 = 0.f, sum1 = 0.f;
             const int k_next = t + 1 < end ? first(t + 1, k0) : 0;
             if (active)
-                for (k = k0; k < p.s; ++k) {
-                    const int vis = visible_rows(p, b, k) - t * kRows;
-                    float a = 0.f, c = 0.f;
+                for (k = k0; k < p.groups; ++k) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const int hd = 32 * set + 8 * g + 2 * l4;
+                        const int hd = 32 * set + 8 * g + 2 * l4, j = t * kRows + row;
                         const float2 l = *reinterpret_cast<const float2*>(&lse[k][hd]);
-                        if (hd < p.h) {
-                            a += fast_exp2(v[g].x - l.x);
-                            c += fast_exp2(v[g].z - l.x);
-                        }
-                        if (hd + 1 < p.h) {
-                            a += fast_exp2(v[g].y - l.y);
-                            c += fast_exp2(v[g].w - l.y);
-                        }
+                        const int2 hv = *reinterpret_cast<const int2*>(&hvis[k][hd]);
+                        sum0 += (hv.x > j ? fast_exp2(v[g].x - l.x) : 0.f) + (hv.y > j ? fast_exp2(v[g].y - l.y) : 0.f);
+                        sum1 += (hv.x > j + 8 ? fast_exp2(v[g].z - l.x) : 0.f) + (hv.y > j + 8 ? fast_exp2(v[g].w - l.y) : 0.f);
                     }
-                    if (k + 1 < p.s) load(t, k + 1);
+                    if (k + 1 < p.groups) load(t, k + 1);
                     else if (t + 1 < end) load(t + 1, k_next);
-                    if (row < vis) sum0 += a;
-                    if (row + 8 < vis) sum1 += c;
                 }
 #pragma unroll
             for (int o = 1; o <= 2; o <<= 1) {
@@ -1401,43 +1476,47 @@ cudaError_t launch_after(void (*kernel)(T...), dim3 grid, int threads, size_t sm
 
 }  // namespace
 
-void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid, int* w_split) {
+AttnFp4Plan attn_fp4_plan(int B, int s, int h, int n_rows, int num_sms) {
+    AttnFp4Plan l;
+    // Few heads: as many queries of a sequence as fill the 64 rows of Q share a tile, which costs the same for any number
+    // of heads (2048 x 16 heads over 2048 rows 659 -> 251 us, 131,072 queries of one head over 20 rows 3853 -> 94).
+    l.pack = h <= 32 ? 64 / h : 1;
+    if (l.pack > s) l.pack = s;
+    const int groups = l.groups = (s + l.pack - 1) / l.pack;
     const int64_t tiles = ((int64_t)n_rows + kRows - 1) / kRows;
     const int64_t all = tiles * B;                                   // row tiles at most
-    const int64_t list = all * s > 0 ? all * s : 1;
-    *grid = (int)(list < num_sms ? list : num_sms);
+    const int64_t list = all * groups > 0 ? all * groups : 1;
+    l.grid = (int)(list < num_sms ? list : num_sms);
     // Row weights: loading a query costs as much as two of its tiles, so a CTA takes about kWTiles tiles of each and
     // the CTAs that this leaves over take other queries (never fewer with more SMs: the workspace counts on it).
     int64_t split = all > 0 ? num_sms * kWTiles / all : 1;
-    const int64_t most = s < num_sms ? s : num_sms;
+    const int64_t most = groups < num_sms ? groups : num_sms;
     split = split > most ? most : split < 1 ? 1 : split;
-    if (s > 0) split = (s + (s + split - 1) / split - 1) / ((s + split - 1) / split);   // same share with fewer CTAs
-    *w_split = (int)split;
+    const int64_t share = (groups + split - 1) / split;
+    split = (groups + share - 1) / share;                            // the same share with fewer CTAs
+    l.w_split = (int)split;
     const int64_t per = num_sms / split;
-    *w_grid = (int)(split * (all < per ? (all > 0 ? all : 1) : per));
-}
-
-// Keeping the scores (256 bytes a row, next to the 288 of its codes) costs less than computing them again: row weights
-// of 32 x 1, 16 x 2 and 4 x 8 queries over 16384 rows 42, 42 and 38 us, computed again 92, 90 and 83; of 8 queries over
-// 1024 rows 7 and 9 us.  Many queries would ask for too large a workspace and, with few rows, for too few blocks.
-size_t attn_fp4_score_bytes(int B, int s, int n_rows) {
-    const int64_t tiles = ((int64_t)n_rows + kRows - 1) / kRows;
-    if (s > kScoreQueries || tiles * s > kScoreTiles / B) return 0;
-    return (size_t)(tiles * s * B) * kRows * 64 * sizeof(float);
+    l.w_grid = (int)(split * (all < per ? (all > 0 ? all : 1) : per));
+    // Keeping the scores (256 bytes a row, next to the 288 of its codes) costs less than computing them again: row
+    // weights of 32 x 1, 16 x 2 and 4 x 8 queries over 16384 rows 42, 42 and 38 us, computed again 92, 90 and 83; of 8
+    // queries over 1024 rows 7 and 9 us.  Many queries would ask for too large a workspace and, with few rows, for too
+    // few blocks.
+    l.score_bytes = groups > kScoreQueries || tiles * groups > kScoreTiles / B ? 0 : (size_t)(tiles * groups * B) * kRows * 64 * 4;
+    return l;
 }
 
 namespace {
 template <int NM>
 cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
-    const int nq = p.B * p.s;
+    const int nq = p.B * p.groups;
     size_t smem = attn_smem(p.d);
-    auto* kernel = p.scores ? attn_fp4_kernel<NM, true> : attn_fp4_kernel<NM, false>;
+    auto* kernel = p.pack > 1 ? attn_fp4_kernel<NM, kPacks> : p.scores ? attn_fp4_kernel<NM, kKeeps> : attn_fp4_kernel<NM, kPlain>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<p.grid, kThreads, smem, stream>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
-    const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)p.h;
+    const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
     e = parts > 16  ? launch_after(merge_kernel<16, 32>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
         : parts > 4 ? launch_after(merge_kernel<2, 128>, dim3(mx, mh), 256, 0, stream, p)
                     : launch_after(merge_kernel<1, 128>, dim3(mx, mh), 128, 0, stream, p);

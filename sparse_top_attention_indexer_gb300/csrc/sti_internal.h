@@ -212,17 +212,20 @@ struct AttnFp4Params {
     uint32_t* status;
     int grid;                   // CTAs of the attention kernel
     int2* rec;                  // [grid]: the split query that starts in a CTA and its last CTA, or {-1, 0}
-    float* part_o;              // [2 * grid][h][d] unnormalised partial outputs
+    float* part_o;              // [2 * grid][pack * h][d] unnormalised partial outputs
     float2* part_ml;            // [2 * grid][64] running maximum (log2) and sum
-    int w_split;                // row weights: query splits (partial sums in w_part when > 1)
+    int pack, groups;           // queries per group, groups per sequence
+    int w_split;                // row weights: splits of the groups (partial sums in w_part when > 1)
     int w_grid;                 // row weights: CTAs, a multiple of w_split
     float* w_part;              // [w_split][B][n_rows]
-    float* scores;              // [B * s][tiles][8 warps][4][32 lanes][4]: kept for the row weights, or null
+    float* scores;              // [B * groups][tiles][8 warps][4][32 lanes][4]: kept for the row weights, or null
 };
-// whether a call with row weights keeps its scores, and their size
-size_t attn_fp4_score_bytes(int B, int s, int n_rows);
-// CTAs of the attention kernel, of the row-weight kernel, and its query splits
-void attn_fp4_plan(int B, int s, int n_rows, int num_sms, int* grid, int* w_grid, int* w_split);
+struct AttnFp4Plan {
+    int pack, groups;           // as in AttnFp4Params
+    int grid, w_grid, w_split;  // CTAs of the attention kernel, of the row-weight kernel, and its splits
+    size_t score_bytes;         // of the scores that a call with row weights keeps (0: it does not)
+};
+AttnFp4Plan attn_fp4_plan(int B, int s, int h, int n_rows, int num_sms);
 cudaError_t launch_attn_fp4(const AttnFp4Params& p, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device properties

@@ -88,6 +88,14 @@ ATTEND = {
     "chunk": (2, 40, 64, 512, 400, [1200, 700], 4, None, True, True, True),
     "no_rows": (2, 3, 8, 64, 0, [5, 9], 1, None, True, True, False),
     "nothing_at_all": (2, 2, 8, 64, 0, [5, 9], 1, None, True, False, False),
+    # few heads, several queries: groups of queries share their tiles
+    "packed_partial_mixed": (2, 7, 20, 512, 300, [30, 2], 4, None, True, True, True),
+    "packed_mixed_no_prev": (3, 9, 8, 128, 90, [0, 2, 500], 4, [0, 0, 130], True, False, True),
+    "packed_split": (1, 5, 12, 256, 5000, [4990], 1, None, True, True, True),
+    "packed_split_pairs": (1, 9, 32, 320, 700, [690], 1, None, False, False, True),
+    "packed_kept_scores": (2, 70, 5, 64, 200, [100, 3], 2, None, True, False, True),
+    "packed_two_passes": (2, 200, 3, 192, 700, [400, 0], 1, None, True, True, True),
+    "packed_one_head": (3, 300, 1, 64, 4, [0, 5, 1], 4, None, True, True, True),
 }
 
 
@@ -200,6 +208,54 @@ def test_attend_nan_row_reaches_only_its_viewers(sti):
     assert torch.isnan(out[0, sees]).all() and torch.isnan(lse[0, sees]).all()
     assert (out[0, ~sees] == clean[0, ~sees]).all() and (out[1] == clean[1]).all()
     assert not torch.isnan(w[1]).any()
+
+
+@gpu
+@pytest.mark.parametrize("name, t", [("packed_split", 1), ("packed_split", 3), ("packed_two_passes", 100),
+                                     ("packed_kept_scores", 31), ("packed_partial_mixed", 5)])
+def test_attend_nan_row_in_a_group_of_queries(sti, name, t):
+    """Queries that share a tile: a NaN row is NaN for those that see it only, in the weights too."""
+    import torch
+
+    a = make_attend(name)
+    b, s, ratio = *a["q"].shape[:2], a["ratio"]
+    vis = (a["start_pos"].astype(np.int64)[:, None] + np.arange(s) + 1) // ratio
+    clean, _, _ = attend(sti, dict(a))
+    bad = vis[0, t] - 1
+    a["scales"][0, bad, 0] |= 0x7F
+    out, lse, w = attend(sti, a)
+    sees = torch.tensor(vis[0] > bad, device="cuda")
+    assert sees.any() and not sees.all()
+    assert torch.isnan(out[0, sees]).all() and torch.isnan(lse[0, sees]).all()
+    assert (out[0, ~sees] == clean[0, ~sees]).all() and not torch.isnan(lse[0, ~sees]).any()
+    seen = torch.arange(w.shape[1], device="cuda") < int(vis[0].max())
+    assert (torch.isnan(w[0]) == seen).all()
+    if b > 1:
+        assert (out[1:] == clean[1:]).all() and not torch.isnan(w[1:]).any()
+
+
+@gpu
+@pytest.mark.parametrize("s, h", [(5, 12), (1, 64)])
+def test_attend_scores_far_below_zero(sti, s, h):
+    """Every row is all ones and every score -256 (e^256 is infinite in fp32): the average of a split query is the
+    row, also for heads that see nothing of a part."""
+    import torch
+
+    d, rows = 256, 5000
+    q = torch.full((1, s, h, d), -1.0, device="cuda", dtype=torch.bfloat16)
+    codes = torch.full((1, rows, d // 2), 0x22, device="cuda", dtype=torch.uint8)
+    scales = torch.full((1, rows, d // 16), 0x38, device="cuda", dtype=torch.uint8)
+    lse = torch.empty(1, s, h, device="cuda")
+    w = torch.zeros(1, rows, device="cuda")
+    start = torch.tensor([4990], device="cuda", dtype=torch.int32)
+    out = sti.attn_fp4kv(q, codes, scales, start, 1, 1.0, lse=lse, row_weight=w)
+    assert (out == 1).all()
+    n = 4991.0 + np.arange(s)
+    # lse: fp32 sums and logarithms next to 256, in units of 2^-16
+    np.testing.assert_allclose(lse.cpu().numpy()[0], np.repeat((np.log(n) - 256)[:, None], h, 1), atol=2.0 ** -13)
+    # e^(s - lse): the error of lse and of s in log2 units (2^-15), one 2^x
+    want = h * (np.arange(rows)[None] < n[:, None]).astype(float).T @ (1 / n)
+    np.testing.assert_allclose(w.cpu().numpy()[0], want, rtol=2.0 ** -12)
 
 
 @gpu
