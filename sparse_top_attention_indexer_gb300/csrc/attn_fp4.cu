@@ -18,8 +18,11 @@
 //   * warps 0..7 load Q, run the online softmax (two sets of 32 heads; the running maxima move only when a
 //     score passes them by 2^8) and write the outputs.
 // With 512 dims, Q (64 KB), two tiles of 64 rows (128 KB) and two P^T (16 KB) fill shared memory.  One tile of
-// 128 rows instead would halve the QK's MMAs (one of M = 64 costs as much as one of M = 128), but leaves
+// 128 rows instead would take a quarter off the QK's operand traffic (48 cycles for M = 128, 32 for M = 64), but leaves
 // decode, QK, softmax and PV of a tile to run one after another: 8,400 cycles per 128 rows.
+// Bound by shared memory: of a tile at 128 B a cycle, QK 1024 cycles, PV 768, the decoded stores 512 and P^T, together
+// 2430.  2048 queries over up to 2048 rows: 2740 cycles a tile, 767 us; one query each over 32 x 16384 rows, where the
+// codes come from HBM: 3500 cycles, 95 us, and the merge 12.  QK and PV issued by one warp in turn: 832 and 112 us.
 //
 // f16 operands: an E2M1 value (2 significant bits) times an E4M3 value (4) is exact in f16 (at most 6
 // significant bits, magnitudes 2^-10 .. 2688), so the tile is exact.  Q is bf16: each head's values are

@@ -15,8 +15,9 @@
 // 12 bits (2^-12 relative), which returns the exact border where x / s is one and moves nothing across
 // a border otherwise; the hardware's conversion then breaks the tie to the even code.
 //
-// Bound by HBM: 2 bytes read and 0.56 (0.53) written per element.  Measured (perf/operators.py's sizes):
-// see the table of the design notes.
+// Reads 2 bytes and writes 0.56 (0.53) per element.  65,536 rows of 512: 19.2 us, 4.5 TB/s of the 6.8 that a copy
+// reaches; without the quantising arithmetic the same accesses take 14.2 us, so the arithmetic of the ten or so
+// instructions per element bounds it.  Two units per thread keep enough loads in flight (one: 25 us).
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
