@@ -423,9 +423,10 @@ sti_status sti_kv_append_fp4(const uint16_t *x, int64_t x_bstride, const int32_t
  * Two kernels, one or two more with row_weight.
  * Supported: 1 <= h <= 64, d a multiple of 64 up to 512; q, out, prev_out, codes 16-byte aligned and
  * codes_bstride a multiple of 16, scales 4-byte aligned and scales_bstride a multiple of 4, both strides
- * covering n_rows rows.  ws: sti_attn_fp4kv_workspace_size() bytes; for up to 8 queries a sequence they
- * include room for the scores that row_weight is summed from, 256 bytes per query and row, up to 256 MB
- * (beyond, and with more queries, the scores are computed a second time).
+ * covering n_rows rows.  ws: sti_attn_fp4kv_workspace_size() bytes; for up to 8
+ * queries a sequence (of few heads: 8 times the queries whose heads together number 64) they include room for
+ * the scores that row_weight is summed from, 256 bytes per row and query (or such a group of queries), up
+ * to 256 MB; beyond, the scores are computed a second time.
  */
 size_t sti_attn_fp4kv_workspace_size(int b, int seqlen, int h, int d, int n_rows);
 sti_status sti_attn_fp4kv(const uint16_t *q, const uint8_t *codes, int64_t codes_bstride, const uint8_t *scales,

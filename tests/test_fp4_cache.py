@@ -374,6 +374,103 @@ def test_attend_repeats_and_graph(sti):
 
 
 @gpu
+def test_attend_two_streams_and_graphs_that_share_a_workspace(sti):
+    """Two streams, each with its workspace, at the same time; then two graphs with one workspace, in turn."""
+    import torch
+
+    names = ("long_split", "packed_two_passes")
+    cases = [make_attend(n) for n in names]
+    want = [[x.clone() for x in attend(sti, a)] for a in cases]
+
+    def call(a, ws, lse, w):
+        return lambda: sti.attn_fp4kv(to_dev_q[id(a)], *dev[id(a)], a["ratio"], a["scale"], lse=lse, row_weight=w, ws=ws, **kws[id(a)])
+
+    to_dev_q = {id(a): to_dev(a["q"]) for a in cases}
+    dev = {id(a): (to_dev_any(a["codes"]), to_dev_any(a["scales"]), to_dev_any(a["start_pos"])) for a in cases}
+    kws = {id(a): dict(attn_sink=to_dev_any(a["sink"]), prev_out=to_dev(a["prev_out"]), prev_lse=to_dev_any(a["prev_lse"]))
+           for a in cases}
+    sizes = [sti.attn_fp4kv_workspace_size(*a["q"].shape, a["codes"].shape[1]) for a in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    own = [sti.workspace(n) for n in sizes]
+    shared = sti.workspace(max(sizes))
+    lses = [torch.empty(a["q"].shape[:3], device="cuda") for a in cases]
+    ws_ = [to_dev_any(a["w0"]) for a in cases]
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for rep in range(8):
+        for w, a in zip(ws_, cases):
+            w.copy_(to_dev_any(a["w0"]))
+        torch.cuda.synchronize()
+        for i, a in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                outs[i] = call(a, own[i], lses[i], ws_[i])()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for x, y in zip(want[i], (outs[i], lses[i], ws_[i])):
+                assert (x == y).all()
+    graphs = []
+    for i, a in enumerate(cases):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs[i] = call(a, shared, lses[i], ws_[i])()
+        graphs.append(g)
+    for rep in range(4):
+        for i, a in enumerate(cases):
+            ws_[i].copy_(to_dev_any(a["w0"]))
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for x, y in zip(want[i], (outs[i], lses[i], ws_[i])):
+                assert (x == y).all()
+
+
+@gpu
+@pytest.mark.parametrize("budget", [100, 9000])
+def test_steps_captured_and_replayed(sti, budget):
+    """A decode step of a full cache (append, attend with row weights in a slice, evict) captured once and replayed
+    leaves the same cache, bit for bit, as the calls made one by one."""
+    import torch
+
+    b, h, d, steps = 2, 24, 128, 12
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    rows = budget + 2
+    xs = torch.randn(steps, b, 1, d, generator=gen, device="cuda").bfloat16()
+    qs = torch.randn(steps, b, 1, h, d, generator=gen, device="cuda").bfloat16()
+
+    def fresh():
+        g = torch.Generator(device="cuda").manual_seed(8)
+        return dict(codes=torch.randint(0, 256, (b, rows, d // 2), generator=g, device="cuda", dtype=torch.uint8),
+                    scales=torch.randint(40, 60, (b, rows, d // 16), generator=g, device="cuda", dtype=torch.uint8),
+                    pos=torch.arange(rows, device="cuda", dtype=torch.int32).repeat(b, 1),
+                    weight=torch.rand(b, rows + 6, generator=g, device="cuda")[:, :rows],
+                    start=torch.tensor([budget, budget - 5], device="cuda", dtype=torch.int32),
+                    dropped=torch.zeros(b, device="cuda", dtype=torch.int32))
+
+    def step(c, x, q):
+        sti.kv_append_fp4(x, c["start"], 1, 1, c["codes"], c["scales"], dropped=c["dropped"], row_pos=c["pos"],
+                          row_weight=c["weight"])
+        out = sti.attn_fp4kv(q, c["codes"], c["scales"], c["start"], 1, d ** -0.5, dropped=c["dropped"], row_weight=c["weight"])
+        sti.kv_evict(c["weight"], c["pos"], c["start"], 1, 1, c["dropped"], budget, 4, 8, [c["codes"], c["scales"]])
+        c["start"] += 1
+        return out
+
+    one, two = fresh(), fresh()
+    want = [step(one, xs[i], qs[i]) for i in range(steps)]
+    x, q = torch.zeros_like(xs[0]), torch.zeros_like(qs[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(two, x, q)
+    for i in range(steps):
+        x.copy_(xs[i])
+        q.copy_(qs[i])
+        g.replay()
+        assert (out == want[i]).all()
+    for k in one:
+        assert (one[k] == two[k]).all(), k
+    assert one["dropped"].tolist() == [steps, steps - 5]
+
+
+@gpu
 def test_attend_matches_sparse_attention(sti):
     """Listing every visible row in sti_sparse_attn_sink_fp4kv gives the same attention (both round P: 2^-8 for
     its bf16, 2^-11 here, and the output 2^-8 each; |rows| <= 6 here and the weights add up to at most 1)."""
