@@ -1491,8 +1491,9 @@ AttnFp4Plan attn_fp4_plan(int B, int s, int h, int n_rows, int num_sms) {
     const int64_t list = all * groups > 0 ? all * groups : 1;
     l.grid = (int)(list < num_sms ? list : num_sms);
     // Row weights: loading a query costs as much as two of its tiles, so a CTA takes about kWTiles tiles of each and
-    // the CTAs that this leaves over take other queries (never fewer with more SMs: the workspace counts on it).
-    int64_t split = all > 0 ? num_sms * kWTiles / all : 1;
+    // the CTAs that this leaves over take other queries (never fewer with more SMs: the workspace counts on it); with
+    // few tiles every CTA takes them all.
+    int64_t split = all >= 2 * kWTiles ? num_sms * kWTiles / all : num_sms;
     const int64_t most = groups < num_sms ? groups : num_sms;
     split = split > most ? most : split < 1 ? 1 : split;
     const int64_t share = (groups + split - 1) / split;
