@@ -440,7 +440,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float bf16_f(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
 // ------------------------------------------------------------------ attention
 
@@ -796,9 +795,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         };
 
         // a segment's O^T and sums: the group's output when the segment holds all its tiles, else a partial
-        // (slot >= 0: where); par: the segment's parity
-        auto epilogue = [&](int q, int slot, int par) {
+        // (slot >= 0: where); par: the segment's parity; sink, prev_lse: of head 32 set + lane
+        auto epilogue = [&](int q, int slot, int par, float sink, float prev_lse) {
             const Group grp = group_of(p, q);
+            // 16 heads x 32 dims of this warp at a time: k / 2 the d-block, heads 32 set + 16 (k & 1) ...
+            // Pieces of 8 dims, two per lane: piece c = lane + 32 j is head c / 4, dims 8 (c % 4) ...
+            auto piece = [&](int k, int j, int64_t& at) {
+                const int c = lane + 32 * j;
+                const int hw = 32 * set + 16 * (k & 1) + (c >> 2), dw = 128 * (k >> 1) + 32 * qd + 8 * (c & 3);
+                at = (grp.row0 + hw) * p.d + dw;
+                return k < 2 * NM && hw < grp.heads && dw < p.d;
+            };
+            const bool joins = p.prev_out != nullptr && slot < 0;
+            uint4 pre[2][2];   // [k & 1]: prev_out, loaded two steps ahead
+            auto load_prev = [&](int k, uint4* v) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    int64_t at;
+                    v[j] = make_uint4(0, 0, 0, 0);
+                    if (piece(k, j, at)) v[j] = *reinterpret_cast<const uint4*>(p.prev_out + at);
+                }
+            };
+            if (joins) {
+                load_prev(0, pre[0]);
+                load_prev(1, pre[1]);
+            }
             mwait(&tl->freed[(n - 1) & 1u][kHalves - 1], ((n - 1) >> 1) & 1u);
             tc_fence_after();
 #pragma unroll
@@ -817,13 +838,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
             } else if (kPack && hh < grp.heads && tl->hvis[par][hh] == 0) {
                 // a query that sees no row, next to one that does: what it had
-                const float pl = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) : -INFINITY;
-                wp = pl == -INFINITY ? 0.f : 1.f;
-                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = pl;
+                wp = prev_lse == -INFINITY ? 0.f : 1.f;
+                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = prev_lse;
             } else if (hh < grp.heads) {
                 // everything relative to the largest of the running maximum, the sink and prev_lse
-                const float sk = p.sink ? __ldg(p.sink + (kPack ? hh % p.h : hh)) * kLog2e : -INFINITY;
-                const float pl = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) * kLog2e : -INFINITY;
+                const float sk = sink * kLog2e, pl = prev_lse * kLog2e;
                 float mx = fmaxf(m_run, fmaxf(sk, pl));
                 if (mx == -INFINITY) mx = 0.f;
                 const float f = lt == 0.f ? 0.f : m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);   // (inf * 0)
@@ -833,81 +852,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 wp = ep / den;
                 if (p.lse && qd == 0) p.lse[grp.row0 + hh] = (mx + log2f(den)) * kLn2;
             }
-            uint16_t* stg = reinterpret_cast<uint16_t*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
-            const bool odd = (lane & 1) != 0;
-            // 16 heads x 32 dims of this warp at a time: k / 2 the d-block, heads 32 set + 16 (k & 1) ...
-            // Pieces of 8 dims, two per lane: piece c = lane + 32 j is head c / 4, dims 8 (c % 4) ...
-            auto piece = [&](int k, int j, int64_t& at) {
-                const int c = lane + 32 * j;
-                const int hw = 32 * set + 16 * (k & 1) + (c >> 2), dw = 128 * (k >> 1) + 32 * qd + 8 * (c & 3);
-                at = (grp.row0 + hw) * p.d + dw;
-                return k < 2 * NM && hw < grp.heads && dw < p.d;
-            };
-            const bool joins = p.prev_out != nullptr && slot < 0;
-            uint4 pre[2];   // prev_out of the step, loaded a step ahead
-            auto load_prev = [&](int k) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    int64_t at;
-                    pre[j] = make_uint4(0, 0, 0, 0);
-                    if (piece(k, j, at)) pre[j] = *reinterpret_cast<const uint4*>(p.prev_out + at);
-                }
-            };
-            if (joins) load_prev(0);
+            // The steps turn O^T over through shared memory, in fp32: lanes hold dims, the pieces are a head's.  The
+            // heads' factors take the place of (c, -m), which the next segment sets anew.
+            float* stg = reinterpret_cast<float*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
+            float2* fac = &tl->cm[set][qd][0];
+            fac[lane] = make_float2(inv, wp);
 #pragma unroll 1
-            for (int k = 0; k < 2 * NM; ++k) {
-                const int m = k >> 1, h0 = 16 * (k & 1);
-                const int dd = 128 * m + 32 * qd + lane;
-                uint32_t r[16];
-                tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set + (uint32_t)h0, r);
-                tmem_ld_wait();
-                if (slot >= 0) {
-                    float* po = p.part_o + ((int64_t)slot * hp + 32 * set + h0) * p.d + dd;
-                    if (dd < p.d) {
+            for (int m = 0; m < NM; ++m)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (32 * set + h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
+                for (int half = 0; half < 2; ++half) {
+                    const int k = 2 * m + half, h0 = 16 * half;
+                    const int dd = 128 * m + 32 * qd + lane;
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set + (uint32_t)h0, r);
+                    tmem_ld_wait();
+                    if (slot >= 0) {
+                        float* po = p.part_o + ((int64_t)slot * hp + 32 * set + h0) * p.d + dd;
+                        if (dd < p.d) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (32 * set + h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
+                        }
+                        continue;
                     }
-                    continue;
-                }
-                float vv[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) vv[i] = dead ? 0.f : __uint_as_float(r[i]) * __shfl_sync(kWarpFull, inv, h0 + i);
-                if (joins) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(stg + (lane + 32 * j) * 8) = pre[j];
-                    load_prev(k + 1);
+                    for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = __uint_as_float(r[i]);
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float w = __shfl_sync(kWarpFull, wp, h0 + i);
-                        const float pv = bf16_f(stg[i * 32 + lane]);
-                        vv[i] = w != 0.f ? vv[i] + w * pv : vv[i];   // weight 0: prev_out is not used
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = lane + 32 * j;
+                        const float2 f = fac[h0 + (c >> 2)];
+                        const float4* src = reinterpret_cast<const float4*>(stg + (c >> 2) * 32 + 8 * (c & 3));
+                        const float4 lo = src[0], hi = src[1];
+                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        const uint32_t pw[4] = {pre[half][j].x, pre[half][j].y, pre[half][j].z, pre[half][j].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x0 = v[2 * i] * f.x, x1 = v[2 * i + 1] * f.x;
+                            if (joins) {   // weight 0: prev_out is not used
+                                x0 = f.y != 0.f ? x0 + f.y * __uint_as_float(pw[i] << 16) : x0;
+                                x1 = f.y != 0.f ? x1 + f.y * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
+                            }
+                            o[i] = dead ? 0u : pack_bf16x2(x0, x1);
+                        }
+                        int64_t at;
+                        if (piece(k, j, at)) *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
+                    if (joins) load_prev(k + 2, pre[half]);
                     __syncwarp();
                 }
-                // lane pairs write 4 bytes: the even lane head i, the odd lane head i + 1
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float send = odd ? vv[i] : vv[i + 1];
-                    const float recv = __shfl_xor_sync(kWarpFull, send, 1);
-                    const uint32_t pk = odd ? pack_bf16x2(recv, vv[i + 1]) : pack_bf16x2(vv[i], recv);
-                    *reinterpret_cast<uint32_t*>(stg + (i + (odd ? 1 : 0)) * 32 + (lane & ~1)) = pk;
-                }
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    int64_t at;
-                    if (piece(k, j, at))
-                        *reinterpret_cast<uint4*>(p.out + at) = *reinterpret_cast<const uint4*>(stg + (lane + 32 * j) * 8);
-                }
-                __syncwarp();
-            }
         };
 
         Walk walk(wk);
         Seg sg;
         int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
+        float pend_sink = -INFINITY, pend_lse = -INFINITY;   // and what it is joined with
         int par = 0;                           // segment parity
         while (walk.next(p, sg)) {
             // the Q buffer is free: this warp has seen the last S^T of the previous query (a warp whose head
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 }
                 if (p.prev_out) prefetch_l2_bulk(p.prev_out + grp.row0 * p.d, (uint32_t)grp.heads * row);
             }
-            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, par ^ 1);
+            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, par ^ 1, pend_sink, pend_lse);
             named_bar_sync(kBarSoft, 256);     // the staging area is every warp's P^T; qc is complete
             m_run = -INFINITY;
             tl->cm[set][qd][lane] = make_float2(tl->qc[32 * set + lane], 0.f);
@@ -944,9 +944,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                             kMode == kPlain ? 0 : (int64_t)sg.q * ((p.n_rows + kRows - 1) / kRows) + t);
             par ^= 1;
             pend_q = sg.q;
+            const int hh = 32 * set + lane;
+            if (hh < grp.heads) {
+                if (p.sink) pend_sink = __ldg(p.sink + (kPack ? hh % p.h : hh));
+                pend_lse = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) : -INFINITY;
+            }
             pend_slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
         }
-        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, par ^ 1);
+        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, par ^ 1, pend_sink, pend_lse);
 
         // groups without a visible row
         for (int q = blockIdx.x; q < nq; q += gridDim.x) {
