@@ -21,8 +21,9 @@
 // 128 rows instead would take a quarter off the QK's operand traffic (48 cycles for M = 128, 32 for M = 64), but leaves
 // decode, QK, softmax and PV of a tile to run one after another: 8,400 cycles per 128 rows.
 // Bound by shared memory: of a tile at 128 B a cycle, QK 1024 cycles, PV 768, the decoded stores 512 and P^T, together
-// 2430.  2048 queries over up to 2048 rows: 2740 cycles a tile, 767 us; one query each over 32 x 16384 rows, where the
-// codes come from HBM: 3500 cycles, 95 us, and the merge 12.  QK and PV issued by one warp in turn: 832 and 112 us.
+// 2430 of the 2800 that a tile takes.  2048 queries over up to 2048 rows: 701 us, 18,000 of a query's 100,000 cycles
+// for its Q and outputs; one query each over 32 x 16384 rows: 95 us (20 of them set-up, change of query and partial
+// outputs), and the merge 12.  QK and PV issued by one warp in turn took 832 and 112 us, outputs scaled by shuffles 765.
 //
 // f16 operands: an E2M1 value (2 significant bits) times an E4M3 value (4) is exact in f16 (at most 6
 // significant bits, magnitudes 2^-10 .. 2688), so the tile is exact.  Q is bf16: each head's values are
@@ -1487,7 +1488,7 @@ cudaError_t launch_after(void (*kernel)(T...), dim3 grid, int threads, size_t sm
 AttnFp4Plan attn_fp4_plan(int B, int s, int h, int n_rows, int num_sms) {
     AttnFp4Plan l;
     // Few heads: as many queries of a sequence as fill the 64 rows of Q share a tile, which costs the same for any number
-    // of heads (2048 x 16 heads over 2048 rows 659 -> 251 us, 131,072 queries of one head over 20 rows 3853 -> 94).
+    // of heads (2048 x 16 heads over 2048 rows 659 -> 235 us, 131,072 queries of one head over 20 rows 3853 -> 80).
     l.pack = h <= 32 ? 64 / h : 1;
     if (l.pack > s) l.pack = s;
     const int groups = l.groups = (s + l.pack - 1) / l.pack;
