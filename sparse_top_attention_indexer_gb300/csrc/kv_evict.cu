@@ -20,8 +20,7 @@
 // per row it reads: 32 sequences of 2049 rows losing one each 10 us, 8 of 8704 rows losing 512 18 us, one of 52,003
 // rows losing 2002 23 us.  Adding equal bins within a warp before the histogram costs more (12, 19, 28 us) than
 // the collisions of its atomics.
-// C = 1 up to kOneCtaRows rows (a CTA covers them in a few iterations and a cluster barrier costs more than it saves),
-// else 8.
+// C = 1, 2, 4 or 8 by the rows and the number of sequences (cluster_size).
 #include <math.h>
 
 #include "sti_internal.h"
@@ -33,7 +32,6 @@ namespace {
 constexpr int kEvThreads = 1024;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kOneCtaRows = 8192;
 constexpr int kKeyCache = 40960;   // keys a CTA holds in shared memory; rows past it are re-read
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
@@ -334,10 +332,36 @@ cudaError_t launch_c(const KvEvictParams& p, cudaStream_t stream) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// CTAs per sequence: the C with the least estimate of waves x (start + a step per row of a CTA).  The constants (us) are
+// fitted to one row lost of n: C = 1 takes 11 us at n = 2049 and 26 at 16,400 for any number of sequences up to the
+// SMs, C = 8 17 and 19 for 8 sequences, but 54 for 32 and 161 for 128, since only 14 such clusters (32 of C = 4, 64 of
+// C = 2) are resident at a time; 32 x 32,000 take 39, 30, 23 and 57 us with C = 1, 2, 4 and 8.  Rows past a CTA's
+// key cache are read again in every pass, at three times the step.
+int cluster_size(int B, int n_rows) {
+    const int resident[4] = {device_num_sms(), 64, 32, 14};
+    const float start[4] = {9.5f, 15.f, 15.5f, 16.5f};
+    int best = 1;
+    float least = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        const float rows = (float)n_rows / (float)(1 << i), waves = (float)((B + resident[i] - 1) / resident[i]);
+        const float t = waves * (start[i] + 0.00093f * rows * (rows > (float)kKeyCache ? 3.f : 1.f));
+        if (i == 0 || t < least) {
+            least = t;
+            best = 1 << i;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 cudaError_t launch_kv_evict(const KvEvictParams& p, cudaStream_t stream) {
-    return p.n_rows <= kOneCtaRows ? launch_c<1>(p, stream) : launch_c<8>(p, stream);
+    switch (cluster_size(p.B, p.n_rows)) {
+        case 1: return launch_c<1>(p, stream);
+        case 2: return launch_c<2>(p, stream);
+        case 4: return launch_c<4>(p, stream);
+        default: return launch_c<8>(p, stream);
+    }
 }
 
 }  // namespace sti

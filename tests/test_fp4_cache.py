@@ -608,6 +608,10 @@ EVICT = [
     (2, 70000, 65000, 4, 128, [70000, 66001], 50, 1, "special"),
     (2, 100, 0, 0, 0, [100, 7], 5, 1, "random"),
     (1, 400000, 399000, 4, 128, [399990], 50, 1, "ties"),
+    # many sequences: clusters of 4, of 2, single CTAs
+    (17, 20000, 19000, 4, 64, [20000 - 60 * i for i in range(17)], 5, 1, "special"),
+    (40, 20000, 19900, 4, 64, [20000 - i for i in range(40)], 5, 1, "ties"),
+    (150, 9000, 8990, 4, 64, [9000 - i % 12 for i in range(150)], 5, 1, "random"),
 ]
 
 
