@@ -138,6 +138,9 @@ __device__ __forceinline__ void regs_down() {
 
 // Bounded wait, as attn_wait, for waits that come several times per tile: reading the global timer takes
 // about 200 ns, so it is read only every 256th failed poll (a failed try_wait has already slept a while).
+// A wait by parity passes at once when the phase before the awaited one is still open, so every waiter here comes after
+// that phase: most wait for a barrier's phases in order; those that wait for freed[.] of some tile n alone
+// have seen S^T of n, whose tile was decoded after freed[.] of n - 2.
 __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {

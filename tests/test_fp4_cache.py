@@ -88,6 +88,8 @@ ATTEND = {
     "chunk": (2, 40, 64, 512, 400, [1200, 700], 4, None, True, True, True),
     "no_rows": (2, 3, 8, 64, 0, [5, 9], 1, None, True, True, False),
     "nothing_at_all": (2, 2, 8, 64, 0, [5, 9], 1, None, True, False, False),
+    # several queries of many tiles per SM, with rows that are split between SMs
+    "long_queries": (1, 400, 64, 512, 1500, [5600], 4, None, True, True, False),
     # few heads, several queries: groups of queries share their tiles
     "packed_partial_mixed": (2, 7, 20, 512, 300, [30, 2], 4, None, True, True, True),
     "packed_mixed_no_prev": (3, 9, 8, 128, 90, [0, 2, 500], 4, [0, 0, 130], True, False, True),
