@@ -418,8 +418,10 @@ sti_status sti_kv_append_fp4(const uint16_t *x, int64_t x_bstride, const int32_t
  *      prev_lse is -inf, prev_out is not used.
  *   lse: fp32 [b, seqlen, h] or NULL;  row_weight: fp32 [b, n_rows] (batch stride in elements) or NULL
  * out may be prev_out itself; otherwise the outputs must not overlap the inputs.
- * f16 tensor-core MMAs over the exactly decoded rows with fp32 accumulation, fp32 online softmax, P rounded
- * to f16 for the PV product, bf16 output; results do not depend on the timing of the GPU (no atomics).
+ * f16 tensor-core MMAs over the exactly decoded rows with fp32 accumulation, fp32 online softmax, bf16 output.  P is
+ * rounded to f16 for the PV product: a row's e^{s} by 2^-11 of itself or, if that is more, by 2^-32 of the e^{s} of the
+ * largest row (so out is off by at most n_rows 2^-32 max|row| more than by relative roundings); lse and row_weight
+ * take it unrounded.  Results do not depend on the timing of the GPU (no atomics).
  * Two kernels, one or two more with row_weight.
  * Supported: 1 <= h <= 64, d a multiple of 64 up to 512; q, out, prev_out, codes 16-byte aligned and
  * codes_bstride a multiple of 16, scales 4-byte aligned and scales_bstride a multiple of 4, both strides

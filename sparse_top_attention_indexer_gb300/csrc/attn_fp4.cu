@@ -15,8 +15,8 @@
 //   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128
 //     dims per block, K = 64 rows; the same tile read as an MN-major operand);
 //   * warp 18 asks for the rows of the next tiles, into L2;
-//   * warps 0..7 load Q, run the online softmax (two sets of 32 heads; the running maxima move only when a
-//     score passes them by 2^8) and write the outputs.
+//   * warps 0..7 load Q, run the online softmax (two sets of 32 heads; what P is relative to moves only when a
+//     score passes the largest so far by 2^8) and write the outputs.
 // With 512 dims, Q (64 KB), two tiles of 64 rows (128 KB) and two P^T (16 KB) fill shared memory.  One tile of
 // 128 rows instead would take a quarter off the QK's operand traffic (48 cycles for M = 128, 32 for M = 64), but leaves
 // decode, QK, softmax and PV of a tile to run one after another: 8,400 cycles per 128 rows.
@@ -29,8 +29,11 @@
 // significant bits, magnitudes 2^-10 .. 2688), so the tile is exact.  Q is bf16: each head's values are
 // scaled by a power of two that puts its largest into [2^12, 2^13) and is undone in fp32 with the
 // softmax scale; an element down to 2^-26 of the head's largest keeps all its 8 bits, smaller ones are
-// off by less than 2^-37 of the largest.  P is rounded to f16 (2^-11) for the PV product; its sum l is
-// taken before the rounding, in fp32.
+// off by less than 2^-37 of the largest.  P is rounded to f16 for the PV product; its sum l is taken before the
+// rounding, in fp32.  P is held at 2^7 .. 2^15 for the row of the largest score, not at 1: f16 keeps 11 bits down to 2^-14
+// and steps of 2^-24 below, so a row's probability is off by 2^-11 of itself or, if that is more, by 2^-32 of the
+// largest's (2^-25 with the largest at 1: rows 17.5 below the largest score were lost to the output, and 2^20 of
+// them 19 below are 0.6 % of it).
 //
 // Row weights (only when asked for): p = e^{s - L} needs the final L, so they come after the merge.  A few queries a
 // sequence (decoding, drafts) leave their scores in the workspace, 4 bytes each, and row_weight_scores_kernel sums
@@ -58,6 +61,8 @@ constexpr uint32_t kPBuf = kRows * 128;        // a P^T buffer: 64 rows x 64 hea
 constexpr uint32_t kTmO = 128;                 // TMEM: S^T of tile parity b at columns [64 b, 64 b + 64), O^T d-block
                                                // m at [128 + 64 m, 192 + 64 m)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr float kTopNew = 7.f, kTopMost = 15.f;   // log2 of the largest P: when a head's reference is set, and at
+                                                  // most (f16 ends below 2^16)
 constexpr int kAhead = 3;                      // tiles whose rows are asked for ahead
 constexpr int kWTiles = 32;                    // row weights: tiles per chunk (accumulators in shared memory)
 constexpr int kScoreQueries = 8;               // row weights from kept scores: at most this many query groups a sequence,
@@ -448,7 +453,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // ------------------------------------------------------------------ attention
 
 struct __align__(16) Tail {
-    float2 cm[2][4][32];      // [head group][warp of the group]: its copy of (softmax scale, -running maximum)
+    float2 cm[2][4][32];      // [head group][warp of the group]: its copy of (softmax scale, -reference)
     float qc[64];             // per head: softmax scale (log2) over its f16 scaling
     float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
     float lsum[2][4][32];
@@ -658,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         const uint32_t bar_set = 1u + (uint32_t)set;
         uint32_t n = 0;
         bool dead = false;
-        float m_run = -INFINITY;                 // lane l: head 32 set + l
+        float m_run = -INFINITY;                 // what P is relative to, in log2: lane l: head 32 set + l
         float l_thr[8];                          // running sums of the thread's heads over its rows
 
         auto mwait = [&](uint64_t* bar, uint32_t parity) {
@@ -666,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
         };
 
         // One tile's probabilities.  cm holds (c, -m) of the thread's heads: c the softmax scale (log2) over the head's
-        // f16 scaling, m its running maximum, so y = S c - m is one FMA and 2^y the probability.
+        // f16 scaling, m its reference, 2^-7 of the maximum that it was taken from; so y = S c - m is one FMA and 2^y the
+        // probability.
         float2 cm[8];
         auto load_cm = [&]() {   // from the warp's copy, which has every head of the group
 #pragma unroll
@@ -730,8 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                     top1 = fmaxf(top1, fmaxf(y[4 * g + 2], y[4 * g + 3]));
                 }
             }
-            // the maxima stay unless a visible score passes its head's by 2^8
-            const bool need = !named_bar_and(bar_set, 128, !(first || ((kPack || v0) && top0 > 8.f) || (v1 && top1 > 8.f)));
+            // the references stay unless a visible score passes the maximum that its head's was taken from by 2^8
+            const bool need = !named_bar_and(bar_set, 128, !(first || ((kPack || v0) && top0 > kTopMost) || (v1 && top1 > kTopMost)));
             if (need) {
                 float* red = &tl->red[buf][set][qd][0];
 #pragma unroll
@@ -749,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 float2* own = &tl->cm[set][qd][0];
                 const float old = -own[lane].y;            // what y is relative to
                 const float mt = fmaxf(fmaxf(rr[0], rr[32]), fmaxf(rr[64], rr[96])) + old;
-                const float m_new = (m_run == -INFINITY || mt > m_run + 8.f) ? fmaxf(m_run, mt) : m_run;
+                const float m_new = (m_run == -INFINITY || mt > m_run + kTopMost) ? fmaxf(m_run, mt - kTopNew) : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
                 m_run = m_new;
                 __syncwarp();
@@ -845,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
                 wp = prev_lse == -INFINITY ? 0.f : 1.f;
                 if (p.lse && qd == 0) p.lse[grp.row0 + hh] = prev_lse;
             } else if (hh < grp.heads) {
-                // everything relative to the largest of the running maximum, the sink and prev_lse
+                // everything relative to the largest of the reference, the sink and prev_lse
                 const float sk = sink * kLog2e, pl = prev_lse * kLog2e;
                 float mx = fmaxf(m_run, fmaxf(sk, pl));
                 if (mx == -INFINITY) mx = 0.f;

@@ -213,7 +213,7 @@ struct AttnFp4Params {
     int grid;                   // CTAs of the attention kernel
     int2* rec;                  // [grid]: the split query that starts in a CTA and its last CTA, or {-1, 0}
     float* part_o;              // [2 * grid][pack * h][d] unnormalised partial outputs
-    float2* part_ml;            // [2 * grid][64] running maximum (log2) and sum
+    float2* part_ml;            // [2 * grid][64] what the partial is relative to (log2), and its sum
     int pack, groups;           // queries per group, groups per sequence
     int w_split;                // row weights: splits of the groups (partial sums in w_part when > 1)
     int w_grid;                 // row weights: CTAs, a multiple of w_split
