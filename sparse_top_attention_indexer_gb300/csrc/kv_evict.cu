@@ -315,7 +315,10 @@ template <int C>
 cudaError_t launch_c(const KvEvictParams& p, cudaStream_t stream) {
     const int64_t per_cta = ((int64_t)p.n_rows + 32 * kEvWarps * C - 1) / (32 * kEvWarps * C) * 32 * kEvWarps;
     const size_t smem = sizeof(EvTail) + 4 * (size_t)(per_cta < kKeyCache ? per_cta : kKeyCache);
-    cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit belongs to the kernel, not to the call: always the most that any call takes, or a call from another host
+    // thread could lower it between this one's two steps
+    cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(sizeof(EvTail) + 4 * (size_t)kKeyCache));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.B * C);
