@@ -425,10 +425,14 @@ sti_status sti_kv_append_fp4(const uint16_t *x, int64_t x_bstride, const int32_t
  * Two kernels, one or two more with row_weight.
  * Supported: 1 <= h <= 64, d a multiple of 64 up to 512; q, out, prev_out, codes 16-byte aligned and
  * codes_bstride a multiple of 16, scales 4-byte aligned and scales_bstride a multiple of 4, both strides
- * covering n_rows rows.  ws: sti_attn_fp4kv_workspace_size() bytes; for up to 8
+ * covering n_rows rows.  ws: sti_attn_fp4kv_workspace_size() bytes, whether row_weight is given or not; for up to 8
  * queries a sequence (of few heads: 8 times the queries whose heads together number 64) they include room for
  * the scores that row_weight is summed from, 256 bytes per row and query (or such a group of queries), up
  * to 256 MB; beyond, the scores are computed a second time.
+ *
+ * sti_attn_fp4kv_noweights: the call without row_weight, for callers that never want it; its workspace,
+ * sti_attn_fp4kv_noweights_workspace_size() bytes, has no such room (32 queries of 64 heads over 16384 rows: 40 MB instead of
+ * 168).
  */
 size_t sti_attn_fp4kv_workspace_size(int b, int seqlen, int h, int d, int n_rows);
 sti_status sti_attn_fp4kv(const uint16_t *q, const uint8_t *codes, int64_t codes_bstride, const uint8_t *scales,
@@ -436,6 +440,13 @@ sti_status sti_attn_fp4kv(const uint16_t *q, const uint8_t *codes, int64_t codes
                           int ratio, const float *attn_sink, float softmax_scale, const uint16_t *prev_out,
                           const float *prev_lse, int b, int seqlen, int h, int d, uint16_t *out, float *lse,
                           float *row_weight, int64_t row_weight_bstride, void *ws, size_t ws_bytes, sti_stream stream);
+size_t sti_attn_fp4kv_noweights_workspace_size(int b, int seqlen, int h, int d, int n_rows);
+sti_status sti_attn_fp4kv_noweights(const uint16_t *q, const uint8_t *codes, int64_t codes_bstride,
+                                    const uint8_t *scales, int64_t scales_bstride, int n_rows,
+                                    const int32_t *start_pos, const int32_t *dropped, int ratio,
+                                    const float *attn_sink, float softmax_scale, const uint16_t *prev_out,
+                                    const float *prev_lse, int b, int seqlen, int h, int d, uint16_t *out, float *lse,
+                                    void *ws, size_t ws_bytes, sti_stream stream);
 
 /*
  * sti_kv_evict: bring every sequence that holds more than `budget` rows back to budget rows.  Of its rows

@@ -38,7 +38,8 @@ EXPORTS = ["sti_status_string", "sti_last_cuda_error", "sti_version", "sti_read_
            "sti_decode_workspace_size",
            "sti_decode_fused", "sti_decode_kernel_count", "sti_decode_fused_noalloc", "sti_decode_noalloc_status",
            "sti_selftest_wait_timeout", "sti_window_idxs_chunked", "sti_idx_scores_mxfp4",
-           "sti_kv_append_fp4", "sti_attn_fp4kv_workspace_size", "sti_attn_fp4kv", "sti_kv_evict_workspace_size",
+           "sti_kv_append_fp4", "sti_attn_fp4kv_workspace_size", "sti_attn_fp4kv",
+           "sti_attn_fp4kv_noweights_workspace_size", "sti_attn_fp4kv_noweights", "sti_kv_evict_workspace_size",
            "sti_kv_evict"]
 FP4_E4M3_16, FP4_E8M0_32 = 0, 1
 
@@ -126,6 +127,10 @@ def lib() -> ctypes.CDLL:
         L.sti_attn_fp4kv_workspace_size.argtypes, L.sti_attn_fp4kv_workspace_size.restype = [I, I, I, I, I], SZ
         L.sti_attn_fp4kv.argtypes = [P, P, I64, P, I64, I, P, P, I, P, F, P, P, I, I, I, I, P, P, P, I64, P, SZ, P]
         L.sti_attn_fp4kv.restype = I
+        L.sti_attn_fp4kv_noweights_workspace_size.argtypes = [I, I, I, I, I]
+        L.sti_attn_fp4kv_noweights_workspace_size.restype = SZ
+        L.sti_attn_fp4kv_noweights.argtypes = [P, P, I64, P, I64, I, P, P, I, P, F, P, P, I, I, I, I, P, P, P, SZ, P]
+        L.sti_attn_fp4kv_noweights.restype = I
         L.sti_kv_evict_workspace_size.argtypes, L.sti_kv_evict_workspace_size.restype = [I, I, I], SZ
         L.sti_kv_evict.argtypes = [P, I64, P, I64, P, P, I, I, I, I, I, I, I, ctypes.POINTER(RowArray), I, P, SZ, P]
         L.sti_kv_evict.restype = I
@@ -561,8 +566,10 @@ def kv_append_fp4(x: torch.Tensor, start_pos: torch.Tensor, seqlen: int, ratio: 
         _check(st, "sti_kv_append_fp4")
 
 
-def attn_fp4kv_workspace_size(b: int, s: int, h: int, d: int, n_rows: int) -> int:
-    return int(lib().sti_attn_fp4kv_workspace_size(b, s, h, d, n_rows))
+def attn_fp4kv_workspace_size(b: int, s: int, h: int, d: int, n_rows: int, row_weight: bool = True) -> int:
+    """Bytes of attn_fp4kv's workspace; row_weight=False: of calls without row_weight, which take less."""
+    size = lib().sti_attn_fp4kv_workspace_size if row_weight else lib().sti_attn_fp4kv_noweights_workspace_size
+    return int(size(b, s, h, d, n_rows))
 
 
 def attn_fp4kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, start_pos: torch.Tensor, ratio: int,
@@ -589,16 +596,17 @@ def attn_fp4kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, start
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if ws is None:
-        ws = _call_workspace(attn_fp4kv_workspace_size(b, s, h, d, n_rows), dev)
+        ws = _call_workspace(attn_fp4kv_workspace_size(b, s, h, d, n_rows, row_weight is not None), dev)
     pc, sc = _rows(codes, torch.uint8, b, n_rows, d // 2, dev, "codes")
     ps, ss = _rows(scales, torch.uint8, b, n_rows, d // 16, dev, "scales")
     pw, sw = _rows(row_weight, torch.float32, b, n_rows, 0, dev, "row_weight")
     bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    st = lib().sti_attn_fp4kv(
+    call, weights = (lib().sti_attn_fp4kv, (pw, sw)) if row_weight is not None else (lib().sti_attn_fp4kv_noweights, ())
+    st = call(
         _dense(q, bf16, shape, dev, "q"), pc, sc, ps, ss, n_rows, _dense(start_pos, i32, (b,), dev, "start_pos"),
         _dense(dropped, i32, (b,), dev, "dropped"), ratio, _dense(attn_sink, f32, (h,), dev, "attn_sink"), softmax_scale,
         _dense(prev_out, bf16, shape, dev, "prev_out"), _dense(prev_lse, f32, (b, s, h), dev, "prev_lse"), b, s, h, d,
-        _dense(out, bf16, shape, dev, "out"), _dense(lse, f32, (b, s, h), dev, "lse"), pw, sw, _workspace_ptr(ws, dev),
+        _dense(out, bf16, shape, dev, "out"), _dense(lse, f32, (b, s, h), dev, "lse"), *weights, _workspace_ptr(ws, dev),
         ws.numel(), _raw_stream(dev.index))
     if st:
         _check(st, "sti_attn_fp4kv")

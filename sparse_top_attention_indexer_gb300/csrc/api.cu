@@ -907,13 +907,13 @@ sti_status sti_kv_append_fp4(const uint16_t* x, int64_t x_bstride, const int32_t
     return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_kv_append_fp4");
 }
 
-// attention workspace: [status | split records | partial (max, sum) | partial outputs | lse | partial row
-// weights | scores].  Sized for the largest GB300 (160 SMs), whatever device is current.
+// attention workspace: [status | split records | partial (max, sum) | partial outputs | with row weights: lse |
+// partial row weights | scores].  Sized for the largest GB300 (160 SMs), whatever device is current.
 static constexpr int kAttnFp4MaxSms = 160;
 struct AttnFp4Layout {
     size_t rec, ml, o, lse, w, scores, end;
 };
-static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows) {
+static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows, bool weights) {
     AttnFp4Layout l;
     const sti::AttnFp4Plan pl = sti::attn_fp4_plan(b, seqlen, h, n_rows, kAttnFp4MaxSms);
     auto after = [](size_t at, size_t bytes) { return sti::align_up(at + bytes, sti::kWsAlign); };
@@ -921,28 +921,31 @@ static AttnFp4Layout attn_fp4_layout(int b, int seqlen, int h, int d, int n_rows
     l.ml = after(l.rec, (size_t)pl.grid * sizeof(int2));
     l.o = after(l.ml, (size_t)2 * pl.grid * 64 * sizeof(float2));
     l.lse = after(l.o, (size_t)2 * pl.grid * pl.pack * h * d * sizeof(float));
+    l.w = l.scores = l.end = l.lse;
+    if (!weights) return l;
     l.w = after(l.lse, (size_t)b * seqlen * h * sizeof(float));
     l.scores = after(l.w, pl.score_bytes == 0 && pl.w_split > 1 ? (size_t)pl.w_split * b * n_rows * sizeof(float) : 0);
     l.end = l.scores + pl.score_bytes;
     return l;
 }
 
-size_t sti_attn_fp4kv_workspace_size(int b, int seqlen, int h, int d, int n_rows) {
+static size_t attn_fp4_ws(int b, int seqlen, int h, int d, int n_rows, bool weights) {
     if (b <= 0 || seqlen < 1 || h < 1 || h > 64 || d < 1 || d > 512 || n_rows < 0) return sti::kWsStatusBytes;
-    return attn_fp4_layout(b, seqlen, h, d, n_rows).end;
+    return attn_fp4_layout(b, seqlen, h, d, n_rows, weights).end;
 }
 
-sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes_bstride, const uint8_t* scales,
-                          int64_t scales_bstride, int n_rows, const int32_t* start_pos, const int32_t* dropped,
-                          int ratio, const float* attn_sink, float softmax_scale, const uint16_t* prev_out,
-                          const float* prev_lse, int b, int seqlen, int h, int d, uint16_t* out, float* lse,
-                          float* row_weight, int64_t row_weight_bstride, void* ws, size_t ws_bytes,
-                          sti_stream stream) {
+// room: the workspace is to hold what row weights need
+static sti_status attn_fp4kv_impl(const uint16_t* q, const uint8_t* codes, int64_t codes_bstride, const uint8_t* scales,
+                                  int64_t scales_bstride, int n_rows, const int32_t* start_pos, const int32_t* dropped,
+                                  int ratio, const float* attn_sink, float softmax_scale, const uint16_t* prev_out,
+                                  const float* prev_lse, int b, int seqlen, int h, int d, uint16_t* out, float* lse,
+                                  float* row_weight, int64_t row_weight_bstride, bool room, void* ws, size_t ws_bytes,
+                                  sti_stream stream) {
     if (b < 0 || seqlen < 1 || h < 1 || d < 1 || n_rows < 0 || ratio < 1) return STI_ERR_INVALID_ARG;
     if (h > 64 || d % 64 != 0 || d > 512 || (int64_t)b * seqlen > 0x3FFFFFFF) return STI_ERR_UNSUPPORTED;
     if (!prev_out != !prev_lse) return STI_ERR_INVALID_ARG;
     if (b == 0) return STI_OK;
-    if (!ws_ok(ws, ws_bytes, sti_attn_fp4kv_workspace_size(b, seqlen, h, d, n_rows))) return STI_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, attn_fp4_ws(b, seqlen, h, d, n_rows, room))) return STI_ERR_INVALID_ARG;
     if (!q || !start_pos || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(prev_out, 16))
         return STI_ERR_INVALID_ARG;
     if (n_rows > 0 &&
@@ -953,7 +956,7 @@ sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes
     if (overlap(out, o_bytes, q, o_bytes) || (out != prev_out && overlap(out, o_bytes, prev_out, o_bytes)) ||
         overlap(lse, l_bytes, prev_lse, l_bytes))
         return STI_ERR_INVALID_ARG;
-    const AttnFp4Layout l = attn_fp4_layout(b, seqlen, h, d, n_rows);
+    const AttnFp4Layout l = attn_fp4_layout(b, seqlen, h, d, n_rows, room);
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     sti::AttnFp4Params p{};
     p.q = q;
@@ -992,6 +995,35 @@ sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes
     p.w_split = pl.w_split;
     const cudaError_t e = sti::launch_attn_fp4(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_attn_fp4kv");
+}
+
+size_t sti_attn_fp4kv_workspace_size(int b, int seqlen, int h, int d, int n_rows) {
+    return attn_fp4_ws(b, seqlen, h, d, n_rows, true);
+}
+
+size_t sti_attn_fp4kv_noweights_workspace_size(int b, int seqlen, int h, int d, int n_rows) {
+    return attn_fp4_ws(b, seqlen, h, d, n_rows, false);
+}
+
+sti_status sti_attn_fp4kv(const uint16_t* q, const uint8_t* codes, int64_t codes_bstride, const uint8_t* scales,
+                          int64_t scales_bstride, int n_rows, const int32_t* start_pos, const int32_t* dropped,
+                          int ratio, const float* attn_sink, float softmax_scale, const uint16_t* prev_out,
+                          const float* prev_lse, int b, int seqlen, int h, int d, uint16_t* out, float* lse,
+                          float* row_weight, int64_t row_weight_bstride, void* ws, size_t ws_bytes,
+                          sti_stream stream) {
+    return attn_fp4kv_impl(q, codes, codes_bstride, scales, scales_bstride, n_rows, start_pos, dropped, ratio, attn_sink,
+                           softmax_scale, prev_out, prev_lse, b, seqlen, h, d, out, lse, row_weight, row_weight_bstride,
+                           /*room=*/true, ws, ws_bytes, stream);
+}
+
+sti_status sti_attn_fp4kv_noweights(const uint16_t* q, const uint8_t* codes, int64_t codes_bstride, const uint8_t* scales,
+                                    int64_t scales_bstride, int n_rows, const int32_t* start_pos, const int32_t* dropped,
+                                    int ratio, const float* attn_sink, float softmax_scale, const uint16_t* prev_out,
+                                    const float* prev_lse, int b, int seqlen, int h, int d, uint16_t* out, float* lse,
+                                    void* ws, size_t ws_bytes, sti_stream stream) {
+    return attn_fp4kv_impl(q, codes, codes_bstride, scales, scales_bstride, n_rows, start_pos, dropped, ratio, attn_sink,
+                           softmax_scale, prev_out, prev_lse, b, seqlen, h, d, out, lse, nullptr, 0, /*room=*/false, ws,
+                           ws_bytes, stream);
 }
 
 // eviction workspace: [status | row lists int32 [b, 2, most]], most = the rows that can move
