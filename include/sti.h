@@ -423,7 +423,7 @@ sti_status sti_kv_append_fp4(const uint16_t *x, int64_t x_bstride, const int32_t
  * largest row (so out is off by at most n_rows 2^-32 max|row| more than by relative roundings); lse and row_weight
  * take it unrounded.  Results do not depend on the timing of the GPU (no atomics).
  * Two kernels, one or two more with row_weight.
- * Supported: 1 <= h <= 64, d a multiple of 64 up to 512; q, out, prev_out, codes 16-byte aligned and
+ * Supported: 1 <= h <= 64, d a multiple of 64 up to 512, n_rows <= 2^30; q, out, prev_out, codes 16-byte aligned and
  * codes_bstride a multiple of 16, scales 4-byte aligned and scales_bstride a multiple of 4, both strides
  * covering n_rows rows.  ws: sti_attn_fp4kv_workspace_size() bytes, whether row_weight is given or not; for up to 8
  * queries a sequence (of few heads: 8 times the queries whose heads together number 64) they include room for
@@ -460,7 +460,7 @@ sti_status sti_attn_fp4kv_noweights(const uint16_t *q, const uint8_t *codes, int
  *   row_weight: fp32 [b, n_rows], row_pos: int32 [b, n_rows] (batch strides in elements)
  *   arrays: n_arrays <= 16 arrays [b, n_rows, row_bytes], batch strides in bytes (a host array, read during
  *      the call)
- * Supported: budget >= n_first + n_recent; row_bytes <= 65536.
+ * Supported: budget >= n_first + n_recent; row_bytes <= 65536; n_rows <= 2^30.
  * ws: sti_kv_evict_workspace_size() bytes.
  */
 typedef struct sti_row_array {

@@ -860,6 +860,9 @@ static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     return a && b && x < y + bn && y < x + an;
 }
 
+// The kernels round row numbers up to tiles and steps of a cluster in 32 bits.
+static constexpr int kMaxCacheRows = 1 << 30;
+
 // A cache array [b, n_rows, row_bytes]: base and batch stride aligned, the stride covering n_rows rows.
 static bool rows_ok(const void* base, int64_t bstride, int n_rows, int64_t row_bytes, int align) {
     return base && aligned(base, align) && bstride % align == 0 && bstride >= (int64_t)n_rows * row_bytes;
@@ -942,7 +945,8 @@ static sti_status attn_fp4kv_impl(const uint16_t* q, const uint8_t* codes, int64
                                   float* row_weight, int64_t row_weight_bstride, bool room, void* ws, size_t ws_bytes,
                                   sti_stream stream) {
     if (b < 0 || seqlen < 1 || h < 1 || d < 1 || n_rows < 0 || ratio < 1) return STI_ERR_INVALID_ARG;
-    if (h > 64 || d % 64 != 0 || d > 512 || (int64_t)b * seqlen > 0x3FFFFFFF) return STI_ERR_UNSUPPORTED;
+    if (h > 64 || d % 64 != 0 || d > 512 || (int64_t)b * seqlen > 0x3FFFFFFF || n_rows > kMaxCacheRows)
+        return STI_ERR_UNSUPPORTED;
     if (!prev_out != !prev_lse) return STI_ERR_INVALID_ARG;
     if (b == 0) return STI_OK;
     if (!ws_ok(ws, ws_bytes, attn_fp4_ws(b, seqlen, h, d, n_rows, room))) return STI_ERR_INVALID_ARG;
@@ -1041,7 +1045,7 @@ sti_status sti_kv_evict(float* row_weight, int64_t row_weight_bstride, int32_t* 
     if (b < 0 || seqlen < 1 || ratio < 1 || n_rows < 0 || budget < 0 || n_first < 0 || n_recent < 0 || n_arrays < 0)
         return STI_ERR_INVALID_ARG;
     if ((int64_t)n_first + n_recent > budget || n_arrays > 16 || (n_arrays > 0 && !arrays)) return STI_ERR_INVALID_ARG;
-    if (b > 0x7FFFFFFF / 8) return STI_ERR_UNSUPPORTED;
+    if (b > 0x7FFFFFFF / 8 || n_rows > kMaxCacheRows) return STI_ERR_UNSUPPORTED;
     if (b == 0) return STI_OK;
     for (int i = 0; i < n_arrays; ++i) {
         const sti_row_array& a = arrays[i];

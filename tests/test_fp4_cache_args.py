@@ -59,3 +59,15 @@ def test_attend_in_the_smaller_workspace(sti, name):  # noqa: F811
     with pytest.raises(sti.StiError):
         sti.attn_fp4kv(to_dev(a["q"]), to_dev_any(a["codes"]), to_dev_any(a["scales"]), to_dev_any(a["start_pos"]), a["ratio"],
                        a["scale"], row_weight=to_dev_any(a["w0"]), ws=ws)
+
+
+def test_refuses_more_rows_than_32_bit_row_numbers_hold(lib):  # noqa: F811
+    """Rows are counted in 32 bits, rounded up to tiles and to a cluster's steps: 2^30 fit, 2^31 - 1 would not."""
+    rows, big = (1 << 30) + 1, 1 << 62
+    for r in (rows, 0x7FFFFFFF):
+        assert lib.sti_attn_fp4kv(P(FAKE), P(FAKE), r * 32, P(FAKE), r * 4, r, P(FAKE), None, 1, None, 0.1, None, None, 1, 1, 8, 64,
+                                  P(FAKE * 4), None, None, 0, P(FAKE * 64), big, None) == 2
+        assert lib.sti_attn_fp4kv_noweights(P(FAKE), P(FAKE), r * 32, P(FAKE), r * 4, r, P(FAKE), None, 1, None, 0.1, None, None, 1,
+                                            1, 8, 64, P(FAKE * 4), None, P(FAKE * 64), big, None) == 2
+        assert lib.sti_kv_evict(P(FAKE), r, P(FAKE), r, P(FAKE), P(FAKE), 1, 1, 1, r, 100, 4, 8, None, 0, P(FAKE * 64), big,
+                                None) == 2
