@@ -389,7 +389,7 @@ sti_status sti_decode_noalloc_status(uint32_t *flags, sti_stream stream);
  *   row_pos: optional int32 [b, n_rows] (batch stride in elements): the row's group number;
  *   row_weight: optional fp32 [b, n_rows]: set to 0 for the rows written.
  *   A row outside [0, n_rows) is not written and raises STI_FLAG_INDEX_RANGE when ws is given (ws: optional,
- *   as for sti_window_idxs).
+ *   as for sti_window_idxs; 256 bytes).
  * Supported: dim a multiple of 64; x and codes 16-byte aligned, codes_bstride a multiple of 16 (the scales
  * may lie anywhere), both strides covering n_rows rows; m * dim < 2^31.
  */

@@ -526,8 +526,9 @@ def _mismatch(t, dtype, form, device, name):
 
 
 def _workspace_ptr(ws, device):
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
+    """Check a workspace; its pointer.  256 bytes at least: the C entry of kv_append_fp4 cannot check that itself."""
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous() or ws.numel() < 256:
+        raise ValueError(f"ws must be a contiguous uint8 tensor of 256 bytes or more on {device}")
     return ws.data_ptr()
 
 

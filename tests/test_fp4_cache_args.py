@@ -71,3 +71,21 @@ def test_refuses_more_rows_than_32_bit_row_numbers_hold(lib):  # noqa: F811
                                             1, 8, 64, P(FAKE * 4), None, P(FAKE * 64), big, None) == 2
         assert lib.sti_kv_evict(P(FAKE), r, P(FAKE), r, P(FAKE), P(FAKE), 1, 1, 1, r, 100, 4, 8, None, 0, P(FAKE * 64), big,
                                 None) == 2
+
+
+@gpu
+@pytest.mark.parametrize("n", [0, 1, 255])
+def test_append_refuses_a_workspace_that_is_too_small(sti, n):  # noqa: F811
+    """A status word that does not fit ws would be written behind it (or, with no bytes, nowhere)."""
+    import torch
+
+    room = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    x = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros(1, 1, 32, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(1, 1, 4, dtype=torch.uint8, device="cuda")
+    start = torch.full((1,), 7, dtype=torch.int32, device="cuda")       # row 7 of 1
+    with pytest.raises(ValueError, match="ws"):
+        sti.kv_append_fp4(x, start, 1, 1, codes, scales, ws=room[:n])
+    assert (room == 0).all() and (codes == 0).all()
+    sti.kv_append_fp4(x, start, 1, 1, codes, scales, ws=room[:256])
+    assert sti.read_device_status(room[:256]) == sti.FLAG_INDEX_RANGE and (codes == 0).all()
