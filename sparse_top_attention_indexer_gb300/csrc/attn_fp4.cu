@@ -1402,78 +1402,75 @@ __global__ void __launch_bounds__(256, 6) row_weight_scores_kernel(const AttnFp4
     const bool active = 32 * set < p.pack * p.h;
     const int tiles = (p.n_rows + kRows - 1) / kRows;
     griddep_wait();
-    for (int b = blockIdx.y; b < p.B; b += gridDim.y) {
-        const int vis_all = visible_rows(p, b, p.s - 1);
-        int t = blockIdx.x * per;
-        const int end = min(t + per, (vis_all + kRows - 1) / kRows);
-        if (t >= end) continue;
-        float4 v[4];
-        auto load = [&](int tt, int kk) {
-            const int64_t q = (int64_t)b * p.groups + kk;
-            const float4* sc = reinterpret_cast<const float4*>(p.scores) + ((q * tiles + tt) * 8 + warp) * 128 + lane;
+    const int b = blockIdx.y;
+    const int vis_all = visible_rows(p, b, p.s - 1);
+    int t = blockIdx.x * per;
+    const int end = min(t + per, (vis_all + kRows - 1) / kRows);
+    if (t >= end) return;
+    float4 v[4];
+    auto load = [&](int tt, int kk) {
+        const int64_t q = (int64_t)b * p.groups + kk;
+        const float4* sc = reinterpret_cast<const float4*>(p.scores) + ((q * tiles + tt) * 8 + warp) * 128 + lane;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) v[g] = __ldcs(sc + 32 * g);
-        };
-        // the groups see ever more rows: those from the first one on that sees the tile's first row
-        auto first = [&](int tt, int kk) {
-            while (group_rows(p, b, kk) <= tt * kRows) ++kk;
-            return kk;
-        };
-        int k0 = first(t, 0), k = k0;
-        if (active) load(t, k);
-        for (int i = tid; i < p.groups * 64; i += 256) {
-            const int hd = i & 63;
-            const Group grp = group_of(p, b * p.groups + (i >> 6));
-            lse[i >> 6][hd] = hd < grp.heads ? __ldcg(p.lse + grp.row0 + hd) * kLog2e : 0.f;
-            hvis[i >> 6][hd] = head_rows(p, grp, hd);
+        for (int g = 0; g < 4; ++g) v[g] = __ldcs(sc + 32 * g);
+    };
+    // the groups see ever more rows: those from the first one on that sees the tile's first row
+    auto first = [&](int tt, int kk) {
+        while (group_rows(p, b, kk) <= tt * kRows) ++kk;
+        return kk;
+    };
+    int k0 = first(t, 0), k = k0;
+    if (active) load(t, k);
+    for (int i = tid; i < p.groups * 64; i += 256) {
+        const int hd = i & 63;
+        const Group grp = group_of(p, b * p.groups + (i >> 6));
+        lse[i >> 6][hd] = hd < grp.heads ? __ldcg(p.lse + grp.row0 + hd) * kLog2e : 0.f;
+        hvis[i >> 6][hd] = head_rows(p, grp, hd);
+    }
+    __syncthreads();
+    while (t < end) {
+        float sum0 = 0.f, sum1 = 0.f;
+        const int k_next = t + 1 < end ? first(t + 1, k0) : 0;
+        if (active)
+            for (k = k0; k < p.groups; ++k) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int hd = 32 * set + 8 * g + 2 * l4, j = t * kRows + row;
+                    const float2 l = *reinterpret_cast<const float2*>(&lse[k][hd]);
+                    const int2 hv = *reinterpret_cast<const int2*>(&hvis[k][hd]);
+                    sum0 += (hv.x > j ? fast_exp2(v[g].x - l.x) : 0.f) + (hv.y > j ? fast_exp2(v[g].y - l.y) : 0.f);
+                    sum1 += (hv.x > j + 8 ? fast_exp2(v[g].z - l.x) : 0.f) + (hv.y > j + 8 ? fast_exp2(v[g].w - l.y) : 0.f);
+                }
+                if (k + 1 < p.groups) load(t, k + 1);
+                else if (t + 1 < end) load(t + 1, k_next);
+            }
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+            sum0 += __shfl_xor_sync(kWarpFull, sum0, o);
+            sum1 += __shfl_xor_sync(kWarpFull, sum1, o);
+        }
+        if (l4 == 0) {
+            part[set][row] = sum0;
+            part[set][row + 8] = sum1;
         }
         __syncthreads();
-        while (t < end) {
-            float sum0 = 0.f, sum1 = 0.f;
-            const int k_next = t + 1 < end ? first(t + 1, k0) : 0;
-            if (active)
-                for (k = k0; k < p.groups; ++k) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int hd = 32 * set + 8 * g + 2 * l4, j = t * kRows + row;
-                        const float2 l = *reinterpret_cast<const float2*>(&lse[k][hd]);
-                        const int2 hv = *reinterpret_cast<const int2*>(&hvis[k][hd]);
-                        sum0 += (hv.x > j ? fast_exp2(v[g].x - l.x) : 0.f) + (hv.y > j ? fast_exp2(v[g].y - l.y) : 0.f);
-                        sum1 += (hv.x > j + 8 ? fast_exp2(v[g].z - l.x) : 0.f) + (hv.y > j + 8 ? fast_exp2(v[g].w - l.y) : 0.f);
-                    }
-                    if (k + 1 < p.groups) load(t, k + 1);
-                    else if (t + 1 < end) load(t + 1, k_next);
-                }
-#pragma unroll
-            for (int o = 1; o <= 2; o <<= 1) {
-                sum0 += __shfl_xor_sync(kWarpFull, sum0, o);
-                sum1 += __shfl_xor_sync(kWarpFull, sum1, o);
-            }
-            if (l4 == 0) {
-                part[set][row] = sum0;
-                part[set][row + 8] = sum1;
-            }
-            __syncthreads();
-            if (tid < kRows && t * kRows + tid < vis_all)
-                p.row_weight[(int64_t)b * p.row_weight_bstride + t * kRows + tid] += part[0][tid] + part[1][tid];
-            __syncthreads();
-            ++t;
-            k0 = k_next;
-        }
+        if (tid < kRows && t * kRows + tid < vis_all)
+            p.row_weight[(int64_t)b * p.row_weight_bstride + t * kRows + tid] += part[0][tid] + part[1][tid];
+        __syncthreads();
+        ++t;
+        k0 = k_next;
     }
 }
 
-// The query splits' partial row weights, added in order.
+// The query splits' partial row weights, added in order; block (x, b) takes rows of sequence b.
 __global__ void __launch_bounds__(256) row_weight_add_kernel(const AttnFp4Params p) {
     const int b = blockIdx.y;
     griddep_wait();
-    for (int bb = b; bb < p.B; bb += gridDim.y) {
-        const int vis = visible_rows(p, bb, p.s - 1);
-        for (int j = blockIdx.x * 256 + threadIdx.x; j < vis; j += gridDim.x * 256) {
-            float v = 0.f;
-            for (int k = 0; k < p.w_split; ++k) v += __ldcg(p.w_part + ((int64_t)k * p.B + bb) * p.n_rows + j);
-            p.row_weight[(int64_t)bb * p.row_weight_bstride + j] += v;
-        }
+    const int vis = visible_rows(p, b, p.s - 1);
+    for (int j = blockIdx.x * 256 + threadIdx.x; j < vis; j += gridDim.x * 256) {
+        float v = 0.f;
+        for (int k = 0; k < p.w_split; ++k) v += __ldcg(p.w_part + ((int64_t)k * p.B + b) * p.n_rows + j);
+        p.row_weight[(int64_t)b * p.row_weight_bstride + j] += v;
     }
 }
 
@@ -1540,11 +1537,11 @@ cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
         : parts > 4 ? launch_after(merge_kernel<2, 128>, dim3(mx, mh), 256, 0, stream, p)
                     : launch_after(merge_kernel<1, 128>, dim3(mx, mh), 128, 0, stream, p);
     if (e != cudaSuccess || !p.row_weight || p.n_rows == 0) return e;
+    // (B fits a grid's y: scores are kept up to kScoreTiles sequences, and split queries mean at most num_sms kWTiles / 2)
     if (p.scores) {
         const int tiles = (p.n_rows + kRows - 1) / kRows, per = (int64_t)tiles * p.B >= kManyTiles ? 4 : 1;
         return launch_after(row_weight_scores_kernel,
-                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)(p.B < 65535 ? p.B : 65535)), 256, 0, stream,
-                            p, per);
+                            dim3((unsigned)((tiles + per - 1) / per), (unsigned)p.B), 256, 0, stream, p, per);
     }
     smem = row_weight_smem(p.d);
     e = cudaFuncSetAttribute(row_weight_kernel<NM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1552,9 +1549,8 @@ cudaError_t launch_nm(const AttnFp4Params& p, cudaStream_t stream) {
     e = launch_after(row_weight_kernel<NM>, dim3((unsigned)p.w_grid), kThreads, smem, stream, p);
     if (e != cudaSuccess || p.w_split == 1) return e;
     const int blocks = (p.n_rows + 255) / 256;
-    return launch_after(row_weight_add_kernel,
-                        dim3((unsigned)(blocks < 64 ? blocks : 64), (unsigned)(p.B < 65535 ? p.B : 65535)), 256, 0,
-                        stream, p);
+    return launch_after(row_weight_add_kernel, dim3((unsigned)(blocks < 64 ? blocks : 64), (unsigned)p.B), 256, 0, stream,
+                        p);
 }
 }  // namespace
 
