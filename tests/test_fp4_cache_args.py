@@ -89,3 +89,24 @@ def test_append_refuses_a_workspace_that_is_too_small(sti, n):  # noqa: F811
     assert (room == 0).all() and (codes == 0).all()
     sti.kv_append_fp4(x, start, 1, 1, codes, scales, ws=room[:256])
     assert sti.read_device_status(room[:256]) == sti.FLAG_INDEX_RANGE and (codes == 0).all()
+
+
+@gpu
+def test_evict_an_array_listed_twice(sti):  # noqa: F811
+    """The same array twice, and row_weight and row_pos themselves, in the list: each row moves once all the same."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    b, rows, budget = 3, 300, 200
+    w = torch.rand(b, rows, generator=gen, device="cuda")
+    pos = torch.arange(rows, device="cuda", dtype=torch.int32).repeat(b, 1)
+    tag = torch.arange(b * rows * 5, device="cuda", dtype=torch.int16).view(b, rows, 5)
+    start = torch.tensor([299, 250, 100], device="cuda", dtype=torch.int32)
+
+    def run(arrays):
+        st = [w.clone(), pos.clone(), tag.clone(), torch.zeros(b, device="cuda", dtype=torch.int32)]
+        sti.kv_evict(st[0], st[1], start, 1, 1, st[3], budget, 4, 8, [st[i] for i in arrays])
+        return st
+
+    for x, y in zip(run([2]), run([2, 0, 1, 2])):
+        assert (x == y).all()
