@@ -581,7 +581,8 @@ def attn_fp4kv(q: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, start
     """Attention of q [b, s, h, d] over every row of a 4-bit cache that each query sees
     (sti_attn_fp4kv).  codes uint8 [b, rows, d/2], scales uint8 [b, rows, d/16]; prev_out / prev_lse: the
     same queries' attention over other rows, joined into the result; lse (fp32 [b, s, h]) is written and
-    row_weight (fp32 [b, rows]) added to when given."""
+    row_weight (fp32 [b, rows]) added to when given.  ws: attn_fp4kv_workspace_size bytes, fewer without
+    row_weight."""
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("q must be a CUDA tensor")

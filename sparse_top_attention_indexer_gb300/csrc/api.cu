@@ -462,7 +462,7 @@ const char* sti_status_string(sti_status s) {
 
 const char* sti_last_cuda_error(void) { return g_last_cuda_error; }
 
-int sti_version(void) { return 200; }
+int sti_version(void) { return 300; }
 
 sti_status sti_read_device_status(void* ws, uint32_t* flags, sti_stream stream) {
     if (!ws) return STI_ERR_INVALID_ARG;

@@ -18,10 +18,12 @@
 //   * warps 0..7 load Q, run the online softmax (two sets of 32 heads; what P is relative to moves only when a
 //     score passes the largest so far by 2^8) and write the outputs.
 // With 512 dims, Q (64 KB), two tiles of 64 rows (128 KB) and two P^T (16 KB) fill shared memory.  One tile of
-// 128 rows instead would take a quarter off the QK's operand traffic (48 cycles for M = 128, 32 for M = 64), but leaves
+// 128 rows instead would take a quarter off the QK (48 cycles a step for M = 128, 32 for M = 64), but leaves
 // decode, QK, softmax and PV of a tile to run one after another: 8,400 cycles per 128 rows.
 // Bound by shared memory: of a tile at 128 B a cycle, QK 1024 cycles, PV 768, the decoded stores 512 and P^T, together
-// 2430 of the 2800 that a tile takes.  2048 queries over up to 2048 rows: 701 us, 18,000 of a query's 100,000 cycles
+// 2430 of the 2800 that a tile takes.  (The QK's 1024 are the tensor core's too, which takes N / 2 cycles for
+// M = 64, half its rate: fewer operand bytes alone would not shorten it.  Steps of M = 64 measured 25, 32 and 64 cycles for
+// N = 32, 64 and 128, of M = 128 48 for N = 64.)  2048 queries over up to 2048 rows: 701 us, 18,000 of a query's 100,000 cycles
 // for its Q and outputs; one query each over 32 x 16384 rows: 95 us (20 of them set-up, change of query and partial
 // outputs), and the merge 12.  QK and PV issued by one warp in turn took 832 and 112 us, outputs scaled by shuffles 765.
 //
@@ -999,8 +1001,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fp4_kernel(const AttnFp4Para
 
 // Block (x, head, z): the x-th split query group (there are at most gridDim.x), dims 4 W z .. 4 W (z + 1) - 1; thread
 // (g, i), g < G, dims 4 (W z + i) + {0..3} of every G-th part, four parts in flight; their sums join in shared memory
-// in a fixed order.  G follows from the parts a query can have: a single long query (152 parts) needs many loads in flight (20 us with G = 8, W = 128),
-// thousands of short ones (two parts each) would spend their time starting wide blocks.
+// in a fixed order.  G follows from the parts of a query when all are alike: a single long query (152 parts) needs many loads
+// in flight (20 us with G = 8, W = 128), thousands of short ones (two parts each) would spend their time starting wide
+// blocks.  A long query among short ones gets the short ones' G: one of 65536 rows x 512 among 59 of 300 takes 58 us for
+// the call, alone 29.
 template <int G, int W>
 __global__ void __launch_bounds__(G * W) merge_kernel(const AttnFp4Params p) {
     __shared__ float fac[256];
