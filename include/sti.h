@@ -474,6 +474,90 @@ sti_status sti_kv_evict(float *row_weight, int64_t row_weight_bstride, int32_t *
                         int budget, int n_first, int n_recent, const sti_row_array *arrays, int n_arrays, void *ws,
                         size_t ws_bytes, sti_stream stream);
 
+/* ------------------------------------------------------------------ paged latent cache */
+/*
+ * Not operations of the pages' listings: the steps around a layer's attention (RMS norm and rotation of the queries and
+ * of the cache rows) and a cache whose rows live in pages, attended as a whole or through a sliding window.  A step brings
+ * seqlen tokens to each of b sequences, the first at position start_pos[b] >= 0; n_new (int32 [b] or NULL: all) of them
+ * are real, clamped to [0, seqlen]: the others of a padded batch are neither read into anything nor written.
+ *
+ * The cache: pages, bf16 [n_pages, page_size, d] with contiguous rows, page i at pages + i*page_stride (elements); table,
+ * int32 [b, max_pages], sequence b at table + b*table_stride: position p of the sequence is row p % page_size of page
+ * table[b, p / page_size].  Entries of positions that a call does not need are not read.  A page outside [0, n_pages)
+ * or a position past the table raises STI_FLAG_INDEX_RANGE; such rows are not written, and not seen.
+ *
+ * sti_rope_freqs: the frequencies of a rotation of rope_dims dims, computed on the host into `turns` (HOST, uint64
+ * [rope_dims/2]; the caller copies it to the device once): pair i turns by f_i = theta^(-2i/rope_dims) radians per
+ * position, stored as turns in units of 2^-64, so that position * f_i mod one turn is an exact integer product.
+ * factor != 1: frequencies scaled for contexts longer than orig_len by YaRN's ramp: pair r(n) = rope_dims ln(orig_len /
+ * (2 pi n)) / (2 ln theta) turns n times over orig_len; from floor(r(beta_fast)) on the frequency goes over linearly to
+ * f_i / factor, reached at ceil(r(beta_slow)) (both clamped to [0, rope_dims - 1]).  orig_len 0: every f_i / factor.
+ * Supported: rope_dims even, 2 .. 1024; theta > 1; factor > 0; 0 < beta_slow < beta_fast.
+ */
+sti_status sti_rope_freqs(int rope_dims, double theta, double factor, int orig_len, double beta_fast, double beta_slow,
+                          uint64_t *turns);
+
+/*
+ * sti_norm_rope: every head's row x of d elements becomes
+ *   y = x / sqrt(mean(x^2) + eps) * weight    (norm != 0; weight: bf16 [d] or NULL for ones)
+ * and dims [rope_off, rope_off + rope_dims) of it are turned, pair by pair, by the angle of the token's position:
+ *   (y_a, y_b) <- rope_gain (y_a cos - y_b sin, y_b cos + y_a sin)
+ * pairs (2i, 2i+1), with STI_ROPE_HALVES (i, i + rope_dims/2) of the range; STI_ROPE_INVERSE: by minus the angle (which
+ * undoes the rotation, and is the gradient of one).  rope_dims 0: no rotation (turns unused).  fp32 inside (squares past
+ * 3e38 overflow), rounded once.
+ *   x, y: bf16 [b, seqlen, h, d], heads contiguous; sequences and tokens *_bstride and *_tstride elements apart
+ *   pos: int32 [b], the position of each sequence's first token, or with pos_per_token int32 [b, seqlen]
+ *   turns: uint64 [rope_dims/2] from sti_rope_freqs, on the device
+ * y may be x itself (with the same strides); otherwise the two must not share elements (heads of one array of tokens
+ * beside one another, as in a fused projection, do not).
+ * Supported: d a multiple of 8 up to 1024; rope_off and rope_dims multiples of 8 (rope_dims of 16 with STI_ROPE_HALVES);
+ * x, y, weight 16-byte aligned, strides multiples of 8; b * seqlen * h < 2^31.
+ */
+#define STI_ROPE_HALVES 1
+#define STI_ROPE_INVERSE 2
+sti_status sti_norm_rope(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, const int32_t *pos, int pos_per_token,
+                         const int32_t *n_new, int b, int seqlen, int h, int d, int norm, const uint16_t *weight,
+                         float eps, const uint64_t *turns, int rope_dims, int rope_off, int rope_flags,
+                         float rope_gain, uint16_t *y, int64_t y_bstride, int64_t y_tstride, sti_stream stream);
+
+/*
+ * sti_kv_append_paged: the rows x of a step's tokens, normed and rotated as by sti_norm_rope (norm 0 and rope_dims 0:
+ * as they are), written to their pages.
+ *   x: bf16 [b, seqlen, d]; pages, table: as above, pages 16-byte aligned, page_stride a multiple of 8 and at least
+ *   page_size * d.  ws: optional, for the status word (256 bytes).  x must not overlap the pages.
+ * Two positions of one call must not share a row.
+ */
+sti_status sti_kv_append_paged(const uint16_t *x, int64_t x_bstride, int64_t x_tstride, const int32_t *start_pos,
+                               const int32_t *n_new, int b, int seqlen, int d, int norm, const uint16_t *weight,
+                               float eps, const uint64_t *turns, int rope_dims, int rope_off, int rope_flags,
+                               float rope_gain, uint16_t *pages, int64_t page_stride, int n_pages, int page_size,
+                               const int32_t *table, int64_t table_stride, int max_pages, void *ws, sti_stream stream);
+
+/*
+ * sti_attn_paged: attention of every query over the positions it sees, a row serving as key and value for all heads.
+ * Query (b, t) at P = start_pos[b] + t sees the positions p <= P (its own among them: append first) and, with window > 0,
+ * of those only p > P - window and p < n_first (a sliding window, and first tokens that stay visible):
+ *   s_hp = softmax_scale * q[b,t,h,:] . row_p
+ *   L_h  = ln( sum_p e^{s_hp} + e^{attn_sink[h]} + e^{prev_lse[b,t,h]} )
+ *   out[b,t,h,:] = ( sum_p e^{s_hp} row_p + e^{prev_lse} prev_out[b,t,h,:] ) / e^{L_h},   lse = L_h
+ * A query that sees no row (bad pages): out = prev_out and lse = prev_lse, or 0 and -inf without them, as in
+ * sti_attn_fp4kv.  Rows that no query of the call sees may hold anything, NaN included; a query that sees a row holding
+ * an infinity or NaN has an undefined output, which does not reach queries that do not see it.
+ *   q, out: bf16 [b, seqlen, h, d]; lse: fp32 [b, seqlen, h] or NULL; attn_sink, prev_out, prev_lse: as sti_attn_fp4kv
+ * out may be prev_out itself; otherwise the outputs must not overlap the inputs.
+ * bf16 tensor-core MMAs with fp32 accumulation, P rounded to bf16 for the PV product, fp32 online softmax.  Results do not
+ * depend on the timing of the GPU (no atomics).  Two kernels.
+ * Supported: 1 <= h <= 64, d a multiple of 64 up to 512, max_pages * page_size <= 2^30; q, out, prev_out, pages 16-byte
+ * aligned, page_stride a multiple of 8 and at least page_size * d; b * seqlen * h < 2^31.
+ * ws: sti_attn_paged_workspace_size() bytes.
+ */
+size_t sti_attn_paged_workspace_size(int b, int seqlen, int h, int d);
+sti_status sti_attn_paged(const uint16_t *q, const uint16_t *pages, int64_t page_stride, int n_pages, int page_size,
+                          const int32_t *table, int64_t table_stride, int max_pages, const int32_t *start_pos,
+                          const int32_t *n_new, int window, int n_first, const float *attn_sink, float softmax_scale,
+                          const uint16_t *prev_out, const float *prev_lse, int b, int seqlen, int h, int d,
+                          uint16_t *out, float *lse, void *ws, size_t ws_bytes, sti_stream stream);
+
 /* ------------------------------------------------------------------ diagnostics */
 /*
  * Not an operation of the paper: a check of the library's failure handling.  Every wait in the

@@ -9,7 +9,8 @@ here, and a missing library is an error.
 
 Functions mirror the C entry points (``sti_`` prefix dropped):
   window_idxs, idx_scores, idx_topk, sparse_attn_sink, decode_fused, read_device_status
-and, for a bounded 4-bit cache, kv_append_fp4, attn_fp4kv, kv_evict.
+for a bounded 4-bit cache, kv_append_fp4, attn_fp4kv, kv_evict,
+and, for a paged cache of bf16 rows, rope_freqs, norm_rope, kv_append_paged, attn_paged.
 """
 from __future__ import annotations
 
@@ -40,8 +41,10 @@ EXPORTS = ["sti_status_string", "sti_last_cuda_error", "sti_version", "sti_read_
            "sti_selftest_wait_timeout", "sti_window_idxs_chunked", "sti_idx_scores_mxfp4",
            "sti_kv_append_fp4", "sti_attn_fp4kv_workspace_size", "sti_attn_fp4kv",
            "sti_attn_fp4kv_noweights_workspace_size", "sti_attn_fp4kv_noweights", "sti_kv_evict_workspace_size",
-           "sti_kv_evict"]
+           "sti_kv_evict", "sti_rope_freqs", "sti_norm_rope", "sti_kv_append_paged", "sti_attn_paged_workspace_size",
+           "sti_attn_paged"]
 FP4_E4M3_16, FP4_E8M0_32 = 0, 1
+ROPE_HALVES, ROPE_INVERSE = 1, 2
 
 
 class StiError(RuntimeError):
@@ -134,6 +137,16 @@ def lib() -> ctypes.CDLL:
         L.sti_kv_evict_workspace_size.argtypes, L.sti_kv_evict_workspace_size.restype = [I, I, I], SZ
         L.sti_kv_evict.argtypes = [P, I64, P, I64, P, P, I, I, I, I, I, I, I, ctypes.POINTER(RowArray), I, P, SZ, P]
         L.sti_kv_evict.restype = I
+        D = ctypes.c_double
+        L.sti_rope_freqs.argtypes, L.sti_rope_freqs.restype = [I, D, D, I, D, D, P], I
+        L.sti_norm_rope.argtypes = [P, I64, I64, P, I, P, I, I, I, I, I, P, F, P, I, I, I, F, P, I64, I64, P]
+        L.sti_norm_rope.restype = I
+        L.sti_kv_append_paged.argtypes = [P, I64, I64, P, P, I, I, I, I, P, F, P, I, I, I, F, P, I64, I, I, P, I64, I, P,
+                                          P]
+        L.sti_kv_append_paged.restype = I
+        L.sti_attn_paged_workspace_size.argtypes, L.sti_attn_paged_workspace_size.restype = [I, I, I, I], SZ
+        L.sti_attn_paged.argtypes = [P, P, I64, I, I, P, I64, I, P, P, I, I, P, F, P, P, I, I, I, I, P, P, P, SZ, P]
+        L.sti_attn_paged.restype = I
         _lib = L
     return _lib
 
@@ -664,3 +677,159 @@ def selftest_wait_timeout(ws: torch.Tensor, limit_us: int = 2000, stream=None) -
     """Launch the kernel whose wait nothing satisfies (see sti_selftest_wait_timeout)."""
     _check(lib().sti_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us), _stream(stream)),
            "sti_selftest_wait_timeout")
+
+
+# ---------------------------------------------------------------------------- paged latent cache
+
+
+def rope_freqs(rope_dims: int, theta: float = 10000.0, factor: float = 1.0, orig_len: int = 0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, device="cuda") -> torch.Tensor:
+    """The frequency table of a rotation of rope_dims dims (sti_rope_freqs), int64 [rope_dims / 2] on `device`, to be
+    kept with the model.  factor: scaled for contexts longer than orig_len (YaRN's ramp between beta_fast and beta_slow
+    turns over orig_len; orig_len 0: all pairs alike)."""
+    turns = torch.empty(max(1, rope_dims // 2), dtype=torch.int64)
+    _check(lib().sti_rope_freqs(rope_dims, theta, factor, orig_len, beta_fast, beta_slow, turns.data_ptr()),
+           "sti_rope_freqs")
+    return turns.to(device)
+
+
+def _token_rows(t, b, s, rest, device, name):
+    """Check bf16 [b, s, *rest] whose tokens are contiguous, sequences and tokens any stride apart; its pointer and those
+    two strides (a single sequence's or token's may be anything: the size)."""
+    shape, stride = t.shape, t.stride()
+    n, dense = 1, True
+    for size, st in zip(reversed(shape[2:]), reversed(stride[2:])):
+        dense = dense and (size == 1 or st == n)
+        n *= size
+    if t.dtype is not torch.bfloat16 or t.get_device() != device.index or tuple(shape) != (b, s, *rest) or not dense:
+        raise _mismatch(t, torch.bfloat16, f"{[b, s, *rest]} with contiguous tokens", device, name)
+    ts = stride[1] if s > 1 else n
+    return t.data_ptr(), stride[0] if b > 1 else s * ts, ts
+
+
+def _rope_args(freqs, rope_off, interleaved, d, device):
+    """Pointer of the frequencies, rotated dims, first rotated dim and flags."""
+    if freqs is None:
+        return None, 0, 0, 0
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be [rope_dims / 2]")
+    rd = 2 * freqs.shape[0]
+    return (_dense(freqs, torch.int64, freqs.shape, device, "freqs"), rd, d - rd if rope_off is None else rope_off,
+            0 if interleaved else ROPE_HALVES)
+
+
+def norm_rope(x: torch.Tensor, start_pos: torch.Tensor, freqs: torch.Tensor | None = None, rope_off: int | None = None,
+              interleaved: bool = True, inverse: bool = False, gain: float = 1.0, norm: bool = True,
+              weight: torch.Tensor | None = None, eps: float = 1e-6, n_new: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """RMS norm and rotation of every head's row in one pass (sti_norm_rope).  x: bf16 [b, s, h, d], heads contiguous;
+    start_pos: int32 [b] (position of each sequence's first token) or [b, s]; freqs: from rope_freqs (None: no
+    rotation); rope_off: first rotated dim (None: the last ones turn); interleaved: pairs (2i, 2i + 1), else
+    (i, i + rope_dims / 2); inverse: back; norm, weight (bf16 [d] or None), eps: the norm; n_new: int32 [b], the step's
+    real tokens (rows of the others stay as they are in `out`).  out may be x."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a CUDA tensor")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return norm_rope(x, start_pos, freqs, rope_off, interleaved, inverse, gain, norm, weight, eps, n_new, out)
+    if x.dim() != 4:
+        raise ValueError("x must be [b, s, h, d]")
+    b, s, h, d = x.shape
+    if out is None:
+        out = (torch.empty if n_new is None else torch.zeros)(b, s, h, d, dtype=torch.bfloat16, device=dev)
+    px, xb, xt = _token_rows(x, b, s, (h, d), dev, "x")
+    py, yb, yt = _token_rows(out, b, s, (h, d), dev, "out")
+    each = start_pos.dim() == 2
+    pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
+    st = lib().sti_norm_rope(
+        px, xb, xt, _dense(start_pos, torch.int32, (b, s) if each else (b,), dev, "start_pos"), each,
+        _dense(n_new, torch.int32, (b,), dev, "n_new"), b, s, h, d, norm, _dense(weight, torch.bfloat16, (d,), dev, "weight"),
+        eps, pf, rd, off, flags | (ROPE_INVERSE if inverse else 0), gain, py, yb, yt, _raw_stream(dev.index))
+    if st:
+        _check(st, "sti_norm_rope")
+    return out
+
+
+def _pages(pages, block_table, b, d, device):
+    """Check a pool of pages [n, page_size, d] and a table [b, most]; the C entries' seven arguments for them."""
+    ps = pages.stride()
+    if (pages.dtype is not torch.bfloat16 or pages.get_device() != device.index or pages.dim() != 3 or
+            pages.shape[2] != d or pages.shape[1] < 1 or ps[2] != 1 or (pages.shape[1] > 1 and ps[1] != d)):
+        raise _mismatch(pages, torch.bfloat16, f"[pages, page_size, {d}] with contiguous rows", device, "pages")
+    ts = block_table.stride()
+    if (block_table.dtype is not torch.int32 or block_table.get_device() != device.index or block_table.dim() != 2 or
+            block_table.shape[0] != b or (block_table.shape[1] > 1 and ts[1] != 1)):
+        raise _mismatch(block_table, torch.int32, f"[{b}, pages per sequence] with contiguous rows", device, "block_table")
+    n, size = pages.shape[0], pages.shape[1]
+    most = block_table.shape[1]
+    return (pages.data_ptr(), ps[0] if n > 1 else size * d, n, size, block_table.data_ptr(), ts[0] if b > 1 else most, most)
+
+
+def kv_append_paged(x: torch.Tensor, start_pos: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
+                    freqs: torch.Tensor | None = None, rope_off: int | None = None, interleaved: bool = True,
+                    gain: float = 1.0, norm: bool = False, weight: torch.Tensor | None = None, eps: float = 1e-6,
+                    n_new: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> None:
+    """Norm and rotate the rows x (bf16 [b, s, d]) of a step's tokens and write them to a paged cache
+    (sti_kv_append_paged).  pages: bf16 [pages, page_size, d]; block_table: int32 [b, pages per sequence], the page of
+    positions page_size * i ...; the rest as norm_rope.  ws: optional workspace whose status word reports
+    rows outside the table or the pool (they are not written)."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a CUDA tensor")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return kv_append_paged(x, start_pos, pages, block_table, freqs, rope_off, interleaved, gain, norm, weight, eps,
+                                   n_new, ws)
+    if x.dim() != 3:
+        raise ValueError("x must be [b, s, d]")
+    b, s, d = x.shape
+    px, xb, xt = _token_rows(x, b, s, (d,), dev, "x")
+    pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
+    st = lib().sti_kv_append_paged(
+        px, xb, xt, _dense(start_pos, torch.int32, (b,), dev, "start_pos"), _dense(n_new, torch.int32, (b,), dev, "n_new"),
+        b, s, d, norm, _dense(weight, torch.bfloat16, (d,), dev, "weight"), eps, pf, rd, off, flags, gain,
+        *_pages(pages, block_table, b, d, dev), None if ws is None else _workspace_ptr(ws, dev), _raw_stream(dev.index))
+    if st:
+        _check(st, "sti_kv_append_paged")
+
+
+def attn_paged_workspace_size(b: int, s: int, h: int, d: int) -> int:
+    return int(lib().sti_attn_paged_workspace_size(b, s, h, d))
+
+
+def attn_paged(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor, start_pos: torch.Tensor,
+               softmax_scale: float, window: int = 0, n_first: int = 0, attn_sink: torch.Tensor | None = None,
+               prev_out: torch.Tensor | None = None, prev_lse: torch.Tensor | None = None,
+               n_new: torch.Tensor | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of q [b, s, h, d] over a paged cache (sti_attn_paged), each query seeing the positions up to its own;
+    with window > 0 only the last `window` of them and the first n_first.  pages, block_table: as kv_append_paged;
+    prev_out / prev_lse: the same queries' attention over other rows, joined into the result; n_new: int32 [b], the
+    step's real tokens (rows of the others stay as they are in `out` and `lse`); lse (fp32 [b, s, h]) is written when
+    given.  ws: attn_paged_workspace_size bytes."""
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return attn_paged(q, pages, block_table, start_pos, softmax_scale, window, n_first, attn_sink, prev_out,
+                              prev_lse, n_new, out, lse, ws)
+    if q.dim() != 4:
+        raise ValueError("q must be [b, s, h, d]")
+    shape = q.shape
+    b, s, h, d = shape
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if out is None:
+        out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=bf16, device=dev)
+    if ws is None:
+        ws = _call_workspace(attn_paged_workspace_size(b, s, h, d), dev)
+    st = lib().sti_attn_paged(
+        _dense(q, bf16, shape, dev, "q"), *_pages(pages, block_table, b, d, dev),
+        _dense(start_pos, i32, (b,), dev, "start_pos"), _dense(n_new, i32, (b,), dev, "n_new"), window, n_first,
+        _dense(attn_sink, f32, (h,), dev, "attn_sink"), softmax_scale, _dense(prev_out, bf16, shape, dev, "prev_out"),
+        _dense(prev_lse, f32, (b, s, h), dev, "prev_lse"), b, s, h, d, _dense(out, bf16, shape, dev, "out"),
+        _dense(lse, f32, (b, s, h), dev, "lse"), _workspace_ptr(ws, dev), ws.numel(), _raw_stream(dev.index))
+    if st:
+        _check(st, "sti_attn_paged")
+    return out

@@ -3,6 +3,7 @@
 // synchronisation (except sti_read_device_status), no torch types.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -1089,6 +1090,227 @@ sti_status sti_kv_evict(float* row_weight, int64_t row_weight_bstride, int32_t* 
         if ((uint64_t)p.most * p.arr[i].pieces > 0xFFFFFFFFu) return STI_ERR_UNSUPPORTED;
     const cudaError_t e = sti::launch_kv_evict(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_kv_evict");
+}
+
+// ------------------------------------------------------------------ paged latent cache
+
+sti_status sti_rope_freqs(int rope_dims, double theta, double factor, int orig_len, double beta_fast, double beta_slow,
+                          uint64_t* turns) {
+    if (!turns || rope_dims < 2 || rope_dims % 2 != 0 || orig_len < 0) return STI_ERR_INVALID_ARG;
+    if (!(theta > 1.0) || !isfinite(theta) || !(factor > 0.0) || !isfinite(factor) || !(beta_slow > 0.0) ||
+        !(beta_fast > beta_slow) || !isfinite(beta_fast))
+        return STI_ERR_INVALID_ARG;
+    if (rope_dims > 1024) return STI_ERR_UNSUPPORTED;
+    const double two_pi = 6.283185307179586476925;
+    auto pair_of = [&](double n) { return rope_dims * log(orig_len / (two_pi * n)) / (2.0 * log(theta)); };
+    double low = 0.0, high = 0.0;
+    if (orig_len > 0) {
+        low = fmax(floor(pair_of(beta_fast)), 0.0);
+        high = fmin(ceil(pair_of(beta_slow)), rope_dims - 1.0);
+    }
+    for (int i = 0; i < rope_dims / 2; ++i) {
+        double f = pow(theta, -2.0 * i / rope_dims);
+        if (factor != 1.0) {
+            const double ramp = orig_len > 0 ? fmin(fmax((i - low) / fmax(high - low, 0.001), 0.0), 1.0) : 1.0;
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        double t = f / two_pi;
+        t -= floor(t);                                    // whole turns do not matter (factor < 1)
+        turns[i] = (uint64_t)ldexp(t, 64);                // (t < 1, 53 bits: below 2^64)
+    }
+    return STI_OK;
+}
+
+// Arguments that the two callers of norm_rope's kernel share.
+static sti_status norm_rope_args(sti::NormRopeParams* p, const uint16_t* x, int64_t x_bstride, int64_t x_tstride,
+                                 const int32_t* pos, const int32_t* n_new, int b, int seqlen, int h, int d, int norm,
+                                 const uint16_t* weight, float eps, const uint64_t* turns, int rope_dims, int rope_off,
+                                 int rope_flags, float rope_gain) {
+    if (b < 0 || seqlen < 1 || h < 1 || d < 1 || rope_dims < 0 || rope_off < 0 || (rope_flags & ~3) != 0 || !(eps >= 0.f))
+        return STI_ERR_INVALID_ARG;
+    if (d % 8 != 0 || d > 1024 || (double)b * seqlen * h >= 2147483648.0) return STI_ERR_UNSUPPORTED;
+    if (rope_dims > 0 && (rope_off % 8 != 0 || rope_dims % (rope_flags & STI_ROPE_HALVES ? 16 : 8) != 0))
+        return STI_ERR_UNSUPPORTED;
+    if ((int64_t)rope_off + rope_dims > d || (weight && !norm)) return STI_ERR_INVALID_ARG;
+    if (b == 0) return STI_OK;
+    if (!x || !pos || !aligned(x, 16) || x_bstride % 8 != 0 || x_tstride % 8 != 0 || !aligned(weight, 16) ||
+        (rope_dims > 0 && (!turns || !aligned(turns, 8))))
+        return STI_ERR_INVALID_ARG;
+    p->x = x;
+    p->x_bstride = x_bstride;
+    p->x_tstride = x_tstride;
+    p->pos = pos;
+    p->n_new = n_new;
+    p->weight = weight;
+    p->turns = turns;
+    p->eps = eps;
+    p->gain = rope_gain;
+    p->B = b;
+    p->s = seqlen;
+    p->h = h;
+    p->d = d;
+    p->norm = norm != 0;
+    p->rd = rope_dims;
+    p->off = rope_off;
+    p->halves = (rope_flags & STI_ROPE_HALVES) != 0;
+    p->inverse = (rope_flags & STI_ROPE_INVERSE) != 0;
+    return STI_OK;
+}
+
+// Rows of n elements at base + i*bstride + j*tstride (i < b, j < s) are apart from one another.
+static bool rows_apart(int64_t bstride, int64_t tstride, int b, int s, int64_t n) {
+    if (s > 1 && tstride < n) return false;
+    return b == 1 || (bstride >= (s - 1) * tstride + n) || (tstride >= (b - 1) * bstride + n && bstride >= n);
+}
+
+sti_status sti_norm_rope(const uint16_t* x, int64_t x_bstride, int64_t x_tstride, const int32_t* pos, int pos_per_token,
+                         const int32_t* n_new, int b, int seqlen, int h, int d, int norm, const uint16_t* weight,
+                         float eps, const uint64_t* turns, int rope_dims, int rope_off, int rope_flags,
+                         float rope_gain, uint16_t* y, int64_t y_bstride, int64_t y_tstride, sti_stream stream) {
+    sti::NormRopeParams p{};
+    const sti_status st = norm_rope_args(&p, x, x_bstride, x_tstride, pos, n_new, b, seqlen, h, d, norm, weight, eps,
+                                         turns, rope_dims, rope_off, rope_flags, rope_gain);
+    if (st != STI_OK || b == 0) return st;
+    const int64_t n = (int64_t)h * d;
+    if (!y || !aligned(y, 16) || y_bstride % 8 != 0 || y_tstride % 8 != 0 || x_bstride < 0 || x_tstride < 0 ||
+        y_bstride < 0 || y_tstride < 0 || !rows_apart(y_bstride, y_tstride, b, seqlen, n))
+        return STI_ERR_INVALID_ARG;
+    const bool same = (b == 1 || x_bstride == y_bstride) && (seqlen == 1 || x_tstride == y_tstride);
+    if (x == y) {
+        if (!same) return STI_ERR_INVALID_ARG;
+    } else {
+        auto extent = [&](int64_t bs, int64_t ts) { return (size_t)((b - 1) * bs + (seqlen - 1) * ts + n) * 2; };
+        if (overlap(x, extent(x_bstride, x_tstride), y, extent(y_bstride, y_tstride))) {
+            // fine where they are parts of the same tokens that lie apart in each
+            if (!same || seqlen < 2 || (b > 1 && x_bstride % x_tstride != 0)) return STI_ERR_INVALID_ARG;
+            const int64_t gap = (y > x ? y - x : x - y) % x_tstride;
+            if (gap < n || x_tstride - gap < n) return STI_ERR_INVALID_ARG;
+        }
+    }
+    p.pos_per_token = pos_per_token != 0;
+    p.y = y;
+    p.y_bstride = y_bstride;
+    p.y_tstride = y_tstride;
+    const cudaError_t e = sti::launch_norm_rope(p, sti::device_num_sms(), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_norm_rope");
+}
+
+static bool pages_ok(const uint16_t* pages, int64_t page_stride, int n_pages, int page_size, int d, const int32_t* table,
+                     int64_t table_stride, int max_pages, int b) {
+    if (!table || (b > 1 && table_stride < max_pages)) return false;
+    return n_pages == 0 || (pages && aligned(pages, 16) && page_stride % 8 == 0 && page_stride >= (int64_t)page_size * d);
+}
+
+sti_status sti_kv_append_paged(const uint16_t* x, int64_t x_bstride, int64_t x_tstride, const int32_t* start_pos,
+                               const int32_t* n_new, int b, int seqlen, int d, int norm, const uint16_t* weight,
+                               float eps, const uint64_t* turns, int rope_dims, int rope_off, int rope_flags,
+                               float rope_gain, uint16_t* pages, int64_t page_stride, int n_pages, int page_size,
+                               const int32_t* table, int64_t table_stride, int max_pages, void* ws, sti_stream stream) {
+    if (ws && !aligned(ws, sti::kWsAlign)) return STI_ERR_INVALID_ARG;
+    if (n_pages < 0 || page_size < 1 || max_pages < 0 || (rope_flags & STI_ROPE_INVERSE)) return STI_ERR_INVALID_ARG;
+    sti::NormRopeParams p{};
+    const sti_status st = norm_rope_args(&p, x, x_bstride, x_tstride, start_pos, n_new, b, seqlen, 1, d, norm, weight, eps,
+                                         turns, rope_dims, rope_off, rope_flags, rope_gain);
+    if (st != STI_OK || b == 0) return st;
+    if (x_bstride < 0 || x_tstride < 0 ||
+        !pages_ok(pages, page_stride, n_pages, page_size, d, table, table_stride, max_pages, b))
+        return STI_ERR_INVALID_ARG;
+    if (n_pages > 0 && overlap(x, (size_t)((b - 1) * x_bstride + (seqlen - 1) * x_tstride + d) * 2, pages,
+                               (size_t)((n_pages - 1) * page_stride + (int64_t)page_size * d) * 2))
+        return STI_ERR_INVALID_ARG;
+    p.pages = pages;
+    p.page_stride = page_stride;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.n_pages = n_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.status = ws ? status_word(ws) : nullptr;
+    const cudaError_t e = sti::launch_norm_rope(p, sti::device_num_sms(), static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_kv_append_paged");
+}
+
+// attention workspace: [status | split records | partial (max, sum) | partial outputs], of the attention over the fp4
+// cache with the largest grid
+struct AttnPagedLayout {
+    size_t rec, ml, o, end;
+};
+static AttnPagedLayout attn_paged_layout(int b, int seqlen, int h, int d) {
+    AttnPagedLayout l;
+    const sti::AttnPagedPlan pl = sti::attn_paged_plan(b, seqlen, h, kMaxCacheRows, 0, 0, kAttnFp4MaxSms);
+    l.rec = sti::kWsStatusBytes;
+    l.ml = sti::align_up(l.rec + (size_t)pl.grid * sizeof(int2), sti::kWsAlign);
+    l.o = sti::align_up(l.ml + (size_t)2 * pl.grid * 64 * sizeof(float2), sti::kWsAlign);
+    l.end = sti::align_up(l.o + (size_t)2 * pl.grid * pl.pack * h * d * sizeof(float), sti::kWsAlign);
+    return l;
+}
+
+size_t sti_attn_paged_workspace_size(int b, int seqlen, int h, int d) {
+    if (b <= 0 || seqlen < 1 || h < 1 || h > 64 || d < 1 || d > 512) return sti::kWsStatusBytes;
+    return attn_paged_layout(b, seqlen, h, d).end;
+}
+
+sti_status sti_attn_paged(const uint16_t* q, const uint16_t* pages, int64_t page_stride, int n_pages, int page_size,
+                          const int32_t* table, int64_t table_stride, int max_pages, const int32_t* start_pos,
+                          const int32_t* n_new, int window, int n_first, const float* attn_sink, float softmax_scale,
+                          const uint16_t* prev_out, const float* prev_lse, int b, int seqlen, int h, int d,
+                          uint16_t* out, float* lse, void* ws, size_t ws_bytes, sti_stream stream) {
+    if (b < 0 || seqlen < 1 || h < 1 || d < 1 || n_pages < 0 || page_size < 1 || max_pages < 0 || window < 0 || n_first < 0)
+        return STI_ERR_INVALID_ARG;
+    if (h > 64 || d % 64 != 0 || d > 512 || (double)b * seqlen * h >= 2147483648.0 ||
+        (int64_t)max_pages * page_size > kMaxCacheRows)
+        return STI_ERR_UNSUPPORTED;
+    if (!prev_out != !prev_lse) return STI_ERR_INVALID_ARG;
+    if (b == 0) return STI_OK;
+    if (!ws_ok(ws, ws_bytes, sti_attn_paged_workspace_size(b, seqlen, h, d))) return STI_ERR_INVALID_ARG;
+    if (!q || !start_pos || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(prev_out, 16))
+        return STI_ERR_INVALID_ARG;
+    if (max_pages > 0 && !pages_ok(pages, page_stride, n_pages, page_size, d, table, table_stride, max_pages, b))
+        return STI_ERR_INVALID_ARG;
+    const size_t o_bytes = (size_t)b * seqlen * h * d * 2, l_bytes = (size_t)b * seqlen * h * 4;
+    const size_t c_bytes = n_pages > 0 && max_pages > 0 ? (size_t)((n_pages - 1) * page_stride + (int64_t)page_size * d) * 2 : 0;
+    if (overlap(out, o_bytes, q, o_bytes) || (out != prev_out && overlap(out, o_bytes, prev_out, o_bytes)) ||
+        overlap(out, o_bytes, pages, c_bytes) || overlap(lse, l_bytes, prev_lse, l_bytes))
+        return STI_ERR_INVALID_ARG;
+    const AttnPagedLayout l = attn_paged_layout(b, seqlen, h, d);
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    sti::AttnPagedParams p{};
+    p.pages = pages;
+    p.page_stride = page_stride;
+    p.table = table;
+    p.table_stride = table_stride;
+    p.start_pos = start_pos;
+    p.n_new = n_new;
+    p.sink = attn_sink;
+    p.prev_out = prev_out;
+    p.prev_lse = prev_lse;
+    p.out = out;
+    p.lse = lse;
+    p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+    p.B = b;
+    p.s = seqlen;
+    p.h = h;
+    p.d = d;
+    p.n_pages = n_pages;
+    p.page_size = page_size;
+    p.cap = max_pages * page_size;
+    p.window = window;
+    p.n_first = n_first;
+    p.status = status_word(ws);
+    p.rec = reinterpret_cast<int2*>(wsb + l.rec);
+    p.part_ml = reinterpret_cast<float2*>(wsb + l.ml);
+    p.part_o = reinterpret_cast<float*>(wsb + l.o);
+    const int sms = sti::device_num_sms();
+    const sti::AttnPagedPlan pl =
+        sti::attn_paged_plan(b, seqlen, h, p.cap, window, n_first, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms);
+    p.pack = pl.pack;
+    p.groups = pl.groups;
+    p.grid = pl.grid;
+    CUtensorMap tm_q;
+    const sti_status st = make_map_2d(&tm_q, q, (uint64_t)d, (uint64_t)b * seqlen * h, (uint64_t)d * 2, 64, 64);
+    if (st != STI_OK) return st;
+    const cudaError_t e = sti::launch_attn_paged(tm_q, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_attn_paged");
 }
 
 sti_status sti_selftest_wait_timeout(void* ws, size_t ws_bytes, uint32_t limit_us, sti_stream stream) {

@@ -1,0 +1,764 @@
+// attn_paged.cu -- attention of a step's queries over a paged cache of bf16 rows: the whole context, or a sliding
+// window and the first tokens.
+//
+// Query (b, t) at position P = start_pos + t sees the positions p <= P with p > P - window or p < n_first (window 0: all
+// p <= P).  Position p is row p % page_size of page table[b, p / page_size]; a row serves as key and value for all heads:
+//   s_hp = softmax_scale q_h . k_p,  L_h = ln(sum_p e^{s_hp} + e^{sink_h} + e^{prev_lse_h})
+//   out_h = (sum_p e^{s_hp} k_p + e^{prev_lse_h} prev_out_h) / e^{L_h}
+//
+// The rows that a group's queries see together form its list: the first min(n_first, lo) positions, then lo .. hi (lo:
+// the first query's window).  Lists are cut into tiles of 64 rows wherever those lie, so a page may end anywhere in
+// a tile and a window of 128 rows is two tiles at any position.  The groups' tiles form one long list that is cut into equal
+// contiguous pieces, one per CTA and SM (sti_attn_tiles.cuh); what a CTA has of a query that others share leaves as an
+// fp32 partial, which merge_kernel joins.  Two tile buffers; 20 warps:
+//   * warps 8..15 fill the tiles: a tile's rows come into registers (64 KB in all, a third buffer) while the buffers are
+//     in use, and are stored to the free buffer as the PV two tiles earlier releases its halves.  Rows that nothing
+//     sees are not read and stored as zeros, so that P = 0 meets no NaN;
+//   * warp 19 loads Q by TMA as soon as the last QK of the query before has read the buffer;
+//   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128 dims
+//     per block, K = the rows of the tile, the same tile read as an MN-major operand);
+//   * warp 18 asks for the rows of the next tiles, into L2;
+//   * warps 0..7 run the online softmax (two sets of 32 heads; what P is relative to moves only when a score passes it
+//     by 2^8) and write the outputs.
+//
+// P is rounded to bf16 for the PV product, as the rows are bf16 and one MMA takes one type: each row's share of the output
+// is off by at most 2^-8 of itself, as much as the output's own rounding.  Its sum is taken before, in fp32.
+#include <cuda_bf16.h>
+
+#include "sti_attn_tiles.cuh"
+#include "sti_internal.h"
+
+namespace sti {
+
+// ------------------------------------------------------------------ queries and the rows they see
+
+// `pack` consecutive queries of a sequence whose heads together fill the 64 rows of Q (pack = 1: one query).  In memory
+// they are one query of pack * h heads.  heads 0: only padding.
+struct PagedGroup {
+    int b, t0, heads;
+    int64_t row0;       // of q, out, prev_out, lse, prev_lse: their first head
+};
+// A list of rows: row i is position i for i < nf, else lo + (i - nf).
+struct PagedRows {
+    int nf, lo, n;
+};
+__device__ __forceinline__ int paged_new(const AttnPagedParams& p, int b) {
+    return p.n_new ? min(max(__ldg(p.n_new + b), 0), p.s) : p.s;
+}
+__device__ __forceinline__ PagedGroup group_of(const AttnPagedParams& p, int u) {
+    PagedGroup g;
+    g.b = u / p.groups;
+    g.t0 = (u - g.b * p.groups) * p.pack;
+    g.heads = max(min(p.pack, paged_new(p, g.b) - g.t0), 0) * p.h;
+    g.row0 = ((int64_t)g.b * p.s + g.t0) * p.h;
+    return g;
+}
+// first position that the query at position P sees through the window (start_pos < 2^31 and t < 2^30: 32 unsigned bits)
+__device__ __forceinline__ uint32_t window_start(const AttnPagedParams& p, uint32_t P) {
+    return p.window > 0 && P + 1u > (uint32_t)p.window ? P + 1u - (uint32_t)p.window : 0u;
+}
+__device__ __forceinline__ PagedRows rows_of(const AttnPagedParams& p, int b, int u) {
+    const int t0 = u * p.pack, t1 = min(t0 + p.pack, paged_new(p, b));
+    PagedRows r{0, 0, 0};
+    if (t0 >= t1) return r;
+    const uint32_t start = (uint32_t)__ldg(p.start_pos + b);
+    const uint32_t hi = min(start + (uint32_t)t1, (uint32_t)p.cap);   // positions past the table have no row
+    r.lo = (int)min(window_start(p, start + (uint32_t)t0), hi);
+    r.nf = min(p.n_first, r.lo);
+    r.n = r.nf + (int)hi - r.lo;
+    return r;
+}
+__device__ __forceinline__ int group_rows(const AttnPagedParams& p, int b, int u) { return rows_of(p, b, u).n; }
+__device__ __forceinline__ bool head_seen(const AttnPagedParams&, const PagedGroup&, int, bool any) { return any; }
+
+namespace {
+
+// registers per thread after setmaxnreg: 256 x 120, 128 x 48 and the loading warps' 256 x 96 of the launch, 61,440 in
+// all, the 640 x 96 of the launch
+constexpr int kRegsSoft = 120, kRegsMma = 48;
+constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
+constexpr int kAhead = 4;                      // tiles whose rows are asked for ahead
+constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
+
+struct __align__(16) Tail {
+    float neg_m[2][4][32];    // [head group][warp of the group]: its copy of -reference
+    float2 fac[2][4][32];     // the outputs' factors
+    float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
+    float lsum[2][4][32];
+    int vis[2][64];           // [segment parity] per head: which rows of the list it sees (kPack), see head_vis
+    uint8_t valid[2][8], bad[2][8];   // [buffer][loading warp]: bit j: row 8 warp + j exists / held a non-finite value
+    Work work;
+    long long scratch[kThreads / 32];
+    uint64_t full[2][2];      // [buffer][half of the dims] filled: one arrival per loading warp
+    uint64_t freed[2][2];     // the PV has read it
+    uint64_t s_full[2], p_full[2];
+    uint64_t q_full, q_free;
+    uint32_t tmem_base;
+    int abort;
+    int qk_tile;              // tiles whose QK was issued, for the prefetching warp
+};
+
+size_t attn_paged_smem(int d) {
+    const int n_cb = (d + 127) / 128 * 2;
+    return 1024 + (size_t)n_cb * (kQBlk + 2 * kTBlk) + 2 * kPBuf + sizeof(Tail);
+}
+
+// Where row i of the group's list lies, 0 if there is none (past the list; a page outside the pool).
+__device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, int b, const PagedRows& r, int i) {
+    if (i >= r.n) return nullptr;
+    const uint32_t pos = (uint32_t)(i < r.nf ? i : r.lo + (i - r.nf));
+    const uint32_t pg = pos / (uint32_t)p.page_size;
+    const int id = __ldg(p.table + (int64_t)b * p.table_stride + pg);
+    if (id < 0 || id >= p.n_pages) {
+        if (p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+        return nullptr;
+    }
+    return p.pages + (int64_t)id * p.page_stride + (int64_t)(pos - pg * (uint32_t)p.page_size) * p.d;
+}
+
+__device__ __forceinline__ uint4 load_once(const uint16_t* p) {   // not kept in L1: the CTA reads it once
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Some bf16 among the eight is an infinity or NaN.
+__device__ __forceinline__ bool non_finite(const uint4& v) {
+    const uint32_t e = 0x7F807F80u;
+    return (__vcmpeq2(v.x & e, e) | __vcmpeq2(v.y & e, e) | __vcmpeq2(v.z & e, e) | __vcmpeq2(v.w & e, e)) != 0u;
+}
+
+// Which rows of the group's list head hd sees: i < n - (v >> 8), and i >= nf + (v & 255) or i < n_first (row i < n_first is
+// position i; queries of a group are at most 63 positions apart).
+__device__ __forceinline__ int head_vis(const AttnPagedParams& p, const PagedGroup& g, const PagedRows& r, int hd) {
+    if (hd >= g.heads) return 0x7FFFFF00;   // none of a list that short; what it sees of another goes nowhere
+    const uint32_t P = (uint32_t)__ldg(p.start_pos + g.b) + (uint32_t)(g.t0 + hd / p.h);
+    const uint32_t hi = (uint32_t)(r.lo + (r.n - r.nf));
+    const uint32_t end = min(P + 1u, hi);
+    const uint32_t lo = min(max(window_start(p, P), (uint32_t)r.lo), hi);
+    return (int)((hi - end) << 8 | (lo - (uint32_t)r.lo));
+}
+
+template <int NM, bool kPack>   // d-blocks of 128 dims; groups of several queries
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnPagedParams p) {
+    constexpr int kHalves = (NM + 1) / 2;
+    constexpr uint32_t kTile = 2 * NM * kTBlk;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int n_cb = p.d / 64;                 // column blocks of 64 dims
+    uint8_t* q_s = smem;                       // [2 NM][64 heads][128 B]
+    uint8_t* t_s = q_s + 2 * NM * kQBlk;       // two tiles [2 NM][64 rows][128 B]
+    uint8_t* p_s = t_s + 2 * kTile;            // two P^T [64 rows][64 heads] bf16
+    Tail* tl = reinterpret_cast<Tail*>(p_s + 2 * kPBuf);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nq = p.B * p.groups;
+    const int hp = p.pack * p.h;               // heads of a full group
+    const int sets = hp > 32 ? 2 : 1;          // sets of 32 heads
+    volatile int* abort = &tl->abort;
+
+    if (warp == 16) {
+        tmem_alloc(&tl->tmem_base, NM <= 2 ? 256 : 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int k = 0; k < 2; ++k) {
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&tl->full[k][h], 8);
+                mbar_init(&tl->freed[k][h], 1);
+            }
+            mbar_init(&tl->s_full[k], 1);
+            mbar_init(&tl->p_full[k], 4 * sets);
+        }
+        mbar_init(&tl->q_full, 1);
+        mbar_init(&tl->q_free, 1);
+        tl->abort = 0;
+        tl->qk_tile = 0;
+        fence_mbar_init();
+    }
+    zero_padding(64, n_cb, NM, q_s, t_s);      // (Q's rows all come by TMA)
+    fence_proxy_async_smem();
+    plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
+              [&](int q) { return (group_rows(p, q / p.groups, q % p.groups) + kRows - 1) / kRows; });
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);   // warp-uniform, as the compiler can see
+    const Work wk = tl->work;
+    griddep_launch_dependents();
+
+    if (warp >= 16) {
+        regs_down<kRegsMma>();
+        const int n_mma = (hp + 15) / 16 * 16;
+        uint32_t n = 0;
+        bool ok = true;   // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = warp_wait(bar, parity, p.status, abort);
+            tc_fence_after();
+            return ok;
+        };
+        Walk walk(wk);
+        Seg sg;
+        if (warp == 16) {
+            // -------------------------------------------------------------- QK: the tile and Q, both K-major
+            const uint32_t idesc = idesc_bf16_f32(kRows, n_mma, false, false);
+            const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
+            uint32_t qn = 0;
+            int2 rec = make_int2(-1, 0);
+            while (ok && walk.next(p, sg)) {
+                if (sg.t0 == 0 && sg.t1 < sg.nt) {
+                    const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
+                    int c = (int)(last * wk.ctas / wk.total);
+                    while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
+                    while ((long long)c * wk.total / wk.ctas > last) --c;
+                    rec = make_int2(sg.q, c);
+                }
+                if (!wait(&tl->q_full, qn & 1u)) break;
+                ++qn;
+                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
+                    if (lane == 0) tl->qk_tile = (int)n;
+                    const uint32_t buf = n & 1u;   // its S^T has been read: the tile was filled after the PV of n - 2
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
+                                qk_blocks(m, tmem + 64u * buf, lo32(dk) + buf * (kTile / 16), lo32(dq), hi32(dk), idesc);
+                            if (h == kHalves - 1) {
+                                umma_commit(&tl->s_full[buf]);
+                                if (t == sg.t1 - 1) umma_commit(&tl->q_free);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+            if (lane == 0) p.rec[blockIdx.x] = rec;
+        } else if (warp == 17) {
+            // -------------------------------------------------------------- PV: the tile and P^T, both MN-major
+            const uint32_t idesc = idesc_bf16_f32(128, n_mma, true, true);
+            const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128), dp = sdesc(smem_u32(p_s), kPBuf, 1024, kLayoutSW128);
+            while (ok && walk.next(p, sg)) {
+                for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+                    const uint32_t buf = n & 1u;
+                    const int steps = min(4, (sg.vis - t * kRows + 15) / 16);   // of 16 rows
+                    if (!wait(&tl->p_full[buf], (n >> 1) & 1u)) break;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int m = 0; m < NM; ++m) {
+                            const uint32_t o = tmem + kTmO + 64u * (uint32_t)m;
+                            const uint32_t a = lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16);
+                            const uint32_t b = lo32(dp) + buf * (kPBuf / 16);
+                            if (steps < 4) {
+                                if (t == sg.t0) umma<false>(o, a, hi32(dv), b, hi32(dp), idesc);
+                                else umma<true>(o, a, hi32(dv), b, hi32(dp), idesc);
+                                for (int k = 1; k < steps; ++k)
+                                    umma<true>(o, a + 128u * (uint32_t)k, hi32(dv), b + 128u * (uint32_t)k, hi32(dp), idesc);
+                            } else if (t == sg.t0) {
+                                pv_block<true>(o, a, hi32(dv), b, hi32(dp), idesc);
+                            } else {
+                                pv_block<false>(o, a, hi32(dv), b, hi32(dp), idesc);
+                            }
+                            if ((m & 1) || m == NM - 1) umma_commit(&tl->freed[buf][m >> 1]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp == 18) {
+            // The rows of the next kAhead tiles are on their way to L2 when a tile is loaded, asked for by a
+            // sequence's first query only: the others find them there.
+            volatile int* now = &tl->qk_tile;
+            bool on = true;
+            while (on && walk.next(p, sg)) {
+                const int u = sg.q - sg.b * p.groups;
+                const PagedRows rows = rows_of(p, sg.b, u);
+                for (int t = sg.t0; on && t < sg.t1; ++t, ++n) {
+                    if (u != 0) continue;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint16_t* at = row_ptr(p, sg.b, rows, t * kRows + lane + 32 * k);
+                        if (at) prefetch_l2_bulk(at, 2u * (uint32_t)p.d);
+                    }
+                    // wait (a while at most) until the tile kAhead before is at hand
+                    for (int i = 0; on; ++i) {
+                        if (__all_sync(kWarpFull, *now + kAhead >= (int)n)) break;
+                        on = __all_sync(kWarpFull, i < 100000 && !*abort);
+                        __nanosleep(200);
+                    }
+                }
+            }
+        } else if (lane == 0) {
+            // -------------------------------------------------------------- Q
+            uint32_t qn = 0;
+            while (walk.next(p, sg)) {
+                const int64_t row0 = ((int64_t)sg.b * p.s + (int64_t)(sg.q - sg.b * p.groups) * p.pack) * p.h;
+                if (qn > 0 && !tile_wait(&tl->q_free, (qn - 1) & 1u, p.status, abort)) break;
+                ++qn;
+                // rows past the group's heads are other queries', or zeros past the last: columns of S^T that nothing uses
+                mbar_arrive_expect_tx(&tl->q_full, (uint32_t)n_cb * kQBlk);
+                for (int cb = 0; cb < n_cb; ++cb) tma_load_2d(q_s + cb * kQBlk, &tm_q, &tl->q_full, 64 * cb, (int)row0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // -------------------------------------------------------------- tiles
+        // The warp's rows are 8 lw .. 8 lw + 7 of each tile, a lane holds 8 of every 256 dims of each.  Three tiles are under
+        // way: one being stored, its successor's rows being loaded after that, the one after's pages looked up.
+        const int lw = warp - 8;
+        Walk walk(wk);
+        Seg sg;
+        PagedRows rows{0, 0, 0};
+        bool more = walk.next(p, sg);
+        int t = 0;
+        if (more) {
+            rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
+            t = sg.t0;
+        }
+        auto look_up = [&]() -> const uint16_t* {   // the next tile's rows: lane j < 8 has row 8 lw + j's place
+            if (!more) return nullptr;
+            const uint16_t* at = lane < 8 ? row_ptr(p, sg.b, rows, t * kRows + 8 * lw + lane) : nullptr;
+            if (++t == sg.t1) {
+                more = walk.next(p, sg);
+                if (more) {
+                    rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
+                    t = sg.t0;
+                }
+            }
+            return at;
+        };
+        uint4 v[8][kHalves];
+        const int chunks = p.d / 8;
+        auto load = [&](const uint16_t* at) {       // returns which rows exist
+            const unsigned long long a = reinterpret_cast<unsigned long long>(at);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(kWarpFull, a, j));
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    v[j][h] = make_uint4(0, 0, 0, 0);
+                    if (src && lane + 32 * h < chunks) v[j][h] = load_once(src + 8 * (lane + 32 * h));
+                }
+            }
+            return __ballot_sync(kWarpFull, at != nullptr) & 0xFFu;
+        };
+        uint32_t left = (uint32_t)(wk.hi - wk.lo);
+        uint32_t have = load(look_up());
+        const uint16_t* next = look_up();
+        bool dead = false;
+        for (uint32_t n = 0; n < left && !dead; ++n) {
+            const uint32_t buf = n & 1u;
+            uint32_t bad = 0;
+            if (kPack) {   // such a row is stored as zeros, so that P = 0 keeps it from the heads that do not see it
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    bool b = false;
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) b = b || non_finite(v[j][h]);
+                    if (__any_sync(kWarpFull, b)) {
+                        bad |= 1u << j;
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) v[j][h] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            uint8_t* dst = t_s + buf * kTile + (size_t)(lane >> 3) * kTBlk + 8 * lw * 128;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                if (n >= 2 && !warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort)) {
+                    dead = true;
+                    break;
+                }
+                if (lane + 32 * h < chunks) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(dst + 4 * h * kTBlk + j * 128 + (((lane & 7) ^ j) << 4)) = v[j][h];
+                }
+                if (h == 0 && lane == 0) {
+                    tl->valid[buf][lw] = (uint8_t)have;
+                    tl->bad[buf][lw] = (uint8_t)bad;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tl->full[buf][h]);
+            }
+            have = load(next);
+            next = look_up();
+        }
+    } else {
+        regs_up<kRegsSoft>();
+        // -------------------------------------------------------------- softmax, outputs
+        const int set = warp >> 2, qd = warp & 3;
+        const int row = 16 * qd + (lane >> 2);   // this thread's tile rows: row, row + 8
+        const int l4 = lane & 3;                 // its heads: 32 set + 8 g + 2 l4 + {0, 1}
+        const bool active = set < sets;          // this warp's set has heads
+        const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
+        const uint32_t bar_set = 1u + (uint32_t)set;
+        const float c = p.scale_log2;
+        uint32_t n = 0;
+        bool dead = false;
+        float m_run = -INFINITY;                 // what P is relative to, in log2: lane l: head 32 set + l
+        float l_thr[8];                          // running sums of the thread's heads over its rows
+        uint32_t saw = 0;                        // bit i: its head i saw a row
+
+        auto mwait = [&](uint64_t* bar, uint32_t parity) {
+            if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
+        };
+
+        // One tile's probabilities 2^(S c - m), m the head's reference.
+        float nm[8];
+        auto load_m = [&]() {   // from the warp's copy, which has every head of the group
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float2 v = *reinterpret_cast<const float2*>(&tl->neg_m[set][qd][8 * g + 2 * l4]);
+                nm[2 * g] = v.x;
+                nm[2 * g + 1] = v.y;
+            }
+        };
+        int hv[8] = {};              // kPack: which rows each of the thread's heads sees
+        // i0: this thread's first row of the list
+        auto softmax = [&](const PagedRows& rows, int i0, bool first) {
+            const uint32_t buf = n & 1u;
+            mwait(&tl->s_full[buf], (n >> 1) & 1u);
+            mwait(&tl->full[buf][0], (n >> 1) & 1u);   // (complete; makes `valid` visible)
+            tc_fence_after();
+            const uint32_t ts = tmem + lane_base + 64u * buf + 32u * (uint32_t)set;
+            uint32_t r[16];
+            tmem_ld_rows16(ts, r);
+            const uint32_t val = *reinterpret_cast<const uint16_t*>(&tl->valid[buf][2 * qd]) >> (lane >> 2);
+            const bool v0 = (val & 1u) && !dead, v1 = (val & 0x100u) && !dead;
+            auto sees = [&](int i, int second) {   // the thread's head i its first or second row
+                const bool v = second ? v1 : v0;
+                if (!kPack) return v;
+                const int at = i0 + 8 * second;
+                return v && at < rows.n - (hv[i] >> 8) && (at >= rows.nf + (hv[i] & 255) || at < p.n_first);
+            };
+            tmem_ld_wait();
+            if (kPack) {
+                const uint32_t bad = *reinterpret_cast<const uint16_t*>(&tl->bad[buf][2 * qd]) >> (lane >> 2);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (bad & 1u) r[4 * g] = r[4 * g + 1] = 0x7FFFFFFFu;
+                    if (bad & 0x100u) r[4 * g + 2] = r[4 * g + 3] = 0x7FFFFFFFu;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) saw |= (sees(i, 0) || sees(i, 1)) ? 1u << i : 0u;
+            } else {
+                saw |= v0 || v1 ? 0xFFu : 0u;
+            }
+            float y[16];
+            float top0 = -INFINITY, top1 = -INFINITY;
+            auto scale = [&]() {
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[4 * g + k] = fmaf(__uint_as_float(r[4 * g + k]), c, nm[2 * g + (k & 1)]);
+            };
+            scale();
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                if (kPack) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (sees(2 * g + (k & 1), k >> 1)) top0 = fmaxf(top0, y[4 * g + k]);
+                } else {
+                    top0 = fmaxf(top0, fmaxf(y[4 * g], y[4 * g + 1]));
+                    top1 = fmaxf(top1, fmaxf(y[4 * g + 2], y[4 * g + 3]));
+                }
+            }
+            // the references stay unless a visible score passes its head's by 2^8
+            const bool need = !named_bar_and(bar_set, 128, !(first || ((kPack || v0) && top0 > kTopMost) || (v1 && top1 > kTopMost)));
+            if (need) {
+                float* red = &tl->red[buf][set][qd][0];
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float v = fmaxf(sees(2 * g + k, 0) ? y[4 * g + k] : -INFINITY,
+                                        sees(2 * g + k, 1) ? y[4 * g + 2 + k] : -INFINITY);
+#pragma unroll
+                        for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kWarpFull, v, o));
+                        if (lane < 4) red[8 * g + 2 * lane + k] = v;
+                    }
+                named_bar_sync(bar_set, 128);
+                const float* rr = &tl->red[buf][set][0][lane];
+                float* own = &tl->neg_m[set][qd][0];
+                const float mt = fmaxf(fmaxf(rr[0], rr[32]), fmaxf(rr[64], rr[96])) - own[lane];
+                const float m_new = (m_run == -INFINITY || mt > m_run + kTopMost) ? fmaxf(m_run, mt) : m_run;
+                const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
+                m_run = m_new;
+                __syncwarp();
+                // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
+                // scores show in its output
+                own[lane] = m_new == -INFINITY ? 0.f : -m_new;
+                __syncwarp();
+                load_m();
+                scale();
+                if (!first && !dead && __any_sync(kWarpFull, alpha != 1.f)) {
+                    mwait(&tl->freed[buf ^ 1u][kHalves - 1], ((n - 1) >> 1) & 1u);   // the previous tile's PV is done
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < 2 * NM; ++k) {
+                        const uint32_t ta = tmem + lane_base + kTmO + 32u * (uint32_t)(2 * (k >> 1) + set) + 16u * (k & 1);
+                        uint32_t o[16];
+                        tmem_ld16(ta, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(kWarpFull, alpha, 16 * (k & 1) + i));
+                        tmem_st16(ta, o);
+                    }
+                    tmem_st_wait();
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        l_thr[2 * g] *= __shfl_sync(kWarpFull, alpha, 8 * g + 2 * l4);
+                        l_thr[2 * g + 1] *= __shfl_sync(kWarpFull, alpha, 8 * g + 2 * l4 + 1);
+                    }
+                }
+            }
+            uint8_t* prow = p_s + buf * kPBuf + row * 128 + 4 * l4;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float a0 = sees(2 * g, 0) ? fast_exp2(y[4 * g]) : 0.f, a1 = sees(2 * g + 1, 0) ? fast_exp2(y[4 * g + 1]) : 0.f;
+                const float b0 = sees(2 * g, 1) ? fast_exp2(y[4 * g + 2]) : 0.f, b1 = sees(2 * g + 1, 1) ? fast_exp2(y[4 * g + 3]) : 0.f;
+                l_thr[2 * g] += a0 + b0;
+                l_thr[2 * g + 1] += a1 + b1;
+                const int at = ((4 * set + g) ^ (row & 7)) << 4;
+                *reinterpret_cast<uint32_t*>(prow + at) = pack_bf16x2(a0, a1);
+                *reinterpret_cast<uint32_t*>(prow + 8 * 128 + at) = pack_bf16x2(b0, b1);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tl->p_full[buf]);
+        };
+
+        // a segment's O^T and sums: the group's output when the segment holds all its tiles, else a partial
+        // (slot >= 0: where); sink, prev_lse: of head 32 set + lane
+        auto epilogue = [&](int q, int slot, float sink, float prev_lse) {
+            const PagedGroup grp = group_of(p, q);
+            // 16 heads x 32 dims of this warp at a time: k / 2 the d-block, heads 32 set + 16 (k & 1) ...
+            // Pieces of 8 dims, two per lane: piece c = lane + 32 j is head c / 4, dims 8 (c % 4) ...
+            auto piece = [&](int k, int j, int64_t& at) {
+                const int pc = lane + 32 * j;
+                const int hw = 32 * set + 16 * (k & 1) + (pc >> 2), dw = 128 * (k >> 1) + 32 * qd + 8 * (pc & 3);
+                at = (grp.row0 + hw) * p.d + dw;
+                return k < 2 * NM && hw < grp.heads && dw < p.d;
+            };
+            const bool joins = p.prev_out != nullptr && slot < 0;
+            uint4 pre[2][2];   // [k & 1]: prev_out, loaded two steps ahead
+            auto load_prev = [&](int k, uint4* v) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    int64_t at;
+                    v[j] = make_uint4(0, 0, 0, 0);
+                    if (piece(k, j, at)) v[j] = *reinterpret_cast<const uint4*>(p.prev_out + at);
+                }
+            };
+            if (joins) {
+                load_prev(0, pre[0]);
+                load_prev(1, pre[1]);
+            }
+            mwait(&tl->freed[(n - 1) & 1u][kHalves - 1], ((n - 1) >> 1) & 1u);
+            tc_fence_after();
+            uint32_t any = saw;
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) any |= __shfl_xor_sync(kWarpFull, any, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v = l_thr[i];
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(kWarpFull, v, o);
+                // the sum of a head that saw none of the rows is -0, which adds up to -0 over such parts alone
+                if (lane < 4) tl->lsum[set][qd][8 * (i >> 1) + 2 * lane + (i & 1)] = any >> i & 1u ? v : -0.f;
+            }
+            named_bar_sync(bar_set, 128);
+            const float* ls = &tl->lsum[set][0][lane];
+            const float lt = (ls[0] + ls[32]) + (ls[64] + ls[96]);
+            const int hh = 32 * set + lane;
+            float inv = 0.f, wp = 0.f;
+            if (slot >= 0) {
+                if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
+            } else if (signbit(lt) && hh < grp.heads) {
+                // a query that sees no row: what it had
+                wp = prev_lse == -INFINITY ? 0.f : 1.f;
+                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = prev_lse;
+            } else if (hh < grp.heads) {
+                // everything relative to the largest of the reference, the sink and prev_lse
+                const float sk = sink * kLog2e, pl = prev_lse * kLog2e;
+                float mx = fmaxf(m_run, fmaxf(sk, pl));
+                if (mx == -INFINITY) mx = 0.f;
+                const float f = lt == 0.f ? 0.f : m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);   // (inf * 0)
+                const float ep = exp2f(pl - mx);
+                const float den = lt * f + exp2f(sk - mx) + ep;
+                inv = f / den;
+                wp = ep / den;
+                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = (mx + log2f(den)) * kLn2;
+            }
+            // The steps turn O^T over through shared memory, in fp32: lanes hold dims, the pieces are a head's.
+            float* stg = reinterpret_cast<float*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
+            float2* fac = &tl->fac[set][qd][0];
+            fac[lane] = make_float2(inv, wp);
+#pragma unroll 1
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int k = 2 * m + half, h0 = 16 * half;
+                    const int dd = 128 * m + 32 * qd + lane;
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set + (uint32_t)h0, r);
+                    tmem_ld_wait();
+                    if (slot >= 0) {
+                        float* po = p.part_o + ((int64_t)slot * hp + 32 * set + h0) * p.d + dd;
+                        if (dd < p.d) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (32 * set + h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
+                        }
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = __uint_as_float(r[i]);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int pc = lane + 32 * j;
+                        const float2 f = fac[h0 + (pc >> 2)];
+                        const float4* src = reinterpret_cast<const float4*>(stg + (pc >> 2) * 32 + 8 * (pc & 3));
+                        const float4 lo = src[0], hi = src[1];
+                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        const uint32_t pw[4] = {pre[half][j].x, pre[half][j].y, pre[half][j].z, pre[half][j].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x0 = v[2 * i] * f.x, x1 = v[2 * i + 1] * f.x;
+                            if (joins) {   // weight 0: prev_out is not used
+                                x0 = f.y != 0.f ? x0 + f.y * __uint_as_float(pw[i] << 16) : x0;
+                                x1 = f.y != 0.f ? x1 + f.y * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
+                            }
+                            o[i] = dead ? 0u : pack_bf16x2(x0, x1);
+                        }
+                        int64_t at;
+                        if (piece(k, j, at)) *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                    if (joins) load_prev(k + 2, pre[half]);
+                    __syncwarp();
+                }
+        };
+
+        Walk walk(wk);
+        Seg sg;
+        int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
+        float pend_sink = -INFINITY, pend_lse = -INFINITY;   // and what it is joined with
+        int par = 0;                           // segment parity
+        while (walk.next(p, sg)) {
+            const PagedGroup grp = group_of(p, sg.q);
+            const PagedRows rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
+            if (kPack && tid < 64) tl->vis[par][tid] = head_vis(p, grp, rows, tid);   // (every warp is done with par's last)
+            if (tid == 0 && p.prev_out)   // what this segment's end will read, into L2
+                prefetch_l2_bulk(p.prev_out + grp.row0 * p.d, (uint32_t)(grp.heads * p.d) * 2u);
+            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, pend_sink, pend_lse);
+            named_bar_sync(kBarSoft, 256);     // the staging area is every warp's P^T; vis is complete
+            m_run = -INFINITY;
+            tl->neg_m[set][qd][lane] = 0.f;
+            __syncwarp();
+            load_m();
+            if (kPack) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hv[i] = tl->vis[par][32 * set + 8 * (i >> 1) + 2 * l4 + (i & 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
+            saw = 0;
+            for (int t = sg.t0; t < sg.t1; ++t, ++n)
+                if (active) softmax(rows, t * kRows + row, t == sg.t0);
+            par ^= 1;
+            pend_q = sg.q;
+            const int hh = 32 * set + lane;
+            if (hh < grp.heads) {
+                if (p.sink) pend_sink = __ldg(p.sink + (kPack ? hh % p.h : hh));
+                pend_lse = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) : -INFINITY;
+            }
+            pend_slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
+        }
+        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, pend_sink, pend_lse);
+
+        // queries past the table are reported; groups whose lists are empty
+        for (int q = blockIdx.x; q < nq; q += gridDim.x) {
+            const PagedGroup grp = group_of(p, q);
+            if (tid == 0 && grp.heads > 0 && p.status &&
+                (uint32_t)__ldg(p.start_pos + grp.b) + (uint32_t)(grp.t0 + grp.heads / p.h) > (uint32_t)p.cap)
+                atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+            if (grp.heads == 0 || group_rows(p, grp.b, q - grp.b * p.groups) > 0) continue;
+            for (int i = tid; i < grp.heads; i += 256)
+                if (p.lse) p.lse[grp.row0 + i] = p.prev_lse ? p.prev_lse[grp.row0 + i] : -INFINITY;
+            const int chunks = p.d / 8;
+#pragma unroll 4
+            for (int i = tid; i < grp.heads * chunks; i += 256) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (p.prev_out) {
+                    v = reinterpret_cast<const uint4*>(p.prev_out + grp.row0 * p.d)[i];
+                    if (p.prev_lse[grp.row0 + i / chunks] == -INFINITY) v = make_uint4(0, 0, 0, 0);
+                }
+                reinterpret_cast<uint4*>(p.out + grp.row0 * p.d)[i] = v;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (*abort) {   // a wait gave up: let the MMAs and copies in flight finish before the CTA's memory goes
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 50000ull) {
+        }
+    }
+    if (warp == 16) {
+        tc_fence_after();
+        tmem_dealloc(tmem, NM <= 2 ? 256 : 512);
+    }
+}
+
+template <int NM>
+cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStream_t stream) {
+    const int nq = p.B * p.groups;
+    const size_t smem = attn_paged_smem(p.d);
+    auto* kernel = p.pack > 1 ? attn_paged_kernel<NM, true> : attn_paged_kernel<NM, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<p.grid, kThreads, smem, stream>>>(tm_q, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int parts = p.grid / nq + 1;   // of a query, when they are alike
+    const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
+    return parts > 16  ? launch_after(merge_kernel<16, 32, AttnPagedParams>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
+           : parts > 4 ? launch_after(merge_kernel<2, 128, AttnPagedParams>, dim3(mx, mh), 256, 0, stream, p)
+                       : launch_after(merge_kernel<1, 128, AttnPagedParams>, dim3(mx, mh), 128, 0, stream, p);
+}
+
+}  // namespace
+
+AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_first, int num_sms) {
+    AttnPagedPlan l;
+    l.pack = h <= 32 ? 64 / h : 1;   // as attn_fp4_plan
+    if (l.pack > s) l.pack = s;
+    l.groups = (s + l.pack - 1) / l.pack;
+    int64_t rows = cap;              // of a group's list, at most
+    if (window > 0 && (int64_t)window + l.pack - 1 + n_first < rows) rows = (int64_t)window + l.pack - 1 + n_first;
+    const int64_t list = (rows + kRows - 1) / kRows * B * l.groups;
+    l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);
+    return l;
+}
+
+cudaError_t launch_attn_paged(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStream_t stream) {
+    switch ((p.d + 127) / 128) {
+        case 1: return launch_nm<1>(tm_q, p, stream);
+        case 2: return launch_nm<2>(tm_q, p, stream);
+        case 3: return launch_nm<3>(tm_q, p, stream);
+        default: return launch_nm<4>(tm_q, p, stream);
+    }
+}
+
+}  // namespace sti

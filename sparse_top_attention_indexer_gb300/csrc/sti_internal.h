@@ -228,6 +228,60 @@ struct AttnFp4Plan {
 AttnFp4Plan attn_fp4_plan(int B, int s, int h, int n_rows, int num_sms);
 cudaError_t launch_attn_fp4(const AttnFp4Params& p, cudaStream_t stream);
 
+// ------------------------------------------------------------------ paged cache: norm and rotate, append, attend
+struct NormRopeParams {
+    const uint16_t* x;          // bf16 [B, s, h, d], strides of sequences and tokens in elements
+    int64_t x_bstride, x_tstride;
+    const int32_t* pos;         // [B] positions of the first tokens, or [B, s]
+    int pos_per_token;
+    const int32_t* n_new;       // [B] or null: tokens of the step that are real
+    const uint16_t* weight;     // bf16 [d] or null
+    const uint64_t* turns;      // [rd / 2] (rd 0: null): turns per position of each pair, in units of 2^-64
+    float eps, gain;
+    int B, s, h, d, norm;
+    int rd, off, halves, inverse;
+    uint16_t* y;                // bf16 [B, s, h, d], or null: rows of pages (h = 1)
+    int64_t y_bstride, y_tstride;
+    uint16_t* pages;            // bf16 [n_pages, page_size, d], page stride in elements
+    int64_t page_stride;
+    const int32_t* table;       // [B, max_pages], row stride in elements
+    int64_t table_stride;
+    int n_pages, page_size, max_pages;
+    uint32_t* status;           // or null
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t stream);
+
+struct AttnPagedParams {
+    const uint16_t* pages;      // bf16 [n_pages, page_size, d], page stride in elements
+    int64_t page_stride;
+    const int32_t* table;       // [B, *], row stride in elements
+    int64_t table_stride;
+    const int32_t* start_pos;
+    const int32_t* n_new;       // [B] or null
+    const float* sink;          // [h] or null
+    const uint16_t* prev_out;   // bf16 [B, s, h, d] or null
+    const float* prev_lse;      // [B, s, h] or null
+    uint16_t* out;
+    float* lse;                 // [B, s, h] or null
+    float scale_log2;           // softmax_scale * log2(e)
+    int B, s, h, d;
+    int n_pages, page_size;
+    int cap;                    // positions that the table covers
+    int window, n_first;        // window 0: every earlier position
+    uint32_t* status;
+    int grid;                   // CTAs of the attention kernel
+    int2* rec;                  // as in AttnFp4Params
+    float* part_o;
+    float2* part_ml;
+    int pack, groups;
+};
+struct AttnPagedPlan {
+    int pack, groups, grid;     // as in AttnPagedParams
+};
+AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_first, int num_sms);
+// tm_q: q as [B*s*h, d], box 64 x 64
+cudaError_t launch_attn_paged(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device properties
 int device_num_sms();
 
