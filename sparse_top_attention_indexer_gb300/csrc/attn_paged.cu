@@ -11,9 +11,8 @@
 // a tile and a window of 128 rows is two tiles at any position.  The groups' tiles form one long list that is cut into equal
 // contiguous pieces, one per CTA and SM (sti_attn_tiles.cuh); what a CTA has of a query that others share leaves as an
 // fp32 partial, which merge_kernel joins.  Two tile buffers; 20 warps:
-//   * warps 8..15 fill the tiles: a tile's rows come into registers (64 KB in all, a third buffer) while the buffers are
-//     in use, and are stored to the free buffer as the PV two tiles earlier releases its halves.  Rows that nothing
-//     sees are not read and stored as zeros, so that P = 0 meets no NaN;
+//   * warps 8..15 copy the rows to the free buffer (16 bytes per thread and copy, past L1 and the registers) as the PV two
+//     tiles earlier releases its halves.  Rows that nothing sees are not read but zeros, so that P = 0 meets no NaN;
 //   * warp 19 loads Q by TMA as soon as the last QK of the query before has read the buffer;
 //   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128 dims
 //     per block, K = the rows of the tile, the same tile read as an MN-major operand);
@@ -73,9 +72,8 @@ __device__ __forceinline__ bool head_seen(const AttnPagedParams&, const PagedGro
 
 namespace {
 
-// registers per thread after setmaxnreg: 256 x 120, 128 x 48 and the loading warps' 256 x 96 of the launch, 61,440 in
-// all, the 640 x 96 of the launch
-constexpr int kRegsSoft = 120, kRegsMma = 48;
+// registers per thread after setmaxnreg: 256 x 144 + 256 x 64 + 128 x 64 = 61,440, the 640 x 96 of the launch
+constexpr int kRegsSoft = 144, kRegsLoad = 64, kRegsMma = 64;
 constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
 constexpr int kAhead = 4;                      // tiles whose rows are asked for ahead
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
@@ -86,10 +84,10 @@ struct __align__(16) Tail {
     float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
     float lsum[2][4][32];
     int vis[2][64];           // [segment parity] per head: which rows of the list it sees (kPack), see head_vis
-    uint8_t valid[2][8], bad[2][8];   // [buffer][loading warp]: bit j: row 8 warp + j exists / held a non-finite value
+    uint8_t valid[2][8];      // [buffer][loading warp]: bit j: row 8 warp + j exists
     Work work;
     long long scratch[kThreads / 32];
-    uint64_t full[2][2];      // [buffer][half of the dims] filled: one arrival per loading warp
+    uint64_t full[2][2];      // [buffer][half of the dims] filled: every loading thread's copies (and each warp's `valid`)
     uint64_t freed[2][2];     // the PV has read it
     uint64_t s_full[2], p_full[2];
     uint64_t q_full, q_free;
@@ -116,19 +114,8 @@ __device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, int
     return p.pages + (int64_t)id * p.page_stride + (int64_t)(pos - pg * (uint32_t)p.page_size) * p.d;
 }
 
-__device__ __forceinline__ uint4 load_once(const uint16_t* p) {   // not kept in L1: the CTA reads it once
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-// Some bf16 among the eight is an infinity or NaN.
-__device__ __forceinline__ bool non_finite(const uint4& v) {
-    const uint32_t e = 0x7F807F80u;
-    return (__vcmpeq2(v.x & e, e) | __vcmpeq2(v.y & e, e) | __vcmpeq2(v.z & e, e) | __vcmpeq2(v.w & e, e)) != 0u;
-}
+// Two bf16, an infinity or NaN as 0.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v) { return v & ~__vcmpeq2(v & 0x7F807F80u, 0x7F807F80u); }
 
 // Which rows of the group's list head hd sees: i < n - (v >> 8), and i >= nf + (v & 255) or i < n_first (row i < n_first is
 // position i; queries of a group are at most 63 positions apart).
@@ -167,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int k = 0; k < 2; ++k) {
             for (int h = 0; h < 2; ++h) {
-                mbar_init(&tl->full[k][h], 8);
+                mbar_init(&tl->full[k][h], h == 0 ? 256 + 8 : 256);
                 mbar_init(&tl->freed[k][h], 1);
             }
             mbar_init(&tl->s_full[k], 1);
@@ -224,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h) {
                         if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
+                        fence_proxy_async_smem();   // the rows were copied by the loading threads
                         if (elect_one()) {
 #pragma unroll
                             for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
@@ -247,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t buf = n & 1u;
                     const int steps = min(4, (sg.vis - t * kRows + 15) / 16);   // of 16 rows
                     if (!wait(&tl->p_full[buf], (n >> 1) & 1u)) break;
+                    fence_proxy_async_smem();
                     if (elect_one()) {
 #pragma unroll
                         for (int m = 0; m < NM; ++m) {
@@ -307,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 8) {
         // -------------------------------------------------------------- tiles
-        // The warp's rows are 8 lw .. 8 lw + 7 of each tile, a lane holds 8 of every 256 dims of each.  Three tiles are under
-        // way: one being stored, its successor's rows being loaded after that, the one after's pages looked up.
+        // The warp's rows are 8 lw .. 8 lw + 7 of each tile, a lane copies 8 of every 256 dims of each.
+        regs_down<kRegsLoad>();
         const int lw = warp - 8;
         Walk walk(wk);
         Seg sg;
@@ -331,64 +320,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return at;
         };
-        uint4 v[8][kHalves];
         const int chunks = p.d / 8;
-        auto load = [&](const uint16_t* at) {       // returns which rows exist
-            const unsigned long long a = reinterpret_cast<unsigned long long>(at);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(kWarpFull, a, j));
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    v[j][h] = make_uint4(0, 0, 0, 0);
-                    if (src && lane + 32 * h < chunks) v[j][h] = load_once(src + 8 * (lane + 32 * h));
-                }
-            }
-            return __ballot_sync(kWarpFull, at != nullptr) & 0xFFu;
-        };
-        uint32_t left = (uint32_t)(wk.hi - wk.lo);
-        uint32_t have = load(look_up());
+        const uint32_t tiles = (uint32_t)(wk.hi - wk.lo);
         const uint16_t* next = look_up();
         bool dead = false;
-        for (uint32_t n = 0; n < left && !dead; ++n) {
+        for (uint32_t n = 0; n < tiles && !dead; ++n) {
             const uint32_t buf = n & 1u;
-            uint32_t bad = 0;
-            if (kPack) {   // such a row is stored as zeros, so that P = 0 keeps it from the heads that do not see it
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    bool b = false;
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h) b = b || non_finite(v[j][h]);
-                    if (__any_sync(kWarpFull, b)) {
-                        bad |= 1u << j;
-#pragma unroll
-                        for (int h = 0; h < kHalves; ++h) v[j][h] = make_uint4(0, 0, 0, 0);
-                    }
-                }
-            }
-            uint8_t* dst = t_s + buf * kTile + (size_t)(lane >> 3) * kTBlk + 8 * lw * 128;
+            const unsigned long long at = reinterpret_cast<unsigned long long>(next);
+            const uint32_t have = __ballot_sync(kWarpFull, next != nullptr);
+            next = look_up();   // (its pages' numbers arrive while this tile's rows are copied)
+            const uint32_t dst = smem_u32(t_s) + buf * kTile + (uint32_t)(lane >> 3) * kTBlk + 8u * (uint32_t)lw * 128u;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 if (n >= 2 && !warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort)) {
                     dead = true;
                     break;
                 }
-                if (lane + 32 * h < chunks) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(dst + 4 * h * kTBlk + j * 128 + (((lane & 7) ^ j) << 4)) = v[j][h];
+                for (int j = 0; j < 8; ++j) {
+                    const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(kWarpFull, at, j));
+                    if (lane + 32 * h < chunks)   // a row that is not there: zeros, nothing is read
+                        cp_async_16(dst + 4u * h * kTBlk + (uint32_t)j * 128u + (uint32_t)(((lane & 7) ^ j) << 4),
+                                    src ? src + 8 * (lane + 32 * h) : p.out, src ? 16u : 0u);
                 }
+                cp_async_mbar_arrive_noinc(&tl->full[buf][h]);
                 if (h == 0 && lane == 0) {
                     tl->valid[buf][lw] = (uint8_t)have;
-                    tl->bad[buf][lw] = (uint8_t)bad;
+                    mbar_arrive(&tl->full[buf][0]);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tl->full[buf][h]);
             }
-            have = load(next);
-            next = look_up();
         }
+        cp_async_wait<0>();
     } else {
         regs_up<kRegsSoft>();
         // -------------------------------------------------------------- softmax, outputs
@@ -419,12 +381,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nm[2 * g + 1] = v.y;
             }
         };
+        auto clear_rows = [&](uint32_t buf, bool first, bool second) {   // the thread's quarter of its rows
+#pragma unroll 1
+            for (int cb = l4; cb < n_cb; cb += 4)
+#pragma unroll 1
+                for (int k = 0; k < 16; ++k) {
+                    if (!(k < 8 ? first : second)) continue;
+                    uint4* at = reinterpret_cast<uint4*>(t_s + buf * kTile + (size_t)cb * kTBlk + (row + (k & 8)) * 128 + 16 * (k & 7));
+                    const uint4 v = *at;
+                    *at = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+                }
+        };
         int hv[8] = {};              // kPack: which rows each of the thread's heads sees
         // i0: this thread's first row of the list
         auto softmax = [&](const PagedRows& rows, int i0, bool first) {
             const uint32_t buf = n & 1u;
             mwait(&tl->s_full[buf], (n >> 1) & 1u);
-            mwait(&tl->full[buf][0], (n >> 1) & 1u);   // (complete; makes `valid` visible)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) mwait(&tl->full[buf][h], (n >> 1) & 1u);   // (complete; makes it visible)
             tc_fence_after();
             const uint32_t ts = tmem + lane_base + 64u * buf + 32u * (uint32_t)set;
             uint32_t r[16];
@@ -439,12 +413,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             tmem_ld_wait();
             if (kPack) {
-                const uint32_t bad = *reinterpret_cast<const uint16_t*>(&tl->bad[buf][2 * qd]) >> (lane >> 2);
+                // A row with an infinity or NaN has such scores with every head: NaN for those that see it, and zeros in
+                // their place in the tile, so that P = 0 keeps them from the others.
+                bool bad0 = false, bad1 = false;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    if (bad & 1u) r[4 * g] = r[4 * g + 1] = 0x7FFFFFFFu;
-                    if (bad & 0x100u) r[4 * g + 2] = r[4 * g + 3] = 0x7FFFFFFFu;
+                for (int k = 0; k < 16; ++k) {
+                    const bool b = (r[k] & 0x7F800000u) == 0x7F800000u;
+                    if (b) r[k] = 0x7FFFFFFFu;
+                    if (k & 2) bad1 = bad1 || b;
+                    else bad0 = bad0 || b;
                 }
+                if (__any_sync(kWarpFull, bad0 || bad1)) clear_rows(buf, bad0, bad1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) saw |= (sees(i, 0) || sees(i, 1)) ? 1u << i : 0u;
             } else {
