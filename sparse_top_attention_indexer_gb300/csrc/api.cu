@@ -1306,6 +1306,7 @@ sti_status sti_attn_paged(const uint16_t* q, const uint16_t* pages, int64_t page
     p.pack = pl.pack;
     p.groups = pl.groups;
     p.grid = pl.grid;
+    p.whole = pl.whole;
     CUtensorMap tm_q;
     const sti_status st = make_map_2d(&tm_q, q, (uint64_t)d, (uint64_t)b * seqlen * h, (uint64_t)d * 2, 64, 64);
     if (st != STI_OK) return st;

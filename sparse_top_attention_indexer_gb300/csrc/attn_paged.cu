@@ -57,10 +57,10 @@ __device__ __forceinline__ uint32_t window_start(const AttnPagedParams& p, uint3
     return p.window > 0 && P + 1u > (uint32_t)p.window ? P + 1u - (uint32_t)p.window : 0u;
 }
 __device__ __forceinline__ PagedRows rows_of(const AttnPagedParams& p, int b, int u) {
+    const uint32_t start = (uint32_t)__ldg(p.start_pos + b);
     const int t0 = u * p.pack, t1 = min(t0 + p.pack, paged_new(p, b));
     PagedRows r{0, 0, 0};
     if (t0 >= t1) return r;
-    const uint32_t start = (uint32_t)__ldg(p.start_pos + b);
     const uint32_t hi = min(start + (uint32_t)t1, (uint32_t)p.cap);   // positions past the table have no row
     r.lo = (int)min(window_start(p, start + (uint32_t)t0), hi);
     r.nf = min(p.n_first, r.lo);
@@ -76,6 +76,7 @@ namespace {
 constexpr int kRegsSoft = 144, kRegsLoad = 64, kRegsMma = 64;
 constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
 constexpr int kAhead = 4;                      // tiles whose rows are asked for ahead
+constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are not split between CTAs
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 struct __align__(16) Tail {
@@ -112,6 +113,22 @@ __device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, int
         return nullptr;
     }
     return p.pages + (int64_t)id * p.page_stride + (int64_t)(pos - pg * (uint32_t)p.page_size) * p.d;
+}
+
+__device__ __forceinline__ void prefetch_l2_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Four 8 x 8 matrices of 16-bit values, each turned over on the way: lane 8 i + j gives the address of 8 values that become
+// (or were) column j of matrix i, of which lane l has row l / 4, columns 2 (l % 4) and the next.
+__device__ __forceinline__ void store_turned(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ void load_turned(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
 // Two bf16, an infinity or NaN as 0.
@@ -187,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return ok;
         };
-        Walk walk(wk);
+        Walk walk(wk, p.whole);
         Seg sg;
         if (warp == 16) {
             // -------------------------------------------------------------- QK: the tile and Q, both K-major
@@ -268,10 +285,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const PagedRows rows = rows_of(p, sg.b, u);
                 for (int t = sg.t0; on && t < sg.t1; ++t, ++n) {
                     if (u != 0) continue;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint16_t* at = row_ptr(p, sg.b, rows, t * kRows + lane + 32 * k);
-                        if (at) prefetch_l2_bulk(at, 2u * (uint32_t)p.d);
+                    // (a row's 128-byte lines side by side in a warp's request; bulk prefetches of 1 KB rows leave the
+                    // warp one after another, some 40 ns each, and fell behind the tiles)
+                    const unsigned long long lo = reinterpret_cast<unsigned long long>(row_ptr(p, sg.b, rows, t * kRows + lane));
+                    const unsigned long long hi = reinterpret_cast<unsigned long long>(row_ptr(p, sg.b, rows, t * kRows + lane + 32));
+                    for (int l = lane; l < kRows * n_cb; l += 32) {
+                        const int r = l / n_cb;
+                        const unsigned long long a = __shfl_sync(kWarpFull, lo, r & 31), b = __shfl_sync(kWarpFull, hi, r & 31);
+                        const unsigned long long at = r < 32 ? a : b;
+                        if (at) prefetch_l2_line(reinterpret_cast<const uint16_t*>(at) + 64 * (l - r * n_cb));
                     }
                     // wait (a while at most) until the tile kAhead before is at hand
                     for (int i = 0; on; ++i) {
@@ -299,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The warp's rows are 8 lw .. 8 lw + 7 of each tile, a lane copies 8 of every 256 dims of each.
         regs_down<kRegsLoad>();
         const int lw = warp - 8;
-        Walk walk(wk);
+        Walk walk(wk, p.whole);
         Seg sg;
         PagedRows rows{0, 0, 0};
         bool more = walk.next(p, sg);
@@ -308,8 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
             t = sg.t0;
         }
-        auto look_up = [&]() -> const uint16_t* {   // the next tile's rows: lane j < 8 has row 8 lw + j's place
-            if (!more) return nullptr;
+        auto look_up = [&]() {   // the next tile's rows: lane j < 8 has row 8 lw + j's place
             const uint16_t* at = lane < 8 ? row_ptr(p, sg.b, rows, t * kRows + 8 * lw + lane) : nullptr;
             if (++t == sg.t1) {
                 more = walk.next(p, sg);
@@ -321,14 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             return at;
         };
         const int chunks = p.d / 8;
-        const uint32_t tiles = (uint32_t)(wk.hi - wk.lo);
-        const uint16_t* next = look_up();
         bool dead = false;
-        for (uint32_t n = 0; n < tiles && !dead; ++n) {
+        for (uint32_t n = 0; more && !dead; ++n) {
             const uint32_t buf = n & 1u;
-            const unsigned long long at = reinterpret_cast<unsigned long long>(next);
-            const uint32_t have = __ballot_sync(kWarpFull, next != nullptr);
-            next = look_up();   // (its pages' numbers arrive while this tile's rows are copied)
+            const uint16_t* rows_at = look_up();   // (the buffer is not free yet: its pages' numbers arrive meanwhile)
+            const unsigned long long at = reinterpret_cast<unsigned long long>(rows_at);
+            const uint32_t have = __ballot_sync(kWarpFull, rows_at != nullptr);
             const uint32_t dst = smem_u32(t_s) + buf * kTile + (uint32_t)(lane >> 3) * kTBlk + 8u * (uint32_t)lw * 128u;
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
@@ -520,28 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (slot >= 0: where); sink, prev_lse: of head 32 set + lane
         auto epilogue = [&](int q, int slot, float sink, float prev_lse) {
             const PagedGroup grp = group_of(p, q);
-            // 16 heads x 32 dims of this warp at a time: k / 2 the d-block, heads 32 set + 16 (k & 1) ...
-            // Pieces of 8 dims, two per lane: piece c = lane + 32 j is head c / 4, dims 8 (c % 4) ...
-            auto piece = [&](int k, int j, int64_t& at) {
-                const int pc = lane + 32 * j;
-                const int hw = 32 * set + 16 * (k & 1) + (pc >> 2), dw = 128 * (k >> 1) + 32 * qd + 8 * (pc & 3);
-                at = (grp.row0 + hw) * p.d + dw;
-                return k < 2 * NM && hw < grp.heads && dw < p.d;
+            // The warp has 32 heads x 32 dims of each d-block.  Pieces of 8 dims, four per lane: piece c = lane + 32 k is
+            // head c / 4 of the set, dims 8 (c % 4) ...
+            const int64_t out0 = (grp.row0 + 32 * set) * p.d + 32 * qd;
+            auto piece = [&](int m, int k, int64_t& at) {
+                const int hd = (lane >> 2) + 8 * k;
+                at = out0 + (int64_t)hd * p.d + 128 * m + 8 * (lane & 3);
+                return 32 * set + hd < grp.heads;
             };
             const bool joins = p.prev_out != nullptr && slot < 0;
-            uint4 pre[2][2];   // [k & 1]: prev_out, loaded two steps ahead
-            auto load_prev = [&](int k, uint4* v) {
+            uint4 pre[4];      // prev_out, loaded a d-block ahead
+            auto load_prev = [&](int m) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int k = 0; k < 4; ++k) {
                     int64_t at;
-                    v[j] = make_uint4(0, 0, 0, 0);
-                    if (piece(k, j, at)) v[j] = *reinterpret_cast<const uint4*>(p.prev_out + at);
+                    pre[k] = make_uint4(0, 0, 0, 0);
+                    if (piece(m, k, at) && 128 * m + 32 * qd < p.d) pre[k] = *reinterpret_cast<const uint4*>(p.prev_out + at);
                 }
             };
-            if (joins) {
-                load_prev(0, pre[0]);
-                load_prev(1, pre[1]);
-            }
+            if (joins) load_prev(0);
             mwait(&tl->freed[(n - 1) & 1u][kHalves - 1], ((n - 1) >> 1) & 1u);
             tc_fence_after();
             uint32_t any = saw;
@@ -578,58 +594,82 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wp = ep / den;
                 if (p.lse && qd == 0) p.lse[grp.row0 + hh] = (mx + log2f(den)) * kLn2;
             }
-            // The steps turn O^T over through shared memory, in fp32: lanes hold dims, the pieces are a head's.
-            float* stg = reinterpret_cast<float*>(p_s) + warp * 16 * 32;   // this warp's [16 heads][32 dims]
+            if (slot >= 0) {   // [head][dim] in fp32, lanes hold dims
+#pragma unroll 1
+                for (int k = 0; k < 2 * NM; ++k) {
+                    const int h0 = 32 * set + 16 * (k & 1), dd = 128 * (k >> 1) + 32 * qd + lane;
+                    uint32_t r[16];
+                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)(k >> 1) + (uint32_t)h0, r);
+                    tmem_ld_wait();
+                    float* po = p.part_o + ((int64_t)slot * hp + h0) * p.d + dd;
+                    if (dd < p.d) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
+                    }
+                }
+                return;
+            }
+            // A lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 l4 + {0, 1}; rounded to bf16, the 8 x 8 blocks are turned over
+            // on their way to this warp's [32 heads][32 dims] of shared memory, where prev_out comes from the same way.  A
+            // head's four pieces lie turned by (head / 2) % 4, so that neither side meets a bank twice.
             float2* fac = &tl->fac[set][qd][0];
             fac[lane] = make_float2(inv, wp);
+            __syncwarp();
+            float fi[8], fw[8];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float4 v = *reinterpret_cast<const float4*>(fac + 8 * g + 2 * l4);
+                fi[2 * g] = v.x;
+                fw[2 * g] = v.y;
+                fi[2 * g + 1] = v.z;
+                fw[2 * g + 1] = v.w;
+            }
+            uint8_t* stg = p_s + warp * 2048;
+            const int j8 = lane & 7;
+            const uint32_t block = smem_u32(stg) + (uint32_t)(j8 * 64 + ((((lane >> 3) + (j8 >> 1)) & 3) << 4));   // + 512 g
+            uint4* mine = reinterpret_cast<uint4*>(stg + (lane >> 2) * 64 + ((((lane & 3) + (((lane >> 2) & 7) >> 1)) & 3) << 4));
 #pragma unroll 1
-            for (int m = 0; m < NM; ++m)
+            for (int m = 0; 128 * m + 32 * qd < p.d; ++m) {
+                uint32_t r[2][16];
+                const uint32_t to = tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set;
+                tmem_ld_rows16(to, r[0]);
+                tmem_ld_rows16(to + (16u << 16), r[1]);
+                if (joins) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int k = 2 * m + half, h0 = 16 * half;
-                    const int dd = 128 * m + 32 * qd + lane;
-                    uint32_t r[16];
-                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set + (uint32_t)h0, r);
-                    tmem_ld_wait();
-                    if (slot >= 0) {
-                        float* po = p.part_o + ((int64_t)slot * hp + 32 * set + h0) * p.d + dd;
-                        if (dd < p.d) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (32 * set + h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
-                        }
-                        continue;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) stg[i * 32 + lane] = __uint_as_float(r[i]);
+                    for (int k = 0; k < 4; ++k) mine[32 * k] = pre[k];
                     __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int pc = lane + 32 * j;
-                        const float2 f = fac[h0 + (pc >> 2)];
-                        const float4* src = reinterpret_cast<const float4*>(stg + (pc >> 2) * 32 + 8 * (pc & 3));
-                        const float4 lo = src[0], hi = src[1];
-                        float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                        const uint32_t pw[4] = {pre[half][j].x, pre[half][j].y, pre[half][j].z, pre[half][j].w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x0 = v[2 * i] * f.x, x1 = v[2 * i + 1] * f.x;
-                            if (joins) {   // weight 0: prev_out is not used
-                                x0 = f.y != 0.f ? x0 + f.y * __uint_as_float(pw[i] << 16) : x0;
-                                x1 = f.y != 0.f ? x1 + f.y * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
-                            }
-                            o[i] = dead ? 0u : pack_bf16x2(x0, x1);
-                        }
-                        int64_t at;
-                        if (piece(k, j, at)) *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                    if (joins) load_prev(k + 2, pre[half]);
-                    __syncwarp();
+                    load_prev(m + 1);
                 }
+                tmem_ld_wait();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    uint32_t w[4], pw[4];
+                    if (joins) load_turned(block + 512u * (uint32_t)g, pw);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x0 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1)]) * fi[2 * g];
+                        float x1 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1) + 1]) * fi[2 * g + 1];
+                        if (joins) {   // weight 0: prev_out is not used
+                            x0 = fw[2 * g] != 0.f ? x0 + fw[2 * g] * __uint_as_float(pw[i] << 16) : x0;
+                            x1 = fw[2 * g + 1] != 0.f ? x1 + fw[2 * g + 1] * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
+                        }
+                        w[i] = pack_bf16x2(x0, x1);
+                    }
+                    store_turned(block + 512u * (uint32_t)g, w);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    int64_t at;
+                    const uint4 v = mine[32 * k];
+                    if (piece(m, k, at) && !dead) *reinterpret_cast<uint4*>(p.out + at) = v;
+                }
+                __syncwarp();
+            }
         };
 
-        Walk walk(wk);
+        Walk walk(wk, p.whole);
         Seg sg;
         int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
         float pend_sink = -INFINITY, pend_lse = -INFINITY;   // and what it is joined with
@@ -712,6 +752,7 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
     const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
+    if (p.whole) return cudaSuccess;
     return parts > 16  ? launch_after(merge_kernel<16, 32, AttnPagedParams>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
            : parts > 4 ? launch_after(merge_kernel<2, 128, AttnPagedParams>, dim3(mx, mh), 256, 0, stream, p)
                        : launch_after(merge_kernel<1, 128, AttnPagedParams>, dim3(mx, mh), 128, 0, stream, p);
@@ -726,7 +767,9 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_fi
     l.groups = (s + l.pack - 1) / l.pack;
     int64_t rows = cap;              // of a group's list, at most
     if (window > 0 && (int64_t)window + l.pack - 1 + n_first < rows) rows = (int64_t)window + l.pack - 1 + n_first;
-    const int64_t list = (rows + kRows - 1) / kRows * B * l.groups;
+    const int64_t tiles = (rows + kRows - 1) / kRows, groups = (int64_t)B * l.groups;
+    l.whole = tiles <= kWholeTiles;
+    const int64_t list = l.whole ? groups : tiles * groups;
     l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);
     return l;
 }

@@ -274,9 +274,11 @@ struct AttnPagedParams {
     float* part_o;
     float2* part_ml;
     int pack, groups;
+    bool whole;                 // no query is split between CTAs
 };
 struct AttnPagedPlan {
     int pack, groups, grid;     // as in AttnPagedParams
+    bool whole;
 };
 AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_first, int num_sms);
 // tm_q: q as [B*s*h, d], box 64 x 64
