@@ -16,7 +16,7 @@
 //   * warp 19 loads Q by TMA as soon as the last QK of the query before has read the buffer;
 //   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128 dims
 //     per block, K = the rows of the tile, the same tile read as an MN-major operand);
-//   * warp 18 asks for the rows of the next tiles, into L2;
+//   * warp 18 walks the list, tells the others what comes next and asks for the rows of the next tiles, into L2;
 //   * warps 0..7 run the online softmax (two sets of 32 heads; what P is relative to moves only when a score passes it
 //     by 2^8) and write the outputs.
 //
@@ -79,7 +79,20 @@ constexpr int kAhead = 4;                      // tiles whose rows are asked for
 constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are not split between CTAs
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
+// A run of one group's tiles, as warp 18 publishes it.
+struct __align__(16) Run {
+    int t0, t1;         // tiles t0 .. t1 - 1 of the group's list; t1 = 0: the CTA has no more
+    int n, nf;          // rows of the list, and those of them before the window
+    int lo, b;          // first position of the window, sequence
+    int heads, row0;    // the group's heads, the first one's place among all
+    int slot;           // of its partial output, -1: the run holds all of the list
+    uint32_t pos;       // position of its first query
+    int pad[2];
+};
+constexpr int kRuns = 4, kReaders = 19;        // runs published ahead; the warps that read them
+
 struct __align__(16) Tail {
+    Run run[kRuns];
     float neg_m[2][4][32];    // [head group][warp of the group]: its copy of -reference
     float2 fac[2][4][32];     // the outputs' factors
     float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
@@ -92,6 +105,7 @@ struct __align__(16) Tail {
     uint64_t freed[2][2];     // the PV has read it
     uint64_t s_full[2], p_full[2];
     uint64_t q_full, q_free;
+    uint64_t run_full[kRuns], run_empty[kRuns];
     uint32_t tmem_base;
     int abort;
     int qk_tile;              // tiles whose QK was issued, for the prefetching warp
@@ -102,12 +116,12 @@ size_t attn_paged_smem(int d) {
     return 1024 + (size_t)n_cb * (kQBlk + 2 * kTBlk) + 2 * kPBuf + sizeof(Tail);
 }
 
-// Where row i of the group's list lies, 0 if there is none (past the list; a page outside the pool).
-__device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, int b, const PagedRows& r, int i) {
+// Where row i of the run's list lies, null if there is none (past the list; a page outside the pool).
+__device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, const Run& r, int i) {
     if (i >= r.n) return nullptr;
     const uint32_t pos = (uint32_t)(i < r.nf ? i : r.lo + (i - r.nf));
     const uint32_t pg = pos / (uint32_t)p.page_size;
-    const int id = __ldg(p.table + (int64_t)b * p.table_stride + pg);
+    const int id = __ldg(p.table + (int64_t)r.b * p.table_stride + pg);
     if (id < 0 || id >= p.n_pages) {
         if (p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
         return nullptr;
@@ -115,7 +129,12 @@ __device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, int
     return p.pages + (int64_t)id * p.page_stride + (int64_t)(pos - pg * (uint32_t)p.page_size) * p.d;
 }
 
-__device__ __forceinline__ void prefetch_l2_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// tmem_ld_rows16 of half the heads: g < 2.
+__device__ __forceinline__ void tmem_ld_rows16_half(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 
 // Four 8 x 8 matrices of 16-bit values, each turned over on the way: lane 8 i + j gives the address of 8 values that become
 // (or were) column j of matrix i, of which lane l has row l / 4, columns 2 (l % 4) and the next.
@@ -136,13 +155,27 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t v) { return v & ~__vcmp
 
 // Which rows of the group's list head hd sees: i < n - (v >> 8), and i >= nf + (v & 255) or i < n_first (row i < n_first is
 // position i; queries of a group are at most 63 positions apart).
-__device__ __forceinline__ int head_vis(const AttnPagedParams& p, const PagedGroup& g, const PagedRows& r, int hd) {
-    if (hd >= g.heads) return 0x7FFFFF00;   // none of a list that short; what it sees of another goes nowhere
-    const uint32_t P = (uint32_t)__ldg(p.start_pos + g.b) + (uint32_t)(g.t0 + hd / p.h);
+__device__ __forceinline__ int head_vis(const AttnPagedParams& p, const Run& r, int hd) {
+    if (hd >= r.heads) return 0x7FFFFF00;   // none of a list that short; what it sees of another goes nowhere
+    const uint32_t P = r.pos + (uint32_t)(hd / p.h);
     const uint32_t hi = (uint32_t)(r.lo + (r.n - r.nf));
     const uint32_t end = min(P + 1u, hi);
     const uint32_t lo = min(max(window_start(p, P), (uint32_t)r.lo), hi);
     return (int)((hi - end) << 8 | (lo - (uint32_t)r.lo));
+}
+
+// An MMA that accumulates if acc is not 0, and happens only if `on`.
+__device__ __forceinline__ void umma_if(bool on, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                        uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\t"
+        "mov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"((uint32_t)on)
+        : "memory");
 }
 
 template <int NM, bool kPack>   // d-blocks of 128 dims; groups of several queries
@@ -179,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&tl->q_full, 1);
         mbar_init(&tl->q_free, 1);
+        for (int k = 0; k < kRuns; ++k) {
+            mbar_init(&tl->run_full[k], 1);
+            mbar_init(&tl->run_empty[k], kReaders);
+        }
         tl->abort = 0;
         tl->qk_tile = 0;
         fence_mbar_init();
@@ -194,6 +231,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Work wk = tl->work;
     griddep_launch_dependents();
 
+    // The next run for this warp (false: none, or a wait gave up).
+    uint32_t runs = 0;
+    auto next_run = [&](Run& r) {
+        const uint32_t k = runs % kRuns;
+        if (!warp_wait(&tl->run_full[k], runs / kRuns & 1u, p.status, abort)) return false;
+        r = tl->run[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tl->run_empty[k]);
+        ++runs;
+        return r.t1 > 0;
+    };
+
     if (warp >= 16) {
         regs_down<kRegsMma>();
         const int n_mma = (hp + 15) / 16 * 16;
@@ -204,71 +253,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return ok;
         };
-        Walk walk(wk, p.whole);
-        Seg sg;
+        Run run;
         if (warp == 16) {
             // -------------------------------------------------------------- QK: the tile and Q, both K-major
             const uint32_t idesc = idesc_bf16_f32(kRows, n_mma, false, false);
             const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
-            uint32_t qn = 0;
-            int2 rec = make_int2(-1, 0);
-            while (ok && walk.next(p, sg)) {
-                if (sg.t0 == 0 && sg.t1 < sg.nt) {
-                    const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
-                    int c = (int)(last * wk.ctas / wk.total);
-                    while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
-                    while ((long long)c * wk.total / wk.ctas > last) --c;
-                    rec = make_int2(sg.q, c);
-                }
-                if (!wait(&tl->q_full, qn & 1u)) break;
-                ++qn;
-                for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
+            while (ok && next_run(run)) {
+                if (!wait(&tl->q_full, (runs - 1) & 1u)) break;
+                for (int t = run.t0; t < run.t1 && ok; ++t, ++n) {
                     if (lane == 0) tl->qk_tile = (int)n;
                     const uint32_t buf = n & 1u;   // its S^T has been read: the tile was filled after the PV of n - 2
-#pragma unroll
+                    // (one half's MMAs as code: with both, what a query runs through no longer fits the instruction cache)
+#pragma unroll 1
                     for (int h = 0; h < kHalves; ++h) {
                         if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
                         fence_proxy_async_smem();   // the rows were copied by the loading threads
                         if (elect_one()) {
+                            const uint32_t at = opaque(lo32(dk) + buf * (kTile / 16) + (uint32_t)h * (4 * kTBlk / 16));
+                            const uint32_t bt = opaque(lo32(dq) + (uint32_t)h * (4 * kQBlk / 16));
 #pragma unroll
-                            for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m)
-                                qk_blocks(m, tmem + 64u * buf, lo32(dk) + buf * (kTile / 16), lo32(dq), hi32(dk), idesc);
+                            for (int k = 0; k < 16; ++k)
+                                if (NM % 2 == 0 || k < 8 || 2 * h + 1 < NM)   // (the last half of an odd NM is one d-block)
+                                    umma_if(true, tmem + 64u * buf, at + (k >> 2) * (kTBlk / 16) + 2 * (k & 3), hi32(dk),
+                                            bt + (k >> 2) * (kQBlk / 16) + 2 * (k & 3), hi32(dq), idesc, h + k);
                             if (h == kHalves - 1) {
                                 umma_commit(&tl->s_full[buf]);
-                                if (t == sg.t1 - 1) umma_commit(&tl->q_free);
+                                if (t == run.t1 - 1) umma_commit(&tl->q_free);
                             }
                         }
                         __syncwarp();
                     }
                 }
             }
-            if (lane == 0) p.rec[blockIdx.x] = rec;
         } else if (warp == 17) {
             // -------------------------------------------------------------- PV: the tile and P^T, both MN-major
             const uint32_t idesc = idesc_bf16_f32(128, n_mma, true, true);
             const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128), dp = sdesc(smem_u32(p_s), kPBuf, 1024, kLayoutSW128);
-            while (ok && walk.next(p, sg)) {
-                for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+            while (ok && next_run(run)) {
+                for (int t = run.t0; t < run.t1; ++t, ++n) {
                     const uint32_t buf = n & 1u;
-                    const int steps = min(4, (sg.vis - t * kRows + 15) / 16);   // of 16 rows
+                    const int steps = (run.n - t * kRows + 15) / 16;   // of 16 rows, four at most
                     if (!wait(&tl->p_full[buf], (n >> 1) & 1u)) break;
                     fence_proxy_async_smem();
                     if (elect_one()) {
 #pragma unroll
                         for (int m = 0; m < NM; ++m) {
-                            const uint32_t o = tmem + kTmO + 64u * (uint32_t)m;
-                            const uint32_t a = lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16);
-                            const uint32_t b = lo32(dp) + buf * (kPBuf / 16);
-                            if (steps < 4) {
-                                if (t == sg.t0) umma<false>(o, a, hi32(dv), b, hi32(dp), idesc);
-                                else umma<true>(o, a, hi32(dv), b, hi32(dp), idesc);
-                                for (int k = 1; k < steps; ++k)
-                                    umma<true>(o, a + 128u * (uint32_t)k, hi32(dv), b + 128u * (uint32_t)k, hi32(dp), idesc);
-                            } else if (t == sg.t0) {
-                                pv_block<true>(o, a, hi32(dv), b, hi32(dp), idesc);
-                            } else {
-                                pv_block<false>(o, a, hi32(dv), b, hi32(dp), idesc);
-                            }
+                            const uint32_t at = opaque(lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16));
+                            const uint32_t bt = opaque(lo32(dp) + buf * (kPBuf / 16));
+#pragma unroll
+                            for (int k = 0; k < kRows / 16; ++k)
+                                umma_if(k < steps, tmem + kTmO + 64u * (uint32_t)m, at + 128 * k, hi32(dv), bt + 128 * k, hi32(dp),
+                                        idesc, (uint32_t)(t - run.t0 + k));
                             if ((m & 1) || m == NM - 1) umma_commit(&tl->freed[buf][m >> 1]);
                         }
                     }
@@ -276,43 +311,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == 18) {
+            // -------------------------------------------------------------- the runs, and their rows' way to L2
             // The rows of the next kAhead tiles are on their way to L2 when a tile is loaded, asked for by a
             // sequence's first query only: the others find them there.
             volatile int* now = &tl->qk_tile;
-            bool on = true;
-            while (on && walk.next(p, sg)) {
-                const int u = sg.q - sg.b * p.groups;
-                const PagedRows rows = rows_of(p, sg.b, u);
-                for (int t = sg.t0; on && t < sg.t1; ++t, ++n) {
-                    if (u != 0) continue;
-                    // (a row's 128-byte lines side by side in a warp's request; bulk prefetches of 1 KB rows leave the
-                    // warp one after another, some 40 ns each, and fell behind the tiles)
-                    const unsigned long long lo = reinterpret_cast<unsigned long long>(row_ptr(p, sg.b, rows, t * kRows + lane));
-                    const unsigned long long hi = reinterpret_cast<unsigned long long>(row_ptr(p, sg.b, rows, t * kRows + lane + 32));
-                    for (int l = lane; l < kRows * n_cb; l += 32) {
-                        const int r = l / n_cb;
-                        const unsigned long long a = __shfl_sync(kWarpFull, lo, r & 31), b = __shfl_sync(kWarpFull, hi, r & 31);
-                        const unsigned long long at = r < 32 ? a : b;
-                        if (at) prefetch_l2_line(reinterpret_cast<const uint16_t*>(at) + 64 * (l - r * n_cb));
-                    }
-                    // wait (a while at most) until the tile kAhead before is at hand
-                    for (int i = 0; on; ++i) {
-                        if (__all_sync(kWarpFull, *now + kAhead >= (int)n)) break;
-                        on = __all_sync(kWarpFull, i < 100000 && !*abort);
-                        __nanosleep(200);
+            Walk walk(wk, p.whole);
+            Seg sg;
+            int2 rec = make_int2(-1, 0);
+            while (ok) {
+                const bool more = walk.next(p, sg);
+                const uint32_t k = runs % kRuns;
+                if (runs >= kRuns && !wait(&tl->run_empty[k], runs / kRuns - 1 & 1u)) break;
+                ++runs;
+                run.t1 = 0;
+                int u = 0;
+                if (more) {
+                    const PagedGroup grp = group_of(p, sg.q);
+                    u = sg.q - sg.b * p.groups;
+                    const PagedRows rows = rows_of(p, sg.b, u);
+                    run.t0 = sg.t0;
+                    run.t1 = sg.t1;
+                    run.n = rows.n;
+                    run.nf = rows.nf;
+                    run.lo = rows.lo;
+                    run.b = sg.b;
+                    run.heads = grp.heads;
+                    run.row0 = (int)grp.row0;
+                    run.slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
+                    run.pos = (uint32_t)__ldg(p.start_pos + sg.b) + (uint32_t)grp.t0;
+                    if (sg.t0 == 0 && sg.t1 < sg.nt) {
+                        const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
+                        int c = (int)(last * wk.ctas / wk.total);
+                        while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
+                        while ((long long)c * wk.total / wk.ctas > last) --c;
+                        rec = make_int2(sg.q, c);
                     }
                 }
+                if (lane == 0) {
+                    tl->run[k] = run;
+                    mbar_arrive(&tl->run_full[k]);
+                }
+                if (!more) break;
+                if (u != 0) {
+                    n += (uint32_t)(sg.t1 - sg.t0);
+                    continue;
+                }
+                for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+                    // rows that lie side by side in one request each: a warp's bulk prefetches leave it one after another
+                    const uint16_t* at[2] = {row_ptr(p, run, t * kRows + lane), row_ptr(p, run, t * kRows + 32 + lane)};
+                    unsigned long long a[2], before[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        a[i] = reinterpret_cast<unsigned long long>(at[i]);
+                        before[i] = __shfl_up_sync(kWarpFull, a[i], 1);
+                    }
+                    const unsigned long long mid = __shfl_sync(kWarpFull, a[0], 31);
+                    if (lane == 0) {
+                        before[0] = 0;
+                        before[1] = mid;
+                    }
+                    const uint32_t bytes = 2u * (uint32_t)p.d;
+                    const bool c0 = a[0] && before[0] && a[0] == before[0] + bytes, c1 = a[1] && before[1] && a[1] == before[1] + bytes;
+                    const unsigned long long goes_on = (unsigned long long)__ballot_sync(kWarpFull, c1) << 32 | __ballot_sync(kWarpFull, c0);
+                    auto length = [&](int i) { return (uint32_t)__ffsll(~((goes_on >> i) >> 1)); };   // of the run of rows from row i on
+                    if (a[0] && !c0) prefetch_l2_bulk(at[0], bytes * length(lane));
+                    if (a[1] && !c1) prefetch_l2_bulk(at[1], bytes * length(lane + 32));
+                    // wait (a while at most) until the tile kAhead before is at hand
+                    for (int i = 0; ok; ++i) {
+                        if (__all_sync(kWarpFull, *now + kAhead >= (int)n)) break;
+                        ok = __all_sync(kWarpFull, i < 10000000 && !*abort);
+                        __nanosleep(100);
+                    }
+                    if (!ok) break;
+                }
             }
-        } else if (lane == 0) {
+            if (lane == 0) p.rec[blockIdx.x] = rec;
+        } else {
             // -------------------------------------------------------------- Q
-            uint32_t qn = 0;
-            while (walk.next(p, sg)) {
-                const int64_t row0 = ((int64_t)sg.b * p.s + (int64_t)(sg.q - sg.b * p.groups) * p.pack) * p.h;
-                if (qn > 0 && !tile_wait(&tl->q_free, (qn - 1) & 1u, p.status, abort)) break;
-                ++qn;
+            while (next_run(run)) {
+                if (runs > 1 && !warp_wait(&tl->q_free, runs & 1u, p.status, abort)) break;
                 // rows past the group's heads are other queries', or zeros past the last: columns of S^T that nothing uses
-                mbar_arrive_expect_tx(&tl->q_full, (uint32_t)n_cb * kQBlk);
-                for (int cb = 0; cb < n_cb; ++cb) tma_load_2d(q_s + cb * kQBlk, &tm_q, &tl->q_full, 64 * cb, (int)row0);
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&tl->q_full, (uint32_t)n_cb * kQBlk);
+                    for (int cb = 0; cb < n_cb; ++cb) tma_load_2d(q_s + cb * kQBlk, &tm_q, &tl->q_full, 64 * cb, run.row0);
+                }
+                __syncwarp();
             }
         }
         __syncwarp();
@@ -321,35 +404,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The warp's rows are 8 lw .. 8 lw + 7 of each tile, a lane copies 8 of every 256 dims of each.
         regs_down<kRegsLoad>();
         const int lw = warp - 8;
-        Walk walk(wk, p.whole);
-        Seg sg;
-        PagedRows rows{0, 0, 0};
-        bool more = walk.next(p, sg);
+        Run run;
+        run.t1 = 0;
         int t = 0;
-        if (more) {
-            rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
-            t = sg.t0;
-        }
-        auto look_up = [&]() {   // the next tile's rows: lane j < 8 has row 8 lw + j's place
-            const uint16_t* at = lane < 8 ? row_ptr(p, sg.b, rows, t * kRows + 8 * lw + lane) : nullptr;
-            if (++t == sg.t1) {
-                more = walk.next(p, sg);
-                if (more) {
-                    rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
-                    t = sg.t0;
-                }
-            }
-            return at;
-        };
         const int chunks = p.d / 8;
         bool dead = false;
-        for (uint32_t n = 0; more && !dead; ++n) {
+        for (uint32_t n = 0; !dead; ++n, ++t) {
+            if (t == run.t1) {
+                if (!next_run(run)) break;
+                t = run.t0;
+            }
             const uint32_t buf = n & 1u;
-            const uint16_t* rows_at = look_up();   // (the buffer is not free yet: its pages' numbers arrive meanwhile)
+            // lane j < 8 has row 8 lw + j's place (the buffer is not free yet: its pages' numbers arrive meanwhile)
+            const uint16_t* rows_at = lane < 8 ? row_ptr(p, run, t * kRows + 8 * lw + lane) : nullptr;
             const unsigned long long at = reinterpret_cast<unsigned long long>(rows_at);
             const uint32_t have = __ballot_sync(kWarpFull, rows_at != nullptr);
             const uint32_t dst = smem_u32(t_s) + buf * kTile + (uint32_t)(lane >> 3) * kTBlk + 8u * (uint32_t)lw * 128u;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < kHalves; ++h) {
                 if (n >= 2 && !warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort)) {
                     dead = true;
@@ -413,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int hv[8] = {};              // kPack: which rows each of the thread's heads sees
         // i0: this thread's first row of the list
-        auto softmax = [&](const PagedRows& rows, int i0, bool first) {
+        auto softmax = [&](const Run& run, int i0, bool first) {
             const uint32_t buf = n & 1u;
             mwait(&tl->s_full[buf], (n >> 1) & 1u);
 #pragma unroll
@@ -428,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool v = second ? v1 : v0;
                 if (!kPack) return v;
                 const int at = i0 + 8 * second;
-                return v && at < rows.n - (hv[i] >> 8) && (at >= rows.nf + (hv[i] & 255) || at < p.n_first);
+                return v && at < run.n - (hv[i] >> 8) && (at >= run.nf + (hv[i] & 255) || at < p.n_first);
             };
             tmem_ld_wait();
             if (kPack) {
@@ -487,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* own = &tl->neg_m[set][qd][0];
                 const float mt = fmaxf(fmaxf(rr[0], rr[32]), fmaxf(rr[64], rr[96])) - own[lane];
                 const float m_new = (m_run == -INFINITY || mt > m_run + kTopMost) ? fmaxf(m_run, mt) : m_run;
-                const float alpha = (m_new == m_run) ? 1.f : exp2f(m_run - m_new);
+                const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
                 m_run = m_new;
                 __syncwarp();
                 // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
@@ -535,17 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&tl->p_full[buf]);
         };
 
-        // a segment's O^T and sums: the group's output when the segment holds all its tiles, else a partial
-        // (slot >= 0: where); sink, prev_lse: of head 32 set + lane
-        auto epilogue = [&](int q, int slot, float sink, float prev_lse) {
-            const PagedGroup grp = group_of(p, q);
+        // a run's O^T and sums: the group's output when the run holds all its tiles, else a partial (slot >= 0: where);
+        // sink, prev_lse: of head 32 set + lane
+        auto epilogue = [&](int64_t row0, int heads, int slot, float sink, float prev_lse) {
             // The warp has 32 heads x 32 dims of each d-block.  Pieces of 8 dims, four per lane: piece c = lane + 32 k is
             // head c / 4 of the set, dims 8 (c % 4) ...
-            const int64_t out0 = (grp.row0 + 32 * set) * p.d + 32 * qd;
+            const int64_t out0 = (row0 + 32 * set) * p.d + 32 * qd;
             auto piece = [&](int m, int k, int64_t& at) {
                 const int hd = (lane >> 2) + 8 * k;
                 at = out0 + (int64_t)hd * p.d + 128 * m + 8 * (lane & 3);
-                return 32 * set + hd < grp.heads;
+                return 32 * set + hd < heads;
             };
             const bool joins = p.prev_out != nullptr && slot < 0;
             uint4 pre[4];      // prev_out, loaded a d-block ahead
@@ -578,21 +648,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             float inv = 0.f, wp = 0.f;
             if (slot >= 0) {
                 if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
-            } else if (signbit(lt) && hh < grp.heads) {
+            } else if (signbit(lt) && hh < heads) {
                 // a query that sees no row: what it had
                 wp = prev_lse == -INFINITY ? 0.f : 1.f;
-                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = prev_lse;
-            } else if (hh < grp.heads) {
+                if (p.lse && qd == 0) p.lse[row0 + hh] = prev_lse;
+            } else if (hh < heads) {
                 // everything relative to the largest of the reference, the sink and prev_lse
                 const float sk = sink * kLog2e, pl = prev_lse * kLog2e;
                 float mx = fmaxf(m_run, fmaxf(sk, pl));
                 if (mx == -INFINITY) mx = 0.f;
-                const float f = lt == 0.f ? 0.f : m_run == -INFINITY ? exp2f(-mx) : exp2f(m_run - mx);   // (inf * 0)
-                const float ep = exp2f(pl - mx);
-                const float den = lt * f + exp2f(sk - mx) + ep;
-                inv = f / den;
-                wp = ep / den;
-                if (p.lse && qd == 0) p.lse[grp.row0 + hh] = (mx + log2f(den)) * kLn2;
+                const float f = lt == 0.f ? 0.f : m_run == -INFINITY ? fast_exp2(-mx) : fast_exp2(m_run - mx);   // (inf * 0)
+                const float ep = fast_exp2(pl - mx);
+                const float den = lt * f + fast_exp2(sk - mx) + ep;
+                const float over = __fdividef(1.f, den);
+                inv = f * over;
+                wp = ep * over;
+                if (p.lse && qd == 0) p.lse[row0 + hh] = (mx + __log2f(den)) * kLn2;
             }
             if (slot >= 0) {   // [head][dim] in fp32, lanes hold dims
 #pragma unroll 1
@@ -615,48 +686,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             // head's four pieces lie turned by (head / 2) % 4, so that neither side meets a bank twice.
             float2* fac = &tl->fac[set][qd][0];
             fac[lane] = make_float2(inv, wp);
-            __syncwarp();
-            float fi[8], fw[8];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float4 v = *reinterpret_cast<const float4*>(fac + 8 * g + 2 * l4);
-                fi[2 * g] = v.x;
-                fw[2 * g] = v.y;
-                fi[2 * g + 1] = v.z;
-                fw[2 * g + 1] = v.w;
-            }
             uint8_t* stg = p_s + warp * 2048;
             const int j8 = lane & 7;
             const uint32_t block = smem_u32(stg) + (uint32_t)(j8 * 64 + ((((lane >> 3) + (j8 >> 1)) & 3) << 4));   // + 512 g
             uint4* mine = reinterpret_cast<uint4*>(stg + (lane >> 2) * 64 + ((((lane & 3) + (((lane >> 2) & 7) >> 1)) & 3) << 4));
 #pragma unroll 1
             for (int m = 0; 128 * m + 32 * qd < p.d; ++m) {
-                uint32_t r[2][16];
-                const uint32_t to = tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set;
-                tmem_ld_rows16(to, r[0]);
-                tmem_ld_rows16(to + (16u << 16), r[1]);
                 if (joins) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) mine[32 * k] = pre[k];
-                    __syncwarp();
                     load_prev(m + 1);
                 }
-                tmem_ld_wait();
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    uint32_t w[4], pw[4];
-                    if (joins) load_turned(block + 512u * (uint32_t)g, pw);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x0 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1)]) * fi[2 * g];
-                        float x1 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1) + 1]) * fi[2 * g + 1];
-                        if (joins) {   // weight 0: prev_out is not used
-                            x0 = fw[2 * g] != 0.f ? x0 + fw[2 * g] * __uint_as_float(pw[i] << 16) : x0;
-                            x1 = fw[2 * g + 1] != 0.f ? x1 + fw[2 * g + 1] * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
-                        }
-                        w[i] = pack_bf16x2(x0, x1);
+                __syncwarp();
+                const uint32_t to = tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set;
+#pragma unroll 1
+                for (int g = 0; g < 4; g += 2) {   // (short bodies: this code is fetched anew for every query)
+                    uint32_t r[2][8];
+                    tmem_ld_rows16_half(to + 8u * (uint32_t)g, r[0]);
+                    tmem_ld_rows16_half(to + 8u * (uint32_t)g + (16u << 16), r[1]);
+                    float4 f[2] = {*reinterpret_cast<const float4*>(fac + 8 * g + 2 * l4),
+                                   *reinterpret_cast<const float4*>(fac + 8 * g + 8 + 2 * l4)};   // (factor, prev's) of two heads
+                    uint32_t pw[2][4];
+                    if (joins) {
+                        load_turned(block + 512u * (uint32_t)g, pw[0]);
+                        load_turned(block + 512u * (uint32_t)g + 512u, pw[1]);
                     }
-                    store_turned(block + 512u * (uint32_t)g, w);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x0 = __uint_as_float(r[i >> 1][4 * e + 2 * (i & 1)]) * f[e].x;
+                            float x1 = __uint_as_float(r[i >> 1][4 * e + 2 * (i & 1) + 1]) * f[e].z;
+                            if (joins) {   // weight 0: prev_out is not used
+                                x0 = f[e].y != 0.f ? x0 + f[e].y * __uint_as_float(pw[e][i] << 16) : x0;
+                                x1 = f[e].w != 0.f ? x1 + f[e].w * __uint_as_float(pw[e][i] & 0xFFFF0000u) : x1;
+                            }
+                            w[i] = pack_bf16x2(x0, x1);
+                        }
+                        store_turned(block + 512u * (uint32_t)(g + e), w);
+                    }
                 }
                 __syncwarp();
 #pragma unroll
@@ -669,18 +739,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
 
-        Walk walk(wk, p.whole);
-        Seg sg;
-        int pend_q = -1, pend_slot = -1;       // the segment whose output is pending
+        Run run;
+        int pend_heads = 0, pend_row0 = 0, pend_slot = -1;   // the run whose output is pending
         float pend_sink = -INFINITY, pend_lse = -INFINITY;   // and what it is joined with
-        int par = 0;                           // segment parity
-        while (walk.next(p, sg)) {
-            const PagedGroup grp = group_of(p, sg.q);
-            const PagedRows rows = rows_of(p, sg.b, sg.q - sg.b * p.groups);
-            if (kPack && tid < 64) tl->vis[par][tid] = head_vis(p, grp, rows, tid);   // (every warp is done with par's last)
-            if (tid == 0 && p.prev_out)   // what this segment's end will read, into L2
-                prefetch_l2_bulk(p.prev_out + grp.row0 * p.d, (uint32_t)(grp.heads * p.d) * 2u);
-            if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, pend_sink, pend_lse);
+        int par = 0;                           // run parity
+        while (next_run(run)) {
+            if (kPack && tid < 64) tl->vis[par][tid] = head_vis(p, run, tid);   // (every warp is done with par's last)
+            if (tid == 0 && p.prev_out)   // what this run's end will read, into L2
+                prefetch_l2_bulk(p.prev_out + (int64_t)run.row0 * p.d, (uint32_t)(run.heads * p.d) * 2u);
+            if (pend_heads > 0 && active) epilogue(pend_row0, pend_heads, pend_slot, pend_sink, pend_lse);
             named_bar_sync(kBarSoft, 256);     // the staging area is every warp's P^T; vis is complete
             m_run = -INFINITY;
             tl->neg_m[set][qd][lane] = 0.f;
@@ -693,18 +760,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
             saw = 0;
-            for (int t = sg.t0; t < sg.t1; ++t, ++n)
-                if (active) softmax(rows, t * kRows + row, t == sg.t0);
+            for (int t = run.t0; t < run.t1; ++t, ++n)
+                if (active) softmax(run, t * kRows + row, t == run.t0);
             par ^= 1;
-            pend_q = sg.q;
+            pend_heads = run.heads;
+            pend_row0 = run.row0;
+            pend_slot = run.slot;
             const int hh = 32 * set + lane;
-            if (hh < grp.heads) {
+            if (hh < run.heads) {
                 if (p.sink) pend_sink = __ldg(p.sink + (kPack ? hh % p.h : hh));
-                pend_lse = p.prev_lse ? __ldg(p.prev_lse + grp.row0 + hh) : -INFINITY;
+                pend_lse = p.prev_lse ? __ldg(p.prev_lse + run.row0 + hh) : -INFINITY;
             }
-            pend_slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
         }
-        if (pend_q >= 0 && active) epilogue(pend_q, pend_slot, pend_sink, pend_lse);
+        if (pend_heads > 0 && active) epilogue(pend_row0, pend_heads, pend_slot, pend_sink, pend_lse);
 
         // queries past the table are reported; groups whose lists are empty
         for (int q = blockIdx.x; q < nq; q += gridDim.x) {
