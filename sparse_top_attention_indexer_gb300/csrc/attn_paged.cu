@@ -129,13 +129,6 @@ __device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, con
     return p.pages + (int64_t)id * p.page_stride + (int64_t)(pos - pg * (uint32_t)p.page_size) * p.d;
 }
 
-// tmem_ld_rows16 of half the heads: g < 2.
-__device__ __forceinline__ void tmem_ld_rows16_half(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
-
 // Four 8 x 8 matrices of 16-bit values, each turned over on the way: lane 8 i + j gives the address of 8 values that become
 // (or were) column j of matrix i, of which lane l has row l / 4, columns 2 (l % 4) and the next.
 __device__ __forceinline__ void store_turned(uint32_t addr, const uint32_t (&r)[4]) {
@@ -162,6 +155,88 @@ __device__ __forceinline__ int head_vis(const AttnPagedParams& p, const Run& r, 
     const uint32_t end = min(P + 1u, hi);
     const uint32_t lo = min(max(window_start(p, P), (uint32_t)r.lo), hi);
     return (int)((hi - end) << 8 | (lo - (uint32_t)r.lo));
+}
+
+// Sum or maximum over the 8 lanes of equal lane % 4 of v[i], in lane 4 j + lane % 4 for i = the bits of j in reverse (7
+// exchanges instead of 24).
+template <bool MAX>
+__device__ __forceinline__ float over_rows(const float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    auto op = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float send = lane & 4 ? v[i] : v[i + 4];
+        a[i] = op(lane & 4 ? v[i + 4] : v[i], __shfl_xor_sync(kWarpFull, send, 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float send = lane & 8 ? a[i] : a[i + 2];
+        b[i] = op(lane & 8 ? a[i + 2] : a[i], __shfl_xor_sync(kWarpFull, send, 8));
+    }
+    const float send = lane & 16 ? b[0] : b[1];
+    return op(lane & 16 ? b[1] : b[0], __shfl_xor_sync(kWarpFull, send, 16));
+}
+
+// O^T of a warp's 32 heads (TMEM columns at `to`, 64 more per d-block) x 32 dims of each d-block, times the heads' factors
+// in fac (of O, of prev_out), as bf16 to p.out + first ...  A lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 (l % 4) +
+// {0, 1}; the 8 x 8 blocks are turned over on their way to [32 heads][32 dims] in shared memory at stg, where prev_out comes
+// from the same way.  A head's four pieces lie turned by (head / 2) % 4, so that neither side meets a bank twice.
+// (Turned over in fp32, with 16 scalar stores for each matrix store here, a query's outputs took 4.6 us, now 2.)
+template <bool JOINS, class F>
+__device__ __forceinline__ void write_out(const AttnPagedParams& p, const float2* fac, uint8_t* stg, uint32_t to, int64_t first,
+                                          int there, int qd, bool dead, uint4 (&pre)[4], F load_prev) {
+    const int lane = threadIdx.x & 31, l4 = lane & 3, j8 = lane & 7;
+    float fi[8], fw[8];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(fac + 8 * g + 2 * l4);
+        fi[2 * g] = v.x;
+        fw[2 * g] = v.y;
+        fi[2 * g + 1] = v.z;
+        fw[2 * g + 1] = v.w;
+    }
+    const uint32_t block = smem_u32(stg) + (uint32_t)(j8 * 64 + ((((lane >> 3) + (j8 >> 1)) & 3) << 4));   // + 512 g
+    uint4* mine = reinterpret_cast<uint4*>(stg + (lane >> 2) * 64 + (((l4 + (((lane >> 2) & 7) >> 1)) & 3) << 4));
+    uint16_t* out = p.out + first;
+    const int step = 8 * p.d;
+    if (dead) there = 0;
+#pragma unroll 1
+    for (int m = 0; 128 * m + 32 * qd < p.d; ++m, out += 128, to += 64) {
+        uint32_t r[2][16];
+        tmem_ld_rows16(to, r[0]);
+        tmem_ld_rows16(to + (16u << 16), r[1]);
+        if (JOINS) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mine[32 * k] = pre[k];
+            __syncwarp();
+            load_prev(m + 1);
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            uint32_t w[4], pw[4];
+            if (JOINS) load_turned(block + 512u * (uint32_t)g, pw);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x0 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1)]) * fi[2 * g];
+                float x1 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1) + 1]) * fi[2 * g + 1];
+                if (JOINS) {   // weight 0: prev_out is not used
+                    x0 = fw[2 * g] != 0.f ? x0 + fw[2 * g] * __uint_as_float(pw[i] << 16) : x0;
+                    x1 = fw[2 * g + 1] != 0.f ? x1 + fw[2 * g + 1] * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
+                }
+                w[i] = pack_bf16x2(x0, x1);
+            }
+            store_turned(block + 512u * (uint32_t)g, w);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 v = mine[32 * k];
+            if (8 * k < there) *reinterpret_cast<uint4*>(out + k * step) = v;
+        }
+        __syncwarp();
+    }
 }
 
 // An MMA that accumulates if acc is not 0, and happens only if `on`.
@@ -451,6 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
         const uint32_t bar_set = 1u + (uint32_t)set;
         const float c = p.scale_log2;
+        const int own_i = (lane >> 2 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 4);   // over_rows leaves the lane its head own_i,
+        const int own_head = 8 * (own_i >> 1) + 2 * l4 + (own_i & 1);                // of the set's 32 this one
         uint32_t n = 0;
         bool dead = false;
         float m_run = -INFINITY;                 // what P is relative to, in log2: lane l: head 32 set + l
@@ -543,16 +620,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool need = !named_bar_and(bar_set, 128, !(first || ((kPack || v0) && top0 > kTopMost) || (v1 && top1 > kTopMost)));
             if (need) {
                 float* red = &tl->red[buf][set][qd][0];
+                float v[8];
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float v = fmaxf(sees(2 * g + k, 0) ? y[4 * g + k] : -INFINITY,
-                                        sees(2 * g + k, 1) ? y[4 * g + 2 + k] : -INFINITY);
-#pragma unroll
-                        for (int o = 4; o <= 16; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kWarpFull, v, o));
-                        if (lane < 4) red[8 * g + 2 * lane + k] = v;
-                    }
+                for (int i = 0; i < 8; ++i)
+                    v[i] = fmaxf(sees(i, 0) ? y[4 * (i >> 1) + (i & 1)] : -INFINITY,
+                                 sees(i, 1) ? y[4 * (i >> 1) + 2 + (i & 1)] : -INFINITY);
+                red[own_head] = over_rows<true>(v);
                 named_bar_sync(bar_set, 128);
                 const float* rr = &tl->red[buf][set][0][lane];
                 float* own = &tl->neg_m[set][qd][0];
@@ -609,22 +682,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a run's O^T and sums: the group's output when the run holds all its tiles, else a partial (slot >= 0: where);
         // sink, prev_lse: of head 32 set + lane
         auto epilogue = [&](int64_t row0, int heads, int slot, float sink, float prev_lse) {
-            // The warp has 32 heads x 32 dims of each d-block.  Pieces of 8 dims, four per lane: piece c = lane + 32 k is
-            // head c / 4 of the set, dims 8 (c % 4) ...
-            const int64_t out0 = (row0 + 32 * set) * p.d + 32 * qd;
-            auto piece = [&](int m, int k, int64_t& at) {
-                const int hd = (lane >> 2) + 8 * k;
-                at = out0 + (int64_t)hd * p.d + 128 * m + 8 * (lane & 3);
-                return 32 * set + hd < heads;
-            };
+            // The warp has 32 heads x 32 dims of each d-block.  Pieces of 8 dims, four per lane: piece k is head lane / 4 + 8 k
+            // of the set, dims 8 (lane % 4) ...
+            const int64_t first = (row0 + 32 * set + (lane >> 2)) * p.d + 32 * qd + 8 * (lane & 3);
+            const int there = heads - 32 * set - (lane >> 2);   // piece k is one if 8 k < there
             const bool joins = p.prev_out != nullptr && slot < 0;
             uint4 pre[4];      // prev_out, loaded a d-block ahead
             auto load_prev = [&](int m) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    int64_t at;
                     pre[k] = make_uint4(0, 0, 0, 0);
-                    if (piece(m, k, at) && 128 * m + 32 * qd < p.d) pre[k] = *reinterpret_cast<const uint4*>(p.prev_out + at);
+                    if (8 * k < there && 128 * m + 32 * qd < p.d)
+                        pre[k] = *reinterpret_cast<const uint4*>(p.prev_out + first + 128 * m + 8 * k * p.d);
                 }
             };
             if (joins) load_prev(0);
@@ -633,14 +702,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t any = saw;
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) any |= __shfl_xor_sync(kWarpFull, any, o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float v = l_thr[i];
-#pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) v += __shfl_xor_sync(kWarpFull, v, o);
-                // the sum of a head that saw none of the rows is -0, which adds up to -0 over such parts alone
-                if (lane < 4) tl->lsum[set][qd][8 * (i >> 1) + 2 * lane + (i & 1)] = any >> i & 1u ? v : -0.f;
-            }
+            // the sum of a head that saw none of the rows is -0, which adds up to -0 over such parts alone
+            const float sum = over_rows<false>(l_thr);
+            tl->lsum[set][qd][own_head] = any >> own_i & 1u ? sum : -0.f;
             named_bar_sync(bar_set, 128);
             const float* ls = &tl->lsum[set][0][lane];
             const float lt = (ls[0] + ls[32]) + (ls[64] + ls[96]);
@@ -686,57 +750,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // head's four pieces lie turned by (head / 2) % 4, so that neither side meets a bank twice.
             float2* fac = &tl->fac[set][qd][0];
             fac[lane] = make_float2(inv, wp);
-            uint8_t* stg = p_s + warp * 2048;
-            const int j8 = lane & 7;
-            const uint32_t block = smem_u32(stg) + (uint32_t)(j8 * 64 + ((((lane >> 3) + (j8 >> 1)) & 3) << 4));   // + 512 g
-            uint4* mine = reinterpret_cast<uint4*>(stg + (lane >> 2) * 64 + ((((lane & 3) + (((lane >> 2) & 7) >> 1)) & 3) << 4));
-#pragma unroll 1
-            for (int m = 0; 128 * m + 32 * qd < p.d; ++m) {
-                if (joins) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mine[32 * k] = pre[k];
-                    load_prev(m + 1);
-                }
-                __syncwarp();
-                const uint32_t to = tmem + lane_base + kTmO + 64u * (uint32_t)m + 32u * (uint32_t)set;
-#pragma unroll 1
-                for (int g = 0; g < 4; g += 2) {   // (short bodies: this code is fetched anew for every query)
-                    uint32_t r[2][8];
-                    tmem_ld_rows16_half(to + 8u * (uint32_t)g, r[0]);
-                    tmem_ld_rows16_half(to + 8u * (uint32_t)g + (16u << 16), r[1]);
-                    float4 f[2] = {*reinterpret_cast<const float4*>(fac + 8 * g + 2 * l4),
-                                   *reinterpret_cast<const float4*>(fac + 8 * g + 8 + 2 * l4)};   // (factor, prev's) of two heads
-                    uint32_t pw[2][4];
-                    if (joins) {
-                        load_turned(block + 512u * (uint32_t)g, pw[0]);
-                        load_turned(block + 512u * (uint32_t)g + 512u, pw[1]);
-                    }
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x0 = __uint_as_float(r[i >> 1][4 * e + 2 * (i & 1)]) * f[e].x;
-                            float x1 = __uint_as_float(r[i >> 1][4 * e + 2 * (i & 1) + 1]) * f[e].z;
-                            if (joins) {   // weight 0: prev_out is not used
-                                x0 = f[e].y != 0.f ? x0 + f[e].y * __uint_as_float(pw[e][i] << 16) : x0;
-                                x1 = f[e].w != 0.f ? x1 + f[e].w * __uint_as_float(pw[e][i] & 0xFFFF0000u) : x1;
-                            }
-                            w[i] = pack_bf16x2(x0, x1);
-                        }
-                        store_turned(block + 512u * (uint32_t)(g + e), w);
-                    }
-                }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    int64_t at;
-                    const uint4 v = mine[32 * k];
-                    if (piece(m, k, at) && !dead) *reinterpret_cast<uint4*>(p.out + at) = v;
-                }
-                __syncwarp();
-            }
+            __syncwarp();
+            if (joins) write_out<true>(p, fac, p_s + warp * 2048, tmem + lane_base + kTmO + 32u * (uint32_t)set, first, there, qd, dead, pre, load_prev);
+            else write_out<false>(p, fac, p_s + warp * 2048, tmem + lane_base + kTmO + 32u * (uint32_t)set, first, there, qd, dead, pre, load_prev);
         };
 
         Run run;
