@@ -693,28 +693,33 @@ def rope_freqs(rope_dims: int, theta: float = 10000.0, factor: float = 1.0, orig
     return turns.to(device)
 
 
-def _token_rows(t, b, s, rest, device, name):
-    """Check bf16 [b, s, *rest] whose tokens are contiguous, sequences and tokens any stride apart; its pointer and those
+def _token_rows(t, shape, device, name):
+    """Check bf16 [b, s, ...] whose tokens are contiguous, sequences and tokens any stride apart; its pointer and those
     two strides (a single sequence's or token's may be anything: the size)."""
-    shape, stride = t.shape, t.stride()
-    n, dense = 1, True
-    for size, st in zip(reversed(shape[2:]), reversed(stride[2:])):
-        dense = dense and (size == 1 or st == n)
-        n *= size
-    if t.dtype is not torch.bfloat16 or t.get_device() != device.index or tuple(shape) != (b, s, *rest) or not dense:
-        raise _mismatch(t, torch.bfloat16, f"{[b, s, *rest]} with contiguous tokens", device, name)
-    ts = stride[1] if s > 1 else n
-    return t.data_ptr(), stride[0] if b > 1 else s * ts, ts
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device.index:
+        raise _mismatch(t, torch.bfloat16, f"{list(shape)} with contiguous tokens", device, name)
+    n = shape[-1] if len(shape) == 3 else shape[2] * shape[3]
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * n, n
+    stride = t.stride()
+    size = 1
+    for i in range(len(shape) - 1, 1, -1):
+        if shape[i] != 1 and stride[i] != size:
+            raise _mismatch(t, torch.bfloat16, f"{list(shape)} with contiguous tokens", device, name)
+        size *= shape[i]
+    ts = stride[1] if shape[1] > 1 else n
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * ts, ts
 
 
 def _rope_args(freqs, rope_off, interleaved, d, device):
     """Pointer of the frequencies, rotated dims, first rotated dim and flags."""
     if freqs is None:
         return None, 0, 0, 0
-    if freqs.dim() != 1:
+    shape = freqs.shape
+    if len(shape) != 1:
         raise ValueError("freqs must be [rope_dims / 2]")
-    rd = 2 * freqs.shape[0]
-    return (_dense(freqs, torch.int64, freqs.shape, device, "freqs"), rd, d - rd if rope_off is None else rope_off,
+    rd = 2 * shape[0]
+    return (_dense(freqs, torch.int64, shape, device, "freqs"), rd, d - rd if rope_off is None else rope_off,
             0 if interleaved else ROPE_HALVES)
 
 
@@ -733,13 +738,14 @@ def norm_rope(x: torch.Tensor, start_pos: torch.Tensor, freqs: torch.Tensor | No
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return norm_rope(x, start_pos, freqs, rope_off, interleaved, inverse, gain, norm, weight, eps, n_new, out)
-    if x.dim() != 4:
+    shape = x.shape
+    if len(shape) != 4:
         raise ValueError("x must be [b, s, h, d]")
-    b, s, h, d = x.shape
+    b, s, h, d = shape
     if out is None:
-        out = (torch.empty if n_new is None else torch.zeros)(b, s, h, d, dtype=torch.bfloat16, device=dev)
-    px, xb, xt = _token_rows(x, b, s, (h, d), dev, "x")
-    py, yb, yt = _token_rows(out, b, s, (h, d), dev, "out")
+        out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=torch.bfloat16, device=dev)
+    px, xb, xt = _token_rows(x, shape, dev, "x")
+    py, yb, yt = _token_rows(out, shape, dev, "out")
     each = start_pos.dim() == 2
     pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
     st = lib().sti_norm_rope(
@@ -753,16 +759,16 @@ def norm_rope(x: torch.Tensor, start_pos: torch.Tensor, freqs: torch.Tensor | No
 
 def _pages(pages, block_table, b, d, device):
     """Check a pool of pages [n, page_size, d] and a table [b, most]; the C entries' seven arguments for them."""
-    ps = pages.stride()
-    if (pages.dtype is not torch.bfloat16 or pages.get_device() != device.index or pages.dim() != 3 or
-            pages.shape[2] != d or pages.shape[1] < 1 or ps[2] != 1 or (pages.shape[1] > 1 and ps[1] != d)):
+    shape, ps = pages.shape, pages.stride()
+    if (pages.dtype is not torch.bfloat16 or pages.get_device() != device.index or len(shape) != 3 or shape[2] != d or
+            shape[1] < 1 or ps[2] != 1 or (ps[1] != d and shape[1] > 1)):
         raise _mismatch(pages, torch.bfloat16, f"[pages, page_size, {d}] with contiguous rows", device, "pages")
-    ts = block_table.stride()
-    if (block_table.dtype is not torch.int32 or block_table.get_device() != device.index or block_table.dim() != 2 or
-            block_table.shape[0] != b or (block_table.shape[1] > 1 and ts[1] != 1)):
+    table, ts = block_table.shape, block_table.stride()
+    if (block_table.dtype is not torch.int32 or block_table.get_device() != device.index or len(table) != 2 or
+            table[0] != b or (ts[1] != 1 and table[1] > 1)):
         raise _mismatch(block_table, torch.int32, f"[{b}, pages per sequence] with contiguous rows", device, "block_table")
-    n, size = pages.shape[0], pages.shape[1]
-    most = block_table.shape[1]
+    n, size = shape[0], shape[1]
+    most = table[1]
     return (pages.data_ptr(), ps[0] if n > 1 else size * d, n, size, block_table.data_ptr(), ts[0] if b > 1 else most, most)
 
 
@@ -781,10 +787,11 @@ def kv_append_paged(x: torch.Tensor, start_pos: torch.Tensor, pages: torch.Tenso
         with _on(dev, stream):
             return kv_append_paged(x, start_pos, pages, block_table, freqs, rope_off, interleaved, gain, norm, weight, eps,
                                    n_new, ws)
-    if x.dim() != 3:
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x must be [b, s, d]")
-    b, s, d = x.shape
-    px, xb, xt = _token_rows(x, b, s, (d,), dev, "x")
+    b, s, d = shape
+    px, xb, xt = _token_rows(x, shape, dev, "x")
     pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
     st = lib().sti_kv_append_paged(
         px, xb, xt, _dense(start_pos, torch.int32, (b,), dev, "start_pos"), _dense(n_new, torch.int32, (b,), dev, "n_new"),

@@ -10,9 +10,9 @@
 // every 32-bit position (in fp32 the angle of position 10^6 is off by 2^-5 radians, its rounding).  The nearest quarter
 // turn is taken off in integers; what is left, at most an eighth of a turn, converts to fp32 and goes to sincospif.
 //
-// A block first computes the (cos, sin) of its tokens' pairs, one each per thread, into shared memory; they serve
-// all heads of the token.  LPR lanes share a row, 8 elements (16 bytes) per lane and chunk; kRowsAhead rows per slot are
-// loaded before the first is used.
+// A block takes the heads of one token, or with few heads several tokens.  It first computes the (cos, sin) of its tokens'
+// pairs, spread over its threads, into shared memory, where they serve all heads.  LPR lanes share a row, 8 elements
+// (16 bytes) per lane and chunk; U rows per slot are loaded before the first is used, the first ones before the angles.
 #include <cuda_bf16.h>
 
 #include "sti_internal.h"
@@ -22,13 +22,11 @@ namespace sti {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsAhead = 4;
+constexpr int kMaxAngles = 4096;   // pairs of a block's tokens: 32 KB
 
-struct Shape {          // how a block divides its rows
-    int heads_at_once;  // row slots that work on one token's heads
-    int tokens;         // tokens per block
-    int per;            // heads per slot
-    int blocks_h;       // blocks that share a token's heads
+struct Shape {      // a block's rows: `tokens` tokens of `heads` heads each
+    int tokens, heads;
+    int blocks_h;   // blocks that share a token's heads
 };
 
 // (cos, sin) of 2 pi turns / 2^64.
@@ -54,83 +52,75 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
     }
 }
 
-// LPR lanes per row, CH chunks of 8 elements per lane
-template <int LPR, int CH>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+// LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time
+template <int LPR, int CH, int U>
+__global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+    constexpr int kSlots = kThreads / LPR;
     extern __shared__ float2 cs[];                      // [tokens][rd / 2]
     const int slot = threadIdx.x / LPR, li = threadIdx.x % LPR;
     const int pairs = p.rd / 2;
-    const int64_t tokens = (int64_t)p.B * p.s;
-    const int64_t tok0 = (int64_t)(blockIdx.x / (unsigned)sh.blocks_h) * sh.tokens;
-    const int tb = slot / sh.heads_at_once, head0 = slot - tb * sh.heads_at_once + (int)(blockIdx.x % (unsigned)sh.blocks_h) * sh.per * sh.heads_at_once;
-    auto position = [&](int64_t tok) {
-        return p.pos_per_token ? __ldg(p.pos + tok) : (int)((uint32_t)__ldg(p.pos + tok / p.s) + (uint32_t)(tok % p.s));
-    };
-    const int64_t tok = tok0 + tb;
-    const int b = (int)(min(tok, tokens - 1) / p.s), t = (int)(min(tok, tokens - 1) - (int64_t)b * p.s);
-    const bool live = tok < tokens && tb < sh.tokens && (!p.n_new || t < __ldg(p.n_new + b));
+    const uint32_t tokens = (uint32_t)p.B * (uint32_t)p.s;              // (below 2^31)
+    const uint32_t tok0 = blockIdx.x / (uint32_t)sh.blocks_h * (uint32_t)sh.tokens;
+    const int head0 = (int)(blockIdx.x % (uint32_t)sh.blocks_h) * sh.heads;
+    const int rows = sh.tokens * sh.heads;
     const int chunks = p.d / 8;
-    const uint16_t* xrow = p.x + (int64_t)b * p.x_bstride + (int64_t)t * p.x_tstride;
-    uint4 v[kRowsAhead][CH];
-    auto load = [&](int k) {
+    auto position = [&](uint32_t tok, uint32_t b) {
+        return p.pos_per_token ? __ldg(p.pos + tok) : (int)((uint32_t)__ldg(p.pos + b) + (tok - b * (uint32_t)p.s));
+    };
+    uint4 v[U][CH];
+    const uint16_t* src[U];                             // null: not a row of this block, or a padding token's
+    int tk[U];                                          // its token among the block's
+    auto load = [&](int i0) {
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r) {
-            const int head = head0 + (k + r) * sh.heads_at_once;
+        for (int r = 0; r < U; ++r) {
+            const int i = i0 + r * kSlots;
+            tk[r] = sh.tokens == 1 ? 0 : i / sh.heads;
+            const int head = head0 + i - tk[r] * sh.heads;
+            const uint32_t tok = tok0 + (uint32_t)tk[r];
+            src[r] = nullptr;
+            if (i < rows && head < p.h && tok < tokens) {
+                const uint32_t b = tok / (uint32_t)p.s, t = tok - b * (uint32_t)p.s;
+                if (!p.n_new || (int)t < __ldg(p.n_new + b))
+                    src[r] = p.x + (int64_t)b * p.x_bstride + (int64_t)t * p.x_tstride + (int64_t)head * p.d;
+            }
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = li + LPR * i;
-                v[r][i] = make_uint4(0, 0, 0, 0);
-                if (live && k + r < sh.per && head < p.h && c < chunks)
-                    v[r][i] = *reinterpret_cast<const uint4*>(xrow + (int64_t)head * p.d + 8 * c);
+            for (int k = 0; k < CH; ++k) {
+                v[r][k] = make_uint4(0, 0, 0, 0);
+                if (src[r] && li + LPR * k < chunks) v[r][k] = *reinterpret_cast<const uint4*>(src[r] + 8 * (li + LPR * k));
             }
         }
     };
-    load(0);
+    load(slot);
     for (int i = threadIdx.x; i < sh.tokens * pairs; i += kThreads) {
-        const int tk = i / pairs, pr = i - tk * pairs;
-        if (tok0 + tk < tokens) {
-            float2 v2 = cos_sin((uint64_t)(int64_t)position(tok0 + tk) * __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + pr));
-            cs[i] = make_float2(v2.x * p.gain, (p.inverse ? -v2.y : v2.y) * p.gain);
+        const int t = i / pairs;
+        const uint32_t tok = tok0 + (uint32_t)t;
+        if (tok < tokens) {
+            const uint64_t f = __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + (i - t * pairs));
+            const float2 a = cos_sin((uint64_t)(int64_t)position(tok, tok / (uint32_t)p.s) * f);
+            cs[i] = make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
         }
     }
     __syncthreads();
-    uint16_t* yrow;
-    if (p.y) {
-        yrow = p.y + (int64_t)b * p.y_bstride + (int64_t)t * p.y_tstride;
-    } else {
-        yrow = nullptr;
-        if (live) {
-            const uint32_t at = (uint32_t)position(tok), pg = at / (uint32_t)p.page_size;
-            const int id = pg < (uint32_t)p.max_pages ? __ldg(p.table + (int64_t)b * p.table_stride + pg) : -1;
-            if (id >= 0 && id < p.n_pages)
-                yrow = p.pages + (int64_t)id * p.page_stride + (int64_t)(at - pg * (uint32_t)p.page_size) * p.d;
-            else if (li == 0 && p.status)
-                atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
-        }
-    }
-    const float2* my = cs + tb * pairs;
     const int c_lo = p.off / 8, c_hi = (p.off + p.rd) / 8, half = p.rd / 16;
-    for (int k = 0; k < sh.per; k += kRowsAhead) {
+    for (int i0 = slot;;) {
 #pragma unroll
-        for (int r = 0; r < kRowsAhead; ++r) {
-            const int head = head0 + (k + r) * sh.heads_at_once;
-            const bool on = live && k + r < sh.per && head < p.h;
+        for (int r = 0; r < U; ++r) {
             // the pairs' other halves, before anything of the row is written
             uint4 other[CH];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = li + LPR * i;
-                other[i] = make_uint4(0, 0, 0, 0);
-                if (p.halves && on && c >= c_lo && c < c_hi)
-                    other[i] = *reinterpret_cast<const uint4*>(xrow + (int64_t)head * p.d + 8 * (c < c_lo + half ? c + half : c - half));
+            for (int k = 0; k < CH; ++k) {
+                const int c = li + LPR * k;
+                other[k] = make_uint4(0, 0, 0, 0);
+                if (p.halves && src[r] && c >= c_lo && c < c_hi)
+                    other[k] = *reinterpret_cast<const uint4*>(src[r] + 8 * (c < c_lo + half ? c + half : c - half));
             }
             float scale = 1.f;
             if (p.norm) {
                 float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
+                for (int k = 0; k < CH; ++k) {
                     float f[8];
-                    unpack(v[r][i], f);
+                    unpack(v[r][k], f);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
                 }
@@ -139,13 +129,29 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                 scale = rsqrtf(sum / (float)p.d + p.eps);
             }
             __syncwarp();
-            if (!on || !yrow) continue;
+            if (!src[r]) continue;
+            // where the row goes
+            const uint32_t tok = tok0 + (uint32_t)tk[r], b = tok / (uint32_t)p.s, t = tok - b * (uint32_t)p.s;
+            uint16_t* dst;
+            if (p.y) {
+                const int head = head0 + i0 + r * kSlots - tk[r] * sh.heads;
+                dst = p.y + (int64_t)b * p.y_bstride + (int64_t)t * p.y_tstride + (int64_t)head * p.d;
+            } else {
+                const uint32_t at = (uint32_t)position(tok, b), pg = at / (uint32_t)p.page_size;
+                const int id = pg < (uint32_t)p.max_pages ? __ldg(p.table + (int64_t)b * p.table_stride + pg) : -1;
+                if (id < 0 || id >= p.n_pages) {
+                    if (li == 0 && p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+                    continue;
+                }
+                dst = p.pages + (int64_t)id * p.page_stride + (int64_t)(at - pg * (uint32_t)p.page_size) * p.d;
+            }
+            const float2* my = cs + tk[r] * pairs;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int c = li + LPR * i;
+            for (int k = 0; k < CH; ++k) {
+                const int c = li + LPR * k;
                 if (c >= chunks) continue;
                 float f[8];
-                unpack(v[r][i], f);
+                unpack(v[r][k], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] *= scale;
                 if (p.weight) {
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                         const bool low = c < c_lo + half;
                         const int oc = low ? c + half : c - half;
                         float g[8];
-                        unpack(other[i], g);
+                        unpack(other[k], g);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) g[j] *= scale;
                         if (p.weight) {
@@ -181,30 +187,31 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
                         }
                     }
                 }
-                *reinterpret_cast<uint4*>(yrow + (int64_t)head * p.d + 8 * c) =
+                *reinterpret_cast<uint4*>(dst + 8 * c) =
                     make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
             }
         }
-        if (k + kRowsAhead < sh.per) load(k + kRowsAhead);
+        i0 += U * kSlots;
+        if (i0 - slot >= rows) break;   // (the same for all of the block)
+        load(i0);
     }
 }
 
-template <int LPR, int CH>
+template <int LPR, int CH, int U>
 cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     constexpr int slots = kThreads / LPR;
     const int64_t tokens = (int64_t)p.B * p.s;
+    auto up = [](int64_t n, int64_t m) { return (n + m - 1) / m; };
     Shape sh;
-    sh.heads_at_once = 1;
-    while (sh.heads_at_once < p.h && sh.heads_at_once < slots) sh.heads_at_once *= 2;
-    sh.tokens = slots / sh.heads_at_once;
-    sh.per = (p.h + sh.heads_at_once - 1) / sh.heads_at_once;
-    const int64_t blocks_t = (tokens + sh.tokens - 1) / sh.tokens;
-    auto blocks_h = [&](int per) { return (p.h + per * sh.heads_at_once - 1) / (per * sh.heads_at_once); };
-    // few tokens: their heads go to several blocks
-    while (sh.per > 1 && blocks_t * blocks_h(sh.per) < num_sms) sh.per = (sh.per + 1) / 2;
-    sh.blocks_h = blocks_h(sh.per);
+    sh.heads = p.h;
+    sh.tokens = p.h >= slots ? 1 : U * slots / p.h;     // (up to U rows per slot)
+    if (p.rd > 0 && sh.tokens > kMaxAngles / (p.rd / 2)) sh.tokens = kMaxAngles / (p.rd / 2);
+    // few tokens: fewer per block, then their heads to several blocks, as long as every slot has a row
+    while (sh.tokens > 1 && sh.tokens * p.h > slots && up(tokens, sh.tokens) < 2 * num_sms) sh.tokens = (sh.tokens + 1) / 2;
+    while (sh.tokens == 1 && sh.heads > slots && tokens * up(p.h, sh.heads) < 2 * num_sms) sh.heads = (sh.heads + 1) / 2;
+    sh.blocks_h = (int)up(p.h, sh.heads);
     const size_t smem = (size_t)sh.tokens * (p.rd / 2) * sizeof(float2);
-    norm_rope_kernel<LPR, CH><<<(unsigned)(blocks_t * sh.blocks_h), kThreads, smem, stream>>>(p, sh);
+    norm_rope_kernel<LPR, CH, U><<<(unsigned)(up(tokens, sh.tokens) * sh.blocks_h), kThreads, smem, stream>>>(p, sh);
     return cudaGetLastError();
 }
 
@@ -212,12 +219,12 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     const int chunks = p.d / 8;
-    if (chunks <= 4) return launch<4, 1>(p, num_sms, stream);
-    if (chunks <= 8) return launch<8, 1>(p, num_sms, stream);
-    if (chunks <= 16) return launch<16, 1>(p, num_sms, stream);
-    if (chunks <= 32) return launch<32, 1>(p, num_sms, stream);
-    if (chunks <= 64) return launch<32, 2>(p, num_sms, stream);
-    return launch<32, 4>(p, num_sms, stream);
+    if (chunks <= 4) return launch<4, 1, 4>(p, num_sms, stream);
+    if (chunks <= 8) return launch<8, 1, 4>(p, num_sms, stream);
+    if (chunks <= 16) return launch<16, 1, 4>(p, num_sms, stream);
+    if (chunks <= 32) return launch<32, 1, 4>(p, num_sms, stream);
+    if (chunks <= 64) return launch<32, 2, 2>(p, num_sms, stream);
+    return launch<32, 4, 1>(p, num_sms, stream);
 }
 
 }  // namespace sti
