@@ -745,13 +745,14 @@ def norm_rope(x: torch.Tensor, start_pos: torch.Tensor, freqs: torch.Tensor | No
     if out is None:
         out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=torch.bfloat16, device=dev)
     px, xb, xt = _token_rows(x, shape, dev, "x")
-    py, yb, yt = _token_rows(out, shape, dev, "out")
-    each = start_pos.dim() == 2
+    py, yb, yt = (px, xb, xt) if out is x else _token_rows(out, shape, dev, "out")
+    each = len(start_pos.shape) == 2
     pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
     st = lib().sti_norm_rope(
         px, xb, xt, _dense(start_pos, torch.int32, (b, s) if each else (b,), dev, "start_pos"), each,
-        _dense(n_new, torch.int32, (b,), dev, "n_new"), b, s, h, d, norm, _dense(weight, torch.bfloat16, (d,), dev, "weight"),
-        eps, pf, rd, off, flags | (ROPE_INVERSE if inverse else 0), gain, py, yb, yt, _raw_stream(dev.index))
+        None if n_new is None else _dense(n_new, torch.int32, (b,), dev, "n_new"), b, s, h, d, norm,
+        None if weight is None else _dense(weight, torch.bfloat16, (d,), dev, "weight"), eps, pf, rd, off,
+        flags | ROPE_INVERSE if inverse else flags, gain, py, yb, yt, _raw_stream(dev.index))
     if st:
         _check(st, "sti_norm_rope")
     return out
@@ -794,8 +795,9 @@ def kv_append_paged(x: torch.Tensor, start_pos: torch.Tensor, pages: torch.Tenso
     px, xb, xt = _token_rows(x, shape, dev, "x")
     pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
     st = lib().sti_kv_append_paged(
-        px, xb, xt, _dense(start_pos, torch.int32, (b,), dev, "start_pos"), _dense(n_new, torch.int32, (b,), dev, "n_new"),
-        b, s, d, norm, _dense(weight, torch.bfloat16, (d,), dev, "weight"), eps, pf, rd, off, flags, gain,
+        px, xb, xt, _dense(start_pos, torch.int32, (b,), dev, "start_pos"),
+        None if n_new is None else _dense(n_new, torch.int32, (b,), dev, "n_new"), b, s, d, norm,
+        None if weight is None else _dense(weight, torch.bfloat16, (d,), dev, "weight"), eps, pf, rd, off, flags, gain,
         *_pages(pages, block_table, b, d, dev), None if ws is None else _workspace_ptr(ws, dev), _raw_stream(dev.index))
     if st:
         _check(st, "sti_kv_append_paged")

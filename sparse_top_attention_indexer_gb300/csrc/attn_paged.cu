@@ -272,11 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sets = hp > 32 ? 2 : 1;          // sets of 32 heads
     volatile int* abort = &tl->abort;
 
-    if (warp == 16) {
-        tmem_alloc(&tl->tmem_base, NM <= 2 ? 256 : 512);
-        tmem_relinquish();
-    }
     if (tid == 0) {
+        tma_prefetch_desc(&tm_q);
         for (int k = 0; k < 2; ++k) {
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&tl->full[k][h], h == 0 ? 256 + 8 : 256);
@@ -297,6 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     zero_padding(64, n_cb, NM, q_s, t_s);      // (Q's rows all come by TMA)
     fence_proxy_async_smem();
+    // From here on what earlier kernels wrote is read.  (TMEM after it too: a CTA that held it while it waits could keep it from
+    // one of the kernel it waits for.)
+    griddep_wait();
+    if (warp == 16) {
+        tmem_alloc(&tl->tmem_base, NM <= 2 ? 256 : 512);
+        tmem_relinquish();
+    }
     plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
               [&](int q) { return (group_rows(p, q / p.groups, q % p.groups) + kRows - 1) / kRows; });
     tc_fence_before();
@@ -832,11 +836,10 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
     auto* kernel = p.pack > 1 ? attn_paged_kernel<NM, true> : attn_paged_kernel<NM, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<p.grid, kThreads, smem, stream>>>(tm_q, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(kernel, dim3((unsigned)p.grid), kThreads, smem, stream, tm_q, p);
+    if (e != cudaSuccess || p.whole) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
     const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
-    if (p.whole) return cudaSuccess;
     return parts > 16  ? launch_after(merge_kernel<16, 32, AttnPagedParams>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
            : parts > 4 ? launch_after(merge_kernel<2, 128, AttnPagedParams>, dim3(mx, mh), 256, 0, stream, p)
                        : launch_after(merge_kernel<1, 128, AttnPagedParams>, dim3(mx, mh), 128, 0, stream, p);

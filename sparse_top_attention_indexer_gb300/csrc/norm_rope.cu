@@ -15,13 +15,14 @@
 // (16 bytes) per lane and chunk; U rows per slot are loaded before the first is used, the first ones before the angles.
 #include <cuda_bf16.h>
 
+#include "sti_attn_tiles.cuh"   // launch_after
 #include "sti_internal.h"
 #include "sti_ptx.cuh"
 
 namespace sti {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kRowThreads = 256;
 constexpr int kMaxAngles = 4096;   // pairs of a block's tokens: 32 KB
 
 struct Shape {      // a block's rows: `tokens` tokens of `heads` heads each
@@ -54,9 +55,9 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
 
 // LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time
 template <int LPR, int CH, int U>
-__global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
-    constexpr int kSlots = kThreads / LPR;
-    extern __shared__ float2 cs[];                      // [tokens][rd / 2]
+__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+    constexpr int kSlots = kRowThreads / LPR;
+    extern __shared__ float2 cs[];                      // [tokens][rd / 2], then int64 [tokens]
     const int slot = threadIdx.x / LPR, li = threadIdx.x % LPR;
     const int pairs = p.rd / 2;
     const uint32_t tokens = (uint32_t)p.B * (uint32_t)p.s;              // (below 2^31)
@@ -90,13 +91,30 @@ __global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_
             }
         }
     };
+    // the next kernel may start to be set up, the one before has to be done
+    griddep_launch_dependents();
+    griddep_wait();
     load(slot);
-    for (int i = threadIdx.x; i < sh.tokens * pairs; i += kThreads) {
+    // rows of pages: where each token's goes, -1 if nowhere
+    int64_t* at_page = reinterpret_cast<int64_t*>(cs + sh.tokens * pairs);
+    if (!p.y) {
+        for (int i = threadIdx.x; i < sh.tokens; i += kRowThreads) {
+            const uint32_t tok = tok0 + (uint32_t)i, b = tok / (uint32_t)p.s;
+            if (tok >= tokens) break;
+            const uint32_t at = (uint32_t)position(tok, b), pg = at / (uint32_t)p.page_size;
+            const int id = pg < (uint32_t)p.max_pages ? __ldg(p.table + (int64_t)b * p.table_stride + pg) : -1;
+            const bool good = id >= 0 && id < p.n_pages;
+            at_page[i] = good ? (int64_t)id * p.page_stride + (int64_t)(at - pg * (uint32_t)p.page_size) * p.d : -1;
+            if (!good && p.status && (!p.n_new || (int)(tok - b * (uint32_t)p.s) < __ldg(p.n_new + b)))
+                atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+        }
+    }
+    for (int i = threadIdx.x; i < sh.tokens * pairs; i += kRowThreads) {
         const int t = i / pairs;
-        const uint32_t tok = tok0 + (uint32_t)t;
-        if (tok < tokens) {
+        const uint32_t tok = tok0 + (uint32_t)t, b = tok / (uint32_t)p.s;
+        if (tok < tokens && (!p.n_new || (int)(tok - b * (uint32_t)p.s) < __ldg(p.n_new + b))) {
             const uint64_t f = __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + (i - t * pairs));
-            const float2 a = cos_sin((uint64_t)(int64_t)position(tok, tok / (uint32_t)p.s) * f);
+            const float2 a = cos_sin((uint64_t)(int64_t)position(tok, b) * f);
             cs[i] = make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
         }
     }
@@ -131,19 +149,14 @@ __global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_
             __syncwarp();
             if (!src[r]) continue;
             // where the row goes
-            const uint32_t tok = tok0 + (uint32_t)tk[r], b = tok / (uint32_t)p.s, t = tok - b * (uint32_t)p.s;
             uint16_t* dst;
             if (p.y) {
+                const uint32_t tok = tok0 + (uint32_t)tk[r], b = tok / (uint32_t)p.s, t = tok - b * (uint32_t)p.s;
                 const int head = head0 + i0 + r * kSlots - tk[r] * sh.heads;
                 dst = p.y + (int64_t)b * p.y_bstride + (int64_t)t * p.y_tstride + (int64_t)head * p.d;
             } else {
-                const uint32_t at = (uint32_t)position(tok, b), pg = at / (uint32_t)p.page_size;
-                const int id = pg < (uint32_t)p.max_pages ? __ldg(p.table + (int64_t)b * p.table_stride + pg) : -1;
-                if (id < 0 || id >= p.n_pages) {
-                    if (li == 0 && p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
-                    continue;
-                }
-                dst = p.pages + (int64_t)id * p.page_stride + (int64_t)(at - pg * (uint32_t)p.page_size) * p.d;
+                if (at_page[tk[r]] < 0) continue;
+                dst = p.pages + at_page[tk[r]];
             }
             const float2* my = cs + tk[r] * pairs;
 #pragma unroll
@@ -199,20 +212,20 @@ __global__ void __launch_bounds__(kThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_
 
 template <int LPR, int CH, int U>
 cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
-    constexpr int slots = kThreads / LPR;
+    constexpr int slots = kRowThreads / LPR;
     const int64_t tokens = (int64_t)p.B * p.s;
     auto up = [](int64_t n, int64_t m) { return (n + m - 1) / m; };
     Shape sh;
     sh.heads = p.h;
-    sh.tokens = p.h >= slots ? 1 : U * slots / p.h;     // (up to U rows per slot)
+    sh.tokens = p.h >= slots ? 1 : 2 * U * slots / p.h;   // (up to 2 U rows per slot)
     if (p.rd > 0 && sh.tokens > kMaxAngles / (p.rd / 2)) sh.tokens = kMaxAngles / (p.rd / 2);
     // few tokens: fewer per block, then their heads to several blocks, as long as every slot has a row
     while (sh.tokens > 1 && sh.tokens * p.h > slots && up(tokens, sh.tokens) < 2 * num_sms) sh.tokens = (sh.tokens + 1) / 2;
     while (sh.tokens == 1 && sh.heads > slots && tokens * up(p.h, sh.heads) < 2 * num_sms) sh.heads = (sh.heads + 1) / 2;
     sh.blocks_h = (int)up(p.h, sh.heads);
-    const size_t smem = (size_t)sh.tokens * (p.rd / 2) * sizeof(float2);
-    norm_rope_kernel<LPR, CH, U><<<(unsigned)(up(tokens, sh.tokens) * sh.blocks_h), kThreads, smem, stream>>>(p, sh);
-    return cudaGetLastError();
+    const size_t smem = (size_t)sh.tokens * ((p.rd / 2) * sizeof(float2) + sizeof(int64_t));
+    return launch_after(norm_rope_kernel<LPR, CH, U>, dim3((unsigned)(up(tokens, sh.tokens) * sh.blocks_h)), kRowThreads, smem,
+                        stream, p, sh);
 }
 
 }  // namespace
