@@ -567,14 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // i0: this thread's first row of the list
         auto softmax = [&](const Run& run, int i0, bool first) {
             const uint32_t buf = n & 1u;
+            mwait(&tl->full[buf][0], (n >> 1) & 1u);   // (long before S^T: makes `valid` visible)
+            const uint32_t val = *reinterpret_cast<const uint16_t*>(&tl->valid[buf][2 * qd]) >> (lane >> 2);
             mwait(&tl->s_full[buf], (n >> 1) & 1u);
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h) mwait(&tl->full[buf][h], (n >> 1) & 1u);   // (complete; makes it visible)
             tc_fence_after();
             const uint32_t ts = tmem + lane_base + 64u * buf + 32u * (uint32_t)set;
             uint32_t r[16];
             tmem_ld_rows16(ts, r);
-            const uint32_t val = *reinterpret_cast<const uint16_t*>(&tl->valid[buf][2 * qd]) >> (lane >> 2);
             const bool v0 = (val & 1u) && !dead, v1 = (val & 0x100u) && !dead;
             auto sees = [&](int i, int second) {   // the thread's head i its first or second row
                 const bool v = second ? v1 : v0;
@@ -594,7 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (k & 2) bad1 = bad1 || b;
                     else bad0 = bad0 || b;
                 }
-                if (__any_sync(kWarpFull, bad0 || bad1)) clear_rows(buf, bad0, bad1);
+                if (__any_sync(kWarpFull, bad0 || bad1)) {
+                    mwait(&tl->full[buf][kHalves - 1], (n >> 1) & 1u);   // (complete: makes the rows visible)
+                    clear_rows(buf, bad0, bad1);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) saw |= (sees(i, 0) || sees(i, 1)) ? 1u << i : 0u;
             } else {
