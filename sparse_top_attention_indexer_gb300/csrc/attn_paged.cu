@@ -91,6 +91,13 @@ struct __align__(16) Run {
 };
 constexpr int kRuns = 4, kReaders = 19;        // runs published ahead; the warps that read them
 
+// This CTA's piece of the list of all groups' tiles: tiles lo .. hi - 1, the first one tile `off` of group q's list.
+struct Piece {
+    long long lo, hi, total;
+    int ctas;           // CTAs that have a piece
+    int q, off;
+};
+
 struct __align__(16) Tail {
     Run run[kRuns];
     float neg_m[2][4][32];    // [head group][warp of the group]: its copy of -reference
@@ -99,17 +106,32 @@ struct __align__(16) Tail {
     float lsum[2][4][32];
     int vis[2][64];           // [segment parity] per head: which rows of the list it sees (kPack), see head_vis
     uint8_t valid[2][8];      // [buffer][loading warp]: bit j: row 8 warp + j exists
-    Work work;
+    Piece piece;
     long long scratch[kThreads / 32];
-    uint64_t full[2][2];      // [buffer][half of the dims] filled: every loading thread's copies (and each warp's `valid`)
+    uint64_t full[2][2];      // [buffer][half of the dims] filled
     uint64_t freed[2][2];     // the PV has read it
     uint64_t s_full[2], p_full[2];
     uint64_t q_full, q_free;
-    uint64_t run_full[kRuns], run_empty[kRuns];
+    uint64_t run_full[kRuns], run_empty[kRuns];   // (the barriers lie in one row, see init_barriers)
     uint32_t tmem_base;
     int abort;
     int qk_tile;              // tiles whose QK was issued, for the prefetching warp
 };
+
+// One barrier per thread.
+__device__ __forceinline__ void init_barriers(Tail* tl, int sets) {
+    constexpr int kBars = 4 + 4 + 2 + 2 + 1 + 1 + 2 * kRuns;
+    static_assert(offsetof(Tail, run_empty) + sizeof(tl->run_empty) == offsetof(Tail, full) + kBars * sizeof(uint64_t), "");
+    const int i = threadIdx.x;
+    if (i >= kBars) return;
+    uint32_t count = 1;                                             // freed, s_full, q_full, q_free, run_full
+    if (i < 4) count = (i & 1) == 0 ? 256 + 8 : 256;                // full: every loading thread's copies, in the first half
+                                                                    // each warp's `valid` too
+    if (i == 10 || i == 11) count = 4 * (uint32_t)sets;             // p_full: the warps that have heads
+    if (i >= kBars - kRuns) count = kReaders;
+    mbar_init(&tl->full[0][0] + i, count);
+    fence_mbar_init();
+}
 
 size_t attn_paged_smem(int d) {
     const int n_cb = (d + 127) / 128 * 2;
@@ -253,6 +275,72 @@ __device__ __forceinline__ void umma_if(bool on, uint32_t d_tmem, uint32_t a_lo,
         : "memory");
 }
 
+__device__ __forceinline__ int tiles_of(const AttnPagedParams& p, int q) {
+    const int b = q / p.groups;
+    return (rows_of(p, b, q - b * p.groups).n + kRows - 1) / kRows;
+}
+
+// x / y for quotients and remainders of a list's positions: 64-bit divisions take some hundred cycles, and their code.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+    return (x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+}
+
+// Pieces of total / ctas tiles, the first total % ctas of them one longer; the CTA that has tile x.
+__device__ __forceinline__ int piece_of(const Piece& w, long long x) {
+    const long long per = divide(w.total, w.ctas), longer = w.total - per * w.ctas;
+    return (int)(x < longer * (per + 1) ? divide(x, per + 1) : longer + divide(x - longer * (per + 1), per));
+}
+
+// This CTA's piece.  Every thread calls it.
+__device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail* tl) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = n <= kThreads ? 1 : (n + kThreads - 1) / kThreads;
+    const long long i0 = (long long)tid * each;
+    long long sum = 0;
+    for (int k = 0; k < each && i0 + k < n; ++k) sum += tiles_of(p, (int)(i0 + k));
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(kWarpFull, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) tl->scratch[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) {
+        const long long u = tl->scratch[k];
+        if (k < warp) before += u;
+        total += u;
+    }
+    const long long first = before + inc - sum;
+    const int part = (int)blockIdx.x, ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+    long long lo = 0, hi = 0;
+    if (part < ctas) {
+        const long long per = divide(total, ctas), longer = total - per * ctas;
+        lo = part * per + (part < longer ? part : longer);
+        hi = lo + per + (part < longer ? 1 : 0);
+    }
+    if (tid == 0) {
+        tl->piece.lo = lo;
+        tl->piece.hi = hi;
+        tl->piece.total = total;
+        tl->piece.ctas = ctas;
+    }
+    if (lo < hi && first <= lo && lo < first + sum) {
+        long long at = first;
+        int i = (int)i0;
+        if (each > 1)
+            for (;; ++i) {
+                const int c = tiles_of(p, i);
+                if (at + c > lo) break;
+                at += c;
+            }
+        tl->piece.q = i;
+        tl->piece.off = (int)(lo - at);
+    }
+}
+
 template <int NM, bool kPack>   // d-blocks of 128 dims; groups of several queries
 __global__ void __launch_bounds__(kThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnPagedParams p) {
@@ -272,27 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sets = hp > 32 ? 2 : 1;          // sets of 32 heads
     volatile int* abort = &tl->abort;
 
-    if (tid == 0) {
+    init_barriers(tl, sets);
+    if (tid == 32) {
         tma_prefetch_desc(&tm_q);
-        for (int k = 0; k < 2; ++k) {
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(&tl->full[k][h], h == 0 ? 256 + 8 : 256);
-                mbar_init(&tl->freed[k][h], 1);
-            }
-            mbar_init(&tl->s_full[k], 1);
-            mbar_init(&tl->p_full[k], 4 * sets);
-        }
-        mbar_init(&tl->q_full, 1);
-        mbar_init(&tl->q_free, 1);
-        for (int k = 0; k < kRuns; ++k) {
-            mbar_init(&tl->run_full[k], 1);
-            mbar_init(&tl->run_empty[k], kReaders);
-        }
         tl->abort = 0;
         tl->qk_tile = 0;
-        fence_mbar_init();
     }
-    zero_padding(64, n_cb, NM, q_s, t_s);      // (Q's rows all come by TMA)
+    if (n_cb & 1) zero_padding(64, n_cb, NM, q_s, t_s);   // (Q's rows all come by TMA)
     fence_proxy_async_smem();
     // From here on what earlier kernels wrote is read.  (TMEM after it too: a CTA that held it while it waits could keep it from
     // one of the kernel it waits for.)
@@ -301,13 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&tl->tmem_base, NM <= 2 ? 256 : 512);
         tmem_relinquish();
     }
-    plan_work(nq, blockIdx.x, gridDim.x, tl->scratch, &tl->work,
-              [&](int q) { return (group_rows(p, q / p.groups, q % p.groups) + kRows - 1) / kRows; });
+    plan_piece(p, nq, tl);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);   // warp-uniform, as the compiler can see
-    const Work wk = tl->work;
     griddep_launch_dependents();
 
     // The next run for this warp (false: none, or a wait gave up).
@@ -394,48 +466,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The rows of the next kAhead tiles are on their way to L2 when a tile is loaded, asked for by a
             // sequence's first query only: the others find them there.
             volatile int* now = &tl->qk_tile;
-            Walk walk(wk, p.whole);
-            Seg sg;
+            const Piece piece = tl->piece;
+            long long at_tile = piece.lo;
+            int q = piece.q, off = piece.off;
             int2 rec = make_int2(-1, 0);
             while (ok) {
-                const bool more = walk.next(p, sg);
-                const uint32_t k = runs % kRuns;
-                if (runs >= kRuns && !wait(&tl->run_empty[k], runs / kRuns - 1 & 1u)) break;
-                ++runs;
-                run.t1 = 0;
-                int u = 0;
-                if (more) {
-                    const PagedGroup grp = group_of(p, sg.q);
-                    u = sg.q - sg.b * p.groups;
-                    const PagedRows rows = rows_of(p, sg.b, u);
-                    run.t0 = sg.t0;
-                    run.t1 = sg.t1;
+                // the next group with a tile in the piece (p.whole: with its first tile there, and then all of it)
+                int nt = 0, u = 0;
+                for (; at_tile < piece.hi; ++q, off = 0) {
+                    run.b = q / p.groups;
+                    u = q - run.b * p.groups;
+                    const uint32_t start = (uint32_t)__ldg(p.start_pos + run.b);
+                    const int real = paged_new(p, run.b);
+                    const PagedRows rows = rows_of(p, run.b, u);
+                    run.pos = start + (uint32_t)(u * p.pack);
+                    run.heads = max(min(p.pack, real - u * p.pack), 0) * p.h;
+                    run.row0 = (run.b * p.s + u * p.pack) * p.h;
                     run.n = rows.n;
                     run.nf = rows.nf;
                     run.lo = rows.lo;
-                    run.b = sg.b;
-                    run.heads = grp.heads;
-                    run.row0 = (int)grp.row0;
-                    run.slot = sg.t0 == 0 && sg.t1 == sg.nt ? -1 : 2 * (int)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
-                    run.pos = (uint32_t)__ldg(p.start_pos + sg.b) + (uint32_t)grp.t0;
-                    if (sg.t0 == 0 && sg.t1 < sg.nt) {
-                        const long long last = walk.pos - sg.t1 + sg.nt - 1;   // list position of the query's last tile
-                        int c = (int)(last * wk.ctas / wk.total);
-                        while ((long long)(c + 1) * wk.total / wk.ctas <= last) ++c;
-                        while ((long long)c * wk.total / wk.ctas > last) --c;
-                        rec = make_int2(sg.q, c);
-                    }
+                    nt = (rows.n + kRows - 1) / kRows;
+                    if (nt > 0 && !(p.whole && off > 0)) break;
+                    at_tile += nt - off;
+                    nt = 0;
+                }
+                const uint32_t k = runs % kRuns;
+                if (runs >= kRuns && !wait(&tl->run_empty[k], runs / kRuns - 1 & 1u)) break;
+                ++runs;
+                run.t0 = run.t1 = 0;
+                if (nt > 0) {
+                    const long long left = piece.hi - at_tile;
+                    run.t0 = off;
+                    run.t1 = p.whole || nt - off < left ? nt : off + (int)left;
+                    run.slot = run.t0 == 0 && run.t1 == nt ? -1 : 2 * (int)blockIdx.x + (run.t0 == 0 ? 1 : 0);
                 }
                 if (lane == 0) {
                     tl->run[k] = run;
                     mbar_arrive(&tl->run_full[k]);
                 }
-                if (!more) break;
+                if (nt == 0) break;
+                if (run.t0 == 0 && run.t1 < nt) rec = make_int2(q, piece_of(piece, at_tile + nt - 1));
+                at_tile += run.t1 - run.t0;
+                ++q;
+                off = 0;
                 if (u != 0) {
-                    n += (uint32_t)(sg.t1 - sg.t0);
+                    n += (uint32_t)(run.t1 - run.t0);
                     continue;
                 }
-                for (int t = sg.t0; t < sg.t1; ++t, ++n) {
+                for (int t = run.t0; t < run.t1; ++t, ++n) {
                     // rows that lie side by side in one request each: a warp's bulk prefetches leave it one after another
                     const uint16_t* at[2] = {row_ptr(p, run, t * kRows + lane), row_ptr(p, run, t * kRows + 32 + lane)};
                     unsigned long long a[2], before[2];

@@ -136,13 +136,10 @@ struct Seg {            // a run of one group's tiles
 
 // Walk the piece: group by group, those without a visible row skipped.  P: a kernel's parameters, with
 // group_rows(p, b, u), the rows that group u of sequence b goes over.
-// whole: a group is not cut but falls to the CTA whose piece has its first tile.
 struct Walk {
     long long pos, hi;
     int q, off;
-    bool whole;
-    __device__ __forceinline__ explicit Walk(const Work& w, bool whole_ = false)
-        : pos(w.lo), hi(w.hi), q(w.q), off(w.off), whole(whole_) {}
+    __device__ __forceinline__ explicit Walk(const Work& w) : pos(w.lo), hi(w.hi), q(w.q), off(w.off) {}
     template <class P>
     __device__ __forceinline__ bool next(const P& p, Seg& s) {
         while (pos < hi) {
@@ -151,13 +148,9 @@ struct Walk {
             s.vis = group_rows(p, s.b, q - s.b * p.groups);
             s.nt = (s.vis + kRows - 1) / kRows;
             s.t0 = off;
-            s.t1 = whole || (long long)(s.nt - off) < hi - pos ? s.nt : off + (int)(hi - pos);
+            s.t1 = (long long)(s.nt - off) < hi - pos ? s.nt : off + (int)(hi - pos);
             off = 0;
             ++q;
-            if (whole && s.t0 > 0) {   // the CTA before has it
-                pos += s.nt - s.t0;
-                continue;
-            }
             if (s.nt > 0) {
                 pos += s.t1 - s.t0;
                 return true;
