@@ -693,34 +693,39 @@ def rope_freqs(rope_dims: int, theta: float = 10000.0, factor: float = 1.0, orig
     return turns.to(device)
 
 
-def _token_rows(t, shape, device, name):
+# These calls are short too: one C call's worth of Python matters, so the checks stand where they are needed and their
+# errors are worded apart.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_current_device, _current_raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _flat(t, dtype, shape, index, name):
+    """_dense by device index: the pointer of a contiguous tensor of a given type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise _mismatch(t, dtype, f"contiguous with shape {list(shape)}", torch.device("cuda", index), name)
+    return t.data_ptr()
+
+
+def _token_rows(t, shape, index, name):
     """Check bf16 [b, s, ...] whose tokens are contiguous, sequences and tokens any stride apart; its pointer and those
     two strides (a single sequence's or token's may be anything: the size)."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device.index:
-        raise _mismatch(t, torch.bfloat16, f"{list(shape)} with contiguous tokens", device, name)
-    n = shape[-1] if len(shape) == 3 else shape[2] * shape[3]
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1] * n, n
-    stride = t.stride()
-    size = 1
-    for i in range(len(shape) - 1, 1, -1):
-        if shape[i] != 1 and stride[i] != size:
-            raise _mismatch(t, torch.bfloat16, f"{list(shape)} with contiguous tokens", device, name)
-        size *= shape[i]
-    ts = stride[1] if shape[1] > 1 else n
-    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * ts, ts
+    n = shape[2] if len(shape) == 3 else shape[2] * shape[3]
+    if t.dtype is _BF16 and t.shape == shape and t.get_device() == index:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1] * n, n
+        stride = t.stride()
+        if (stride[-1] == 1 or shape[-1] == 1) and (len(shape) == 3 or stride[2] == shape[3] or shape[2] == 1):
+            ts = stride[1] if shape[1] > 1 else n
+            return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * ts, ts
+    raise _mismatch(t, _BF16, f"{list(shape)} with contiguous tokens", torch.device("cuda", index), name)
 
 
-def _rope_args(freqs, rope_off, interleaved, d, device):
-    """Pointer of the frequencies, rotated dims, first rotated dim and flags."""
-    if freqs is None:
-        return None, 0, 0, 0
+def _freqs(freqs, index):
+    """Pointer of the frequencies and the number of rotated dims."""
     shape = freqs.shape
     if len(shape) != 1:
         raise ValueError("freqs must be [rope_dims / 2]")
-    rd = 2 * shape[0]
-    return (_dense(freqs, torch.int64, shape, device, "freqs"), rd, d - rd if rope_off is None else rope_off,
-            0 if interleaved else ROPE_HALVES)
+    return _flat(freqs, _I64, shape, index, "freqs"), 2 * shape[0]
 
 
 def norm_rope(x: torch.Tensor, start_pos: torch.Tensor, freqs: torch.Tensor | None = None, rope_off: int | None = None,
@@ -732,45 +737,47 @@ def norm_rope(x: torch.Tensor, start_pos: torch.Tensor, freqs: torch.Tensor | No
     rotation); rope_off: first rotated dim (None: the last ones turn); interleaved: pairs (2i, 2i + 1), else
     (i, i + rope_dims / 2); inverse: back; norm, weight (bf16 [d] or None), eps: the norm; n_new: int32 [b], the step's
     real tokens (rows of the others stay as they are in `out`).  out may be x."""
-    dev = x.device
-    if dev.type != "cuda":
+    index = x.get_device()
+    if index < 0:
         raise ValueError("x must be a CUDA tensor")
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None or index != _current_device():
+        with _on(x.device, stream):
             return norm_rope(x, start_pos, freqs, rope_off, interleaved, inverse, gain, norm, weight, eps, n_new, out)
     shape = x.shape
     if len(shape) != 4:
         raise ValueError("x must be [b, s, h, d]")
     b, s, h, d = shape
     if out is None:
-        out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=torch.bfloat16, device=dev)
-    px, xb, xt = _token_rows(x, shape, dev, "x")
-    py, yb, yt = (px, xb, xt) if out is x else _token_rows(out, shape, dev, "out")
-    each = len(start_pos.shape) == 2
-    pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
-    st = lib().sti_norm_rope(
-        px, xb, xt, _dense(start_pos, torch.int32, (b, s) if each else (b,), dev, "start_pos"), each,
-        None if n_new is None else _dense(n_new, torch.int32, (b,), dev, "n_new"), b, s, h, d, norm,
-        None if weight is None else _dense(weight, torch.bfloat16, (d,), dev, "weight"), eps, pf, rd, off,
-        flags | ROPE_INVERSE if inverse else flags, gain, py, yb, yt, _raw_stream(dev.index))
+        out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=_BF16, device=x.device)
+    px, xb, xt = _token_rows(x, shape, index, "x")
+    py, yb, yt = (px, xb, xt) if out is x else _token_rows(out, shape, index, "out")
+    each = start_pos.dim() == 2
+    pf, rd = (None, 0) if freqs is None else _freqs(freqs, index)
+    st = (_lib or lib()).sti_norm_rope(
+        px, xb, xt, _flat(start_pos, _I32, (b, s) if each else (b,), index, "start_pos"), each,
+        None if n_new is None else _flat(n_new, _I32, (b,), index, "n_new"), b, s, h, d, norm,
+        None if weight is None else _flat(weight, _BF16, (d,), index, "weight"), eps, pf, rd,
+        rope_off if rope_off is not None else d - rd if rd else 0,
+        (0 if interleaved else ROPE_HALVES) + (ROPE_INVERSE if inverse else 0), gain, py, yb, yt, _current_raw_stream(index))
     if st:
         _check(st, "sti_norm_rope")
     return out
 
 
-def _pages(pages, block_table, b, d, device):
+def _pages(pages, block_table, b, d, index):
     """Check a pool of pages [n, page_size, d] and a table [b, most]; the C entries' seven arguments for them."""
     shape, ps = pages.shape, pages.stride()
-    if (pages.dtype is not torch.bfloat16 or pages.get_device() != device.index or len(shape) != 3 or shape[2] != d or
+    if (pages.dtype is not _BF16 or pages.get_device() != index or len(shape) != 3 or shape[2] != d or
             shape[1] < 1 or ps[2] != 1 or (ps[1] != d and shape[1] > 1)):
-        raise _mismatch(pages, torch.bfloat16, f"[pages, page_size, {d}] with contiguous rows", device, "pages")
+        raise _mismatch(pages, _BF16, f"[pages, page_size, {d}] with contiguous rows", torch.device("cuda", index), "pages")
     table, ts = block_table.shape, block_table.stride()
-    if (block_table.dtype is not torch.int32 or block_table.get_device() != device.index or len(table) != 2 or
+    if (block_table.dtype is not _I32 or block_table.get_device() != index or len(table) != 2 or
             table[0] != b or (ts[1] != 1 and table[1] > 1)):
-        raise _mismatch(block_table, torch.int32, f"[{b}, pages per sequence] with contiguous rows", device, "block_table")
+        raise _mismatch(block_table, _I32, f"[{b}, pages per sequence] with contiguous rows", torch.device("cuda", index),
+                        "block_table")
     n, size = shape[0], shape[1]
     most = table[1]
-    return (pages.data_ptr(), ps[0] if n > 1 else size * d, n, size, block_table.data_ptr(), ts[0] if b > 1 else most, most)
+    return pages.data_ptr(), ps[0] if n > 1 else size * d, n, size, block_table.data_ptr(), ts[0] if b > 1 else most, most
 
 
 def kv_append_paged(x: torch.Tensor, start_pos: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor,
@@ -781,24 +788,26 @@ def kv_append_paged(x: torch.Tensor, start_pos: torch.Tensor, pages: torch.Tenso
     (sti_kv_append_paged).  pages: bf16 [pages, page_size, d]; block_table: int32 [b, pages per sequence], the page of
     positions page_size * i ...; the rest as norm_rope.  ws: optional workspace whose status word reports
     rows outside the table or the pool (they are not written)."""
-    dev = x.device
-    if dev.type != "cuda":
+    index = x.get_device()
+    if index < 0:
         raise ValueError("x must be a CUDA tensor")
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None or index != _current_device():
+        with _on(x.device, stream):
             return kv_append_paged(x, start_pos, pages, block_table, freqs, rope_off, interleaved, gain, norm, weight, eps,
                                    n_new, ws)
     shape = x.shape
     if len(shape) != 3:
         raise ValueError("x must be [b, s, d]")
     b, s, d = shape
-    px, xb, xt = _token_rows(x, shape, dev, "x")
-    pf, rd, off, flags = _rope_args(freqs, rope_off, interleaved, d, dev)
-    st = lib().sti_kv_append_paged(
-        px, xb, xt, _dense(start_pos, torch.int32, (b,), dev, "start_pos"),
-        None if n_new is None else _dense(n_new, torch.int32, (b,), dev, "n_new"), b, s, d, norm,
-        None if weight is None else _dense(weight, torch.bfloat16, (d,), dev, "weight"), eps, pf, rd, off, flags, gain,
-        *_pages(pages, block_table, b, d, dev), None if ws is None else _workspace_ptr(ws, dev), _raw_stream(dev.index))
+    px, xb, xt = _token_rows(x, shape, index, "x")
+    pf, rd = (None, 0) if freqs is None else _freqs(freqs, index)
+    st = (_lib or lib()).sti_kv_append_paged(
+        px, xb, xt, _flat(start_pos, _I32, (b,), index, "start_pos"),
+        None if n_new is None else _flat(n_new, _I32, (b,), index, "n_new"), b, s, d, norm,
+        None if weight is None else _flat(weight, _BF16, (d,), index, "weight"), eps, pf, rd,
+        rope_off if rope_off is not None else d - rd if rd else 0, 0 if interleaved else ROPE_HALVES, gain,
+        *_pages(pages, block_table, b, d, index), None if ws is None else _workspace_ptr(ws, x.device),
+        _current_raw_stream(index))
     if st:
         _check(st, "sti_kv_append_paged")
 
@@ -817,28 +826,32 @@ def attn_paged(q: torch.Tensor, pages: torch.Tensor, block_table: torch.Tensor, 
     prev_out / prev_lse: the same queries' attention over other rows, joined into the result; n_new: int32 [b], the
     step's real tokens (rows of the others stay as they are in `out` and `lse`); lse (fp32 [b, s, h]) is written when
     given.  ws: attn_paged_workspace_size bytes."""
-    dev = q.device
-    if dev.type != "cuda":
+    index = q.get_device()
+    if index < 0:
         raise ValueError("q must be a CUDA tensor")
-    if _elsewhere(dev, stream):
-        with _on(dev, stream):
+    if stream is not None or index != _current_device():
+        with _on(q.device, stream):
             return attn_paged(q, pages, block_table, start_pos, softmax_scale, window, n_first, attn_sink, prev_out,
                               prev_lse, n_new, out, lse, ws)
-    if q.dim() != 4:
-        raise ValueError("q must be [b, s, h, d]")
     shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [b, s, h, d]")
     b, s, h, d = shape
-    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     if out is None:
-        out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=bf16, device=dev)
+        out = (torch.empty if n_new is None else torch.zeros)(shape, dtype=_BF16, device=q.device)
     if ws is None:
-        ws = _call_workspace(attn_paged_workspace_size(b, s, h, d), dev)
-    st = lib().sti_attn_paged(
-        _dense(q, bf16, shape, dev, "q"), *_pages(pages, block_table, b, d, dev),
-        _dense(start_pos, i32, (b,), dev, "start_pos"), _dense(n_new, i32, (b,), dev, "n_new"), window, n_first,
-        _dense(attn_sink, f32, (h,), dev, "attn_sink"), softmax_scale, _dense(prev_out, bf16, shape, dev, "prev_out"),
-        _dense(prev_lse, f32, (b, s, h), dev, "prev_lse"), b, s, h, d, _dense(out, bf16, shape, dev, "out"),
-        _dense(lse, f32, (b, s, h), dev, "lse"), _workspace_ptr(ws, dev), ws.numel(), _raw_stream(dev.index))
+        ws = _call_workspace(attn_paged_workspace_size(b, s, h, d), q.device)
+    elif ws.dtype is not _U8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {q.device}")
+    st = (_lib or lib()).sti_attn_paged(
+        _flat(q, _BF16, shape, index, "q"), *_pages(pages, block_table, b, d, index),
+        _flat(start_pos, _I32, (b,), index, "start_pos"),
+        None if n_new is None else _flat(n_new, _I32, (b,), index, "n_new"), window, n_first,
+        None if attn_sink is None else _flat(attn_sink, _F32, (h,), index, "attn_sink"), softmax_scale,
+        None if prev_out is None else _flat(prev_out, _BF16, shape, index, "prev_out"),
+        None if prev_lse is None else _flat(prev_lse, _F32, (b, s, h), index, "prev_lse"), b, s, h, d,
+        _flat(out, _BF16, shape, index, "out"), None if lse is None else _flat(lse, _F32, (b, s, h), index, "lse"),
+        ws.data_ptr(), ws.numel(), _current_raw_stream(index))
     if st:
         _check(st, "sti_attn_paged")
     return out

@@ -24,6 +24,8 @@
 // is off by at most 2^-8 of itself, as much as the output's own rounding.  Its sum is taken before, in fp32.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "sti_attn_tiles.cuh"
 #include "sti_internal.h"
 
@@ -914,8 +916,16 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
     const int nq = p.B * p.groups;
     const size_t smem = attn_paged_smem(p.d);
     auto* kernel = p.pack > 1 ? attn_paged_kernel<NM, true> : attn_paged_kernel<NM, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The kernel's shared-memory limit, once per device (it follows from NM alone, so no other call asks for another).
+    static std::atomic<uint64_t> set[2];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(set[p.pack > 1].load(std::memory_order_acquire) & bit)) {
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+        set[p.pack > 1].fetch_or(bit, std::memory_order_release);
+    }
     e = launch_after(kernel, dim3((unsigned)p.grid), kThreads, smem, stream, tm_q, p);
     if (e != cudaSuccess || p.whole) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
