@@ -1145,6 +1145,7 @@ static sti_status norm_rope_args(sti::NormRopeParams* p, const uint16_t* x, int6
     p->turns = turns;
     p->eps = eps;
     p->gain = rope_gain;
+    p->inv_d = (float)(1.0 / d);
     p->B = b;
     p->s = seqlen;
     p->h = h;

@@ -7,8 +7,7 @@
 // pairs (2i, 2i + 1) or (i, i + rd / 2) of dims [off, off + rd); the inverse turns by -t.  All in fp32, rounded once.
 //
 // Angles: f_i comes as turns per position in units of 2^-64, so P f_i mod 1 is one 64-bit integer product, exact for
-// every 32-bit position (in fp32 the angle of position 10^6 is off by 2^-5 radians, its rounding).  The nearest quarter
-// turn is taken off in integers; what is left, at most an eighth of a turn, converts to fp32 and goes to sincospif.
+// every 32-bit position (in fp32 the angle of position 10^6 is off by 2^-5 radians, its rounding).
 //
 // A block takes the heads of one token, or with few heads several tokens.  It first computes the (cos, sin) of its tokens'
 // pairs, spread over its threads, into shared memory, where they serve all heads.  LPR lanes share a row, 8 elements
@@ -28,20 +27,21 @@ constexpr int kMaxAngles = 4096;   // pairs of a block's tokens: 32 KB
 struct Shape {      // a block's rows: `tokens` tokens of `heads` heads each
     int tokens, heads;
     int blocks_h;   // blocks that share a token's heads
+    int lanes;      // log2 of the threads that take a token's pairs
 };
 
-// (cos, sin) of 2 pi turns / 2^64.
+// (cos, sin) of 2 pi turns / 2^64.  With the nearest quarter turn off, x = 2 pi r is at most pi/4 = 0.786, where the
+// Taylor polynomials of degree 9 and 10 are off by x^11 / 11! < 2^-28 and x^12 / 12! < 2^-32.  (sincospif, made for
+// every argument, takes four times the instructions, a third of what an appended row took.)
 __device__ __forceinline__ float2 cos_sin(uint64_t turns) {
-    const uint64_t q = (turns + (1ull << 61)) >> 62;                     // nearest quarter, mod 4
-    const float r = (float)(int64_t)(turns - (q << 62)) * 0x1p-63f;      // the rest in half turns, [-1/4, 1/4]
-    float s, c;
-    sincospif(r, &s, &c);
-    switch ((int)q & 3) {
-        case 0: return make_float2(c, s);
-        case 1: return make_float2(-s, c);
-        case 2: return make_float2(-c, -s);
-        default: return make_float2(s, -c);
-    }
+    const uint32_t top = (uint32_t)(turns >> 32);                        // 2^-32 of a turn is 1.5e-9
+    const uint32_t q = (top + (1u << 29)) >> 30;                         // nearest quarter, mod 4
+    const float x = (float)(int)(top - (q << 30)) * 1.46291808e-9f;      // 2 pi 2^-32
+    const float y = x * x;
+    const float s = x + x * y * (-1.f / 6 + y * (1.f / 120 + y * (-1.f / 5040 + y * (1.f / 362880))));
+    const float c = 1.f + y * (-1.f / 2 + y * (1.f / 24 + y * (-1.f / 720 + y * (1.f / 40320 + y * (-1.f / 3628800)))));
+    const float a = q & 1 ? s : c, b = q & 1 ? c : s;                    // cos turns to -sin, sin to cos
+    return make_float2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
 }
 
 __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
@@ -55,19 +55,36 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
 
 // LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time
 template <int LPR, int CH, int U>
-__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+__global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 3 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
     constexpr int kSlots = kRowThreads / LPR;
-    extern __shared__ float2 cs[];                      // [tokens][rd / 2], then int64 [tokens]
+    extern __shared__ float2 cs[];                      // [tokens][rd / 2], then the tokens' places
     const int slot = threadIdx.x / LPR, li = threadIdx.x % LPR;
     const int pairs = p.rd / 2;
-    const uint32_t tokens = (uint32_t)p.B * (uint32_t)p.s;              // (below 2^31)
-    const uint32_t tok0 = blockIdx.x / (uint32_t)sh.blocks_h * (uint32_t)sh.tokens;
-    const int head0 = (int)(blockIdx.x % (uint32_t)sh.blocks_h) * sh.heads;
+    int64_t* from = reinterpret_cast<int64_t*>(cs + sh.tokens * pairs);   // of its first head in x, -1: padding or past the end
+    int64_t* to = from + sh.tokens;                                       // of its first head in y, its row's in the pages (-1: none)
+    int* at = reinterpret_cast<int*>(to + sh.tokens);                     // its position
+    const uint32_t bt = sh.blocks_h == 1 ? blockIdx.x : blockIdx.x / (uint32_t)sh.blocks_h;
+    const uint32_t tok0 = bt * (uint32_t)sh.tokens;
+    const int head0 = (int)(blockIdx.x - bt * (uint32_t)sh.blocks_h) * sh.heads;
     const int rows = sh.tokens * sh.heads;
     const int chunks = p.d / 8;
-    auto position = [&](uint32_t tok, uint32_t b) {
-        return p.pos_per_token ? __ldg(p.pos + tok) : (int)((uint32_t)__ldg(p.pos + b) + (tok - b * (uint32_t)p.s));
-    };
+    // the next kernel may start to be set up, the one before has to be done
+    griddep_launch_dependents();
+    griddep_wait();
+    uint32_t b = 0, t = 0;
+    int pos = 0;
+    if ((int)threadIdx.x < sh.tokens) {
+        const uint32_t tok = tok0 + threadIdx.x;
+        int64_t place = -1;
+        if (tok < (uint32_t)p.B * (uint32_t)p.s) {      // (below 2^31)
+            b = tok / (uint32_t)p.s;
+            t = tok - b * (uint32_t)p.s;
+            pos = p.pos_per_token ? __ldg(p.pos + tok) : (int)((uint32_t)__ldg(p.pos + b) + t);
+            if (!p.n_new || (int)t < __ldg(p.n_new + b)) place = (int64_t)b * p.x_bstride + (int64_t)t * p.x_tstride;
+        }
+        from[threadIdx.x] = place;
+    }
+    __syncthreads();
     uint4 v[U][CH];
     const uint16_t* src[U];                             // null: not a row of this block, or a padding token's
     int tk[U];                                          // its token among the block's
@@ -75,15 +92,10 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) no
 #pragma unroll
         for (int r = 0; r < U; ++r) {
             const int i = i0 + r * kSlots;
-            tk[r] = sh.tokens == 1 ? 0 : i / sh.heads;
+            tk[r] = sh.tokens == 1 ? 0 : sh.heads == 1 ? i : i / sh.heads;
             const int head = head0 + i - tk[r] * sh.heads;
-            const uint32_t tok = tok0 + (uint32_t)tk[r];
             src[r] = nullptr;
-            if (i < rows && head < p.h && tok < tokens) {
-                const uint32_t b = tok / (uint32_t)p.s, t = tok - b * (uint32_t)p.s;
-                if (!p.n_new || (int)t < __ldg(p.n_new + b))
-                    src[r] = p.x + (int64_t)b * p.x_bstride + (int64_t)t * p.x_tstride + (int64_t)head * p.d;
-            }
+            if (i < rows && head < p.h && from[tk[r]] >= 0) src[r] = p.x + from[tk[r]] + (int64_t)head * p.d;
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 v[r][k] = make_uint4(0, 0, 0, 0);
@@ -91,32 +103,36 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) no
             }
         }
     };
-    // the next kernel may start to be set up, the one before has to be done
-    griddep_launch_dependents();
-    griddep_wait();
     load(slot);
-    // rows of pages: where each token's goes, -1 if nowhere
-    int64_t* at_page = reinterpret_cast<int64_t*>(cs + sh.tokens * pairs);
-    if (!p.y) {
-        for (int i = threadIdx.x; i < sh.tokens; i += kRowThreads) {
-            const uint32_t tok = tok0 + (uint32_t)i, b = tok / (uint32_t)p.s;
-            if (tok >= tokens) break;
-            const uint32_t at = (uint32_t)position(tok, b), pg = at / (uint32_t)p.page_size;
+    if ((int)threadIdx.x < sh.tokens && from[threadIdx.x] >= 0) {
+        at[threadIdx.x] = pos;
+        int64_t place;
+        if (p.y) {
+            place = (int64_t)b * p.y_bstride + (int64_t)t * p.y_tstride;
+        } else {
+            const uint32_t pg = (uint32_t)pos / (uint32_t)p.page_size;
             const int id = pg < (uint32_t)p.max_pages ? __ldg(p.table + (int64_t)b * p.table_stride + pg) : -1;
             const bool good = id >= 0 && id < p.n_pages;
-            at_page[i] = good ? (int64_t)id * p.page_stride + (int64_t)(at - pg * (uint32_t)p.page_size) * p.d : -1;
-            if (!good && p.status && (!p.n_new || (int)(tok - b * (uint32_t)p.s) < __ldg(p.n_new + b)))
-                atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+            place = good ? (int64_t)id * p.page_stride + (int64_t)((uint32_t)pos - pg * (uint32_t)p.page_size) * p.d : -1;
+            if (!good && p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+        }
+        to[threadIdx.x] = place;
+    }
+    __syncthreads();
+    // 2^sh.lanes threads side by side take a token's pairs
+    for (int pr = threadIdx.x & ((1 << sh.lanes) - 1); pr < pairs; pr += 1 << sh.lanes) {
+        const uint64_t f = __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + pr);
+        for (int i = threadIdx.x >> sh.lanes; i < sh.tokens; i += kRowThreads >> sh.lanes) {
+            if (from[i] < 0) continue;
+            const float2 a = cos_sin((uint64_t)(int64_t)at[i] * f);
+            cs[i * pairs + pr] = make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
         }
     }
-    for (int i = threadIdx.x; i < sh.tokens * pairs; i += kRowThreads) {
-        const int t = i / pairs;
-        const uint32_t tok = tok0 + (uint32_t)t, b = tok / (uint32_t)p.s;
-        if (tok < tokens && (!p.n_new || (int)(tok - b * (uint32_t)p.s) < __ldg(p.n_new + b))) {
-            const uint64_t f = __ldg(reinterpret_cast<const unsigned long long*>(p.turns) + (i - t * pairs));
-            const float2 a = cos_sin((uint64_t)(int64_t)position(tok, b) * f);
-            cs[i] = make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
-        }
+    uint4 weight[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+        weight[k] = make_uint4(0, 0, 0, 0);
+        if (p.weight && li + LPR * k < chunks) weight[k] = __ldg(reinterpret_cast<const uint4*>(p.weight) + li + LPR * k);
     }
     __syncthreads();
     const int c_lo = p.off / 8, c_hi = (p.off + p.rd) / 8, half = p.rd / 16;
@@ -144,20 +160,13 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) no
                 }
 #pragma unroll
                 for (int o = LPR / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-                scale = rsqrtf(sum / (float)p.d + p.eps);
+                scale = rsqrtf(sum * p.inv_d + p.eps);
             }
             __syncwarp();
             if (!src[r]) continue;
-            // where the row goes
-            uint16_t* dst;
-            if (p.y) {
-                const uint32_t tok = tok0 + (uint32_t)tk[r], b = tok / (uint32_t)p.s, t = tok - b * (uint32_t)p.s;
-                const int head = head0 + i0 + r * kSlots - tk[r] * sh.heads;
-                dst = p.y + (int64_t)b * p.y_bstride + (int64_t)t * p.y_tstride + (int64_t)head * p.d;
-            } else {
-                if (at_page[tk[r]] < 0) continue;
-                dst = p.pages + at_page[tk[r]];
-            }
+            uint16_t* dst = p.y ? p.y : p.pages;        // where the row goes
+            if (to[tk[r]] < 0) continue;
+            dst += to[tk[r]] + (int64_t)(head0 + i0 + r * kSlots - tk[r] * sh.heads) * p.d;
             const float2* my = cs + tk[r] * pairs;
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
@@ -169,7 +178,7 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 3 : CH == 2 ? 4 : 2) no
                 for (int j = 0; j < 8; ++j) f[j] *= scale;
                 if (p.weight) {
                     float w[8];
-                    unpack(__ldg(reinterpret_cast<const uint4*>(p.weight) + c), w);
+                    unpack(weight[k], w);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] *= w[j];
                 }
@@ -218,12 +227,15 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     Shape sh;
     sh.heads = p.h;
     sh.tokens = p.h >= slots ? 1 : 2 * U * slots / p.h;   // (up to 2 U rows per slot)
+    if (sh.tokens > kRowThreads) sh.tokens = kRowThreads;
     if (p.rd > 0 && sh.tokens > kMaxAngles / (p.rd / 2)) sh.tokens = kMaxAngles / (p.rd / 2);
     // few tokens: fewer per block, then their heads to several blocks, as long as every slot has a row
     while (sh.tokens > 1 && sh.tokens * p.h > slots && up(tokens, sh.tokens) < 2 * num_sms) sh.tokens = (sh.tokens + 1) / 2;
     while (sh.tokens == 1 && sh.heads > slots && tokens * up(p.h, sh.heads) < 2 * num_sms) sh.heads = (sh.heads + 1) / 2;
     sh.blocks_h = (int)up(p.h, sh.heads);
-    const size_t smem = (size_t)sh.tokens * ((p.rd / 2) * sizeof(float2) + sizeof(int64_t));
+    sh.lanes = 0;
+    while (1 << sh.lanes < p.rd / 2 && 1 << sh.lanes < kRowThreads) ++sh.lanes;
+    const size_t smem = (size_t)sh.tokens * ((p.rd / 2) * sizeof(float2) + 2 * sizeof(int64_t) + sizeof(int));
     return launch_after(norm_rope_kernel<LPR, CH, U>, dim3((unsigned)(up(tokens, sh.tokens) * sh.blocks_h)), kRowThreads, smem,
                         stream, p, sh);
 }

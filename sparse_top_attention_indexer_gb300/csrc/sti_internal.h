@@ -237,7 +237,7 @@ struct NormRopeParams {
     const int32_t* n_new;       // [B] or null: tokens of the step that are real
     const uint16_t* weight;     // bf16 [d] or null
     const uint64_t* turns;      // [rd / 2] (rd 0: null): turns per position of each pair, in units of 2^-64
-    float eps, gain;
+    float eps, gain, inv_d;     // inv_d = 1 / d
     int B, s, h, d, norm;
     int rd, off, halves, inverse;
     uint16_t* y;                // bf16 [B, s, h, d], or null: rows of pages (h = 1)
