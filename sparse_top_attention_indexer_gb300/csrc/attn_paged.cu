@@ -12,13 +12,14 @@
 // contiguous pieces, one per CTA and SM (sti_attn_tiles.cuh); what a CTA has of a query that others share leaves as an
 // fp32 partial, which merge_kernel joins.  Two tile buffers; 20 warps:
 //   * warps 8..15 copy the rows to the free buffer (16 bytes per thread and copy, past L1 and the registers) as the PV two
-//     tiles earlier releases its halves.  Rows that nothing sees are not read but zeros, so that P = 0 meets no NaN;
+//     tiles earlier releases its halves.  Rows that nothing sees are not read but zeros, so that P = 0 meets no NaN.  They
+//     also write the outputs, while the softmax of the next query's first tiles runs;
 //   * warp 19 loads Q by TMA as soon as the last QK of the query before has read the buffer;
 //   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128 dims
 //     per block, K = the rows of the tile, the same tile read as an MN-major operand);
 //   * warp 18 walks the list, tells the others what comes next and asks for the rows of the next tiles, into L2;
 //   * warps 0..7 run the online softmax (two sets of 32 heads; what P is relative to moves only when a score passes it
-//     by 2^8) and write the outputs.
+//     by 2^8).
 //
 // P is rounded to bf16 for the PV product, as the rows are bf16 and one MMA takes one type: each row's share of the output
 // is off by at most 2^-8 of itself, as much as the output's own rounding.  Its sum is taken before, in fp32.
@@ -74,10 +75,14 @@ __device__ __forceinline__ bool head_seen(const AttnPagedParams&, const PagedGro
 
 namespace {
 
-// registers per thread after setmaxnreg: 256 x 144 + 256 x 64 + 128 x 64 = 61,440, the 640 x 96 of the launch
-constexpr int kRegsSoft = 144, kRegsLoad = 64, kRegsMma = 64;
+constexpr int kWarps = 24;                     // 8 softmax, 8 output, 4 loading, 4 others
+constexpr int kPThreads = 32 * kWarps;
+constexpr int kOutWarp = 8, kLoadWarp = 16, kQkWarp = 20, kPvWarp = 21, kListWarp = 22;   // (23 loads Q)
+// registers per thread after setmaxnreg: 256 x 104 + 256 x 72 + 128 x 64 + 128 x 64 = 61,440, the 768 x 80 of the launch
+constexpr int kRegsSoft = 104, kRegsOut = 72, kRegsLoad = 64, kRegsMma = 64;
 constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
 constexpr int kAhead = 4;                      // tiles whose rows are asked for ahead
+constexpr uint32_t kStage = 1024;              // 16 heads x 32 dims of bf16
 constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are not split between CTAs
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
@@ -91,7 +96,7 @@ struct __align__(16) Run {
     uint32_t pos;       // position of its first query
     int pad[2];
 };
-constexpr int kRuns = 4, kReaders = 19;        // runs published ahead; the warps that read them
+constexpr int kRuns = 4, kReaders = 23;        // runs published ahead; the warps that read them
 
 // This CTA's piece of the list of all groups' tiles: tiles lo .. hi - 1, the first one tile `off` of group q's list.
 struct Piece {
@@ -103,18 +108,22 @@ struct Piece {
 struct __align__(16) Tail {
     Run run[kRuns];
     float neg_m[2][4][32];    // [head group][warp of the group]: its copy of -reference
-    float2 fac[2][4][32];     // the outputs' factors
+    float2 fac[kRuns][64];    // [run % kRuns][head]: the outputs' factors, of O and of prev_out
     float red[2][2][4][32];   // [tile parity][group][warp]: per-warp maxima
     float lsum[2][4][32];
-    int vis[2][64];           // [segment parity] per head: which rows of the list it sees (kPack), see head_vis
-    uint8_t valid[2][8];      // [buffer][loading warp]: bit j: row 8 warp + j exists
+    int vis[2][64];           // [run parity] per head: which rows of the list it sees (kPack), see head_vis
+    uint8_t valid[2][8];      // [buffer][row / 8]: bit row % 8: it exists
     Piece piece;
-    long long scratch[kThreads / 32];
+    long long scratch[kWarps];
+    // the barriers lie in one row, see init_barriers
     uint64_t full[2][2];      // [buffer][half of the dims] filled
     uint64_t freed[2][2];     // the PV has read it
     uint64_t s_full[2], p_full[2];
     uint64_t q_full, q_free;
-    uint64_t run_full[kRuns], run_empty[kRuns];   // (the barriers lie in one row, see init_barriers)
+    uint64_t o_full[kRuns];                       // a run's PVs are done
+    uint64_t fac_full[kRuns];                     // its factors are there
+    uint64_t o_free[2][kRuns];                    // the first half of its O, all of it has been read
+    uint64_t run_full[kRuns], run_empty[kRuns];
     uint32_t tmem_base;
     int abort;
     int qk_tile;              // tiles whose QK was issued, for the prefetching warp
@@ -122,14 +131,16 @@ struct __align__(16) Tail {
 
 // One barrier per thread.
 __device__ __forceinline__ void init_barriers(Tail* tl, int sets) {
-    constexpr int kBars = 4 + 4 + 2 + 2 + 1 + 1 + 2 * kRuns;
+    constexpr int kBars = 4 + 4 + 2 + 2 + 2 + 6 * kRuns;
     static_assert(offsetof(Tail, run_empty) + sizeof(tl->run_empty) == offsetof(Tail, full) + kBars * sizeof(uint64_t), "");
     const int i = threadIdx.x;
     if (i >= kBars) return;
-    uint32_t count = 1;                                             // freed, s_full, q_full, q_free, run_full
-    if (i < 4) count = (i & 1) == 0 ? 256 + 8 : 256;                // full: every loading thread's copies, in the first half
+    uint32_t count = 1;                                             // freed, s_full, q_full, q_free, o_full, run_full
+    if (i < 4) count = (i & 1) == 0 ? 128 + 4 : 128;                // full: every loading thread's copies, in the first half
                                                                     // each warp's `valid` too
     if (i == 10 || i == 11) count = 4 * (uint32_t)sets;             // p_full: the warps that have heads
+    if (i >= 14 + kRuns && i < 14 + 2 * kRuns) count = (uint32_t)sets;   // fac_full: a warp of each set
+    if (i >= 14 + 2 * kRuns && i < 14 + 4 * kRuns) count = 8;       // o_free: the output warps
     if (i >= kBars - kRuns) count = kReaders;
     mbar_init(&tl->full[0][0] + i, count);
     fence_mbar_init();
@@ -137,20 +148,26 @@ __device__ __forceinline__ void init_barriers(Tail* tl, int sets) {
 
 size_t attn_paged_smem(int d) {
     const int n_cb = (d + 127) / 128 * 2;
-    return 1024 + (size_t)n_cb * (kQBlk + 2 * kTBlk) + 2 * kPBuf + sizeof(Tail);
+    return 1024 + (size_t)n_cb * (kQBlk + 2 * kTBlk) + 2 * kPBuf + 8 * kStage + sizeof(Tail);
 }
 
-// Where row i of the run's list lies, null if there is none (past the list; a page outside the pool).
-__device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, const Run& r, int i) {
-    if (i >= r.n) return nullptr;
+// Where row i of the run's list lies: its page's number, looked up in the table (-1 past the list), and its place in the page.
+struct RowAt {
+    int page, row;
+};
+__device__ __forceinline__ RowAt look_up(const AttnPagedParams& p, const Run& r, int i) {
+    if (i >= r.n) return RowAt{-1, 0};
     const uint32_t pos = (uint32_t)(i < r.nf ? i : r.lo + (i - r.nf));
     const uint32_t pg = pos / (uint32_t)p.page_size;
-    const int id = __ldg(p.table + (int64_t)r.b * p.table_stride + pg);
-    if (id < 0 || id >= p.n_pages) {
-        if (p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
+    return RowAt{__ldg(p.table + (int64_t)r.b * p.table_stride + pg), (int)(pos - pg * (uint32_t)p.page_size)};
+}
+// Its address, null if there is none (past the list; a page outside the pool, which is reported).
+__device__ __forceinline__ const uint16_t* row_ptr(const AttnPagedParams& p, const RowAt& at, bool listed) {
+    if (at.page < 0 || at.page >= p.n_pages) {
+        if (listed && p.status) atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
         return nullptr;
     }
-    return p.pages + (int64_t)id * p.page_stride + (int64_t)(pos - pg * (uint32_t)p.page_size) * p.d;
+    return p.pages + (int64_t)at.page * p.page_stride + (int64_t)at.row * p.d;
 }
 
 // Four 8 x 8 matrices of 16-bit values, each turned over on the way: lane 8 i + j gives the address of 8 values that become
@@ -202,52 +219,61 @@ __device__ __forceinline__ float over_rows(const float (&v)[8]) {
     return op(lane & 16 ? b[1] : b[0], __shfl_xor_sync(kWarpFull, send, 16));
 }
 
-// O^T of a warp's 32 heads (TMEM columns at `to`, 64 more per d-block) x 32 dims of each d-block, times the heads' factors
-// in fac (of O, of prev_out), as bf16 to p.out + first ...  A lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 (l % 4) +
-// {0, 1}; the 8 x 8 blocks are turned over on their way to [32 heads][32 dims] in shared memory at stg, where prev_out comes
-// from the same way.  A head's four pieces lie turned by (head / 2) % 4, so that neither side meets a bank twice.
-// (Turned over in fp32, with 16 scalar stores for each matrix store here, a query's outputs took 4.6 us, now 2.)
-template <bool JOINS, class F>
-__device__ __forceinline__ void write_out(const AttnPagedParams& p, const float2* fac, uint8_t* stg, uint32_t to, int64_t first,
-                                          int there, int qd, bool dead, uint4 (&pre)[4], F load_prev) {
-    const int lane = threadIdx.x & 31, l4 = lane & 3, j8 = lane & 7;
-    float fi[8], fw[8];
+// tmem_ld_rows16 of half the heads: g < 2.
+__device__ __forceinline__ void tmem_ld_rows16_half(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// Two pieces of 8 dims for a lane, of heads `first` and first + 8 from its own on (zeros past the group's).
+__device__ __forceinline__ void load_prev(uint4 (&pre)[2], const uint16_t* at, int first, int there, int d) {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const float4 v = *reinterpret_cast<const float4*>(fac + 8 * g + 2 * l4);
-        fi[2 * g] = v.x;
-        fw[2 * g] = v.y;
-        fi[2 * g + 1] = v.z;
-        fw[2 * g + 1] = v.w;
+    for (int k = 0; k < 2; ++k) {
+        pre[k] = make_uint4(0, 0, 0, 0);
+        if (first + 8 * k < there) pre[k] = *reinterpret_cast<const uint4*>(at + (int64_t)(first + 8 * k) * d);
     }
+}
+
+// O^T of a warp's 32 heads (TMEM columns at `to`) x 32 dims of a d-block, times the heads' factors in fac (of O, of prev), as
+// bf16 to out (JOINS: with what prev holds at the same place; pre: its first pieces, then the next block's if there is
+// one).  Half the heads at a time: a lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 (l % 4) + {0, 1}; the 8 x 8 blocks
+// are turned over on their way to [16 heads][32 dims] in shared memory at stg, where prev comes from the same way, in
+// pieces of 8 dims, two per lane: piece k is head lane / 4 + 8 k, dims 8 (lane % 4) ...  A head's four pieces lie
+// turned by (head / 2) % 4, so that neither side meets a bank twice.  out, prev: the lane's first piece; there: heads from
+// that one on.  (Turned over in fp32 with scalar stores, a query's outputs took twice as long.)
+template <bool JOINS>
+__device__ __forceinline__ void write_block(const float2* fac, uint8_t* stg, uint32_t to, uint16_t* out, const uint16_t* prev,
+                                            uint4 (&pre)[2], int there, int d, bool another) {
+    const int lane = threadIdx.x & 31, l4 = lane & 3, j8 = lane & 7;
     const uint32_t block = smem_u32(stg) + (uint32_t)(j8 * 64 + ((((lane >> 3) + (j8 >> 1)) & 3) << 4));   // + 512 g
     uint4* mine = reinterpret_cast<uint4*>(stg + (lane >> 2) * 64 + (((l4 + (((lane >> 2) & 7) >> 1)) & 3) << 4));
-    uint16_t* out = p.out + first;
-    const int step = 8 * p.d;
-    if (dead) there = 0;
 #pragma unroll 1
-    for (int m = 0; 128 * m + 32 * qd < p.d; ++m, out += 128, to += 64) {
-        uint32_t r[2][16];
-        tmem_ld_rows16(to, r[0]);
-        tmem_ld_rows16(to + (16u << 16), r[1]);
+    for (int h = 0; h < 32; h += 16) {
+        uint32_t r[2][8];
+        tmem_ld_rows16_half(to + (uint32_t)h, r[0]);
+        tmem_ld_rows16_half(to + (uint32_t)h + (16u << 16), r[1]);
+        const float4 f[2] = {*reinterpret_cast<const float4*>(fac + h + 2 * l4),
+                             *reinterpret_cast<const float4*>(fac + h + 8 + 2 * l4)};   // (of O, of prev) of two heads
         if (JOINS) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mine[32 * k] = pre[k];
+            mine[0] = pre[0];
+            mine[32] = pre[1];
             __syncwarp();
-            load_prev(m + 1);
+            if (h == 0) load_prev(pre, prev, 16, there, d);
+            else if (another) load_prev(pre, prev + 128, 0, there, d);
         }
         tmem_ld_wait();
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
             uint32_t w[4], pw[4];
             if (JOINS) load_turned(block + 512u * (uint32_t)g, pw);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float x0 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1)]) * fi[2 * g];
-                float x1 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1) + 1]) * fi[2 * g + 1];
-                if (JOINS) {   // weight 0: prev_out is not used
-                    x0 = fw[2 * g] != 0.f ? x0 + fw[2 * g] * __uint_as_float(pw[i] << 16) : x0;
-                    x1 = fw[2 * g + 1] != 0.f ? x1 + fw[2 * g + 1] * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
+                float x0 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1)]) * f[g].x;
+                float x1 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1) + 1]) * f[g].z;
+                if (JOINS) {   // weight 0: prev is not used
+                    x0 = f[g].y != 0.f ? x0 + f[g].y * __uint_as_float(pw[i] << 16) : x0;
+                    x1 = f[g].w != 0.f ? x1 + f[g].w * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
                 }
                 w[i] = pack_bf16x2(x0, x1);
             }
@@ -255,9 +281,9 @@ __device__ __forceinline__ void write_out(const AttnPagedParams& p, const float2
         }
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             const uint4 v = mine[32 * k];
-            if (8 * k < there) *reinterpret_cast<uint4*>(out + k * step) = v;
+            if (h + 8 * k < there) *reinterpret_cast<uint4*>(out + (int64_t)(h + 8 * k) * d) = v;
         }
         __syncwarp();
     }
@@ -296,7 +322,7 @@ __device__ __forceinline__ int piece_of(const Piece& w, long long x) {
 // This CTA's piece.  Every thread calls it.
 __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail* tl) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int each = n <= kThreads ? 1 : (n + kThreads - 1) / kThreads;
+    const int each = n <= kPThreads ? 1 : (n + kPThreads - 1) / kPThreads;
     const long long i0 = (long long)tid * each;
     long long sum = 0;
     for (int k = 0; k < each && i0 + k < n; ++k) sum += tiles_of(p, (int)(i0 + k));
@@ -310,7 +336,7 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
+    for (int k = 0; k < kWarps; ++k) {
         const long long u = tl->scratch[k];
         if (k < warp) before += u;
         total += u;
@@ -344,17 +370,24 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
 }
 
 template <int NM, bool kPack>   // d-blocks of 128 dims; groups of several queries
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnPagedParams p) {
     constexpr int kHalves = (NM + 1) / 2;
     constexpr uint32_t kTile = 2 * NM * kTBlk;
+    constexpr uint32_t kTmem = NM == 1 ? 256 : 512;
+    // TMEM columns of O^T: d-block m of run r lies in the (r NM + m)-th of a ring of blocks, so that the next run's PVs begin while
+    // this one's outputs are written: twice NM blocks, or the six that fit beside S^T (NM = 4: the second half of a run's
+    // blocks waits for the first half of the run before).
+    constexpr uint32_t kRing = 2 * NM < 6 ? 2 * NM : 6;
+    auto o_block = [](uint32_t r, uint32_t m) { return kTmO + 64u * ((r * NM + m) % kRing); };
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int n_cb = p.d / 64;                 // column blocks of 64 dims
     uint8_t* q_s = smem;                       // [2 NM][64 heads][128 B]
     uint8_t* t_s = q_s + 2 * NM * kQBlk;       // two tiles [2 NM][64 rows][128 B]
     uint8_t* p_s = t_s + 2 * kTile;            // two P^T [64 rows][64 heads] bf16
-    Tail* tl = reinterpret_cast<Tail*>(p_s + 2 * kPBuf);
+    uint8_t* o_s = p_s + 2 * kPBuf;            // per writing warp: outputs being turned over
+    Tail* tl = reinterpret_cast<Tail*>(o_s + 8 * kStage);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int nq = p.B * p.groups;
@@ -373,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // From here on what earlier kernels wrote is read.  (TMEM after it too: a CTA that held it while it waits could keep it from
     // one of the kernel it waits for.)
     griddep_wait();
-    if (warp == 16) {
-        tmem_alloc(&tl->tmem_base, NM <= 2 ? 256 : 512);
+    if (warp == kQkWarp) {
+        tmem_alloc(&tl->tmem_base, kTmem);
         tmem_relinquish();
     }
     plan_piece(p, nq, tl);
@@ -396,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r.t1 > 0;
     };
 
-    if (warp >= 16) {
+    if (warp >= kQkWarp) {
         regs_down<kRegsMma>();
         const int n_mma = (hp + 15) / 16 * 16;
         uint32_t n = 0;
@@ -407,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         };
         Run run;
-        if (warp == 16) {
+        if (warp == kQkWarp) {
             // -------------------------------------------------------------- QK: the tile and Q, both K-major
             const uint32_t idesc = idesc_bf16_f32(kRows, n_mma, false, false);
             const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
@@ -438,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-        } else if (warp == 17) {
+        } else if (warp == kPvWarp) {
             // -------------------------------------------------------------- PV: the tile and P^T, both MN-major
             const uint32_t idesc = idesc_bf16_f32(128, n_mma, true, true);
             const uint64_t dv = sdesc(smem_u32(t_s), kTBlk, 1024, kLayoutSW128), dp = sdesc(smem_u32(p_s), kPBuf, 1024, kLayoutSW128);
@@ -448,22 +481,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int steps = (run.n - t * kRows + 15) / 16;   // of 16 rows, four at most
                     if (!wait(&tl->p_full[buf], (n >> 1) & 1u)) break;
                     fence_proxy_async_smem();
-                    if (elect_one()) {
+                    const uint32_t r = runs - 1;
 #pragma unroll
-                        for (int m = 0; m < NM; ++m) {
-                            const uint32_t at = opaque(lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16));
-                            const uint32_t bt = opaque(lo32(dp) + buf * (kPBuf / 16));
+                    for (int h = 0; h < kHalves; ++h) {
+                        // a run's first tile: its blocks of the ring have been read
+                        if (t == run.t0 && h == 0 && r >= 2 && !wait(&tl->o_free[1][(r - 2) % kRuns], (r - 2) / kRuns & 1u)) break;
+                        if (t == run.t0 && h == 1 && NM == 4 && r >= 1 && !wait(&tl->o_free[0][(r - 1) % kRuns], (r - 1) / kRuns & 1u))
+                            break;
+                        if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < kRows / 16; ++k)
-                                umma_if(k < steps, tmem + kTmO + 64u * (uint32_t)m, at + 128 * k, hi32(dv), bt + 128 * k, hi32(dp),
-                                        idesc, (uint32_t)(t - run.t0 + k));
-                            if ((m & 1) || m == NM - 1) umma_commit(&tl->freed[buf][m >> 1]);
+                            for (int m = 2 * h; m < NM && m < 2 * h + 2; ++m) {
+                                const uint32_t at = opaque(lo32(dv) + buf * (kTile / 16) + (uint32_t)m * (2 * kTBlk / 16));
+                                const uint32_t bt = opaque(lo32(dp) + buf * (kPBuf / 16));
+                                const uint32_t o = tmem + o_block(r, (uint32_t)m);
+#pragma unroll
+                                for (int k = 0; k < kRows / 16; ++k)
+                                    umma_if(k < steps, o, at + 128 * k, hi32(dv), bt + 128 * k, hi32(dp), idesc,
+                                            (uint32_t)(t - run.t0 + k));
+                            }
+                            umma_commit(&tl->freed[buf][h]);
+                            if (h == kHalves - 1 && t == run.t1 - 1) umma_commit(&tl->o_full[r % kRuns]);
                         }
+                        __syncwarp();
                     }
+                    if (!ok) break;
                     __syncwarp();
                 }
             }
-        } else if (warp == 18) {
+        } else if (warp == kListWarp) {
             // -------------------------------------------------------------- the runs, and their rows' way to L2
             // The rows of the next kAhead tiles are on their way to L2 when a tile is loaded, asked for by a
             // sequence's first query only: the others find them there.
@@ -507,6 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&tl->run_full[k]);
                 }
                 if (nt == 0) break;
+                if (p.prev_out && lane == 0)   // what the run's end will read
+                    prefetch_l2_bulk(p.prev_out + (int64_t)run.row0 * p.d, (uint32_t)(run.heads * p.d) * 2u);
                 if (run.t0 == 0 && run.t1 < nt) rec = make_int2(q, piece_of(piece, at_tile + nt - 1));
                 at_tile += run.t1 - run.t0;
                 ++q;
@@ -517,7 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int t = run.t0; t < run.t1; ++t, ++n) {
                     // rows that lie side by side in one request each: a warp's bulk prefetches leave it one after another
-                    const uint16_t* at[2] = {row_ptr(p, run, t * kRows + lane), row_ptr(p, run, t * kRows + 32 + lane)};
+                    const int i0 = t * kRows + lane;
+                    const RowAt l0 = look_up(p, run, i0), l1 = look_up(p, run, i0 + 32);
+                    const uint16_t* at[2] = {row_ptr(p, l0, i0 < run.n), row_ptr(p, l1, i0 + 32 < run.n)};
                     unsigned long long a[2], before[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -558,27 +607,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= 8) {
+    } else if (warp >= kLoadWarp) {
         // -------------------------------------------------------------- tiles
-        // The warp's rows are 8 lw .. 8 lw + 7 of each tile, a lane copies 8 of every 256 dims of each.
+        // The warp's rows are 16 lw .. 16 lw + 15 of each tile; a lane copies 16 bytes of rows 16 lw + lane / 8 + 4 i (i < 4) of
+        // every column block, eight lanes a row's 128.
         regs_down<kRegsLoad>();
-        const int lw = warp - 8;
+        const int lw = warp - kLoadWarp, r8 = lane >> 3, ch = lane & 7;
         Run run;
         run.t1 = 0;
         int t = 0;
-        const int chunks = p.d / 8;
         bool dead = false;
-        for (uint32_t n = 0; !dead; ++n, ++t) {
+        // Lane j < 16 looks up where row 16 lw + j lies, a tile ahead of its use: the table's entry takes as long to come as
+        // the copies of a tile.
+        RowAt ahead{-1, 0};
+        bool more = true, listed = false;
+        auto next_tile = [&]() {
             if (t == run.t1) {
-                if (!next_run(run)) break;
+                more = next_run(run);
                 t = run.t0;
+                if (!more) return;
             }
+            const int i = t * kRows + 16 * lw + (lane & 15);
+            listed = i < run.n;
+            ahead = look_up(p, run, i);
+            ++t;
+        };
+        next_tile();
+        for (uint32_t n = 0; more && !dead; ++n) {
             const uint32_t buf = n & 1u;
-            // lane j < 8 has row 8 lw + j's place (the buffer is not free yet: its pages' numbers arrive meanwhile)
-            const uint16_t* rows_at = lane < 8 ? row_ptr(p, run, t * kRows + 8 * lw + lane) : nullptr;
-            const unsigned long long at = reinterpret_cast<unsigned long long>(rows_at);
-            const uint32_t have = __ballot_sync(kWarpFull, rows_at != nullptr);
-            const uint32_t dst = smem_u32(t_s) + buf * kTile + (uint32_t)(lane >> 3) * kTBlk + 8u * (uint32_t)lw * 128u;
+            const unsigned long long at = reinterpret_cast<unsigned long long>(row_ptr(p, ahead, listed));
+            const uint32_t have = __ballot_sync(kWarpFull, at != 0) & 0xFFFFu;
+            const uint16_t* src[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) src[i] = reinterpret_cast<const uint16_t*>(__shfl_sync(kWarpFull, at, r8 + 4 * i));
+            next_tile();
+            const uint32_t dst = smem_u32(t_s) + buf * kTile + (uint32_t)(16 * lw + r8) * 128u;
 #pragma unroll 1
             for (int h = 0; h < kHalves; ++h) {
                 if (n >= 2 && !warp_wait(&tl->freed[buf][h], ((n >> 1) - 1) & 1u, p.status, abort)) {
@@ -586,23 +649,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint16_t* src = reinterpret_cast<const uint16_t*>(__shfl_sync(kWarpFull, at, j));
-                    if (lane + 32 * h < chunks)   // a row that is not there: zeros, nothing is read
-                        cp_async_16(dst + 4u * h * kTBlk + (uint32_t)j * 128u + (uint32_t)(((lane & 7) ^ j) << 4),
-                                    src ? src + 8 * (lane + 32 * h) : p.out, src ? 16u : 0u);
+                for (int cb = 0; cb < 4; ++cb) {
+                    if (4 * h + cb >= n_cb) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)   // a row that is not there: zeros, nothing is read
+                        cp_async_16(dst + (uint32_t)(4 * h + cb) * kTBlk + 512u * i + (uint32_t)((ch ^ ((r8 + 4 * i) & 7)) << 4),
+                                    src[i] ? src[i] + 64 * (4 * h + cb) + 8 * ch : p.out, src[i] ? 16u : 0u);
                 }
                 cp_async_mbar_arrive_noinc(&tl->full[buf][h]);
                 if (h == 0 && lane == 0) {
-                    tl->valid[buf][lw] = (uint8_t)have;
+                    *reinterpret_cast<uint16_t*>(&tl->valid[buf][2 * lw]) = (uint16_t)have;
                     mbar_arrive(&tl->full[buf][0]);
                 }
             }
         }
         cp_async_wait<0>();
+    } else if (warp >= kOutWarp) {
+        // -------------------------------------------------------------- outputs
+        // A run's, while the next run's tiles are under way.
+        regs_down<kRegsOut>();
+        const int lw = warp - kOutWarp, set = lw >> 2, qd = lw & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * qd) << 16) + 32u * (uint32_t)set;
+        Run run;
+        while (next_run(run)) {
+            const uint32_t r = runs - 1, k = r % kRuns;
+            if (!warp_wait(&tl->fac_full[k], r / kRuns & 1u, p.status, abort)) break;
+            if (!warp_wait(&tl->o_full[k], r / kRuns & 1u, p.status, abort)) break;
+            tc_fence_after();
+            auto read = [&](int half) {   // of O
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tl->o_free[half][k]);
+            };
+            if (set < sets && run.slot >= 0) {   // a partial, [head][dim] in fp32: lanes hold dims
+                float* po = p.part_o + ((int64_t)run.slot * hp + 32 * set) * p.d + 32 * qd + lane;
+#pragma unroll 1
+                for (int i = 0; i < 2 * NM; ++i) {
+                    if (i == 4) read(0);
+                    if (128 * (i >> 1) + 32 * qd >= p.d) break;
+                    uint32_t v[16];
+                    tmem_ld16(lanes + o_block(r, (uint32_t)i >> 1) + 16u * (i & 1), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (32 * set + 16 * (i & 1) + j < hp)
+                            po[(int64_t)(16 * (i & 1) + j) * p.d + 128 * (i >> 1)] = __uint_as_float(v[j]);
+                }
+            } else if (set < sets) {
+                const int64_t first = (int64_t)(run.row0 + 32 * set + (lane >> 2)) * p.d + 32 * qd + 8 * (lane & 3);
+                const int there = run.heads - 32 * set - (lane >> 2);
+                const float2* fac = &tl->fac[k][32 * set];
+                uint16_t* out = p.out + first;
+                const uint16_t* prev = p.prev_out ? p.prev_out + first : nullptr;
+                uint4 pre[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};   // prev of the next step
+                if (prev) load_prev(pre, prev, 0, there, p.d);
+#pragma unroll 1
+                for (int m = 0; m < NM; ++m) {
+                    if (m == 2) read(0);
+                    const int left = p.d - 128 * m - 32 * qd;
+                    if (left <= 0) break;
+                    if (prev) write_block<true>(fac, o_s + lw * kStage, lanes + o_block(r, (uint32_t)m), out + 128 * m, prev + 128 * m, pre, there, p.d, left > 128);
+                    else write_block<false>(fac, o_s + lw * kStage, lanes + o_block(r, (uint32_t)m), out + 128 * m, out, pre, there, p.d, false);
+                }
+            } else if (NM > 2) {
+                read(0);
+            }
+            read(1);
+        }
     } else {
         regs_up<kRegsSoft>();
-        // -------------------------------------------------------------- softmax, outputs
+        // -------------------------------------------------------------- softmax
         const int set = warp >> 2, qd = warp & 3;
         const int row = 16 * qd + (lane >> 2);   // this thread's tile rows: row, row + 8
         const int l4 = lane & 3;                 // its heads: 32 set + 8 g + 2 l4 + {0, 1}
@@ -731,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < 2 * NM; ++k) {
-                        const uint32_t ta = tmem + lane_base + kTmO + 32u * (uint32_t)(2 * (k >> 1) + set) + 16u * (k & 1);
+                        const uint32_t ta = tmem + lane_base + o_block(runs - 1, (uint32_t)k >> 1) + 32u * (uint32_t)set + 16u * (k & 1);
                         uint32_t o[16];
                         tmem_ld16(ta, o);
                         tmem_ld_wait();
@@ -765,26 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&tl->p_full[buf]);
         };
 
-        // a run's O^T and sums: the group's output when the run holds all its tiles, else a partial (slot >= 0: where);
-        // sink, prev_lse: of head 32 set + lane
-        auto epilogue = [&](int64_t row0, int heads, int slot, float sink, float prev_lse) {
-            // The warp has 32 heads x 32 dims of each d-block.  Pieces of 8 dims, four per lane: piece k is head lane / 4 + 8 k
-            // of the set, dims 8 (lane % 4) ...
-            const int64_t first = (row0 + 32 * set + (lane >> 2)) * p.d + 32 * qd + 8 * (lane & 3);
-            const int there = heads - 32 * set - (lane >> 2);   // piece k is one if 8 k < there
-            const bool joins = p.prev_out != nullptr && slot < 0;
-            uint4 pre[4];      // prev_out, loaded a d-block ahead
-            auto load_prev = [&](int m) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    pre[k] = make_uint4(0, 0, 0, 0);
-                    if (8 * k < there && 128 * m + 32 * qd < p.d)
-                        pre[k] = *reinterpret_cast<const uint4*>(p.prev_out + first + 128 * m + 8 * k * p.d);
-                }
-            };
-            if (joins) load_prev(0);
-            mwait(&tl->freed[(n - 1) & 1u][kHalves - 1], ((n - 1) >> 1) & 1u);
-            tc_fence_after();
+        // The end of a run: its heads' sums, lse and factors, or for a partial (slot >= 0) sums and references.
+        auto finish = [&](const Run& run, float sink, float prev_lse) {
             uint32_t any = saw;
 #pragma unroll
             for (int o = 4; o <= 16; o <<= 1) any |= __shfl_xor_sync(kWarpFull, any, o);
@@ -792,17 +890,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float sum = over_rows<false>(l_thr);
             tl->lsum[set][qd][own_head] = any >> own_i & 1u ? sum : -0.f;
             named_bar_sync(bar_set, 128);
+            if (qd != 0) return;
             const float* ls = &tl->lsum[set][0][lane];
             const float lt = (ls[0] + ls[32]) + (ls[64] + ls[96]);
             const int hh = 32 * set + lane;
             float inv = 0.f, wp = 0.f;
-            if (slot >= 0) {
-                if (qd == 0) p.part_ml[slot * 64 + hh] = make_float2(m_run, lt);
-            } else if (signbit(lt) && hh < heads) {
+            if (run.slot >= 0) {
+                p.part_ml[run.slot * 64 + hh] = make_float2(m_run, lt);
+            } else if (signbit(lt) && hh < run.heads) {
                 // a query that sees no row: what it had
                 wp = prev_lse == -INFINITY ? 0.f : 1.f;
-                if (p.lse && qd == 0) p.lse[row0 + hh] = prev_lse;
-            } else if (hh < heads) {
+                if (p.lse) p.lse[run.row0 + hh] = prev_lse;
+            } else if (hh < run.heads) {
                 // everything relative to the largest of the reference, the sink and prev_lse
                 const float sk = sink * kLog2e, pl = prev_lse * kLog2e;
                 float mx = fmaxf(m_run, fmaxf(sk, pl));
@@ -813,68 +912,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float over = __fdividef(1.f, den);
                 inv = f * over;
                 wp = ep * over;
-                if (p.lse && qd == 0) p.lse[row0 + hh] = (mx + __log2f(den)) * kLn2;
+                if (p.lse) p.lse[run.row0 + hh] = (mx + __log2f(den)) * kLn2;
             }
-            if (slot >= 0) {   // [head][dim] in fp32, lanes hold dims
-#pragma unroll 1
-                for (int k = 0; k < 2 * NM; ++k) {
-                    const int h0 = 32 * set + 16 * (k & 1), dd = 128 * (k >> 1) + 32 * qd + lane;
-                    uint32_t r[16];
-                    tmem_ld16(tmem + lane_base + kTmO + 64u * (uint32_t)(k >> 1) + (uint32_t)h0, r);
-                    tmem_ld_wait();
-                    float* po = p.part_o + ((int64_t)slot * hp + h0) * p.d + dd;
-                    if (dd < p.d) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (h0 + i < hp) po[i * p.d] = __uint_as_float(r[i]);
-                    }
-                }
-                return;
-            }
-            // A lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 l4 + {0, 1}; rounded to bf16, the 8 x 8 blocks are turned over
-            // on their way to this warp's [32 heads][32 dims] of shared memory, where prev_out comes from the same way.  A
-            // head's four pieces lie turned by (head / 2) % 4, so that neither side meets a bank twice.
-            float2* fac = &tl->fac[set][qd][0];
-            fac[lane] = make_float2(inv, wp);
+            // (this run's scores mean that a PV of the run two before is done, and so that the run four before has been written)
+            const uint32_t k = (runs - 1) % kRuns;
+            tl->fac[k][hh] = make_float2(inv, wp);
             __syncwarp();
-            if (joins) write_out<true>(p, fac, p_s + warp * 2048, tmem + lane_base + kTmO + 32u * (uint32_t)set, first, there, qd, dead, pre, load_prev);
-            else write_out<false>(p, fac, p_s + warp * 2048, tmem + lane_base + kTmO + 32u * (uint32_t)set, first, there, qd, dead, pre, load_prev);
+            if (lane == 0) mbar_arrive(&tl->fac_full[k]);
         };
 
         Run run;
-        int pend_heads = 0, pend_row0 = 0, pend_slot = -1;   // the run whose output is pending
-        float pend_sink = -INFINITY, pend_lse = -INFINITY;   // and what it is joined with
-        int par = 0;                           // run parity
+        const int hh = 32 * set + lane;
+        const float sink = p.sink && hh < hp ? __ldg(p.sink + hh % p.h) : -INFINITY;
+        uint32_t par = 0;                      // run parity
         while (next_run(run)) {
-            if (kPack && tid < 64) tl->vis[par][tid] = head_vis(p, run, tid);   // (every warp is done with par's last)
-            if (tid == 0 && p.prev_out)   // what this run's end will read, into L2
-                prefetch_l2_bulk(p.prev_out + (int64_t)run.row0 * p.d, (uint32_t)(run.heads * p.d) * 2u);
-            if (pend_heads > 0 && active) epilogue(pend_row0, pend_heads, pend_slot, pend_sink, pend_lse);
-            named_bar_sync(kBarSoft, 256);     // the staging area is every warp's P^T; vis is complete
+            const float prev_lse = p.prev_lse && qd == 0 && hh < run.heads ? __ldg(p.prev_lse + run.row0 + hh) : -INFINITY;
+            if (kPack) {
+                if (tid < 64) tl->vis[par][tid] = head_vis(p, run, tid);   // (every warp is done with par's last)
+                named_bar_sync(kBarSoft, 256);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hv[i] = tl->vis[par][32 * set + 8 * (i >> 1) + 2 * l4 + (i & 1)];
+            }
             m_run = -INFINITY;
             tl->neg_m[set][qd][lane] = 0.f;
             __syncwarp();
             load_m();
-            if (kPack) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) hv[i] = tl->vis[par][32 * set + 8 * (i >> 1) + 2 * l4 + (i & 1)];
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
             saw = 0;
             for (int t = run.t0; t < run.t1; ++t, ++n)
                 if (active) softmax(run, t * kRows + row, t == run.t0);
-            par ^= 1;
-            pend_heads = run.heads;
-            pend_row0 = run.row0;
-            pend_slot = run.slot;
-            const int hh = 32 * set + lane;
-            if (hh < run.heads) {
-                if (p.sink) pend_sink = __ldg(p.sink + (kPack ? hh % p.h : hh));
-                pend_lse = p.prev_lse ? __ldg(p.prev_lse + run.row0 + hh) : -INFINITY;
-            }
+            if (active) finish(run, sink, prev_lse);
+            par ^= 1u;
         }
-        if (pend_heads > 0 && active) epilogue(pend_row0, pend_heads, pend_slot, pend_sink, pend_lse);
 
         // queries past the table are reported; groups whose lists are empty
         for (int q = blockIdx.x; q < nq; q += gridDim.x) {
@@ -905,9 +975,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (global_timer_ns() - t0 < 50000ull) {
         }
     }
-    if (warp == 16) {
+    if (warp == kQkWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, NM <= 2 ? 256 : 512);
+        tmem_dealloc(tmem, kTmem);
     }
 }
 
@@ -926,7 +996,7 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
         set[p.pack > 1].fetch_or(bit, std::memory_order_release);
     }
-    e = launch_after(kernel, dim3((unsigned)p.grid), kThreads, smem, stream, tm_q, p);
+    e = launch_after(kernel, dim3((unsigned)p.grid), kPThreads, smem, stream, tm_q, p);
     if (e != cudaSuccess || p.whole) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
     const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
