@@ -1276,6 +1276,7 @@ sti_status sti_attn_paged(const uint16_t* q, const uint16_t* pages, int64_t page
     const AttnPagedLayout l = attn_paged_layout(b, seqlen, h, d);
     uint8_t* wsb = static_cast<uint8_t*>(ws);
     sti::AttnPagedParams p{};
+    p.q = q;
     p.pages = pages;
     p.page_stride = page_stride;
     p.table = table;

@@ -83,7 +83,7 @@ constexpr int kRegsSoft = 104, kRegsOut = 72, kRegsLoad = 64, kRegsMma = 64;
 constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
 constexpr int kAhead = 4;                      // tiles whose rows are asked for ahead
 constexpr uint32_t kStage = 1024;              // 16 heads x 32 dims of bf16
-constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are not split between CTAs
+constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are never split between CTAs
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 // A run of one group's tiles, as warp 18 publishes it.
@@ -119,7 +119,7 @@ struct __align__(16) Tail {
     uint64_t full[2][2];      // [buffer][half of the dims] filled
     uint64_t freed[2][2];     // the PV has read it
     uint64_t s_full[2], p_full[2];
-    uint64_t q_full, q_free;
+    uint64_t q_full[2], q_free[2];                // per half of the dims
     uint64_t o_full[kRuns];                       // a run's PVs are done
     uint64_t fac_full[kRuns];                     // its factors are there
     uint64_t o_free[2][kRuns];                    // the first half of its O, all of it has been read
@@ -131,7 +131,7 @@ struct __align__(16) Tail {
 
 // One barrier per thread.
 __device__ __forceinline__ void init_barriers(Tail* tl, int sets) {
-    constexpr int kBars = 4 + 4 + 2 + 2 + 2 + 6 * kRuns;
+    constexpr int kBars = 4 + 4 + 2 + 2 + 4 + 6 * kRuns;
     static_assert(offsetof(Tail, run_empty) + sizeof(tl->run_empty) == offsetof(Tail, full) + kBars * sizeof(uint64_t), "");
     const int i = threadIdx.x;
     if (i >= kBars) return;
@@ -139,8 +139,8 @@ __device__ __forceinline__ void init_barriers(Tail* tl, int sets) {
     if (i < 4) count = (i & 1) == 0 ? 128 + 4 : 128;                // full: every loading thread's copies, in the first half
                                                                     // each warp's `valid` too
     if (i == 10 || i == 11) count = 4 * (uint32_t)sets;             // p_full: the warps that have heads
-    if (i >= 14 + kRuns && i < 14 + 2 * kRuns) count = (uint32_t)sets;   // fac_full: a warp of each set
-    if (i >= 14 + 2 * kRuns && i < 14 + 4 * kRuns) count = 8;       // o_free: the output warps
+    if (i >= 16 + kRuns && i < 16 + 2 * kRuns) count = (uint32_t)sets;   // fac_full: a warp of each set
+    if (i >= 16 + 2 * kRuns && i < 16 + 4 * kRuns) count = 8;       // o_free: the output warps
     if (i >= kBars - kRuns) count = kReaders;
     mbar_init(&tl->full[0][0] + i, count);
     fence_mbar_init();
@@ -445,13 +445,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const uint32_t idesc = idesc_bf16_f32(kRows, n_mma, false, false);
             const uint64_t dk = sdesc(smem_u32(t_s), 16, 1024, kLayoutSW128), dq = sdesc(smem_u32(q_s), 16, 1024, kLayoutSW128);
             while (ok && next_run(run)) {
-                if (!wait(&tl->q_full, (runs - 1) & 1u)) break;
                 for (int t = run.t0; t < run.t1 && ok; ++t, ++n) {
                     if (lane == 0) tl->qk_tile = (int)n;
                     const uint32_t buf = n & 1u;   // its S^T has been read: the tile was filled after the PV of n - 2
                     // (one half's MMAs as code: with both, what a query runs through no longer fits the instruction cache)
 #pragma unroll 1
                     for (int h = 0; h < kHalves; ++h) {
+                        if (t == run.t0 && !wait(&tl->q_full[h], (runs - 1) & 1u)) break;
                         if (!wait(&tl->full[buf][h], (n >> 1) & 1u)) break;
                         fence_proxy_async_smem();   // the rows were copied by the loading threads
                         if (elect_one()) {
@@ -462,10 +462,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                 if (NM % 2 == 0 || k < 8 || 2 * h + 1 < NM)   // (the last half of an odd NM is one d-block)
                                     umma_if(true, tmem + 64u * buf, at + (k >> 2) * (kTBlk / 16) + 2 * (k & 3), hi32(dk),
                                             bt + (k >> 2) * (kQBlk / 16) + 2 * (k & 3), hi32(dq), idesc, h + k);
-                            if (h == kHalves - 1) {
-                                umma_commit(&tl->s_full[buf]);
-                                if (t == run.t1 - 1) umma_commit(&tl->q_free);
-                            }
+                            if (t == run.t1 - 1) umma_commit(&tl->q_free[h]);
+                            if (h == kHalves - 1) umma_commit(&tl->s_full[buf]);
                         }
                         __syncwarp();
                     }
@@ -552,8 +550,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     mbar_arrive(&tl->run_full[k]);
                 }
                 if (nt == 0) break;
-                if (p.prev_out && lane == 0)   // what the run's end will read
-                    prefetch_l2_bulk(p.prev_out + (int64_t)run.row0 * p.d, (uint32_t)(run.heads * p.d) * 2u);
+                if (lane == 0) {   // what the run will read first and last
+                    const uint32_t bytes = (uint32_t)(run.heads * p.d) * 2u;
+                    prefetch_l2_bulk(p.q + (int64_t)run.row0 * p.d, bytes);
+                    if (p.prev_out) prefetch_l2_bulk(p.prev_out + (int64_t)run.row0 * p.d, bytes);
+                }
                 if (run.t0 == 0 && run.t1 < nt) rec = make_int2(q, piece_of(piece, at_tile + nt - 1));
                 at_tile += run.t1 - run.t0;
                 ++q;
@@ -596,14 +597,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (lane == 0) p.rec[blockIdx.x] = rec;
         } else {
             // -------------------------------------------------------------- Q
-            while (next_run(run)) {
-                if (runs > 1 && !warp_wait(&tl->q_free, runs & 1u, p.status, abort)) break;
-                // rows past the group's heads are other queries', or zeros past the last: columns of S^T that nothing uses
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(&tl->q_full, (uint32_t)n_cb * kQBlk);
-                    for (int cb = 0; cb < n_cb; ++cb) tma_load_2d(q_s + cb * kQBlk, &tm_q, &tl->q_full, 64 * cb, run.row0);
+            // Half by half: the first half's buffer is free, and its QK can begin, that much earlier (64 rows of 128 bytes per
+            // box, a Q takes some 3000 cycles to come).
+            while (ok && next_run(run)) {
+                for (int h = 0; h < kHalves && ok; ++h) {
+                    if (runs > 1 && !wait(&tl->q_free[h], runs & 1u)) break;
+                    // rows past the group's heads are other queries', or zeros past the last: columns of S^T that nothing uses
+                    if (elect_one()) {
+                        const int cb1 = min(n_cb, 4 * h + 4);
+                        mbar_arrive_expect_tx(&tl->q_full[h], (uint32_t)(cb1 - 4 * h) * kQBlk);
+                        for (int cb = 4 * h; cb < cb1; ++cb)
+                            tma_load_2d(q_s + cb * kQBlk, &tm_q, &tl->q_full[h], 64 * cb, run.row0);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
         }
         __syncwarp();
@@ -1015,7 +1022,9 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_fi
     int64_t rows = cap;              // of a group's list, at most
     if (window > 0 && (int64_t)window + l.pack - 1 + n_first < rows) rows = (int64_t)window + l.pack - 1 + n_first;
     const int64_t tiles = (rows + kRows - 1) / kRows, groups = (int64_t)B * l.groups;
-    l.whole = tiles <= kWholeTiles;
+    // Splitting costs a second kernel, some 12 us or eight tiles; not splitting at most a list's tiles on some CTAs while
+    // others wait, and with fewer groups than SMs, SMs without work.
+    l.whole = tiles <= kWholeTiles || (groups >= num_sms && tiles <= 4 * kWholeTiles);
     const int64_t list = l.whole ? groups : tiles * groups;
     l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);
     return l;

@@ -252,6 +252,7 @@ struct NormRopeParams {
 cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t stream);
 
 struct AttnPagedParams {
+    const uint16_t* q;          // bf16 [B, s, h, d]
     const uint16_t* pages;      // bf16 [n_pages, page_size, d], page stride in elements
     int64_t page_stride;
     const int32_t* table;       // [B, *], row stride in elements
