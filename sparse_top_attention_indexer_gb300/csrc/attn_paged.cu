@@ -988,6 +988,103 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
 }
 
+// Joins the parts of the queries that are split between CTAs, when those are few: block (c, y) takes the query whose first
+// part is CTA c's last, a warp one of its heads (8 y ...), a lane dims 4 lane + 128 j + {0..3}; U parts at a time add up in
+// order.  The first U parts are on their way before it is known whether there are any: all the kernel waits for
+// then comes at once.  (merge_kernel, with a block for each head that first looks its query up, took 26 us of the time of
+// 152 queries of two parts each.)
+template <int NM, int U>
+__global__ void __launch_bounds__(256) merge_few_kernel(const AttnPagedParams p) {
+    const int c = blockIdx.x, lane = threadIdx.x & 31, hh = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5);
+    const int hp = p.pack * p.h;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (hh >= hp) return;
+    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * min(c + i, p.grid - 1); };   // (the last CTA's again past the end)
+    const float* src = p.part_o + (int64_t)hh * p.d + 4 * lane;
+    float4 v[U][NM];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int j = 0; j < NM; ++j) {
+                v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (128 * j + 4 * lane < p.d)
+                    v[k][j] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)slot(i0 + k) * hp * p.d + 128 * j));
+            }
+    };
+    const int2 rec = __ldcg(p.rec + c);
+    float2 ml = __ldcg(p.part_ml + slot(lane) * 64 + hh);
+    load(0);
+    if (rec.x < 0) return;
+    const PagedGroup grp = group_of(p, rec.x);
+    if (hh >= grp.heads) return;
+    const int parts = rec.y - c + 1;
+    const int64_t at = grp.row0 + hh;
+    const float pl_in = p.prev_lse ? p.prev_lse[at] : -INFINITY, pl = pl_in * kLog2e;
+    // The largest reference, 32 parts at a time.  A part of which the head sees nothing has a sum of -0.
+    bool any = false;
+    float mx = -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+        if (i >= 32) ml = __ldcg(p.part_ml + slot(i) * 64 + hh);
+        any = any || !signbit(ml.y);
+        mx = fmaxf(mx, ml.x);
+    }
+    const bool seen = __any_sync(kWarpFull, any);
+    const float sk = p.sink && seen ? __ldg(p.sink + hh % p.h) * kLog2e : -INFINITY;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kWarpFull, mx, o));
+    mx = fmaxf(mx, fmaxf(sk, pl));
+    if (mx == -INFINITY) mx = 0.f;
+    float l = 0.f, f = 0.f;
+    float4 o[NM];
+#pragma unroll
+    for (int j = 0; j < NM; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0;;) {
+        if ((i0 & 31) == 0) {   // the factors of parts i0 .. i0 + 31, one per lane
+            if (parts > 32 && i0 + lane < parts) ml = __ldcg(p.part_ml + slot(i0 + lane) * 64 + hh);
+            f = i0 + lane >= parts || ml.y == 0.f ? 0.f : exp2f((ml.x == -INFINITY ? 0.f : ml.x) - mx);   // (inf * 0)
+            l += i0 + lane < parts ? ml.y * f : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float w = __shfl_sync(kWarpFull, f, (i0 + k) & 31);
+            if (w != 0.f) {
+#pragma unroll
+                for (int j = 0; j < NM; ++j) {
+                    o[j].x += w * v[k][j].x;
+                    o[j].y += w * v[k][j].y;
+                    o[j].z += w * v[k][j].z;
+                    o[j].w += w * v[k][j].w;
+                }
+            }
+        }
+        i0 += U;
+        if (i0 >= parts) break;
+        load(i0);
+    }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) l += __shfl_xor_sync(kWarpFull, l, s);
+    const float ep = exp2f(pl - mx), den = l + exp2f(sk - mx) + ep;
+    // a query that sees no row keeps what it had
+    const float inv = seen ? 1.f / den : 0.f, wp = seen ? ep / den : pl == -INFINITY ? 0.f : 1.f;
+    if (p.lse && lane == 0) p.lse[at] = seen ? (mx + log2f(den)) * kLn2 : pl_in;
+#pragma unroll
+    for (int j = 0; j < NM; ++j) {
+        if (128 * j + 4 * lane >= p.d) continue;
+        const int64_t to = at * p.d + 128 * j + 4 * lane;
+        float4 x = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
+        if (wp != 0.f && p.prev_out) {
+            const uint2 pv = *reinterpret_cast<const uint2*>(p.prev_out + to);
+            x.x += wp * __uint_as_float(pv.x << 16);
+            x.y += wp * __uint_as_float(pv.x & 0xFFFF0000u);
+            x.z += wp * __uint_as_float(pv.y << 16);
+            x.w += wp * __uint_as_float(pv.y & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint2*>(p.out + to) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
+}
+
 template <int NM>
 cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStream_t stream) {
     const int nq = p.B * p.groups;
@@ -1007,9 +1104,11 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
     if (e != cudaSuccess || p.whole) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
     const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
+    const dim3 few((unsigned)p.grid, (mh + 7) / 8);
     return parts > 16  ? launch_after(merge_kernel<16, 32, AttnPagedParams>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
-           : parts > 4 ? launch_after(merge_kernel<2, 128, AttnPagedParams>, dim3(mx, mh), 256, 0, stream, p)
-                       : launch_after(merge_kernel<1, 128, AttnPagedParams>, dim3(mx, mh), 128, 0, stream, p);
+           : parts > 8 ? launch_after(merge_kernel<2, 128, AttnPagedParams>, dim3(mx, mh), 256, 0, stream, p)
+           : parts > 4 ? launch_after(merge_few_kernel<NM, 4>, few, 256, 0, stream, p)
+                       : launch_after(merge_few_kernel<NM, 2>, few, 256, 0, stream, p);
 }
 
 }  // namespace
