@@ -236,13 +236,12 @@ __device__ __forceinline__ void load_prev(uint4 (&pre)[2], const uint16_t* at, i
 }
 
 // O^T of a warp's 32 heads (TMEM columns at `to`) x 32 dims of a d-block, times the heads' factors in fac (of O, of prev), as
-// bf16 to out (JOINS: with what prev holds at the same place; pre: its first pieces, then the next block's if there is
-// one).  Half the heads at a time: a lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 (l % 4) + {0, 1}; the 8 x 8 blocks
+// bf16 to out (kJoins: with prev at the same place; pre: its first pieces, then the next block's if there is one).  Half the heads at a time: a lane has dims l / 4 + 8 i (i < 4) of heads 8 g + 2 (l % 4) + {0, 1}; the 8 x 8 blocks
 // are turned over on their way to [16 heads][32 dims] in shared memory at stg, where prev comes from the same way, in
 // pieces of 8 dims, two per lane: piece k is head lane / 4 + 8 k, dims 8 (lane % 4) ...  A head's four pieces lie
 // turned by (head / 2) % 4, so that neither side meets a bank twice.  out, prev: the lane's first piece; there: heads from
 // that one on.  (Turned over in fp32 with scalar stores, a query's outputs took twice as long.)
-template <bool JOINS>
+template <bool kJoins>
 __device__ __forceinline__ void write_block(const float2* fac, uint8_t* stg, uint32_t to, uint16_t* out, const uint16_t* prev,
                                             uint4 (&pre)[2], int there, int d, bool another) {
     const int lane = threadIdx.x & 31, l4 = lane & 3, j8 = lane & 7;
@@ -255,7 +254,7 @@ __device__ __forceinline__ void write_block(const float2* fac, uint8_t* stg, uin
         tmem_ld_rows16_half(to + (uint32_t)h + (16u << 16), r[1]);
         const float4 f[2] = {*reinterpret_cast<const float4*>(fac + h + 2 * l4),
                              *reinterpret_cast<const float4*>(fac + h + 8 + 2 * l4)};   // (of O, of prev) of two heads
-        if (JOINS) {
+        if (kJoins) {
             mine[0] = pre[0];
             mine[32] = pre[1];
             __syncwarp();
@@ -266,12 +265,12 @@ __device__ __forceinline__ void write_block(const float2* fac, uint8_t* stg, uin
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
             uint32_t w[4], pw[4];
-            if (JOINS) load_turned(block + 512u * (uint32_t)g, pw);
+            if (kJoins) load_turned(block + 512u * (uint32_t)g, pw);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x0 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1)]) * f[g].x;
                 float x1 = __uint_as_float(r[i >> 1][4 * g + 2 * (i & 1) + 1]) * f[g].z;
-                if (JOINS) {   // weight 0: prev is not used
+                if (kJoins) {   // weight 0: prev is not used
                     x0 = f[g].y != 0.f ? x0 + f[g].y * __uint_as_float(pw[i] << 16) : x0;
                     x1 = f[g].w != 0.f ? x1 + f[g].w * __uint_as_float(pw[i] & 0xFFFF0000u) : x1;
                 }
@@ -369,7 +368,7 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
     }
 }
 
-template <int NM, bool kPack>   // d-blocks of 128 dims; groups of several queries
+template <int NM, bool kPack, bool kJoins>   // d-blocks of 128 dims; groups of several queries; prev_out to be joined
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnPagedParams p) {
     constexpr int kHalves = (NM + 1) / 2;
@@ -410,7 +409,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_alloc(&tl->tmem_base, kTmem);
         tmem_relinquish();
     }
-    plan_piece(p, nq, tl);
+    // (a group for each CTA: nothing to plan)
+    const bool single = p.whole && nq <= (int)gridDim.x;
+    if (!single) plan_piece(p, nq, tl);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -511,7 +512,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // The rows of the next kAhead tiles are on their way to L2 when a tile is loaded, asked for by a
             // sequence's first query only: the others find them there.
             volatile int* now = &tl->qk_tile;
-            const Piece piece = tl->piece;
+            Piece piece = tl->piece;
+            if (single) {
+                piece.lo = 0;
+                piece.hi = 1;
+                piece.q = blockIdx.x;
+                piece.off = 0;
+            }
             long long at_tile = piece.lo;
             int q = piece.q, off = piece.off;
             int2 rec = make_int2(-1, 0);
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     run.lo = rows.lo;
                     nt = (rows.n + kRows - 1) / kRows;
                     if (nt > 0 && !(p.whole && off > 0)) break;
-                    at_tile += nt - off;
+                    at_tile += single ? 1 : nt - off;
                     nt = 0;
                 }
                 const uint32_t k = runs % kRuns;
@@ -705,18 +712,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
             } else if (set < sets) {
                 const int64_t first = (int64_t)(run.row0 + 32 * set + (lane >> 2)) * p.d + 32 * qd + 8 * (lane & 3);
                 const int there = run.heads - 32 * set - (lane >> 2);
-                const float2* fac = &tl->fac[k][32 * set];
-                uint16_t* out = p.out + first;
-                const uint16_t* prev = p.prev_out ? p.prev_out + first : nullptr;
+                const uint16_t* prev = (kJoins ? p.prev_out : p.out) + first;
                 uint4 pre[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};   // prev of the next step
-                if (prev) load_prev(pre, prev, 0, there, p.d);
+                if (kJoins) load_prev(pre, prev, 0, there, p.d);
 #pragma unroll 1
                 for (int m = 0; m < NM; ++m) {
                     if (m == 2) read(0);
                     const int left = p.d - 128 * m - 32 * qd;
                     if (left <= 0) break;
-                    if (prev) write_block<true>(fac, o_s + lw * kStage, lanes + o_block(r, (uint32_t)m), out + 128 * m, prev + 128 * m, pre, there, p.d, left > 128);
-                    else write_block<false>(fac, o_s + lw * kStage, lanes + o_block(r, (uint32_t)m), out + 128 * m, out, pre, there, p.d, false);
+                    write_block<kJoins>(&tl->fac[k][32 * set], o_s + lw * kStage, lanes + o_block(r, (uint32_t)m), p.out + first + 128 * m,
+                                prev + 128 * m, pre, there, p.d, left > 128);
                 }
             } else if (NM > 2) {
                 read(0);
@@ -1089,16 +1094,20 @@ template <int NM>
 cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStream_t stream) {
     const int nq = p.B * p.groups;
     const size_t smem = attn_paged_smem(p.d);
-    auto* kernel = p.pack > 1 ? attn_paged_kernel<NM, true> : attn_paged_kernel<NM, false>;
+    const int kind = 2 * (p.pack > 1) + (p.prev_out != nullptr);
+    auto* kernel = kind == 3   ? attn_paged_kernel<NM, true, true>
+                   : kind == 2 ? attn_paged_kernel<NM, true, false>
+                   : kind == 1 ? attn_paged_kernel<NM, false, true>
+                               : attn_paged_kernel<NM, false, false>;
     // The kernel's shared-memory limit, once per device (it follows from NM alone, so no other call asks for another).
-    static std::atomic<uint64_t> set[2];
+    static std::atomic<uint64_t> set[4];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(set[p.pack > 1].load(std::memory_order_acquire) & bit)) {
+    if (!(set[kind].load(std::memory_order_acquire) & bit)) {
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-        set[p.pack > 1].fetch_or(bit, std::memory_order_release);
+        set[kind].fetch_or(bit, std::memory_order_release);
     }
     e = launch_after(kernel, dim3((unsigned)p.grid), kPThreads, smem, stream, tm_q, p);
     if (e != cudaSuccess || p.whole) return e;
