@@ -44,17 +44,36 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turns) {
     return make_float2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
 }
 
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+// Two fp32 at a time, in one instruction each.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+    return v;
+}
+__device__ __forceinline__ float2 parts2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
 }
 
-// LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time
-template <int LPR, int CH, int U>
+__device__ __forceinline__ void unpack(const uint4& v, uint64_t (&f)[4]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+// LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time; pairs (i, i + rd / 2)
+template <int LPR, int CH, int U, bool kHalves>
 __global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 3 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
     constexpr int kSlots = kRowThreads / LPR;
     extern __shared__ float2 cs[];                      // [tokens][rd / 2], then the tokens' places
@@ -128,11 +147,12 @@ __global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 3 : 2) norm_rope_kernel
             cs[i * pairs + pr] = make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
         }
     }
-    uint4 weight[CH];
+    uint64_t weight[CH][4];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-        weight[k] = make_uint4(0, 0, 0, 0);
-        if (p.weight && li + LPR * k < chunks) weight[k] = __ldg(reinterpret_cast<const uint4*>(p.weight) + li + LPR * k);
+        uint4 w = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // ones
+        if (p.weight && li + LPR * k < chunks) w = __ldg(reinterpret_cast<const uint4*>(p.weight) + li + LPR * k);
+        unpack(w, weight[k]);
     }
     __syncthreads();
     const int c_lo = p.off / 8, c_hi = (p.off + p.rd) / 8, half = p.rd / 16;
@@ -140,24 +160,27 @@ __global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 3 : 2) norm_rope_kernel
 #pragma unroll
         for (int r = 0; r < U; ++r) {
             // the pairs' other halves, before anything of the row is written
-            uint4 other[CH];
-#pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int c = li + LPR * k;
-                other[k] = make_uint4(0, 0, 0, 0);
-                if (p.halves && src[r] && c >= c_lo && c < c_hi)
-                    other[k] = *reinterpret_cast<const uint4*>(src[r] + 8 * (c < c_lo + half ? c + half : c - half));
-            }
-            float scale = 1.f;
-            if (p.norm) {
-                float sum = 0.f;
+            uint4 other[kHalves ? CH : 1];
+            if (kHalves) {
 #pragma unroll
                 for (int k = 0; k < CH; ++k) {
-                    float f[8];
-                    unpack(v[r][k], f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(f[j], f[j], sum);
+                    const int c = li + LPR * k;
+                    other[k] = make_uint4(0, 0, 0, 0);
+                    if (src[r] && c >= c_lo && c < c_hi)
+                        other[k] = *reinterpret_cast<const uint4*>(src[r] + 8 * (c < c_lo + half ? c + half : c - half));
                 }
+            }
+            uint64_t f[CH][4];
+#pragma unroll
+            for (int k = 0; k < CH; ++k) unpack(v[r][k], f[k]);
+            float scale = 1.f;
+            if (p.norm) {
+                uint64_t sq = 0;
+#pragma unroll
+                for (int k = 0; k < CH; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) sq = fma2(f[k][j], f[k][j], sq);
+                float sum = parts2(sq).x + parts2(sq).y;
 #pragma unroll
                 for (int o = LPR / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
                 scale = rsqrtf(sum * p.inv_d + p.eps);
@@ -168,49 +191,39 @@ __global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 3 : 2) norm_rope_kernel
             if (to[tk[r]] < 0) continue;
             dst += to[tk[r]] + (int64_t)(head0 + i0 + r * kSlots - tk[r] * sh.heads) * p.d;
             const float2* my = cs + tk[r] * pairs;
+            const uint64_t scale2 = pack2(scale, scale);
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 const int c = li + LPR * k;
                 if (c >= chunks) continue;
-                float f[8];
-                unpack(v[r][k], f);
+                float2 x[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] *= scale;
-                if (p.weight) {
-                    float w[8];
-                    unpack(weight[k], w);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] *= w[j];
-                }
+                for (int j = 0; j < 4; ++j) x[j] = parts2(mul2(mul2(f[k][j], scale2), weight[k][j]));
                 if (c >= c_lo && c < c_hi) {
-                    if (p.halves) {
+                    if (kHalves) {
                         const bool low = c < c_lo + half;
                         const int oc = low ? c + half : c - half;
-                        float g[8];
+                        uint64_t g[4], w[4];
                         unpack(other[k], g);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) g[j] *= scale;
-                        if (p.weight) {
-                            float w[8];
-                            unpack(__ldg(reinterpret_cast<const uint4*>(p.weight) + oc), w);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) g[j] *= w[j];
-                        }
+                        unpack(p.weight ? __ldg(reinterpret_cast<const uint4*>(p.weight) + oc)
+                                        : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), w);
                         const float2* a = my + 8 * ((low ? c : oc) - c_lo);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) f[j] = low ? f[j] * a[j].x - g[j] * a[j].y : f[j] * a[j].x + g[j] * a[j].y;
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 z = parts2(mul2(mul2(g[j], scale2), w[j])), a0 = a[2 * j], a1 = a[2 * j + 1];
+                            x[j].x = x[j].x * a0.x + (low ? -z.x : z.x) * a0.y;
+                            x[j].y = x[j].y * a1.x + (low ? -z.y : z.y) * a1.y;
+                        }
                     } else {
                         const float2* a = my + 4 * (c - c_lo);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float x = f[2 * j], z = f[2 * j + 1];
-                            f[2 * j] = x * a[j].x - z * a[j].y;
-                            f[2 * j + 1] = z * a[j].x + x * a[j].y;
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = make_float2(x[j].x * a[j].x - x[j].y * a[j].y, x[j].y * a[j].x + x[j].x * a[j].y);
                     }
                 }
                 *reinterpret_cast<uint4*>(dst + 8 * c) =
-                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                    make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                               pack_bf16x2(x[3].x, x[3].y));
             }
         }
         i0 += U * kSlots;
@@ -236,7 +249,7 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     sh.lanes = 0;
     while (1 << sh.lanes < p.rd / 2 && 1 << sh.lanes < kRowThreads) ++sh.lanes;
     const size_t smem = (size_t)sh.tokens * ((p.rd / 2) * sizeof(float2) + 2 * sizeof(int64_t) + sizeof(int));
-    return launch_after(norm_rope_kernel<LPR, CH, U>, dim3((unsigned)(up(tokens, sh.tokens) * sh.blocks_h)), kRowThreads, smem,
+    return launch_after(p.halves ? norm_rope_kernel<LPR, CH, U, true> : norm_rope_kernel<LPR, CH, U, false>, dim3((unsigned)(up(tokens, sh.tokens) * sh.blocks_h)), kRowThreads, smem,
                         stream, p, sh);
 }
 
