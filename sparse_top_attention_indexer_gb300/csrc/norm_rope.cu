@@ -74,7 +74,7 @@ __device__ __forceinline__ void unpack(const uint4& v, uint64_t (&f)[4]) {
 
 // LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time; pairs (i, i + rd / 2)
 template <int LPR, int CH, int U, bool kHalves>
-__global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 3 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
     constexpr int kSlots = kRowThreads / LPR;
     extern __shared__ float2 cs[];                      // [tokens][rd / 2], then the tokens' places
     const int slot = threadIdx.x / LPR, li = threadIdx.x % LPR;
@@ -257,10 +257,10 @@ cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     const int chunks = p.d / 8;
-    if (chunks <= 4) return launch<4, 1, 4>(p, num_sms, stream);
-    if (chunks <= 8) return launch<8, 1, 4>(p, num_sms, stream);
-    if (chunks <= 16) return launch<16, 1, 4>(p, num_sms, stream);
-    if (chunks <= 32) return launch<32, 1, 4>(p, num_sms, stream);
+    if (chunks <= 4) return launch<4, 1, 2>(p, num_sms, stream);
+    if (chunks <= 8) return launch<8, 1, 2>(p, num_sms, stream);
+    if (chunks <= 16) return launch<16, 1, 2>(p, num_sms, stream);
+    if (chunks <= 32) return launch<32, 1, 2>(p, num_sms, stream);
     if (chunks <= 64) return launch<32, 2, 2>(p, num_sms, stream);
     return launch<32, 4, 1>(p, num_sms, stream);
 }
