@@ -1238,7 +1238,7 @@ struct AttnPagedLayout {
 };
 static AttnPagedLayout attn_paged_layout(int b, int seqlen, int h, int d) {
     AttnPagedLayout l;
-    const sti::AttnPagedPlan pl = sti::attn_paged_plan(b, seqlen, h, kMaxCacheRows, 0, 0, kAttnFp4MaxSms);
+    const sti::AttnPagedPlan pl = sti::attn_paged_plan(b, seqlen, h, d, kMaxCacheRows, 0, 0, kAttnFp4MaxSms);
     l.rec = sti::kWsStatusBytes;
     l.ml = sti::align_up(l.rec + (size_t)pl.grid * sizeof(int2), sti::kWsAlign);
     l.o = sti::align_up(l.ml + (size_t)2 * pl.grid * 64 * sizeof(float2), sti::kWsAlign);
@@ -1304,11 +1304,12 @@ sti_status sti_attn_paged(const uint16_t* q, const uint16_t* pages, int64_t page
     p.part_o = reinterpret_cast<float*>(wsb + l.o);
     const int sms = sti::device_num_sms();
     const sti::AttnPagedPlan pl =
-        sti::attn_paged_plan(b, seqlen, h, p.cap, window, n_first, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms);
+        sti::attn_paged_plan(b, seqlen, h, d, p.cap, window, n_first, sms < kAttnFp4MaxSms ? sms : kAttnFp4MaxSms);
     p.pack = pl.pack;
     p.groups = pl.groups;
     p.grid = pl.grid;
     p.whole = pl.whole;
+    p.least = pl.least;
     CUtensorMap tm_q;
     const sti_status st = make_map_2d(&tm_q, q, (uint64_t)d, (uint64_t)b * seqlen * h, (uint64_t)d * 2, 64, 64);
     if (st != STI_OK) return st;

@@ -9,17 +9,25 @@
 // The rows that a group's queries see together form its list: the first min(n_first, lo) positions, then lo .. hi (lo:
 // the first query's window).  Lists are cut into tiles of 64 rows wherever those lie, so a page may end anywhere in
 // a tile and a window of 128 rows is two tiles at any position.  The groups' tiles form one long list that is cut into equal
-// contiguous pieces, one per CTA and SM (sti_attn_tiles.cuh); what a CTA has of a query that others share leaves as an
-// fp32 partial, which merge_kernel joins.  Two tile buffers; 20 warps:
-//   * warps 8..15 copy the rows to the free buffer (16 bytes per thread and copy, past L1 and the registers) as the PV two
-//     tiles earlier releases its halves.  Rows that nothing sees are not read but zeros, so that P = 0 meets no NaN.  They
-//     also write the outputs, while the softmax of the next query's first tiles runs;
-//   * warp 19 loads Q by TMA as soon as the last QK of the query before has read the buffer;
-//   * warp 16 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 17 the PVs, O^T += V^T . P^T (M = 128 dims
-//     per block, K = the rows of the tile, the same tile read as an MN-major operand);
-//   * warp 18 walks the list, tells the others what comes next and asks for the rows of the next tiles, into L2;
+// contiguous pieces, one per CTA and SM; what a CTA has of a query that others share leaves as an fp32 partial, which a
+// second kernel joins (short lists are not cut).  Two tile buffers; 24 warps:
 //   * warps 0..7 run the online softmax (two sets of 32 heads; what P is relative to moves only when a score passes it
-//     by 2^8).
+//     by 2^8);
+//   * warps 8..15 write the outputs, while the next query's tiles are under way: O^T lies in a ring of TMEM blocks;
+//   * warps 16..19 copy the rows to the free buffer (16 bytes per thread and copy, past L1 and the registers) as the PV two
+//     tiles earlier releases its halves.  Rows that nothing sees are not read but zeros, so that P = 0 meets no NaN;
+//   * warp 20 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 21 the PVs, O^T += V^T . P^T (M = 128 dims
+//     per block, K = the rows of the tile, the same tile read as an MN-major operand);
+//   * warp 22 walks the list, tells the others what comes next and asks for the rows of the next tiles, into L2;
+//   * warp 23 loads Q by TMA as soon as the last QK of the query before has read the buffer.
+//
+// A long chunk is bound by shared memory: of a tile at 128 B a cycle, QK 1024 cycles, PV 768, the rows' copies 512 and
+// P^T and scores 100, together 2400 of the 2750 that a tile takes (the MMAs alone would take 2100: at N = 64 an M = 128 step
+// costs what one at N = 128 does).  2048 queries of 64 heads x 512 at 6144: 2100 us, 0.48 of the measured bf16 peak.  Decoding
+// is bound by HBM: 32 queries over 16384 rows 124 us, of which the rows alone take 81 at the measured copy rate and
+// the join 12.  Windows are bound by one query's chain: its Q has to come, the QK of its first tile, the softmax, the
+// PV that frees the third tile's buffer; 4096 queries through a window of 128 rows and 4 first ones 182 us, 81 at the
+// copy rate.  The code that a query runs through has to stay in the instruction cache: 10 % more of it cost 5 to 9 %.
 //
 // P is rounded to bf16 for the PV product, as the rows are bf16 and one MMA takes one type: each row's share of the output
 // is off by at most 2^-8 of itself, as much as the output's own rounding.  Its sum is taken before, in fp32.
@@ -341,7 +349,8 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
         total += u;
     }
     const long long first = before + inc - sum;
-    const int part = (int)blockIdx.x, ctas = total < (long long)gridDim.x ? (int)total : (int)gridDim.x;
+    const long long pieces = p.whole ? total : (total + p.least - 1) / p.least;
+    const int part = (int)blockIdx.x, ctas = pieces < (long long)gridDim.x ? (int)pieces : (int)gridDim.x;
     long long lo = 0, hi = 0;
     if (part < ctas) {
         const long long per = divide(total, ctas), longer = total - per * ctas;
@@ -1122,7 +1131,7 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
 
 }  // namespace
 
-AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_first, int num_sms) {
+AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, int n_first, int num_sms) {
     AttnPagedPlan l;
     l.pack = h <= 32 ? 64 / h : 1;   // as attn_fp4_plan
     if (l.pack > s) l.pack = s;
@@ -1133,7 +1142,12 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_fi
     // Splitting costs a second kernel, some 12 us or eight tiles; not splitting at most a list's tiles on some CTAs while
     // others wait, and with fewer groups than SMs, SMs without work.
     l.whole = tiles <= kWholeTiles || (groups >= num_sms && tiles <= 4 * kWholeTiles);
-    const int64_t list = l.whole ? groups : tiles * groups;
+    // Pieces of at least four tiles, when the parts of a few queries otherwise take longer to write and join than the tiles
+    // (4 queries of 64 heads x 512 over 2000 rows 28 -> 21 us, 32 over 1000 rows 33 -> 27, 8 groups of 4 x 16 heads x 256 over
+    // 3000 rows 30 -> 23); not for one or two queries (one over 4000 rows 18 -> 21) nor for short rows of several
+    // queries (12 groups of 3 x 20 heads x 128 over 1000 rows 16 -> 18.5).
+    l.least = groups >= 3 && (l.pack == 1 || d > 128) ? 4 : 1;
+    const int64_t list = l.whole ? groups : (tiles * groups + l.least - 1) / l.least;
     l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);
     return l;
 }

@@ -276,12 +276,14 @@ struct AttnPagedParams {
     float2* part_ml;
     int pack, groups;
     bool whole;                 // no query is split between CTAs
+    int least;                  // otherwise: tiles of a piece, at least
 };
 struct AttnPagedPlan {
     int pack, groups, grid;     // as in AttnPagedParams
     bool whole;
+    int least;
 };
-AttnPagedPlan attn_paged_plan(int B, int s, int h, int cap, int window, int n_first, int num_sms);
+AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, int n_first, int num_sms);
 // tm_q: q as [B*s*h, d], box 64 x 64
 cudaError_t launch_attn_paged(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStream_t stream);
 

@@ -323,6 +323,16 @@ ATTEND = {
     "packed_causal": (2, 300, 16, 128, 64, [0, 7], None, 0, 0, True, False),
     "packed_one_head": (3, 130, 1, 64, 64, [0, 5, 1], None, 0, 0, True, True),
     "packed_split": (1, 5, 12, 448, 64, [4990], None, 0, 0, True, True),
+    # several queries per SM, each of a tile or two, for every number of 128-dim blocks
+    "runs_d64": (2, 300, 64, 64, 16, [0, 90], None, 20, 0, True, False),
+    "runs_d128_prev": (3, 250, 33, 128, 16, [5, 40, 0], [250, 0, 249], 64, 0, True, True),
+    "runs_d256": (2, 400, 64, 256, 64, [70, 1], None, 60, 3, True, True),
+    "runs_d384": (2, 350, 64, 384, 24, [300, 0], None, 100, 1, True, False),
+    "runs_d448": (2, 300, 64, 448, 64, [64, 0], None, 1, 0, True, True),
+    "runs_d512_prev": (2, 300, 64, 512, 64, [64, 0], None, 40, 2, False, True),
+    "whole_16_tiles": (2, 90, 64, 192, 64, [900, 500], None, 940, 60, True, False),
+    "pieces_of_4": (5, 1, 64, 320, 64, [1999, 0, 700, 64, 1300], None, 0, 0, True, True),
+    "packed_runs_d320": (2, 700, 20, 320, 64, [0, 50], [700, 650], 33, 5, True, True),
     "packed_pairs_d448": (2, 5, 32, 448, 64, [380, 100], None, 0, 0, True, True),
 }
 
