@@ -1242,7 +1242,7 @@ static AttnPagedLayout attn_paged_layout(int b, int seqlen, int h, int d) {
     l.rec = sti::kWsStatusBytes;
     l.ml = sti::align_up(l.rec + (size_t)pl.grid * sizeof(int2), sti::kWsAlign);
     l.o = sti::align_up(l.ml + (size_t)2 * pl.grid * 64 * sizeof(float2), sti::kWsAlign);
-    l.end = sti::align_up(l.o + (size_t)2 * pl.grid * pl.pack * h * d * sizeof(float), sti::kWsAlign);
+    l.end = sti::align_up(l.o + (size_t)2 * pl.grid * ((pl.pack * h + 3) / 4 * 4) * d * sizeof(float), sti::kWsAlign);
     return l;
 }
 
@@ -1310,6 +1310,7 @@ sti_status sti_attn_paged(const uint16_t* q, const uint16_t* pages, int64_t page
     p.grid = pl.grid;
     p.whole = pl.whole;
     p.least = pl.least;
+    p.by_query = pl.by_query;
     CUtensorMap tm_q;
     const sti_status st = make_map_2d(&tm_q, q, (uint64_t)d, (uint64_t)b * seqlen * h, (uint64_t)d * 2, 64, 64);
     if (st != STI_OK) return st;

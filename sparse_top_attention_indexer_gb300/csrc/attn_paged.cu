@@ -39,6 +39,7 @@
 #include "sti_internal.h"
 
 namespace sti {
+namespace {
 
 // ------------------------------------------------------------------ queries and the rows they see
 
@@ -79,9 +80,6 @@ __device__ __forceinline__ PagedRows rows_of(const AttnPagedParams& p, int b, in
     return r;
 }
 __device__ __forceinline__ int group_rows(const AttnPagedParams& p, int b, int u) { return rows_of(p, b, u).n; }
-__device__ __forceinline__ bool head_seen(const AttnPagedParams&, const PagedGroup&, int, bool any) { return any; }
-
-namespace {
 
 constexpr int kWarps = 24;                     // 8 softmax, 8 output, 4 loading, 4 others
 constexpr int kPThreads = 32 * kWarps;
@@ -94,7 +92,7 @@ constexpr uint32_t kStage = 1024;              // 16 heads x 32 dims of bf16
 constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are never split between CTAs
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
-// A run of one group's tiles, as warp 18 publishes it.
+// A run of one group's tiles, as the list's warp publishes it.
 struct __align__(16) Run {
     int t0, t1;         // tiles t0 .. t1 - 1 of the group's list; t1 = 0: the CTA has no more
     int n, nf;          // rows of the list, and those of them before the window
@@ -409,7 +407,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tl->abort = 0;
         tl->qk_tile = 0;
     }
-    if (n_cb & 1) zero_padding(64, n_cb, NM, q_s, t_s);   // (Q's rows all come by TMA)
+    if (n_cb & 1)   // the dims past d of the last d-block, which no copy writes
+        for (int i = tid; i < 3 * (int)kTBlk / 16; i += kPThreads) {
+            const int part = i / (int)(kTBlk / 16), k = i % (int)(kTBlk / 16);   // Q, the tiles (kQBlk = kTBlk)
+            reinterpret_cast<uint4*>(q_s + (size_t)(2 * NM * part + n_cb) * kTBlk)[k] = make_uint4(0, 0, 0, 0);
+        }
     fence_proxy_async_smem();
     // From here on what earlier kernels wrote is read.  (TMEM after it too: a CTA that held it while it waits could keep it from
     // one of the kernel it waits for.)
@@ -571,7 +573,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     prefetch_l2_bulk(p.q + (int64_t)run.row0 * p.d, bytes);
                     if (p.prev_out) prefetch_l2_bulk(p.prev_out + (int64_t)run.row0 * p.d, bytes);
                 }
-                if (run.t0 == 0 && run.t1 < nt) rec = make_int2(q, piece_of(piece, at_tile + nt - 1));
+                if (run.t0 == 0) {
+                    const int last = run.t1 < nt ? piece_of(piece, at_tile + nt - 1) : -1;
+                    if (p.by_query && lane == 0) p.rec[q] = make_int2(last < 0 ? -1 : (int)blockIdx.x, last);
+                    if (last >= 0) rec = make_int2(q, last);
+                }
                 at_tile += run.t1 - run.t0;
                 ++q;
                 off = 0;
@@ -610,7 +616,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     if (!ok) break;
                 }
             }
-            if (lane == 0) p.rec[blockIdx.x] = rec;
+            if (lane == 0 && !p.by_query) p.rec[blockIdx.x] = rec;
         } else {
             // -------------------------------------------------------------- Q
             // Half by half: the first half's buffer is free, and its QK can begin, that much earlier (64 rows of 128 bytes per
@@ -704,19 +710,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tl->o_free[half][k]);
             };
-            if (set < sets && run.slot >= 0) {   // a partial, [head][dim] in fp32: lanes hold dims
-                float* po = p.part_o + ((int64_t)run.slot * hp + 32 * set) * p.d + 32 * qd + lane;
+            if (set < sets && run.slot >= 0) {
+                // A partial, fp32 [32 dims][4 heads][dim, head]: a lane has a dim, and writes four heads' at a time (128 KB
+                // in 2 us; as [head][dim] with 4 bytes per lane and store 5 us).
+                const int quads = (hp + 3) / 4;
+                float4* po = reinterpret_cast<float4*>(p.part_o) + (int64_t)run.slot * p.d * quads + lane;
 #pragma unroll 1
                 for (int i = 0; i < 2 * NM; ++i) {
                     if (i == 4) read(0);
-                    if (128 * (i >> 1) + 32 * qd >= p.d) break;
+                    const int block = 4 * (i >> 1) + qd, quad = 8 * set + 4 * (i & 1);
+                    if (32 * block >= p.d) break;
                     uint32_t v[16];
                     tmem_ld16(lanes + o_block(r, (uint32_t)i >> 1) + 16u * (i & 1), v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (32 * set + 16 * (i & 1) + j < hp)
-                            po[(int64_t)(16 * (i & 1) + j) * p.d + 128 * (i >> 1)] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 4; ++j)
+                        if (quad + j < quads)
+                            po[(block * quads + quad + j) * 32] =
+                                make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                            __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
                 }
             } else if (set < sets) {
                 const int64_t first = (int64_t)(run.row0 + 32 * set + (lane >> 2)) * p.d + 32 * qd + 8 * (lane & 3);
@@ -973,7 +985,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (tid == 0 && grp.heads > 0 && p.status &&
                 (uint32_t)__ldg(p.start_pos + grp.b) + (uint32_t)(grp.t0 + grp.heads / p.h) > (uint32_t)p.cap)
                 atomicOr(p.status, 1u /* STI_FLAG_INDEX_RANGE */);
-            if (grp.heads == 0 || group_rows(p, grp.b, q - grp.b * p.groups) > 0) continue;
+            if (group_rows(p, grp.b, q - grp.b * p.groups) > 0) continue;
+            if (tid == 0 && p.by_query) p.rec[q] = make_int2(-1, 0);
             for (int i = tid; i < grp.heads; i += 256)
                 if (p.lse) p.lse[grp.row0 + i] = p.prev_lse ? p.prev_lse[grp.row0 + i] : -INFINITY;
             const int chunks = p.d / 8;
@@ -1002,101 +1015,240 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
 }
 
-// Joins the parts of the queries that are split between CTAs, when those are few: block (c, y) takes the query whose first
-// part is CTA c's last, a warp one of its heads (8 y ...), a lane dims 4 lane + 128 j + {0..3}; U parts at a time add up in
-// order.  The first U parts are on their way before it is known whether there are any: all the kernel waits for
-// then comes at once.  (merge_kernel, with a block for each head that first looks its query up, took 26 us of the time of
-// 152 queries of two parts each.)
-template <int NM, int U>
+// ------------------------------------------------------------------ joining split queries
+
+// What a warp of the joining kernels has: four heads (lane l looks after head l % 4 of them) x 32 Q dims of a query, a lane
+// dims lane + 32 j.  (Going through the code once before the wait, with nothing read or written, so that it is in the
+// instruction cache: 118 -> 120 us for 32 queries over 16384 rows, since not all blocks are there that early.)
+struct Quad {
+    float mx, l, sink, prev_lse;   // of the lane's head: largest reference, sum relative to it; -inf: none
+    bool seen;                     // it sees a row
+};
+__device__ __forceinline__ float over_parts_max(float v) {
+#pragma unroll
+    for (int o = 16; o >= 4; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kWarpFull, v, o));
+    return v;
+}
+// The largest reference becomes that of the sink and prev_lse too.
+__device__ __forceinline__ void quad_top(Quad& q, bool any) {
+    q.seen = (__ballot_sync(kWarpFull, any) >> (threadIdx.x & 3) & 0x11111111u) != 0;
+    if (!q.seen) q.sink = -INFINITY;
+    q.mx = fmaxf(over_parts_max(q.mx), fmaxf(q.sink, q.prev_lse * kLog2e));
+    if (q.mx == -INFINITY) q.mx = 0.f;
+}
+// This block's record, {-1, 0} if there is none: also where the attention gave up a wait and left anything (first: below n).
+__device__ __forceinline__ int2 split_of(const AttnPagedParams& p, int n) {
+    const int2 rec = __ldcg(p.rec + blockIdx.x);
+    const int c = p.by_query ? rec.x : (int)blockIdx.x;
+    return rec.x >= 0 && rec.x < n && rec.y > c && rec.y < p.grid ? rec : make_int2(-1, 0);
+}
+// The factor of a part.  One of which the head sees nothing has a sum of -0 (and O = 0: not inf * 0).
+__device__ __forceinline__ float part_factor(const float2& ml, float mx) {
+    return ml.y == 0.f ? 0.f : exp2f((ml.x == -INFINITY ? 0.f : ml.x) - mx);
+}
+__device__ __forceinline__ void add4(float4& o, const float4& w, const float4& v) {
+    o.x += w.x * v.x;
+    o.y += w.y * v.y;
+    o.z += w.z * v.z;
+    o.w += w.w * v.w;
+}
+// prev_out of the warp's heads and dims, from its first on.
+template <int Q>
+__device__ __forceinline__ void quad_prev(const AttnPagedParams& p, int64_t at, int there, int blocks, uint16_t (&pv)[Q][4]) {
+#pragma unroll
+    for (int j = 0; j < Q; ++j)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            pv[j][h] = 0;
+            if (p.prev_out && j < blocks && h < there) pv[j][h] = p.prev_out[at + 32 * j + (int64_t)h * p.d];
+        }
+}
+// lse (lse_at >= 0) and the outputs.
+template <int Q>
+__device__ __forceinline__ void quad_out(const AttnPagedParams& p, const Quad& q, int64_t lse_at, int64_t at, int there, int blocks,
+                                         const float4 (&o)[Q], const uint16_t (&pv)[Q][4]) {
+    const float pl = q.prev_lse * kLog2e, ep = exp2f(pl - q.mx), den = q.l + exp2f(q.sink - q.mx) + ep;
+    if (lse_at >= 0) p.lse[lse_at] = q.seen ? (q.mx + log2f(den)) * kLn2 : q.prev_lse;
+    // a query that sees no row keeps what it had
+    const float inv = q.seen ? 1.f / den : 0.f, wp = q.seen ? ep / den : pl == -INFINITY ? 0.f : 1.f;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const float f = __shfl_sync(kWarpFull, inv, h), w = __shfl_sync(kWarpFull, wp, h);
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            float x = (h == 0 ? o[j].x : h == 1 ? o[j].y : h == 2 ? o[j].z : o[j].w) * f;
+            if (w != 0.f) x += w * __uint_as_float((uint32_t)pv[j][h] << 16);   // weight 0: prev_out is not used
+            if (j < blocks && h < there) p.out[at + 32 * j + (int64_t)h * p.d] = __bfloat16_as_ushort(__float2bfloat16(x));
+        }
+    }
+}
+
+// Few parts: a warp adds them up in order, U at a time (block (x, y): warps 8 y ... of a query).  kByQuery: x is the
+// query, of which p.rec says whether it is split.  Otherwise, when there are more queries than CTAs, most CTAs' last query
+// is: x is the CTA, and the first U parts are on their way before it is known whether there are any.
+template <int U, bool kByQuery>
 __global__ void __launch_bounds__(256) merge_few_kernel(const AttnPagedParams p) {
-    const int c = blockIdx.x, lane = threadIdx.x & 31, hh = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5);
-    const int hp = p.pack * p.h;
+    const int lane = threadIdx.x & 31, quads = (p.pack * p.h + 3) / 4, unit = (int)blockIdx.y * 8 + ((int)threadIdx.x >> 5);
+    const int m = unit / quads, quad = unit - m * quads, blocks = min(4, p.d / 32 - 4 * m);
+    const int hd = 4 * quad + (lane & 3), own = lane >> 2;   // the lane's head, and its part of 8 at a time
     griddep_launch_dependents();
     griddep_wait();
-    if (hh >= hp) return;
+    if (blocks <= 0) return;
+    const int2 rec = split_of(p, kByQuery ? p.grid : p.B * p.groups);
+    if (kByQuery && rec.x < 0) return;
+    const int c = kByQuery ? rec.x : (int)blockIdx.x;
     auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * min(c + i, p.grid - 1); };   // (the last CTA's again past the end)
-    const float* src = p.part_o + (int64_t)hh * p.d + 4 * lane;
-    float4 v[U][NM];
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (4 * m * quads + quad) * 32 + lane;
+    const float2* stats = p.part_ml + hd;
+    float4 v[U][4];
     auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
 #pragma unroll
-            for (int j = 0; j < NM; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (128 * j + 4 * lane < p.d)
-                    v[k][j] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)slot(i0 + k) * hp * p.d + 128 * j));
+                if (j < blocks) v[k][j] = __ldcg(src + (int64_t)slot(i0 + k) * p.d * quads + j * quads * 32);
             }
     };
-    const int2 rec = __ldcg(p.rec + c);
-    float2 ml = __ldcg(p.part_ml + slot(lane) * 64 + hh);
+    float2 ml = __ldcg(stats + slot(own) * 64);
     load(0);
     if (rec.x < 0) return;
-    const PagedGroup grp = group_of(p, rec.x);
-    if (hh >= grp.heads) return;
-    const int parts = rec.y - c + 1;
-    const int64_t at = grp.row0 + hh;
-    const float pl_in = p.prev_lse ? p.prev_lse[at] : -INFINITY, pl = pl_in * kLog2e;
-    // The largest reference, 32 parts at a time.  A part of which the head sees nothing has a sum of -0.
+    const PagedGroup grp = group_of(p, kByQuery ? (int)blockIdx.x : rec.x);
+    const int there = grp.heads - 4 * quad, parts = rec.y - c + 1;
+    if (there <= 0) return;
+    const bool mine = (lane & 3) < there;
+    const int64_t at = (grp.row0 + 4 * quad) * p.d + 128 * m + lane;
+    uint16_t pv[4][4];
+    quad_prev(p, at, there, blocks, pv);
+    Quad q{-INFINITY, 0.f, p.sink && mine ? __ldg(p.sink + hd % p.h) * kLog2e : -INFINITY,
+           p.prev_lse && mine ? p.prev_lse[grp.row0 + hd] : -INFINITY, false};
     bool any = false;
-    float mx = -INFINITY;
-    for (int i = lane; i < parts; i += 32) {
-        if (i >= 32) ml = __ldcg(p.part_ml + slot(i) * 64 + hh);
+    for (int i = own; i < parts; i += 8) {
+        if (i >= 8) ml = __ldcg(stats + slot(i) * 64);
         any = any || !signbit(ml.y);
-        mx = fmaxf(mx, ml.x);
+        q.mx = fmaxf(q.mx, ml.x);
     }
-    const bool seen = __any_sync(kWarpFull, any);
-    const float sk = p.sink && seen ? __ldg(p.sink + hh % p.h) * kLog2e : -INFINITY;
+    quad_top(q, any);
+    float f = 0.f;
+    float4 o[4];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kWarpFull, mx, o));
-    mx = fmaxf(mx, fmaxf(sk, pl));
-    if (mx == -INFINITY) mx = 0.f;
-    float l = 0.f, f = 0.f;
-    float4 o[NM];
-#pragma unroll
-    for (int j = 0; j < NM; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0;;) {
-        if ((i0 & 31) == 0) {   // the factors of parts i0 .. i0 + 31, one per lane
-            if (parts > 32 && i0 + lane < parts) ml = __ldcg(p.part_ml + slot(i0 + lane) * 64 + hh);
-            f = i0 + lane >= parts || ml.y == 0.f ? 0.f : exp2f((ml.x == -INFINITY ? 0.f : ml.x) - mx);   // (inf * 0)
-            l += i0 + lane < parts ? ml.y * f : 0.f;
+        if ((i0 & 7) == 0) {   // the factors of parts i0 .. i0 + 7
+            if (parts > 8 && i0 + own < parts) ml = __ldcg(stats + slot(i0 + own) * 64);
+            f = i0 + own < parts ? part_factor(ml, q.mx) : 0.f;
+            q.l += i0 + own < parts ? ml.y * f : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const float w = __shfl_sync(kWarpFull, f, (i0 + k) & 31);
-            if (w != 0.f) {
+            const int from = ((i0 + k) & 7) * 4;
+            const float4 w = make_float4(__shfl_sync(kWarpFull, f, from), __shfl_sync(kWarpFull, f, from + 1),
+                                         __shfl_sync(kWarpFull, f, from + 2), __shfl_sync(kWarpFull, f, from + 3));
+            if (i0 + k < parts)
 #pragma unroll
-                for (int j = 0; j < NM; ++j) {
-                    o[j].x += w * v[k][j].x;
-                    o[j].y += w * v[k][j].y;
-                    o[j].z += w * v[k][j].z;
-                    o[j].w += w * v[k][j].w;
-                }
-            }
+                for (int j = 0; j < 4; ++j) add4(o[j], w, v[k][j]);
         }
         i0 += U;
         if (i0 >= parts) break;
         load(i0);
     }
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) l += __shfl_xor_sync(kWarpFull, l, s);
-    const float ep = exp2f(pl - mx), den = l + exp2f(sk - mx) + ep;
-    // a query that sees no row keeps what it had
-    const float inv = seen ? 1.f / den : 0.f, wp = seen ? ep / den : pl == -INFINITY ? 0.f : 1.f;
-    if (p.lse && lane == 0) p.lse[at] = seen ? (mx + log2f(den)) * kLn2 : pl_in;
+    for (int s = 16; s >= 4; s >>= 1) q.l += __shfl_xor_sync(kWarpFull, q.l, s);
+    quad_out(p, q, p.lse && m == 0 && lane < 4 && mine ? grp.row0 + hd : -1, at, there, blocks, o, pv);
+}
+
+// Queries of many parts, by query: G warps take every G-th part; the first of them works the factors out while everyone's
+// first parts are on their way, and adds up the warps' sums in order.
+template <int G, int Q>
+__global__ void __launch_bounds__(256) merge_many_kernel(const AttnPagedParams p) {
+    constexpr int U = 4, kUnits = 8 / G, kMost = 160;   // parts in flight; units per block; parts, at most
+    __shared__ float4 fac[kUnits][kMost];
+    __shared__ float4 sums[8][Q][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = warp % G, own_unit = warp / G;
+    const int quads = (p.pack * p.h + 3) / 4, unit = (int)blockIdx.y * kUnits + own_unit;
+    const int m = unit / quads, quad = unit - m * quads, blocks = min(Q, p.d / 32 - Q * m);   // none past the last unit
+    const int hd = 4 * quad + (lane & 3), own = lane >> 2;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int2 rec = split_of(p, p.grid);
+    if (rec.x < 0) return;
+    const int c = rec.x, parts = rec.y - c + 1;
+    auto slot = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + min(i, parts - 1)); };   // (the last one again past the end)
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (Q * m * quads + quad) * 32 + lane;
+    float4 v[U][Q];
+    auto load = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < NM; ++j) {
-        if (128 * j + 4 * lane >= p.d) continue;
-        const int64_t to = at * p.d + 128 * j + 4 * lane;
-        float4 x = make_float4(o[j].x * inv, o[j].y * inv, o[j].z * inv, o[j].w * inv);
-        if (wp != 0.f && p.prev_out) {
-            const uint2 pv = *reinterpret_cast<const uint2*>(p.prev_out + to);
-            x.x += wp * __uint_as_float(pv.x << 16);
-            x.y += wp * __uint_as_float(pv.x & 0xFFFF0000u);
-            x.z += wp * __uint_as_float(pv.y << 16);
-            x.w += wp * __uint_as_float(pv.y & 0xFFFF0000u);
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int j = 0; j < Q; ++j) {
+                v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < blocks) v[k][j] = __ldcg(src + (int64_t)slot(i0 + k * G) * p.d * quads + j * quads * 32);
+            }
+    };
+    load(g);
+    const PagedGroup grp = group_of(p, (int)blockIdx.x);
+    const int there = blocks > 0 ? grp.heads - 4 * quad : 0;
+    const bool mine = (lane & 3) < there;
+    const int64_t at = (grp.row0 + 4 * quad) * p.d + 32 * Q * m + lane;
+    Quad q{-INFINITY, 0.f, -INFINITY, -INFINITY, false};
+    uint16_t pv[Q][4];
+    if (g == 0) {
+        const float2* stats = p.part_ml + hd;
+        float2 ml[kMost / 8];
+#pragma unroll
+        for (int k = 0; k < kMost / 8; ++k) {
+            if (8 * k >= parts) break;
+            ml[k] = own + 8 * k < parts ? __ldcg(stats + slot(own + 8 * k) * 64) : make_float2(-INFINITY, -0.f);
         }
-        *reinterpret_cast<uint2*>(p.out + to) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+        quad_prev(p, at, there, blocks, pv);
+        if (p.sink && mine) q.sink = __ldg(p.sink + hd % p.h) * kLog2e;
+        if (p.prev_lse && mine) q.prev_lse = p.prev_lse[grp.row0 + hd];
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < kMost / 8; ++k) {
+            if (8 * k >= parts) break;
+            any = any || !signbit(ml[k].y);
+            q.mx = fmaxf(q.mx, ml[k].x);
+        }
+        quad_top(q, any);
+#pragma unroll
+        for (int k = 0; k < kMost / 8; ++k) {
+            if (8 * k >= parts) break;
+            if (own + 8 * k < parts) {
+                const float f = part_factor(ml[k], q.mx);
+                reinterpret_cast<float*>(&fac[own_unit][own + 8 * k])[lane & 3] = f;
+                q.l += ml[k].y * f;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o >= 4; o >>= 1) q.l += __shfl_xor_sync(kWarpFull, q.l, o);
     }
+    __syncthreads();
+    float4 o[Q];
+#pragma unroll
+    for (int j = 0; j < Q; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = g; i0 < parts; i0 += U * G) {
+        if (i0 != g) load(i0);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k * G >= parts) break;
+            const float4 w = fac[own_unit][i0 + k * G];
+#pragma unroll
+            for (int j = 0; j < Q; ++j) add4(o[j], w, v[k][j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < Q; ++j) sums[warp][j][lane] = o[j];
+    __syncthreads();
+    if (g != 0) return;
+#pragma unroll
+    for (int j = 0; j < Q; ++j)
+#pragma unroll
+        for (int k = 1; k < G; ++k) {
+            const float4 x = sums[warp + k][j][lane];
+            o[j] = make_float4(o[j].x + x.x, o[j].y + x.y, o[j].z + x.z, o[j].w + x.w);
+        }
+    quad_out(p, q, p.lse && m == 0 && lane < 4 && mine ? grp.row0 + hd : -1, at, there, blocks, o, pv);
 }
 
 template <int NM>
@@ -1121,12 +1273,15 @@ cudaError_t launch_nm(const CUtensorMap& tm_q, const AttnPagedParams& p, cudaStr
     e = launch_after(kernel, dim3((unsigned)p.grid), kPThreads, smem, stream, tm_q, p);
     if (e != cudaSuccess || p.whole) return e;
     const int parts = p.grid / nq + 1;   // of a query, when they are alike
-    const unsigned mx = (unsigned)(nq < p.grid ? nq : p.grid), mh = (unsigned)(p.pack * p.h);
-    const dim3 few((unsigned)p.grid, (mh + 7) / 8);
-    return parts > 16  ? launch_after(merge_kernel<16, 32, AttnPagedParams>, dim3(mx, mh, (unsigned)NM), 512, 0, stream, p)
-           : parts > 8 ? launch_after(merge_kernel<2, 128, AttnPagedParams>, dim3(mx, mh), 256, 0, stream, p)
-           : parts > 4 ? launch_after(merge_few_kernel<NM, 4>, few, 256, 0, stream, p)
-                       : launch_after(merge_few_kernel<NM, 2>, few, 256, 0, stream, p);
+    const int quads = (p.pack * p.h + 3) / 4;
+    auto grid = [&](int warps, int dims) {   // warps of four heads x dims, of each query that may be split
+        return dim3((unsigned)(nq < p.grid ? nq : p.grid), (unsigned)((quads * ((p.d + dims - 1) / dims) * warps + 7) / 8));
+    };
+    return parts > 16   ? launch_after(merge_many_kernel<8, 2>, grid(8, 64), 256, 0, stream, p)
+           : parts > 8  ? launch_after(merge_many_kernel<2, 4>, grid(2, 128), 256, 0, stream, p)
+           : parts > 4  ? launch_after(merge_few_kernel<4, true>, grid(1, 128), 256, 0, stream, p)
+           : p.by_query ? launch_after(merge_few_kernel<2, true>, grid(1, 128), 256, 0, stream, p)
+                        : launch_after(merge_few_kernel<2, false>, grid(1, 128), 256, 0, stream, p);
 }
 
 }  // namespace
@@ -1149,6 +1304,7 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, i
     l.least = groups >= 3 && (l.pack == 1 || d > 128) ? 4 : 1;
     const int64_t list = l.whole ? groups : (tiles * groups + l.least - 1) / l.least;
     l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);
+    l.by_query = !l.whole && groups <= l.grid;
     return l;
 }
 

@@ -271,17 +271,19 @@ struct AttnPagedParams {
     int window, n_first;        // window 0: every earlier position
     uint32_t* status;
     int grid;                   // CTAs of the attention kernel
-    int2* rec;                  // as in AttnFp4Params
+    int2* rec;                  // as in AttnFp4Params; by_query, [queries]: the CTAs of its first and last part, or {-1, 0}
     float* part_o;
     float2* part_ml;
     int pack, groups;
     bool whole;                 // no query is split between CTAs
     int least;                  // otherwise: tiles of a piece, at least
+    bool by_query;              // what rec holds
 };
 struct AttnPagedPlan {
     int pack, groups, grid;     // as in AttnPagedParams
     bool whole;
     int least;
+    bool by_query;
 };
 AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, int n_first, int num_sms);
 // tm_q: q as [B*s*h, d], box 64 x 64
