@@ -89,7 +89,6 @@ constexpr int kRegsSoft = 104, kRegsOut = 72, kRegsLoad = 64, kRegsMma = 64;
 constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
 constexpr int kAhead = 4;                      // tiles whose rows are asked for ahead
 constexpr uint32_t kStage = 1024;              // 16 heads x 32 dims of bf16
-constexpr int kWholeTiles = 4;                 // lists of at most this many tiles are never split between CTAs
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 // A run of one group's tiles, as the list's warp publishes it.
@@ -347,8 +346,10 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
         total += u;
     }
     const long long first = before + inc - sum;
-    const long long pieces = p.whole ? total : (total + p.least - 1) / p.least;
-    const int part = (int)blockIdx.x, ctas = pieces < (long long)gridDim.x ? (int)pieces : (int)gridDim.x;
+    // as many pieces as make the largest no longer (equal queries are then often cut into equal parts)
+    const long long grid = gridDim.x, size = max(divide(total + grid - 1, grid), (long long)p.least);
+    const long long pieces = p.whole ? total : divide(total + size - 1, size);
+    const int part = (int)blockIdx.x, ctas = pieces < grid ? (int)pieces : (int)grid;
     long long lo = 0, hi = 0;
     if (part < ctas) {
         const long long per = divide(total, ctas), longer = total - per * ctas;
@@ -1294,14 +1295,14 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, i
     int64_t rows = cap;              // of a group's list, at most
     if (window > 0 && (int64_t)window + l.pack - 1 + n_first < rows) rows = (int64_t)window + l.pack - 1 + n_first;
     const int64_t tiles = (rows + kRows - 1) / kRows, groups = (int64_t)B * l.groups;
-    // Splitting costs a second kernel, some 12 us or eight tiles; not splitting at most a list's tiles on some CTAs while
-    // others wait, and with fewer groups than SMs, SMs without work.
-    l.whole = tiles <= kWholeTiles || (groups >= num_sms && tiles <= 4 * kWholeTiles);
-    // Pieces of at least four tiles, when the parts of a few queries otherwise take longer to write and join than the tiles
-    // (4 queries of 64 heads x 512 over 2000 rows 28 -> 21 us, 32 over 1000 rows 33 -> 27, 8 groups of 4 x 16 heads x 256 over
-    // 3000 rows 30 -> 23); not for one or two queries (one over 4000 rows 18 -> 21) nor for short rows of several
-    // queries (12 groups of 3 x 20 heads x 128 over 1000 rows 16 -> 18.5).
-    l.least = groups >= 3 && (l.pack == 1 || d > 128) ? 4 : 1;
+    // A list of t tiles takes its CTA some 5 us and 1.45 t.  Splitting evens the CTAs' tiles out, but costs as much as another 5 tiles
+    // (second kernel; parts written and read), with more queries 13 (several parts per CTA).
+    const int64_t waves = (groups + num_sms - 1) / num_sms;
+    const double extra = 5.0 + (12 * groups < 8 * num_sms ? 12.0 * groups / num_sms : 8.0);
+    l.whole = (double)(waves * tiles) <= (double)(tiles * groups) / num_sms + extra;
+    // Pieces of at least two tiles, when the parts of a few queries otherwise take longer to write and join than the tiles
+    // (16 queries of 64 heads x 512 over 640 rows 20.7 -> 16.8 us, 8 groups of 4 x 16 heads over 1000 rows 22.8 -> 17.5).
+    l.least = groups >= 3 && (l.pack == 1 || d > 128) ? 2 : 1;
     const int64_t list = l.whole ? groups : (tiles * groups + l.least - 1) / l.least;
     l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);
     l.by_query = !l.whole && groups <= l.grid;
