@@ -334,6 +334,15 @@ ATTEND = {
     "pieces_of_4": (5, 1, 64, 320, 64, [1999, 0, 700, 64, 1300], None, 0, 0, True, True),
     "packed_runs_d320": (2, 700, 20, 320, 64, [0, 50], [700, 650], 33, 5, True, True),
     "packed_pairs_d448": (2, 5, 32, 448, 64, [380, 100], None, 0, 0, True, True),
+    # lists cut into parts: few and many of them, of few and many queries, heads that fill no group of four
+    "parts_13": (12, 1, 57, 64, 16, [1990 - 160 * i for i in range(12)], None, 0, 0, True, True),
+    "parts_9_d512": (18, 1, 64, 512, 64, [1500, 3, 700] * 6, None, 0, 0, True, True),
+    "parts_7_heads_33": (25, 1, 33, 448, 24, [1400 - 50 * i for i in range(25)], None, 0, 0, True, True),
+    "parts_3": (60, 1, 64, 320, 64, [1500, 40, 900, 0] * 15, [1, 1, 0, 1] * 15, 0, 0, True, True),
+    "parts_2_many_queries": (170, 1, 39, 128, 16, [1790 - 10 * i for i in range(170)], None, 0, 0, True, True),
+    "parts_2_packed": (160, 3, 19, 64, 64, [1600, 900] * 80, [3, 0, 1, 2] * 40, 0, 0, True, True),
+    "parts_many_one_head": (1, 1, 1, 64, 16, [9000], None, 0, 0, True, True),
+    "parts_window": (3, 40, 64, 192, 64, [3000, 2500, 0], [40, 2, 40], 2000, 70, True, True),
 }
 
 
@@ -674,7 +683,7 @@ def test_layer_against_definition(sti):  # noqa: F811
 @gpu
 def test_layer_captured_and_replayed(sti):  # noqa: F811
     """A decode step of the layer captured once and replayed leaves the same pages and outputs as the calls made one by
-    one; a graph of another batch shares the workspaces that torch's pool gives both."""
+    one."""
     import torch
 
     h, d, steps = 64, 512, 9
