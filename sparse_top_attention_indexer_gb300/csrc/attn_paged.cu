@@ -15,10 +15,11 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, i
     if (window > 0 && (int64_t)window + l.pack - 1 + n_first < rows) rows = (int64_t)window + l.pack - 1 + n_first;
     const int64_t tiles = (rows + kRows - 1) / kRows, groups = (int64_t)B * l.groups;
     // A list of t tiles takes its CTA some 5 us and 1.45 t.  Splitting evens the CTAs' tiles out, but costs as much as another 5 tiles
-    // (second kernel; parts written and read), with more queries 13 (several parts per CTA).
+    // (second kernel; parts written and read), with more queries 13 (several parts per CTA).  Of long lists some may be much longer
+    // than others, which only splitting evens out: those are not taken whole.
     const int64_t waves = (groups + num_sms - 1) / num_sms;
     const double extra = 5.0 + (12 * groups < 8 * num_sms ? 12.0 * groups / num_sms : 8.0);
-    l.whole = (double)(waves * tiles) <= (double)(tiles * groups) / num_sms + extra;
+    l.whole = tiles <= 16 && (double)(waves * tiles) <= (double)(tiles * groups) / num_sms + extra;
     // Pieces of at least two tiles, when the parts of a few queries otherwise take longer to write and join than the tiles
     // (16 queries of 64 heads x 512 over 640 rows 20.7 -> 16.8 us, 8 groups of 4 x 16 heads over 1000 rows 22.8 -> 17.5).
     l.least = groups >= 3 && (l.pack == 1 || d > 128) ? 2 : 1;

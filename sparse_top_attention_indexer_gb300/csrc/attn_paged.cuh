@@ -101,6 +101,7 @@ struct __align__(16) Run {
     uint32_t pos;       // position of its first query
     int pad[2];
 };
+constexpr int kWarpPlan = 256;                 // groups that one warp plans for
 constexpr int kRuns = 4, kReaders = 23;        // runs published ahead; the warps that read them
 
 // This CTA's piece of the list of all groups' tiles: tiles lo .. hi - 1, the first one tile `off` of group q's list.
@@ -118,7 +119,7 @@ struct __align__(16) Tail {
     float lsum[2][4][32];
     int vis[2][64];           // [run parity] per head: which rows of the list it sees (kPack), see head_vis
     uint8_t valid[2][8];      // [buffer][row / 8]: bit row % 8: it exists
-    Piece piece;
+    int2 start;               // a wide plan's: Piece's q, off
     long long scratch[kWarps];
     // the barriers lie in one row, see init_barriers
     uint64_t full[2][2];      // [buffer][half of the dims] filled
@@ -323,10 +324,13 @@ __device__ __forceinline__ int piece_of(const Piece& w, long long x) {
     return (int)(x < longer * (per + 1) ? divide(x, per + 1) : longer + divide(x - longer * (per + 1), per));
 }
 
-// This CTA's piece.  Every thread calls it.
-__device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail* tl) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int each = n <= kPThreads ? 1 : (n + kPThreads - 1) / kPThreads;
+// This CTA's piece.  kWide: every thread calls it; else one warp (for few groups: nothing to wait for, and only the warp that
+// walks the list has to know; 1 us less).
+template <bool kWide>
+__device__ __forceinline__ Piece plan_piece(const AttnPagedParams& p, int n, Tail* tl) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = kWide ? threadIdx.x : lane;
+    constexpr int kBy = kWide ? kPThreads : 32;
+    const int each = n <= kBy ? 1 : (n + kBy - 1) / kBy;
     const long long i0 = (long long)tid * each;
     long long sum = 0;
     for (int k = 0; k < each && i0 + k < n; ++k) sum += tiles_of(p, (int)(i0 + k));
@@ -336,14 +340,18 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
         const long long u = __shfl_up_sync(kWarpFull, inc, o);
         if (lane >= o) inc += u;
     }
-    if (lane == 31) tl->scratch[warp] = inc;
-    __syncthreads();
     long long before = 0, total = 0;
+    if (kWide) {
+        if (lane == 31) tl->scratch[warp] = inc;
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        const long long u = tl->scratch[k];
-        if (k < warp) before += u;
-        total += u;
+        for (int k = 0; k < kWarps; ++k) {
+            const long long u = tl->scratch[k];
+            if (k < warp) before += u;
+            total += u;
+        }
+    } else {
+        total = __shfl_sync(kWarpFull, inc, 31);
     }
     const long long first = before + inc - sum;
     // as many pieces as make the largest no longer (equal queries are then often cut into equal parts)
@@ -356,13 +364,9 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
         lo = part * per + (part < longer ? part : longer);
         hi = lo + per + (part < longer ? 1 : 0);
     }
-    if (tid == 0) {
-        tl->piece.lo = lo;
-        tl->piece.hi = hi;
-        tl->piece.total = total;
-        tl->piece.ctas = ctas;
-    }
-    if (lo < hi && first <= lo && lo < first + sum) {
+    Piece w{lo, hi, total, ctas, 0, 0};
+    bool mine = lo < hi && first <= lo && lo < first + sum;
+    if (mine) {
         long long at = first;
         int i = (int)i0;
         if (each > 1)
@@ -371,9 +375,18 @@ __device__ __forceinline__ void plan_piece(const AttnPagedParams& p, int n, Tail
                 if (at + c > lo) break;
                 at += c;
             }
-        tl->piece.q = i;
-        tl->piece.off = (int)(lo - at);
+        w.q = i;
+        w.off = (int)(lo - at);
+        if (kWide) tl->start = make_int2(w.q, w.off);
     }
+    if (!kWide) {
+        const int from = __ffs(__ballot_sync(kWarpFull, mine)) - 1;
+        if (from >= 0) {
+            w.q = __shfl_sync(kWarpFull, w.q, from);
+            w.off = __shfl_sync(kWarpFull, w.off, from);
+        }
+    }
+    return w;
 }
 
 // d-blocks of 128 dims; groups of several queries; prev_out to be joined; one group per sequence
@@ -423,8 +436,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tmem_relinquish();
     }
     // (a group for each CTA: nothing to plan)
-    const bool single = p.whole && nq <= (int)gridDim.x;
-    if (!single) plan_piece(p, nq, tl);
+    const bool single = p.whole && nq <= (int)gridDim.x, wide = nq > kWarpPlan;
+    Piece piece;
+    if (!single && wide) piece = plan_piece<true>(p, nq, tl);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -522,18 +536,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
         } else if (warp == kListWarp) {
             // -------------------------------------------------------------- the runs, and their rows' way to L2
-            Piece piece = tl->piece;
             if (single) {
-                piece.lo = 0;
-                piece.hi = 1;
-                piece.q = blockIdx.x;
-                piece.off = 0;
+                piece = Piece{0, 1, 1, 1, (int)blockIdx.x, 0};
+            } else if (wide) {
+                piece.q = tl->start.x;
+                piece.off = tl->start.y;
+            } else {
+                piece = plan_piece<false>(p, nq, tl);
             }
             long long at_tile = piece.lo;
             int q = piece.q, off = piece.off;
             int2 rec = make_int2(-1, 0);
             while (ok) {
-                // the next group with a tile in the piece (p.whole: with its first tile there, and then all of it)
+                // the next group with a tile in the piece (p.whole: with its middle there, and then all of it; by their first tiles,
+                // queries of 121 to 128 tiles would fall to CTAs by two and by four where there are three for each)
                 int nt = 0, u = 0;
                 for (; at_tile < piece.hi; ++q, off = 0) {
                     run.b = q / p.groups;
@@ -548,7 +564,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     run.nf = rows.nf;
                     run.lo = rows.lo;
                     nt = (rows.n + kRows - 1) / kRows;
-                    if (nt > 0 && !(p.whole && off > 0)) break;
+                    const long long mid = at_tile - off + (nt - 1) / 2;
+                    if (nt > 0 && (!p.whole || single || (mid >= piece.lo && mid < piece.hi))) break;
                     at_tile += single ? 1 : nt - off;
                     nt = 0;
                 }
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 run.t0 = run.t1 = 0;
                 if (nt > 0) {
                     const long long left = piece.hi - at_tile;
-                    run.t0 = off;
+                    run.t0 = p.whole ? 0 : off;
                     run.t1 = p.whole || nt - off < left ? nt : off + (int)left;
                     run.slot = run.t0 == 0 && run.t1 == nt ? -1 : 2 * (int)blockIdx.x + (run.t0 == 0 ? 1 : 0);
                 }
@@ -577,7 +594,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     if (p.by_query && lane == 0) p.rec[q] = make_int2(last < 0 ? -1 : (int)blockIdx.x, last);
                     if (last >= 0) rec = make_int2(q, last);
                 }
-                at_tile += run.t1 - run.t0;
+                at_tile += run.t1 - off;
                 ++q;
                 off = 0;
                 n += (uint32_t)(run.t1 - run.t0);
