@@ -479,7 +479,8 @@ sti_status sti_kv_evict(float *row_weight, int64_t row_weight_bstride, int32_t *
  * Not operations of the pages' listings: the steps around a layer's attention (RMS norm and rotation of the queries and
  * of the cache rows) and a cache whose rows live in pages, attended as a whole or through a sliding window.  A step brings
  * seqlen tokens to each of b sequences, the first at position start_pos[b] >= 0; n_new (int32 [b] or NULL: all) of them
- * are real, clamped to [0, seqlen]: the others of a padded batch are neither read into anything nor written.
+ * are real, clamped to [0, seqlen]: the others of a padded batch are neither read into anything nor written.  The kernels of
+ * these calls may be set up while the stream's kernel before them ends; they read and write once it is done.
  *
  * The cache: pages, bf16 [n_pages, page_size, d] with contiguous rows, page i at pages + i*page_stride (elements); table,
  * int32 [b, max_pages], sequence b at table + b*table_stride: position p of the sequence is row p % page_size of page
@@ -546,7 +547,7 @@ sti_status sti_kv_append_paged(const uint16_t *x, int64_t x_bstride, int64_t x_t
  *   q, out: bf16 [b, seqlen, h, d]; lse: fp32 [b, seqlen, h] or NULL; attn_sink, prev_out, prev_lse: as sti_attn_fp4kv
  * out may be prev_out itself; otherwise the outputs must not overlap the inputs.
  * bf16 tensor-core MMAs with fp32 accumulation, P rounded to bf16 for the PV product, fp32 online softmax.  Results do not
- * depend on the timing of the GPU (no atomics).  Two kernels.
+ * depend on the timing of the GPU (no atomics).  One kernel, or two when queries' rows are split between SMs.
  * Supported: 1 <= h <= 64, d a multiple of 64 up to 512, max_pages * page_size <= 2^30; q, out, prev_out, pages 16-byte
  * aligned, page_stride a multiple of 8 and at least page_size * d; b * seqlen * h < 2^31.
  * ws: sti_attn_paged_workspace_size() bytes.

@@ -10,7 +10,7 @@
 // the first query's window).  Lists are cut into tiles of 64 rows wherever those lie, so a page may end anywhere in
 // a tile and a window of 128 rows is two tiles at any position.  The groups' tiles form one long list that is cut into equal
 // contiguous pieces, one per CTA and SM; what a CTA has of a query that others share leaves as an fp32 partial, which a
-// second kernel joins (short lists are not cut).  Two tile buffers; 24 warps:
+// second kernel joins.  Where splitting would cost more than it evens out, a list goes to one CTA as a whole.  Two tile buffers; 24 warps:
 //   * warps 0..7 run the online softmax (two sets of 32 heads; what P is relative to moves only when a score passes it
 //     by 2^8);
 //   * warps 8..15 write the outputs, while the next query's tiles are under way: O^T lies in a ring of TMEM blocks;
@@ -18,15 +18,16 @@
 //     tiles earlier releases its halves.  Rows that nothing sees are not read but zeros, so that P = 0 meets no NaN;
 //   * warp 20 issues the QKs, S^T = tile . Q^T (M = 64 rows, N = heads), warp 21 the PVs, O^T += V^T . P^T (M = 128 dims
 //     per block, K = the rows of the tile, the same tile read as an MN-major operand);
-//   * warp 22 walks the list, tells the others what comes next and asks for the rows of the next tiles, into L2;
+//   * warp 22 walks the list, tells the others what comes next and, when decoding, asks for the next tile's rows, into L2;
 //   * warp 23 loads Q by TMA as soon as the last QK of the query before has read the buffer.
 //
 // A long chunk is bound by shared memory: of a tile at 128 B a cycle, QK 1024 cycles, PV 768, the rows' copies 512 and
 // P^T and scores 100, together 2400 of the 2750 that a tile takes (the MMAs alone would take 2100: at N = 64 an M = 128 step
-// costs what one at N = 128 does).  2048 queries of 64 heads x 512 at 6144: 2100 us, 0.48 of the measured bf16 peak.  Decoding
-// is bound by HBM: 32 queries over 16384 rows 124 us, of which the rows alone take 81 at the measured copy rate and
-// the join 12.  Windows are bound by one query's chain: its Q has to come, the QK of its first tile, the softmax, the
-// PV that frees the third tile's buffer; 4096 queries through a window of 128 rows and 4 first ones 182 us, 81 at the
+// costs what one at N = 128 does).  2048 queries of 64 heads x 512 at 6144: 2105 us, 0.48 of the measured bf16 peak.  Decoding
+// is bound by HBM: 32 queries over 16384 rows 103 us; a tile more costs what its rows take at 6.8 TB/s (81 us for all at the
+// measured copy rate), next to 20 us at the start (plan, Q, first tile: 5), the end (parts written 2, joined 4) and between
+// the two kernels.  Windows are bound by one query's chain: its Q has to come, the QK of its first tile, the softmax, the
+// PV that frees the third tile's buffer; 4096 queries through a window of 128 rows and 4 first ones 181 us, 81 at the
 // copy rate.  The code that a query runs through has to stay in the instruction cache: 10 % more of it cost 5 to 9 %.
 //
 // P is rounded to bf16 for the PV product, as the rows are bf16 and one MMA takes one type: each row's share of the output
@@ -372,7 +373,7 @@ __device__ __forceinline__ Piece plan_piece(const AttnPagedParams& p, int n, Tai
         if (each > 1)
             for (;; ++i) {
                 const int c = tiles_of(p, i);
-                if (at + c > lo) break;
+                if (at + c > lo || i + 1 >= n) break;   // (the second: lengths that another stream changes meanwhile)
                 at += c;
             }
         w.q = i;
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 // the next group with a tile in the piece (p.whole: with its middle there, and then all of it; by their first tiles,
                 // queries of 121 to 128 tiles would fall to CTAs by two and by four where there are three for each)
                 int nt = 0, u = 0;
-                for (; at_tile < piece.hi; ++q, off = 0) {
+                for (; at_tile < piece.hi && q < nq; ++q, off = 0) {   // (the second as in plan_piece)
                     run.b = q / p.groups;
                     u = q - run.b * p.groups;
                     const uint32_t start = (uint32_t)__ldg(p.start_pos + run.b);
