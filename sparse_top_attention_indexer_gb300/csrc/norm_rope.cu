@@ -13,11 +13,11 @@
 // pairs, spread over its threads, into shared memory, where they serve all heads.  LPR lanes share a row, 8 elements
 // (16 bytes) per lane and chunk; U rows per slot are loaded before the first is used, the first ones before the angles.
 //
-// Many rows are bound by HBM: queries of 4096 tokens, 64 heads x 512, 82 us, 0.97 of the measured copy rate.  Rows of one head
-// are bound by the way to a block's first row (its place, its position, its angles) and by instructions, some 400 per row: 8 x
-// 8192 tokens of which half are padding 20 us (10 at the copy rate).  Steps of that: several tokens per block and rows in flight
-// 109 -> 39 us, places looked up once per token -> 32, angles by polynomials -> 23, two fp32 per instruction and four
-// blocks per SM -> 20.
+// Many rows are bound by HBM: queries of 4096 tokens, 64 heads x 512, 82 us, 0.97 of the measured copy rate (0.90 to 0.95 for 64
+// to 256 dims, 0.85 to 0.95 with 8 heads).  Rows of one head are bound by the way to a block's first row (its place, its position, its
+// angles) and by instructions, some 400 per row: 8 x 8192 tokens of which half are padding 20 us (10 at the copy rate).  Steps of that:
+// several tokens per block and rows in flight 109 -> 39 us, places looked up once per token -> 32, angles by polynomials -> 23,
+// two fp32 per instruction and four blocks per SM -> 20.
 #include <cuda_bf16.h>
 
 #include "sti_attn_tiles.cuh"   // launch_after
@@ -28,6 +28,9 @@ namespace sti {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kPerSlot = 8;        // rows that a block takes per slot, where there are enough (8 heads x 512: 0.92 of the copy rate, 4 0.88,
+                                   // 2 0.83, one token per block 0.57)
+constexpr int kPad = 2;            // between tokens' angles: whole powers of two would put them all to the same banks
 constexpr int kMaxAngles = 4096;   // pairs of a block's tokens: 32 KB
 
 struct Shape {      // a block's rows: `tokens` tokens of `heads` heads each
@@ -78,14 +81,16 @@ __device__ __forceinline__ void unpack(const uint4& v, uint64_t (&f)[4]) {
     for (int i = 0; i < 4; ++i) f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-// LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time; pairs (i, i + rd / 2)
+// LPR lanes per row, CH chunks of 8 elements per lane, U rows at a time.  kHalves: pairs (i, i + rd / 2); a lane has both
+// chunks of its pairs then (fetched again by the lane of either: 64 heads x 64 0.58 of the copy rate, here 0.86).
 template <int LPR, int CH, int U, bool kHalves>
-__global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+__global__ void __launch_bounds__(kRowThreads, CH <= 2 ? 4 : CH == 3 ? 3 : 2) norm_rope_kernel(const NormRopeParams p, const Shape sh) {
+    static_assert(!kHalves || CH % 2 == 0, "");
     constexpr int kSlots = kRowThreads / LPR;
-    extern __shared__ float2 cs[];                      // [tokens][rd / 2], then the tokens' places
+    extern __shared__ __align__(16) float2 cs[];                      // [tokens][rd / 2], then the tokens' places
     const int slot = threadIdx.x / LPR, li = threadIdx.x % LPR;
-    const int pairs = p.rd / 2;
-    int64_t* from = reinterpret_cast<int64_t*>(cs + sh.tokens * pairs);   // of its first head in x, -1: padding or past the end
+    const int pairs = p.rd / 2, row_pairs = pairs + kPad;
+    int64_t* from = reinterpret_cast<int64_t*>(cs + sh.tokens * row_pairs);   // of its first head in x, -1: padding or past the end
     int64_t* to = from + sh.tokens;                                       // of its first head in y, its row's in the pages (-1: none)
     int* at = reinterpret_cast<int*>(to + sh.tokens);                     // its position
     const uint32_t bt = sh.blocks_h == 1 ? blockIdx.x : blockIdx.x / (uint32_t)sh.blocks_h;
@@ -93,6 +98,17 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) no
     const int head0 = (int)(blockIdx.x - bt * (uint32_t)sh.blocks_h) * sh.heads;
     const int rows = sh.tokens * sh.heads;
     const int chunks = p.d / 8;
+    // Which chunks a lane has, and of which unit of angles: a chunk's four pairs, or the eight of two chunks half a range apart.
+    // A unit's angles lie in pieces of two, piece j of all units side by side.
+    constexpr int kPieces = kHalves ? 4 : 2;
+    const int c_lo = p.off / 8, units = p.rd / (4 * kPieces);
+    auto unit_of = [&](int k) { return kHalves ? li + LPR * (k >> 1) : li + LPR * k - c_lo; };
+    auto turns_at = [&](int k) { return (uint32_t)unit_of(k) < (uint32_t)units; };   // whether chunk k is rotated
+    auto chunk = [&](int k) {
+        if (!kHalves) return li + LPR * k;
+        const int u = unit_of(k), rest = 2 * (u - units) + (k & 1);   // (of the chunks outside the range)
+        return u < units ? c_lo + u + (k & 1) * units : rest < c_lo ? rest : rest + 2 * units;
+    };
     // the next kernel may start to be set up, the one before has to be done
     griddep_launch_dependents();
     griddep_wait();
@@ -124,7 +140,7 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) no
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
                 v[r][k] = make_uint4(0, 0, 0, 0);
-                if (src[r] && li + LPR * k < chunks) v[r][k] = *reinterpret_cast<const uint4*>(src[r] + 8 * (li + LPR * k));
+                if (src[r] && chunk(k) < chunks) v[r][k] = *reinterpret_cast<const uint4*>(src[r] + 8 * chunk(k));
             }
         }
     };
@@ -150,32 +166,21 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) no
         for (int i = threadIdx.x >> sh.lanes; i < sh.tokens; i += kRowThreads >> sh.lanes) {
             if (from[i] < 0) continue;
             const float2 a = cos_sin((uint64_t)(int64_t)at[i] * f);
-            cs[i * pairs + pr] = make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
+            cs[i * row_pairs + ((pr / 2 % kPieces) * units + pr / (2 * kPieces)) * 2 + (pr & 1)] =
+                make_float2(a.x * p.gain, (p.inverse ? -a.y : a.y) * p.gain);
         }
     }
     uint64_t weight[CH][4];
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
         uint4 w = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // ones
-        if (p.weight && li + LPR * k < chunks) w = __ldg(reinterpret_cast<const uint4*>(p.weight) + li + LPR * k);
+        if (p.weight && chunk(k) < chunks) w = __ldg(reinterpret_cast<const uint4*>(p.weight) + chunk(k));
         unpack(w, weight[k]);
     }
     __syncthreads();
-    const int c_lo = p.off / 8, c_hi = (p.off + p.rd) / 8, half = p.rd / 16;
     for (int i0 = slot;;) {
 #pragma unroll
         for (int r = 0; r < U; ++r) {
-            // the pairs' other halves, before anything of the row is written
-            uint4 other[kHalves ? CH : 1];
-            if (kHalves) {
-#pragma unroll
-                for (int k = 0; k < CH; ++k) {
-                    const int c = li + LPR * k;
-                    other[k] = make_uint4(0, 0, 0, 0);
-                    if (src[r] && c >= c_lo && c < c_hi)
-                        other[k] = *reinterpret_cast<const uint4*>(src[r] + 8 * (c < c_lo + half ? c + half : c - half));
-                }
-            }
             uint64_t f[CH][4];
 #pragma unroll
             for (int k = 0; k < CH; ++k) unpack(v[r][k], f[k]);
@@ -191,45 +196,47 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) no
                 for (int o = LPR / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
                 scale = rsqrtf(sum * p.inv_d + p.eps);
             }
-            __syncwarp();
             if (!src[r]) continue;
             uint16_t* dst = p.y ? p.y : p.pages;        // where the row goes
             if (to[tk[r]] < 0) continue;
             dst += to[tk[r]] + (int64_t)(head0 + i0 + r * kSlots - tk[r] * sh.heads) * p.d;
-            const float2* my = cs + tk[r] * pairs;
+            const float2* my = cs + tk[r] * row_pairs;
+            auto angles = [&](int k, int j) { return *reinterpret_cast<const float4*>(my + 2 * (j * units + unit_of(k))); };
             const uint64_t scale2 = pack2(scale, scale);
+            auto write = [&](int k, const float2 (&x)[4]) {
+                if (chunk(k) < chunks)
+                    *reinterpret_cast<uint4*>(dst + 8 * chunk(k)) = make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                                                                              pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+            };
 #pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int c = li + LPR * k;
-                if (c >= chunks) continue;
-                float2 x[4];
+            for (int k = 0; k < CH; k += kHalves ? 2 : 1) {
+                float2 x[4], z[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = parts2(mul2(mul2(f[k][j], scale2), weight[k][j]));
-                if (c >= c_lo && c < c_hi) {
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = parts2(mul2(mul2(f[k][j], scale2), weight[k][j]));
+                    if (kHalves) z[j] = parts2(mul2(mul2(f[k + kHalves][j], scale2), weight[k + kHalves][j]));
+                }
+                if (turns_at(k)) {
                     if (kHalves) {
-                        const bool low = c < c_lo + half;
-                        const int oc = low ? c + half : c - half;
-                        uint64_t g[4], w[4];
-                        unpack(other[k], g);
-                        unpack(p.weight ? __ldg(reinterpret_cast<const uint4*>(p.weight) + oc)
-                                        : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), w);
-                        const float2* a = my + 8 * ((low ? c : oc) - c_lo);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float2 z = parts2(mul2(mul2(g[j], scale2), w[j])), a0 = a[2 * j], a1 = a[2 * j + 1];
-                            x[j].x = x[j].x * a0.x + (low ? -z.x : z.x) * a0.y;
-                            x[j].y = x[j].y * a1.x + (low ? -z.y : z.y) * a1.y;
+                            const float4 a = angles(k, j);
+                            const float2 u = x[j], w = z[j];
+                            x[j] = make_float2(u.x * a.x - w.x * a.y, u.y * a.z - w.y * a.w);
+                            z[j] = make_float2(w.x * a.x + u.x * a.y, w.y * a.z + u.y * a.w);
                         }
                     } else {
-                        const float2* a = my + 4 * (c - c_lo);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            x[j] = make_float2(x[j].x * a[j].x - x[j].y * a[j].y, x[j].y * a[j].x + x[j].x * a[j].y);
+                        for (int j = 0; j < 4; j += 2) {
+                            const float4 a = angles(k, j / 2);
+                            const float2 u = x[j], w = x[j + 1];
+                            x[j] = make_float2(u.x * a.x - u.y * a.y, u.y * a.x + u.x * a.y);
+                            x[j + 1] = make_float2(w.x * a.z - w.y * a.w, w.y * a.z + w.x * a.w);
+                        }
                     }
                 }
-                *reinterpret_cast<uint4*>(dst + 8 * c) =
-                    make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
-                               pack_bf16x2(x[3].x, x[3].y));
+                write(k, x);
+                if (kHalves) write(k + kHalves, z);
             }
         }
         i0 += U * kSlots;
@@ -238,37 +245,49 @@ __global__ void __launch_bounds__(kRowThreads, CH == 1 ? 4 : CH == 2 ? 4 : 2) no
     }
 }
 
-template <int LPR, int CH, int U>
+template <int LPR, int CH, int U, bool kHalves>
 cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     constexpr int slots = kRowThreads / LPR;
     const int64_t tokens = (int64_t)p.B * p.s;
     auto up = [](int64_t n, int64_t m) { return (n + m - 1) / m; };
     Shape sh;
     sh.heads = p.h;
-    sh.tokens = p.h >= slots ? 1 : 2 * U * slots / p.h;   // (up to 2 U rows per slot)
+    sh.tokens = kPerSlot * slots / p.h;
+    if (sh.tokens < 1) sh.tokens = 1;
     if (sh.tokens > kRowThreads) sh.tokens = kRowThreads;
     if (p.rd > 0 && sh.tokens > kMaxAngles / (p.rd / 2)) sh.tokens = kMaxAngles / (p.rd / 2);
-    // few tokens: fewer per block, then their heads to several blocks, as long as every slot has a row
-    while (sh.tokens > 1 && sh.tokens * p.h > slots && up(tokens, sh.tokens) < 2 * num_sms) sh.tokens = (sh.tokens + 1) / 2;
+    // few tokens: fewer per block (two waves of blocks), then their heads to several blocks, as long as every slot has a row
+    while (sh.tokens > 1 && sh.tokens * p.h > slots && up(tokens, sh.tokens) < 8 * num_sms) sh.tokens = (sh.tokens + 1) / 2;
     while (sh.tokens == 1 && sh.heads > slots && tokens * up(p.h, sh.heads) < 2 * num_sms) sh.heads = (sh.heads + 1) / 2;
     sh.blocks_h = (int)up(p.h, sh.heads);
     sh.lanes = 0;
     while (1 << sh.lanes < p.rd / 2 && 1 << sh.lanes < kRowThreads) ++sh.lanes;
-    const size_t smem = (size_t)sh.tokens * ((p.rd / 2) * sizeof(float2) + 2 * sizeof(int64_t) + sizeof(int));
-    return launch_after(p.halves ? norm_rope_kernel<LPR, CH, U, true> : norm_rope_kernel<LPR, CH, U, false>, dim3((unsigned)(up(tokens, sh.tokens) * sh.blocks_h)), kRowThreads, smem,
-                        stream, p, sh);
+    const size_t smem = (size_t)sh.tokens * ((p.rd / 2 + kPad) * sizeof(float2) + 2 * sizeof(int64_t) + sizeof(int));
+    return launch_after(norm_rope_kernel<LPR, CH, U, kHalves>, dim3((unsigned)(up(tokens, sh.tokens) * sh.blocks_h)), kRowThreads,
+                        smem, stream, p, sh);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
     const int chunks = p.d / 8;
-    if (chunks <= 4) return launch<4, 1, 2>(p, num_sms, stream);
-    if (chunks <= 8) return launch<8, 1, 2>(p, num_sms, stream);
-    if (chunks <= 16) return launch<16, 1, 2>(p, num_sms, stream);
-    if (chunks <= 32) return launch<32, 1, 2>(p, num_sms, stream);
-    if (chunks <= 64) return launch<32, 2, 2>(p, num_sms, stream);
-    return launch<32, 4, 1>(p, num_sms, stream);
+    // Two chunks per lane where they fit the row: 8 heads x 128 0.91 of the copy rate, one per lane 0.60; three for what lies between
+    // (320 dims leave three lanes in eight idle otherwise: 0.84, with two 0.74).
+    if (p.halves) {
+        if (chunks <= 8) return launch<4, 2, 2, true>(p, num_sms, stream);
+        if (chunks <= 16) return launch<8, 2, 2, true>(p, num_sms, stream);
+        if (chunks <= 32) return launch<16, 2, 2, true>(p, num_sms, stream);
+        if (chunks <= 64) return launch<32, 2, 2, true>(p, num_sms, stream);
+        return launch<32, 4, 1, true>(p, num_sms, stream);
+    }
+    if (chunks <= 4) return launch<4, 1, 2, false>(p, num_sms, stream);
+    if (chunks <= 8) return launch<4, 2, 2, false>(p, num_sms, stream);
+    if (chunks <= 16) return launch<8, 2, 2, false>(p, num_sms, stream);
+    if (chunks <= 32) return launch<16, 2, 2, false>(p, num_sms, stream);
+    if (chunks <= 48) return launch<16, 3, 2, false>(p, num_sms, stream);
+    if (chunks <= 64) return launch<32, 2, 2, false>(p, num_sms, stream);
+    if (chunks <= 96) return launch<32, 3, 2, false>(p, num_sms, stream);
+    return launch<32, 4, 1, false>(p, num_sms, stream);
 }
 
 }  // namespace sti
