@@ -110,6 +110,16 @@ ROTATE = {
     "copy": (2, 3, 7, 64, 0, 0, True, False, False, False, [0, 3], None, 1.0, 1),
     "padded": (4, 37, 6, 64, 64, 0, True, False, True, False, [10, 20, 30, 40], [37, 0, 1, 36], 1.0, 1),
     "many_tokens": (2, 500, 3, 32, 16, 16, False, False, True, False, [0, 60000], [500, 499], 1.0, 8),
+    "d_320": (2, 40, 5, 320, 64, 256, True, False, True, True, [3, 100000], [40, 33], 1.0, 1),
+    "d_384": (1, 3, 50, 384, 128, 0, True, True, False, False, [9], None, 1.0, 1),
+    "d_576": (3, 90, 1, 576, 64, 512, True, False, True, True, [0, 70, 8], [90, 0, 1], 1.0, 40),
+    "d_768": (1, 5, 3, 768, 768, 0, True, False, True, False, [1], None, 1.0, 1),
+    "d_576_halves": (3, 30, 1, 576, 48, 40, False, False, True, True, [0, 70, 8], [30, 2, 0], 1.0, 1),
+    "d_320_halves": (2, 9, 8, 320, 304, 8, False, True, True, True, [3, 100000], None, 1.0, 1),
+    "d_512_halves_mid": (2, 70, 3, 512, 16, 200, False, False, True, True, [3, 100000], None, 1.0, 1),
+    "d_64_halves_all": (2, 700, 2, 64, 64, 0, False, False, True, True, [0, 9000], [700, 650], 1.0, 1),
+    "d_128_many": (1, 3000, 8, 128, 96, 32, False, False, True, True, [17], None, 1.0, 1),
+    "d_16_many": (7, 300, 1, 16, 16, 0, True, False, False, False, [0, 1, 2, 3, 4, 5, 6], None, 1.0, 1),
 }
 
 
