@@ -151,3 +151,65 @@ def test_rotate_in_place_of_a_strided_slice(sti):  # noqa: F811
     assert sti.norm_rope(q, pos, f, interleaved=False, n_new=n_new, out=q, stream=stream) is q
     stream.synchronize()
     assert (x == want).all()
+
+
+@gpu
+def test_nothing_to_attend(sti):  # noqa: F811
+    """No sequences; a table of no pages; no pool; a long table and a batch of padding alone."""
+    import torch
+
+    q = torch.randn(3, 2, 8, 64, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    pages = torch.zeros(4, 16, 64, dtype=torch.bfloat16, device="cuda")
+    start = torch.zeros(3, dtype=torch.int32, device="cuda")
+    empty = torch.zeros(3, 0, dtype=torch.int32, device="cuda")
+    table = torch.full((3, 4000), -1, dtype=torch.int32, device="cuda")
+    lse = torch.full((3, 2, 8), -7.0, device="cuda")
+    assert sti.attn_paged(q[:0], pages, table[:0], start[:0], 1.0).shape == (0, 2, 8, 64)
+    sti.kv_append_paged(q[:0, :, 0], start[:0], pages, table[:0])
+    prev, prev_lse = torch.ones_like(q), torch.randn(3, 2, 8, device="cuda")
+    for pool, tab in ((pages, empty), (pages[:0], table)):
+        ws = sti.workspace(sti.attn_paged_workspace_size(3, 2, 8, 64))
+        assert (sti.attn_paged(q, pool, tab, start, 1.0, lse=lse, ws=ws) == 0).all() and (lse == float("-inf")).all()
+        assert sti.read_device_status(ws) == sti.FLAG_INDEX_RANGE
+        assert (sti.attn_paged(q, pool, tab, start, 1.0, lse=lse, prev_out=prev, prev_lse=prev_lse, ws=ws) == 1).all()
+        assert (lse == prev_lse).all()
+    ws = sti.workspace(sti.attn_paged_workspace_size(3, 2, 8, 64))
+    out = torch.full_like(q, 5)
+    lse.fill_(5)
+    sti.attn_paged(q, pages, table, start + 60000, 1.0, out=out, lse=lse, n_new=start, ws=ws)
+    assert (out == 5).all() and (lse == 5).all() and sti.read_device_status(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("rows", [40, 3000])
+def test_calls_follow_one_another(sti, rows):  # noqa: F811
+    """Rows appended, attended and the outputs rotated in one stream, again and again with other inputs and no wait in between:
+    each kernel sees all that the one before wrote."""
+    import torch
+
+    b, h, d, page = 5, 64, 512, 64
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    table = torch.randperm(b * (rows // page + 1), generator=g, device="cuda").int().view(b, -1)
+    f, start = sti.rope_freqs(64), torch.zeros(b, dtype=torch.int32, device="cuda")
+    at = torch.full((b,), rows - 1, dtype=torch.int32, device="cuda")
+    xs = [torch.randn(b, rows, d, generator=g, device="cuda").bfloat16() for _ in range(3)]
+    qs = [torch.randn(b, 1, h, d, generator=g, device="cuda").bfloat16() for _ in range(3)]
+    pages = torch.zeros(table.numel(), page, d, dtype=torch.bfloat16, device="cuda")
+    ws = sti.workspace(sti.attn_paged_workspace_size(b, 1, h, d))
+
+    def run(i, wait):
+        steps = (lambda _: sti.norm_rope(qs[i], at, f),
+                 lambda q: sti.kv_append_paged(xs[i], start, pages, table, f, norm=True) or q,
+                 lambda q: sti.attn_paged(q, pages, table, at, d ** -0.5, ws=ws),
+                 lambda o: sti.norm_rope(o, at, f, inverse=True, norm=False, out=o))
+        v = None
+        for step in steps:
+            v = step(v)
+            if wait:
+                torch.cuda.synchronize()
+        return v
+
+    want = [run(i, True) for i in range(3)]
+    got = [run(i % 3, False) for i in range(60)]
+    for i, o in enumerate(got):
+        assert (o == want[i % 3]).all(), i
