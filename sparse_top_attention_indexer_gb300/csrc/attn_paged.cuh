@@ -790,6 +790,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         float m_run = -INFINITY;                 // what P is relative to, in log2: lane l: head 32 set + l
         float l_thr[8];                          // running sums of the thread's heads over its rows
         uint32_t saw = 0;                        // bit i: its head i saw a row
+        bool unset = true;                       // a head of the set has no reference yet (the same in all of its warps)
 
         auto mwait = [&](uint64_t* bar, uint32_t parity) {
             if (!dead) dead = !warp_wait(bar, parity, p.status, abort);
@@ -875,8 +876,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     top1 = fmaxf(top1, fmaxf(y[4 * g + 2], y[4 * g + 3]));
                 }
             }
-            // the references stay unless a visible score passes its head's by 2^8
-            const bool need = !named_bar_and(bar_set, 128, !(first || ((kPack || v0) && top0 > kTopMost) || (v1 && top1 > kTopMost)));
+            // the references stay unless a visible score passes its head's by 2^8 or a head has none yet (of a run's first tile
+            // it may see no row: pages outside the pool)
+            const bool need = !named_bar_and(bar_set, 128, !(first || unset || ((kPack || v0) && top0 > kTopMost) || (v1 && top1 > kTopMost)));
             if (need) {
                 float* red = &tl->red[buf][set][qd][0];
                 float v[8];
@@ -892,6 +894,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float m_new = (m_run == -INFINITY || mt > m_run + kTopMost) ? fmaxf(m_run, mt) : m_run;
                 const float alpha = (m_new == m_run) ? 1.f : fast_exp2(m_run - m_new);
                 m_run = m_new;
+                unset = __any_sync(kWarpFull, m_new == -INFINITY && 32 * set + lane < run.heads);
                 __syncwarp();
                 // a head without any finite score keeps -inf; its exponents are taken from 0, so that NaN
                 // scores show in its output
@@ -963,7 +966,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float sk = sink * kLog2e, pl = prev_lse * kLog2e;
                 float mx = fmaxf(m_run, fmaxf(sk, pl));
                 if (mx == -INFINITY) mx = 0.f;
-                const float f = lt == 0.f ? 0.f : m_run == -INFINITY ? fast_exp2(-mx) : fast_exp2(m_run - mx);   // (inf * 0)
+                const float f = lt == 0.f ? 0.f : fast_exp2(m_run - mx);   // (without a reference lt is 0 or NaN)
                 const float ep = fast_exp2(pl - mx);
                 const float den = lt * f + fast_exp2(sk - mx) + ep;
                 const float over = __fdividef(1.f, den);
@@ -997,6 +1000,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) l_thr[i] = 0.f;
             saw = 0;
+            unset = false;
             for (int t = run.t0; t < run.t1; ++t, ++n)
                 if (active) softmax(run, t * kRows + row, t == run.t0);
             if (active) finish(run, sink, prev_lse);
@@ -1066,10 +1070,9 @@ __device__ __forceinline__ int2 split_of(const AttnPagedParams& p, int n) {
     const int c = p.by_query ? rec.x : (int)blockIdx.x;
     return rec.x >= 0 && rec.x < n && rec.y > c && rec.y < p.grid ? rec : make_int2(-1, 0);
 }
-// The factor of a part.  One of which the head sees nothing has a sum of -0 (and O = 0: not inf * 0).
-__device__ __forceinline__ float part_factor(const float2& ml, float mx) {
-    return ml.y == 0.f ? 0.f : exp2f((ml.x == -INFINITY ? 0.f : ml.x) - mx);
-}
+// The factor of a part.  One of which the head sees nothing has a sum of -0 and O = 0; one without a finite score has no
+// reference, and a sum of 0 or NaN.
+__device__ __forceinline__ float part_factor(const float2& ml, float mx) { return ml.y == 0.f ? 0.f : exp2f(ml.x - mx); }
 __device__ __forceinline__ void add4(float4& o, const float4& w, const float4& v) {
     o.x += w.x * v.x;
     o.y += w.y * v.y;

@@ -1,0 +1,46 @@
+"""The paged latent cache at its edges."""
+import numpy as np
+import pytest
+
+from tests._util import bf16_out_to_f64
+from tests.test_fp4_cache import sti  # noqa: F401  (the fixture)
+from tests.test_paged_cache import attend, attend_reference, check_attention, page_table
+from workloads import rng_for, to_bf16_bits
+
+gpu = pytest.mark.gpu
+
+
+def attention(b, s, h, d, page, rows, level=0.0, sink=None, prev_lse=None, seed=0):
+    """Queries after `rows` rows per sequence, every score about `level`."""
+    rng = rng_for(7600 + seed, b * s * h + d)
+    kv = rng.standard_normal((b, rows + s, d))
+    kv[..., 0] = -20 if level < 0 else 20
+    q = 0.1 * rng.standard_normal((b, s, h, d))
+    q[..., 0] = abs(level) * d ** 0.5 / 20
+    kv, q = to_bf16_bits(kv), to_bf16_bits(q)
+    table, n = page_table(rng, b, [-(-(rows + s) // page)] * b)
+    pool = np.zeros((n, page, d), np.uint16)
+    for i in range(b):
+        for p in range(rows + s):
+            pool[table[i, p // page], p % page] = kv[i, p]
+    a = dict(q=q, pool=pool, table=table, start=np.full(b, rows, np.int32), count=np.full(b, s, np.int32), n_new=None, window=0,
+             n_first=0, scale=d ** -0.5, kv=list(kv), sink=None if sink is None else np.full(h, sink, np.float32),
+             prev_out=None, prev_lse=None)
+    if prev_lse is not None:
+        a["prev_out"] = to_bf16_bits(rng.standard_normal((b, s, h, d)))
+        a["prev_lse"] = np.full((b, s, h), prev_lse, np.float32)
+    return a
+
+
+@gpu
+@pytest.mark.parametrize("level", [-120.0, 0.0, 100.0])
+@pytest.mark.parametrize("sink,prev_lse", [(None, None), (-200.0, None), (None, -200.0), (-118.0, -121.0)])
+@pytest.mark.parametrize("b,s,h,rows", [(2, 1, 64, 200), (2, 5, 6, 250), (3, 1, 40, 5000), (3, 3, 20, 5000)])
+def test_first_tile_of_bad_pages(sti, b, s, h, rows, sink, prev_lse, level):  # noqa: F811
+    """Every other tile lies in pages that the pool does not have, the first among them (in the cases of 5000 rows, the first
+    tile of every SM's two): the other rows' attention, however low their scores, the sink and the other part's lse are."""
+    a = attention(b, s, h, 64, 64, rows, level, sink, prev_lse)
+    a["table"][:, ::2] = [-1, a["pool"].shape[0]][h & 1]
+    out, lse, ws = attend(sti, a)
+    assert sti.read_device_status(ws) == sti.FLAG_INDEX_RANGE
+    check_attention(a, bf16_out_to_f64(out), lse.cpu().numpy().astype(np.float64), attend_reference(a, lambda i, p: p // 64 % 2 == 0))
