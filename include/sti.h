@@ -509,8 +509,9 @@ sti_status sti_rope_freqs(int rope_dims, double theta, double factor, int orig_l
  *   x, y: bf16 [b, seqlen, h, d], heads contiguous; sequences and tokens *_bstride and *_tstride elements apart
  *   pos: int32 [b], the position of each sequence's first token, or with pos_per_token int32 [b, seqlen]
  *   turns: uint64 [rope_dims/2] from sti_rope_freqs, on the device
- * y may be x itself (with the same strides); otherwise the two must not share elements (heads of one array of tokens
- * beside one another, as in a fused projection, do not).
+ * y may be x itself (with the same strides); otherwise the two must not share elements.  Parts of the same tokens beside one
+ * another, as in a fused projection, do not, in any order of sequences and tokens: where the memory from the first to the last
+ * element of one overlaps the other's, the strides have to be the same.
  * Supported: d a multiple of 8 up to 1024; rope_off and rope_dims multiples of 8 (rope_dims of 16 with STI_ROPE_HALVES);
  * x, y, weight 16-byte aligned, strides multiples of 8; b * seqlen * h < 2^31.
  */

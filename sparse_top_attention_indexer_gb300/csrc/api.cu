@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <utility>
 
 #include "sti.h"
 #include "sti_internal.h"
@@ -1176,6 +1177,25 @@ static bool rows_apart(int64_t bstride, int64_t tstride, int b, int s, int64_t n
     return b == 1 || (bstride >= (s - 1) * tstride + n) || (tstride >= (b - 1) * bstride + n && bstride >= n);
 }
 
+// Whether such rows share an element with the same ones `gap` elements further on: |gap + i*bstride - j*tstride| < n for an
+// |i| < b and a |j| < s.  For each i of the shorter index, the two j next to it.
+static bool shifted_rows_meet(int64_t gap, int64_t bstride, int64_t tstride, int b, int s, int64_t n) {
+    if (b > s) {
+        std::swap(b, s);
+        std::swap(bstride, tstride);
+    }
+    for (int64_t i = 1 - b; i < b; ++i) {
+        const int64_t at = gap + i * bstride, below = tstride > 0 ? at / tstride - (at < 0) : 0;
+        for (int64_t j : {below, below + 1}) {
+            if (j < 1 - s) j = 1 - s;
+            if (j > s - 1) j = s - 1;
+            const int64_t apart = at - j * tstride;
+            if (apart > -n && apart < n) return true;
+        }
+    }
+    return false;
+}
+
 sti_status sti_norm_rope(const uint16_t* x, int64_t x_bstride, int64_t x_tstride, const int32_t* pos, int pos_per_token,
                          const int32_t* n_new, int b, int seqlen, int h, int d, int norm, const uint16_t* weight,
                          float eps, const uint64_t* turns, int rope_dims, int rope_off, int rope_flags,
@@ -1195,9 +1215,7 @@ sti_status sti_norm_rope(const uint16_t* x, int64_t x_bstride, int64_t x_tstride
         auto extent = [&](int64_t bs, int64_t ts) { return (size_t)((b - 1) * bs + (seqlen - 1) * ts + n) * 2; };
         if (overlap(x, extent(x_bstride, x_tstride), y, extent(y_bstride, y_tstride))) {
             // fine where they are parts of the same tokens that lie apart in each
-            if (!same || seqlen < 2 || (b > 1 && x_bstride % x_tstride != 0)) return STI_ERR_INVALID_ARG;
-            const int64_t gap = (y > x ? y - x : x - y) % x_tstride;
-            if (gap < n || x_tstride - gap < n) return STI_ERR_INVALID_ARG;
+            if (!same || shifted_rows_meet(y - x, y_bstride, y_tstride, b, seqlen, n)) return STI_ERR_INVALID_ARG;
         }
     }
     p.pos_per_token = pos_per_token != 0;

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from tests._util import bf16_out_to_f64
-from tests.test_fp4_cache import sti  # noqa: F401  (the fixture)
+from tests.test_fp4_cache import FAKE, P, lib, sti  # noqa: F401  (fixtures among them)
 from tests.test_paged_cache import attend, attend_reference, check_attention, page_table
 from workloads import rng_for, to_bf16_bits
 
@@ -44,3 +44,45 @@ def test_first_tile_of_bad_pages(sti, b, s, h, rows, sink, prev_lse, level):  # 
     out, lse, ws = attend(sti, a)
     assert sti.read_device_status(ws) == sti.FLAG_INDEX_RANGE
     check_attention(a, bf16_out_to_f64(out), lse.cpu().numpy().astype(np.float64), attend_reference(a, lambda i, p: p // 64 % 2 == 0))
+
+
+@gpu
+@pytest.mark.parametrize("b,s,tokens_first", [(3, 1, False), (32, 1, False), (3, 5, True), (3, 1, True), (1, 4, True), (1, 1, False)])
+def test_rotate_between_slices(sti, b, s, tokens_first):  # noqa: F811
+    """From one part of a fused projection into another of the same tokens, for a prompt, a single token and tokens outermost."""
+    import torch
+
+    h, d = 6, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    freqs, pos = sti.rope_freqs(32), torch.arange(b, dtype=torch.int32, device="cuda")
+    first, second = (s, b) if tokens_first else (b, s)
+    whole = torch.randn(first, second, 3 * h * d, generator=g, device="cuda").bfloat16()
+    qkv = whole.transpose(0, 1) if tokens_first else whole
+    part = lambda t, i: t[..., i * h * d:(i + 1) * h * d].unflatten(-1, (h, d))  # noqa: E731
+    for src, dst in ((0, 2), (0, 1), (2, 1)):
+        keep = qkv.clone()
+        want = sti.norm_rope(part(keep, src).contiguous(), pos, freqs)
+        sti.norm_rope(part(qkv, src), pos, freqs, out=part(qkv, dst))
+        assert (part(qkv, dst) == want).all()
+        for i in {0, 1, 2} - {dst}:
+            assert (part(qkv, i) == part(keep, i)).all()
+
+
+def test_rotate_onto_itself_refused(lib):  # noqa: F811
+    """Parts that share elements, by every order of the strides: refused."""
+    h, d = 4, 64
+    n = h * d
+
+    def call(b, s, bs, ts, off):
+        return lib.sti_norm_rope(P(FAKE), bs, ts, P(FAKE), 0, None, b, s, h, d, 1, None, 1e-6, P(FAKE), 32, 32, 0, 1.0,
+                                 P(FAKE + 2 * off), bs, ts, None)
+
+    for b, s, bs, ts in ((3, 1, 3 * n, n), (3, 5, 15 * n, 3 * n), (3, 5, 3 * n, 9 * n), (1, 5, 0, 3 * n), (1, 1, n, n),
+                         (3, 2, 7 * n, 3 * n)):
+        apart = {i * bs + j * ts for i in range(1 - b, b) for j in range(1 - s, s)}
+        tried = 0
+        for off in {at + k for at in apart for k in (8 - n, -8, 0, 8, n - 8)}:
+            if off > 0:
+                assert call(b, s, bs, ts, off) == 1, (b, s, bs, ts, off)
+                tried += 1
+        assert tried >= 2
