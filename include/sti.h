@@ -485,7 +485,8 @@ sti_status sti_kv_evict(float *row_weight, int64_t row_weight_bstride, int32_t *
  * The cache: pages, bf16 [n_pages, page_size, d] with contiguous rows, page i at pages + i*page_stride (elements); table,
  * int32 [b, max_pages], sequence b at table + b*table_stride: position p of the sequence is row p % page_size of page
  * table[b, p / page_size].  Entries of positions that a call does not need are not read.  A page outside [0, n_pages)
- * or a position past the table raises STI_FLAG_INDEX_RANGE; such rows are not written, and not seen.
+ * or a position past the table raises STI_FLAG_INDEX_RANGE; such rows are not written, and not seen.  max_pages may be 0 (table
+ * unused).
  *
  * sti_rope_freqs: the frequencies of a rotation of rope_dims dims, computed on the host into `turns` (HOST, uint64
  * [rope_dims/2]; the caller copies it to the device once): pair i turns by f_i = theta^(-2i/rope_dims) radians per

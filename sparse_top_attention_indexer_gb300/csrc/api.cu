@@ -1228,7 +1228,7 @@ sti_status sti_norm_rope(const uint16_t* x, int64_t x_bstride, int64_t x_tstride
 
 static bool pages_ok(const uint16_t* pages, int64_t page_stride, int n_pages, int page_size, int d, const int32_t* table,
                      int64_t table_stride, int max_pages, int b) {
-    if (!table || (b > 1 && table_stride < max_pages)) return false;
+    if (max_pages > 0 && (!table || (b > 1 && table_stride < max_pages))) return false;
     return n_pages == 0 || (pages && aligned(pages, 16) && page_stride % 8 == 0 && page_stride >= (int64_t)page_size * d);
 }
 

@@ -86,3 +86,17 @@ def test_rotate_onto_itself_refused(lib):  # noqa: F811
                 assert call(b, s, bs, ts, off) == 1, (b, s, bs, ts, off)
                 tried += 1
         assert tried >= 2
+
+
+@gpu
+def test_append_to_a_table_of_no_pages(sti):  # noqa: F811
+    """A table without columns: every position is past it, nothing is written, and it is reported."""
+    import torch
+
+    x = torch.randn(2, 3, 64, device="cuda").bfloat16()
+    pages = torch.full((4, 16, 64), -7.0, dtype=torch.bfloat16, device="cuda")
+    start, empty = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, 0, dtype=torch.int32, device="cuda")
+    ws = sti.workspace(256)
+    sti.kv_append_paged(x, start, pages, empty, ws=ws)
+    assert sti.read_device_status(ws) == sti.FLAG_INDEX_RANGE
+    assert (pages == -7).all()
