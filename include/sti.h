@@ -545,7 +545,8 @@ sti_status sti_kv_append_paged(const uint16_t *x, int64_t x_bstride, int64_t x_t
  *   out[b,t,h,:] = ( sum_p e^{s_hp} row_p + e^{prev_lse} prev_out[b,t,h,:] ) / e^{L_h},   lse = L_h
  * A query that sees no row (bad pages): out = prev_out and lse = prev_lse, or 0 and -inf without them, as in
  * sti_attn_fp4kv.  Rows that no query of the call sees may hold anything, NaN included; a query that sees a row holding
- * an infinity or NaN has an undefined output, which does not reach queries that do not see it.
+ * an infinity or NaN has an undefined output, which does not reach queries that do not see it.  A score below fp32's range has no
+ * weight; one above it leaves its head's output undefined.
  *   q, out: bf16 [b, seqlen, h, d]; lse: fp32 [b, seqlen, h] or NULL; attn_sink, prev_out, prev_lse: as sti_attn_fp4kv
  * out may be prev_out itself; otherwise the outputs must not overlap the inputs.
  * bf16 tensor-core MMAs with fp32 accumulation, P rounded to bf16 for the PV product, fp32 online softmax.  Results do not

@@ -191,8 +191,14 @@ __device__ __forceinline__ void load_turned(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
-// Two bf16, an infinity or NaN as 0.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t v) { return v & ~__vcmpeq2(v & 0x7F807F80u, 0x7F807F80u); }
+// Two bf16, an infinity or NaN as -2^-133 (kCleared); cleared: whether there is one such, or there was.  (Both sets of heads look
+// at a row, in any order, and have to find the same.)
+constexpr uint32_t kCleared = 0x80018001u;
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v, bool& cleared) {
+    const uint32_t is = __vcmpeq2(v & 0x7F807F80u, 0x7F807F80u);
+    cleared = cleared || (is | __vcmpeq2(v, kCleared)) != 0;
+    return (v & ~is) | (kCleared & is);
+}
 
 // Which rows of the group's list head hd sees: i < n - (v >> 8), and i >= nf + (v & 255) or i < n_first (row i < n_first is
 // position i; queries of a group are at most 63 positions apart).
@@ -806,16 +812,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 nm[2 * g + 1] = v.y;
             }
         };
-        auto clear_rows = [&](uint32_t buf, bool first, bool second) {   // the thread's quarter of its rows
+        auto clear_row = [&](uint8_t* at) {      // its column blocks l4, l4 + 4: whether it holds (or held) an infinity or NaN
+            bool cleared = false;
 #pragma unroll 1
             for (int cb = l4; cb < n_cb; cb += 4)
 #pragma unroll 1
-                for (int k = 0; k < 16; ++k) {
-                    if (!(k < 8 ? first : second)) continue;
-                    uint4* at = reinterpret_cast<uint4*>(t_s + buf * kTile + (size_t)cb * kTBlk + (row + (k & 8)) * 128 + 16 * (k & 7));
-                    const uint4 v = *at;
-                    *at = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+                for (int k = 0; k < 8; ++k) {
+                    uint4* piece = reinterpret_cast<uint4*>(at + (size_t)cb * kTBlk + 16 * k);
+                    const uint4 v = *piece;
+                    const uint4 w = make_uint4(finite_pair(v.x, cleared), finite_pair(v.y, cleared), finite_pair(v.z, cleared),
+                                               finite_pair(v.w, cleared));
+                    *piece = w;
                 }
+            return cleared;
         };
         int hv[8] = {};              // kPack: which rows each of the thread's heads sees
         // i0: this thread's first row of the list
@@ -837,19 +846,27 @@ __global__ void __launch_bounds__(kPThreads, 1)
             };
             tmem_ld_wait();
             if (kPack) {
-                // A row with an infinity or NaN has such scores with every head: NaN for those that see it, and zeros in
-                // their place in the tile, so that P = 0 keeps them from the others.
+                // A row with an infinity or NaN has such scores with every head: NaN for those that see it, and something finite in
+                // their place in the tile, so that P = 0 keeps them from the others.  (A finite row's score may pass fp32 too.)
                 bool bad0 = false, bad1 = false;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const bool b = (r[k] & 0x7F800000u) == 0x7F800000u;
-                    if (b) r[k] = 0x7FFFFFFFu;
                     if (k & 2) bad1 = bad1 || b;
                     else bad0 = bad0 || b;
                 }
                 if (__any_sync(kWarpFull, bad0 || bad1)) {
                     mwait(&tl->full[buf][kHalves - 1], (n >> 1) & 1u);   // (complete: makes the rows visible)
-                    clear_rows(buf, bad0, bad1);
+                    auto holds = [&](bool bad, int at) {   // four lanes have a quarter of the row each
+                        const uint32_t lanes = 0xFu << (lane & 28);
+                        const bool look = (__ballot_sync(kWarpFull, bad) & lanes) != 0;
+                        return (__ballot_sync(kWarpFull, look && clear_row(t_s + buf * kTile + at * 128)) & lanes) != 0;
+                    };
+                    bad0 = holds(bad0, row);
+                    bad1 = holds(bad1, row + 8);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        if (k & 2 ? bad1 : bad0) r[k] = 0x7FFFFFFFu;
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) saw |= (sees(i, 0) || sees(i, 1)) ? 1u << i : 0u;

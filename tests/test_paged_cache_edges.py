@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from tests._util import bf16_out_to_f64
+from tests._util import bf16_out_to_f64, to_dev
 from tests.test_fp4_cache import FAKE, P, lib, sti  # noqa: F401  (fixtures among them)
 from tests.test_paged_cache import attend, attend_reference, check_attention, page_table
 from workloads import rng_for, to_bf16_bits
@@ -100,3 +100,44 @@ def test_append_to_a_table_of_no_pages(sti):  # noqa: F811
     sti.kv_append_paged(x, start, pages, empty, ws=ws)
     assert sti.read_device_status(ws) == sti.FLAG_INDEX_RANGE
     assert (pages == -7).all()
+
+
+@gpu
+@pytest.mark.parametrize("s,h", [(1, 64), (4, 4), (4, 16), (7, 9)])
+def test_scores_past_fp32(sti, s, h):  # noqa: F811
+    """A finite row whose scores are below fp32's range has no weight, with few heads as with many."""
+    a = attention(1, s, h, 128, 16, 90, seed=1)
+    q, kv = a["q"], a["kv"][0]
+    q[..., 0] = to_bf16_bits(np.array([1e20]))[0]
+    kv[:, 0] = 0
+    kv[37, 0] = kv[70, 0] = to_bf16_bits(np.array([-1e20]))[0]
+    kv[70, 1] = to_bf16_bits(np.array([3e38]))[0]
+    q[..., 1] = to_bf16_bits(np.array([-2.0]))[0]
+    kv[np.arange(len(kv)) != 70, 1] = 0
+    for p in range(len(kv)):
+        a["pool"][a["table"][0, p // 16], p % 16] = kv[p]
+    out, lse, ws = attend(sti, a)
+    assert sti.read_device_status(ws) == 0
+    check_attention(a, bf16_out_to_f64(out), lse.cpu().numpy().astype(np.float64),
+                    attend_reference(a, lambda i, p: (p == 37) | (p == 70)))
+
+
+@gpu
+@pytest.mark.parametrize("s,h", [(4, 4), (8, 8), (2, 32)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_non_finite_rows_of_one_sign(sti, s, h, value):  # noqa: F811
+    """Queries that share tiles with one that sees a row with an infinity or NaN, all scores with it of one sign: those that see
+    it have an undefined output, every head of theirs, the others what they had without it."""
+    import torch
+
+    a = attention(1, s, h, 128, 16, 90, seed=2)
+    q, pages = to_dev(a["q"]), to_dev(a["pool"])
+    table, start = torch.from_numpy(a["table"]).cuda(), torch.tensor([90], dtype=torch.int32, device="cuda")
+    q[..., 7] = -3.0
+    want = sti.attn_paged(q, pages, table, start, a["scale"])
+    at = 90 + s // 2
+    pages[int(table[0, at // 16]), at % 16, 7] = value
+    got = [sti.attn_paged(q, pages, table, start, a["scale"]) for _ in range(5)]
+    for o in got:
+        assert (o[0, :s // 2] == want[0, :s // 2]).all()
+        assert o[0, s // 2:].isnan().any(-1).all()
