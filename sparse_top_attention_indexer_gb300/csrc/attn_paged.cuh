@@ -134,6 +134,7 @@ struct __align__(16) Tail {
     uint32_t tmem_base;
     int abort;
     int qk_tile;              // tiles whose QK was issued, for the prefetching warp
+    int list_done;            // the list's warp publishes no more runs
 };
 
 // One barrier per thread.
@@ -428,6 +429,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         tma_prefetch_desc(&tm_q);
         tl->abort = 0;
         tl->qk_tile = 0;
+        tl->list_done = 0;
     }
     if (n_cb & 1)   // the dims past d of the last d-block, which no copy writes
         for (int i = tid; i < 3 * (int)kTBlk / 16; i += kPThreads) {
@@ -452,11 +454,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t tmem = __shfl_sync(kWarpFull, tl->tmem_base, 0);   // warp-uniform, as the compiler can see
     griddep_launch_dependents();
 
-    // The next run for this warp (false: none, or a wait gave up).
+    // The next run for this warp (false: none, or a wait gave up).  The softmax warps meet at barriers, so they take the same runs
+    // whatever waits gave up: all that the list's warp publishes before it ends (which is well before their own limit).
     uint32_t runs = 0;
-    auto next_run = [&](Run& r) {
+    auto next_run = [&](Run& r, bool together = false) {
         const uint32_t k = runs % kRuns;
-        if (!warp_wait(&tl->run_full[k], runs / kRuns & 1u, p.status, abort)) return false;
+        if (!(together ? warp_wait<true>(&tl->run_full[k], runs / kRuns & 1u, p.status, &tl->list_done, 4 * STI_WAIT_TIMEOUT_NS)
+                       : warp_wait(&tl->run_full[k], runs / kRuns & 1u, p.status, abort)))
+            return false;
         r = tl->run[k];
         __syncwarp();
         if (lane == 0) mbar_arrive(&tl->run_empty[k]);
@@ -606,7 +611,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 off = 0;
                 n += (uint32_t)(run.t1 - run.t0);
             }
-            if (lane == 0 && !p.by_query) p.rec[blockIdx.x] = rec;
+            __syncwarp();
+            if (lane == 0) {
+                *static_cast<volatile int*>(&tl->list_done) = 1;
+                if (!p.by_query) p.rec[blockIdx.x] = rec;
+            }
             // One query group per sequence: of the last runs (a long list's CTA has no more), a tile's rows set out for L2 as soon as
             // the tile before is being copied, for HBM to be kept busy: 32 queries over 16384 rows 102 us, without it 110; two
             // tiles ahead 104, five 117, as what was asked for is dropped from L2 before its turn.  (Several groups find each other's
@@ -1002,7 +1011,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int hh = 32 * set + lane;
         const float sink = p.sink && hh < hp ? __ldg(p.sink + hh % p.h) : -INFINITY;
         uint32_t par = 0;                      // run parity
-        while (next_run(run)) {
+        while (next_run(run, true)) {
             const float prev_lse = p.prev_lse && qd == 0 && hh < run.heads ? __ldg(p.prev_lse + run.row0 + hh) : -INFINITY;
             if (kPack) {
                 if (tid < 64) tl->vis[par][tid] = head_vis(p, run, tid);   // (every warp is done with par's last)

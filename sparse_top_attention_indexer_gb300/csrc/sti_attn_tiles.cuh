@@ -51,15 +51,18 @@ __device__ __forceinline__ void regs_down() {
 // A wait by parity passes at once when the phase before the awaited one is still open, so every waiter here comes after
 // that phase: most wait for a barrier's phases in order; those that wait for freed[.] of some tile n alone
 // have seen S^T of n, whose tile was decoded after freed[.] of n - 2.
-__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
+// kLast: the barrier is looked at once more after `abort`, which says that nobody arrives any more.
+template <bool kLast = false>
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort,
+                                          uint64_t limit_ns = STI_WAIT_TIMEOUT_NS) {
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 255u) == 0u) {
-            if (*abort) return false;
+            if (*abort) return kLast && mbar_try_wait(bar, parity);
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
-            else if (now - t0 > STI_WAIT_TIMEOUT_NS) {
+            else if (now - t0 > limit_ns) {
                 if (status) atomicOr(status, 2u /* STI_FLAG_TIMEOUT */);
                 *abort = 1;
                 return false;
@@ -70,8 +73,10 @@ __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, uint32
 
 // tile_wait for a converged warp.  The vote makes the result visibly warp-uniform; without it the compiler
 // treats what follows as divergent, and the MMAs of the issuing warp take three times as long to issue.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort) {
-    return __all_sync(kWarpFull, tile_wait(bar, parity, status, abort));
+template <bool kLast = false>
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status, volatile int* abort,
+                                          uint64_t limit_ns = STI_WAIT_TIMEOUT_NS) {
+    return __all_sync(kWarpFull, tile_wait<kLast>(bar, parity, status, abort, limit_ns));
 }
 
 // One lane of the (converged) warp.
