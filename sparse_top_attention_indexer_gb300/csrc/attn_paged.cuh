@@ -90,6 +90,8 @@ constexpr int kOutWarp = 8, kLoadWarp = 16, kQkWarp = 20, kPvWarp = 21, kListWar
 constexpr int kRegsSoft = 104, kRegsOut = 72, kRegsLoad = 64, kRegsMma = 64;
 constexpr float kTopMost = 8.f;                // log2 of the largest P before its reference moves
 constexpr uint32_t kStage = 1024;              // 16 heads x 32 dims of bf16
+constexpr uint64_t kRunWaitNs = 1ull << 37;    // 137 s: limit of the waits that last as long as a list, of 2^24 tiles at most (25 s);
+                                               // those for a tile have 1 s, and one that runs out ends all
 constexpr uint32_t kBarSoft = 3;               // named barriers: 1, 2 the head groups, 3 all softmax warps
 
 // A run of one group's tiles, as the list's warp publishes it.
@@ -459,8 +461,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     uint32_t runs = 0;
     auto next_run = [&](Run& r, bool together = false) {
         const uint32_t k = runs % kRuns;
-        if (!(together ? warp_wait<true>(&tl->run_full[k], runs / kRuns & 1u, p.status, &tl->list_done, 4 * STI_WAIT_TIMEOUT_NS)
-                       : warp_wait(&tl->run_full[k], runs / kRuns & 1u, p.status, abort)))
+        if (!(together ? warp_wait<true>(&tl->run_full[k], runs / kRuns & 1u, p.status, &tl->list_done, 4 * kRunWaitNs)
+                       : warp_wait(&tl->run_full[k], runs / kRuns & 1u, p.status, abort, kRunWaitNs)))
             return false;
         r = tl->run[k];
         __syncwarp();
@@ -474,8 +476,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int n_mma = (hp + 15) / 16 * 16;
         uint32_t n = 0;
         bool ok = true;   // the whole warp waits, one elected lane issues (so the operands stay warp-uniform)
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = warp_wait(bar, parity, p.status, abort);
+        auto wait = [&](uint64_t* bar, uint32_t parity, uint64_t limit_ns = STI_WAIT_TIMEOUT_NS) {
+            ok = warp_wait(bar, parity, p.status, abort, limit_ns);
             tc_fence_after();
             return ok;
         };
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     nt = 0;
                 }
                 const uint32_t k = runs % kRuns;
-                if (runs >= kRuns && !wait(&tl->run_empty[k], runs / kRuns - 1 & 1u)) break;
+                if (runs >= kRuns && !wait(&tl->run_empty[k], runs / kRuns - 1 & 1u, kRunWaitNs)) break;
                 ++runs;
                 run.t0 = run.t1 = 0;
                 if (nt > 0) {
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // box, a Q takes some 3000 cycles to come).
             while (ok && next_run(run)) {
                 for (int h = 0; h < kHalves && ok; ++h) {
-                    if (runs > 1 && !wait(&tl->q_free[h], runs & 1u)) break;
+                    if (runs > 1 && !wait(&tl->q_free[h], runs & 1u, kRunWaitNs)) break;
                     // rows past the group's heads are other queries', or zeros past the last: columns of S^T that nothing uses
                     if (elect_one()) {
                         const int cb1 = min(n_cb, 4 * h + 4);
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         Run run;
         while (next_run(run)) {
             const uint32_t r = runs - 1, k = r % kRuns;
-            if (!warp_wait(&tl->fac_full[k], r / kRuns & 1u, p.status, abort)) break;
+            if (!warp_wait(&tl->fac_full[k], r / kRuns & 1u, p.status, abort, kRunWaitNs)) break;
             if (!warp_wait(&tl->o_full[k], r / kRuns & 1u, p.status, abort)) break;
             tc_fence_after();
             auto read = [&](int half) {   // of O

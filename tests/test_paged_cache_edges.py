@@ -141,3 +141,29 @@ def test_non_finite_rows_of_one_sign(sti, s, h, value):  # noqa: F811
     for o in got:
         assert (o[0, :s // 2] == want[0, :s // 2]).all()
         assert o[0, s // 2:].isnan().any(-1).all()
+
+
+@gpu
+@pytest.mark.parametrize("tokens", [True, False])
+def test_lists_of_seconds(sti, tokens):  # noqa: F811
+    """As many queries as SMs, each over 268 million rows, all but the last page's the same page of zeros: two seconds of one CTA
+    per query, longer than any wait for a single tile may take.  The last page has all of the weight: the others' rows have e^-40 of
+    a row's there each, 2 10^-9 together."""
+    import torch
+
+    n = torch.cuda.get_device_properties(0).multi_processor_count
+    b, s = (1, n) if tokens else (n, 1)
+    h, d, page, most = 64, 64, 8192, 32768
+    a = attention(1, s, h, d, page, 200, 40.0, seed=3)      # what is seen of the last page
+    q = to_dev(a["q"]).expand(b, s, h, d).contiguous()
+    pages = torch.zeros(2, page, d, dtype=torch.bfloat16, device="cuda")
+    pages[1] = to_dev(a["pool"])[int(a["table"][0, 0])]
+    table = torch.zeros(b, most, dtype=torch.int32, device="cuda")
+    table[:, -1] = 1
+    start = torch.full((b,), (most - 1) * page + 200, dtype=torch.int32, device="cuda")
+    ws, lse = sti.workspace(sti.attn_paged_workspace_size(b, s, h, d)), torch.empty(b, s, h, device="cuda")
+    out = sti.attn_paged(q, pages, table, start, a["scale"], lse=lse, ws=ws)
+    assert sti.read_device_status(ws) == 0
+    ref = attend_reference(a)
+    for i in {0, b // 2, b - 1}:
+        check_attention(a, bf16_out_to_f64(out[i:i + 1]), lse[i:i + 1].cpu().numpy().astype(np.float64), ref)
