@@ -1014,7 +1014,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const float sink = p.sink && hh < hp ? __ldg(p.sink + hh % p.h) : -INFINITY;
         uint32_t par = 0;                      // run parity
         while (next_run(run, true)) {
-            const float prev_lse = p.prev_lse && qd == 0 && hh < run.heads ? __ldg(p.prev_lse + run.row0 + hh) : -INFINITY;
+            // (not by __ldg: the kernel before, which may have written it, can still run when this one starts)
+            const float prev_lse = p.prev_lse && qd == 0 && hh < run.heads ? __ldcg(p.prev_lse + run.row0 + hh) : -INFINITY;
             if (kPack) {
                 if (tid < 64) tl->vis[par][tid] = head_vis(p, run, tid);   // (every warp is done with par's last)
                 named_bar_sync(kBarSoft, 256);

@@ -167,3 +167,37 @@ def test_lists_of_seconds(sti, tokens):  # noqa: F811
     ref = attend_reference(a)
     for i in {0, b // 2, b - 1}:
         check_attention(a, bf16_out_to_f64(out[i:i + 1]), lse[i:i + 1].cpu().numpy().astype(np.float64), ref)
+
+
+@gpu
+@pytest.mark.parametrize("s,h", [(1, 64), (3, 10)])
+def test_joined_calls_follow_one_another(sti, s, h):  # noqa: F811
+    """Two parts of a context attended one after the other, the second joined with the first, again and again into the same buffers
+    with other queries, lengths and pages each time and no wait in between: what calls with waits give."""
+    import torch
+
+    b, d, page = 6, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(s)
+    pages = torch.randn(2, 60, page, d, generator=g, device="cuda").bfloat16()
+    qs = [torch.randn(b, s, h, d, generator=g, device="cuda").bfloat16() for _ in range(4)]
+    starts = [torch.randint(0, 600, (b,), generator=g, device="cuda", dtype=torch.int32) for _ in range(4)]
+    tables = [torch.randint(0, 60, (b, 10), generator=g, device="cuda", dtype=torch.int32) for _ in range(4)]
+    q, start, table = qs[0].clone(), starts[0].clone(), tables[0].clone()
+    part, lse = torch.empty_like(q), torch.empty(b, s, h, device="cuda")
+    ws = sti.workspace(sti.attn_paged_workspace_size(b, s, h, d))
+    f = sti.rope_freqs(64)
+
+    def step(i, wait=lambda: None):
+        for to, one in ((q, qs[i]), (start, starts[i]), (table, tables[i])):
+            to.copy_(one)
+        wait()
+        sti.norm_rope(q, start, f, out=q)
+        wait()
+        sti.attn_paged(q, pages[0], table, start, d ** -0.5, out=part, lse=lse, ws=ws)
+        wait()
+        return sti.attn_paged(q, pages[1], table, start, d ** -0.5, prev_out=part, prev_lse=lse, ws=ws)
+
+    want = [step(i, torch.cuda.synchronize) for i in range(4)]
+    got = [step(i % 4) for i in range(80)]
+    for i, o in enumerate(got):
+        assert (o == want[i % 4]).all(), i
