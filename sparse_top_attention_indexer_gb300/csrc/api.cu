@@ -1261,18 +1261,20 @@ sti_status sti_kv_append_paged(const uint16_t* x, int64_t x_bstride, int64_t x_t
     return e == cudaSuccess ? STI_OK : cuda_fail(e, "sti_kv_append_paged");
 }
 
-// attention workspace: [status | split records | partial (max, sum) | partial outputs], of the attention over the fp4
-// cache with the largest grid
+// paged attention's workspace: [status | split records | partial (max, sum) | partial outputs]: a record per CTA (or per query, where
+// there are no more of them), two parts per CTA.  For the most CTAs that a plan may have, whatever the lengths and the GPU: no
+// call launches more than kAttnFp4MaxSms.
 struct AttnPagedLayout {
     size_t rec, ml, o, end;
 };
 static AttnPagedLayout attn_paged_layout(int b, int seqlen, int h, int d) {
     AttnPagedLayout l;
-    const sti::AttnPagedPlan pl = sti::attn_paged_plan(b, seqlen, h, d, kMaxCacheRows, 0, 0, kAttnFp4MaxSms);
+    const int pack = sti::attn_paged_plan(b, seqlen, h, d, 0, 0, 0, kAttnFp4MaxSms).pack;
+    constexpr size_t grid = kAttnFp4MaxSms;
     l.rec = sti::kWsStatusBytes;
-    l.ml = sti::align_up(l.rec + (size_t)pl.grid * sizeof(int2), sti::kWsAlign);
-    l.o = sti::align_up(l.ml + (size_t)2 * pl.grid * 64 * sizeof(float2), sti::kWsAlign);
-    l.end = sti::align_up(l.o + (size_t)2 * pl.grid * ((pl.pack * h + 3) / 4 * 4) * d * sizeof(float), sti::kWsAlign);
+    l.ml = sti::align_up(l.rec + grid * sizeof(int2), sti::kWsAlign);
+    l.o = sti::align_up(l.ml + 2 * grid * 64 * sizeof(float2), sti::kWsAlign);
+    l.end = sti::align_up(l.o + 2 * grid * ((pack * h + 3) / 4 * 4) * d * sizeof(float), sti::kWsAlign);
     return l;
 }
 

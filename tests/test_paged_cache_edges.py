@@ -201,3 +201,16 @@ def test_joined_calls_follow_one_another(sti, s, h):  # noqa: F811
     got = [step(i % 4) for i in range(80)]
     for i, o in enumerate(got):
         assert (o == want[i % 4]).all(), i
+
+
+def test_workspace_sizes(lib):  # noqa: F811
+    """Room for a record and two parts (maximum and sum of 64 heads, outputs of the heads that share tiles) of each of the 160 CTAs
+    that a call has at most, for every number of sequences, tokens and heads."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    for b in (1, 2, 7, 150, 4096):
+        for s in (1, 2, 5, 63, 64, 2048):
+            for h in (1, 2, 3, 5, 16, 20, 31, 32, 33, 57, 64):
+                for d in (64, 192, 512):
+                    heads = h * (min(64 // h, s) if h <= 32 else 1)
+                    want = 256 + up(160 * 8) + up(320 * 64 * 8) + up(320 * (-(-heads // 4) * 4) * d * 4)
+                    assert lib.sti_attn_paged_workspace_size(b, s, h, d) == want, (b, s, h, d)
