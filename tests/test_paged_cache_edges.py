@@ -4,8 +4,8 @@ import pytest
 
 from tests._util import bf16_out_to_f64, to_dev
 from tests.test_fp4_cache import FAKE, P, lib, sti  # noqa: F401  (fixtures among them)
-from tests.test_paged_cache import attend, attend_reference, check_attention, page_table
-from workloads import rng_for, to_bf16_bits
+from tests.test_paged_cache import attend, attend_reference, check_attention, page_table, seen_by
+from workloads import bf16_bits_to_f32, rng_for, to_bf16_bits
 
 gpu = pytest.mark.gpu
 
@@ -214,3 +214,41 @@ def test_workspace_sizes(lib):  # noqa: F811
                     heads = h * (min(64 // h, s) if h <= 32 else 1)
                     want = 256 + up(160 * 8) + up(320 * 64 * 8) + up(320 * (-(-heads // 4) * 4) * d * 4)
                     assert lib.sti_attn_paged_workspace_size(b, s, h, d) == want, (b, s, h, d)
+
+
+@gpu
+@pytest.mark.parametrize("b,s,h,d,window", [(3, 1, 64, 512, 128), (2, 4, 64, 128, 40), (2, 9, 16, 64, 20)])
+def test_joined_with_selected_rows(sti, b, s, h, d, window):  # noqa: F811
+    """A layer's attention over the rows that the indexer chose (with the sink), joined with a window of the paged cache, one query
+    without any chosen row: the attention over both.  Rounded to bf16: P in both kernels (2^-8 of each row's share), the first one's
+    output (2^-8 of its share) and the output; the first one's lse is off by at most 1e-4 (1 + |lse|), as its own tests hold it to."""
+    import torch
+
+    rng = rng_for(7700, b * s * h + d)
+    a = attention(b, s, h, d, 16, 60, seed=4)
+    a.update(window=window, n_first=2, q=to_bf16_bits(2 * rng.standard_normal((b, s, h, d))))
+    sink = rng.standard_normal(h).astype(np.float32)
+    rows, k = 300, 96
+    chosen = to_bf16_bits(rng.standard_normal((b, rows, d)))
+    idx = np.stack([[rng.permutation(rows)[:k] for _ in range(s)] for _ in range(b)]).astype(np.int32)
+    idx[..., k - 5:] = -1
+    idx[b - 1, s - 1] = -1
+    part_lse = torch.empty(b, s, h, device="cuda")
+    q = to_dev(a["q"])
+    part = sti.sparse_attn_sink(q, to_dev(chosen), torch.from_numpy(sink).cuda(), torch.from_numpy(idx).cuda(), a["scale"], lse=part_lse)
+    assert (part_lse[b - 1, s - 1] == float("-inf")).all()
+    out, lse, ws = attend(sti, a, prev_out=part, prev_lse=part_lse)
+    assert sti.read_device_status(ws) == 0
+    got, got_lse = bf16_out_to_f64(out), lse.cpu().numpy().astype(np.float64)
+    qf, scale = bf16_bits_to_f32(a["q"]).astype(np.float64), a["scale"]
+    for i in range(b):
+        for t in range(s):
+            p = np.nonzero(seen_by(60 + t, window, 2))[0]
+            one = idx[i, t][idx[i, t] >= 0]
+            kv = bf16_bits_to_f32(np.concatenate([a["kv"][i][p], chosen[i][one]])).astype(np.float64)
+            e = np.exp(scale * qf[i, t] @ kv.T)
+            total = e.sum(1) + (np.exp(sink.astype(np.float64)) if len(one) else 0)
+            want, mass, L = e @ kv / total[:, None], e @ np.abs(kv) / total[:, None], np.log(total)
+            assert (np.abs(got_lse[i, t] - L) <= 2e-4 * (1 + np.abs(L))).all()
+            off = 2.0 ** -8 * np.abs(want) + (2.0 ** -7 + 2e-4 * (1 + np.abs(L[:, None]))) * mass
+            assert (np.abs(got[i, t] - want) <= off).all()
