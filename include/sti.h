@@ -506,7 +506,7 @@ sti_status sti_rope_freqs(int rope_dims, double theta, double factor, int orig_l
  *   (y_a, y_b) <- rope_gain (y_a cos - y_b sin, y_b cos + y_a sin)
  * pairs (2i, 2i+1), with STI_ROPE_HALVES (i, i + rope_dims/2) of the range; STI_ROPE_INVERSE: by minus the angle (which
  * undoes the rotation, and is the gradient of one).  rope_dims 0: no rotation (turns unused).  fp32 inside (squares past
- * 3e38 overflow), rounded once.
+ * 3e38 overflow, those below 1e-38 lose bits, which shows with an eps as small), rounded once.
  *   x, y: bf16 [b, seqlen, h, d], heads contiguous; sequences and tokens *_bstride and *_tstride elements apart
  *   pos: int32 [b], the position of each sequence's first token, or with pos_per_token int32 [b, seqlen]
  *   turns: uint64 [rope_dims/2] from sti_rope_freqs, on the device
@@ -550,7 +550,8 @@ sti_status sti_kv_append_paged(const uint16_t *x, int64_t x_bstride, int64_t x_t
  *   q, out: bf16 [b, seqlen, h, d]; lse: fp32 [b, seqlen, h] or NULL; attn_sink, prev_out, prev_lse: as sti_attn_fp4kv
  * out may be prev_out itself; otherwise the outputs must not overlap the inputs.
  * bf16 tensor-core MMAs with fp32 accumulation, P rounded to bf16 for the PV product, fp32 online softmax.  Results do not
- * depend on the timing of the GPU (no atomics).  One kernel, or two when queries' rows are split between SMs.
+ * depend on the timing of the GPU (no atomics).  One kernel, or two when queries' rows are split between SMs; which, goes by
+ * max_pages * page_size and the window, not by the lengths: a table no wider than needed makes short contexts faster.
  * Supported: 1 <= h <= 64, d a multiple of 64 up to 512, max_pages * page_size <= 2^30; q, out, prev_out, pages 16-byte
  * aligned, page_stride a multiple of 8 and at least page_size * d; b * seqlen * h < 2^31.
  * ws: sti_attn_paged_workspace_size() bytes.

@@ -16,12 +16,13 @@ AttnPagedPlan attn_paged_plan(int B, int s, int h, int d, int cap, int window, i
     const int64_t tiles = (rows + kRows - 1) / kRows, groups = (int64_t)B * l.groups;
     // A list of t tiles takes its CTA some 5 us and 1.45 t.  Splitting evens the CTAs' tiles out, but costs as much as another 5 tiles
     // (second kernel; parts written and read), with more queries 13 (several parts per CTA).  Of long lists some may be much longer
-    // than others, which only splitting evens out: those are not taken whole.
+    // than others, which only splitting evens out: those are not taken whole.  (All by what the table and the window allow, as the
+    // lengths are on the device: 128 queries over 600 rows take 24 us with a table of 1024 positions, 39 with one of 65536.)
     const int64_t waves = (groups + num_sms - 1) / num_sms;
     const double extra = 5.0 + (12 * groups < 8 * num_sms ? 12.0 * groups / num_sms : 8.0);
     l.whole = tiles <= 16 && (double)(waves * tiles) <= (double)(tiles * groups) / num_sms + extra;
     // Pieces of at least two tiles, when the parts of a few queries otherwise take longer to write and join than the tiles
-    // (16 queries of 64 heads x 512 over 640 rows 20.7 -> 16.8 us, 8 groups of 4 x 16 heads over 1000 rows 22.8 -> 17.5).
+    // (16 queries of 64 heads x 512 over 640 rows 20.7 -> 16.0 us, 8 groups of 4 x 16 heads over 1000 rows 22.8 -> 17.5).
     l.least = groups >= 3 && (l.pack == 1 || d > 128) ? 2 : 1;
     const int64_t list = l.whole ? groups : (tiles * groups + l.least - 1) / l.least;
     l.grid = (int)(list < 1 ? 1 : list < num_sms ? list : num_sms);

@@ -21,9 +21,9 @@
 //   * warp 22 walks the list, tells the others what comes next and, when decoding, asks for the next tile's rows, into L2;
 //   * warp 23 loads Q by TMA as soon as the last QK of the query before has read the buffer.
 //
-// A long chunk is bound by shared memory: of a tile at 128 B a cycle, QK 1024 cycles, PV 768, the rows' copies 512 and
-// P^T and scores 100, together 2400 of the 2750 that a tile takes (the MMAs alone would take 2100: at N = 64 an M = 128 step
-// costs what one at N = 128 does).  2048 queries of 64 heads x 512 at 6144: 2105 us, 0.48 of the measured bf16 peak.  Decoding
+// A long chunk is bound by shared memory: a tile takes 2770 cycles, of which the MMAs read operands in 1790 (counted; at 128 B a
+// cycle QK 1024, PV 768) and the other warps' accesses, the rows' copies most of them, take 450; the tensor pipe is active in 1540.
+// 2048 queries of 64 heads x 512 at 6144: 2110 us, 0.47 of the measured bf16 peak.  Decoding
 // is bound by HBM: 32 queries over 16384 rows 103 us; a tile more costs what its rows take at 6.8 TB/s (81 us for all at the
 // measured copy rate), next to 20 us at the start (plan, Q, first tile: 5), the end (parts written 2, joined 4) and between
 // the two kernels.  Windows are bound by one query's chain: its Q has to come, the QK of its first tile, the softmax, the
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             int2 rec = make_int2(-1, 0);
             while (ok) {
                 // the next group with a tile in the piece (p.whole: with its middle there, and then all of it; by their first tiles,
-                // queries of 121 to 128 tiles would fall to CTAs by two and by four where there are three for each)
+                // 300 queries of 1 to 16 tiles take 60.5 us instead of 55.0, 456 of 13 to 16 109.7 instead of 106.7)
                 int nt = 0, u = 0;
                 for (; at_tile < piece.hi && q < nq; ++q, off = 0) {   // (the second as in plan_piece)
                     run.b = q / p.groups;
@@ -1333,7 +1333,9 @@ cudaError_t launch_attn_paged_nm(const CUtensorMap& tm_q, const AttnPagedParams&
     }
     e = launch_after(kernel, dim3((unsigned)p.grid), kPThreads, smem, stream, tm_q, p);
     if (e != cudaSuccess || p.whole) return e;
-    const int parts = p.grid / nq + 1;   // of a query, when they are alike
+    // Parts of a query when they are alike.  A long one among short ones gets the short ones' join: one of 65536 rows x 512 among 63 of
+    // 512 takes 62 us for the call, alone 29.
+    const int parts = p.grid / nq + 1;
     const int quads = (p.pack * p.h + 3) / 4;
     auto grid = [&](int warps, int dims) {   // warps of four heads x dims, of each query that may be split
         return dim3((unsigned)(nq < p.grid ? nq : p.grid), (unsigned)((quads * ((p.d + dims - 1) / dims) * warps + 7) / 8));
